@@ -13,6 +13,7 @@ import ctypes
 import math
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -44,6 +45,17 @@ _TORCH_TO_FA = {torch.float32: FA_F32, torch.float16: FA_F16, torch.bfloat16: FA
 
 class FaStrides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
+class _Kv8CacheArg(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("H", ctypes.c_int), ("d", ctypes.c_int), ("strides", FaStrides)]
+
+
+class _Kv8SeqsArg(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p),
+                ("new_lens", ctypes.c_void_p), ("B", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 class FaError(RuntimeError):
@@ -101,6 +113,22 @@ def load_library(path: str = LIB_PATH):
     lib.fa_bwd_alibi.argtypes = [vp] * 9 + [i, i, i, i, FaStrides, i, f, i, i, f, u64, u64, vp, i64, i, vp, sz,
                                             vp]
     lib.fa_bwd_alibi.restype = i
+    st = FaStrides
+    lib.fa_qk_norm_rope_fwd.argtypes = [vp] * 9 + [i64] + [i] * 8 + [st] * 4 + [i, i, f, vp]
+    lib.fa_qk_norm_rope_fwd.restype = i
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i64] + [i] * 8 + [st] * 6 + [i, i, f, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.restype = i
+    cache, seqs = ctypes.POINTER(_Kv8CacheArg), ctypes.POINTER(_Kv8SeqsArg)
+    lib.fa_kv8_append.argtypes = [cache, seqs, vp, vp, i, st, st, i, vp]
+    lib.fa_kv8_append.restype = i
+    lib.fa_kv8_norm_rope_append.argtypes = [cache, seqs] + [vp] * 8 + [i] * 5 + [st] * 4 + [i, i, f, vp]
+    lib.fa_kv8_norm_rope_append.restype = i
+    lib.fa_kv8_attn_workspace_size.argtypes = [i] * 10
+    lib.fa_kv8_attn_workspace_size.restype = sz
+    lib.fa_kv8_attn.argtypes = [cache, seqs, vp, vp, vp, i, i, i, st, st, i, f, i, i, vp, i64, vp, sz, vp]
+    lib.fa_kv8_attn.restype = i
     _lib = lib
     return lib
 
@@ -500,3 +528,307 @@ def flash_attn_varlen_func(q, k, v, cu_seqlens, max_seqlen, causal=False, window
     v = v if v.stride() == q.stride() else _match_layout(v, q)
     return _FlashAttnVarlenFunc.apply(q, k, v, cu_seqlens, int(max_seqlen), softmax_scale, causal, window,
                                       deterministic, alibi_slopes)
+
+
+# ---------------- norm of queries and keys, and their rotation ----------------
+def _rows_layout(t: torch.Tensor, shape, ref: torch.Tensor, name: str):
+    """Strides of a [B, N, H, d] CUDA tensor that must match ``ref``'s dtype and device."""
+    if tuple(t.shape) != tuple(shape) or t.stride(3) != 1:
+        raise ValueError(f"{name} must be {list(shape)} with a contiguous head dimension")
+    if t.dtype != ref.dtype or t.device != ref.device:
+        raise ValueError(f"{name} must have the dtype and device of the queries (or keys)")
+    s = t.stride()
+    return FaStrides(s[0], s[1], s[2])
+
+
+def _current_cuda(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.device.index is not None and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} lives on {t.device} but the current device is "
+                         f"cuda:{torch.cuda.current_device()} (use torch.cuda.device(...))")
+    if t.dtype not in _TORCH_TO_FA:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+
+
+def _int32(t, shape, ref: torch.Tensor, name: str):
+    """Pointer of an int32 tensor [B] or [B, x] with contiguous rows (None passes through)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != ref.device or tuple(t.shape) != tuple(shape) or \
+            (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be an int32 tensor {list(shape)} with contiguous rows on {ref.device}")
+    return t.data_ptr()
+
+
+def _rope_args(q, k, q_weight, k_weight, cos, sin):
+    """Checks shared by the norm-and-rotation calls: (rot_dim, max_pos, weight dtype code, four pointers)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("queries and keys are [B, N, H, d]")
+    _current_cuda(q, "q")
+    d = q.shape[3]
+    wt = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if tuple(w.shape) != (d,) or (d > 1 and w.stride(0) != 1) or w.device != q.device:
+            raise ValueError(f"{name} must be a contiguous [{d}] tensor on {q.device}")
+        if w.dtype not in (torch.float32, q.dtype) or (wt is not None and w.dtype != wt):
+            raise ValueError("weights are float32 or of the tensors' dtype, both alike")
+        wt = w.dtype
+    rot, rows = 0, 0
+    if (cos is None) != (sin is None):
+        raise ValueError("pass both tables or neither")
+    if cos is not None:
+        for name, t in (("cos", cos), ("sin", sin)):
+            if t.dim() != 2 or t.dtype != torch.float32 or t.device != q.device or not t.is_contiguous() or \
+                    t.shape != cos.shape:
+                raise ValueError(f"{name} must be a contiguous float32 [max_pos, rot_dim / 2] tensor on {q.device}")
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        if rot > d:
+            raise ValueError(f"the tables rotate {rot} values of heads of {d}")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return rot, rows, _TORCH_TO_FA[q.dtype if wt is None else wt], (ptr(q_weight), ptr(k_weight), ptr(cos), ptr(sin))
+
+
+def _positions(positions, q):
+    """(pointer, stride) of int32 positions [N] or [B, N], or (None, 0)."""
+    if positions is None:
+        return None, 0
+    B, N = q.shape[:2]
+    if positions.dim() == 1:
+        return _int32(positions, (N,), q, "positions"), 0
+    return _int32(positions, (B, N), q, "positions"), positions.stride(0)
+
+
+def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """cos and sin tables [max_pos, rot_dim / 2] (fp32) of the angles pos * base^(-2i / rot_dim),
+    computed in float64 (in fp32 the angles of far positions lose their fraction)."""
+    if max_pos < 1 or rot_dim < 2 or rot_dim % 2:
+        raise ValueError("max_pos must be positive and rot_dim positive and even")
+    freq = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return angle.cos().float(), angle.sin().float()
+
+
+def fa_qk_norm_rope_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                        eps=1e-6, interleaved=False, stream=None):
+    """Per-head RMS norm and rotation through the C ABI: fills q_out and k_out (shaped as q and k)."""
+    rot, rows, wt, ptrs = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    B, N, Hq, d = q.shape
+    st = [_rows_layout(q, q.shape, q, "q"), _rows_layout(k, (B, N, k.shape[2], d), q, "k"),
+          _rows_layout(q_out, q.shape, q, "q_out"), _rows_layout(k_out, k.shape, q, "k_out")]
+    _check(load_library().fa_qk_norm_rope_fwd(
+        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *ptrs, *_positions(positions, q), B, N, Hq,
+        k.shape[2], d, rot, int(interleaved), rows, *st, _TORCH_TO_FA[q.dtype], wt, float(eps), _stream(stream)))
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_size(int(d)))
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, q_weight=None, k_weight=None,
+                        cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """Its backward through the C ABI: fills dq, dk and, where there are weights, dq_weight and dk_weight.
+    ``workspace`` is a uint8 CUDA tensor of fa_qk_norm_rope_bwd_workspace_size(d) bytes."""
+    rot, rows, wt, ptrs = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    B, N, Hq, d = q.shape
+    st = [_rows_layout(t, s.shape, q, name) for name, t, s in (
+        ("q", q, q), ("k", k, k), ("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q), ("dk", dk, k))]
+    if tuple(k.shape) != (B, N, k.shape[2], d):
+        raise ValueError("q and k must share batch, length and head dimension")
+    for name, g, w in (("dq_weight", dq_weight, q_weight), ("dk_weight", dk_weight, k_weight)):
+        if (g is None) != (w is None) or (g is not None and (g.dtype != w.dtype or g.shape != w.shape or
+                                                             g.device != w.device or not g.is_contiguous())):
+            raise ValueError(f"{name} must match its weight (None for None)")
+    _on_device(workspace, q, "workspace")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _check(load_library().fa_qk_norm_rope_bwd(
+        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), *ptrs[:2],
+        ptr(dq_weight), ptr(dk_weight), *ptrs[2:], *_positions(positions, q), B, N, Hq, k.shape[2], d, rot,
+        int(interleaved), rows, *st, _TORCH_TO_FA[q.dtype], wt, float(eps), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
+                         interleaved=False):
+    """Allocate the outputs and run the norm and rotation; returns (q_out, k_out), contiguous."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    fa_qk_norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                          eps=1e-6, interleaved=False):
+    """Allocate the gradients and the workspace and run the backward; returns
+    (dq, dk, dq_weight, dk_weight), contiguous, None for a weight that is None."""
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    ws = torch.empty(fa_qk_norm_rope_bwd_workspace_size(q.shape[3]), dtype=torch.uint8, device=q.device)
+    fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dqw, dkw, ws, q_weight, k_weight, cos, sin, positions, eps,
+                        interleaved)
+    return dq, dk, dqw, dkw
+
+
+class _QkNormRopeFunc(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.cfg = (eps, interleaved)
+        return qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        grads = qk_norm_rope_backward(q, k, _readable(dq_out), _readable(dk_out), q_weight, k_weight, cos, sin,
+                                      positions, *ctx.cfg)
+        return (*grads, None, None, None, None, None)
+
+
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels read it: a copy where its strides (an expanded one's zeros,
+    unaligned rows) or its base do not allow reading it in place."""
+    s = t.stride()
+    unit = 8 if t.element_size() == 2 else 1
+    if s[3] != 1 or min(s) < 1 or any(x % unit for x in s[:3]) or t.data_ptr() % 16:
+        return t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def qk_norm_rope_func(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
+                      interleaved=False):
+    """Per-head RMS norm and rotation of q [B, N, Hq, d] and k [B, N, Hk, d] with autograd
+    (forward fa_qk_norm_rope_fwd, backward fa_qk_norm_rope_bwd): (q_out, k_out), as
+    flash_attn_func takes them. Gradients reach q, k and the weights."""
+    return _QkNormRopeFunc.apply(_readable(q), _readable(k), q_weight, k_weight, cos, sin, positions, float(eps),
+                                 bool(interleaved))
+
+
+# ---------------------------- 8-bit key/value cache ----------------------------
+class Kv8Cache(NamedTuple):
+    """A paged cache: k and v float8_e4m3fn [num_pages, page_size, H, d], k_scale and v_scale
+    float32 [num_pages, H]; the values held are ``k.float() * k_scale[:, None, :, None]``."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv8_cache_alloc(num_pages: int, page_size: int, H: int, d: int, device="cuda") -> Kv8Cache:
+    """An empty cache; each head's part of a page is contiguous, which reads fastest."""
+    k, v = (torch.zeros((num_pages, H, page_size, d), dtype=torch.uint8, device=device)
+            .view(torch.float8_e4m3fn).transpose(1, 2) for _ in range(2))
+    k_scale, v_scale = (torch.ones((num_pages, H), dtype=torch.float32, device=device) for _ in range(2))
+    return Kv8Cache(k, v, k_scale, v_scale)
+
+
+def _kv8_args(cache: Kv8Cache, ref: torch.Tensor, block_table, seq_lens, new_lens):
+    """The two C structs of a cache and its sequences, for new tokens ``ref`` [B, T, *, d]."""
+    if ref.dim() != 4:
+        raise ValueError("new queries, keys and values are [B, T, H, d]")
+    _current_cuda(ref, "the new tokens' tensors")
+    if ref.dtype == torch.float32:
+        raise ValueError("the 8-bit cache takes float16 or bfloat16 tensors")
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype or v.shape != k.shape or \
+            v.stride() != k.stride() or k.stride(3) != 1:
+        raise ValueError("cache.k and cache.v must be float8_e4m3fn [num_pages, page_size, H, d] of the same "
+                         "strides with a contiguous head dimension")
+    P, page, H, d = k.shape
+    for name, s in (("k_scale", ks), ("v_scale", vs)):
+        if s.dtype != torch.float32 or tuple(s.shape) != (P, H) or not s.is_contiguous() or s.device != ref.device:
+            raise ValueError(f"cache.{name} must be a contiguous float32 [{P}, {H}] tensor on {ref.device}")
+    if k.device != ref.device or v.device != ref.device:
+        raise ValueError(f"the cache must live on {ref.device}")
+    B = ref.shape[0]
+    if ref.shape[3] != d:
+        raise ValueError(f"the cache holds heads of {d}, the new tokens' tensors of {ref.shape[3]}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    st = k.stride()
+    c = _Kv8CacheArg(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, page, H, d,
+                     FaStrides(st[0], st[1], st[2]))
+    s = _Kv8SeqsArg(_int32(block_table, (B, block_table.shape[1]), ref, "block_table"), block_table.stride(0),
+                    _int32(seq_lens, (B,), ref, "seq_lens"), _int32(new_lens, (B,), ref, "new_lens"), B,
+                    block_table.shape[1])
+    return c, s
+
+
+def kv8_append(cache: Kv8Cache, k, v, block_table, seq_lens, new_lens=None, stream=None):
+    """Write new keys and values [B, T, H, d] into the cache (fa_kv8_append).
+
+    ``seq_lens`` (int32 [B]) counts the new tokens already; they are the last ``new_lens``
+    (int32 [B], None: T) of each sequence, further rows of k and v are padding. Token j of
+    sequence b lies in page ``block_table[b, j // page_size]`` (int32 [B, max_pages])."""
+    c, s = _kv8_args(cache, k, block_table, seq_lens, new_lens)
+    shape = (k.shape[0], k.shape[1], c.H, c.d)
+    _check(load_library().fa_kv8_append(
+        c, s, k.data_ptr(), v.data_ptr(), k.shape[1], _rows_layout(k, shape, k, "k"), _rows_layout(v, shape, k, "v"),
+        _TORCH_TO_FA[k.dtype], _stream(stream)))
+
+
+def fa_kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens,
+                            new_lens=None, eps=1e-6, interleaved=False, stream=None):
+    """Norm and rotation of new q and k, then k and v into the cache, through the C ABI: fills q_out."""
+    c, s = _kv8_args(cache, q, block_table, seq_lens, new_lens)
+    rot, rows, wt, ptrs = _rope_args(q, k, q_weight, k_weight, cos, sin)
+    B, T, Hq, d = q.shape
+    shape = (B, T, c.H, d)
+    _check(load_library().fa_kv8_norm_rope_append(
+        c, s, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *ptrs, T, Hq, rot, int(interleaved), rows,
+        _rows_layout(q, q.shape, q, "q"), _rows_layout(k, shape, q, "k"), _rows_layout(v, shape, q, "v"),
+        _rows_layout(q_out, q.shape, q, "q_out"), _TORCH_TO_FA[q.dtype], wt, float(eps), _stream(stream)))
+
+
+def kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens=None,
+                         eps=1e-6, interleaved=False):
+    """qk_norm_rope_forward of new q and k at their positions and kv8_append of the result in one
+    launch; returns the normed and rotated q (zeros in padding rows)."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fa_kv8_norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
+                            interleaved)
+    return q_out
+
+
+def fa_kv8_attn_workspace_size(B: int, T: int, Hq: int, H: int, d: int, page_size: int, max_pages: int,
+                               max_seqlen: int, causal: bool = True, window: int = 0) -> int:
+    return int(load_library().fa_kv8_attn_workspace_size(B, T, Hq, H, d, page_size, max_pages, int(max_seqlen),
+                                                         int(causal), int(window)))
+
+
+def fa_kv8_attn(q, cache: Kv8Cache, o, lse, block_table, seq_lens, max_seqlen, workspace, new_lens=None, scale=None,
+                causal=True, window=0, alibi_slopes=None, stream=None):
+    """Attention over the cache through the C ABI: fills o ([B, T, Hq, d]) and lse ([B, Hq, T] fp32).
+    ``workspace`` is a uint8 CUDA tensor of fa_kv8_attn_workspace_size(...) bytes."""
+    c, s = _kv8_args(cache, q, block_table, seq_lens, new_lens)
+    B, T, Hq, d = q.shape
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or not lse.is_contiguous() or \
+            lse.device != q.device:
+        raise ValueError(f"lse must be a contiguous float32 [B, Hq, T] tensor on {q.device}")
+    _on_device(workspace, q, "workspace")
+    _check(load_library().fa_kv8_attn(
+        c, s, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T, Hq, int(max_seqlen), _rows_layout(q, q.shape, q, "q"),
+        _rows_layout(o, q.shape, q, "o"), _TORCH_TO_FA[q.dtype], default_scale(d) if scale is None else float(scale),
+        int(causal), int(window), *_alibi(alibi_slopes, B, Hq, q.device), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kv8_attention(q, cache: Kv8Cache, block_table, seq_lens, max_seqlen, new_lens=None, scale=None, causal=True,
+                  window=0, alibi_slopes=None):
+    """Attention of the newest tokens' queries [B, T, Hq, d] over the cache; returns (o, lse).
+
+    The queries belong to the last ``new_lens`` tokens of each sequence (as for kv8_append, which
+    comes first: a token attends to itself through the cache). Hq must be a multiple of the
+    cache's heads. ``max_seqlen`` is an upper bound of ``seq_lens``."""
+    B, T, Hq, d = q.shape
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    ws = torch.empty(fa_kv8_attn_workspace_size(B, T, Hq, cache.k.shape[2], d, cache.k.shape[1],
+                                                block_table.shape[1], max_seqlen, causal, window),
+                     dtype=torch.uint8, device=q.device)
+    fa_kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, ws, new_lens, scale, causal, window,
+                alibi_slopes)
+    return o, lse

@@ -37,6 +37,9 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 unsigned int* g_status_ptr[kMaxDevices] = {};
 
+}  // namespace
+
+namespace fa {
 int status_ptr(unsigned int** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
@@ -49,6 +52,11 @@ int status_ptr(unsigned int** out) {
   *out = g_status_ptr[dev];
   return FA_OK;
 }
+}  // namespace fa
+
+namespace {
+
+using fa::status_ptr;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -160,6 +168,9 @@ int bind_device_context() {
   return FA_OK;
 }
 
+}  // namespace
+
+namespace fa {
 // Every buffer a kernel touches must be memory of the current device (or
 // managed memory): a host or another device's pointer would make the kernels
 // fault. Checked last, after the cheap argument checks and before any launch.
@@ -179,6 +190,11 @@ int check_device_ptrs(std::initializer_list<const void*> ptrs) {
   }
   return FA_OK;
 }
+}  // namespace fa
+
+namespace {
+
+using fa::check_device_ptrs;
 
 // Validation shared by the forward and the backward. Returns FA_OK or an error.
 int check_common(int B, int H, int N, int d, fa_strides s, int dtype, float scale, int window, float dropout_p) {

@@ -1,5 +1,10 @@
 // Host-side entry shared by the C-ABI translation units.
 #pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
 #include "fa.h"
 
 namespace fa {
@@ -45,5 +50,14 @@ int fwd_run(const void* q, const void* k, const void* v, void* o, float* lse, in
 // The shape, dtype, stride and scalar checks every entry point applies.
 int check_bwd_args(int B, int H, int N, int d, fa_strides strides, fa_dtype dtype, float scale, int window,
                    float dropout_p);
+
+// FA_OK if every non-null pointer is memory of the current device (or managed
+// memory), FA_ERR_INVALID_ARG otherwise; the last check before a launch.
+int check_device_ptrs(std::initializer_list<const void*> ptrs);
+
+// Address of the current device's status word.
+int status_ptr(unsigned int** out);
+
+inline bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 }  // namespace fa

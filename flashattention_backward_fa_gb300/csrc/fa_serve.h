@@ -1,0 +1,112 @@
+// Parameters and launchers of the norm-and-rotation operators and of the 8-bit
+// key/value cache, shared by their C entry points (fa_serve.cu) and kernels.
+#pragma once
+
+#include "fa_host.h"
+#include "fa_internal.h"
+
+namespace fa {
+
+// One of q and k: x [B, N, H, d], forward output (backward: the gradient that
+// comes in, `dout`, with out_st its strides) and the backward's outputs.
+struct RopeSide {
+  const void* x;
+  const void* dout;
+  void* out;
+  void* dx;
+  const void* w;  // weight vector [d] or null (ones)
+  void* dw;
+  fa_strides x_st, out_st, dx_st;
+  int H;
+};
+
+struct RopeParams {
+  RopeSide q, k;
+  const float* cos;  // [max_pos, rot / 2]
+  const float* sin;
+  const int* positions;  // [B, N], rows pos_stride apart, or null: 0 .. N - 1
+  int64_t pos_stride;
+  int B, N, d, rot, max_pos;
+  int neighbours;  // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+  int w_f32;       // weights (and their gradients) are fp32 whatever the tensors' type
+  float eps;
+  float* part;          // backward: a row of d partial weight gradients per block
+  int q_blocks, blocks;  // set by the launcher: blocks [0, q_blocks) take q's rows
+};
+
+// Most rows of `part` that a backward launch writes.
+int rope_bwd_max_blocks();
+cudaError_t launch_norm_rope_fwd(RopeParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(RopeParams& p, int dtype, cudaStream_t st);
+
+// Device status bit: a block table names a page outside the cache (the page's
+// tokens are skipped).
+constexpr unsigned int kStatusBadPage = 4u;
+
+// A paged cache of e4m3 codes and its sequences (fa.h, fa_kv8_cache and fa_kv8_seqs).
+struct Kv8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;  // [num_pages, H]
+  float* v_scale;
+  int num_pages, page_shift, H;
+  int64_t sp, sn, sh;  // element strides of a page, a token and a head (k and v alike)
+  const int* table;    // [B, max_pages], rows table_stride apart
+  int64_t table_stride;
+  int max_pages;
+  const int* seq_lens;  // [B], the call's new tokens counted
+  const int* new_lens;  // [B] or null: T each
+  unsigned int* status;
+};
+
+struct Kv8AppendParams {
+  Kv8Cache c;
+  const void* k;
+  const void* v;
+  fa_strides k_st, v_st;
+  int B, T, d;
+  int pages;  // most pages that T tokens reach
+  // norm and rotation (null q: the append alone)
+  const void* q;
+  void* q_out;
+  fa_strides q_st, q_out_st;
+  int Hq;
+  const void* q_w;
+  const void* k_w;
+  const float* cos;
+  const float* sin;
+  int rot, max_pos, neighbours, w_f32;
+  float eps;
+  int kv_blocks;  // set by the launcher: blocks [0, kv_blocks) take the cache's pages, the others q's rows
+};
+cudaError_t launch_kv8_append(Kv8AppendParams& p, bool bf16, cudaStream_t st);
+
+struct Kv8AttnParams {
+  Kv8Cache c;
+  const void* q;
+  void* o;
+  float* lse;  // [B, Hq, T]
+  fa_strides q_st, o_st;
+  int B, T, Hq, G, d;  // G = Hq / H query heads share a key head
+  float scale_log2;
+  int causal, window;
+  const float* alibi;
+  int64_t alibi_sb;
+  int key_limit;  // keys past it are never attended: min(max_seqlen, max_pages * page size)
+  int chunk;      // keys of a split (a multiple of 64)
+  int splits;     // most splits of a sequence
+  int row_tiles;
+  float* part_o;   // [B, H, T * G, splits, d]: normalised outputs of the splits
+  float* part_lse;  // [B, H, T * G, splits]: their log2-sum-exp2
+};
+
+struct Kv8AttnPlan {
+  int tiles;      // 8-row query tiles of a block (1, 2 or 4)
+  int row_tiles;  // blocks that share the T * G rows of a key head
+  int chunk, splits;
+  size_t workspace;
+};
+Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window);
+cudaError_t launch_kv8_attn(Kv8AttnParams& p, const Kv8AttnPlan& plan, bool bf16, cudaStream_t st);
+
+}  // namespace fa

@@ -1,0 +1,285 @@
+// New keys and values into the paged 8-bit cache, alone (kv8_append) or behind
+// the per-head norm and rotation of queries and keys (kv8_norm_rope_append).
+//
+// A page holds page-size tokens of every head as e4m3 codes of x / s, with one
+// scale s per (page, head), a power of two: s = 2^e, e the least integer with
+// amax <= 448 * 2^e (448 is the largest e4m3 value). A power of two costs
+// e4m3 nothing but range (its precision is relative), and it makes every step
+// exact but the one rounding: x / s is a change of exponent, and when a page
+// that already holds tokens needs a larger scale, its codes are divided by a
+// power of two, which moves only those that reach e4m3's subnormals.
+//
+// One block takes one (page, head) of the new keys or of the new values: it
+// loads the page's new rows once, keeps them in registers while the block
+// agrees on their largest magnitude, and writes the codes. With norm and
+// rotation the keys' rows are normed, rotated and rounded to their type in
+// registers in between, so the cache holds the same codes as after the two
+// operators one by one; further blocks take q's rows. Nothing but the inputs
+// and the outputs moves through memory. Bound by memory (2 bytes in and 1 byte
+// out an element of k and v, 2 and 2 of q); for single tokens by the launch and
+// three dependent loads (length, page number, rows).
+#include <algorithm>
+
+#include "fa_serve.h"
+#include "rope_common.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kMinExp = -100;  // least scale exponent: blocks of zeros (or below 2^-91) get it
+
+// The scale's bits for a largest finite magnitude: 448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = max((int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0), kMinExp);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two fp32 values to a pair of e4m3 codes, lo in the low byte (round to nearest even).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void unpack_e4m3x2(uint32_t two, float& lo, float& hi) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
+  unpack2<false>(h, lo, hi);
+}
+
+// Bits of an infinity of the type, sign cleared: magnitudes from it up are not finite.
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t inf_bits() {
+  return std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+}
+
+// Largest magnitude of eight values as bits of their type (kFinite: of the finite ones).
+template <typename T, bool kFinite>
+__device__ __forceinline__ uint32_t amax_bits(const uint4& a) {
+  const uint32_t wv[4] = {a.x, a.y, a.z, a.w};
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t v = wv[i] & 0x7FFF7FFFu;
+    if (kFinite) {
+      if ((v & 0xFFFFu) >= inf_bits<T>()) v &= 0xFFFF0000u;
+      if ((v >> 16) >= inf_bits<T>()) v &= 0x0000FFFFu;
+    }
+    m = max_u16x2(m, v);
+  }
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Largest value over the block (every thread gets it); red: one word a warp.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  uint32_t m = red[0];
+  for (int i = 1; i < warps; ++i) m = max(m, red[i]);
+  __syncthreads();
+  return m;
+}
+
+// Eight values to eight codes. kAny: infinities become NaN codes as NaN do (a
+// finite value is never beyond 448 times the scale).
+template <typename T, bool kAny>
+__device__ __forceinline__ uint2 quantise8(const Raw8<T>& raw, float inv) {
+  float f[8];
+  raw.unpack(f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    f[i] *= inv;
+    if (kAny && fabsf(f[i]) == INFINITY) f[i] = __int_as_float(0x7FC00000);
+  }
+  return make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+}
+
+struct NewTokens {
+  int start, len, count;  // position of the first, tokens of the sequence with them, how many
+};
+
+__device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T) {
+  NewTokens n;
+  n.count = c.new_lens ? min(max(__ldg(c.new_lens + b), 0), T) : T;
+  n.len = max(__ldg(c.seq_lens + b), 0);
+  n.start = n.len - n.count;
+  return n;
+}
+
+// Blocks [0, kv_blocks): (sequence, reached page, keys or values, head), heads
+// fastest. kRows rows of a page a thread; blockDim.x * kRows * 8 values hold a
+// page's new rows. kNorm: 0 append alone, 1 / 2 norm and rotation with partners
+// rot / 2 apart / neighbours.
+template <typename T, int D, int kRows, int kNorm>
+__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
+  constexpr int G = D / 8;
+  constexpr bool kNeighbours = kNorm == 2;
+  __shared__ uint32_t red[8];
+  const Kv8Cache& c = p.c;
+  const int lane = threadIdx.x & 31, e0 = (lane % G) * 8;
+  if (kNorm != 0 && blockIdx.x >= (unsigned)p.kv_blocks) {
+    // q: one row (b, t, head) a row group; rows without a token become zeros
+    const long long rows = (long long)p.B * p.T * p.Hq;
+    const long long row = (long long)(blockIdx.x - p.kv_blocks) * (blockDim.x / G) + threadIdx.x / G;
+    const bool inside = row < rows;
+    const int h = inside ? (int)(row % p.Hq) : 0;
+    const long long bt = inside ? row / p.Hq : 0;
+    const int b = (int)(bt / p.T), t = (int)(bt - (long long)b * p.T);
+    const NewTokens n = new_tokens(c, b, p.T);
+    const bool live = inside && t < n.count && n.start + t >= 0;
+    const int partner = partner_lane<kNeighbours>(lane, e0, p.rot);
+    Raw8<T> raw;
+    raw.zero();
+    if (live) raw.load(static_cast<const T*>(p.q) + b * p.q_st.b + t * p.q_st.n + h * p.q_st.h + e0);
+    float w[8], w_p[8], cc[8], ss[8], out[8];
+    load_weight8<T>(p.q_w, p.w_f32, e0, w);
+    load_weight8<T>(p.q_w, p.w_f32, (partner % G) * 8, w_p);
+    const long long at = live ? (long long)min(n.start + t, p.max_pos - 1) * (p.rot >> 1) : 0;
+    load_rotation<kNeighbours>(p.cos + at, p.sin + at, e0, live ? p.rot : 0, cc, ss);
+    norm_rope_chunk<T, D, kNeighbours>(raw, partner, w, w_p, cc, ss, p.eps, out);
+    if (inside) {
+      if (live) raw.pack(out);  // (else the zeros)
+      raw.store(static_cast<T*>(p.q_out) + b * p.q_out_st.b + t * p.q_out_st.n + h * p.q_out_st.h + e0);
+    }
+    return;
+  }
+  unsigned x = blockIdx.x;
+  const int h = x % c.H;
+  x /= c.H;
+  const bool is_v = (x & 1u) != 0;
+  x >>= 1;
+  const int reached = x % p.pages, b = x / p.pages;
+  const NewTokens n = new_tokens(c, b, p.T);
+  const int size = 1 << c.page_shift;
+  const int pg = (max(n.start, 0) >> c.page_shift) + reached;
+  if (pg >= c.max_pages) return;  // (and positions below stay in 31 bits)
+  const int t_lo = max(max(n.start, 0), pg << c.page_shift);
+  const int t_hi = min(n.len, (pg + 1) << c.page_shift);  // positions [t_lo, t_hi)
+  if (t_lo >= t_hi) return;
+  const int id = __ldg(c.table + b * c.table_stride + pg);
+  if (id < 0 || id >= c.num_pages) {
+    if (threadIdx.x == 0) atomicOr(c.status, kStatusBadPage);
+    return;
+  }
+  const int rows = t_hi - t_lo, slot0 = t_lo & (size - 1);
+  const fa_strides& st = is_v ? p.v_st : p.k_st;
+  const T* src = static_cast<const T*>(is_v ? p.v : p.k) + b * st.b + (long long)(t_lo - n.start) * st.n + h * st.h;
+  const int groups = blockDim.x / G, row0 = threadIdx.x / G;
+  Raw8<T> raw[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = row0 + i * groups;
+    raw[i].zero();
+    if (r < rows) raw[i].load(src + r * st.n + e0);
+  }
+  uint8_t* page = (is_v ? c.v : c.k) + id * c.sp + h * c.sh;
+  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)id * c.H + h;
+  const float was = slot0 > 0 ? *scale_at : 0.f;  // a page without earlier tokens has no former scale
+  if (kNorm != 0 && !is_v) {
+    const int partner = partner_lane<kNeighbours>(lane, e0, p.rot);
+    float w[8], w_p[8];
+    load_weight8<T>(p.k_w, p.w_f32, e0, w);
+    load_weight8<T>(p.k_w, p.w_f32, (partner % G) * 8, w_p);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row0 + i * groups;
+      const bool live = r < rows;
+      float cc[8], ss[8], out[8];
+      const long long at = live ? (long long)min(t_lo + r, p.max_pos - 1) * (p.rot >> 1) : 0;
+      load_rotation<kNeighbours>(p.cos + at, p.sin + at, e0, live ? p.rot : 0, cc, ss);
+      norm_rope_chunk<T, D, kNeighbours>(raw[i], partner, w, w_p, cc, ss, p.eps, out);
+      if (live) raw[i].pack(out);
+    }
+  }
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) m = max(m, amax_bits<T, false>(raw[i].a));
+  m = block_max(m, red);
+  const bool any = m >= inf_bits<T>();  // infinities or NaN among the new values
+  if (any) {
+    m = 0u;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) m = max(m, amax_bits<T, true>(raw[i].a));
+    m = block_max(m, red);
+  }
+  const float scale = fmaxf(scale_for(h16_bits_to_f32<std::is_same<T, __nv_bfloat16>::value>(m)), was);
+  const float inv = 1.f / scale;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = row0 + i * groups;
+    if (r >= rows) continue;
+    const uint2 q = any ? quantise8<T, true>(raw[i], inv) : quantise8<T, false>(raw[i], inv);
+    *reinterpret_cast<uint2*>(page + (slot0 + r) * c.sn + e0) = q;
+  }
+  if (slot0 > 0 && scale != was) {  // earlier tokens to the larger scale
+    const float ratio = was * inv;
+    for (int r = row0; r < slot0; r += groups) {
+      uint2* at = reinterpret_cast<uint2*>(page + r * c.sn + e0);
+      const uint2 q = *at;
+      const uint32_t in[2] = {q.x, q.y};
+      uint32_t to[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float f[4];
+        unpack_e4m3x2(in[i] & 0xFFFFu, f[0], f[1]);
+        unpack_e4m3x2(in[i] >> 16, f[2], f[3]);
+        to[i] = e4m3x2(f[0] * ratio, f[1] * ratio) | (e4m3x2(f[2] * ratio, f[3] * ratio) << 16);
+      }
+      *at = make_uint2(to[0], to[1]);
+    }
+  }
+  // (every thread has read the former scale: block_max synchronised since)
+  if (threadIdx.x == 0) *scale_at = scale;
+}
+
+template <typename T, int D, int kRows>
+cudaError_t launch_rows(const Kv8AppendParams& p, unsigned grid, int threads, cudaStream_t st) {
+  if (p.q == nullptr)
+    kv8_append_kernel<T, D, kRows, 0><<<grid, threads, 0, st>>>(p);
+  else if (!p.neighbours)
+    kv8_append_kernel<T, D, kRows, 1><<<grid, threads, 0, st>>>(p);
+  else
+    kv8_append_kernel<T, D, kRows, 2><<<grid, threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_d(Kv8AppendParams& p, cudaStream_t st) {
+  constexpr int G = D / 8;
+  const int rows = std::min(1 << p.c.page_shift, p.T);  // most new rows of one page
+  // up to 256 threads, then more rows a thread; at least two warps, so that a
+  // single token still shares out the rescaling of its page
+  const int lanes = rows * G;
+  const int per = lanes <= 256 ? 1 : lanes <= 512 ? 2 : lanes <= 1024 ? 4 : 8;
+  const int threads = std::max(64, ((lanes + per - 1) / per + 31) / 32 * 32);
+  const long long kv = (long long)p.B * p.pages * 2 * p.c.H;
+  const long long q = p.q ? ((long long)p.B * p.T * p.Hq + threads / G - 1) / (threads / G) : 0;
+  if (kv + q > 0x7fffffffll) return cudaErrorInvalidValue;
+  p.kv_blocks = (int)kv;
+  const unsigned grid = (unsigned)(kv + q);
+  switch (per) {
+    case 1: return launch_rows<T, D, 1>(p, grid, threads, st);
+    case 2: return launch_rows<T, D, 2>(p, grid, threads, st);
+    case 4: return launch_rows<T, D, 4>(p, grid, threads, st);
+    default: return launch_rows<T, D, 8>(p, grid, threads, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(Kv8AppendParams& p, bool bf16, cudaStream_t st) {
+  if (p.d == 64) return bf16 ? launch_d<__nv_bfloat16, 64>(p, st) : launch_d<__half, 64>(p, st);
+  return bf16 ? launch_d<__nv_bfloat16, 128>(p, st) : launch_d<__half, 128>(p, st);
+}
+
+}  // namespace fa

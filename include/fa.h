@@ -291,10 +291,135 @@ int fa_varlen_bwd(const void* q, const void* k, const void* v, const void* o, co
                   const float* alibi_slopes, int64_t alibi_stride_seq, int deterministic, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Per-head RMS norm of queries and keys and their position rotation, in one
+ * pass: what most models do between the projections and the attention. For
+ * every row x (d values of one head of one token) with its side's weights w:
+ *   y = w o x / sqrt(mean(x^2) + eps)
+ *   out = y with each pair (a, b) of its first rot_dim values turned into
+ *         (a cos - b sin, b cos + a sin),
+ * the pairs being (i, i + rot_dim / 2), or neighbours (2i, 2i + 1) with
+ * interleaved != 0; pair i takes cos_table[pos][i], sin_table[pos][i], two
+ * [max_pos, rot_dim / 2] contiguous fp32 arrays. Norm and rotation are computed
+ * in fp32 and rounded once. rot_dim = 0 is the norm alone (null tables).
+ *
+ * q, q_out: [B, N, Hq, d]; k, k_out: [B, N, Hk, d] (Hk may differ from Hq), each
+ * with its own strides. Outputs must not overlap inputs. positions: device
+ * int32, element (b, n) at b * pos_stride + n, clamped into [0, max_pos); null
+ * means n. Packed [total, H, d] input is B = 1 with positions. q_weight,
+ * k_weight: contiguous [d] of weight_dtype (FA_F32 or the tensors' type), null
+ * for ones.
+ *
+ * Supported: fp16 / bf16 with d in {64, 128}, rot_dim a multiple of 16, strides
+ * multiples of 8; fp32 with d <= 128, any even rot_dim, any positive strides;
+ * sizes as fa_fwd. Tensors and tables 16-byte aligned. eps > 0.
+ *
+ * Backward: from q, k and the gradients of q_out and k_out, the gradients of q,
+ * k and of the weights ([d], weight_dtype, summed over all rows in fp32 in a
+ * fixed order: the same bits on every run; null exactly where the weight is
+ * null). Nothing of the forward is needed but its inputs. `workspace`: 256-byte
+ * aligned, fa_qk_norm_rope_bwd_workspace_size(d) bytes (0 for an invalid d);
+ * its contents on entry do not matter. Errors as fa_fwd / fa_bwd.
+ * ------------------------------------------------------------------------- */
+int fa_qk_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                        const void* k_weight, const float* cos_table, const float* sin_table, const int* positions,
+                        int64_t pos_stride, int B, int N, int Hq, int Hk, int d, int rot_dim, int interleaved,
+                        int max_pos, fa_strides q_strides, fa_strides k_strides, fa_strides q_out_strides,
+                        fa_strides k_out_strides, fa_dtype dtype, fa_dtype weight_dtype, float eps, void* stream);
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                        const void* q_weight, const void* k_weight, void* dq_weight, void* dk_weight,
+                        const float* cos_table, const float* sin_table, const int* positions, int64_t pos_stride,
+                        int B, int N, int Hq, int Hk, int d, int rot_dim, int interleaved, int max_pos,
+                        fa_strides q_strides, fa_strides k_strides, fa_strides dq_out_strides,
+                        fa_strides dk_out_strides, fa_strides dq_strides, fa_strides dk_strides, fa_dtype dtype,
+                        fa_dtype weight_dtype, float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache in 8 bits, with a scale for each page and head.
+ *
+ * Pages hold page_size tokens (16, 32, 64 or 128) of H key heads, d in {64,
+ * 128}: k and v are e4m3 codes, element (page p, token t, head h, value i) at
+ * p * strides.b + t * strides.n + h * strides.h + i (strides multiples of 16,
+ * bases 16-byte aligned; [num_pages, page_size, H, d] and [num_pages, H,
+ * page_size, d] storage are both expressible, the second reads fastest), and
+ * stand for code * scale with k_scale, v_scale contiguous fp32 [num_pages, H].
+ *
+ * Sequences: sequence b has seq_lens[b] tokens (device int32 [B]); its token j
+ * is in page block_table[b * table_stride + j / page_size] (device int32,
+ * max_pages entries a sequence), slot j % page_size. The new tokens of a call
+ * (the rows t of its [B, T, H, d] tensors) are the LAST new_lens[b] of them
+ * (device int32 [B], values in [0, T]; null: T each): seq_lens already counts
+ * them, and row t is at position seq_lens[b] - new_lens[b] + t. Rows from
+ * new_lens[b] on are padding, and so is a row whose position is negative.
+ * The library cannot check device contents: tokens past max_pages pages are
+ * ignored, a table entry outside [0, num_pages) makes its page's tokens be
+ * skipped (not written, not attended to) and sets bit 4 of the device status
+ * word. B <= 65535, H <= 1024, max_pages * page_size <= 2^30.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int num_pages, page_size, H, d;
+  fa_strides strides; /* b: page, n: token, h: head */
+} fa_kv8_cache;
+
+typedef struct {
+  const int* block_table;
+  int64_t table_stride;
+  const int* seq_lens;
+  const int* new_lens;
+  int B, max_pages;
+} fa_kv8_seqs;
+
+/* Writes new keys and values k, v ([B, T, H, d], fp16 or bf16, strides
+ * multiples of 8) into the cache. The scale of a (page, head) is the least
+ * power of two s (of at least 2^-100) with amax <= 448 s, amax the largest
+ * finite magnitude that the call brings to it, and not less than its former
+ * scale where the page holds earlier tokens of the sequence; those are rounded
+ * anew to a larger scale. Codes are x / s rounded to nearest even; NaN and
+ * infinities are stored as NaN. A page that the call writes must belong to one
+ * sequence (and to one place in it); other pages may be shared. */
+int fa_kv8_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* k, const void* v, int T,
+                  fa_strides k_strides, fa_strides v_strides, fa_dtype dtype, void* stream);
+
+/* fa_qk_norm_rope_fwd of new q ([B, T, Hq, d]) and k at their positions in the
+ * sequences, then fa_kv8_append of the normed and rotated k (rounded to its
+ * type) and of v, in one launch: bit for bit the two calls' results. q_out gets
+ * zeros in padding rows and must not overlap q. */
+int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, const void* k,
+                            const void* v, void* q_out, const void* q_weight, const void* k_weight,
+                            const float* cos_table, const float* sin_table, int T, int Hq, int rot_dim,
+                            int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
+                            fa_strides v_strides, fa_strides q_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                            float eps, void* stream);
+
+/* Attention of the new tokens' queries q ([B, T, Hq, d], fp16 or bf16) over the
+ * cache: o ([B, T, Hq, d], q's type) and lse ([B, Hq, T] contiguous fp32, natural
+ * log). Query heads h * Hq / H .. share key head h (Hq a multiple of H). The
+ * query at position i attends to the keys j < min(seq_lens[b], max_seqlen) with
+ * j <= i (causal != 0) and j > i - window (window > 0); scores are scale * q.k -
+ * m |i - j| with optional ALiBi slopes as for fa_fwd_alibi (m =
+ * alibi_slopes[b * alibi_stride_b + hq]). A row without keys, and a padding
+ * row, gets O = 0 and lse = -inf. A NaN in k or v reaches only the rows that
+ * attend to its token. max_seqlen: an upper bound of seq_lens (it sizes the
+ * launch). `workspace`: 256-byte aligned, fa_kv8_attn_workspace_size(...) bytes
+ * for the same sizes (0 for invalid ones); its contents on entry do not matter.
+ * The same inputs give the same bits on every run. */
+size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,
+                                  int causal, int window);
+int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, void* o, float* lse, int T, int Hq,
+                int max_seqlen, fa_strides q_strides, fa_strides o_strides, fa_dtype dtype, float scale, int causal,
+                int window, const float* alibi_slopes, int64_t alibi_stride_b, void* workspace,
+                size_t workspace_bytes, void* stream);
+
 /* Reads (and with clear != 0 resets) the status word of the current device.
  * Call after synchronising the streams the kernels ran on. *status receives
  * the raw bits (1 = a bounded wait timed out; 2 = an FA_DQ_ORDERED dK/dV
- * launch found its unit ticket not reset and did nothing). Returns FA_OK, FA_ERR_TIMEOUT
+ * launch found its unit ticket not reset and did nothing; 4 = a block table
+ * named a page outside the cache). Returns FA_OK, FA_ERR_TIMEOUT
  * when the timeout bit is set, or FA_ERR_CUDA. This call synchronises the device. */
 int fa_get_device_status(unsigned int* status, int clear);
 
