@@ -13,6 +13,7 @@ import ctypes
 import math
 import os
 import re
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -181,7 +182,8 @@ def _on_device(t: torch.Tensor, ref: torch.Tensor, name: str):
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # the handle alone: building a torch.cuda.Stream object costs about 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -213,6 +215,7 @@ def _bias(bias, q):
     return bias.data_ptr(), FaStrides(sb, bias.stride(2), sh)
 
 
+@lru_cache(maxsize=None)
 def default_scale(d: int) -> float:
     return float(torch.tensor(1.0 / math.sqrt(d), dtype=torch.float32))
 
@@ -531,74 +534,88 @@ def flash_attn_varlen_func(q, k, v, cu_seqlens, max_seqlen, causal=False, window
 
 
 # ---------------- norm of queries and keys, and their rotation ----------------
-def _rows_layout(t: torch.Tensor, shape, ref: torch.Tensor, name: str):
-    """Strides of a [B, N, H, d] CUDA tensor that must match ``ref``'s dtype and device."""
-    if tuple(t.shape) != tuple(shape) or t.stride(3) != 1:
-        raise ValueError(f"{name} must be {list(shape)} with a contiguous head dimension")
-    if t.dtype != ref.dtype or t.device != ref.device:
-        raise ValueError(f"{name} must have the dtype and device of the queries (or keys)")
+# A serving loop makes these calls once a layer and token, where the GPU's work is a few
+# microseconds: the checks below fetch every tensor property once, and the structs of
+# strides that recur from call to call are built once.
+@lru_cache(maxsize=1024)
+def _strides(b: int, n: int, h: int) -> FaStrides:
+    return FaStrides(b, n, h)
+
+
+def _rows_layout(t: torch.Tensor, shape, dtype, dev: int, name: str) -> FaStrides:
+    """Strides of a [B, N, H, d] CUDA tensor of that shape, dtype and device index."""
     s = t.stride()
-    return FaStrides(s[0], s[1], s[2])
+    if t.shape != shape or s[3] != 1:
+        raise ValueError(f"{name} must be {list(shape)} with a contiguous head dimension")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on cuda:{dev}, as the call's other tensors")
+    return _strides(s[0], s[1], s[2])
 
 
-def _current_cuda(t: torch.Tensor, name: str):
-    if not t.is_cuda:
+def _new_tensor(t: torch.Tensor, name: str):
+    """(shape, dtype, device index) of a [B, N, H, d] tensor on the current device."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.device.index is not None and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} lives on {t.device} but the current device is "
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} lives on cuda:{dev} but the current device is "
                          f"cuda:{torch.cuda.current_device()} (use torch.cuda.device(...))")
-    if t.dtype not in _TORCH_TO_FA:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be four-dimensional: [B, N, H, d]")
+    dtype = t.dtype
+    if dtype not in _TORCH_TO_FA:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {dtype}")
+    return t.shape, dtype, dev
 
 
-def _int32(t, shape, ref: torch.Tensor, name: str):
-    """Pointer of an int32 tensor [B] or [B, x] with contiguous rows (None passes through)."""
+def _int32(t, shape, dev: int, name: str):
+    """Pointer of an int32 tensor of that shape with contiguous rows (None passes through)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != ref.device or tuple(t.shape) != tuple(shape) or \
-            (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be an int32 tensor {list(shape)} with contiguous rows on {ref.device}")
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != shape or \
+            (shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be an int32 tensor {list(shape)} with contiguous rows on cuda:{dev}")
     return t.data_ptr()
 
 
-def _rope_args(q, k, q_weight, k_weight, cos, sin):
-    """Checks shared by the norm-and-rotation calls: (rot_dim, max_pos, weight dtype code, four pointers)."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("queries and keys are [B, N, H, d]")
-    _current_cuda(q, "q")
-    d = q.shape[3]
-    wt = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if tuple(w.shape) != (d,) or (d > 1 and w.stride(0) != 1) or w.device != q.device:
-            raise ValueError(f"{name} must be a contiguous [{d}] tensor on {q.device}")
-        if w.dtype not in (torch.float32, q.dtype) or (wt is not None and w.dtype != wt):
-            raise ValueError("weights are float32 or of the tensors' dtype, both alike")
-        wt = w.dtype
-    rot, rows = 0, 0
-    if (cos is None) != (sin is None):
-        raise ValueError("pass both tables or neither")
-    if cos is not None:
-        for name, t in (("cos", cos), ("sin", sin)):
-            if t.dim() != 2 or t.dtype != torch.float32 or t.device != q.device or not t.is_contiguous() or \
-                    t.shape != cos.shape:
-                raise ValueError(f"{name} must be a contiguous float32 [max_pos, rot_dim / 2] tensor on {q.device}")
-        rows, rot = cos.shape[0], 2 * cos.shape[1]
-        if rot > d:
-            raise ValueError(f"the tables rotate {rot} values of heads of {d}")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return rot, rows, _TORCH_TO_FA[q.dtype if wt is None else wt], (ptr(q_weight), ptr(k_weight), ptr(cos), ptr(sin))
+def _weight(w, d: int, dtype, dev: int, name: str):
+    if w is None:
+        return None
+    if w.shape != (d,) or (d > 1 and w.stride(0) != 1) or w.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous [{d}] tensor on cuda:{dev}")
+    if w.dtype is not dtype and w.dtype is not torch.float32:
+        raise ValueError(f"{name} must be float32 or of the tensors' dtype")
+    return w.data_ptr()
 
 
-def _positions(positions, q):
+def _rope_args(d: int, dtype, dev: int, q_weight, k_weight, cos, sin):
+    """Weights and tables of the norm-and-rotation calls: (rot_dim, max_pos, weight dtype code, four pointers)."""
+    qw, kw = _weight(q_weight, d, dtype, dev, "q_weight"), _weight(k_weight, d, dtype, dev, "k_weight")
+    wt = dtype if qw is kw is None else (k_weight if qw is None else q_weight).dtype
+    if qw is not None and kw is not None and k_weight.dtype is not wt:
+        raise ValueError("q_weight and k_weight must have the same dtype")
+    if cos is None or sin is None:
+        if cos is not sin:
+            raise ValueError("pass both tables or neither")
+        return 0, 0, _TORCH_TO_FA[wt], (qw, kw, None, None)
+    shape = cos.shape
+    for name, t in (("cos", cos), ("sin", sin)):
+        if len(shape) != 2 or t.shape != shape or t.dtype is not torch.float32 or t.get_device() != dev or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [max_pos, rot_dim / 2] tensor on cuda:{dev}")
+    rows, half = shape
+    if 2 * half > d:
+        raise ValueError(f"the tables rotate {2 * half} values of heads of {d}")
+    return 2 * half, rows, _TORCH_TO_FA[wt], (qw, kw, cos.data_ptr(), sin.data_ptr())
+
+
+def _positions(positions, B: int, N: int, dev: int):
     """(pointer, stride) of int32 positions [N] or [B, N], or (None, 0)."""
     if positions is None:
         return None, 0
-    B, N = q.shape[:2]
     if positions.dim() == 1:
-        return _int32(positions, (N,), q, "positions"), 0
-    return _int32(positions, (B, N), q, "positions"), positions.stride(0)
+        return _int32(positions, (N,), dev, "positions"), 0
+    return _int32(positions, (B, N), dev, "positions"), positions.stride(0)
 
 
 def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -611,63 +628,90 @@ def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"
     return angle.cos().float(), angle.sin().float()
 
 
+def _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream):
+    shape, dtype, dev = _new_tensor(q, "q")
+    B, N, Hq, d = shape
+    kshape = k.shape
+    if len(kshape) != 4 or kshape[0] != B or kshape[1] != N or kshape[3] != d:
+        raise ValueError(f"k must be [{B}, {N}, Hk, {d}] as q is {list(shape)}")
+    Hk = kshape[2]
+    rot, rows, wt, ptrs = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
+    q_st, k_st = _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        qo_st, ko_st = _strides(N * Hq * d, Hq * d, d), _strides(N * Hk * d, Hk * d, d)
+    else:
+        qo_st = _rows_layout(q_out, shape, dtype, dev, "q_out")
+        ko_st = _rows_layout(k_out, kshape, dtype, dev, "k_out")
+    _check((_lib or load_library()).fa_qk_norm_rope_fwd(
+        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *ptrs, *_positions(positions, B, N, dev), B,
+        N, Hq, Hk, d, rot, interleaved, rows, q_st, k_st, qo_st, ko_st, _TORCH_TO_FA[dtype], wt, eps,
+        _stream(stream)))
+    return q_out, k_out
+
+
 def fa_qk_norm_rope_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
                         eps=1e-6, interleaved=False, stream=None):
     """Per-head RMS norm and rotation through the C ABI: fills q_out and k_out (shaped as q and k)."""
-    rot, rows, wt, ptrs = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    B, N, Hq, d = q.shape
-    st = [_rows_layout(q, q.shape, q, "q"), _rows_layout(k, (B, N, k.shape[2], d), q, "k"),
-          _rows_layout(q_out, q.shape, q, "q_out"), _rows_layout(k_out, k.shape, q, "k_out")]
-    _check(load_library().fa_qk_norm_rope_fwd(
-        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *ptrs, *_positions(positions, q), B, N, Hq,
-        k.shape[2], d, rot, int(interleaved), rows, *st, _TORCH_TO_FA[q.dtype], wt, float(eps), _stream(stream)))
+    _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream)
 
 
+def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
+                         interleaved=False):
+    """Allocate the outputs and run the norm and rotation; returns (q_out, k_out), contiguous.
+
+    q [B, N, Hq, d], k [B, N, Hk, d]; weights [d] (None: ones); tables as from rope_tables (None: no
+    rotation); positions int32 [N] or [B, N] (None: 0 .. N - 1)."""
+    return _norm_rope_fwd(q, k, None, None, q_weight, k_weight, cos, sin, positions, eps, interleaved, None)
+
+
+@lru_cache(maxsize=None)
 def fa_qk_norm_rope_bwd_workspace_size(d: int) -> int:
     return int(load_library().fa_qk_norm_rope_bwd_workspace_size(int(d)))
+
+
+def _weight_grad(g, w, dev: int, name: str):
+    if g is None or w is None:
+        if g is not w:
+            raise ValueError(f"{name} must be None exactly where its weight is")
+        return None
+    if g.dtype is not w.dtype or g.shape != w.shape or g.get_device() != dev or not g.is_contiguous():
+        raise ValueError(f"{name} must match its weight")
+    return g.data_ptr()
 
 
 def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, q_weight=None, k_weight=None,
                         cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, stream=None):
     """Its backward through the C ABI: fills dq, dk and, where there are weights, dq_weight and dk_weight.
     ``workspace`` is a uint8 CUDA tensor of fa_qk_norm_rope_bwd_workspace_size(d) bytes."""
-    rot, rows, wt, ptrs = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    B, N, Hq, d = q.shape
-    st = [_rows_layout(t, s.shape, q, name) for name, t, s in (
-        ("q", q, q), ("k", k, k), ("dq_out", dq_out, q), ("dk_out", dk_out, k), ("dq", dq, q), ("dk", dk, k))]
-    if tuple(k.shape) != (B, N, k.shape[2], d):
-        raise ValueError("q and k must share batch, length and head dimension")
-    for name, g, w in (("dq_weight", dq_weight, q_weight), ("dk_weight", dk_weight, k_weight)):
-        if (g is None) != (w is None) or (g is not None and (g.dtype != w.dtype or g.shape != w.shape or
-                                                             g.device != w.device or not g.is_contiguous())):
-            raise ValueError(f"{name} must match its weight (None for None)")
-    _on_device(workspace, q, "workspace")
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _check(load_library().fa_qk_norm_rope_bwd(
-        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), *ptrs[:2],
-        ptr(dq_weight), ptr(dk_weight), *ptrs[2:], *_positions(positions, q), B, N, Hq, k.shape[2], d, rot,
-        int(interleaved), rows, *st, _TORCH_TO_FA[q.dtype], wt, float(eps), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
-
-
-def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
-                         interleaved=False):
-    """Allocate the outputs and run the norm and rotation; returns (q_out, k_out), contiguous."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    fa_qk_norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    return q_out, k_out
+    shape, dtype, dev = _new_tensor(q, "q")
+    B, N, Hq, d = shape
+    kshape = k.shape
+    if len(kshape) != 4 or kshape[0] != B or kshape[1] != N or kshape[3] != d:
+        raise ValueError(f"k must be [{B}, {N}, Hk, {d}] as q is {list(shape)}")
+    rot, rows, wt, (qw, kw, cp, sp) = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
+    _check((_lib or load_library()).fa_qk_norm_rope_bwd(
+        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), qw, kw,
+        _weight_grad(dq_weight, q_weight, dev, "dq_weight"), _weight_grad(dk_weight, k_weight, dev, "dk_weight"), cp,
+        sp, *_positions(positions, B, N, dev), B, N, Hq, kshape[2], d, rot, interleaved, rows,
+        _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k"),
+        _rows_layout(dq_out, shape, dtype, dev, "dq_out"), _rows_layout(dk_out, kshape, dtype, dev, "dk_out"),
+        _rows_layout(dq, shape, dtype, dev, "dq"), _rows_layout(dk, kshape, dtype, dev, "dk"), _TORCH_TO_FA[dtype], wt,
+        eps, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
                           eps=1e-6, interleaved=False):
     """Allocate the gradients and the workspace and run the backward; returns
     (dq, dk, dq_weight, dk_weight), contiguous, None for a weight that is None."""
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    dk = torch.empty_like(k, memory_format=torch.contiguous_format)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
-    ws = torch.empty(fa_qk_norm_rope_bwd_workspace_size(q.shape[3]), dtype=torch.uint8, device=q.device)
+    ws = torch.empty(fa_qk_norm_rope_bwd_workspace_size(q.shape[-1]), dtype=torch.uint8, device=q.device)
     fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dqw, dkw, ws, q_weight, k_weight, cos, sin, positions, eps,
                         interleaved)
     return dq, dk, dqw, dkw
@@ -725,36 +769,31 @@ def kv8_cache_alloc(num_pages: int, page_size: int, H: int, d: int, device="cuda
     return Kv8Cache(k, v, k_scale, v_scale)
 
 
-def _kv8_args(cache: Kv8Cache, ref: torch.Tensor, block_table, seq_lens, new_lens):
-    """The two C structs of a cache and its sequences, for new tokens ``ref`` [B, T, *, d]."""
-    if ref.dim() != 4:
-        raise ValueError("new queries, keys and values are [B, T, H, d]")
-    _current_cuda(ref, "the new tokens' tensors")
-    if ref.dtype == torch.float32:
+def _kv8_args(cache: Kv8Cache, B: int, d: int, dtype, dev: int, block_table, seq_lens, new_lens):
+    """The two C structs of a cache and its sequences, for new tokens [B, T, *, d]."""
+    if dtype is torch.float32:
         raise ValueError("the 8-bit cache takes float16 or bfloat16 tensors")
     k, v, ks, vs = cache
-    if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype or v.shape != k.shape or \
-            v.stride() != k.stride() or k.stride(3) != 1:
+    shape, st = k.shape, k.stride()
+    if len(shape) != 4 or k.dtype is not torch.float8_e4m3fn or v.dtype is not torch.float8_e4m3fn or \
+            v.shape != shape or v.stride() != st or st[3] != 1:
         raise ValueError("cache.k and cache.v must be float8_e4m3fn [num_pages, page_size, H, d] of the same "
                          "strides with a contiguous head dimension")
-    P, page, H, d = k.shape
-    for name, s in (("k_scale", ks), ("v_scale", vs)):
-        if s.dtype != torch.float32 or tuple(s.shape) != (P, H) or not s.is_contiguous() or s.device != ref.device:
-            raise ValueError(f"cache.{name} must be a contiguous float32 [{P}, {H}] tensor on {ref.device}")
-    if k.device != ref.device or v.device != ref.device:
-        raise ValueError(f"the cache must live on {ref.device}")
-    B = ref.shape[0]
-    if ref.shape[3] != d:
-        raise ValueError(f"the cache holds heads of {d}, the new tokens' tensors of {ref.shape[3]}")
+    P, page, H, dc = shape
+    if k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"the cache must live on cuda:{dev}")
+    for s in (ks, vs):
+        if s.dtype is not torch.float32 or s.shape != (P, H) or not s.is_contiguous() or s.get_device() != dev:
+            raise ValueError(f"the cache's scales must be contiguous float32 [{P}, {H}] tensors on cuda:{dev}")
+    if dc != d:
+        raise ValueError(f"the cache holds heads of {dc}, the new tokens' tensors of {d}")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    st = k.stride()
-    c = _Kv8CacheArg(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, page, H, d,
-                     FaStrides(st[0], st[1], st[2]))
-    s = _Kv8SeqsArg(_int32(block_table, (B, block_table.shape[1]), ref, "block_table"), block_table.stride(0),
-                    _int32(seq_lens, (B,), ref, "seq_lens"), _int32(new_lens, (B,), ref, "new_lens"), B,
-                    block_table.shape[1])
-    return c, s
+    pages = block_table.shape[1]
+    return (_Kv8CacheArg(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, page, H, d,
+                         _strides(st[0], st[1], st[2])),
+            _Kv8SeqsArg(_int32(block_table, (B, pages), dev, "block_table"), block_table.stride(0),
+                        _int32(seq_lens, (B,), dev, "seq_lens"), _int32(new_lens, (B,), dev, "new_lens"), B, pages))
 
 
 def kv8_append(cache: Kv8Cache, k, v, block_table, seq_lens, new_lens=None, stream=None):
@@ -763,57 +802,91 @@ def kv8_append(cache: Kv8Cache, k, v, block_table, seq_lens, new_lens=None, stre
     ``seq_lens`` (int32 [B]) counts the new tokens already; they are the last ``new_lens``
     (int32 [B], None: T) of each sequence, further rows of k and v are padding. Token j of
     sequence b lies in page ``block_table[b, j // page_size]`` (int32 [B, max_pages])."""
-    c, s = _kv8_args(cache, k, block_table, seq_lens, new_lens)
-    shape = (k.shape[0], k.shape[1], c.H, c.d)
-    _check(load_library().fa_kv8_append(
-        c, s, k.data_ptr(), v.data_ptr(), k.shape[1], _rows_layout(k, shape, k, "k"), _rows_layout(v, shape, k, "v"),
-        _TORCH_TO_FA[k.dtype], _stream(stream)))
+    shape, dtype, dev = _new_tensor(k, "k")
+    B, T, _, d = shape
+    c, s = _kv8_args(cache, B, d, dtype, dev, block_table, seq_lens, new_lens)
+    shape = (B, T, c.H, d)
+    _check((_lib or load_library()).fa_kv8_append(
+        c, s, k.data_ptr(), v.data_ptr(), T, _rows_layout(k, shape, dtype, dev, "k"),
+        _rows_layout(v, shape, dtype, dev, "v"), _TORCH_TO_FA[dtype], _stream(stream)))
+
+
+def _norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
+                      interleaved, stream):
+    shape, dtype, dev = _new_tensor(q, "q")
+    B, T, Hq, d = shape
+    c, s = _kv8_args(cache, B, d, dtype, dev, block_table, seq_lens, new_lens)
+    rot, rows, wt, ptrs = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
+    kshape = (B, T, c.H, d)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        qo_st = _strides(T * Hq * d, Hq * d, d)
+    else:
+        qo_st = _rows_layout(q_out, shape, dtype, dev, "q_out")
+    _check((_lib or load_library()).fa_kv8_norm_rope_append(
+        c, s, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *ptrs, T, Hq, rot, interleaved, rows,
+        _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k"),
+        _rows_layout(v, kshape, dtype, dev, "v"), qo_st, _TORCH_TO_FA[dtype], wt, eps, _stream(stream)))
+    return q_out
 
 
 def fa_kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens,
                             new_lens=None, eps=1e-6, interleaved=False, stream=None):
     """Norm and rotation of new q and k, then k and v into the cache, through the C ABI: fills q_out."""
-    c, s = _kv8_args(cache, q, block_table, seq_lens, new_lens)
-    rot, rows, wt, ptrs = _rope_args(q, k, q_weight, k_weight, cos, sin)
-    B, T, Hq, d = q.shape
-    shape = (B, T, c.H, d)
-    _check(load_library().fa_kv8_norm_rope_append(
-        c, s, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *ptrs, T, Hq, rot, int(interleaved), rows,
-        _rows_layout(q, q.shape, q, "q"), _rows_layout(k, shape, q, "k"), _rows_layout(v, shape, q, "v"),
-        _rows_layout(q_out, q.shape, q, "q_out"), _TORCH_TO_FA[q.dtype], wt, float(eps), _stream(stream)))
+    _norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
+                      interleaved, stream)
 
 
 def kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens=None,
                          eps=1e-6, interleaved=False):
     """qk_norm_rope_forward of new q and k at their positions and kv8_append of the result in one
     launch; returns the normed and rotated q (zeros in padding rows)."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    fa_kv8_norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
-                            interleaved)
-    return q_out
+    return _norm_rope_append(cache, q, k, v, None, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
+                             interleaved, None)
 
 
 def fa_kv8_attn_workspace_size(B: int, T: int, Hq: int, H: int, d: int, page_size: int, max_pages: int,
                                max_seqlen: int, causal: bool = True, window: int = 0) -> int:
-    return int(load_library().fa_kv8_attn_workspace_size(B, T, Hq, H, d, page_size, max_pages, int(max_seqlen),
-                                                         int(causal), int(window)))
+    return load_library().fa_kv8_attn_workspace_size(B, T, Hq, H, d, page_size, max_pages, int(max_seqlen),
+                                                     int(causal), int(window))
+
+
+def _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, new_lens, scale, causal, window,
+              alibi_slopes, stream):
+    shape, dtype, dev = _new_tensor(q, "q")
+    B, T, Hq, d = shape
+    c, s = _kv8_args(cache, B, d, dtype, dev, block_table, seq_lens, new_lens)
+    lib = _lib or load_library()
+    q_st = _rows_layout(q, shape, dtype, dev, "q")
+    if o is None:
+        size = lib.fa_kv8_attn_workspace_size(B, T, Hq, c.H, d, c.page_size, s.max_pages, max_seqlen, causal, window)
+        device = q.device
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        o_st = _strides(T * Hq * d, Hq * d, d)
+    else:
+        o_st = _rows_layout(o, shape, dtype, dev, "o")
+        if lse.dtype is not torch.float32 or lse.shape != (B, Hq, T) or not lse.is_contiguous() or \
+                lse.get_device() != dev:
+            raise ValueError(f"lse must be a contiguous float32 [B, Hq, T] tensor on cuda:{dev}")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
+        size = workspace.numel() * workspace.element_size()
+    slopes, per_seq = (None, 0) if alibi_slopes is None else _alibi(alibi_slopes, B, Hq, q.device)
+    _check(lib.fa_kv8_attn(
+        c, s, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T, Hq, max_seqlen, q_st, o_st, _TORCH_TO_FA[dtype],
+        default_scale(d) if scale is None else scale, causal, window, slopes, per_seq, workspace.data_ptr(), size,
+        _stream(stream)))
+    return o, lse
 
 
 def fa_kv8_attn(q, cache: Kv8Cache, o, lse, block_table, seq_lens, max_seqlen, workspace, new_lens=None, scale=None,
                 causal=True, window=0, alibi_slopes=None, stream=None):
     """Attention over the cache through the C ABI: fills o ([B, T, Hq, d]) and lse ([B, Hq, T] fp32).
     ``workspace`` is a uint8 CUDA tensor of fa_kv8_attn_workspace_size(...) bytes."""
-    c, s = _kv8_args(cache, q, block_table, seq_lens, new_lens)
-    B, T, Hq, d = q.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, T) or not lse.is_contiguous() or \
-            lse.device != q.device:
-        raise ValueError(f"lse must be a contiguous float32 [B, Hq, T] tensor on {q.device}")
-    _on_device(workspace, q, "workspace")
-    _check(load_library().fa_kv8_attn(
-        c, s, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T, Hq, int(max_seqlen), _rows_layout(q, q.shape, q, "q"),
-        _rows_layout(o, q.shape, q, "o"), _TORCH_TO_FA[q.dtype], default_scale(d) if scale is None else float(scale),
-        int(causal), int(window), *_alibi(alibi_slopes, B, Hq, q.device), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, new_lens, scale, causal, window,
+              alibi_slopes, stream)
 
 
 def kv8_attention(q, cache: Kv8Cache, block_table, seq_lens, max_seqlen, new_lens=None, scale=None, causal=True,
@@ -823,12 +896,5 @@ def kv8_attention(q, cache: Kv8Cache, block_table, seq_lens, max_seqlen, new_len
     The queries belong to the last ``new_lens`` tokens of each sequence (as for kv8_append, which
     comes first: a token attends to itself through the cache). Hq must be a multiple of the
     cache's heads. ``max_seqlen`` is an upper bound of ``seq_lens``."""
-    B, T, Hq, d = q.shape
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    ws = torch.empty(fa_kv8_attn_workspace_size(B, T, Hq, cache.k.shape[2], d, cache.k.shape[1],
-                                                block_table.shape[1], max_seqlen, causal, window),
-                     dtype=torch.uint8, device=q.device)
-    fa_kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, ws, new_lens, scale, causal, window,
-                alibi_slopes)
-    return o, lse
+    return _kv8_attn(q, cache, None, None, block_table, seq_lens, max_seqlen, None, new_lens, scale, causal, window,
+                     alibi_slopes, None)

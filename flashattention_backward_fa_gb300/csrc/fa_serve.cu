@@ -334,8 +334,9 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
   p.key_limit = (int)std::min<long long>(max_seqlen, (long long)seqs->max_pages << shift);
   p.chunk = plan.chunk;
   p.splits = plan.splits;
+  p.cluster = plan.cluster;
   p.row_tiles = plan.row_tiles;
-  if (plan.splits > 1) {
+  if (plan.splits > 1 && !plan.cluster) {
     const size_t rows = (size_t)seqs->B * Hq * T * plan.splits;
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o + rows * cache->d;

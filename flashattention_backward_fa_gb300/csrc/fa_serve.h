@@ -2,10 +2,43 @@
 // key/value cache, shared by their C entry points (fa_serve.cu) and kernels.
 #pragma once
 
+#include <atomic>
+
 #include "fa_host.h"
 #include "fa_internal.h"
 
 namespace fa {
+
+// Raises a kernel's limit of dynamic shared memory to `bytes`, once per kernel and device (the
+// default limit, 48 KB, includes the kernel's static part).
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0ull};
+  if (bytes <= 32 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev > 63) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  if (done.load(std::memory_order_relaxed) >> dev & 1ull) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
+// Launches a kernel that may begin while the one before it in the stream ends (it waits for that
+// one's outputs itself, with griddepcontrol.wait).
+template <typename Params>
+cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads, const Params& p, cudaStream_t st) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 // One of q and k: x [B, N, H, d], forward output (backward: the gradient that
 // comes in, `dout`, with out_st its strides) and the backward's outputs.
@@ -18,6 +51,7 @@ struct RopeSide {
   void* dw;
   fa_strides x_st, out_st, dx_st;
   int H;
+  int span;  // set by the launcher: consecutive rows of a row group
 };
 
 struct RopeParams {
@@ -77,7 +111,8 @@ struct Kv8AppendParams {
   const float* sin;
   int rot, max_pos, neighbours, w_f32;
   float eps;
-  int kv_blocks;  // set by the launcher: blocks [0, kv_blocks) take the cache's pages, the others q's rows
+  // set by the launcher: blocks [0, kv_blocks) take the cache's pages, the others q's rows, q_span a row group
+  int kv_blocks, q_span;
 };
 cudaError_t launch_kv8_append(Kv8AppendParams& p, bool bf16, cudaStream_t st);
 
@@ -95,6 +130,7 @@ struct Kv8AttnParams {
   int key_limit;  // keys past it are never attended: min(max_seqlen, max_pages * page size)
   int chunk;      // keys of a split (a multiple of 64)
   int splits;     // most splits of a sequence
+  int cluster;    // the splits are the blocks of a cluster, which joins them (chunk does not apply)
   int row_tiles;
   float* part_o;   // [B, H, T * G, splits, d]: normalised outputs of the splits
   float* part_lse;  // [B, H, T * G, splits]: their log2-sum-exp2
@@ -103,7 +139,7 @@ struct Kv8AttnParams {
 struct Kv8AttnPlan {
   int tiles;      // 8-row query tiles of a block (1, 2 or 4)
   int row_tiles;  // blocks that share the T * G rows of a key head
-  int chunk, splits;
+  int chunk, splits, cluster;
   size_t workspace;
 };
 Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window);

@@ -27,6 +27,7 @@ namespace fa {
 
 namespace {
 
+constexpr int kQDepth = 3;    // rows of q a row group has on their way, and the one at hand
 constexpr int kMinExp = -100;  // least scale exponent: blocks of zeros (or below 2^-91) get it
 
 // The scale's bits for a largest finite magnitude: 448 = 1.75 * 2^8.
@@ -94,14 +95,20 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
 // finite value is never beyond 448 times the scale).
 template <typename T, bool kAny>
 __device__ __forceinline__ uint2 quantise8(const Raw8<T>& raw, float inv) {
-  float f[8];
-  raw.unpack(f);
+  uint64_t v[4];
+  raw.unpack(v);
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[i] *= inv;
-    if (kAny && fabsf(f[i]) == INFINITY) f[i] = __int_as_float(0x7FC00000);
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f2_mul(v[i], f2_pack(inv, inv)), lo, hi);
+    if (kAny) {
+      if (fabsf(lo) == INFINITY) lo = __int_as_float(0x7FC00000);
+      if (fabsf(hi) == INFINITY) hi = __int_as_float(0x7FC00000);
+    }
+    c[i] = e4m3x2(lo, hi);
   }
-  return make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16), e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 struct NewTokens {
@@ -122,35 +129,22 @@ __device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T)
 // rot / 2 apart / neighbours.
 template <typename T, int D, int kRows, int kNorm>
 __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
-  constexpr int G = D / 8;
-  constexpr bool kNeighbours = kNorm == 2;
+  extern __shared__ __align__(16) unsigned char ring[];  // (q's rows only)
+  constexpr int G = D / 16;
+  constexpr bool kNeighbours = kNorm != 1;
   __shared__ uint32_t red[8];
   const Kv8Cache& c = p.c;
-  const int lane = threadIdx.x & 31, e0 = (lane % G) * 8;
+  __shared__ __align__(16) float w[D];
   if (kNorm != 0 && blockIdx.x >= (unsigned)p.kv_blocks) {
-    // q: one row (b, t, head) a row group; rows without a token become zeros
-    const long long rows = (long long)p.B * p.T * p.Hq;
-    const long long row = (long long)(blockIdx.x - p.kv_blocks) * (blockDim.x / G) + threadIdx.x / G;
-    const bool inside = row < rows;
-    const int h = inside ? (int)(row % p.Hq) : 0;
-    const long long bt = inside ? row / p.Hq : 0;
-    const int b = (int)(bt / p.T), t = (int)(bt - (long long)b * p.T);
-    const NewTokens n = new_tokens(c, b, p.T);
-    const bool live = inside && t < n.count && n.start + t >= 0;
-    const int partner = partner_lane<kNeighbours>(lane, e0, p.rot);
-    Raw8<T> raw;
-    raw.zero();
-    if (live) raw.load(static_cast<const T*>(p.q) + b * p.q_st.b + t * p.q_st.n + h * p.q_st.h + e0);
-    float w[8], w_p[8], cc[8], ss[8], out[8];
-    load_weight8<T>(p.q_w, p.w_f32, e0, w);
-    load_weight8<T>(p.q_w, p.w_f32, (partner % G) * 8, w_p);
-    const long long at = live ? (long long)min(n.start + t, p.max_pos - 1) * (p.rot >> 1) : 0;
-    load_rotation<kNeighbours>(p.cos + at, p.sin + at, e0, live ? p.rot : 0, cc, ss);
-    norm_rope_chunk<T, D, kNeighbours>(raw, partner, w, w_p, cc, ss, p.eps, out);
-    if (inside) {
-      if (live) raw.pack(out);  // (else the zeros)
-      raw.store(static_cast<T*>(p.q_out) + b * p.q_out_st.b + t * p.q_out_st.n + h * p.q_out_st.h + e0);
-    }
+    // q: q_span rows (b, t, head) a row group; rows without a token become zeros
+    const long long group = (long long)(blockIdx.x - p.kv_blocks) * (blockDim.x / G) + threadIdx.x / G;
+    norm_rope_rows<T, D, kNeighbours, true, kQDepth>(
+        ring, static_cast<const T*>(p.q), static_cast<T*>(p.q_out), p.q_st, p.q_out_st, (long long)p.B * p.T * p.Hq, p.T,
+        p.Hq, group * p.q_span, p.q_span, p.q_w, p.w_f32, w, p.cos, p.sin, p.rot, p.eps, [&](long long b, int t) {
+          const NewTokens n = new_tokens(c, (int)b, p.T);
+          return t < n.count && n.start + t >= 0 ? (long long)min(n.start + t, max(p.max_pos - 1, 0)) * (p.rot >> 1)
+                                                 : -1ll;
+        });
     return;
   }
   unsigned x = blockIdx.x;
@@ -175,41 +169,45 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
   const fa_strides& st = is_v ? p.v_st : p.k_st;
   const T* src = static_cast<const T*>(is_v ? p.v : p.k) + b * st.b + (long long)(t_lo - n.start) * st.n + h * st.h;
   const int groups = blockDim.x / G, row0 = threadIdx.x / G;
-  Raw8<T> raw[kRows];
+  const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % G, p.rot);
+  Raw8<T> ra[kRows], rb[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = row0 + i * groups;
-    raw[i].zero();
-    if (r < rows) raw[i].load(src + r * st.n + e0);
+    zero8(ra[i]);
+    zero8(rb[i]);
+    if (r < rows) {
+      load8(ra[i], src + r * st.n + at.a);
+      load8(rb[i], src + r * st.n + at.b);
+    }
   }
   uint8_t* page = (is_v ? c.v : c.k) + id * c.sp + h * c.sh;
   float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)id * c.H + h;
   const float was = slot0 > 0 ? *scale_at : 0.f;  // a page without earlier tokens has no former scale
   if (kNorm != 0 && !is_v) {
-    const int partner = partner_lane<kNeighbours>(lane, e0, p.rot);
-    float w[8], w_p[8];
-    load_weight8<T>(p.k_w, p.w_f32, e0, w);
-    load_weight8<T>(p.k_w, p.w_f32, (partner % G) * 8, w_p);
+    stage_weights<T>(p.k_w, p.w_f32, D, w);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = row0 + i * groups;
       const bool live = r < rows;
-      float cc[8], ss[8], out[8];
-      const long long at = live ? (long long)min(t_lo + r, p.max_pos - 1) * (p.rot >> 1) : 0;
-      load_rotation<kNeighbours>(p.cos + at, p.sin + at, e0, live ? p.rot : 0, cc, ss);
-      norm_rope_chunk<T, D, kNeighbours>(raw[i], partner, w, w_p, cc, ss, p.eps, out);
-      if (live) raw[i].pack(out);
+      const long long row = live ? (long long)min(t_lo + r, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
+      float cc[8], ss[8];
+      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, live ? p.rot : 0, cc, ss);
+      Factors f;
+      fold_weights<kNeighbours>(w, at, cc, ss, f);
+      norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], f, p.eps);  // (zeros stay zeros)
     }
   }
   uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) m = max(m, amax_bits<T, false>(raw[i].a));
+  for (int i = 0; i < kRows; ++i) m = max(m, max(amax_bits<T, false>(ra[i].q[0]), amax_bits<T, false>(rb[i].q[0])));
   m = block_max(m, red);
   const bool any = m >= inf_bits<T>();  // infinities or NaN among the new values
   if (any) {
     m = 0u;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) m = max(m, amax_bits<T, true>(raw[i].a));
+    for (int i = 0; i < kRows; ++i) m = max(m, max(amax_bits<T, true>(ra[i].q[0]), amax_bits<T, true>(rb[i].q[0])));
     m = block_max(m, red);
   }
   const float scale = fmaxf(scale_for(h16_bits_to_f32<std::is_same<T, __nv_bfloat16>::value>(m)), was);
@@ -218,24 +216,24 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
   for (int i = 0; i < kRows; ++i) {
     const int r = row0 + i * groups;
     if (r >= rows) continue;
-    const uint2 q = any ? quantise8<T, true>(raw[i], inv) : quantise8<T, false>(raw[i], inv);
-    *reinterpret_cast<uint2*>(page + (slot0 + r) * c.sn + e0) = q;
+    uint8_t* to = page + (slot0 + r) * c.sn;
+    *reinterpret_cast<uint2*>(to + at.a) = any ? quantise8<T, true>(ra[i], inv) : quantise8<T, false>(ra[i], inv);
+    *reinterpret_cast<uint2*>(to + at.b) = any ? quantise8<T, true>(rb[i], inv) : quantise8<T, false>(rb[i], inv);
   }
-  if (slot0 > 0 && scale != was) {  // earlier tokens to the larger scale
+  if (slot0 > 0 && scale != was) {  // earlier tokens to the larger scale, 16 codes a thread
     const float ratio = was * inv;
     for (int r = row0; r < slot0; r += groups) {
-      uint2* at = reinterpret_cast<uint2*>(page + r * c.sn + e0);
-      const uint2 q = *at;
-      const uint32_t in[2] = {q.x, q.y};
-      uint32_t to[2];
+      uint4* to = reinterpret_cast<uint4*>(page + r * c.sn) + threadIdx.x % G;
+      const uint4 q = *to;
+      uint32_t v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         float f[4];
-        unpack_e4m3x2(in[i] & 0xFFFFu, f[0], f[1]);
-        unpack_e4m3x2(in[i] >> 16, f[2], f[3]);
-        to[i] = e4m3x2(f[0] * ratio, f[1] * ratio) | (e4m3x2(f[2] * ratio, f[3] * ratio) << 16);
+        unpack_e4m3x2(v[i] & 0xFFFFu, f[0], f[1]);
+        unpack_e4m3x2(v[i] >> 16, f[2], f[3]);
+        v[i] = e4m3x2(f[0] * ratio, f[1] * ratio) | (e4m3x2(f[2] * ratio, f[3] * ratio) << 16);
       }
-      *at = make_uint2(to[0], to[1]);
+      *to = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
   // (every thread has read the former scale: block_max synchronised since)
@@ -244,35 +242,35 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
 
 template <typename T, int D, int kRows>
 cudaError_t launch_rows(const Kv8AppendParams& p, unsigned grid, int threads, cudaStream_t st) {
+  const int ring = RowRing<T, 2, kQDepth>::bytes(threads);
   if (p.q == nullptr)
     kv8_append_kernel<T, D, kRows, 0><<<grid, threads, 0, st>>>(p);
   else if (!p.neighbours)
-    kv8_append_kernel<T, D, kRows, 1><<<grid, threads, 0, st>>>(p);
+    kv8_append_kernel<T, D, kRows, 1><<<grid, threads, ring, st>>>(p);
   else
-    kv8_append_kernel<T, D, kRows, 2><<<grid, threads, 0, st>>>(p);
+    kv8_append_kernel<T, D, kRows, 2><<<grid, threads, ring, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_d(Kv8AppendParams& p, cudaStream_t st) {
-  constexpr int G = D / 8;
+  constexpr int G = D / 16;
   const int rows = std::min(1 << p.c.page_shift, p.T);  // most new rows of one page
   // up to 256 threads, then more rows a thread; at least two warps, so that a
   // single token still shares out the rescaling of its page
   const int lanes = rows * G;
-  const int per = lanes <= 256 ? 1 : lanes <= 512 ? 2 : lanes <= 1024 ? 4 : 8;
+  const int per = lanes <= 256 ? 1 : lanes <= 512 ? 2 : 4;
   const int threads = std::max(64, ((lanes + per - 1) / per + 31) / 32 * 32);
   const long long kv = (long long)p.B * p.pages * 2 * p.c.H;
-  const long long q = p.q ? ((long long)p.B * p.T * p.Hq + threads / G - 1) / (threads / G) : 0;
+  // q: one row a group up to a resident set of blocks, then more rows a group
+  const long long q_rows = p.q ? (long long)p.B * p.T * p.Hq : 0, groups = threads / G;
+  p.q_span = (int)std::max<long long>(1, std::min<long long>(16, q_rows / (groups * 152 * 8)));
+  const long long q = (q_rows + groups * p.q_span - 1) / (groups * p.q_span);
   if (kv + q > 0x7fffffffll) return cudaErrorInvalidValue;
   p.kv_blocks = (int)kv;
   const unsigned grid = (unsigned)(kv + q);
-  switch (per) {
-    case 1: return launch_rows<T, D, 1>(p, grid, threads, st);
-    case 2: return launch_rows<T, D, 2>(p, grid, threads, st);
-    case 4: return launch_rows<T, D, 4>(p, grid, threads, st);
-    default: return launch_rows<T, D, 8>(p, grid, threads, st);
-  }
+  if (per == 1) return launch_rows<T, D, 1>(p, grid, threads, st);
+  return per == 2 ? launch_rows<T, D, 2>(p, grid, threads, st) : launch_rows<T, D, 4>(p, grid, threads, st);
 }
 
 }  // namespace

@@ -11,7 +11,7 @@
 //
 // Both are bound by memory: about 30 (forward) and 80 (backward) operations an
 // element against 4 and 6 bytes. The row is in registers between its one load
-// and its one store, and every lane has several rows' loads in flight.
+// and its one store, and several rows' loads are in flight to shared memory.
 #include <algorithm>
 
 #include "fa_serve.h"
@@ -22,197 +22,187 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kFwdRows = 4;  // consecutive rows a row group of the forward takes
-constexpr int kBwdRows = 2;  // rows a row group of the backward loads at a time
-constexpr int kBwdBlocks = 152 * 3;  // most blocks of the backward (and rows of partial weight gradients)
+constexpr int kFwdDepth = 3;          // rows a row group of the forward has on their way, and the one at hand
+constexpr int kBwdDepth = 2;          // the same of the backward (x and dout each)
+constexpr int kFwdBlocks = 152 * 12;  // four resident sets of blocks: ragged ends even out
+constexpr int kBwdBlocks = 152 * 2;   // one resident set: every block adds a row of partial sums
 
-// Row `row` of a [B, N, H] enumeration; next() moves to the row after it. The
-// divisions are 32-bit wherever the row number is (a 64-bit division costs as
-// much as the rest of a row's index arithmetic together).
-struct RowAt {
-  long long b;
-  int n, head;
-  __device__ __forceinline__ RowAt(long long row, int N, int H) {
-    long long token;
-    if (row >> 32) {
-      token = row / H;
-      b = token / N;
-    } else {
-      token = (unsigned)row / (unsigned)H;
-      b = (unsigned)token / (unsigned)N;
-    }
-    head = (int)(row - token * H);
-    n = (int)(token - b * N);
-  }
-  __device__ __forceinline__ void next(int N, int H) {
-    if (++head < H) return;
-    head = 0;
-    if (++n < N) return;
-    n = 0;
-    ++b;
-  }
-  __device__ __forceinline__ long long offset(const fa_strides& st) const {
-    return b * st.b + (long long)n * st.n + (long long)head * st.h;
-  }
-};
-
-// The token's row in the tables: its position, clamped into them.
-__device__ __forceinline__ long long table_row(const RopeParams& p, const RowAt& a) {
-  const int pos = p.positions ? __ldg(p.positions + a.b * p.pos_stride + a.n) : a.n;
+// The token's rows in the tables: its position, clamped into them.
+__device__ __forceinline__ long long table_row(const RopeParams& p, long long b, int n) {
+  const int pos = p.positions ? __ldg(p.positions + b * p.pos_stride + n) : n;
   return (long long)min(max(pos, 0), p.max_pos - 1) * (p.rot >> 1);
 }
 
 template <typename T, int D, bool kNeighbours>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int G = D / 8;
-  const int lane = threadIdx.x & 31, e0 = (lane % G) * 8;
+__global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ __align__(16) float w[D];
   const bool is_k = blockIdx.x >= (unsigned)p.q_blocks;
   const RopeSide& sd = is_k ? p.k : p.q;
-  const long long rows = (long long)p.B * p.N * sd.H;
-  const long long first =
-      ((long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * (kRopeThreads / G) + threadIdx.x / G) * kFwdRows;
-  const int partner = partner_lane<kNeighbours>(lane, e0, p.rot);
-  Raw8<T> raw[kFwdRows];
-  RowAt a(first, p.N, sd.H);
-  const RowAt a0 = a;
-#pragma unroll
-  for (int r = 0; r < kFwdRows; ++r) {
-    raw[r].zero();
-    if (first + r < rows) raw[r].load(static_cast<const T*>(sd.x) + a.offset(sd.x_st) + e0);
-    a.next(p.N, sd.H);
-  }
-  float w[8], w_p[8], c[8], s[8];
-  load_weight8<T>(sd.w, p.w_f32, e0, w);
-  load_weight8<T>(sd.w, p.w_f32, (partner % G) * 8, w_p);
-  a = a0;
-#pragma unroll
-  for (int r = 0; r < kFwdRows; ++r) {
-    const bool live = first + r < rows;
-    if (r == 0 || a.head == 0) {  // a new token
-      const long long at = live && p.rot ? table_row(p, a) : 0;
-      load_rotation<kNeighbours>(p.cos + at, p.sin + at, e0, live ? p.rot : 0, c, s);
-    }
-    float out[8];
-    norm_rope_chunk<T, D, kNeighbours>(raw[r], partner, w, w_p, c, s, p.eps, out);
-    if (live) {
-      raw[r].pack(out);
-      raw[r].store(static_cast<T*>(sd.out) + a.offset(sd.out_st) + e0);
-    }
-    a.next(p.N, sd.H);
-  }
+  const long long group =
+      (long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * (kRopeThreads / (D / 16)) + threadIdx.x / (D / 16);
+  norm_rope_rows<T, D, kNeighbours, false, kFwdDepth>(
+      ring, static_cast<const T*>(sd.x), static_cast<T*>(sd.out), sd.x_st, sd.out_st, (long long)p.B * p.N * sd.H, p.N,
+      sd.H, group * sd.span, sd.span, sd.w, p.w_f32, w, p.cos, p.sin, p.rot, p.eps,
+      [&](long long b, int n) { return p.rot ? table_row(p, b, n) : 0ll; });
 }
 
+// Each row group takes sd.span consecutive rows, as in the forward; its lanes
+// keep the weight gradients of their columns.
 template <typename T, int D, bool kNeighbours>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int G = D / 8, kGroups = kRopeThreads / G;
-  __shared__ float sums[kGroups][D];
-  const int lane = threadIdx.x & 31, e0 = (lane % G) * 8, group = threadIdx.x / G;
+__global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int G = D / 16, kGroups = kRopeThreads / G;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(16) float w[D];
+  const RowRing<T, 4, kBwdDepth> ring(smem);
+  const int group = threadIdx.x / G;
   const bool is_k = blockIdx.x >= (unsigned)p.q_blocks;
   const RopeSide& sd = is_k ? p.k : p.q;
-  const int blk = blockIdx.x - (is_k ? p.q_blocks : 0), blks = is_k ? gridDim.x - p.q_blocks : p.q_blocks;
   const long long rows = (long long)p.B * p.N * sd.H;
-  const int partner = partner_lane<kNeighbours>(lane, e0, p.rot);
-  float w[8], dw[8], c[8], s[8];
-  load_weight8<T>(sd.w, p.w_f32, e0, w);
+  const long long first = ((long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * kGroups + group) * sd.span;
+  const int live = (int)min((long long)sd.span, max(rows - first, 0ll));
+  const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % G, p.rot);
+  RowWalk wx, wg, wo;
+  wx.start(first, p.N, sd.H, sd.x_st);
+  wg.start(first, p.N, sd.H, sd.out_st);
+  wo.start(first, p.N, sd.H, sd.dx_st);
+  uint64_t dwa[4], dwb[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
-  const long long step = (long long)blks * kGroups * kBwdRows;
-  // every lane of a warp runs the same number of turns (the shuffles need all of them)
-  for (long long base = (long long)blk * kGroups * kBwdRows; base < rows; base += step) {
-    const long long first = base + (long long)group * kBwdRows;
-    Raw8<T> raw[kBwdRows], grad[kBwdRows];
-    RowAt a(first, p.N, sd.H);
-    const RowAt a0 = a;
+  for (int i = 0; i < 4; ++i) dwa[i] = dwb[i] = 0ull;
+  float c[8], s[8];
+  int loaded = 0;
+  auto fetch = [&] {
+    const bool ok = loaded < live;
+    const T* x = static_cast<const T*>(sd.x) + (ok ? wx.at : 0);
+    const T* g = static_cast<const T*>(sd.dout) + (ok ? wg.at : 0);
+    ring.fetch(loaded, 0, x + at.a, ok);
+    ring.fetch(loaded, 1, x + at.b, ok);
+    ring.fetch(loaded, 2, g + at.a, ok);
+    ring.fetch(loaded, 3, g + at.b, ok);
+    copies_commit();
+    wx.next(p.N, sd.H, sd.x_st);
+    wg.next(p.N, sd.H, sd.out_st);
+    ++loaded;
+  };
 #pragma unroll
-    for (int r = 0; r < kBwdRows; ++r) {
-      raw[r].zero();
-      grad[r].zero();
-      if (first + r < rows) {
-        raw[r].load(static_cast<const T*>(sd.x) + a.offset(sd.x_st) + e0);
-        grad[r].load(static_cast<const T*>(sd.dout) + a.offset(sd.out_st) + e0);
-      }
-      a.next(p.N, sd.H);
+  for (int i = 0; i < kBwdDepth - 1; ++i) fetch();
+  stage_weights<T>(sd.w, p.w_f32, D, w);
+  __syncthreads();
+  bool token = true;
+  for (int i = 0; i < sd.span; ++i) {
+    fetch();
+    if (token) {
+      const bool ok = i < live;
+      const long long row = ok && p.rot ? table_row(p, wo.b, wo.n) : 0;
+      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, ok ? p.rot : 0, c, s);
     }
-    a = a0;
+    copies_wait<kBwdDepth - 1>();
+    Raw8<T> raw;
+    uint64_t xa[4], xb[4], ga[4], gb[4];
+    ring.take(i, 2, raw);
+    raw.unpack(ga);
+    ring.take(i, 3, raw);
+    raw.unpack(gb);
+    // dy = R^T dout
 #pragma unroll
-    for (int r = 0; r < kBwdRows; ++r) {
-      const bool live = first + r < rows;
-      if (r == 0 || a.head == 0) {  // a new token
-        const long long at = live && p.rot ? table_row(p, a) : 0;
-        load_rotation<kNeighbours>(p.cos + at, p.sin + at, e0, live ? p.rot : 0, c, s);
-      }
-      float x[8], g[8], dy[8];
-      raw[r].unpack(x);
-      grad[r].unpack(g);
+    for (int j = 0; j < 4; ++j) {
       if (kNeighbours) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dy[i] = fmaf(g[i], c[i], -g[i ^ 1] * s[i]);
+        const uint64_t cj = f2_pack(c[j], c[j]), sj = f2_pack(s[j], -s[j]);
+        const uint64_t ck = f2_pack(c[4 + j], c[4 + j]), sk = f2_pack(s[4 + j], -s[4 + j]);
+        ga[j] = f2_fma(ga[j], cj, f2_mul(f2_swap(ga[j]), sj));
+        gb[j] = f2_fma(gb[j], ck, f2_mul(f2_swap(gb[j]), sk));
       } else {
-        float gp[8];
-        grad[r].from_lane(partner).unpack(gp);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dy[i] = fmaf(g[i], c[i], -gp[i] * s[i]);
+        const uint64_t cj = f2_pack(c[2 * j], c[2 * j + 1]), sj = f2_pack(s[2 * j], s[2 * j + 1]);
+        const uint64_t nj = f2_pack(-s[2 * j], -s[2 * j + 1]);
+        const uint64_t da = f2_fma(ga[j], cj, f2_mul(gb[j], sj));
+        gb[j] = f2_fma(gb[j], cj, f2_mul(ga[j], nj));
+        ga[j] = da;
       }
-      float ss = 0.f, gx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(x[i], x[i], ss);
-        gx = fmaf(dy[i] * w[i], x[i], gx);
-      }
-      ss = row_sum<G>(ss);
-      gx = row_sum<G>(gx);
-      const float rr = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-      const float k1 = gx * (1.f / D) * rr;  // mean(g o xn)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xn = x[i] * rr;
-        dw[i] = fmaf(dy[i], xn, dw[i]);
-        g[i] = rr * fmaf(-xn, k1, dy[i] * w[i]);
-      }
-      if (live) {
-        raw[r].pack(g);
-        raw[r].store(static_cast<T*>(sd.dx) + a.offset(sd.dx_st) + e0);
-      }
-      a.next(p.N, sd.H);
     }
-  }
-  if (sd.w == nullptr) return;
+    ring.take(i, 0, raw);
+    raw.unpack(xa);
+    ring.take(i, 1, raw);
+    raw.unpack(xb);
+    uint64_t s2 = 0ull, g2 = 0ull, wa[4], wb[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[group][e0 + i] = dw[i];
+    for (int j = 0; j < 4; ++j) {
+      const float2 u = reinterpret_cast<const float2*>(w + at.a)[j], v = reinterpret_cast<const float2*>(w + at.b)[j];
+      wa[j] = f2_mul(ga[j], f2_pack(u.x, u.y));  // g = w o dy
+      wb[j] = f2_mul(gb[j], f2_pack(v.x, v.y));
+      s2 = f2_fma(xa[j], xa[j], f2_fma(xb[j], xb[j], s2));
+      g2 = f2_fma(wa[j], xa[j], f2_fma(wb[j], xb[j], g2));
+    }
+    const float ss = row_sum<G>(f2_sum(s2)), gx = row_sum<G>(f2_sum(g2));
+    const float rr = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+    const float k1 = -gx * (1.f / D) * rr;  // -mean(g o xn)
+    const uint64_t r2 = f2_pack(rr, rr), k2 = f2_pack(k1, k1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      xa[j] = f2_mul(xa[j], r2);
+      xb[j] = f2_mul(xb[j], r2);
+      dwa[j] = f2_fma(ga[j], xa[j], dwa[j]);
+      dwb[j] = f2_fma(gb[j], xb[j], dwb[j]);
+      wa[j] = f2_mul(r2, f2_fma(xa[j], k2, wa[j]));
+      wb[j] = f2_mul(r2, f2_fma(xb[j], k2, wb[j]));
+    }
+    if (i < live) {
+      T* dx = static_cast<T*>(sd.dx) + wo.at;
+      raw.pack(wa);
+      store8(raw, dx + at.a);
+      raw.pack(wb);
+      store8(raw, dx + at.b);
+    }
+    token = wo.next(p.N, sd.H, sd.dx_st);
+  }
+  let_next_begin();
+  if (sd.w == nullptr) return;
+  // the block's sums take the ring's place once every copy into it has landed (none is pending
+  // beyond the rows above: the last fetches were of nothing but are waited for all the same)
+  copies_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);  // [kGroups][D]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float lo, hi;
+    f2_unpack(dwa[j], lo, hi);
+    reinterpret_cast<float2*>(sums + group * D + at.a)[j] = make_float2(lo, hi);
+    f2_unpack(dwb[j], lo, hi);
+    reinterpret_cast<float2*>(sums + group * D + at.b)[j] = make_float2(lo, hi);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kRopeThreads) {
     float t = 0.f;
 #pragma unroll 8
-    for (int g = 0; g < kGroups; ++g) t += sums[g][e];
+    for (int g = 0; g < kGroups; ++g) t += sums[g * D + e];
     p.part[(long long)blockIdx.x * D + e] = t;
   }
 }
 
-// Adds the blocks' partial weight gradients: block x = side (q, k), eight
-// warps that take every eighth row, one column a lane.
+// Adds the blocks' partial weight gradients: block x = side (q, k), 32 warps
+// that take every 32nd row, one column a lane.
 template <typename T>
-__global__ void __launch_bounds__(256) weight_grad_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float sums[8][32];
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float sums[32][33];
   const bool is_k = blockIdx.x != 0;
   const RopeSide& sd = is_k ? p.k : p.q;
   if (sd.w == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.y * 32 + lane;
   const int lo = is_k ? p.q_blocks : 0, hi = is_k ? p.blocks : p.q_blocks;
+  wait_for_previous();
   float t = 0.f;
   if (e < p.d) {
-#pragma unroll 8
-    for (int r = lo + warp; r < hi; r += 8) t += p.part[(long long)r * p.d + e];
+#pragma unroll 12
+    for (int r = lo + warp; r < hi; r += 32) t += __ldcg(p.part + (long long)r * p.d + e);
   }
   sums[warp][lane] = t;
   __syncthreads();
-  if (warp == 0 && e < p.d) {
-    t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += sums[i][lane];
+  t = row_sum<32>(sums[lane][warp]);  // column `warp`
+  const int col = blockIdx.y * 32 + warp;
+  if (lane == 0 && col < p.d) {
     if (p.w_f32)
-      static_cast<float*>(sd.dw)[e] = t;
+      static_cast<float*>(sd.dw)[col] = t;
     else
-      static_cast<T*>(sd.dw)[e] = static_cast<T>(t);
+      static_cast<T*>(sd.dw)[col] = static_cast<T>(t);
   }
 }
 
@@ -231,11 +221,13 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
   const float* wv = static_cast<const float*>(sd.w);
   float dw[4] = {0.f, 0.f, 0.f, 0.f};
   for (long long row = (long long)blk * 8 + warp; row < rows; row += (long long)blks * 8) {
-    const RowAt a(row, p.N, sd.H);
-    const float* x = static_cast<const float*>(sd.x) + a.offset(sd.x_st);
-    const long long at = p.rot ? table_row(p, a) : 0;
+    RowWalk a;
+    a.start(row, p.N, sd.H, sd.x_st);
+    const auto offset = [&](const fa_strides& st) { return a.b * st.b + (long long)a.n * st.n + (long long)a.head * st.h; };
+    const float* x = static_cast<const float*>(sd.x) + a.at;
+    const long long at = p.rot ? table_row(p, a.b, a.n) : 0;
     float xv[4], gv[4], ss = 0.f;
-    const float* go = kBackward ? static_cast<const float*>(sd.dout) + a.offset(sd.out_st) : nullptr;
+    const float* go = kBackward ? static_cast<const float*>(sd.dout) + offset(sd.out_st) : nullptr;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int e = lane + 32 * j;
@@ -268,7 +260,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
     }
     __syncwarp();
     if (!kBackward) {
-      float* o = static_cast<float*>(sd.out) + a.offset(sd.out_st);
+      float* o = static_cast<float*>(sd.out) + offset(sd.out_st);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (lane + 32 * j < d) o[lane + 32 * j] = y[j];
@@ -282,7 +274,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
       }
       gx = row_sum<32>(gx);
       const float k1 = gx / d * r;
-      float* o = static_cast<float*>(sd.dx) + a.offset(sd.dx_st);
+      float* o = static_cast<float*>(sd.dx) + offset(sd.dx_st);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float xn = xv[j] * r;
@@ -304,7 +296,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
   }
 }
 
-// Whether the vector kernels cover the call: eight-value lanes need d in {64, 128}, rot a
+// Whether the vector kernels cover the call: 16-value lanes need d in {64, 128}, rot a
 // multiple of 16 and rows that start on 16 bytes (16-bit calls always meet this, the entry
 // points see to it).
 bool vector_rows(const RopeParams& p, int dtype, bool backward) {
@@ -318,90 +310,90 @@ bool vector_rows(const RopeParams& p, int dtype, bool backward) {
   return true;
 }
 
-template <typename T>
-cudaError_t launch_fwd(const RopeParams& p, unsigned grid, cudaStream_t st) {
-  if (p.d == 64) {
-    if (p.neighbours)
-      norm_rope_fwd_kernel<T, 64, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else
-      norm_rope_fwd_kernel<T, 64, false><<<grid, kRopeThreads, 0, st>>>(p);
-  } else {
-    if (p.neighbours)
-      norm_rope_fwd_kernel<T, 128, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else
-      norm_rope_fwd_kernel<T, 128, false><<<grid, kRopeThreads, 0, st>>>(p);
-  }
+template <auto kKernel>
+cudaError_t launch_ring(const RopeParams& p, int bytes, cudaStream_t st) {
+  const cudaError_t e = allow_smem<kKernel>(bytes);
+  if (e != cudaSuccess) return e;
+  kKernel<<<p.blocks, kRopeThreads, bytes, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_bwd(const RopeParams& p, unsigned grid, cudaStream_t st) {
-  if (p.d == 64) {
-    if (p.neighbours)
-      norm_rope_bwd_kernel<T, 64, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else
-      norm_rope_bwd_kernel<T, 64, false><<<grid, kRopeThreads, 0, st>>>(p);
-  } else {
-    if (p.neighbours)
-      norm_rope_bwd_kernel<T, 128, true><<<grid, kRopeThreads, 0, st>>>(p);
-    else
-      norm_rope_bwd_kernel<T, 128, false><<<grid, kRopeThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_fwd(const RopeParams& p, cudaStream_t st) {
+  constexpr int bytes = RowRing<T, 2, kFwdDepth>::bytes(kRopeThreads);
+  if (p.d == 64)
+    return p.neighbours ? launch_ring<norm_rope_fwd_kernel<T, 64, true>>(p, bytes, st)
+                        : launch_ring<norm_rope_fwd_kernel<T, 64, false>>(p, bytes, st);
+  return p.neighbours ? launch_ring<norm_rope_fwd_kernel<T, 128, true>>(p, bytes, st)
+                      : launch_ring<norm_rope_fwd_kernel<T, 128, false>>(p, bytes, st);
 }
 
-long long blocks_for(long long rows, int per_block) { return (rows + per_block - 1) / per_block; }
+template <typename T>
+cudaError_t launch_bwd(const RopeParams& p, cudaStream_t st) {
+  constexpr int bytes = RowRing<T, 4, kBwdDepth>::bytes(kRopeThreads);
+  static_assert(bytes >= kRopeThreads * 16 * 4, "the block's weight gradients fit into the ring");
+  if (p.d == 64)
+    return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, 64, true>>(p, bytes, st)
+                        : launch_ring<norm_rope_bwd_kernel<T, 64, false>>(p, bytes, st);
+  return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, 128, true>>(p, bytes, st)
+                      : launch_ring<norm_rope_bwd_kernel<T, 128, false>>(p, bytes, st);
+}
+
+long long div_up(long long a, long long b) { return (a + b - 1) / b; }
+
+// Shares `blocks` blocks between q and k by their rows and gives every row group
+// its number of consecutive rows: a few resident sets of blocks where there
+// is work for them, so that a group's prologue (weights, first loads) is paid
+// once, and one row a group where there is not.
+void share_rows(RopeParams& p, int groups, long long blocks) {
+  const long long rq = (long long)p.B * p.N * p.q.H, rk = (long long)p.B * p.N * p.k.H;
+  for (int side = 0; side < 2; ++side) {
+    RopeSide& s = side ? p.k : p.q;
+    const long long rows = side ? rk : rq;
+    const long long share = std::max<long long>(1, blocks * rows / (rq + rk)) * groups;
+    s.span = (int)std::min<long long>(div_up(rows, share), 1 << 30);
+    const int n = (int)div_up(rows, groups * (long long)s.span);
+    if (side)
+      p.blocks = p.q_blocks + n;
+    else
+      p.q_blocks = n;
+  }
+}
 
 }  // namespace
 
 int rope_bwd_max_blocks() { return kBwdBlocks + 2; }
 
 cudaError_t launch_norm_rope_fwd(RopeParams& p, int dtype, cudaStream_t st) {
-  const long long rq = (long long)p.B * p.N * p.q.H, rk = (long long)p.B * p.N * p.k.H;
   if (!vector_rows(p, dtype, false)) {
-    // enough blocks of eight rows to fill the GPU twice; longer inputs loop
-    p.q_blocks = (int)std::min<long long>(blocks_for(rq, 8), 152 * 8);
-    const int kb = (int)std::min<long long>(blocks_for(rk, 8), 152 * 8);
-    norm_rope_any_f32_kernel<false><<<p.q_blocks + kb, kRopeThreads, 0, st>>>(p);
+    share_rows(p, 8, 152 * 8);
+    norm_rope_any_f32_kernel<false><<<p.blocks, kRopeThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
-  const int per = kRopeThreads / (p.d / 8) * kFwdRows;
-  const long long qb = blocks_for(rq, per), kb = blocks_for(rk, per);
-  if (qb + kb > 0x7fffffffll) return cudaErrorInvalidValue;
-  p.q_blocks = (int)qb;
-  const unsigned grid = (unsigned)(qb + kb);
-  if (dtype == FA_F32) return launch_fwd<float>(p, grid, st);
-  return dtype == FA_BF16 ? launch_fwd<__nv_bfloat16>(p, grid, st) : launch_fwd<__half>(p, grid, st);
+  share_rows(p, kRopeThreads / (p.d / 16), kFwdBlocks);
+  if (dtype == FA_F32) return launch_fwd<float>(p, st);
+  return dtype == FA_BF16 ? launch_fwd<__nv_bfloat16>(p, st) : launch_fwd<__half>(p, st);
 }
 
 cudaError_t launch_norm_rope_bwd(RopeParams& p, int dtype, cudaStream_t st) {
   const bool vec = vector_rows(p, dtype, true);
-  const int per = vec ? kRopeThreads / (p.d / 8) * kBwdRows : 8;
-  const long long rq = (long long)p.B * p.N * p.q.H, rk = (long long)p.B * p.N * p.k.H;
-  // one resident set of blocks, shared between q and k by their rows
-  const long long want = std::min<long long>(blocks_for(rq, per) + blocks_for(rk, per), kBwdBlocks);
-  const long long qb = std::min<long long>(std::max<long long>(1, want * rq / (rq + rk)), blocks_for(rq, per));
-  const long long kb = std::min<long long>(std::max<long long>(1, want - qb), blocks_for(rk, per));
-  p.q_blocks = (int)qb;
-  p.blocks = (int)(qb + kb);
   cudaError_t e;
   if (!vec) {
+    share_rows(p, 8, kBwdBlocks);
     norm_rope_any_f32_kernel<true><<<p.blocks, kRopeThreads, 0, st>>>(p);
     e = cudaGetLastError();
-  } else if (dtype == FA_F32) {
-    e = launch_bwd<float>(p, p.blocks, st);
   } else {
-    e = dtype == FA_BF16 ? launch_bwd<__nv_bfloat16>(p, p.blocks, st) : launch_bwd<__half>(p, p.blocks, st);
+    share_rows(p, kRopeThreads / (p.d / 16), kBwdBlocks);
+    if (dtype == FA_F32)
+      e = launch_bwd<float>(p, st);
+    else
+      e = dtype == FA_BF16 ? launch_bwd<__nv_bfloat16>(p, st) : launch_bwd<__half>(p, st);
   }
   if (e != cudaSuccess || (p.q.w == nullptr && p.k.w == nullptr)) return e;
   const dim3 grid(2, (p.d + 31) / 32);
-  if (dtype == FA_F32 || p.w_f32)
-    weight_grad_kernel<float><<<grid, 256, 0, st>>>(p);
-  else if (dtype == FA_BF16)
-    weight_grad_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
-  else
-    weight_grad_kernel<__half><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  if (dtype == FA_F32 || p.w_f32) return launch_behind(weight_grad_kernel<float>, grid, 1024, p, st);
+  return dtype == FA_BF16 ? launch_behind(weight_grad_kernel<__nv_bfloat16>, grid, 1024, p, st)
+                          : launch_behind(weight_grad_kernel<__half>, grid, 1024, p, st);
 }
 
 }  // namespace fa

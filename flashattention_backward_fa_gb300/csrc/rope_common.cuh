@@ -5,80 +5,103 @@
 //   out = R(pos) y: the pairs (a, b) of the first rot values become
 //         (a cos - b sin, b cos + a sin)
 //
-// A row of D values is held by D/8 lanes, eight consecutive values each, so a
-// lane's load is 16 bytes (16-bit types) and a warp moves whole rows. The
-// rotation is written element-wise, out_i = y_i c_i + y_partner(i) s_i, with the
-// sign of the pair folded into s_i: partners rot/2 apart sit in another lane of
-// the row at the same place in its eight (rot is a multiple of 16), so the raw
-// words are exchanged by shuffles before they are unpacked; neighbouring
-// partners sit in the same lane. Values past rot have c = 1, s = 0.
+// A row of D values is held by D/16 lanes, two chunks of eight consecutive
+// values each, so that a load is 16 bytes (16-bit types) and both values of
+// every pair are in one lane: with partners rot / 2 apart the second chunk is
+// the first one's partners (rot is a multiple of 16; what is not rotated goes
+// to the remaining lanes), with neighbouring partners the second chunk is D / 2
+// further on. Only the sum of squares crosses lanes. With the weights folded
+// into the token's factors, out = r (x C + partner S) is three packed (two-wide)
+// operations for two values; a layout with one chunk a lane, which exchanges
+// partners by shuffles, took 238 instructions for 16 values against about 90
+// and ran at 70% of the copy rate.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
+#include "fa.h"
 
 namespace fa {
 
-// Eight consecutive values of a row as loaded.
+// Eight consecutive values of a row as they lie in memory.
 template <typename T>
 struct Raw8 {
-  uint4 a;
-  __device__ __forceinline__ void load(const T* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+  static constexpr int kQuads = 1;  // 16-byte pieces
+  uint4 q[1];
+  __device__ __forceinline__ void unpack(uint64_t (&f)[4]) const {
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-    unpack2<bf>(a.x, f[0], f[1]);
-    unpack2<bf>(a.y, f[2], f[3]);
-    unpack2<bf>(a.z, f[4], f[5]);
-    unpack2<bf>(a.w, f[6], f[7]);
+    const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpack2<bf>(w[i], lo, hi);
+      f[i] = f2_pack(lo, hi);
+    }
   }
-  __device__ __forceinline__ void pack(const float (&f)[8]) {
+  __device__ __forceinline__ void pack(const uint64_t (&f)[4]) {
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-    a = make_uint4(pack2<bf>(f[0], f[1]), pack2<bf>(f[2], f[3]), pack2<bf>(f[4], f[5]), pack2<bf>(f[6], f[7]));
-  }
-  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = a; }
-  __device__ __forceinline__ Raw8 from_lane(int src) const {
-    Raw8 r;
-    r.a.x = __shfl_sync(0xffffffffu, a.x, src);
-    r.a.y = __shfl_sync(0xffffffffu, a.y, src);
-    r.a.z = __shfl_sync(0xffffffffu, a.z, src);
-    r.a.w = __shfl_sync(0xffffffffu, a.w, src);
-    return r;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f2_unpack(f[i], lo, hi);
+      w[i] = pack2<bf>(lo, hi);
+    }
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
 template <>
 struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void unpack(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
-  __device__ __forceinline__ void pack(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ __forceinline__ Raw8 from_lane(int src) const {
-    float f[8];
-    unpack(f);
+  static constexpr int kQuads = 2;
+  uint4 q[2];
+  __device__ __forceinline__ void unpack(uint64_t (&f)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __shfl_sync(0xffffffffu, f[i], src);
-    Raw8 r;
-    r.pack(f);
-    return r;
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = f2_pack(__uint_as_float(q[i].x), __uint_as_float(q[i].y));
+      f[2 * i + 1] = f2_pack(__uint_as_float(q[i].z), __uint_as_float(q[i].w));
+    }
+  }
+  __device__ __forceinline__ void pack(const uint64_t (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a, b, c, d;
+      f2_unpack(f[2 * i], a, b);
+      f2_unpack(f[2 * i + 1], c, d);
+      q[i] = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
   }
 };
+
+template <typename T>
+__device__ __forceinline__ void load8(Raw8<T>& v, const T* p) {
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kQuads; ++i) v.q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+}
+template <typename T>
+__device__ __forceinline__ void store8(const Raw8<T>& v, T* p) {
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kQuads; ++i) reinterpret_cast<uint4*>(p)[i] = v.q[i];
+}
+template <typename T>
+__device__ __forceinline__ void zero8(Raw8<T>& v) {
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kQuads; ++i) v.q[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// 16 bytes from global to shared memory, asynchronously; zeros where !valid (nothing is read then).
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 
 // Sum over the kLanes lanes of a row (kLanes a power of two, rows aligned in the warp).
 template <int kLanes>
@@ -88,90 +111,236 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// A lane's eight weights (fp32 or T in memory; ones without a weight vector).
+// A weight vector to shared memory as fp32 (fp32 or T in memory; ones where there is none).
 template <typename T>
-__device__ __forceinline__ void load_weight8(const void* w, bool w_f32, int e0, float (&f)[8]) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
-  } else if (w_f32) {
-    const float* p = static_cast<const float*>(w) + e0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __ldg(p + i);
-  } else {
-    const T* p = static_cast<const T*>(w) + e0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(p[i]);
-  }
+__device__ __forceinline__ void stage_weights(const void* w, bool w_f32, int d, float* to) {
+  for (int e = threadIdx.x; e < d; e += blockDim.x)
+    to[e] = w == nullptr ? 1.f : w_f32 ? static_cast<const float*>(w)[e] : static_cast<float>(static_cast<const T*>(w)[e]);
 }
 
-// Which lane of the warp holds the rotation partners of a lane's eight values
-// (itself where there are none or where partners are neighbours).
-template <bool kNeighbours>
-__device__ __forceinline__ int partner_lane(int lane, int e0, int rot) {
-  if (kNeighbours || e0 >= rot) return lane;
-  const int hop = rot >> 4;  // lanes between partners: (rot / 2) / 8
-  return e0 < (rot >> 1) ? lane + hop : lane - hop;
+__device__ __forceinline__ void read4(const float* p, float* f) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
 }
 
-// c_i and signed s_i of a lane's eight values from the token's table rows (rot / 2 values each).
+// First values of the two chunks of lane j of a row.
+struct LanePlace {
+  int a, b;
+};
+template <int D, bool kNeighbours>
+__device__ __forceinline__ LanePlace lane_place(int j, int rot) {
+  if (kNeighbours) return {8 * j, 8 * j + D / 2};
+  const int pairs = rot >> 4;  // lanes that hold rotated values
+  if (j < pairs) return {8 * j, 8 * j + (rot >> 1)};
+  return {rot + 16 * (j - pairs), rot + 16 * (j - pairs) + 8};
+}
+
+// cos and sin of a lane's eight pairs (a token's table rows hold rot / 2 values each): pairs
+// (a_i, b_i) of the two chunks, or, with neighbours, four pairs of each chunk.
 template <bool kNeighbours>
-__device__ __forceinline__ void load_rotation(const float* cos_row, const float* sin_row, int e0, int rot,
+__device__ __forceinline__ void load_rotation(const float* cos_row, const float* sin_row, const LanePlace& at, int rot,
                                               float (&c)[8], float (&s)[8]) {
-  if (e0 >= rot) {
+  // neighbours: pair indices of the chunks; else both halves are the chunk's one run
+  const int lo = kNeighbours ? at.a >> 1 : at.a, hi = kNeighbours ? at.b >> 1 : at.a + 4;
+  const bool has_lo = at.a < rot, has_hi = (kNeighbours ? at.b : at.a) < rot;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-    return;
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  if (has_lo) {
+    read4(cos_row + lo, c);
+    read4(sin_row + lo, s);
   }
-  if (kNeighbours) {
-    const float4 cc = __ldg(reinterpret_cast<const float4*>(cos_row + (e0 >> 1)));
-    const float4 ss = __ldg(reinterpret_cast<const float4*>(sin_row + (e0 >> 1)));
-    const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c[2 * j] = c[2 * j + 1] = cv[j];
-      s[2 * j] = -sv[j];
-      s[2 * j + 1] = sv[j];
-    }
-  } else {
-    const int h = rot >> 1;
-    const bool low = e0 < h;
-    const int at = low ? e0 : e0 - h;
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(cos_row + at));
-    const float4 c1 = __ldg(reinterpret_cast<const float4*>(cos_row + at) + 1);
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(sin_row + at));
-    const float4 s1 = __ldg(reinterpret_cast<const float4*>(sin_row + at) + 1);
-    const float sg = low ? -1.f : 1.f;
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    s[0] = sg * s0.x, s[1] = sg * s0.y, s[2] = sg * s0.z, s[3] = sg * s0.w;
-    s[4] = sg * s1.x, s[5] = sg * s1.y, s[6] = sg * s1.z, s[7] = sg * s1.w;
+  if (has_hi) {
+    read4(cos_row + hi, c + 4);
+    read4(sin_row + hi, s + 4);
   }
 }
 
-// Forward of one row chunk: every lane of the warp calls it (shuffles). w_p are
-// the partners' weights (equal to w where the partner lane is the lane itself
-// and partners are neighbours, where they are not used).
+// A token's factors with the weights folded in: out_a = r (a ca + pa sa), pa the partners of a
+// (b, or a with neighbours swapped), and alike for b.
+struct Factors {
+  uint64_t ca[4], sa[4], cb[4], sb[4];
+};
+template <bool kNeighbours>
+__device__ __forceinline__ void fold_weights(const float* w, const LanePlace& at, const float (&c)[8],
+                                             const float (&s)[8], Factors& f) {
+  float wa[8], wb[8];
+  read4(w + at.a, wa);
+  read4(w + at.a + 4, wa + 4);
+  read4(w + at.b, wb);
+  read4(w + at.b + 4, wb + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = 2 * i, y = 2 * i + 1;
+    if (kNeighbours) {
+      f.ca[i] = f2_pack(c[i] * wa[x], c[i] * wa[y]);
+      f.sa[i] = f2_pack(-s[i] * wa[y], s[i] * wa[x]);
+      f.cb[i] = f2_pack(c[4 + i] * wb[x], c[4 + i] * wb[y]);
+      f.sb[i] = f2_pack(-s[4 + i] * wb[y], s[4 + i] * wb[x]);
+    } else {
+      f.ca[i] = f2_pack(c[x] * wa[x], c[y] * wa[y]);
+      f.sa[i] = f2_pack(-s[x] * wb[x], -s[y] * wb[y]);
+      f.cb[i] = f2_pack(c[x] * wb[x], c[y] * wb[y]);
+      f.sb[i] = f2_pack(s[x] * wa[x], s[y] * wa[y]);
+    }
+  }
+}
+
+__device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return f2_pack(hi, lo);
+}
+
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
+}
+
+// Forward of a lane's 16 values, in place; every lane of the warp calls it (shuffles).
 template <typename T, int D, bool kNeighbours>
-__device__ __forceinline__ void norm_rope_chunk(const Raw8<T>& raw, int partner, const float (&w)[8],
-                                                const float (&w_p)[8], const float (&c)[8], const float (&s)[8],
-                                                float eps, float (&out)[8]) {
-  float x[8];
-  raw.unpack(x);
-  float ss = 0.f;
+__device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const Factors& f, float eps) {
+  uint64_t a[4], b[4], oa[4], ob[4];
+  ra.unpack(a);
+  rb.unpack(b);
+  uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = row_sum<D / 8>(ss);
-  const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-  if (kNeighbours) {
+  for (int i = 0; i < 4; ++i) {
+    s0 = f2_fma(a[i], a[i], s0);
+    s1 = f2_fma(b[i], b[i], s1);
+  }
+  const float ss = row_sum<D / 16>(f2_sum(f2_add(s0, s1)));
+  const float r1 = rsqrtf(fmaf(ss, 1.f / D, eps));
+  const uint64_t r = f2_pack(r1, r1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+  for (int i = 0; i < 4; ++i) {
+    oa[i] = f2_mul(r, f2_fma(a[i], f.ca[i], f2_mul(kNeighbours ? f2_swap(a[i]) : b[i], f.sa[i])));
+    ob[i] = f2_mul(r, f2_fma(b[i], f.cb[i], f2_mul(kNeighbours ? f2_swap(b[i]) : a[i], f.sb[i])));
+  }
+  ra.pack(oa);
+  rb.pack(ob);
+}
+
+// A walk over the rows (b, n, head) of [B, N, H, *], heads fastest, with the
+// offset of the row in one tensor. The one decomposition of a row number is in
+// 32 bits where it fits (a 64-bit division costs as much as a row's arithmetic).
+struct RowWalk {
+  long long b, at;
+  int n, head;
+  __device__ __forceinline__ void start(long long row, int N, int H, const fa_strides& st) {
+    long long token;
+    if (row >> 32) {
+      token = row / H;
+      b = token / N;
+    } else {
+      token = (unsigned)row / (unsigned)H;
+      b = (unsigned)token / (unsigned)N;
+    }
+    head = (int)(row - token * H);
+    n = (int)(token - b * N);
+    at = b * st.b + (long long)n * st.n + (long long)head * st.h;
+  }
+  // To the next row; true when it is another token's.
+  __device__ __forceinline__ bool next(int N, int H, const fa_strides& st) {
+    at += st.h;
+    if (++head < H) return false;
+    head = 0;
+    if (++n == N) {
+      n = 0;
+      ++b;
+    }
+    at = b * st.b + (long long)n * st.n;
+    return true;
+  }
+};
+
+// A lane's slots for rows on their way: kDepth rows of kChunks chunks, each lane reading back
+// only what it copied itself, so waiting for its own copies is all the synchronisation needed.
+// Slots of a chunk are 16 bytes a thread apart (no bank conflicts).
+template <typename T, int kChunks, int kDepth>
+struct RowRing {
+  static constexpr int kPieces = kChunks * Raw8<T>::kQuads;
+  static constexpr int bytes(int threads) { return kDepth * kPieces * threads * 16; }
+  uint32_t base;
+  int threads;
+  __device__ __forceinline__ RowRing(void* smem) : base(smem_u32(smem) + threadIdx.x * 16), threads(blockDim.x) {}
+  __device__ __forceinline__ uint32_t slot(int row, int chunk, int piece) const {
+    return base + (uint32_t)(((row % kDepth) * kPieces + chunk * Raw8<T>::kQuads + piece) * threads) * 16u;
+  }
+  __device__ __forceinline__ void fetch(int row, int chunk, const T* p, bool valid) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = fmaf(x[i], c[i], x[i ^ 1] * s[i]);
-  } else {
-    float xp[8];
-    raw.from_lane(partner).unpack(xp);
+    for (int i = 0; i < Raw8<T>::kQuads; ++i)
+      copy16_async(slot(row, chunk, i), reinterpret_cast<const uint4*>(p) + i, valid);
+  }
+  __device__ __forceinline__ void take(int row, int chunk, Raw8<T>& v) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = fmaf(x[i] * r * w[i], c[i], xp[i] * r * w_p[i] * s[i]);
+    for (int i = 0; i < Raw8<T>::kQuads; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.q[i].x), "=r"(v.q[i].y), "=r"(v.q[i].z), "=r"(v.q[i].w)
+                   : "r"(slot(row, chunk, i))
+                   : "memory");
+  }
+};
+
+// The launch that follows a kernel in the stream may begin (its own prologue) while the
+// kernel ends; what reads the kernel's outputs waits for all of it first. Both are no-ops
+// in launches without the attribute.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Rows [first, first + count) of one tensor by one row group (D / 16 lanes; the
+// groups of a warp call it together, each with its own rows and all with the same
+// count). kDepth - 1 rows are on their way while a row is computed.
+// table_at(b, n): offset of the token's table rows, or -1 for a padding row, which
+// becomes zeros (kPadding) and is not read. The weights are staged into w (a block-wide step)
+// once the first copies are under way.
+template <typename T, int D, bool kNeighbours, bool kPadding, int kDepth, typename TableAt>
+__device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, const fa_strides& x_st,
+                                               const fa_strides& out_st, long long rows, int N, int H, long long first,
+                                               int count, const void* weights, bool w_f32, float* w,
+                                               const float* cos, const float* sin, int rot, float eps,
+                                               const TableAt& table_at) {
+  const RowRing<T, 2, kDepth> ring(smem);
+  const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % (D / 16), rot);
+  const int live = (int)min((long long)count, max(rows - first, 0ll));
+  RowWalk in, to;
+  in.start(first, N, H, x_st);
+  to.start(first, N, H, out_st);
+  int loaded = 0;
+  auto fetch = [&] {
+    const bool ok = loaded < live && (!kPadding || table_at(in.b, in.n) >= 0);
+    const T* p = x + (ok ? in.at : 0);
+    ring.fetch(loaded, 0, p + at.a, ok);
+    ring.fetch(loaded, 1, p + at.b, ok);
+    copies_commit();
+    in.next(N, H, x_st);
+    ++loaded;
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch();
+  stage_weights<T>(weights, w_f32, D, w);
+  __syncthreads();
+  Factors f;
+  bool token = true;
+  for (int i = 0; i < count; ++i) {
+    fetch();
+    if (token) {
+      const bool ok = i < live;
+      const long long row = ok ? max(table_at(to.b, to.n), 0ll) : 0;
+      float c[8], s[8];
+      load_rotation<kNeighbours>(cos + row, sin + row, at, ok ? rot : 0, c, s);
+      fold_weights<kNeighbours>(w, at, c, s, f);
+    }
+    copies_wait<kDepth - 1>();
+    Raw8<T> a, b;
+    ring.take(i, 0, a);
+    ring.take(i, 1, b);
+    norm_rope_lane<T, D, kNeighbours>(a, b, f, eps);  // (zeros stay zeros)
+    if (i < live) {
+      store8(a, out + to.at + at.a);
+      store8(b, out + to.at + at.b);
+    }
+    token = to.next(N, H, out_st);
   }
 }
 

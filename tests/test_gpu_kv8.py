@@ -264,6 +264,9 @@ ATTN = [
     (1, 2, 16, 2, 64, 16, torch.float16, [3001], None, 0, True, False),
     (2, 5, 4, 4, 64, 32, torch.float16, [900, 333], [3, 4], 500, True, False),  # padding rows in whole steps
     (2, 4, 2, 1, 128, 64, torch.bfloat16, [64, 48], [1, 0], 0, False, False),
+    (1, 3, 4, 2, 64, 64, torch.float16, [9000], None, 0, True, True),
+    (2, 2, 12, 1, 128, 128, torch.bfloat16, [7001, 13], [2, 1], 6000, True, False),
+    (1, 9, 4, 1, 128, 128, torch.bfloat16, [6500], None, 0, False, False),
 ]
 
 
@@ -414,16 +417,16 @@ def test_strided_cache_queries_and_outputs():
 
 def test_workspace_is_not_overrun_by_splits():
     g = torch.Generator().manual_seed(59)
-    cache = _filled(130, 16, 1, 64, g)
+    cache = _filled(130, 64, 1, 64, g)
     table = torch.arange(130, dtype=torch.int32)[None].contiguous()
     q = _values((1, 2, 3, 64), torch.float16, g, 1.0).cuda()
-    size = fa.fa_kv8_attn_workspace_size(1, 2, 3, 1, 64, 16, 130, 2080)
+    size = fa.fa_kv8_attn_workspace_size(1, 2, 3, 1, 64, 64, 130, 8320)
     assert size > 256  # split
     ws = torch.full((size + 256,), 165, dtype=torch.uint8, device="cuda")
     o, lse = torch.empty_like(q), torch.empty(1, 3, 2, device="cuda")
-    fa.fa_kv8_attn(q, cache, o, lse, _cu(table), _cu([2077]), 2080, ws[:size])
+    fa.fa_kv8_attn(q, cache, o, lse, _cu(table), _cu([8309]), 8320, ws[:size])
     assert bool((ws[size:] == 165).all())
-    _check(q, cache, table, [2077], None, 2080, torch.float16, o=o, lse=lse)
+    _check(q, cache, table, [8309], None, 8320, torch.float16, o=o, lse=lse)
 
 
 def test_offsets_past_32_bits():
