@@ -92,6 +92,8 @@ int check_cache(const fa_kv8_cache* c, const fa_kv8_seqs* s, int* shift) {
   if (c->H > 1024 || s->B > 65535) return FA_ERR_UNSUPPORTED;
   // positions and page offsets within a sequence stay in 31 bits
   if (s->max_pages > (1 << 30) >> *shift) return FA_ERR_UNSUPPORTED;
+  // and so do the offsets of a page's tokens
+  if (c->strides.n > (1ll << 30) >> *shift) return FA_ERR_UNSUPPORTED;
   if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || ((c->strides.b | c->strides.n | c->strides.h) & 15))
     return FA_ERR_ALIGNMENT;
   if (!aligned_to(c->k_scale, 4) || !aligned_to(c->v_scale, 4) || !aligned_to(s->block_table, 4) ||

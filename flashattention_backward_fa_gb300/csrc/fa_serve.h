@@ -128,7 +128,7 @@ struct Kv8AttnParams {
   const float* alibi;
   int64_t alibi_sb;
   int key_limit;  // keys past it are never attended: min(max_seqlen, max_pages * page size)
-  int chunk;      // keys of a split (a multiple of 64)
+  int chunk;      // keys of a split (a multiple of 128)
   int splits;     // most splits of a sequence
   int cluster;    // the splits are the blocks of a cluster, which joins them (chunk does not apply)
   int row_tiles;

@@ -7,32 +7,39 @@
 // head value of a token), so everything serves keeping loads in flight:
 //
 // * Queries are the narrow side of the products: S^T = K Q^T and O^T = V^T P^T,
-//   16 keys x 8 rows an instruction (mma.sync m16n8k16, f16 operands, fp32
-//   sums). A tcgen05 tile has at least 64 rows of M from shared memory and its
-//   smallest useful N; with one to a few dozen rows the codes would have to be
-//   widened into shared memory first (2 bytes a value written and read again),
-//   while here they go from global memory straight into the registers that the
-//   instruction reads. Its rate is not what bounds the kernel up to 32 rows.
+//   16 keys x 8 rows an instruction (mma.sync, fp32 sums). A tcgen05 tile has at
+//   least 64 rows of M from shared memory; with one to a few dozen rows, V would
+//   have to be widened and P written to shared memory and read again, while here
+//   codes and weights go from registers to the instruction. Its rate is not what
+//   bounds the kernel up to 32 rows.
 // * Any order of the head dimension serves S, and any order of the output
 //   columns serves O: a lane takes 16 consecutive codes of a key (K) or of a
-//   key's values (V) with one load and uses them in place. A warp's loads cover
-//   whole 64-byte (K) and 128-byte (V) pieces of rows.
-// * e4m3 is exact in f16, so codes enter the products unrounded; the page's key
-//   scale multiplies S in fp32. V's codes are summed in units of their scale;
-//   the sums are rescaled on the rare page whose scale differs (exact for
-//   powers of two). bf16 queries become f16 after division by a power of two of
-//   each row (exact down to 2^-28 of the row's largest value).
+//   key's values (V) and uses them in place.
+// * K's codes enter the e4m3 instruction (k32, measured at 0.94 a clock and SM,
+//   four times the f16 rate, sums exact to fp32) as they are. The queries are
+//   divided by a power of two of each row and written as two (bf16) or three (f16)
+//   e4m3 pieces, each the rounding error of those before it times 16: exact down
+//   to 2^-22 (2^-26) of the row's largest value. Widening K to f16 instead took
+//   48 more ALU operations a step, at 2 a clock and SM.
+// * V's codes are widened to f16 (exact) for the f16 instruction, because the
+//   weights P need its range: an e4m3 piece ends 2^-18 below the largest weight,
+//   and a long sequence can hold most of its mass below that. They are summed in
+//   units of their page's scale; the sums are rescaled on the rare page whose scale
+//   differs (exact for powers of two).
 // * Running maximum and sum per row in fp32, kept per lane; the reference m
 //   moves only when a score exceeds it by 2^15 (P is then at most 2^15, inside
 //   f16), starting 2^7 above the first maximum, so warps agree on a new m a few
 //   times a sequence and vote otherwise. P is rounded to f16 (2^-12 of itself);
 //   for f16 outputs, whose own rounding is no larger, its rounding residual is
 //   multiplied too.
-// * Four warps take steps of 16 keys in turn. A lane's pieces of the next steps
-//   are on their way to shared memory (cp.async) in slots that it alone reads
-//   back, so a warp waits for its own copies and for nothing else, and about 48
-//   KB a block are in flight without a register. The warps are merged once, at
-//   the end.
+// * Four warps take steps of 32 keys (two tiles, whose chains of instructions
+//   overlap) in turn. The next step is on its way to the warp's own part of shared
+//   memory (cp.async), so a warp waits for itself alone, and 96 KB an SM are in
+//   flight without a register. Eight lanes copy one 128-byte line: copied in the
+//   order in which lanes use them, the codes of eight lanes lie in two (K) or four
+//   (V) lines, and the lines a clock of L1, not DRAM, bounded the kernel at 61% of
+//   the copy rate whatever else it did. Lines are swizzled so that neither the
+//   copies nor the reads in the instructions' order meet in a bank.
 // * A sequence's keys are split over blocks: up to eight blocks of a cluster join
 //   their outputs through distributed shared memory; where few sequences and
 //   heads leave the GPU empty otherwise, more blocks write normalised outputs
@@ -52,7 +59,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kStep = 16;       // keys of a step
+constexpr int kHopKeys = 128;   // splits are multiples of it (two tiles a warp)
+constexpr int kTile = 16;       // keys of an instruction
 constexpr float kNoMax = -3.0e38f;  // m before any score
 constexpr float kHead = 7.f;    // m starts that far below 2^15: P of the first maximum is 2^7
 constexpr float kTop = 15.f;    // scores may pass m by this much (in log2)
@@ -63,6 +71,27 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two fp32 values to a pair of e4m3 codes, lo in the low byte, and what the rounding leaves, times 16.
+__device__ __forceinline__ uint32_t e4m3_piece(float& lo, float& hi) {
+  uint16_t r;
+  uint32_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(r));
+  float a, b;
+  unpack2<false>(h, a, b);
+  lo = (lo - a) * 16.f;
+  hi = (hi - b) * 16.f;
+  return r;
 }
 
 // Four codes to two f16 pairs (exact).
@@ -113,7 +142,7 @@ __device__ __forceinline__ float4 read_cluster_f32x4(const void* p, int rank) {
 }
 
 // What a block needs to know of its sequence: keys [lo, hi) are those that some
-// row of the row tile attends to, lo rounded down to a step.
+// row of the row tile attends to, lo rounded down to a tile.
 struct Range {
   int len, count;  // tokens of the sequence; how many of them are new
   int keys;        // keys that exist for attention
@@ -131,7 +160,7 @@ __device__ __forceinline__ Range key_range(const Kv8AttnParams& p, int b, int ro
   if (t_lo <= t_hi) {
     const int i_lo = r.len - r.count + t_lo, i_hi = r.len - r.count + t_hi;
     r.hi = p.causal ? min(r.keys, i_hi + 1) : r.keys;
-    r.lo = p.window > 0 ? max(0, i_lo - p.window + 1) & ~(kStep - 1) : 0;
+    r.lo = p.window > 0 ? max(0, i_lo - p.window + 1) & ~(kTile - 1) : 0;
     if (r.lo >= r.hi) r.lo = r.hi = 0;
   }
   return r;
@@ -140,28 +169,29 @@ __device__ __forceinline__ Range key_range(const Kv8AttnParams& p, int b, int ro
 // Keys of a split: the plan's, or, in a cluster, the sequence's own keys shared out evenly.
 __device__ __forceinline__ int split_keys(const Kv8AttnParams& p, const Range& r) {
   if (!p.cluster) return p.chunk;
-  const int hop = kStep * kWarps, n = r.hi - r.lo, per = p.splits * hop;
-  return max(1, (n + per - 1) / per) * hop;
+  const int n = r.hi - r.lo, per = p.splits * kHopKeys;
+  return max(1, (n + per - 1) / per) * kHopKeys;
 }
 
-// A lane's pieces of one step: lane (r = lane / 4, c = lane % 4) takes codes
-// [64 x + 16 c, + 16) of keys r and r + 8 (K) and codes [(D / 8) r, + D / 8) of
-// keys 2c, 2c + 1, 2c + 8, 2c + 9 (V). Slots of a piece are a thread apart.
-template <int D>
+// Shared memory of the steps under way: a stage holds U tiles a warp, a tile 16
+// keys of K and of V in 128-byte lines (a key, or two with D = 64). Sixteen-byte
+// chunk x of line y lies at x ^ swizzle(y).
+template <int D, int U>
 struct Ring {
-  static constexpr int kK = 2 * (D / 64);          // 16-byte pieces of K
-  static constexpr int kVBytes = D / 8;            // bytes of a piece of V (four of them)
-  static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kStageBytes = (kK * 16 + 4 * kVBytes) * kThreads;
-  static constexpr int kScales = kStages * kStageBytes;  // then (K scale, V scale) a warp and stage
-  static constexpr int kBytes = kScales + kStages * kWarps * 8;
+  static constexpr int kLines = D / 8;             // lines of a tile of K, and of V
+  static constexpr int kHalf = kLines * 128;       // bytes of K (then V) of a tile
+  static constexpr int kStages = (D == 128 ? 4 : 8) / U;
+  static constexpr int kWarpBytes = U * 2 * kHalf;
+  static constexpr int kStageBytes = kWarps * kWarpBytes;
+  static constexpr int kScales = kStages * kStageBytes;  // then (K scale, V scale) a stage, warp and tile
+  static constexpr int kBytes = kScales + kStages * kWarps * U * 8;
 };
 
-__device__ __forceinline__ void copy8_async(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint4 read_slot16(uint32_t a) {
   uint4 v;
@@ -174,52 +204,77 @@ __device__ __forceinline__ uint2 read_slot8(uint32_t a) {
   return v;
 }
 
-// Starts the copies of the step at `slot` of a page into a stage (zeros for a page outside the cache).
-template <int D>
-__device__ __forceinline__ void fetch_step(const Kv8Cache& c, uint32_t ring, int stage, int page, int slot, int h,
-                                           bool page_ok) {
-  using G = Ring<D>;
-  const int lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-  const long long at = page_ok ? (long long)page * c.sp + (long long)h * c.sh + (long long)slot * c.sn : 0;
-  const uint32_t base = ring + stage * G::kStageBytes + threadIdx.x * 16;
-  const uint8_t* kp = c.k + at + (page_ok ? r * c.sn + 16 * q : 0);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int x = 0; x < D / 64; ++x)
-      copy16_async(base + (i * (D / 64) + x) * (kThreads * 16), kp + (page_ok ? (long long)(8 * i) * c.sn + 64 * x : 0), page_ok);
-  const uint8_t* vp = c.v + at + (page_ok ? (long long)(2 * q) * c.sn + G::kVBytes * r : 0);
-  const uint32_t vbase = ring + stage * G::kStageBytes + G::kK * 16 * kThreads + threadIdx.x * G::kVBytes;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint8_t* row = vp + (page_ok ? (long long)((i & 1) + 8 * (i >> 1)) * c.sn : 0);
-    if (D == 128)
-      copy16_async(vbase + i * (kThreads * G::kVBytes), row, page_ok);
-    else
-      copy8_async(vbase + i * (kThreads * G::kVBytes), row, page_ok);
+// What a lane keeps to start its copies: its place in page 0 of the head, its rows' stride (a
+// page's offsets fit into 31 bits, the entry point sees to it) and its slots. Lane l copies
+// chunk l % 8 of lines l / 8, l / 8 + 4, ... of a tile.
+template <int D, int U>
+struct Fetch {
+  using G = Ring<D, U>;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* scale;  // lane 0: K's, lane 1: V's
+  uint32_t slot_k, slot_v, slot_scale;
+  __device__ __forceinline__ Fetch(const Kv8Cache& c, uint32_t ring, int h) {
+    const int lane = threadIdx.x & 31, line = lane >> 3, x = lane & 7;
+    const long long at = (long long)h * c.sh +
+                         (D == 128 ? line * (int)c.sn + 16 * x : (2 * line + (x >> 2)) * (int)c.sn + 16 * (x & 3));
+    k = c.k + at;
+    v = c.v + at;
+    scale = (lane ? c.v_scale : c.k_scale) + h;
+    const uint32_t base = ring + (threadIdx.x >> 5) * G::kWarpBytes + line * 128;
+    slot_k = base + (D == 128 ? x ^ ((line & 1) * 4) : x) * 16;
+    slot_v = base + G::kHalf + (D == 128 ? x ^ (line & 2) : x ^ (line * 2)) * 16;
+    slot_scale = ring + G::kScales + (threadIdx.x >> 5) * (U * 8) + (lane & 1) * 4;
   }
-  if (lane < 2) {
-    const float* s = (lane ? c.v_scale : c.k_scale) + (page_ok ? (long long)page * c.H + h : 0);
-    copy4_async(ring + G::kScales + (stage * kWarps + (threadIdx.x >> 5)) * 8 + lane * 4, s, page_ok);
+  // V's slot of the lane's i-th line (with D = 128 the swizzle has a bit of the line past the fourth).
+  __device__ __forceinline__ uint32_t v_slot(uint32_t to, int i) const {
+    return ((slot_v + to) ^ (D == 128 && (i & 1) ? 64u : 0u)) + i * 512;
   }
-}
+  // Tile u of a step, at token `slot` of a page, into a stage. A page outside the cache leaves zeros.
+  __device__ __forceinline__ void operator()(const Kv8Cache& c, int stage, int u, int page, int slot,
+                                             bool page_ok) const {
+    const uint32_t to = stage * G::kStageBytes + u * 2 * G::kHalf;
+    if (!page_ok) {
+#pragma unroll
+      for (int i = 0; i < G::kLines / 4; ++i) {
+        st_shared_v4(slot_k + to + i * 512, 0u, 0u, 0u, 0u);
+        st_shared_v4(v_slot(to, i), 0u, 0u, 0u, 0u);
+      }
+      return;
+    }
+    const int sn = (int)c.sn;
+    const long long at = (long long)page * c.sp + slot * sn;
+    const uint8_t* kp = k + at;
+    const uint8_t* vp = v + at;
+    constexpr int kTokens = D == 128 ? 4 : 8;  // tokens of four lines
+#pragma unroll
+    for (int i = 0; i < G::kLines / 4; ++i) copy16_async(slot_k + to + i * 512, kp + i * kTokens * sn);
+#pragma unroll
+    for (int i = 0; i < G::kLines / 4; ++i) copy16_async(v_slot(to, i), vp + i * kTokens * sn);
+    if ((threadIdx.x & 31) < 2)
+      copy4_async(slot_scale + stage * (kWarps * U * 8) + u * 8, scale + (long long)page * c.H);
+  }
+};
 
 // Bytes of w that hold an e4m3 NaN (0x7F, 0xFF), as 0x80 flags.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 3 : 2) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr bool kResidual = !kBf16;  // see the head of the file
-  constexpr int KS = D / 16;          // instructions' depth steps over the head dimension (S), row tiles of O^T
+  constexpr bool kResidual = !kBf16;   // see the head of the file
+  constexpr int NP = kBf16 ? 2 : 3;    // e4m3 pieces of a query
+  constexpr int U = NT == 4 ? 1 : 2;   // tiles of a step
+  constexpr int KS = D / 16;           // row tiles of O^T
+  constexpr int KQ = D / 32;           // instructions over the head dimension (S)
   constexpr int kRows = 8 * NT;
   constexpr int kAcc = KS * NT * 4;
-  __shared__ uint2 q_frag[KS][NT][32];
+  __shared__ uint2 q_frag[KQ][NT][NP][32];
   __shared__ float q_factor[kRows];
   __shared__ float w_m[kWarps][kRows], w_l[kWarps][kRows];
   __shared__ float block_lse[kRows];
-  extern __shared__ __align__(16) unsigned char dyn[];
-  using G = Ring<D>;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  using G = Ring<D, U>;
   static_assert(G::kScales >= (kWarps / 2) * kAcc * 32 * 4 && G::kScales >= kRows * D * 4, "merging reuses the ring");
   float (*merge)[kAcc][32] = reinterpret_cast<float (*)[kAcc][32]>(dyn);
   const uint32_t ring = smem_u32(dyn);
@@ -233,71 +288,89 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 3 : 2) kv8_a
   // (the joining kernel counts splits the same way; the blocks of a cluster all come along)
   if (begin >= end && p.splits > 1 && !p.cluster) return;
 
-  // Steps of this warp: begin + 16 warp, + 64, ...; kStages - 1 of them are under way while one is
-  // computed, their page numbers read one step earlier still.
-  constexpr int kHop = kStep * kWarps;
+  // Steps of this warp: begin + 16 U warp, + 64 U, ...; kStages - 1 of them are under way while
+  // one is computed, their page numbers read one step earlier still.
+  constexpr int kStep = kTile * U, kHop = kStep * kWarps;
   const int* table = p.c.table + b * p.c.table_stride;
   const int shift = p.c.page_shift, mask = (1 << shift) - 1;
   const int first = begin + kStep * warp;
   int ahead = first;          // key of the next step to fetch
-  uint32_t page_bits = 0u;    // bit n % 32: step n's page is in the cache
-  int fetched = 0;
+  uint32_t bad_tiles = 0u;    // bit n U + u: tile u of stage n is in a page outside the cache
   bool bad = false;
-  auto page_of = [&](int key) { return key < end ? __ldg(table + (key >> shift)) : -1; };
-  auto fetch = [&](int page) {
-    if (ahead < end) {
-      const bool ok = (unsigned)page < (unsigned)p.c.num_pages;
-      bad |= !ok;
-      page_bits = (page_bits & ~(1u << (fetched & 31))) | ((ok ? 1u : 0u) << (fetched & 31));
-      fetch_step<D>(p.c, ring, fetched % G::kStages, page, ahead & mask, h, ok);
+  int into = 0;               // stage of the next fetch
+  const Fetch<D, U> copy(p.c, ring, h);
+  struct Pages {
+    int id[U];
+  };
+  auto pages_of = [&](int key) {
+    Pages pg;
+#pragma unroll
+    for (int u = 0; u < U; ++u) pg.id[u] = key + kTile * u < end ? __ldg(table + ((key + kTile * u) >> shift)) : -1;
+    return pg;
+  };
+  auto fetch = [&](const Pages& pg) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int key = ahead + kTile * u;
+      const bool inside = key < end;  // (a tile past the end counts as one outside the cache)
+      const bool ok = inside && (unsigned)pg.id[u] < (unsigned)p.c.num_pages;
+      if (!ok) {
+        bad |= inside;
+        bad_tiles |= 1u << (into * U + u);
+      }
+      if (ahead < end) copy(p.c, into, u, pg.id[u], key & mask, ok);
     }
     copies_commit();
-    ++fetched;
+    into = into + 1 == G::kStages ? 0 : into + 1;
     ahead += kHop;
   };
-  int pages[G::kStages];
+  Pages pages[G::kStages];
 #pragma unroll
-  for (int i = 0; i < G::kStages; ++i) pages[i] = page_of(first + i * kHop);
+  for (int i = 0; i < G::kStages; ++i) pages[i] = pages_of(first + i * kHop);
 #pragma unroll
   for (int i = 0; i < G::kStages - 1; ++i) fetch(pages[i]);
-  int next_page = pages[G::kStages - 1];
+  Pages next_pages = pages[G::kStages - 1];
 
-  // Queries: row tile nt of this warp's share as f16 operand registers in shared memory.
+  // Queries: row tile nt of this warp's share as e4m3 operand registers in shared memory.
   for (int nt = warp; nt < NT; nt += kWarps) {
     const int row = row0 + 8 * nt + r, t = row / p.G, hq = h * p.G + row % p.G;
     const bool live = row < R && t < kr.count && kr.len - kr.count + t >= 0;
     const T* qp = static_cast<const T*>(p.q) + b * p.q_st.b + (long long)t * p.q_st.n + (long long)hq * p.q_st.h;
-    uint2 raw[KS];
-    uint32_t top = 0u;
+    float x[KQ][8], top = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      raw[ks] = live ? __ldg(reinterpret_cast<const uint2*>(qp + 64 * (ks >> 2) + 16 * c + 4 * (ks & 3)))
-                     : make_uint2(0u, 0u);
-      const uint32_t a = raw[ks].x & 0x7FFF7FFFu, e = raw[ks].y & 0x7FFF7FFFu;
-      top = max(top, max(max(a & 0xFFFFu, a >> 16), max(e & 0xFFFFu, e >> 16)));
-    }
-    float factor = p.scale_log2;
-    if (kBf16) {
-      // largest magnitude of the row to [2^14, 2^15): a division by a power of two
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int ex = min(max((int)(top >> 7) - 127 - 14, -110), 113);
-      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-      factor *= __uint_as_float((uint32_t)(127 + ex) << 23);
+    for (int i = 0; i < KQ; ++i) {
+      const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 16 * c + 8 * (i & 1)))
+                             : make_uint4(0u, 0u, 0u, 0u);
+      unpack2<kBf16>(raw.x, x[i][0], x[i][1]);
+      unpack2<kBf16>(raw.y, x[i][2], x[i][3]);
+      unpack2<kBf16>(raw.z, x[i][4], x[i][5]);
+      unpack2<kBf16>(raw.w, x[i][6], x[i][7]);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        float x0, x1, x2, x3;
-        unpack2<true>(raw[ks].x, x0, x1);
-        unpack2<true>(raw[ks].y, x2, x3);
-        raw[ks] = make_uint2(pack2<false>(x0 * down, x1 * down), pack2<false>(x2 * down, x3 * down));
+      for (int e = 0; e < 8; ++e) {
+        if (fabsf(x[i][e]) == INFINITY) x[i][e] = __int_as_float(0x7FC00000);  // (its row becomes NaN)
+        top = fmaxf(top, fabsf(x[i][e]));
       }
     }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // largest magnitude of the row to [2^7, 2^8): a division by a power of two
+    const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127 - 7, -110), 120);
+    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q_frag[ks][nt][lane] = raw[ks];
-    if (c == 0) q_factor[8 * nt + r] = factor;
+    for (int i = 0; i < KQ; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] *= down;
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        const uint32_t w0 = e4m3_piece(x[i][0], x[i][1]), w1 = e4m3_piece(x[i][2], x[i][3]);
+        const uint32_t w2 = e4m3_piece(x[i][4], x[i][5]), w3 = e4m3_piece(x[i][6], x[i][7]);
+        q_frag[i][nt][n][lane] = make_uint2(w0 | (w1 << 16), w2 | (w3 << 16));
+      }
+    }
+    if (c == 0) q_factor[8 * nt + r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
   }
 
-  // This lane's rows are 2c and 2c + 1 of every tile: scale, key limits, slope.
+  // This lane's rows are 2c and 2c + 1 of every tile: scale, position, slope.
   float m[NT][2], l[NT][2], slope[NT][2];
   int pos[NT][2];
   int all_lo = 0, all_hi = kr.hi;  // keys [all_lo, all_hi) are attended by every live row of the block
@@ -327,10 +400,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 3 : 2) kv8_a
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
   float unit = 1.f, unit_top = 0.f;  // acc is in units of `unit`
   __syncthreads();
-  uint2 q_reg[NT == 1 ? KS : 1];
+  uint2 q_reg[NT == 1 ? KQ : 1][NP];
   if (NT == 1) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q_reg[NT == 1 ? ks : 0] = q_frag[ks][0][lane];
+    for (int i = 0; i < KQ; ++i)
+#pragma unroll
+      for (int n = 0; n < NP; ++n) q_reg[NT == 1 ? i : 0][n] = q_frag[i][0][n][lane];
   }
   float fac[NT][2];
 #pragma unroll
@@ -338,58 +413,94 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 3 : 2) kv8_a
 #pragma unroll
     for (int e = 0; e < 2; ++e) fac[nt][e] = q_factor[8 * nt + 2 * c + e];
 
-  auto compute = [&](int stage, bool page_ok, int at) {
-    const uint32_t slot = ring + stage * G::kStageBytes + threadIdx.x * 16;
-    float2 scales;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                 : "=f"(scales.x), "=f"(scales.y)
-                 : "r"(ring + G::kScales + (stage * kWarps + warp) * 8)
-                 : "memory");
-    uint4 kv[G::kK];
+  // where in a tile the lane reads (key r and value row 2c, each first chunk)
+  const uint32_t k_read = D == 128 ? r * 128 + (c ^ ((r & 1) * 4)) * 16 : (r >> 1) * 128 + ((r & 1) * 4 + c) * 16;
+  const uint32_t v_read = D == 128 ? 2 * c * 128 + (r ^ (2 * c)) * 16 : c * 128 + ((r >> 1) ^ (2 * c)) * 16 + (r & 1) * 8;
+
+  auto compute = [&](int stage, int at) {
+    const uint32_t step_bad = bad_tiles >> (stage * U) & ((1u << U) - 1u);
+    if (step_bad) bad_tiles &= ~(((1u << U) - 1u) << (stage * U));
+    const uint32_t slot = ring + stage * G::kStageBytes + warp * G::kWarpBytes;
+    float ks[U], vs[U], sc[U][NT][4];
 #pragma unroll
-    for (int i = 0; i < G::kK; ++i) kv[i] = read_slot16(slot + i * (kThreads * 16));
-    float sc[NT][4];
+    for (int u = 0; u < U; ++u) {
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(ks[u]), "=f"(vs[u])
+                   : "r"(ring + G::kScales + ((stage * kWarps + warp) * U + u) * 8)
+                   : "memory");
+      // codes [64 x + 16 c, + 16) of keys r and r + 8
+      uint4 kv[2 * (D / 64)];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint4 k0 = kv[ks >> 2], k1 = kv[(D / 64) + (ks >> 2)];
-      const uint32_t w0 = (ks & 3) == 0 ? k0.x : (ks & 3) == 1 ? k0.y : (ks & 3) == 2 ? k0.z : k0.w;
-      const uint32_t w1 = (ks & 3) == 0 ? k1.x : (ks & 3) == 1 ? k1.y : (ks & 3) == 2 ? k1.z : k1.w;
-      uint32_t a0, a1, a2, a3;
-      widen4(w0, a0, a2);
-      widen4(w1, a1, a3);
+        for (int x = 0; x < D / 64; ++x)
+          kv[i * (D / 64) + x] = read_slot16(((slot + k_read) ^ (64u * x)) + u * 2 * G::kHalf + i * (G::kHalf / 2));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint2 f = NT == 1 ? q_reg[NT == 1 ? ks : 0] : q_frag[ks][nt][lane];
-        mma_f16(sc[nt], a0, a1, a2, a3, f.x, f.y);
+        float part[NP][4];
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KQ; ++i) {
+          const uint4 k0 = kv[i >> 1], k1 = kv[(D / 64) + (i >> 1)];
+#pragma unroll
+          for (int n = 0; n < NP; ++n) {
+            const uint2 f = NT == 1 ? q_reg[NT == 1 ? i : 0][n] : q_frag[i][nt][n][lane];
+            mma_e4m3(part[n], i & 1 ? k0.z : k0.x, i & 1 ? k1.z : k1.x, i & 1 ? k0.w : k0.y, i & 1 ? k1.w : k1.y, f.x, f.y);
+          }
+        }
+        const float f[2] = {ks[u] * fac[nt][0], ks[u] * fac[nt][1]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = part[NP - 1][e];
+#pragma unroll
+          for (int n = NP - 2; n >= 0; --n) x = fmaf(x, 0.0625f, part[n][e]);
+          sc[u][nt][e] = x * f[e & 1];
+        }
       }
     }
-    const float vs = page_ok ? scales.y : unit;
-    const bool whole = at >= all_lo && at + kStep <= all_hi && page_ok;
+    const bool whole = at >= all_lo && at + kStep <= all_hi && step_bad == 0u;
+    auto attends = [&](int u, int nt, int e) {
+      const int j = at + kTile * u + r + 8 * (e >> 1), i = pos[nt][e & 1];
+      return !(step_bad >> u & 1u) && j < kr.keys && i >= 0 && (!p.causal || j <= i) && (p.window <= 0 || j > i - p.window);
+    };
+    if (p.alibi) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[u][nt][e] = fmaf(-slope[nt][e & 1], fabsf((float)(pos[nt][e & 1] - (at + kTile * u + r + 8 * (e >> 1)))),
+                                sc[u][nt][e]);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!attends(u, nt, e)) sc[u][nt][e] = -INFINITY;
+    }
     bool over = false;
-    bool keep[NT][4];
+    float top[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = at + r + 8 * (e >> 1), i = pos[nt][e & 1];
-        float x = sc[nt][e] * (scales.x * fac[nt][e & 1]);
-        if (p.alibi) x = fmaf(-slope[nt][e & 1], fabsf((float)(i - j)), x);
-        keep[nt][e] = true;
-        if (!whole) {
-          keep[nt][e] = page_ok && j < kr.keys && i >= 0 && (!p.causal || j <= i) && (p.window <= 0 || j > i - p.window);
-          if (!keep[nt][e]) x = -INFINITY;
-        }
-        sc[nt][e] = x;
-        over |= x > m[nt][e & 1] + kTop;
+      for (int e = 0; e < 2; ++e) {
+        top[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
+        if (U == 2) top[nt][e] = fmax3(top[nt][e], sc[U - 1][nt][e], sc[U - 1][nt][e + 2]);
+        over |= top[nt][e] > m[nt][e] + kTop;
       }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
+          float x = top[nt][e];
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -405,12 +516,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 3 : 2) kv8_a
           }
         }
     }
-    float pv = 1.f;
-    if (vs != unit) {
-      // another V scale: the sums go over to its unit, but not below 2^-64 of
-      // the largest so far (P takes the rest), so that they stay in range
-      unit_top = fmaxf(unit_top, vs);
-      const float to = fmaxf(fmaxf(vs, unit_top * 5.421010862427522e-20f), 1.1754944e-38f);
+    float pv[U];
+    bool other = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (step_bad >> u & 1u) vs[u] = unit;
+      pv[u] = 1.f;
+      other |= vs[u] != unit;
+    }
+    if (other) {
+      // another V scale: the sums go over to its unit (the larger one of a step's two), but not
+      // below 2^-64 of the largest so far (P takes the rest), so that they stay in range
+      float to = vs[0];
+#pragma unroll
+      for (int u = 1; u < U; ++u) to = fmaxf(to, vs[u]);
+      unit_top = fmaxf(unit_top, to);
+      to = fmaxf(fmaxf(to, unit_top * 5.421010862427522e-20f), 1.1754944e-38f);
       const float f = unit / to;
 #pragma unroll
       for (int i = 0; i < KS; ++i)
@@ -419,115 +540,123 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 3 : 2) kv8_a
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][nt][e] *= f;
       unit = to;
-      pv = vs / to;
-    }
-    uint32_t b0[NT], b1[NT], d0[NT], d1[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = ex2_approx(sc[nt][e] - m[nt][e & 1]);
-        l[nt][e & 1] += x[e];
-        x[e] *= pv;
-      }
-      const uint32_t lo = pack2<false>(x[0], x[1]), hi = pack2<false>(x[2], x[3]);
-      if (kResidual) {
-        d0[nt] = transpose8x8(pack2_residual<false>(x[0], x[1], lo));
-        d1[nt] = transpose8x8(pack2_residual<false>(x[2], x[3], hi));
-      }
-      b0[nt] = transpose8x8(lo);
-      b1[nt] = transpose8x8(hi);
+      for (int u = 0; u < U; ++u) pv[u] = vs[u] / to;
     }
-    uint32_t v[4][D / 32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = ring + stage * G::kStageBytes + G::kK * 16 * kThreads + (i * kThreads + threadIdx.x) * G::kVBytes;
-      if (D == 128) {
-        const uint4 x = read_slot16(a);
-        v[i][0] = x.x, v[i][1] = x.y, v[i][D / 32 - 2] = x.z, v[i][D / 32 - 1] = x.w;
-      } else {
-        const uint2 x = read_slot8(a);
-        v[i][0] = x.x, v[i][1] = x.y;
+    for (int u = 0; u < U; ++u) {
+      uint32_t b0[NT], b1[NT], d0[NT], d1[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = ex2_approx(sc[u][nt][e] - m[nt][e & 1]);
+          l[nt][e & 1] += x[e];
+        }
+        if (pv[u] != 1.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] *= pv[u];
+        }
+        const uint32_t lo = pack2<false>(x[0], x[1]), hi = pack2<false>(x[2], x[3]);
+        if (kResidual) {
+          d0[nt] = transpose8x8(pack2_residual<false>(x[0], x[1], lo));
+          d1[nt] = transpose8x8(pack2_residual<false>(x[2], x[3], hi));
+        }
+        b0[nt] = transpose8x8(lo);
+        b1[nt] = transpose8x8(hi);
       }
-    }
-    if (!whole) {
-      // Values behind the last key are whatever the page holds: zeros for the
-      // product. A NaN among the others belongs to the rows that attend to its
-      // key and to no other row, but the product would give it to all (0 * NaN):
-      // it is taken out here, and rows that attend to it get their NaN by a
-      // product of where the NaNs are with who attends.
-      bool has = false;
+      // values [(D / 8) r, + D / 8) of keys 2c, 2c + 1, 2c + 8, 2c + 9
+      uint32_t v[4][D / 32];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool dead = at + 2 * c + (i & 1) + 8 * (i >> 1) >= kr.keys;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          if (dead) v[i][w] = 0u;
-          has |= nan_bytes(v[i][w]) != 0u;
+        const uint32_t far = u * 2 * G::kHalf + G::kHalf + (i >> 1) * (G::kHalf / 2);
+        if (D == 128) {
+          const uint4 x = read_slot16(slot + v_read + far + (i & 1) * 128);
+          v[i][0] = x.x, v[i][1] = x.y, v[i][D / 32 - 2] = x.z, v[i][D / 32 - 1] = x.w;
+        } else {
+          const uint2 x = read_slot8(((slot + v_read) ^ (64u * (i & 1))) + far);
+          v[i][0] = x.x, v[i][1] = x.y;
         }
       }
-      if (__any_sync(0xffffffffu, has)) {
-        uint32_t i0[NT], i1[NT];
+      if (!whole) {
+        // Values behind the last key are whatever the page holds: zeros for the
+        // product. A NaN among the others belongs to the rows that attend to its
+        // key and to no other row, but the product would give it to all (0 * NaN):
+        // it is taken out here, and rows that attend to it get their NaN by a
+        // product of where the NaNs are with who attends.
+        bool has = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          i0[nt] = transpose8x8((keep[nt][0] ? 0x3C00u : 0u) | (keep[nt][1] ? 0x3C000000u : 0u));
-          i1[nt] = transpose8x8((keep[nt][2] ? 0x3C00u : 0u) | (keep[nt][3] ? 0x3C000000u : 0u));
-        }
+        for (int i = 0; i < 4; ++i) {
+          const bool dead = at + kTile * u + 2 * c + (i & 1) + 8 * (i >> 1) >= kr.keys;
 #pragma unroll
-        for (int mt = 0; mt < KS; ++mt) {
-          const int w = mt >> 1, sh = 16 * (mt & 1);
-          uint32_t f[4];  // flags (f16 one or zero) of the two values of this tile for the four keys
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = nan_bytes(v[i][w]) >> sh;
-          auto pair = [](uint32_t a, uint32_t b2, uint32_t bit) {
-            return ((a & bit) ? 0x3C00u : 0u) | ((b2 & bit) ? 0x3C000000u : 0u);
-          };
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float hit[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(hit, pair(f[0], f[1], 0x80u), pair(f[0], f[1], 0x8000u), pair(f[2], f[3], 0x80u),
-                    pair(f[2], f[3], 0x8000u), i0[nt], i1[nt]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (hit[e] > 0.f) acc[mt][nt][e] = __int_as_float(0x7FC00000);
+          for (int w = 0; w < D / 32; ++w) {
+            if (dead) v[i][w] = 0u;
+            has |= nan_bytes(v[i][w]) != 0u;
           }
         }
+        if (__any_sync(0xffffffffu, has)) {
+          uint32_t i0[NT], i1[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int nt = 0; nt < NT; ++nt) {
+            i0[nt] = transpose8x8((attends(u, nt, 0) ? 0x3C00u : 0u) | (attends(u, nt, 1) ? 0x3C000000u : 0u));
+            i1[nt] = transpose8x8((attends(u, nt, 2) ? 0x3C00u : 0u) | (attends(u, nt, 3) ? 0x3C000000u : 0u));
+          }
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) v[i][w] &= ~((nan_bytes(v[i][w]) >> 7) * 0xFFu);
+          for (int mt = 0; mt < KS; ++mt) {
+            const int w = mt >> 1, sh = 16 * (mt & 1);
+            uint32_t f[4];  // NaN flags of the two values of this tile for the four keys
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = nan_bytes(v[i][w]) >> sh;
+            auto pair = [](uint32_t x, uint32_t y, uint32_t bit) {
+              return ((x & bit) ? 0x3C00u : 0u) | ((y & bit) ? 0x3C000000u : 0u);
+            };
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float hit[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(hit, pair(f[0], f[1], 0x80u), pair(f[0], f[1], 0x8000u), pair(f[2], f[3], 0x80u),
+                      pair(f[2], f[3], 0x8000u), i0[nt], i1[nt]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (hit[e] > 0.f) acc[mt][nt][e] = __int_as_float(0x7FC00000);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) v[i][w] &= ~((nan_bytes(v[i][w]) >> 7) * 0xFFu);
+        }
       }
-    }
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      // codes of two keys side by side: bytes (k0.0, k1.0, k0.1, k1.1) and (k0.2, k1.2, k0.3, k1.3)
-      const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-      const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-      uint32_t a0, a1, a2, a3;
+      for (int w = 0; w < D / 32; ++w) {
+        // codes of two keys side by side: bytes (k0.0, k1.0, k0.1, k1.1) and (k0.2, k1.2, k0.3, k1.3)
+        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        uint32_t a0, a1, a2, a3;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        widen4(half ? x1 : x0, a0, a1);
-        widen4(half ? y1 : y0, a2, a3);
+        for (int half = 0; half < 2; ++half) {
+          widen4(half ? x1 : x0, a0, a1);
+          widen4(half ? y1 : y0, a2, a3);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, b0[nt], b1[nt]);
-          if (kResidual) mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, d0[nt], d1[nt]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, b0[nt], b1[nt]);
+            if (kResidual) mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, d0[nt], d1[nt]);
+          }
         }
       }
     }
   };
 
-  int stage = 0, step = 0;
+  int stage = 0;
   for (int base = first; base < end; base += kHop) {
-    const int page = next_page;
-    next_page = page_of(base + G::kStages * kHop);
-    fetch(page);
+    const Pages pg = next_pages;
+    next_pages = pages_of(base + G::kStages * kHop);
+    __syncwarp();  // (every lane has read what the next copies overwrite)
+    fetch(pg);
     copies_wait<G::kStages - 1>();
-    __syncwarp();  // (the scales' copies are lanes 0's and 1's)
-    compute(stage, (page_bits >> (step & 31)) & 1u, base);
+    __syncwarp();  // every lane's copies have landed
+    compute(stage, base);
     stage = stage + 1 == G::kStages ? 0 : stage + 1;
-    ++step;
   }
   if (bad && lane == 0) atomicOr(p.c.status, kStatusBadPage);
   copies_wait<0>();
@@ -739,7 +868,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(const __grid_
 template <typename T, int D, int NT>
 cudaError_t launch_nt(const Kv8AttnParams& p, cudaStream_t st) {
   constexpr auto kKernel = kv8_attn_kernel<T, D, NT>;
-  cudaError_t e = allow_smem<kKernel>(Ring<D>::kBytes);
+  constexpr int kBytes = Ring<D, NT == 4 ? 1 : 2>::kBytes;
+  cudaError_t e = allow_smem<kKernel>(kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -748,7 +878,7 @@ cudaError_t launch_nt(const Kv8AttnParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.splits, p.c.H * p.row_tiles, p.B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Ring<D>::kBytes;
+  cfg.dynamicSmemBytes = kBytes;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = p.cluster ? 1 : 0;
@@ -771,19 +901,20 @@ cudaError_t launch_tiles(const Kv8AttnParams& p, int tiles, cudaStream_t st) {
 // that more blocks would gain less than the joining kernel's launch costs. What is
 // left, few sequences with long contexts, gets one resident set of blocks.
 Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window) {
-  constexpr long long kClusterKeys = 512, hop = kStep * kWarps;
+  constexpr long long kClusterKeys = 512, hop = kHopKeys;
+  // with that many blocks in line already, splits of fewer keys cost more than they even out
+  constexpr long long kSplitBlocks = 1, kSplitKeys = 4096;
   Kv8AttnPlan plan;
   const long long R = (long long)T * (Hq / H);
   plan.tiles = R <= 8 ? 1 : R <= 16 ? 2 : 4;
   plan.row_tiles = (int)((R + 8 * plan.tiles - 1) / (8 * plan.tiles));
   // keys that one block's rows can reach
   long long range = key_limit;
-  if (causal && window > 0) range = std::min<long long>(range, (long long)window + T + kStep);
-  const long long units = (long long)B * H * plan.row_tiles, slots = 152 * (plan.tiles == 4 ? 2 : 3);
+  if (causal && window > 0) range = std::min<long long>(range, (long long)window + T + kTile);
+  const long long units = (long long)B * H * plan.row_tiles, slots = 152 * (plan.tiles == 1 ? 3 : 2);
   const auto round_hop = [&](long long x) { return std::max(hop, (x + hop - 1) / hop * hop); };
   long long splits = std::min<long long>(kMaxCluster, (range + hop - 1) / hop);
-  // (with more units than slots several rounds of blocks run anyway: splits of at least 1024 keys then)
-  while (splits > 1 && units * splits > 8 * slots && range / splits < 1024) splits >>= 1;
+  while (splits > 1 && units * splits > kSplitBlocks * slots && range / splits < kSplitKeys) splits >>= 1;
   plan.cluster = 1;
   if (units * kMaxCluster < slots && round_hop((range + splits - 1) / splits) > kClusterKeys) {
     plan.cluster = 0;

@@ -355,7 +355,8 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
  * The library cannot check device contents: tokens past max_pages pages are
  * ignored, a table entry outside [0, num_pages) makes its page's tokens be
  * skipped (not written, not attended to) and sets bit 4 of the device status
- * word. B <= 65535, H <= 1024, max_pages * page_size <= 2^30.
+ * word. B <= 65535, H <= 1024, max_pages * page_size <= 2^30,
+ * strides.n * page_size <= 2^30.
  * ------------------------------------------------------------------------- */
 typedef struct {
   void* k;

@@ -101,6 +101,7 @@ def _calls(lib, c, s, *, T=1, Hq=4, dt=BF16, q=P, k=P, st=None):
     (dict(k=P + 8), {}, {}, EALIGN), (dict(k_scale=P + 2), {}, {}, EALIGN),
     (dict(strides=fa.FaStrides(16384, 136, 8192)), {}, {}, EALIGN),
     (dict(strides=fa.FaStrides(0, 128, 8192)), {}, {}, EINVAL),
+    (dict(strides=fa.FaStrides(1 << 40, 1 << 28, 128)), {}, {}, EUNSUP),
     ({}, dict(block_table=0), {}, EINVAL), ({}, dict(seq_lens=0), {}, EINVAL), ({}, dict(B=0), {}, EINVAL),
     ({}, dict(max_pages=0), {}, EINVAL), ({}, dict(table_stride=-1), {}, EINVAL), ({}, dict(B=65536), {}, EUNSUP),
     ({}, dict(max_pages=(1 << 24) + 1), {}, EUNSUP), ({}, dict(seq_lens=P + 2), {}, EALIGN),
