@@ -845,6 +845,7 @@ def kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_weight, k_weight, cos, sin,
                              interleaved, None)
 
 
+@lru_cache(maxsize=1024)
 def fa_kv8_attn_workspace_size(B: int, T: int, Hq: int, H: int, d: int, page_size: int, max_pages: int,
                                max_seqlen: int, causal: bool = True, window: int = 0) -> int:
     return load_library().fa_kv8_attn_workspace_size(B, T, Hq, H, d, page_size, max_pages, int(max_seqlen),
@@ -859,24 +860,26 @@ def _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, ne
     lib = _lib or load_library()
     q_st = _rows_layout(q, shape, dtype, dev, "q")
     if o is None:
-        size = lib.fa_kv8_attn_workspace_size(B, T, Hq, c.H, d, c.page_size, s.max_pages, max_seqlen, causal, window)
+        size = fa_kv8_attn_workspace_size(B, T, Hq, c.H, d, c.page_size, s.max_pages, max_seqlen, causal, window)
         device = q.device
         o = torch.empty_like(q, memory_format=torch.contiguous_format)
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=device)
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device) if size else None
         o_st = _strides(T * Hq * d, Hq * d, d)
     else:
         o_st = _rows_layout(o, shape, dtype, dev, "o")
         if lse.dtype is not torch.float32 or lse.shape != (B, Hq, T) or not lse.is_contiguous() or \
                 lse.get_device() != dev:
             raise ValueError(f"lse must be a contiguous float32 [B, Hq, T] tensor on cuda:{dev}")
-        if workspace.get_device() != dev:
-            raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
-        size = workspace.numel() * workspace.element_size()
+        size = 0
+        if workspace is not None:
+            if workspace.get_device() != dev:
+                raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
+            size = workspace.numel() * workspace.element_size()
     slopes, per_seq = (None, 0) if alibi_slopes is None else _alibi(alibi_slopes, B, Hq, q.device)
     _check(lib.fa_kv8_attn(
         c, s, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T, Hq, max_seqlen, q_st, o_st, _TORCH_TO_FA[dtype],
-        default_scale(d) if scale is None else scale, causal, window, slopes, per_seq, workspace.data_ptr(), size,
+        default_scale(d) if scale is None else scale, causal, window, slopes, per_seq, None if workspace is None else workspace.data_ptr(), size,
         _stream(stream)))
     return o, lse
 
@@ -884,7 +887,7 @@ def _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, ne
 def fa_kv8_attn(q, cache: Kv8Cache, o, lse, block_table, seq_lens, max_seqlen, workspace, new_lens=None, scale=None,
                 causal=True, window=0, alibi_slopes=None, stream=None):
     """Attention over the cache through the C ABI: fills o ([B, T, Hq, d]) and lse ([B, Hq, T] fp32).
-    ``workspace`` is a uint8 CUDA tensor of fa_kv8_attn_workspace_size(...) bytes."""
+    ``workspace`` is a uint8 CUDA tensor of fa_kv8_attn_workspace_size(...) bytes (None where that is 0)."""
     _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, new_lens, scale, causal, window,
               alibi_slopes, stream)
 

@@ -133,7 +133,7 @@ int append_run(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q
   if (rc) return rc;
   if (T < 1) return FA_ERR_INVALID_ARG;
   if ((rc = check_16bit(dtype))) return rc;
-  if (T > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (T > (1 << 19)) return FA_ERR_UNSUPPORTED;  // the pages that T tokens reach are a grid's y extent
   if (norm && (rc = check_rope(seqs->B, T, Hq, cache->H, cache->d, rot_dim, max_pos, dtype, weight_dtype, eps)))
     return rc;
   if ((rc = first_error({check_tensor(k, k_strides, dtype), check_tensor(v, v_strides, dtype)}))) return rc;
@@ -151,10 +151,8 @@ int append_run(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q
   p.B = seqs->B;
   p.T = T;
   p.d = cache->d;
-  p.pages = std::min((T - 1 + cache->page_size - 1) / cache->page_size + 1, seqs->max_pages);
-  const long long blocks = (long long)p.B * p.pages * 2 * cache->H;
-  const long long q_rows = norm ? (long long)p.B * T * Hq : 0;
-  if (blocks + q_rows > 0x7fffffffll) return FA_ERR_UNSUPPORTED;
+  p.pages = (T - 1 + cache->page_size - 1) / cache->page_size + 1;
+  if (!norm) p.pages = std::min(p.pages, seqs->max_pages);  // (q's rows need no page)
   if (norm) {
     p.q = q;
     p.q_out = q_out;
@@ -314,7 +312,9 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
   if (alibi_stride_b < 0) return FA_ERR_INVALID_ARG;
   const fa::Kv8AttnPlan plan = attn_plan(seqs->B, T, Hq, cache->H, cache->d, cache->page_size, seqs->max_pages,
                                          max_seqlen, causal, window);
-  if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < plan.workspace) return FA_ERR_WORKSPACE;
+  if (plan.workspace > 0 && (!workspace || !aligned_to(workspace, 256) || workspace_bytes < plan.workspace))
+    return FA_ERR_WORKSPACE;
+  if (plan.workspace == 0) workspace = nullptr;  // not used
   fa::Kv8AttnParams p;
   std::memset(&p, 0, sizeof(p));
   fill_cache(p.c, cache, seqs, shift);

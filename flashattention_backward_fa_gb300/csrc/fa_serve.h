@@ -111,8 +111,7 @@ struct Kv8AppendParams {
   const float* sin;
   int rot, max_pos, neighbours, w_f32;
   float eps;
-  // set by the launcher: blocks [0, kv_blocks) take the cache's pages, the others q's rows, q_span a row group
-  int kv_blocks, q_span;
+  int q_span;  // set by the launcher: rows of q a row group takes
 };
 cudaError_t launch_kv8_append(Kv8AppendParams& p, bool bf16, cudaStream_t st);
 

@@ -28,6 +28,7 @@ namespace fa {
 namespace {
 
 constexpr int kQDepth = 3;    // rows of q a row group has on their way, and the one at hand
+constexpr int kQRows = 32;    // most rows of q that a row group takes
 constexpr int kMinExp = -100;  // least scale exponent: blocks of zeros (or below 2^-91) get it
 
 // The scale's bits for a largest finite magnitude: 448 = 1.75 * 2^8.
@@ -123,48 +124,49 @@ __device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T)
   return n;
 }
 
-// Blocks [0, kv_blocks): (sequence, reached page, keys or values, head), heads
-// fastest. kRows rows of a page a thread; blockDim.x * kRows * 8 values hold a
-// page's new rows. kNorm: 0 append alone, 1 / 2 norm and rotation with partners
-// rot / 2 apart / neighbours.
+// Grid: x the heads of k, then of v, then (kNorm) blocks that share q's rows of
+// the page's tokens; y the page among those that T tokens reach; z the sequence.
+// kRows rows of a page a thread; blockDim.x * kRows * 16 values hold a page's new
+// rows. kNorm: 0 append alone, 1 / 2 norm and rotation with partners rot / 2
+// apart / neighbours.
 template <typename T, int D, int kRows, int kNorm>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
+__global__ void __launch_bounds__(256, kNorm == 0 ? (kRows == 4 ? 4 : 8) : (kRows == 4 ? 2 : 3)) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   extern __shared__ __align__(16) unsigned char ring[];  // (q's rows only)
   constexpr int G = D / 16;
   constexpr bool kNeighbours = kNorm != 1;
   __shared__ uint32_t red[8];
   const Kv8Cache& c = p.c;
   __shared__ __align__(16) float w[D];
-  if (kNorm != 0 && blockIdx.x >= (unsigned)p.kv_blocks) {
-    // q: q_span rows (b, t, head) a row group; rows without a token become zeros
-    const long long group = (long long)(blockIdx.x - p.kv_blocks) * (blockDim.x / G) + threadIdx.x / G;
+  const int b = blockIdx.z;
+  const NewTokens n = new_tokens(c, b, p.T);
+  if (kNorm != 0 && blockIdx.x >= 2u * c.H) {
+    // q: rows (t, head) of the tokens whose positions fall into the page (the positions of padding
+    // rows run on past the sequence, or before it), q_span a row group; padding rows become zeros
+    const long long lo = ((long long)(n.start >> c.page_shift) + blockIdx.y) << c.page_shift;
+    const int t_lo = (int)max(lo - n.start, 0ll);
+    const int t_hi = (int)min(lo + (1 << c.page_shift) - n.start, (long long)p.T);
+    if (t_lo >= t_hi) return;
+    fa_strides in = p.q_st, out = p.q_out_st;
+    const long long group = (long long)(blockIdx.x - 2u * c.H) * (blockDim.x / G) + threadIdx.x / G;
     norm_rope_rows<T, D, kNeighbours, true, kQDepth>(
-        ring, static_cast<const T*>(p.q), static_cast<T*>(p.q_out), p.q_st, p.q_out_st, (long long)p.B * p.T * p.Hq, p.T,
-        p.Hq, group * p.q_span, p.q_span, p.q_w, p.w_f32, w, p.cos, p.sin, p.rot, p.eps, [&](long long b, int t) {
-          const NewTokens n = new_tokens(c, (int)b, p.T);
+        ring, static_cast<const T*>(p.q) + b * in.b + t_lo * in.n, static_cast<T*>(p.q_out) + b * out.b + t_lo * out.n,
+        in, out, (long long)(t_hi - t_lo) * p.Hq, t_hi - t_lo, p.Hq, group * p.q_span, p.q_span, p.q_w, p.w_f32, w,
+        p.cos, p.sin, p.rot, p.eps, [&](long long, int i) {
+          const int t = t_lo + i;
           return t < n.count && n.start + t >= 0 ? (long long)min(n.start + t, max(p.max_pos - 1, 0)) * (p.rot >> 1)
                                                  : -1ll;
         });
     return;
   }
-  unsigned x = blockIdx.x;
-  const int h = x % c.H;
-  x /= c.H;
-  const bool is_v = (x & 1u) != 0;
-  x >>= 1;
-  const int reached = x % p.pages, b = x / p.pages;
-  const NewTokens n = new_tokens(c, b, p.T);
+  const bool is_v = blockIdx.x >= (unsigned)c.H;
+  const int h = blockIdx.x - (is_v ? c.H : 0);
   const int size = 1 << c.page_shift;
-  const int pg = (max(n.start, 0) >> c.page_shift) + reached;
+  const int pg = (max(n.start, 0) >> c.page_shift) + blockIdx.y;
   if (pg >= c.max_pages) return;  // (and positions below stay in 31 bits)
   const int t_lo = max(max(n.start, 0), pg << c.page_shift);
   const int t_hi = min(n.len, (pg + 1) << c.page_shift);  // positions [t_lo, t_hi)
   if (t_lo >= t_hi) return;
-  const int id = __ldg(c.table + b * c.table_stride + pg);
-  if (id < 0 || id >= c.num_pages) {
-    if (threadIdx.x == 0) atomicOr(c.status, kStatusBadPage);
-    return;
-  }
+  const int id = __ldg(c.table + b * c.table_stride + pg);  // (checked once the rows' loads are under way)
   const int rows = t_hi - t_lo, slot0 = t_lo & (size - 1);
   const fa_strides& st = is_v ? p.v_st : p.k_st;
   const T* src = static_cast<const T*>(is_v ? p.v : p.k) + b * st.b + (long long)(t_lo - n.start) * st.n + h * st.h;
@@ -181,22 +183,32 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
       load8(rb[i], src + r * st.n + at.b);
     }
   }
+  if (id < 0 || id >= c.num_pages) {
+    if (threadIdx.x == 0) atomicOr(c.status, kStatusBadPage);
+    return;
+  }
   uint8_t* page = (is_v ? c.v : c.k) + id * c.sp + h * c.sh;
   float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)id * c.H + h;
   const float was = slot0 > 0 ? *scale_at : 0.f;  // a page without earlier tokens has no former scale
   if (kNorm != 0 && !is_v) {
+    // every load of the rows, the weights and the tables is under way before the first is used
+    constexpr int kAhead = kRows < 2 ? kRows : 2;
+    float cc[kAhead][8], ss[kAhead][8];
+    auto rotation = [&](int i, float (&cr)[8], float (&sr)[8]) {
+      const int r = row0 + i * groups;
+      const long long row = r < rows ? (long long)min(t_lo + r, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
+      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, r < rows ? p.rot : 0, cr, sr);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) rotation(i, cc[i], ss[i]);
     stage_weights<T>(p.k_w, p.w_f32, D, w);
     __syncthreads();
+    LaneWeights lw;
+    lw.read(w, at);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int r = row0 + i * groups;
-      const bool live = r < rows;
-      const long long row = live ? (long long)min(t_lo + r, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
-      float cc[8], ss[8];
-      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, live ? p.rot : 0, cc, ss);
-      Factors f;
-      fold_weights<kNeighbours>(w, at, cc, ss, f);
-      norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], f, p.eps);  // (zeros stay zeros)
+      norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], lw, cc[i % kAhead], ss[i % kAhead], p.eps);  // (zeros stay zeros)
+      if (i + kAhead < kRows) rotation(i + kAhead, cc[i % kAhead], ss[i % kAhead]);
     }
   }
   uint32_t m = 0u;
@@ -241,7 +253,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(const __grid_constant__
 }
 
 template <typename T, int D, int kRows>
-cudaError_t launch_rows(const Kv8AppendParams& p, unsigned grid, int threads, cudaStream_t st) {
+cudaError_t launch_rows(const Kv8AppendParams& p, dim3 grid, int threads, cudaStream_t st) {
   const int ring = RowRing<T, 2, kQDepth>::bytes(threads);
   if (p.q == nullptr)
     kv8_append_kernel<T, D, kRows, 0><<<grid, threads, 0, st>>>(p);
@@ -261,14 +273,15 @@ cudaError_t launch_d(Kv8AppendParams& p, cudaStream_t st) {
   const int lanes = rows * G;
   const int per = lanes <= 256 ? 1 : lanes <= 512 ? 2 : 4;
   const int threads = std::max(64, ((lanes + per - 1) / per + 31) / 32 * 32);
-  const long long kv = (long long)p.B * p.pages * 2 * p.c.H;
-  // q: one row a group up to a resident set of blocks, then more rows a group
-  const long long q_rows = p.q ? (long long)p.B * p.T * p.Hq : 0, groups = threads / G;
-  p.q_span = (int)std::max<long long>(1, std::min<long long>(16, q_rows / (groups * 152 * 8)));
-  const long long q = (q_rows + groups * p.q_span - 1) / (groups * p.q_span);
-  if (kv + q > 0x7fffffffll) return cudaErrorInvalidValue;
-  p.kv_blocks = (int)kv;
-  const unsigned grid = (unsigned)(kv + q);
+  int q_blocks = 0;
+  if (p.q) {
+    // q's rows of a page's tokens: kQRows a row group where there are that many, so that a token's
+    // factors serve several heads, and one where that leaves the GPU empty
+    const long long q_rows = (long long)rows * p.Hq, groups = threads / G;
+    p.q_span = (int)std::max<long long>(1, std::min<long long>(kQRows, q_rows * p.pages * p.B / (groups * 152 * 4)));
+    q_blocks = (int)((q_rows + groups * p.q_span - 1) / (groups * p.q_span));
+  }
+  const dim3 grid(2 * p.c.H + q_blocks, p.pages, p.B);
   if (per == 1) return launch_rows<T, D, 1>(p, grid, threads, st);
   return per == 2 ? launch_rows<T, D, 2>(p, grid, threads, st) : launch_rows<T, D, 4>(p, grid, threads, st);
 }

@@ -187,9 +187,6 @@ struct Ring {
   static constexpr int kBytes = kScales + kStages * kWarps * U * 8;
 };
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -923,7 +920,7 @@ Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int
   plan.chunk = (int)round_hop((range + splits - 1) / splits);
   plan.splits = (int)((range + plan.chunk - 1) / plan.chunk);
   if (plan.splits == 1) plan.cluster = 0;
-  plan.workspace = 256;
+  plan.workspace = 0;
   if (plan.splits > 1 && !plan.cluster)
     plan.workspace = ((size_t)B * Hq * T * plan.splits * (d + 1) * 4 + 255) / 256 * 256;
   return plan;

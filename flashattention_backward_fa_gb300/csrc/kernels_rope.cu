@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
   constexpr int G = D / 16, kGroups = kRopeThreads / G;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float w[D];
-  const RowRing<T, 4, kBwdDepth> ring(smem);
+  RowRing<T, 4, kBwdDepth> ring(smem);
   const int group = threadIdx.x / G;
   const bool is_k = blockIdx.x >= (unsigned)p.q_blocks;
   const RopeSide& sd = is_k ? p.k : p.q;
@@ -62,24 +62,31 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
   const long long first = ((long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * kGroups + group) * sd.span;
   const int live = (int)min((long long)sd.span, max(rows - first, 0ll));
   const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % G, p.rot);
-  RowWalk wx, wg, wo;
+  RowWalk wx;
   wx.start(first, p.N, sd.H, sd.x_st);
-  wg.start(first, p.N, sd.H, sd.out_st);
-  wo.start(first, p.N, sd.H, sd.dx_st);
+  RowWalk wg = wx.in(sd.out_st), wo = wx.in(sd.dx_st);
   uint64_t dwa[4], dwb[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dwa[i] = dwb[i] = 0ull;
   float c[8], s[8];
   int loaded = 0;
+  const T* x_in = static_cast<const T*>(sd.x) + at.a;
+  const T* g_in = static_cast<const T*>(sd.dout) + at.a;
+  T* dx_out = static_cast<T*>(sd.dx) + at.a;
+  const int hop = at.b - at.a;
   auto fetch = [&] {
-    const bool ok = loaded < live;
-    const T* x = static_cast<const T*>(sd.x) + (ok ? wx.at : 0);
-    const T* g = static_cast<const T*>(sd.dout) + (ok ? wg.at : 0);
-    ring.fetch(loaded, 0, x + at.a, ok);
-    ring.fetch(loaded, 1, x + at.b, ok);
-    ring.fetch(loaded, 2, g + at.a, ok);
-    ring.fetch(loaded, 3, g + at.b, ok);
+    if (loaded < live) {
+      const T* x = x_in + wx.at;
+      const T* g = g_in + wg.at;
+      ring.fetch(0, x);
+      ring.fetch(1, x + hop);
+      ring.fetch(2, g);
+      ring.fetch(3, g + hop);
+    } else if (loaded < sd.span) {
+      ring.clear();
+    }
     copies_commit();
+    ring.step(ring.put);
     wx.next(p.N, sd.H, sd.x_st);
     wg.next(p.N, sd.H, sd.out_st);
     ++loaded;
@@ -99,9 +106,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
     copies_wait<kBwdDepth - 1>();
     Raw8<T> raw;
     uint64_t xa[4], xb[4], ga[4], gb[4];
-    ring.take(i, 2, raw);
+    ring.take(2, raw);
     raw.unpack(ga);
-    ring.take(i, 3, raw);
+    ring.take(3, raw);
     raw.unpack(gb);
     // dy = R^T dout
 #pragma unroll
@@ -119,10 +126,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
         ga[j] = da;
       }
     }
-    ring.take(i, 0, raw);
+    ring.take(0, raw);
     raw.unpack(xa);
-    ring.take(i, 1, raw);
+    ring.take(1, raw);
     raw.unpack(xb);
+    ring.step(ring.got);
     uint64_t s2 = 0ull, g2 = 0ull, wa[4], wb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -146,11 +154,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
       wb[j] = f2_mul(r2, f2_fma(xb[j], k2, wb[j]));
     }
     if (i < live) {
-      T* dx = static_cast<T*>(sd.dx) + wo.at;
+      T* dx = dx_out + wo.at;
       raw.pack(wa);
-      store8(raw, dx + at.a);
+      store8(raw, dx);
       raw.pack(wb);
-      store8(raw, dx + at.b);
+      store8(raw, dx + hop);
     }
     token = wo.next(p.N, sd.H, sd.dx_st);
   }
@@ -223,11 +231,10 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
   for (long long row = (long long)blk * 8 + warp; row < rows; row += (long long)blks * 8) {
     RowWalk a;
     a.start(row, p.N, sd.H, sd.x_st);
-    const auto offset = [&](const fa_strides& st) { return a.b * st.b + (long long)a.n * st.n + (long long)a.head * st.h; };
     const float* x = static_cast<const float*>(sd.x) + a.at;
     const long long at = p.rot ? table_row(p, a.b, a.n) : 0;
     float xv[4], gv[4], ss = 0.f;
-    const float* go = kBackward ? static_cast<const float*>(sd.dout) + offset(sd.out_st) : nullptr;
+    const float* go = kBackward ? static_cast<const float*>(sd.dout) + a.offset(sd.out_st) : nullptr;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int e = lane + 32 * j;
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
     }
     __syncwarp();
     if (!kBackward) {
-      float* o = static_cast<float*>(sd.out) + offset(sd.out_st);
+      float* o = static_cast<float*>(sd.out) + a.offset(sd.out_st);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (lane + 32 * j < d) o[lane + 32 * j] = y[j];
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
       }
       gx = row_sum<32>(gx);
       const float k1 = gx / d * r;
-      float* o = static_cast<float*>(sd.dx) + offset(sd.dx_st);
+      float* o = static_cast<float*>(sd.dx) + a.offset(sd.dx_st);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float xn = xv[j] * r;
@@ -341,18 +348,19 @@ cudaError_t launch_bwd(const RopeParams& p, cudaStream_t st) {
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }
 
-// Shares `blocks` blocks between q and k by their rows and gives every row group
-// its number of consecutive rows: a few resident sets of blocks where there
-// is work for them, so that a group's prologue (weights, first loads) is paid
-// once, and one row a group where there is not.
-void share_rows(RopeParams& p, int groups, long long blocks) {
+// Gives every row group its number of consecutive rows, and q and k their blocks:
+// blocks of `groups` row groups, at most `most` of them, and no fewer than `fewest`
+// (one resident set) for the sake of longer spans: from eight rows on a group's
+// prologue (weights, first loads, the row's place) no longer counts. Measured with
+// the forward at bf16 4x16x2048x128: 5 rows 26.1 us, 9 rows 24.3 us; at
+// 1x32x8192x128: 9 rows 47.2 us, 36 rows 50.1 us (ragged ends).
+void share_rows(RopeParams& p, int groups, long long fewest, long long most) {
   const long long rq = (long long)p.B * p.N * p.q.H, rk = (long long)p.B * p.N * p.k.H;
+  const long long span = std::max(div_up(rq + rk, most * groups), std::min(8ll, div_up(rq + rk, fewest * groups)));
   for (int side = 0; side < 2; ++side) {
     RopeSide& s = side ? p.k : p.q;
-    const long long rows = side ? rk : rq;
-    const long long share = std::max<long long>(1, blocks * rows / (rq + rk)) * groups;
-    s.span = (int)std::min<long long>(div_up(rows, share), 1 << 30);
-    const int n = (int)div_up(rows, groups * (long long)s.span);
+    s.span = (int)std::min<long long>(span, 1 << 30);
+    const int n = (int)div_up(side ? rk : rq, groups * (long long)s.span);
     if (side)
       p.blocks = p.q_blocks + n;
     else
@@ -366,11 +374,11 @@ int rope_bwd_max_blocks() { return kBwdBlocks + 2; }
 
 cudaError_t launch_norm_rope_fwd(RopeParams& p, int dtype, cudaStream_t st) {
   if (!vector_rows(p, dtype, false)) {
-    share_rows(p, 8, 152 * 8);
+    share_rows(p, 8, 152 * 8, 152 * 8);
     norm_rope_any_f32_kernel<false><<<p.blocks, kRopeThreads, 0, st>>>(p);
     return cudaGetLastError();
   }
-  share_rows(p, kRopeThreads / (p.d / 16), kFwdBlocks);
+  share_rows(p, kRopeThreads / (p.d / 16), kFwdBlocks / 4, kFwdBlocks);
   if (dtype == FA_F32) return launch_fwd<float>(p, st);
   return dtype == FA_BF16 ? launch_fwd<__nv_bfloat16>(p, st) : launch_fwd<__half>(p, st);
 }
@@ -379,11 +387,11 @@ cudaError_t launch_norm_rope_bwd(RopeParams& p, int dtype, cudaStream_t st) {
   const bool vec = vector_rows(p, dtype, true);
   cudaError_t e;
   if (!vec) {
-    share_rows(p, 8, kBwdBlocks);
+    share_rows(p, 8, kBwdBlocks, kBwdBlocks);
     norm_rope_any_f32_kernel<true><<<p.blocks, kRopeThreads, 0, st>>>(p);
     e = cudaGetLastError();
   } else {
-    share_rows(p, kRopeThreads / (p.d / 16), kBwdBlocks);
+    share_rows(p, kRopeThreads / (p.d / 16), kBwdBlocks, kBwdBlocks);
     if (dtype == FA_F32)
       e = launch_bwd<float>(p, st);
     else

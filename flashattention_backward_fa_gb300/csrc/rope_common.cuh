@@ -10,11 +10,9 @@
 // every pair are in one lane: with partners rot / 2 apart the second chunk is
 // the first one's partners (rot is a multiple of 16; what is not rotated goes
 // to the remaining lanes), with neighbouring partners the second chunk is D / 2
-// further on. Only the sum of squares crosses lanes. With the weights folded
-// into the token's factors, out = r (x C + partner S) is three packed (two-wide)
-// operations for two values; a layout with one chunk a lane, which exchanges
-// partners by shuffles, took 238 instructions for 16 values against about 90
-// and ran at 70% of the copy rate.
+// further on. Only the sum of squares crosses lanes, and everything else is packed
+// (two-wide) arithmetic. A layout with one chunk a lane, which exchanges partners
+// by shuffles, ran at 70% of the copy rate, bound by its instructions.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -93,9 +91,9 @@ __device__ __forceinline__ void zero8(Raw8<T>& v) {
   for (int i = 0; i < Raw8<T>::kQuads; ++i) v.q[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// 16 bytes from global to shared memory, asynchronously; zeros where !valid (nothing is read then).
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
@@ -155,41 +153,29 @@ __device__ __forceinline__ void load_rotation(const float* cos_row, const float*
   }
 }
 
-// A token's factors with the weights folded in: out_a = r (a ca + pa sa), pa the partners of a
-// (b, or a with neighbours swapped), and alike for b.
-struct Factors {
-  uint64_t ca[4], sa[4], cb[4], sb[4];
-};
-template <bool kNeighbours>
-__device__ __forceinline__ void fold_weights(const float* w, const LanePlace& at, const float (&c)[8],
-                                             const float (&s)[8], Factors& f) {
-  float wa[8], wb[8];
-  read4(w + at.a, wa);
-  read4(w + at.a + 4, wa + 4);
-  read4(w + at.b, wb);
-  read4(w + at.b + 4, wb + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int x = 2 * i, y = 2 * i + 1;
-    if (kNeighbours) {
-      f.ca[i] = f2_pack(c[i] * wa[x], c[i] * wa[y]);
-      f.sa[i] = f2_pack(-s[i] * wa[y], s[i] * wa[x]);
-      f.cb[i] = f2_pack(c[4 + i] * wb[x], c[4 + i] * wb[y]);
-      f.sb[i] = f2_pack(-s[4 + i] * wb[y], s[4 + i] * wb[x]);
-    } else {
-      f.ca[i] = f2_pack(c[x] * wa[x], c[y] * wa[y]);
-      f.sa[i] = f2_pack(-s[x] * wb[x], -s[y] * wb[y]);
-      f.cb[i] = f2_pack(c[x] * wb[x], c[y] * wb[y]);
-      f.sb[i] = f2_pack(s[x] * wa[x], s[y] * wa[y]);
-    }
-  }
-}
-
 __device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);
   return f2_pack(hi, lo);
 }
+
+__device__ __forceinline__ void read_pairs(const float* p, uint64_t (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 a = reinterpret_cast<const float4*>(p)[i];
+    f[2 * i] = f2_pack(a.x, a.y);
+    f[2 * i + 1] = f2_pack(a.z, a.w);
+  }
+}
+
+// The weights of a lane's two chunks.
+struct LaneWeights {
+  uint64_t a[4], b[4];
+  __device__ __forceinline__ void read(const float* w, const LanePlace& at) {
+    read_pairs(w + at.a, a);
+    read_pairs(w + at.b, b);
+  }
+};
 
 __device__ __forceinline__ float f2_sum(uint64_t v) {
   float lo, hi;
@@ -199,8 +185,9 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
 
 // Forward of a lane's 16 values, in place; every lane of the warp calls it (shuffles).
 template <typename T, int D, bool kNeighbours>
-__device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const Factors& f, float eps) {
-  uint64_t a[4], b[4], oa[4], ob[4];
+__device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const LaneWeights& w, const float (&c)[8],
+                                               const float (&s)[8], float eps) {
+  uint64_t a[4], b[4];
   ra.unpack(a);
   rb.unpack(b);
   uint64_t s0 = 0ull, s1 = 0ull;
@@ -214,11 +201,20 @@ __device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const F
   const uint64_t r = f2_pack(r1, r1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    oa[i] = f2_mul(r, f2_fma(a[i], f.ca[i], f2_mul(kNeighbours ? f2_swap(a[i]) : b[i], f.sa[i])));
-    ob[i] = f2_mul(r, f2_fma(b[i], f.cb[i], f2_mul(kNeighbours ? f2_swap(b[i]) : a[i], f.sb[i])));
+    a[i] = f2_mul(a[i], f2_mul(r, w.a[i]));
+    b[i] = f2_mul(b[i], f2_mul(r, w.b[i]));
+    if (kNeighbours) {
+      a[i] = f2_fma(a[i], f2_pack(c[i], c[i]), f2_mul(f2_swap(a[i]), f2_pack(-s[i], s[i])));
+      b[i] = f2_fma(b[i], f2_pack(c[4 + i], c[4 + i]), f2_mul(f2_swap(b[i]), f2_pack(-s[4 + i], s[4 + i])));
+    } else {
+      const uint64_t ci = f2_pack(c[2 * i], c[2 * i + 1]), si = f2_pack(s[2 * i], s[2 * i + 1]);
+      const uint64_t oa = f2_fma(a[i], ci, f2_mul(b[i], f2_pack(-s[2 * i], -s[2 * i + 1])));
+      b[i] = f2_fma(b[i], ci, f2_mul(a[i], si));
+      a[i] = oa;
+    }
   }
-  ra.pack(oa);
-  rb.pack(ob);
+  ra.pack(a);
+  rb.pack(b);
 }
 
 // A walk over the rows (b, n, head) of [B, N, H, *], heads fastest, with the
@@ -238,7 +234,16 @@ struct RowWalk {
     }
     head = (int)(row - token * H);
     n = (int)(token - b * N);
-    at = b * st.b + (long long)n * st.n + (long long)head * st.h;
+    at = offset(st);
+  }
+  __device__ __forceinline__ long long offset(const fa_strides& st) const {
+    return b * st.b + (long long)n * st.n + (long long)head * st.h;
+  }
+  // The same row in another tensor.
+  __device__ __forceinline__ RowWalk in(const fa_strides& st) const {
+    RowWalk w = *this;
+    w.at = offset(st);
+    return w;
   }
   // To the next row; true when it is another token's.
   __device__ __forceinline__ bool next(int N, int H, const fa_strides& st) {
@@ -261,23 +266,28 @@ template <typename T, int kChunks, int kDepth>
 struct RowRing {
   static constexpr int kPieces = kChunks * Raw8<T>::kQuads;
   static constexpr int bytes(int threads) { return kDepth * kPieces * threads * 16; }
-  uint32_t base;
-  int threads;
-  __device__ __forceinline__ RowRing(void* smem) : base(smem_u32(smem) + threadIdx.x * 16), threads(blockDim.x) {}
-  __device__ __forceinline__ uint32_t slot(int row, int chunk, int piece) const {
-    return base + (uint32_t)(((row % kDepth) * kPieces + chunk * Raw8<T>::kQuads + piece) * threads) * 16u;
+  uint32_t base, apart, put, got;  // slots of this thread, bytes between pieces, of the next row to come and to take
+  __device__ __forceinline__ RowRing(void* smem)
+      : base(smem_u32(smem) + threadIdx.x * 16), apart(blockDim.x * 16), put(base), got(base) {}
+  __device__ __forceinline__ void step(uint32_t& at) const {
+    at += kPieces * apart;
+    if (at == base + kDepth * kPieces * apart) at = base;
   }
-  __device__ __forceinline__ void fetch(int row, int chunk, const T* p, bool valid) const {
+  __device__ __forceinline__ void fetch(int chunk, const T* p) const {
 #pragma unroll
     for (int i = 0; i < Raw8<T>::kQuads; ++i)
-      copy16_async(slot(row, chunk, i), reinterpret_cast<const uint4*>(p) + i, valid);
+      copy16_async(put + (chunk * Raw8<T>::kQuads + i) * apart, reinterpret_cast<const uint4*>(p) + i);
   }
-  __device__ __forceinline__ void take(int row, int chunk, Raw8<T>& v) const {
+  __device__ __forceinline__ void clear() const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) st_shared_v4(put + i * apart, 0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void take(int chunk, Raw8<T>& v) const {
 #pragma unroll
     for (int i = 0; i < Raw8<T>::kQuads; ++i)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.q[i].x), "=r"(v.q[i].y), "=r"(v.q[i].z), "=r"(v.q[i].w)
-                   : "r"(slot(row, chunk, i))
+                   : "r"(got + (chunk * Raw8<T>::kQuads + i) * apart)
                    : "memory");
   }
 };
@@ -300,19 +310,26 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
                                                int count, const void* weights, bool w_f32, float* w,
                                                const float* cos, const float* sin, int rot, float eps,
                                                const TableAt& table_at) {
-  const RowRing<T, 2, kDepth> ring(smem);
+  RowRing<T, 2, kDepth> ring(smem);
   const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % (D / 16), rot);
   const int live = (int)min((long long)count, max(rows - first, 0ll));
-  RowWalk in, to;
+  RowWalk in;
   in.start(first, N, H, x_st);
-  to.start(first, N, H, out_st);
+  RowWalk to = in.in(out_st);
+  x += at.a;
+  out += at.a;
+  const int hop = at.b - at.a;
   int loaded = 0;
   auto fetch = [&] {
-    const bool ok = loaded < live && (!kPadding || table_at(in.b, in.n) >= 0);
-    const T* p = x + (ok ? in.at : 0);
-    ring.fetch(loaded, 0, p + at.a, ok);
-    ring.fetch(loaded, 1, p + at.b, ok);
+    if (loaded < live && (!kPadding || table_at(in.b, in.n) >= 0)) {
+      const T* p = x + in.at;
+      ring.fetch(0, p);
+      ring.fetch(1, p + hop);
+    } else if (loaded < count) {
+      ring.clear();
+    }
     copies_commit();
+    ring.step(ring.put);
     in.next(N, H, x_st);
     ++loaded;
   };
@@ -320,25 +337,27 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
   for (int i = 0; i < kDepth - 1; ++i) fetch();
   stage_weights<T>(weights, w_f32, D, w);
   __syncthreads();
-  Factors f;
+  LaneWeights lw;
+  lw.read(w, at);
+  float c[8], s[8];
   bool token = true;
   for (int i = 0; i < count; ++i) {
     fetch();
     if (token) {
       const bool ok = i < live;
       const long long row = ok ? max(table_at(to.b, to.n), 0ll) : 0;
-      float c[8], s[8];
       load_rotation<kNeighbours>(cos + row, sin + row, at, ok ? rot : 0, c, s);
-      fold_weights<kNeighbours>(w, at, c, s, f);
     }
     copies_wait<kDepth - 1>();
     Raw8<T> a, b;
-    ring.take(i, 0, a);
-    ring.take(i, 1, b);
-    norm_rope_lane<T, D, kNeighbours>(a, b, f, eps);  // (zeros stay zeros)
+    ring.take(0, a);
+    ring.take(1, b);
+    ring.step(ring.got);
+    norm_rope_lane<T, D, kNeighbours>(a, b, lw, c, s, eps);  // (zeros stay zeros)
     if (i < live) {
-      store8(a, out + to.at + at.a);
-      store8(b, out + to.at + at.b);
+      T* p = out + to.at;
+      store8(a, p);
+      store8(b, p + hop);
     }
     token = to.next(N, H, out_st);
   }

@@ -376,7 +376,7 @@ typedef struct {
 } fa_kv8_seqs;
 
 /* Writes new keys and values k, v ([B, T, H, d], fp16 or bf16, strides
- * multiples of 8) into the cache. The scale of a (page, head) is the least
+ * multiples of 8, T <= 2^19) into the cache. The scale of a (page, head) is the least
  * power of two s (of at least 2^-100) with amax <= 448 s, amax the largest
  * finite magnitude that the call brings to it, and not less than its former
  * scale where the page holds earlier tokens of the sequence; those are rounded
@@ -407,8 +407,9 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * row, gets O = 0 and lse = -inf. A NaN in k or v reaches only the rows that
  * attend to its token. max_seqlen: an upper bound of seq_lens (it sizes the
  * launch). `workspace`: 256-byte aligned, fa_kv8_attn_workspace_size(...) bytes
- * for the same sizes (0 for invalid ones); its contents on entry do not matter.
- * The same inputs give the same bits on every run. */
+ * for the same sizes; its contents on entry do not matter. The size is 0 where
+ * the call needs none (workspace may then be null) and for sizes that the call
+ * refuses. The same inputs give the same bits on every run. */
 size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,
                                   int causal, int window);
 int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, void* o, float* lse, int T, int Hq,

@@ -113,6 +113,11 @@ def test_cache_calls_reject_bad_arguments(lib, cache, seqs, call, code):
     assert set(_calls(lib, _cache(**cache), _seqs(**seqs), **call)) == {code}
 
 
+def test_append_limits_its_tokens(lib):
+    a, n, _ = _calls(lib, _cache(), _seqs(), T=(1 << 19) + 1)
+    assert (a, n) == (EUNSUP, EUNSUP)
+
+
 def test_null_structs_and_tensors(lib):
     st = _st(1, 2, 128)
     assert lib.fa_kv8_append(None, _seqs(), P, P, 1, st, st, BF16, None) == EINVAL
@@ -141,23 +146,30 @@ def test_attention_rejects_bad_arguments(lib):
     assert _attn(lib, alibi=P, asb=-1) == EINVAL
     assert _attn(lib, T=(1 << 24) + 1) == EUNSUP
     assert _attn(lib, T=1 << 20) == EUNSUP           # more row tiles than a grid's y extent
-    assert _attn(lib, ws=0) == EWS
-    assert _attn(lib, ws=P + 128) == EWS
-    need = fa.fa_kv8_attn_workspace_size(3, 1, 4, 2, 128, 64, 4, 256)
-    assert need >= 256 and need % 256 == 0
-    assert _attn(lib, ws_bytes=need - 1) == EWS
+    # sequences long enough for the split outputs to need a workspace
+    need = fa.fa_kv8_attn_workspace_size(3, 1, 4, 2, 128, 64, 400, 25600)
+    assert need > 0 and need % 256 == 0
+
+    def long(ws=P, ws_bytes=1 << 40):
+        st = _st(1, 4, 128)
+        return lib.fa_kv8_attn(_cache(), _seqs(max_pages=400, table_stride=400), P, P, P, 1, 4, 25600, st, st, BF16,
+                               0.1, 1, 0, None, 0, ws, ws_bytes, None)
+    assert long(ws=0) == EWS
+    assert long(ws=P + 128) == EWS
+    assert long(ws_bytes=need - 1) == EWS
 
 
 def test_attention_workspace_size(lib):
     size = fa.fa_kv8_attn_workspace_size
-    assert size(1, 1, 8, 8, 128, 64, 1, 64) >= 256
+    assert size(1, 1, 8, 8, 128, 64, 1, 64) == 0       # one block a sequence and head
     # split outputs and their log-sum-exp: a whole number of splits of (d + 1) floats a row
     big = size(1, 1, 32, 8, 128, 64, 2048, 131072)
-    assert big > 256 and abs(big / (32 * 129 * 4) - round(big / (32 * 129 * 4))) < 0.02
+    assert big > 0 and abs(big / (32 * 129 * 4) - round(big / (32 * 129 * 4))) < 0.02
     # a window bounds the keys, whatever the length
     assert size(1, 1, 32, 8, 128, 64, 2048, 131072, True, 256) < big
-    for bad in ((0, 1, 8, 8, 128, 64, 1, 64), (1, 1, 9, 8, 128, 64, 1, 64), (1, 1, 8, 8, 96, 64, 1, 64),
-                (1, 1, 8, 8, 128, 48, 1, 64), (1, 1, 8, 8, 128, 64, 0, 64), (1, 1, 8, 8, 128, 64, 1, 0)):
+    for bad in ((0, 1, 8, 8, 128, 64, 2048, 131072), (1, 1, 9, 8, 128, 64, 2048, 131072),
+                (1, 1, 8, 8, 96, 64, 2048, 131072), (1, 1, 8, 8, 128, 48, 2048, 131072),
+                (1, 1, 8, 8, 128, 64, 0, 64), (1, 1, 8, 8, 128, 64, 2048, 0)):
         assert size(*bad) == 0
 
 
