@@ -349,7 +349,7 @@ int side_stream_locked(SideStream** out) {
 
 extern "C" {
 
-int fa_version(void) { return 100; }
+int fa_version(void) { return 101; }
 
 const char* fa_strerror(int code) {
   switch (code) {

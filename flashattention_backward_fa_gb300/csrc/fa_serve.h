@@ -136,7 +136,7 @@ struct Kv8AttnParams {
 };
 
 struct Kv8AttnPlan {
-  int tiles;      // 8-row query tiles of a block (1, 2 or 4)
+  int tiles;      // 8-row query tiles of a block (1 or 2)
   int row_tiles;  // blocks that share the T * G rows of a key head
   int chunk, splits, cluster;
   size_t workspace;

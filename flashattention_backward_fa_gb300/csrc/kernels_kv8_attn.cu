@@ -11,7 +11,7 @@
 //   least 64 rows of M from shared memory; with one to a few dozen rows, V would
 //   have to be widened and P written to shared memory and read again, while here
 //   codes and weights go from registers to the instruction. Its rate is not what
-//   bounds the kernel up to 32 rows.
+//   bounds the kernel up to 16 rows.
 // * Any order of the head dimension serves S, and any order of the output
 //   columns serves O: a lane takes 16 consecutive codes of a key (K) or of a
 //   key's values (V) and uses them in place.
@@ -59,8 +59,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
-constexpr int kHopKeys = 128;   // splits are multiples of it (two tiles a warp)
 constexpr int kTile = 16;       // keys of an instruction
+constexpr int U = 2;            // tiles of a step
+constexpr int kHopKeys = kTile * U * kWarps;  // keys of a step of all warps; splits are multiples of it
 constexpr float kNoMax = -3.0e38f;  // m before any score
 constexpr float kHead = 7.f;    // m starts that far below 2^15: P of the first maximum is 2^7
 constexpr float kTop = 15.f;    // scores may pass m by this much (in log2)
@@ -176,7 +177,7 @@ __device__ __forceinline__ int split_keys(const Kv8AttnParams& p, const Range& r
 // Shared memory of the steps under way: a stage holds U tiles a warp, a tile 16
 // keys of K and of V in 128-byte lines (a key, or two with D = 64). Sixteen-byte
 // chunk x of line y lies at x ^ swizzle(y).
-template <int D, int U>
+template <int D>
 struct Ring {
   static constexpr int kLines = D / 8;             // lines of a tile of K, and of V
   static constexpr int kHalf = kLines * 128;       // bytes of K (then V) of a tile
@@ -204,9 +205,9 @@ __device__ __forceinline__ uint2 read_slot8(uint32_t a) {
 // What a lane keeps to start its copies: its place in page 0 of the head, its rows' stride (a
 // page's offsets fit into 31 bits, the entry point sees to it) and its slots. Lane l copies
 // chunk l % 8 of lines l / 8, l / 8 + 4, ... of a tile.
-template <int D, int U>
+template <int D>
 struct Fetch {
-  using G = Ring<D, U>;
+  using G = Ring<D>;
   const uint8_t* k;
   const uint8_t* v;
   const float* scale;  // lane 0: K's, lane 1: V's
@@ -261,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr bool kResidual = !kBf16;   // see the head of the file
   constexpr int NP = kBf16 ? 2 : 3;    // e4m3 pieces of a query
-  constexpr int U = NT == 4 ? 1 : 2;   // tiles of a step
   constexpr int KS = D / 16;           // row tiles of O^T
   constexpr int KQ = D / 32;           // instructions over the head dimension (S)
   constexpr int kRows = 8 * NT;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   __shared__ float w_m[kWarps][kRows], w_l[kWarps][kRows];
   __shared__ float block_lse[kRows];
   extern __shared__ __align__(128) unsigned char dyn[];
-  using G = Ring<D, U>;
+  using G = Ring<D>;
   static_assert(G::kScales >= (kWarps / 2) * kAcc * 32 * 4 && G::kScales >= kRows * D * 4, "merging reuses the ring");
   float (*merge)[kAcc][32] = reinterpret_cast<float (*)[kAcc][32]>(dyn);
   const uint32_t ring = smem_u32(dyn);
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   uint32_t bad_tiles = 0u;    // bit n U + u: tile u of stage n is in a page outside the cache
   bool bad = false;
   int into = 0;               // stage of the next fetch
-  const Fetch<D, U> copy(p.c, ring, h);
+  const Fetch<D> copy(p.c, ring, h);
   struct Pages {
     int id[U];
   };
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         top[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
-        if (U == 2) top[nt][e] = fmax3(top[nt][e], sc[U - 1][nt][e], sc[U - 1][nt][e + 2]);
+        top[nt][e] = fmax3(top[nt][e], sc[1][nt][e], sc[1][nt][e + 2]);
         over |= top[nt][e] > m[nt][e] + kTop;
       }
     if (__any_sync(0xffffffffu, over)) {
@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(const __grid_
 template <typename T, int D, int NT>
 cudaError_t launch_nt(const Kv8AttnParams& p, cudaStream_t st) {
   constexpr auto kKernel = kv8_attn_kernel<T, D, NT>;
-  constexpr int kBytes = Ring<D, NT == 4 ? 1 : 2>::kBytes;
+  constexpr int kBytes = Ring<D>::kBytes;
   cudaError_t e = allow_smem<kKernel>(kBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
@@ -886,8 +886,7 @@ cudaError_t launch_nt(const Kv8AttnParams& p, cudaStream_t st) {
 
 template <typename T, int D>
 cudaError_t launch_tiles(const Kv8AttnParams& p, int tiles, cudaStream_t st) {
-  if (tiles == 1) return launch_nt<T, D, 1>(p, st);
-  return tiles == 2 ? launch_nt<T, D, 2>(p, st) : launch_nt<T, D, 4>(p, st);
+  return tiles == 1 ? launch_nt<T, D, 1>(p, st) : launch_nt<T, D, 2>(p, st);
 }
 
 }  // namespace
@@ -903,7 +902,11 @@ Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int
   constexpr long long kSplitBlocks = 1, kSplitKeys = 4096;
   Kv8AttnPlan plan;
   const long long R = (long long)T * (Hq / H);
-  plan.tiles = R <= 8 ? 1 : R <= 16 ? 2 : 4;
+  // More than eight rows: 16 a block, further ones in blocks of their own that find the cache in
+  // L2. (Blocks of 32 rows spill registers and hold eight warps an SM: 153 us against 126 us for
+  // 16 sequences of 4096 tokens with 64 rows a key head; blocks of eight rows 90 us against 69 us
+  // for 8192 tokens with 16.)
+  plan.tiles = R <= 8 ? 1 : 2;
   plan.row_tiles = (int)((R + 8 * plan.tiles - 1) / (8 * plan.tiles));
   // keys that one block's rows can reach
   long long range = key_limit;

@@ -355,7 +355,8 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
  * The library cannot check device contents: tokens past max_pages pages are
  * ignored, a table entry outside [0, num_pages) makes its page's tokens be
  * skipped (not written, not attended to) and sets bit 4 of the device status
- * word. B <= 65535, H <= 1024, max_pages * page_size <= 2^30,
+ * word. The first of these calls on a device looks up that word's address: make
+ * it before any stream capture. B <= 65535, H <= 1024, max_pages * page_size <= 2^30,
  * strides.n * page_size <= 2^30.
  * ------------------------------------------------------------------------- */
 typedef struct {
@@ -387,7 +388,7 @@ int fa_kv8_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void
                   fa_strides k_strides, fa_strides v_strides, fa_dtype dtype, void* stream);
 
 /* fa_qk_norm_rope_fwd of new q ([B, T, Hq, d]) and k at their positions in the
- * sequences, then fa_kv8_append of the normed and rotated k (rounded to its
+ * sequences (clamped into the tables), then fa_kv8_append of the normed and rotated k (rounded to its
  * type) and of v, in one launch: bit for bit the two calls' results. q_out gets
  * zeros in padding rows and must not overlap q. */
 int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, const void* k,
@@ -409,7 +410,8 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * launch). `workspace`: 256-byte aligned, fa_kv8_attn_workspace_size(...) bytes
  * for the same sizes; its contents on entry do not matter. The size is 0 where
  * the call needs none (workspace may then be null) and for sizes that the call
- * refuses. The same inputs give the same bits on every run. */
+ * refuses; calls that overlap on the GPU need workspaces of their own. o must
+ * not overlap q. The same inputs give the same bits on every run. */
 size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,
                                   int causal, int window);
 int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, void* o, float* lse, int T, int Hq,

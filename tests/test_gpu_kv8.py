@@ -267,6 +267,8 @@ ATTN = [
     (1, 3, 4, 2, 64, 64, torch.float16, [9000], None, 0, True, True),
     (2, 2, 12, 1, 128, 128, torch.bfloat16, [7001, 13], [2, 1], 6000, True, False),
     (1, 9, 4, 1, 128, 128, torch.bfloat16, [6500], None, 0, False, False),
+    (1, 1, 33, 1, 64, 32, torch.bfloat16, [200], None, 0, True, False),     # rows in three blocks of 16
+    (40, 1, 16, 16, 64, 16, torch.float16, [(37 * b) % 300 for b in range(40)], None, 0, True, False),
 ]
 
 
@@ -511,6 +513,54 @@ def test_serving_loop_together_and_captured():
     for c, *_ in made:
         for a, b in zip(c, eager):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("length,heads", [(600, 2), (9000, 1)])
+def test_attention_captured_and_two_threads(length, heads):
+    """Split over a cluster and over a workspace: captured twice and replayed in turn with new queries, and
+    called by two host threads on two streams at once, every result equals the lone call's."""
+    import threading
+
+    g = torch.Generator().manual_seed(83)
+    pages, table_h = _layout(1, 64, length, g)
+    cache = _filled(pages, 64, heads, 128, g)
+    table, lens = _cu(table_h), _cu([length])
+    qs = [_values((1, 1, 4 * heads, 128), torch.bfloat16, g, 1.0).cuda() for _ in range(4)]
+    want = [fa.kv8_attention(q, cache, table, lens, length) for q in qs]
+    made = []
+    for _ in range(2):
+        x = torch.empty_like(qs[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = fa.kv8_attention(x, cache, table, lens, length)
+        made.append((x, graph, out))
+    for i in (0, 2):
+        for j, (x, graph, _) in enumerate(made):
+            x.copy_(qs[i + j])
+        for _, graph, _ in made:
+            graph.replay()
+        for j, (_, _, out) in enumerate(made):
+            assert torch.equal(out[0], want[i + j][0]) and torch.equal(out[1], want[i + j][1])
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def worker(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = [fa.kv8_attention(qs[i], cache, table, lens, length) for _ in range(20)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # surfaced below
+            errors.append(e)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
 def test_other_stream():

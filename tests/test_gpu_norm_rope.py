@@ -256,6 +256,81 @@ def test_side_stream_graph_and_two_graphs():
             assert torch.equal(a, b)
 
 
+def test_one_weight_alone():
+    """A weight on one side only: the other side is normed with ones and has no weight gradient."""
+    g = torch.Generator().manual_seed(41)
+    x = [_make((2, 9, h, 64), torch.float16, g) for h in (3, 2, 3, 2)]
+    w = (1 + 0.3 * torch.randn(64, generator=g)).half().cuda()
+    ones = torch.ones_like(w)
+    cos, sin = fa.rope_tables(9, 32)
+    for a, b in ((w, None), (None, w)):
+        full = (w, ones) if b is None else (ones, w)
+        got = fa.qk_norm_rope_forward(x[0], x[1], a, b, cos, sin)
+        for u, v in zip(got, fa.qk_norm_rope_forward(x[0], x[1], *full, cos, sin)):
+            assert torch.equal(u, v)
+        got = fa.qk_norm_rope_backward(*x, a, b, cos, sin)
+        want = fa.qk_norm_rope_backward(*x, *full, cos, sin)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert (got[2] is None) == (a is None) and (got[3] is None) == (b is None)
+        assert torch.equal(got[2] if b is None else got[3], want[2] if b is None else want[3])
+
+
+def test_autograd_captured_into_a_graph():
+    """Forward and backward of qk_norm_rope_func captured with leaves of their own: a replay on new values
+    gives the eager gradients."""
+    g = torch.Generator().manual_seed(43)
+    q, k = (_make((1, 30, h, 128), torch.bfloat16, g).requires_grad_() for h in (4, 2))
+    w = [(1 + 0.2 * torch.randn(128, generator=g)).to(torch.bfloat16).cuda().requires_grad_() for _ in range(2)]
+    dq, dk = _make((1, 30, 4, 128), torch.bfloat16, g), _make((1, 30, 2, 128), torch.bfloat16, g)
+    cos, sin = fa.rope_tables(30, 128)
+
+    def step():
+        out = fa.qk_norm_rope_func(q, k, *w, cos, sin)
+        return torch.autograd.grad(out, (q, k, *w), (dq, dk))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    with torch.no_grad():
+        q.copy_(_make(q.shape, q.dtype, g))
+        w[0].mul_(1.5)
+    graph.replay()
+    for a, b in zip(out, step()):
+        assert torch.equal(a, b)
+
+
+def test_many_rows_a_group():
+    """Enough rows that every row group takes several, with heads that do not divide the span: against the
+    same rows in small calls."""
+    g = torch.Generator().manual_seed(47)
+    B, N, Hq, Hk, d = 3, 2100, 23, 5, 64
+    q, k, dq, dk = (_make((B, N, h, d), torch.bfloat16, g) for h in (Hq, Hk, Hq, Hk))
+    w = [(1 + 0.2 * torch.randn(d, generator=g)).cuda() for _ in range(2)]
+    cos, sin = fa.rope_tables(N, d)
+    out = fa.qk_norm_rope_forward(q, k, *w, cos, sin)
+    grads = fa.qk_norm_rope_backward(q, k, dq, dk, *w, cos, sin)
+    sums = [torch.zeros(d, dtype=torch.float64, device="cuda") for _ in range(2)]
+    for b in range(B):
+        for n in range(0, N, 700):
+            at = (slice(b, b + 1), slice(n, n + 700))
+            pos = torch.arange(n, n + 700, dtype=torch.int32, device="cuda")
+            o = fa.qk_norm_rope_forward(q[at], k[at], *w, cos, sin, pos)
+            gr = fa.qk_norm_rope_backward(q[at], k[at], dq[at], dk[at], *w, cos, sin, pos)
+            for x, y in zip((*o, *gr[:2]), (*out, *grads[:2])):
+                assert torch.equal(x, y[at])
+            for s, y in zip(sums, gr[2:]):
+                s += y.double()
+    for s, y, x, dd in zip(sums, grads[2:], (q, k), (dq, dk)):
+        # two orders of the same fp32 sums of `rows` products of up to about 2 max|dout| max|xn|
+        rows = x[..., 0].numel()
+        assert torch.all((s - y.double()).abs() <= rows * EPS32 * (2 * dd.float().abs().amax() * 2 * rows ** 0.5).double())
+
+
 def test_large_offsets():
     """Rows past 2^31 elements of one buffer (a stride that reaches there) are read and written in place."""
     d, far = 128, (1 << 31) + 128 * 8
