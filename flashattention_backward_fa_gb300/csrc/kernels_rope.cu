@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
       g2 = f2_fma(wa[j], xa[j], f2_fma(wb[j], xb[j], g2));
     }
     const float ss = row_sum<G>(f2_sum(s2)), gx = row_sum<G>(f2_sum(g2));
-    const float rr = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+    const float rr = inv_sqrt(fmaf(ss, 1.f / D, p.eps));
     const float k1 = -gx * (1.f / D) * rr;  // -mean(g o xn)
     const uint64_t r2 = f2_pack(rr, rr), k2 = f2_pack(k1, k1);
 #pragma unroll
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
       ss = fmaf(xv[j], xv[j], ss);
     }
     ss = row_sum<32>(ss);
-    const float r = rsqrtf(ss / d + p.eps);
+    const float r = inv_sqrt(ss / d + p.eps);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int e = lane + 32 * j;

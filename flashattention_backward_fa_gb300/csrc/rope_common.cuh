@@ -183,6 +183,13 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
   return lo + hi;
 }
 
+// 1 / sqrt(x). rsqrtf is off by up to two units in the last place, which all values of a row
+// would share; a Newton step leaves about half a unit. (x past the fp32 range: 0.)
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return x < INFINITY ? fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r) : r;
+}
+
 // Forward of a lane's 16 values, in place; every lane of the warp calls it (shuffles).
 template <typename T, int D, bool kNeighbours>
 __device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const LaneWeights& w, const float (&c)[8],
@@ -197,7 +204,7 @@ __device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const L
     s1 = f2_fma(b[i], b[i], s1);
   }
   const float ss = row_sum<D / 16>(f2_sum(f2_add(s0, s1)));
-  const float r1 = rsqrtf(fmaf(ss, 1.f / D, eps));
+  const float r1 = inv_sqrt(fmaf(ss, 1.f / D, eps));
   const uint64_t r = f2_pack(r1, r1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
