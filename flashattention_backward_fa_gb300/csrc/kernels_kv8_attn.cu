@@ -897,7 +897,7 @@ cudaError_t launch_tiles(const Kv8AttnParams& p, int tiles, cudaStream_t st) {
 // that more blocks would gain less than the joining kernel's launch costs. What is
 // left, few sequences with long contexts, gets one resident set of blocks.
 Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window) {
-  constexpr long long kClusterKeys = 512, hop = kHopKeys;
+  constexpr long long kClusterKeys = 256, hop = kHopKeys;
   // with that many blocks in line already, splits of fewer keys cost more than they even out
   constexpr long long kSplitBlocks = 1, kSplitKeys = 4096;
   Kv8AttnPlan plan;
