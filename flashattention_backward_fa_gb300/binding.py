@@ -17,6 +17,7 @@ from functools import lru_cache
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libfa.so")
@@ -636,6 +637,7 @@ def _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, 
         raise ValueError(f"k must be [{B}, {N}, Hk, {d}] as q is {list(shape)}")
     Hk = kshape[2]
     rot, rows, wt, ptrs = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
+    eps, interleaved = float(eps), bool(interleaved)
     q_st, k_st = _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k")
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -691,6 +693,7 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, work
     if len(kshape) != 4 or kshape[0] != B or kshape[1] != N or kshape[3] != d:
         raise ValueError(f"k must be [{B}, {N}, Hk, {d}] as q is {list(shape)}")
     rot, rows, wt, (qw, kw, cp, sp) = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
+    eps, interleaved = float(eps), bool(interleaved)
     if workspace.get_device() != dev:
         raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
     _check((_lib or load_library()).fa_qk_norm_rope_bwd(
@@ -725,6 +728,7 @@ class _QkNormRopeFunc(torch.autograd.Function):
         return qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
         grads = qk_norm_rope_backward(q, k, _readable(dq_out), _readable(dk_out), q_weight, k_weight, cos, sin,
@@ -797,7 +801,7 @@ def _kv8_args(cache: Kv8Cache, B: int, d: int, dtype, dev: int, block_table, seq
 
 
 def kv8_append(cache: Kv8Cache, k, v, block_table, seq_lens, new_lens=None, stream=None):
-    """Write new keys and values [B, T, H, d] into the cache (fa_kv8_append).
+    """Write new keys and values [B, T, H, d] into the cache (fa_kv8_append). Not differentiable.
 
     ``seq_lens`` (int32 [B]) counts the new tokens already; they are the last ``new_lens``
     (int32 [B], None: T) of each sequence, further rows of k and v are padding. Token j of
@@ -817,6 +821,7 @@ def _norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block
     B, T, Hq, d = shape
     c, s = _kv8_args(cache, B, d, dtype, dev, block_table, seq_lens, new_lens)
     rot, rows, wt, ptrs = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
+    eps, interleaved = float(eps), bool(interleaved)
     kshape = (B, T, c.H, d)
     if q_out is None:
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -858,6 +863,7 @@ def _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, ne
     B, T, Hq, d = shape
     c, s = _kv8_args(cache, B, d, dtype, dev, block_table, seq_lens, new_lens)
     lib = _lib or load_library()
+    max_seqlen, causal, window = int(max_seqlen), bool(causal), int(window)
     q_st = _rows_layout(q, shape, dtype, dev, "q")
     if o is None:
         size = fa_kv8_attn_workspace_size(B, T, Hq, c.H, d, c.page_size, s.max_pages, max_seqlen, causal, window)
@@ -879,7 +885,7 @@ def _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, ne
     slopes, per_seq = (None, 0) if alibi_slopes is None else _alibi(alibi_slopes, B, Hq, q.device)
     _check(lib.fa_kv8_attn(
         c, s, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T, Hq, max_seqlen, q_st, o_st, _TORCH_TO_FA[dtype],
-        default_scale(d) if scale is None else scale, causal, window, slopes, per_seq, None if workspace is None else workspace.data_ptr(), size,
+        default_scale(d) if scale is None else float(scale), causal, window, slopes, per_seq, None if workspace is None else workspace.data_ptr(), size,
         _stream(stream)))
     return o, lse
 
@@ -898,6 +904,6 @@ def kv8_attention(q, cache: Kv8Cache, block_table, seq_lens, max_seqlen, new_len
 
     The queries belong to the last ``new_lens`` tokens of each sequence (as for kv8_append, which
     comes first: a token attends to itself through the cache). Hq must be a multiple of the
-    cache's heads. ``max_seqlen`` is an upper bound of ``seq_lens``."""
+    cache's heads. ``max_seqlen`` is an upper bound of ``seq_lens``. Not differentiable."""
     return _kv8_attn(q, cache, None, None, block_table, seq_lens, max_seqlen, None, new_lens, scale, causal, window,
                      alibi_slopes, None)

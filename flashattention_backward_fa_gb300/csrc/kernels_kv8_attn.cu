@@ -28,7 +28,7 @@
 //   differs (exact for powers of two).
 // * Running maximum and sum per row in fp32, kept per lane; the reference m
 //   moves only when a score exceeds it by 2^15 (P is then at most 2^15, inside
-//   f16), starting 2^7 above the first maximum, so warps agree on a new m a few
+//   f16), and is set so that the maximum's P is 2^7, so warps agree on a new m a few
 //   times a sequence and vote otherwise. P is rounded to f16 (2^-12 of itself);
 //   for f16 outputs, whose own rounding is no larger, its rounding residual is
 //   multiplied too.
@@ -63,8 +63,8 @@ constexpr int kTile = 16;       // keys of an instruction
 constexpr int U = 2;            // tiles of a step
 constexpr int kHopKeys = kTile * U * kWarps;  // keys of a step of all warps; splits are multiples of it
 constexpr float kNoMax = -3.0e38f;  // m before any score
-constexpr float kHead = 7.f;    // m starts that far below 2^15: P of the first maximum is 2^7
-constexpr float kTop = 15.f;    // scores may pass m by this much (in log2)
+constexpr float kHead = 7.f;    // a new m is set that far below the maximum, whose P is then 2^7
+constexpr float kTop = 15.f;    // scores may pass m by this much before it moves (log2): P stays within 2^15
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -120,7 +120,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // All threads of the cluster: shared-memory writes before it are seen behind it by the other blocks.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 // A word of block `rank`'s shared memory at the place of this block's p.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
@@ -687,11 +687,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       for (int w = 0; w < kWarps; ++w) sum += w_l[w][row] * ex2_approx(w_m[w][row] - top);
       if (pos[nt][e] < 0) sum = 0.f;  // a padding row (unmasked in whole steps)
       lse2[nt][e] = sum == 0.f ? -INFINITY : top + lg2_approx(sum);
-      const float f = sum == 0.f ? 0.f : ex2_approx(m[nt][e] - top) / sum * unit;
+      const bool none = sum == 0.f;  // (its sums may hold NaN all the same: a padding row's)
+      const float f = ex2_approx(m[nt][e] - top) / sum * unit;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
-        acc[i][nt][e] *= f;
-        acc[i][nt][e + 2] *= f;
+        acc[i][nt][e] = none ? 0.f : acc[i][nt][e] * f;
+        acc[i][nt][e + 2] = none ? 0.f : acc[i][nt][e + 2] * f;
       }
     }
 #pragma unroll

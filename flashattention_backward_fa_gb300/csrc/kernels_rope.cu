@@ -5,13 +5,15 @@
 //   dx = r (g - xn mean(g o xn));  dw = sum over rows of dy o xn
 // r is formed again from x, which the backward reads anyway, so nothing but
 // the inputs is kept between the two passes. dw: every lane keeps the sums of
-// its eight columns over its rows, a block adds its lanes' sums in a fixed
+// its 16 columns over its rows, a block adds its lanes' sums in a fixed
 // order into one row of the workspace, and a second kernel adds the blocks'
 // rows in a fixed order, so the gradients are the same bits on every run.
 //
-// Both are bound by memory: about 30 (forward) and 80 (backward) operations an
-// element against 4 and 6 bytes. The row is in registers between its one load
-// and its one store, and several rows' loads are in flight to shared memory.
+// Both are bound by memory: 4 bytes an element (forward) and 6 (backward, 16-bit
+// types), against about 13 and 18 thread instructions. A row is in registers
+// between its one load and its one store, and the next rows are on their way to
+// shared memory. Measured, bf16: forward 1x32x8192x128 (q and k) 46.9 us a call
+// (86% of the copy rate), backward 4x16x2048x128 35 us (86%).
 #include <algorithm>
 
 #include "fa_serve.h"

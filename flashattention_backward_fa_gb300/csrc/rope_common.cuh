@@ -347,12 +347,13 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
   LaneWeights lw;
   lw.read(w, at);
   float c[8], s[8];
-  bool token = true;
+  bool token = true, padding = false;
   for (int i = 0; i < count; ++i) {
     fetch();
     if (token) {
       const bool ok = i < live;
-      const long long row = ok ? max(table_at(to.b, to.n), 0ll) : 0;
+      const long long found = ok ? table_at(to.b, to.n) : 0, row = max(found, 0ll);
+      padding = found < 0;
       load_rotation<kNeighbours>(cos + row, sin + row, at, ok ? rot : 0, c, s);
     }
     copies_wait<kDepth - 1>();
@@ -360,7 +361,11 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
     ring.take(0, a);
     ring.take(1, b);
     ring.step(ring.got);
-    norm_rope_lane<T, D, kNeighbours>(a, b, lw, c, s, eps);  // (zeros stay zeros)
+    norm_rope_lane<T, D, kNeighbours>(a, b, lw, c, s, eps);
+    if (kPadding && padding) {
+      zero8(a);
+      zero8(b);
+    }
     if (i < live) {
       T* p = out + to.at;
       store8(a, p);

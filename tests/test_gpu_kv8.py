@@ -332,6 +332,42 @@ def test_nan_reaches_only_the_rows_that_attend_to_it():
     assert not bool(o[0, :4, 2:].isnan().any()) and bool(o[0, 4:, 2:].isnan().all())
 
 
+@pytest.mark.parametrize("length", [200, 3000, 9000])
+def test_nan_does_not_reach_padding_rows(length):
+    """Keys and values that hold NaN everywhere: padding rows are zeros and -inf all the same, whether one
+    block, a cluster or a second kernel writes them; rows with a token are NaN."""
+    g = torch.Generator().manual_seed(38)
+    pages, table = _layout(1, 64, length, g)
+    cache = _filled(pages, 64, 1, 64, g)
+    cache.k.view(torch.uint8).fill_(0x7F)
+    cache.v.view(torch.uint8).fill_(0xFF)
+    q = _values((1, 4, 2, 64), torch.bfloat16, g, 1.0).cuda()
+    o, lse = fa.kv8_attention(q, cache, _cu(table), _cu([length]), length, _cu([2]))
+    assert bool(o[0, :2].isnan().all()) and bool((o[0, 2:] == 0).all())
+    assert bool(lse[0, :, :2].isnan().all()) and bool((lse[0, :, 2:] == -math.inf).all())
+
+
+def test_nan_weights_do_not_reach_padding():
+    """A NaN weight makes the rows with a token NaN and nothing else: padding rows of q stay zeros, and the
+    values and the other pages of the cache are untouched."""
+    g = torch.Generator().manual_seed(39)
+    cache = fa.kv8_cache_alloc(4, 16, 2, 64)
+    want = ref.RefCache(cache)
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32)
+    q, k, v = (_values((2, 5, h, 64), torch.float16, g, 1.0) for h in (4, 2, 2))
+    w = torch.ones(64, dtype=torch.float16)
+    w[3] = float("nan")
+    cos, sin = fa.rope_tables(32, 32)
+    qo = fa.kv8_norm_rope_append(cache, q.cuda(), k.cuda(), v.cuda(), w.cuda(), w.cuda(), cos, sin, _cu(table),
+                                 _cu([5, 2]), _cu([5, 2]))
+    assert bool((qo[1, 2:] == 0).all()) and bool(qo[1, :2].isnan().any())
+    want.append(ref.f64(k), ref.f64(v), table, [5, 2], [5, 2])
+    assert torch.equal(cache.v.cpu().float().double(), want.codes[1])
+    held = cache.k.cpu().float()
+    assert bool(held[0, :5, :, 3].isnan().all()) and bool((held[1] == 0).all()) and bool((held[2, 2:] == 0).all())
+    assert bool(held[0, :5, :, 32:].isfinite().all())  # (past the rotated half a NaN weight touches its value alone)
+
+
 def test_bad_pages_are_not_attended_to():
     g = torch.Generator().manual_seed(41)
     cache = _filled(5, 16, 2, 64, g)
