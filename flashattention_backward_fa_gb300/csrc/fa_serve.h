@@ -111,7 +111,7 @@ struct Kv8AppendParams {
   const float* sin;
   int rot, max_pos, neighbours, w_f32;
   float eps;
-  int q_span;  // set by the launcher: rows of q a row group takes
+  int kv_heads, q_heads;  // set by the launcher: heads of k and v, and of q, that a block takes
 };
 cudaError_t launch_kv8_append(Kv8AppendParams& p, bool bf16, cudaStream_t st);
 

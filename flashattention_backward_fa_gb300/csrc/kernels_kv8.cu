@@ -9,18 +9,21 @@
 // that already holds tokens needs a larger scale, its codes are divided by a
 // power of two, which moves only those that reach e4m3's subnormals.
 //
-// One block takes one (page, head) of the new keys or of the new values: it
-// loads the page's new rows once, keeps them in registers while the block
-// agrees on their largest magnitude, and writes the codes. With norm and
-// rotation the keys' rows are normed, rotated and rounded to their type in
-// registers in between, so the cache holds the same codes as after the two
-// operators one by one; further blocks take q's rows. Nothing but the inputs
-// and the outputs moves through memory. Bound by memory (2 bytes in and 1 byte
-// out an element of k and v, 2 and 2 of q); for single tokens by the launch and
-// two dependent loads (length, then rows and page number side by side). Measured,
-// bf16: 1x32x8192x128 32.7 us (91% of the copy rate; eight blocks an SM at 32
-// registers, five at 40 took 35 us); 4x16x2048x128 with norm and rotation 45.2 us
-// (56%: at 80 registers three blocks an SM, bound by the instructions they issue).
+// A block takes one page's new keys or new values of one head: it loads the
+// page's new rows once, keeps them in registers while the block agrees on their
+// largest magnitude, and writes the codes. With norm and rotation a block takes
+// several heads one after the other (or several heads of q): a thread keeps its
+// tokens, so the tables' values and the weights are read once for all of them,
+// and the next head's rows are on their way to shared memory while one is
+// finished. The keys' rows are normed, rotated and rounded to their type in
+// registers, so the cache holds the same codes as after the two operators one by
+// one. Nothing but the inputs and the outputs moves through memory. Bound by
+// memory (2 bytes in and 1 byte out an element of k and v, 2 and 2 of q); for
+// single tokens by the launch and two dependent loads (length, then rows and page
+// number side by side). Measured, bf16: 1x32x8192x128 32.8 us (90% of the copy
+// rate; eight blocks an SM at 32 registers, five at 40 took 35 us); 4x16x2048x128
+// with norm and rotation 40.4 us (63%: two blocks an SM at 120 registers; one head
+// a block, with the tables read for each, took 45.2 us).
 #include <algorithm>
 
 #include "fa_serve.h"
@@ -30,8 +33,9 @@ namespace fa {
 
 namespace {
 
-constexpr int kQDepth = 3;    // rows of q a row group has on their way, and the one at hand
-constexpr int kQRows = 32;    // most rows of q that a row group takes
+constexpr int kAhead = 2;        // heads in a block with norm: one on its way, one at hand (three and four ran alike)
+constexpr int kMaxHeads = 8;     // most heads that a block of the form with norm takes
+constexpr int kBlocks = 152 * 2;  // blocks of k, of v and of q that are kept where there is work for them
 constexpr int kMinExp = -100;  // least scale exponent: blocks of zeros (or below 2^-91) get it
 
 // The scale's bits for a largest finite magnitude: 448 = 1.75 * 2^8.
@@ -127,150 +131,224 @@ __device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T)
   return n;
 }
 
-// Grid: x the heads of k, then of v, then (kNorm) blocks that share q's rows of
-// the page's tokens; y the page among those that T tokens reach; z the sequence.
-// kRows rows of a page a thread; blockDim.x * kRows * 16 values hold a page's new
-// rows. kNorm: 0 append alone, 1 / 2 norm and rotation with partners rot / 2
-// apart / neighbours.
+// Grid: x a group of heads of k, then of v, then (kNorm) of q; y the page among
+// those that T tokens reach; z the sequence. A block takes the heads of its group
+// one after the other: a thread keeps its tokens, so the tables' values and the
+// weights are loaded once for all heads, and the next head's rows are on their way
+// while one is finished. kRows rows of a page a thread; blockDim.x * kRows * 16
+// values hold a page's new rows. kNorm: 0 append alone, 1 / 2 norm and rotation
+// with partners rot / 2 apart / neighbours.
 template <typename T, int D, int kRows, int kNorm>
-__global__ void __launch_bounds__(256, kNorm == 0 ? (kRows == 4 ? 4 : 8) : (kRows == 4 ? 2 : 3)) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
-  extern __shared__ __align__(16) unsigned char ring[];  // (q's rows only)
+__global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows == 4 ? 4 : 8) : 1)
+    kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   constexpr int G = D / 16;
   constexpr bool kNeighbours = kNorm != 1;
-  __shared__ uint32_t red[8];
-  const Kv8Cache& c = p.c;
+  extern __shared__ __align__(16) unsigned char smem[];  // (kNorm) rows of the next heads
+  __shared__ uint32_t red[16];
   __shared__ __align__(16) float w[D];
+  const Kv8Cache& c = p.c;
   const int b = blockIdx.z;
   const NewTokens n = new_tokens(c, b, p.T);
-  if (kNorm != 0 && blockIdx.x >= 2u * c.H) {
-    // q: rows (t, head) of the tokens whose positions fall into the page (the positions of padding
-    // rows run on past the sequence, or before it), q_span a row group; padding rows become zeros
-    const long long lo = ((long long)(n.start >> c.page_shift) + blockIdx.y) << c.page_shift;
-    const int t_lo = (int)max(lo - n.start, 0ll);
-    const int t_hi = (int)min(lo + (1 << c.page_shift) - n.start, (long long)p.T);
-    if (t_lo >= t_hi) return;
-    fa_strides in = p.q_st, out = p.q_out_st;
-    const long long group = (long long)(blockIdx.x - 2u * c.H) * (blockDim.x / G) + threadIdx.x / G;
-    norm_rope_rows<T, D, kNeighbours, true, kQDepth>(
-        ring, static_cast<const T*>(p.q) + b * in.b + t_lo * in.n, static_cast<T*>(p.q_out) + b * out.b + t_lo * out.n,
-        in, out, (long long)(t_hi - t_lo) * p.Hq, t_hi - t_lo, p.Hq, group * p.q_span, p.q_span, p.q_w, p.w_f32, w,
-        p.cos, p.sin, p.rot, p.eps, [&](long long, int i) {
-          const int t = t_lo + i;
-          return t < n.count && n.start + t >= 0 ? (long long)min(n.start + t, max(p.max_pos - 1, 0)) * (p.rot >> 1)
-                                                 : -1ll;
-        });
-    return;
-  }
-  const bool is_v = blockIdx.x >= (unsigned)c.H;
-  const int h = blockIdx.x - (is_v ? c.H : 0);
+  const int kv_groups = kNorm == 0 ? c.H : (c.H + p.kv_heads - 1) / p.kv_heads;
+  const bool is_q = kNorm != 0 && blockIdx.x >= 2u * kv_groups;
+  const bool is_v = !is_q && blockIdx.x >= (unsigned)kv_groups;
+  int first, rows;  // the block's tokens: t = first .. first + rows - 1
   const int size = 1 << c.page_shift;
   const int pg = (max(n.start, 0) >> c.page_shift) + blockIdx.y;
-  if (pg >= c.max_pages) return;  // (and positions below stay in 31 bits)
-  const int t_lo = max(max(n.start, 0), pg << c.page_shift);
-  const int t_hi = min(n.len, (pg + 1) << c.page_shift);  // positions [t_lo, t_hi)
-  if (t_lo >= t_hi) return;
-  const int id = __ldg(c.table + b * c.table_stride + pg);  // (checked once the rows' loads are under way)
-  const int rows = t_hi - t_lo, slot0 = t_lo & (size - 1);
-  const fa_strides& st = is_v ? p.v_st : p.k_st;
-  const T* src = static_cast<const T*>(is_v ? p.v : p.k) + b * st.b + (long long)(t_lo - n.start) * st.n + h * st.h;
-  const int groups = blockDim.x / G, row0 = threadIdx.x / G;
+  if (is_q) {
+    // tokens whose positions fall into the page; those of padding rows run on past the sequence, or
+    // before it
+    const long long lo = ((long long)(n.start >> c.page_shift) + blockIdx.y) << c.page_shift;
+    first = (int)max(lo - n.start, 0ll);
+    rows = (int)min(lo + size - n.start, (long long)p.T) - first;
+  } else {
+    if (pg >= c.max_pages) return;  // (and positions below stay in 31 bits)
+    const int lo = max(max(n.start, 0), pg << c.page_shift);
+    first = lo - n.start;
+    rows = min(n.len, (pg + 1) << c.page_shift) - lo;
+  }
+  if (rows <= 0) return;
+  // (checked once the rows' loads are under way)
+  const int id = is_q ? 0 : __ldg(c.table + b * c.table_stride + pg);
+  // Row groups beside each other: rows of the page, or, with few tokens, q's further heads.
+  const int groups = blockDim.x / G;
+  int row0 = threadIdx.x / G, beside = 1, head = 0;
+  if (kRows == 1 && is_q && groups >= 2 * rows) {
+    beside = groups / rows;
+    head = row0 / rows;
+    row0 -= head * rows;
+    if (head >= beside) row0 = rows;  // (left over)
+  }
+  const int H = is_q ? p.Hq : c.H, span = kNorm == 0 ? 1 : is_q ? p.q_heads : p.kv_heads;
+  const int group = blockIdx.x - (is_q ? 2 * kv_groups : is_v ? kv_groups : 0);
+  const int heads = min(span, H - group * span);
+  head += group * span;
+  const int turns = kNorm == 0 ? 1 : (heads + beside - 1) / beside, head_end = group * span + heads;
+  const fa_strides& st = is_q ? p.q_st : is_v ? p.v_st : p.k_st;
   const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % G, p.rot);
-  Raw8<T> ra[kRows], rb[kRows];
+  const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) + b * st.b + (long long)(first + row0) * st.n +
+                 at.a;
+  const int hop = at.b - at.a;
+  bool live[kRows];  // the row has a token (q: padding rows have none)
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i * groups;
-    zero8(ra[i]);
-    zero8(rb[i]);
-    if (r < rows) {
-      load8(ra[i], src + r * st.n + at.a);
-      load8(rb[i], src + r * st.n + at.b);
-    }
+    const int r = row0 + i * groups, t = first + r;
+    live[i] = r < rows && (!is_q || (t < n.count && n.start + t >= 0));
   }
-  if (id < 0 || id >= c.num_pages) {
-    if (threadIdx.x == 0) atomicOr(c.status, kStatusBadPage);
-    return;
-  }
-  uint8_t* page = (is_v ? c.v : c.k) + id * c.sp + h * c.sh;
-  float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)id * c.H + h;
-  const float was = slot0 > 0 ? *scale_at : 0.f;  // a page without earlier tokens has no former scale
-  if (kNorm != 0 && !is_v) {
-    // every load of the rows, the weights and the tables is under way before the first is used
-    constexpr int kAhead = kRows < 2 ? kRows : 2;
-    float cc[kAhead][8], ss[kAhead][8];
-    auto rotation = [&](int i, float (&cr)[8], float (&sr)[8]) {
-      const int r = row0 + i * groups;
-      const long long row = r < rows ? (long long)min(t_lo + r, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
-      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, r < rows ? p.rot : 0, cr, sr);
-    };
+  const int head0 = head;
+  Raw8<T> ra[kRows], rb[kRows];
+  RowRing<T, 2 * kRows, kAhead> ring(smem);
+  int fetched = 0;
+  auto fetch = [&] {  // the rows of one more head, on their way to shared memory
+    const int h = head0 + fetched * beside;
+    if (fetched < turns) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) rotation(i, cc[i], ss[i]);
-    stage_weights<T>(p.k_w, p.w_f32, D, w);
-    __syncthreads();
-    LaneWeights lw;
-    lw.read(w, at);
+      for (int i = 0; i < kRows; ++i) {
+        if (live[i] && h < head_end) {
+          const T* x = src + (long long)(i * groups) * st.n + h * st.h;
+          ring.fetch(2 * i, x);
+          ring.fetch(2 * i + 1, x + hop);
+        } else {
+          ring.clear(2 * i);
+          ring.clear(2 * i + 1);
+        }
+      }
+    }
+    copies_commit();
+    ring.step(ring.put);
+    ++fetched;
+  };
+  if (kNorm != 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) fetch();
+  } else {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], lw, cc[i % kAhead], ss[i % kAhead], p.eps);
-      if (i + kAhead < kRows) rotation(i + kAhead, cc[i % kAhead], ss[i % kAhead]);
-    }
-  }
-  // (places without a row: zeros, also where a NaN among the weights has reached them)
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (kNorm != 0 && row0 + i * groups >= rows) {
       zero8(ra[i]);
       zero8(rb[i]);
-    }
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) m = max(m, max(amax_bits<T, false>(ra[i].q[0]), amax_bits<T, false>(rb[i].q[0])));
-  m = block_max(m, red);
-  const bool any = m >= inf_bits<T>();  // infinities or NaN among the new values
-  if (any) {
-    m = 0u;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) m = max(m, max(amax_bits<T, true>(ra[i].q[0]), amax_bits<T, true>(rb[i].q[0])));
-    m = block_max(m, red);
-  }
-  const float scale = fmaxf(scale_for(h16_bits_to_f32<std::is_same<T, __nv_bfloat16>::value>(m)), was);
-  const float inv = 1.f / scale;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i * groups;
-    if (r >= rows) continue;
-    uint8_t* to = page + (slot0 + r) * c.sn;
-    *reinterpret_cast<uint2*>(to + at.a) = any ? quantise8<T, true>(ra[i], inv) : quantise8<T, false>(ra[i], inv);
-    *reinterpret_cast<uint2*>(to + at.b) = any ? quantise8<T, true>(rb[i], inv) : quantise8<T, false>(rb[i], inv);
-  }
-  if (slot0 > 0 && scale != was) {  // earlier tokens to the larger scale, 16 codes a thread
-    const float ratio = was * inv;
-    for (int r = row0; r < slot0; r += groups) {
-      uint4* to = reinterpret_cast<uint4*>(page + r * c.sn) + threadIdx.x % G;
-      const uint4 q = *to;
-      uint32_t v[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[4];
-        unpack_e4m3x2(v[i] & 0xFFFFu, f[0], f[1]);
-        unpack_e4m3x2(v[i] >> 16, f[2], f[3]);
-        v[i] = e4m3x2(f[0] * ratio, f[1] * ratio) | (e4m3x2(f[2] * ratio, f[3] * ratio) << 16);
+      if (live[i]) {
+        const T* x = src + (long long)(i * groups) * st.n + head * st.h;
+        load8(ra[i], x);
+        load8(rb[i], x + hop);
       }
-      *to = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
-  // (every thread has read the former scale: block_max synchronised since)
-  if (threadIdx.x == 0) *scale_at = scale;
+  float cc[kRows][8], ss[kRows][8];
+  LaneWeights lw;
+  if (kNorm != 0 && !is_v) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long row =
+          live[i] ? (long long)min(n.start + first + row0 + i * groups, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
+      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, live[i] ? p.rot : 0, cc[i], ss[i]);
+    }
+    stage_weights<T>(is_q ? p.q_w : p.k_w, p.w_f32, D, w);
+    __syncthreads();
+    lw.read(w, at);
+  }
+  if (!is_q && (id < 0 || id >= c.num_pages)) {
+    if (threadIdx.x == 0) atomicOr(c.status, kStatusBadPage);
+    if (kNorm != 0) copies_wait<0>();
+    return;
+  }
+  const int slot0 = (n.start + first) & (size - 1);
+  for (int turn = 0; turn < turns; ++turn) {
+    if (kNorm != 0) {
+      fetch();
+      head = head0 + turn * beside;
+      copies_wait<kAhead - 1>();
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        ring.take(2 * i, ra[i]);
+        ring.take(2 * i + 1, rb[i]);
+      }
+      ring.step(ring.got);
+    }
+    if (kNorm != 0 && !is_v) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], lw, cc[i], ss[i], p.eps);
+        if (!live[i]) {  // zeros, also where a NaN among the weights has reached them
+          zero8(ra[i]);
+          zero8(rb[i]);
+        }
+      }
+    }
+    if (is_q) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = row0 + i * groups;
+        if (r >= rows || head >= head_end) continue;
+        T* to = static_cast<T*>(p.q_out) + b * p.q_out_st.b + (long long)(first + r) * p.q_out_st.n +
+                head * p.q_out_st.h + at.a;
+        store8(ra[i], to);
+        store8(rb[i], to + hop);
+      }
+      continue;
+    }
+    uint8_t* page = (is_v ? c.v : c.k) + id * c.sp + head * c.sh;
+    float* scale_at = (is_v ? c.v_scale : c.k_scale) + (long long)id * c.H + head;
+    const float was = slot0 > 0 ? *scale_at : 0.f;  // a page without earlier tokens has no former scale
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) m = max(m, max(amax_bits<T, false>(ra[i].q[0]), amax_bits<T, false>(rb[i].q[0])));
+    m = block_max(m, red);
+    const bool any = m >= inf_bits<T>();  // infinities or NaN among the new values
+    if (any) {
+      m = 0u;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) m = max(m, max(amax_bits<T, true>(ra[i].q[0]), amax_bits<T, true>(rb[i].q[0])));
+      m = block_max(m, red);
+    }
+    const float scale = fmaxf(scale_for(h16_bits_to_f32<std::is_same<T, __nv_bfloat16>::value>(m)), was);
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row0 + i * groups;
+      if (r >= rows) continue;
+      uint8_t* to = page + (slot0 + r) * c.sn + at.a;
+      *reinterpret_cast<uint2*>(to) = any ? quantise8<T, true>(ra[i], inv) : quantise8<T, false>(ra[i], inv);
+      *reinterpret_cast<uint2*>(to + hop) = any ? quantise8<T, true>(rb[i], inv) : quantise8<T, false>(rb[i], inv);
+    }
+    if (slot0 > 0 && scale != was) {  // earlier tokens to the larger scale, 16 codes a thread
+      const float ratio = was * inv;
+      for (int r = threadIdx.x / G; r < slot0; r += groups) {
+        uint4* to = reinterpret_cast<uint4*>(page + r * c.sn) + threadIdx.x % G;
+        const uint4 q = *to;
+        uint32_t v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[4];
+          unpack_e4m3x2(v[i] & 0xFFFFu, f[0], f[1]);
+          unpack_e4m3x2(v[i] >> 16, f[2], f[3]);
+          v[i] = e4m3x2(f[0] * ratio, f[1] * ratio) | (e4m3x2(f[2] * ratio, f[3] * ratio) << 16);
+        }
+        *to = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    // (every thread has read the former scale: block_max synchronised since)
+    if (threadIdx.x == 0) *scale_at = scale;
+  }
+  if (kNorm != 0) copies_wait<0>();
 }
 
 template <typename T, int D, int kRows>
 cudaError_t launch_rows(const Kv8AppendParams& p, dim3 grid, int threads, cudaStream_t st) {
-  const int ring = RowRing<T, 2, kQDepth>::bytes(threads);
-  if (p.q == nullptr)
-    kv8_append_kernel<T, D, kRows, 0><<<grid, threads, 0, st>>>(p);
-  else if (!p.neighbours)
-    kv8_append_kernel<T, D, kRows, 1><<<grid, threads, ring, st>>>(p);
-  else
-    kv8_append_kernel<T, D, kRows, 2><<<grid, threads, ring, st>>>(p);
+  if constexpr (kRows <= 2) {
+    if (p.q != nullptr) {
+      const int ring = RowRing<T, 2 * kRows, kAhead>::bytes(threads);
+      constexpr int most = RowRing<T, 2 * kRows, kAhead>::bytes(512);
+      const cudaError_t e = p.neighbours ? allow_smem<kv8_append_kernel<T, D, kRows, 2>>(most)
+                                         : allow_smem<kv8_append_kernel<T, D, kRows, 1>>(most);
+      if (e != cudaSuccess) return e;
+      if (!p.neighbours)
+        kv8_append_kernel<T, D, kRows, 1><<<grid, threads, ring, st>>>(p);
+      else
+        kv8_append_kernel<T, D, kRows, 2><<<grid, threads, ring, st>>>(p);
+      return cudaGetLastError();
+    }
+  }
+  kv8_append_kernel<T, D, kRows, 0><<<grid, threads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -278,20 +356,26 @@ template <typename T, int D>
 cudaError_t launch_d(Kv8AppendParams& p, cudaStream_t st) {
   constexpr int G = D / 16;
   const int rows = std::min(1 << p.c.page_shift, p.T);  // most new rows of one page
-  // up to 256 threads, then more rows a thread; at least two warps, so that a
-  // single token still shares out the rescaling of its page
+  // up to 256 threads, then more rows a thread (with norm, whose rows keep their tables' values
+  // in registers, two at most); at least two warps, so that a single token still shares out the
+  // rescaling of its page
   const int lanes = rows * G;
-  const int per = lanes <= 256 ? 1 : lanes <= 512 ? 2 : 4;
+  const int per = lanes <= 256 ? 1 : lanes <= 512 || p.q ? 2 : 4;
   const int threads = std::max(64, ((lanes + per - 1) / per + 31) / 32 * 32);
-  int q_blocks = 0;
+  int x = 2 * p.c.H;
   if (p.q) {
-    // q's rows of a page's tokens: kQRows a row group where there are that many, so that a token's
-    // factors serve several heads, and one where that leaves the GPU empty
-    const long long q_rows = (long long)rows * p.Hq, groups = threads / G;
-    p.q_span = (int)std::max<long long>(1, std::min<long long>(kQRows, q_rows * p.pages * p.B / (groups * 152 * 4)));
-    q_blocks = (int)((q_rows + groups * p.q_span - 1) / (groups * p.q_span));
+    // Heads a block: up to kMaxHeads where kBlocks blocks remain, else one (q, with few tokens: one a
+    // row group).
+    const long long places = (long long)p.pages * p.B;
+    const auto share = [&](int heads, int least) {
+      const long long most = places * heads / kBlocks;
+      return std::min(heads, (int)std::max<long long>(least, std::min<long long>(kMaxHeads, most)));
+    };
+    p.kv_heads = share(p.c.H, 1);
+    p.q_heads = share(p.Hq, per == 1 ? std::max(1, threads / G / rows) : 1);
+    x = 2 * ((p.c.H + p.kv_heads - 1) / p.kv_heads) + (p.Hq + p.q_heads - 1) / p.q_heads;
   }
-  const dim3 grid(2 * p.c.H + q_blocks, p.pages, p.B);
+  const dim3 grid(x, p.pages, p.B);
   if (per == 1) return launch_rows<T, D, 1>(p, grid, threads, st);
   return per == 2 ? launch_rows<T, D, 2>(p, grid, threads, st) : launch_rows<T, D, 4>(p, grid, threads, st);
 }

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const __
   const RopeSide& sd = is_k ? p.k : p.q;
   const long long group =
       (long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * (kRopeThreads / (D / 16)) + threadIdx.x / (D / 16);
-  norm_rope_rows<T, D, kNeighbours, false, kFwdDepth>(
+  norm_rope_rows<T, D, kNeighbours, kFwdDepth>(
       ring, static_cast<const T*>(sd.x), static_cast<T*>(sd.out), sd.x_st, sd.out_st, (long long)p.B * p.N * sd.H, p.N,
       sd.H, group * sd.span, sd.span, sd.w, p.w_f32, w, p.cos, p.sin, p.rot, p.eps,
       [&](long long b, int n) { return p.rot ? table_row(p, b, n) : 0ll; });
@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
       ring.fetch(2, g);
       ring.fetch(3, g + hop);
     } else if (loaded < sd.span) {
-      ring.clear();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ring.clear(i);
     }
     copies_commit();
     ring.step(ring.put);

@@ -285,9 +285,10 @@ struct RowRing {
     for (int i = 0; i < Raw8<T>::kQuads; ++i)
       copy16_async(put + (chunk * Raw8<T>::kQuads + i) * apart, reinterpret_cast<const uint4*>(p) + i);
   }
-  __device__ __forceinline__ void clear() const {
+  __device__ __forceinline__ void clear(int chunk) const {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) st_shared_v4(put + i * apart, 0u, 0u, 0u, 0u);
+    for (int i = 0; i < Raw8<T>::kQuads; ++i)
+      st_shared_v4(put + (chunk * Raw8<T>::kQuads + i) * apart, 0u, 0u, 0u, 0u);
   }
   __device__ __forceinline__ void take(int chunk, Raw8<T>& v) const {
 #pragma unroll
@@ -308,10 +309,9 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 // Rows [first, first + count) of one tensor by one row group (D / 16 lanes; the
 // groups of a warp call it together, each with its own rows and all with the same
 // count). kDepth - 1 rows are on their way while a row is computed.
-// table_at(b, n): offset of the token's table rows, or -1 for a padding row, which
-// becomes zeros (kPadding) and is not read. The weights are staged into w (a block-wide step)
-// once the first copies are under way.
-template <typename T, int D, bool kNeighbours, bool kPadding, int kDepth, typename TableAt>
+// table_at(b, n): offset of the token's table rows. The weights are staged into w (a
+// block-wide step) once the first copies are under way.
+template <typename T, int D, bool kNeighbours, int kDepth, typename TableAt>
 __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, const fa_strides& x_st,
                                                const fa_strides& out_st, long long rows, int N, int H, long long first,
                                                int count, const void* weights, bool w_f32, float* w,
@@ -328,12 +328,13 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
   const int hop = at.b - at.a;
   int loaded = 0;
   auto fetch = [&] {
-    if (loaded < live && (!kPadding || table_at(in.b, in.n) >= 0)) {
+    if (loaded < live) {
       const T* p = x + in.at;
       ring.fetch(0, p);
       ring.fetch(1, p + hop);
     } else if (loaded < count) {
-      ring.clear();
+      ring.clear(0);
+      ring.clear(1);
     }
     copies_commit();
     ring.step(ring.put);
@@ -347,13 +348,12 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
   LaneWeights lw;
   lw.read(w, at);
   float c[8], s[8];
-  bool token = true, padding = false;
+  bool token = true;
   for (int i = 0; i < count; ++i) {
     fetch();
     if (token) {
       const bool ok = i < live;
-      const long long found = ok ? table_at(to.b, to.n) : 0, row = max(found, 0ll);
-      padding = found < 0;
+      const long long row = ok ? table_at(to.b, to.n) : 0;
       load_rotation<kNeighbours>(cos + row, sin + row, at, ok ? rot : 0, c, s);
     }
     copies_wait<kDepth - 1>();
@@ -362,10 +362,6 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
     ring.take(1, b);
     ring.step(ring.got);
     norm_rope_lane<T, D, kNeighbours>(a, b, lw, c, s, eps);
-    if (kPadding && padding) {
-      zero8(a);
-      zero8(b);
-    }
     if (i < live) {
       T* p = out + to.at;
       store8(a, p);

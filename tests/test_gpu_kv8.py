@@ -170,6 +170,11 @@ NRA = [
     (2, 50, 4, 4, 128, 96, False, 128, torch.float16, "own", [100, 0], None),
     (1, 130, 2, 1, 128, 128, True, 32, torch.bfloat16, "own", [3], None),
     (1, 9, 2, 2, 128, 0, False, 32, torch.bfloat16, "own", [3], None),
+    (1, 150, 3, 2, 128, 64, False, 128, torch.bfloat16, "own", [5], None),       # the largest page, 512 threads
+    (2, 600, 27, 9, 64, 64, True, 16, torch.float16, "f32", [3, 40], [600, 333]),  # several heads a block, a short last group
+    (2, 600, 27, 9, 128, 128, False, 64, torch.bfloat16, "own", [3, 40], [600, 333]),
+    (70, 1, 20, 10, 128, 128, False, 16, torch.bfloat16, "own", list(range(70)), None),
+    (3, 5, 13, 1, 64, 32, False, 32, torch.float16, None, [0, 30, 31], [5, 0, 4]),  # q's heads beside each other
 ]
 
 
