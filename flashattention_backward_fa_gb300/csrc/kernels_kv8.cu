@@ -22,7 +22,7 @@
 // single tokens by the launch and two dependent loads (length, then rows and page
 // number side by side). Measured, bf16: 1x32x8192x128 32.8 us (90% of the copy
 // rate; eight blocks an SM at 32 registers, five at 40 took 35 us); 4x16x2048x128
-// with norm and rotation 40.4 us (63%: two blocks an SM at 120 registers; one head
+// with norm and rotation 40.2 us (63%: two blocks an SM at 120 registers; one head
 // a block, with the tables read for each, took 45.2 us).
 #include <algorithm>
 
