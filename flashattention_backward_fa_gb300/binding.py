@@ -683,41 +683,55 @@ def _weight_grad(g, w, dev: int, name: str):
     return g.data_ptr()
 
 
-def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, q_weight=None, k_weight=None,
-                        cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, stream=None):
-    """Its backward through the C ABI: fills dq, dk and, where there are weights, dq_weight and dk_weight.
-    ``workspace`` is a uint8 CUDA tensor of fa_qk_norm_rope_bwd_workspace_size(d) bytes."""
+def _norm_rope_bwd(q, k, dq_out, dk_out, outs, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream):
+    """``outs``: (dq, dk, dq_weight, dk_weight, workspace) of the caller, or None to allocate them."""
     shape, dtype, dev = _new_tensor(q, "q")
     B, N, Hq, d = shape
     kshape = k.shape
     if len(kshape) != 4 or kshape[0] != B or kshape[1] != N or kshape[3] != d:
         raise ValueError(f"k must be [{B}, {N}, Hk, {d}] as q is {list(shape)}")
+    Hk = kshape[2]
     rot, rows, wt, (qw, kw, cp, sp) = _rope_args(d, dtype, dev, q_weight, k_weight, cos, sin)
-    eps, interleaved = float(eps), bool(interleaved)
-    if workspace.get_device() != dev:
-        raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
+    q_st, k_st = _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k")
+    gq_st = _rows_layout(dq_out, shape, dtype, dev, "dq_out")
+    gk_st = _rows_layout(dk_out, kshape, dtype, dev, "dk_out")
+    if outs is None:
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+        dqw = None if q_weight is None else torch.empty_like(q_weight)
+        dkw = None if k_weight is None else torch.empty_like(k_weight)
+        size = fa_qk_norm_rope_bwd_workspace_size(d)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        dq_st, dk_st = _strides(N * Hq * d, Hq * d, d), _strides(N * Hk * d, Hk * d, d)
+        dqw_ptr, dkw_ptr = (None if dqw is None else dqw.data_ptr()), (None if dkw is None else dkw.data_ptr())
+    else:
+        dq, dk, dqw, dkw, workspace = outs
+        dq_st, dk_st = _rows_layout(dq, shape, dtype, dev, "dq"), _rows_layout(dk, kshape, dtype, dev, "dk")
+        dqw_ptr = _weight_grad(dqw, q_weight, dev, "dq_weight")
+        dkw_ptr = _weight_grad(dkw, k_weight, dev, "dk_weight")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
+        size = workspace.numel() * workspace.element_size()
     _check((_lib or load_library()).fa_qk_norm_rope_bwd(
-        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), qw, kw,
-        _weight_grad(dq_weight, q_weight, dev, "dq_weight"), _weight_grad(dk_weight, k_weight, dev, "dk_weight"), cp,
-        sp, *_positions(positions, B, N, dev), B, N, Hq, kshape[2], d, rot, interleaved, rows,
-        _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k"),
-        _rows_layout(dq_out, shape, dtype, dev, "dq_out"), _rows_layout(dk_out, kshape, dtype, dev, "dk_out"),
-        _rows_layout(dq, shape, dtype, dev, "dq"), _rows_layout(dk, kshape, dtype, dev, "dk"), _TORCH_TO_FA[dtype], wt,
-        eps, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+        q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), qw, kw, dqw_ptr,
+        dkw_ptr, cp, sp, *_positions(positions, B, N, dev), B, N, Hq, Hk, d, rot, bool(interleaved), rows, q_st, k_st,
+        gq_st, gk_st, dq_st, dk_st, _TORCH_TO_FA[dtype], wt, float(eps), workspace.data_ptr(), size, _stream(stream)))
+    return dq, dk, dqw, dkw
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, q_weight=None, k_weight=None,
+                        cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """Its backward through the C ABI: fills dq, dk and, where there are weights, dq_weight and dk_weight.
+    ``workspace`` is a uint8 CUDA tensor of fa_qk_norm_rope_bwd_workspace_size(d) bytes."""
+    _norm_rope_bwd(q, k, dq_out, dk_out, (dq, dk, dq_weight, dk_weight, workspace), q_weight, k_weight, cos, sin,
+                   positions, eps, interleaved, stream)
 
 
 def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
                           eps=1e-6, interleaved=False):
     """Allocate the gradients and the workspace and run the backward; returns
     (dq, dk, dq_weight, dk_weight), contiguous, None for a weight that is None."""
-    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
-    dk = torch.empty_like(k, memory_format=torch.contiguous_format)
-    dqw = None if q_weight is None else torch.empty_like(q_weight)
-    dkw = None if k_weight is None else torch.empty_like(k_weight)
-    ws = torch.empty(fa_qk_norm_rope_bwd_workspace_size(q.shape[-1]), dtype=torch.uint8, device=q.device)
-    fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dqw, dkw, ws, q_weight, k_weight, cos, sin, positions, eps,
-                        interleaved)
-    return dq, dk, dqw, dkw
+    return _norm_rope_bwd(q, k, dq_out, dk_out, None, q_weight, k_weight, cos, sin, positions, eps, interleaved, None)
 
 
 class _QkNormRopeFunc(torch.autograd.Function):

@@ -24,19 +24,28 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
-// Launches a kernel that may begin while the one before it in the stream ends (it waits for that
-// one's outputs itself, with griddepcontrol.wait).
+// Launches a kernel whose blocks may take their places while the kernel before it in the stream
+// ends (sooner where that one calls let_next_begin). Each of them waits for that kernel's end
+// (wait_for_previous) before it touches memory; towards other kernels this is an ordinary launch.
+// Between two of these kernels it saves 1 to 3 us: bf16 norm and rotation 1x32x8192x128 46.9 ->
+// 44.2 us, append 32.8 -> 30.6 us, 100 tokens of attention 6.2 -> 5.5 us. cluster > 1: blocks of a
+// cluster along x.
 template <typename Params>
-cudaError_t launch_behind(void (*kernel)(Params), dim3 grid, int threads, const Params& p, cudaStream_t st) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_chained(void (*kernel)(Params), dim3 grid, int threads, int smem, int cluster, const Params& p,
+                           cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -20,10 +20,10 @@
 // one. Nothing but the inputs and the outputs moves through memory. Bound by
 // memory (2 bytes in and 1 byte out an element of k and v, 2 and 2 of q); for
 // single tokens by the launch and two dependent loads (length, then rows and page
-// number side by side). Measured, bf16: 1x32x8192x128 32.8 us (90% of the copy
-// rate; eight blocks an SM at 32 registers, five at 40 took 35 us); 4x16x2048x128
-// with norm and rotation 40.2 us (63%: two blocks an SM at 120 registers; one head
-// a block, with the tables read for each, took 45.2 us).
+// number side by side). Measured, bf16: 1x32x8192x128 30.6 us (97% of the copy
+// rate; eight blocks an SM at 32 registers, five at 40 took 2 us more); 4x16x2048x128
+// with norm and rotation 38.0 us (67%: two blocks an SM at 120 registers; one head
+// a block, with the tables read for each, took 5 us more).
 #include <algorithm>
 
 #include "fa_serve.h"
@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
   extern __shared__ __align__(16) unsigned char smem[];  // (kNorm) rows of the next heads
   __shared__ uint32_t red[16];
   __shared__ __align__(16) float w[D];
+  let_next_begin();
+  wait_for_previous();
   const Kv8Cache& c = p.c;
   const int b = blockIdx.z;
   const NewTokens n = new_tokens(c, b, p.T);
@@ -341,15 +343,11 @@ cudaError_t launch_rows(const Kv8AppendParams& p, dim3 grid, int threads, cudaSt
       const cudaError_t e = p.neighbours ? allow_smem<kv8_append_kernel<T, D, kRows, 2>>(most)
                                          : allow_smem<kv8_append_kernel<T, D, kRows, 1>>(most);
       if (e != cudaSuccess) return e;
-      if (!p.neighbours)
-        kv8_append_kernel<T, D, kRows, 1><<<grid, threads, ring, st>>>(p);
-      else
-        kv8_append_kernel<T, D, kRows, 2><<<grid, threads, ring, st>>>(p);
-      return cudaGetLastError();
+      return p.neighbours ? launch_chained(kv8_append_kernel<T, D, kRows, 2>, grid, threads, ring, 1, p, st)
+                          : launch_chained(kv8_append_kernel<T, D, kRows, 1>, grid, threads, ring, 1, p, st);
     }
   }
-  kv8_append_kernel<T, D, kRows, 0><<<grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_chained(kv8_append_kernel<T, D, kRows, 0>, grid, threads, 0, 1, p, st);
 }
 
 template <typename T, int D>

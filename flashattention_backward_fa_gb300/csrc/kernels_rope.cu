@@ -12,8 +12,8 @@
 // Both are bound by memory: 4 bytes an element (forward) and 6 (backward, 16-bit
 // types), against about 13 and 18 thread instructions. A row is in registers
 // between its one load and its one store, and the next rows are on their way to
-// shared memory. Measured, bf16: forward 1x32x8192x128 (q and k) 46.9 us a call
-// (86% of the copy rate), backward 4x16x2048x128 35 us (86%).
+// shared memory. Measured, bf16: forward 1x32x8192x128 (q and k) 44.2 us a call
+// (91% of the copy rate), backward 4x16x2048x128 35 us (86%).
 #include <algorithm>
 
 #include "fa_serve.h"
@@ -39,6 +39,8 @@ template <typename T, int D, bool kNeighbours>
 __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) float w[D];
+  let_next_begin();
+  wait_for_previous();
   const bool is_k = blockIdx.x >= (unsigned)p.q_blocks;
   const RopeSide& sd = is_k ? p.k : p.q;
   const long long group =
@@ -56,6 +58,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
   constexpr int G = D / 16, kGroups = kRopeThreads / G;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float w[D];
+  let_next_begin();
+  wait_for_previous();
   RowRing<T, 4, kBwdDepth> ring(smem);
   const int group = threadIdx.x / G;
   const bool is_k = blockIdx.x >= (unsigned)p.q_blocks;
@@ -165,7 +169,6 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
     }
     token = wo.next(p.N, sd.H, sd.dx_st);
   }
-  let_next_begin();
   if (sd.w == nullptr) return;
   // the block's sums take the ring's place once every copy into it has landed (none is pending
   // beyond the rows above: the last fetches were of nothing but are waited for all the same)
@@ -194,12 +197,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
 template <typename T>
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float sums[32][33];
+  let_next_begin();
+  wait_for_previous();
   const bool is_k = blockIdx.x != 0;
   const RopeSide& sd = is_k ? p.k : p.q;
   if (sd.w == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.y * 32 + lane;
   const int lo = is_k ? p.q_blocks : 0, hi = is_k ? p.blocks : p.q_blocks;
-  wait_for_previous();
   float t = 0.f;
   if (e < p.d) {
 #pragma unroll 12
@@ -224,6 +228,8 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const __grid_constant
 template <bool kBackward>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float buf[8][128];
+  let_next_begin();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = p.d, h = p.rot >> 1;
   const bool is_k = blockIdx.x >= (unsigned)p.q_blocks;
   const RopeSide& sd = is_k ? p.k : p.q;
@@ -324,8 +330,7 @@ template <auto kKernel>
 cudaError_t launch_ring(const RopeParams& p, int bytes, cudaStream_t st) {
   const cudaError_t e = allow_smem<kKernel>(bytes);
   if (e != cudaSuccess) return e;
-  kKernel<<<p.blocks, kRopeThreads, bytes, st>>>(p);
-  return cudaGetLastError();
+  return launch_chained(kKernel, p.blocks, kRopeThreads, bytes, 1, p, st);
 }
 
 template <typename T>
@@ -378,8 +383,7 @@ int rope_bwd_max_blocks() { return kBwdBlocks + 2; }
 cudaError_t launch_norm_rope_fwd(RopeParams& p, int dtype, cudaStream_t st) {
   if (!vector_rows(p, dtype, false)) {
     share_rows(p, 8, 152 * 8, 152 * 8);
-    norm_rope_any_f32_kernel<false><<<p.blocks, kRopeThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_chained(norm_rope_any_f32_kernel<false>, p.blocks, kRopeThreads, 0, 1, p, st);
   }
   share_rows(p, kRopeThreads / (p.d / 16), kFwdBlocks / 4, kFwdBlocks);
   if (dtype == FA_F32) return launch_fwd<float>(p, st);
@@ -391,8 +395,7 @@ cudaError_t launch_norm_rope_bwd(RopeParams& p, int dtype, cudaStream_t st) {
   cudaError_t e;
   if (!vec) {
     share_rows(p, 8, kBwdBlocks, kBwdBlocks);
-    norm_rope_any_f32_kernel<true><<<p.blocks, kRopeThreads, 0, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_chained(norm_rope_any_f32_kernel<true>, p.blocks, kRopeThreads, 0, 1, p, st);
   } else {
     share_rows(p, kRopeThreads / (p.d / 16), kBwdBlocks, kBwdBlocks);
     if (dtype == FA_F32)
@@ -402,9 +405,9 @@ cudaError_t launch_norm_rope_bwd(RopeParams& p, int dtype, cudaStream_t st) {
   }
   if (e != cudaSuccess || (p.q.w == nullptr && p.k.w == nullptr)) return e;
   const dim3 grid(2, (p.d + 31) / 32);
-  if (dtype == FA_F32 || p.w_f32) return launch_behind(weight_grad_kernel<float>, grid, 1024, p, st);
-  return dtype == FA_BF16 ? launch_behind(weight_grad_kernel<__nv_bfloat16>, grid, 1024, p, st)
-                          : launch_behind(weight_grad_kernel<__half>, grid, 1024, p, st);
+  if (dtype == FA_F32 || p.w_f32) return launch_chained(weight_grad_kernel<float>, grid, 1024, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(weight_grad_kernel<__nv_bfloat16>, grid, 1024, 0, 1, p, st)
+                          : launch_chained(weight_grad_kernel<__half>, grid, 1024, 0, 1, p, st);
 }
 
 }  // namespace fa

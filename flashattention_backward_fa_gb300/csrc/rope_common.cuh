@@ -25,6 +25,12 @@
 
 namespace fa {
 
+// Waits until the kernel before this one in the stream has ended and its writes are there (see
+// launch_chained). Every block calls it before it touches memory.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the blocks of the next kernel take their places once all of this one's have called it or ended.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Eight consecutive values of a row as they lie in memory.
 template <typename T>
 struct Raw8 {
@@ -299,12 +305,6 @@ struct RowRing {
                    : "memory");
   }
 };
-
-// The launch that follows a kernel in the stream may begin (its own prologue) while the
-// kernel ends; what reads the kernel's outputs waits for all of it first. Both are no-ops
-// in launches without the attribute.
-__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Rows [first, first + count) of one tensor by one row group (D / 16 lanes; the
 // groups of a warp call it together, each with its own rows and all with the same
