@@ -814,27 +814,43 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv8_join_kernel(const __grid_
   const Range kr = key_range(p, b, rt * 8 * NT, min((rt + 1) * 8 * NT, R));
   const int n = (kr.hi - kr.lo + p.chunk - 1) / p.chunk;
   const long long at = (((long long)b * p.c.H + h) * R + row) * p.splits;
-  // every warp on its own: its splits' maximum, weights and sums, joined at the end
+  // every warp on its own, eight of its splits at a time with all their loads under way at once
   float top = -INFINITY, acc[kPer], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int s = warp + kJoinWarps * lane; s < n; s += kJoinWarps * 32) top = fmaxf(top, __ldcg(p.part_lse + at + s));
+  for (int base = warp; base < n; base += 8 * kJoinWarps) {
+    float x[8], v[8][kPer];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll 8
-  for (int s = warp; s < n; s += kJoinWarps) {
-    const float x = __ldcg(p.part_lse + at + s);
-    const float w = x == -INFINITY ? 0.f : ex2_approx(x - top);  // (a split without a key for this row)
-    sum += w;
-    const float* o = p.part_o + (at + s) * D + kPer * lane;
-    if (kPer == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
-      acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-      acc[kPer - 2] = fmaf(w, v.z, acc[kPer - 2]), acc[kPer - 1] = fmaf(w, v.w, acc[kPer - 1]);
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
-      acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+    for (int i = 0; i < 8; ++i) {
+      const int s = base + i * kJoinWarps;
+      x[i] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[i][e] = 0.f;
+      if (s < n) {
+        x[i] = __ldcg(p.part_lse + at + s);
+        const float* o = p.part_o + (at + s) * D + kPer * lane;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 two = __ldcg(reinterpret_cast<const float2*>(o + e));
+          v[i][e] = two.x, v[i][e + 1] = two.y;
+        }
+      }
     }
+    float t = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = fmaxf(t, x[i]);
+    const float f = top == t ? 1.f : ex2_approx(top - t);
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = x[i] == -INFINITY ? 0.f : ex2_approx(x[i] - t);  // (a split without a key for this row)
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[i][e], acc[e]);
+    }
+    top = t;
   }
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc_s[warp][kPer * lane + e] = acc[e];

@@ -304,6 +304,9 @@ def test_max_seqlen_bounds_the_keys(max_seqlen):
     cache = _filled(pages, 16, 2, 128, g)
     q = _values((2, 1, 4, 128), torch.bfloat16, g, 1.0).cuda()
     _check(q, cache, table, [100, 63], None, max_seqlen, torch.bfloat16)
+    # with a window that ends before the last key in reach: rows without a key
+    o, lse = _check(q, cache, table, [100, 63], None, max_seqlen, torch.bfloat16, window=20)
+    assert bool((o[0] == 0).all()) == (max_seqlen == 40) and bool((lse[0] == -math.inf).all()) == (max_seqlen == 40)
 
 
 def test_nan_reaches_only_the_rows_that_attend_to_it():
@@ -602,6 +605,86 @@ def test_attention_captured_and_two_threads(length, heads):
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_captured_with_forked_streams():
+    """A step whose append runs on a side stream beside another kernel and is joined before the attention,
+    captured into a graph and replayed on new values: the eager results. (The kernels are launched so that
+    they may begin early; across streams the events alone order them.)"""
+    g = torch.Generator().manual_seed(89)
+    B, Hq, H, d, page, tokens = 2, 4, 2, 128, 16, 40
+    pages, table_h = _layout(B, page, tokens, g)
+    table, lens = _cu(table_h), _cu([tokens] * B)
+    made = [_values((B, tokens, h, d), torch.bfloat16, g, 1.0).cuda() for h in (Hq, H, H, Hq, H, H)]
+    x = [torch.empty_like(t) for t in made[:3]]
+    cache = fa.kv8_cache_alloc(pages, page, H, d)
+    cos, sin = fa.rope_tables(tokens, d)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        k, v = x[1] * 1, x[2] * 1
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            fa.kv8_append(cache, k, v, table, lens)
+        q, _ = fa.qk_norm_rope_forward(x[0], x[1], None, None, cos, sin)
+        main.wait_stream(side)
+        return fa.kv8_attention(q, cache, table, lens, tokens)
+
+    want = []
+    for i in (0, 3):
+        for a, b in zip(x, made[i:i + 3]):
+            a.copy_(b)
+        want.append([t.clone() for t in step()])
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for n in (0, 1, 0):
+        for a, b in zip(x, made[3 * n:3 * n + 3]):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[n][0]) and torch.equal(out[1], want[n][1])
+
+
+def test_a_row_of_calls_without_waiting():
+    """Calls enqueued one behind the other, each reading what the one before wrote (early beginnings must
+    not be seen): token by token through append and attention on one stream, against the same calls with
+    the GPU waited for after each."""
+    g = torch.Generator().manual_seed(97)
+    B, Hq, H, d, page, tokens = 3, 8, 2, 128, 32, 70
+    pages, table_h = _layout(B, page, tokens, g)
+    table = _cu(table_h)
+    cos, sin = fa.rope_tables(tokens, d)
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(torch.bfloat16).cuda()
+    q, k, v = (_values((B, tokens, h, d), torch.bfloat16, g, 2.0).cuda() for h in (Hq, H, H))
+    lens = [_cu([t + 1] * B) for t in range(tokens)]
+
+    def loop(wait):
+        cache = fa.kv8_cache_alloc(pages, page, H, d)
+        x = q[:, :1].contiguous()
+        outs = []
+        torch.cuda.synchronize()
+        if not wait:
+            torch.cuda._sleep(40_000_000)  # so that the calls pile up
+        for t in range(tokens):
+            # the next query depends on the last output
+            x = fa.kv8_norm_rope_append(cache, (q[:, t:t + 1] + x).contiguous(), k[:, t:t + 1], v[:, t:t + 1], w, w, cos,
+                                        sin, table, lens[t])
+            x, lse = fa.kv8_attention(x, cache, table, lens[t], tokens)
+            x, _ = fa.qk_norm_rope_forward(x, x, None, None, cos, sin)
+            outs.append((x, lse))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs, cache
+
+    (a, ca), (b, cb) = loop(True), loop(False)
+    for (x, l), (y, m) in zip(a, b):
+        assert torch.equal(x, y) and torch.equal(l, m)
+    for s, t in zip(ca, cb):
+        assert torch.equal(s.view(torch.uint8), t.view(torch.uint8))
 
 
 def test_other_stream():
