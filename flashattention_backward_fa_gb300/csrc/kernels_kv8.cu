@@ -363,7 +363,8 @@ cudaError_t launch_d(Kv8AppendParams& p, cudaStream_t st) {
   int x = 2 * p.c.H;
   if (p.q) {
     // Heads a block: up to kMaxHeads where kBlocks blocks remain, else one (q, with few tokens: one a
-    // row group).
+    // row group). At bf16 4x16x2048x128: one head a block 45.2 us, up to eight 40.2 us; 152 or 608 for
+    // kBlocks 50 and 43 us.
     const long long places = (long long)p.pages * p.B;
     const auto share = [&](int heads, int least) {
       const long long most = places * heads / kBlocks;
