@@ -337,6 +337,7 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
   p.chunk = plan.chunk;
   p.splits = plan.splits;
   p.cluster = plan.cluster;
+  p.longest_first = plan.longest_first;
   p.row_tiles = plan.row_tiles;
   if (plan.splits > 1 && !plan.cluster) {
     const size_t rows = (size_t)seqs->B * Hq * T * plan.splits;

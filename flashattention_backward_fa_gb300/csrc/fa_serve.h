@@ -140,6 +140,7 @@ struct Kv8AttnParams {
   int splits;     // most splits of a sequence
   int cluster;    // the splits are the blocks of a cluster, which joins them (chunk does not apply)
   int row_tiles;
+  int longest_first;  // blocks take the sequences in the order of falling lengths
   float* part_o;   // [B, H, T * G, splits, d]: normalised outputs of the splits
   float* part_lse;  // [B, H, T * G, splits]: their log2-sum-exp2
 };
@@ -147,7 +148,7 @@ struct Kv8AttnParams {
 struct Kv8AttnPlan {
   int tiles;      // 8-row query tiles of a block (1 or 2)
   int row_tiles;  // blocks that share the T * G rows of a key head
-  int chunk, splits, cluster;
+  int chunk, splits, cluster, longest_first;
   size_t workspace;
 };
 Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window);

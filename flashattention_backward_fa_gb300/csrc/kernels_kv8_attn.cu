@@ -48,6 +48,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "fa_serve.h"
 #include "rope_common.cuh"
@@ -167,6 +168,24 @@ __device__ __forceinline__ Range key_range(const Kv8AttnParams& p, int b, int ro
   return r;
 }
 
+// The sequence that comes at `place` in the order of falling lengths, equal ones by their number.
+// `lens` is shared memory for kThreads numbers.
+__device__ __forceinline__ int sequence_of(const Kv8AttnParams& p, int place, int* lens) {
+  __shared__ int found;
+  const int me = threadIdx.x, mine = me < p.B ? __ldg(p.c.seq_lens + me) : INT_MIN;
+  lens[me] = mine;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < p.B; i += 4) {
+    const int4 x = *reinterpret_cast<const int4*>(lens + i);  // (those past the last are behind all)
+    before += (x.x > mine || (x.x == mine && i < me)) + (x.y > mine || (x.y == mine && i + 1 < me)) +
+              (x.z > mine || (x.z == mine && i + 2 < me)) + (x.w > mine || (x.w == mine && i + 3 < me));
+  }
+  if (me < p.B && before == place) found = me;
+  __syncthreads();
+  return found;
+}
+
 // Keys of a split: the plan's, or, in a cluster, the sequence's own keys shared out evenly.
 __device__ __forceinline__ int split_keys(const Kv8AttnParams& p, const Range& r) {
   if (!p.cluster) return p.chunk;
@@ -266,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   constexpr int KQ = D / 32;           // instructions over the head dimension (S)
   constexpr int kRows = 8 * NT;
   constexpr int kAcc = KS * NT * 4;
-  __shared__ uint2 q_frag[KQ][NT][NP][32];
+  __shared__ __align__(16) uint2 q_frag[KQ][NT][NP][32];
   __shared__ float q_factor[kRows];
   __shared__ float w_m[kWarps][kRows], w_l[kWarps][kRows];
   __shared__ float block_lse[kRows];
@@ -277,11 +296,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   const uint32_t ring = smem_u32(dyn);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-  const int b = blockIdx.z, h = blockIdx.y % p.c.H, rt = blockIdx.y / p.c.H, R = p.T * p.G;
+  const int h = blockIdx.y % p.c.H, rt = blockIdx.y / p.c.H, R = p.T * p.G;
   const int row0 = rt * kRows;
   // (and no let_next_begin here: blocks of the next call would take the places of this one's; the
   // call at 131071 tokens took 57 us with it at the start, 51.4 us at the end, 51.2 us without)
   wait_for_previous();
+  static_assert(sizeof(q_frag) >= kThreads * sizeof(int), "sequence_of uses its place");
+  const int b = p.longest_first ? sequence_of(p, blockIdx.z, reinterpret_cast<int*>(q_frag)) : blockIdx.z;
   const Range kr = key_range(p, b, row0, min(row0 + kRows, R));
   const int chunk = split_keys(p, kr);
   const int begin = kr.lo + blockIdx.x * chunk, end = min(kr.hi, begin + chunk);
@@ -938,6 +959,7 @@ Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int
   plan.chunk = (int)round_hop((range + splits - 1) / splits);
   plan.splits = (int)((range + plan.chunk - 1) / plan.chunk);
   if (plan.splits == 1) plan.cluster = 0;
+  plan.longest_first = B > 1 && B <= kThreads && units * plan.splits > slots;
   plan.workspace = 0;
   if (plan.splits > 1 && !plan.cluster)
     plan.workspace = ((size_t)B * Hq * T * plan.splits * (d + 1) * 4 + 255) / 256 * 256;
