@@ -421,13 +421,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
   float unit = 1.f, unit_top = 0.f;  // acc is in units of `unit`
   __syncthreads();
+  // One row tile: all pieces of the queries but the last in registers. The last one is read from
+  // shared memory at its use; with it in registers the f16 form spilled in the loop (d = 128, 32
+  // sequences of up to 4096 tokens, 32 heads: 127 us against 102.5 us; bf16 as well, 32 sequences
+  // of up to 16384 tokens: 104.4 us against 102.2 us). Two row tiles have no register to spare.
+  constexpr int kHeld = NT == 1 ? NP - 1 : 0;
   uint2 q_reg[NT == 1 ? KQ : 1][NP];
-  if (NT == 1) {
 #pragma unroll
-    for (int i = 0; i < KQ; ++i)
+  for (int i = 0; i < KQ; ++i)
 #pragma unroll
-      for (int n = 0; n < NP; ++n) q_reg[NT == 1 ? i : 0][n] = q_frag[i][0][n][lane];
-  }
+    for (int n = 0; n < kHeld; ++n) q_reg[NT == 1 ? i : 0][n] = q_frag[i][0][n][lane];
   float fac[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
           const uint4 k0 = kv[i >> 1], k1 = kv[(D / 64) + (i >> 1)];
 #pragma unroll
           for (int n = 0; n < NP; ++n) {
-            const uint2 f = NT == 1 ? q_reg[NT == 1 ? i : 0][n] : q_frag[i][nt][n][lane];
+            const uint2 f = n < kHeld ? q_reg[NT == 1 ? i : 0][n] : q_frag[i][nt][n][lane];
             mma_e4m3(part[n], i & 1 ? k0.z : k0.x, i & 1 ? k1.z : k1.x, i & 1 ? k0.w : k0.y, i & 1 ? k1.w : k1.y, f.x, f.y);
           }
         }
@@ -653,16 +656,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
         // codes of two keys side by side: bytes (k0.0, k1.0, k0.1, k1.1) and (k0.2, k1.2, k0.3, k1.3)
         const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
         const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        uint32_t a0, a1, a2, a3;
+        uint32_t a[2][4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          widen4(half ? x1 : x0, a0, a1);
-          widen4(half ? y1 : y0, a2, a3);
+          widen4(half ? x1 : x0, a[half][0], a[half][1]);
+          widen4(half ? y1 : y0, a[half][2], a[half][3]);
+        }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, b0[nt], b1[nt]);
-            if (kResidual) mma_f16(acc[2 * w + half][nt], a0, a1, a2, a3, d0[nt], d1[nt]);
-          }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            mma_f16(acc[2 * w + half][nt], a[half][0], a[half][1], a[half][2], a[half][3], b0[nt], b1[nt]);
+        if (kResidual) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              mma_f16(acc[2 * w + half][nt], a[half][0], a[half][1], a[half][2], a[half][3], d0[nt], d1[nt]);
         }
       }
     }
