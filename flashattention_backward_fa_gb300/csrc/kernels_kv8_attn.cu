@@ -940,9 +940,15 @@ cudaError_t launch_tiles(const Kv8AttnParams& p, int tiles, cudaStream_t st) {
 //   blocks at 131071 tokens 56 us against 50 us.
 // * Where the units alone fill the GPU (kSplitBlocks sets of slots) a split has at
 //   least kSplitKeys keys: its start and its merge cost about 4 us. 16 sequences
-//   with 5 queries and a window of 1024 (f16, d = 64, 16 heads) 14.3 us against
-//   21.0 us with two sets; 32 sequences of up to 16384 tokens 108 us, 143 us
-//   unsplit (unequal lengths) and 119 us from 8192 keys on.
+//   with 5 queries and a window of 1024 (f16, d = 64, 16 heads) 14.6 us against
+//   22.9 us with two sets; 32 sequences of up to 16384 tokens 102 us, 141 us
+//   unsplit (unequal lengths) and 122 us with splits from 2048 keys on.
+// * Where the blocks come in several rounds, the longest sequences come first: a
+//   round's free places go to shorter ones (same batch 108 us in the given order; 8
+//   sequences of up to 32768 tokens with 64 heads 69 -> 60 us). Each block ranks
+//   the lengths for itself, which it can up to its number of threads; equal lengths
+//   take 176 us against 174.5 us without (32 of 4096 tokens, 32 key heads). More
+//   sequences are taken in the given order.
 Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window) {
   constexpr long long kClusterKeys = 256, hop = kHopKeys;
   constexpr long long kSplitBlocks = 1, kSplitKeys = 4096;

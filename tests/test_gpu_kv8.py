@@ -296,6 +296,32 @@ def test_attention_against_float64(case):
     assert fa.fa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("B,T,Hq,H,d,page,width,dtype", [
+    (127, 1, 4, 4, 64, 16, 0, torch.float16),
+    (128, 1, 8, 4, 128, 32, 0, torch.bfloat16),
+    (129, 1, 4, 4, 64, 16, 0, torch.bfloat16),      # taken in their own order
+    (32, 1, 8, 8, 64, 16, 16384, torch.bfloat16),   # clusters of four blocks a sequence
+    (3, 40, 32, 4, 64, 16, 0, torch.float16),       # forty row tiles a key head
+    (2, 64, 64, 4, 128, 64, 9000, torch.bfloat16),
+])
+def test_unequal_lengths_in_several_rounds_of_blocks(B, T, Hq, H, d, page, width, dtype):
+    # lengths that come several times, that are zero, that pass max_seqlen
+    lens = [(29 * b * b + T) % 83 for b in range(B)]
+    lens[0], lens[-1] = 0, 200
+    g = torch.Generator().manual_seed(29)
+    pages, table = _layout(B, page, max(lens), g)
+    cache = _filled(pages, page, H, d, g)
+    q = _values((B, T, Hq, d), dtype, g, 1.0).cuda()
+    limit = max(lens)
+    if width:  # a table made for longer sequences
+        table = torch.nn.functional.pad(torch.as_tensor(table), (0, width // page - len(table[0])), value=-1)
+        limit = width
+    else:
+        lens[1] = page * len(table[0]) + 7
+    _check(q, cache, table, lens, None, limit, dtype)
+    assert fa.fa_get_device_status() == 0
+
+
 @pytest.mark.parametrize("max_seqlen", [40, 100, 4000])
 def test_max_seqlen_bounds_the_keys(max_seqlen):
     """Any upper bound gives the same values up to the tolerance (another split); a smaller one ends the keys."""
