@@ -284,15 +284,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   constexpr int KS = D / 16;           // row tiles of O^T
   constexpr int KQ = D / 32;           // instructions over the head dimension (S)
   constexpr int kRows = 8 * NT;
-  constexpr int kAcc = KS * NT * 4;
   __shared__ __align__(16) uint2 q_frag[KQ][NT][NP][32];
   __shared__ float q_factor[kRows];
   __shared__ float w_m[kWarps][kRows], w_l[kWarps][kRows];
   __shared__ float block_lse[kRows];
   extern __shared__ __align__(128) unsigned char dyn[];
   using G = Ring<D>;
-  static_assert(G::kScales >= (kWarps / 2) * kAcc * 32 * 4 && G::kScales >= kRows * D * 4, "merging reuses the ring");
-  float (*merge)[kAcc][32] = reinterpret_cast<float (*)[kAcc][32]>(dyn);
+  static_assert(G::kScales >= kWarps * kRows * D * 4, "merging reuses the ring");
   const uint32_t ring = smem_u32(dyn);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
@@ -728,104 +726,82 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
         acc[i][nt][e + 2] = none ? 0.f : acc[i][nt][e + 2] * f;
       }
     }
-#pragma unroll
-  for (int half = kWarps / 2; half > 0; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) merge[warp - half][(i * NT + nt) * 4 + e][lane] = acc[i][nt][e];
-    }
-    __syncthreads();
-    if (warp < half) {
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][nt][e] += merge[warp][(i * NT + nt) * 4 + e][lane];
-    }
-    __syncthreads();
-  }
-  // Lane (r, c) of warp 0 holds values [(D / 8) r, + D / 8) of rows 2c and 2c + 1 of every tile.
-  if (p.cluster) {
-    // every block's normalised outputs and log-sum-exp in its shared memory, then each block
-    // joins its share of the (row, four values) items from all of them
-    float* mine = reinterpret_cast<float*>(dyn);  // [kRows][D]; the merge is over
-    if (warp == 0) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 8 * nt + 2 * c + e;
-          float4* o = reinterpret_cast<float4*>(mine + row * D + (D / 8) * r);
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            o[x] = make_float4(acc[2 * x][nt][e], acc[2 * x][nt][e + 2], acc[2 * x + 1][nt][e], acc[2 * x + 1][nt][e + 2]);
-          if (r == 0) block_lse[row] = lse2[nt][e];
-        }
-    }
-    cluster_sync();
-    const int n = p.splits, rows = min(kRows, R - row0);
-    for (int item = blockIdx.x * kThreads + threadIdx.x; item < rows * (D / 4); item += n * kThreads) {
-      const int row = item / (D / 4), e = (item % (D / 4)) * 4;
-      float part[kMaxCluster], top = -INFINITY;
-      float4 o[kMaxCluster];
-#pragma unroll
-      for (int s = 0; s < kMaxCluster; ++s)
-        if (s < n) {
-          part[s] = read_cluster_f32(&block_lse[row], s);
-          o[s] = read_cluster_f32x4(mine + row * D + e, s);
-          top = fmaxf(top, part[s]);
-        }
-      float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < kMaxCluster; ++s)
-        if (s < n) {
-          const float w = part[s] == -INFINITY ? 0.f : ex2_approx(part[s] - top);  // (no key for this row there)
-          sum += w;
-          v[0] = fmaf(w, o[s].x, v[0]), v[1] = fmaf(w, o[s].y, v[1]);
-          v[2] = fmaf(w, o[s].z, v[2]), v[3] = fmaf(w, o[s].w, v[3]);
-        }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int t = (row0 + row) / p.G, hq = h * p.G + (row0 + row) % p.G;
-      T* to = static_cast<T*>(p.o) + b * p.o_st.b + (long long)t * p.o_st.n + (long long)hq * p.o_st.h + e;
-      *reinterpret_cast<uint2*>(to) = make_uint2(pack2<kBf16>(v[0] * inv, v[1] * inv), pack2<kBf16>(v[2] * inv, v[3] * inv));
-      if (e == 0)
-        p.lse[((long long)b * p.Hq + hq) * p.T + t] = sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * kLn2;
-    }
-    cluster_sync();  // (no block leaves while another reads its shared memory)
-    return;
-  }
-  if (warp != 0) return;
+  // Every warp's outputs in shared memory, summed there by (row, four values). Lane (r, c) holds
+  // values [(D / 8) r, + D / 8) of rows 2c and 2c + 1 of every tile; chunk x of a row lies at
+  // x ^ turn(row), so that eight lanes' stores meet in no bank.
+  const auto turn = [](int row) { return D == 128 ? (row >> 1) & 3 : ((row >> 1) & 1) | (row & 4); };
+  float* sums = reinterpret_cast<float*>(dyn);  // [kWarps][kRows][D], then in [0] the block's
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = row0 + 8 * nt + 2 * c + e;
-      if (row >= R) continue;
-      const int t = row / p.G, hq = h * p.G + row % p.G;
-      if (p.splits == 1) {
-        T* o = static_cast<T*>(p.o) + b * p.o_st.b + (long long)t * p.o_st.n + (long long)hq * p.o_st.h + (D / 8) * r;
+      const int row = 8 * nt + 2 * c + e;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack2<kBf16>(acc[4 * x + i][nt][e], acc[4 * x + i][nt][e + 2]);
-          reinterpret_cast<uint4*>(o)[x] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (r == 0) p.lse[((long long)b * p.Hq + hq) * p.T + t] = lse2[nt][e] * kLn2;
-      } else {
-        const long long at = (((long long)b * p.c.H + h) * R + row) * p.splits + blockIdx.x;
-        float4* o = reinterpret_cast<float4*>(p.part_o + at * D + (D / 8) * r);
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x)
-          o[x] = make_float4(acc[2 * x][nt][e], acc[2 * x][nt][e + 2], acc[2 * x + 1][nt][e], acc[2 * x + 1][nt][e + 2]);
-        if (r == 0) p.part_lse[at] = lse2[nt][e];
-      }
+      for (int x = 0; x < D / 32; ++x)
+        *reinterpret_cast<float4*>(sums + (warp * kRows + row) * D + (((D / 32) * r + x) ^ turn(row)) * 4) =
+            make_float4(acc[2 * x][nt][e], acc[2 * x][nt][e + 2], acc[2 * x + 1][nt][e], acc[2 * x + 1][nt][e + 2]);
+      if (warp == 0 && r == 0) block_lse[row] = lse2[nt][e];
     }
+  __syncthreads();
+  const int items = min(kRows, R - row0) * (D / 4);
+  const auto out = [&](int row, int x) {
+    const int t = (row0 + row) / p.G, hq = h * p.G + (row0 + row) % p.G;
+    return static_cast<T*>(p.o) + b * p.o_st.b + (long long)t * p.o_st.n + (long long)hq * p.o_st.h + 4 * x;
+  };
+  const auto out_lse = [&](int row, float lse) {
+    const int t = (row0 + row) / p.G, hq = h * p.G + (row0 + row) % p.G;
+    p.lse[((long long)b * p.Hq + hq) * p.T + t] = lse * kLn2;
+  };
+  for (int item = threadIdx.x; item < items; item += kThreads) {
+    const int row = item / (D / 4), x = item % (D / 4);
+    float4* at = reinterpret_cast<float4*>(sums + row * D + (x ^ turn(row)) * 4);
+    float4 v = at[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 o = at[w * kRows * (D / 4)];
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    if (p.cluster) {
+      at[0] = v;
+    } else if (p.splits == 1) {
+      *reinterpret_cast<uint2*>(out(row, x)) = make_uint2(pack2<kBf16>(v.x, v.y), pack2<kBf16>(v.z, v.w));
+      if (x == 0) out_lse(row, block_lse[row]);
+    } else {
+      const long long to = (((long long)b * p.c.H + h) * R + row0 + row) * p.splits + blockIdx.x;
+      *reinterpret_cast<float4*>(p.part_o + to * D + 4 * x) = v;
+      if (x == 0) p.part_lse[to] = block_lse[row];
+    }
+  }
+  if (!p.cluster) return;
+  // Each block of the cluster joins its share of the items from all of them.
+  cluster_sync();
+  const int n = p.splits;
+  for (int item = blockIdx.x * kThreads + threadIdx.x; item < items; item += n * kThreads) {
+    const int row = item / (D / 4), x = item % (D / 4);
+    float part[kMaxCluster], top = -INFINITY;
+    float4 o[kMaxCluster];
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      if (s < n) {
+        part[s] = read_cluster_f32(&block_lse[row], s);
+        o[s] = read_cluster_f32x4(sums + row * D + (x ^ turn(row)) * 4, s);
+        top = fmaxf(top, part[s]);
+      }
+    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      if (s < n) {
+        const float w = part[s] == -INFINITY ? 0.f : ex2_approx(part[s] - top);  // (no key for this row there)
+        sum += w;
+        v[0] = fmaf(w, o[s].x, v[0]), v[1] = fmaf(w, o[s].y, v[1]);
+        v[2] = fmaf(w, o[s].z, v[2]), v[3] = fmaf(w, o[s].w, v[3]);
+      }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(out(row, x)) =
+        make_uint2(pack2<kBf16>(v[0] * inv, v[1] * inv), pack2<kBf16>(v[2] * inv, v[3] * inv));
+    if (x == 0) out_lse(row, sum == 0.f ? -INFINITY : top + lg2_approx(sum));
+  }
+  cluster_sync();  // (no block leaves while another reads its shared memory)
 }
 
 // Joins the splits of one row (a block): O = sum_s w_s O_s / sum_s w_s with
