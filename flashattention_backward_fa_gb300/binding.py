@@ -899,8 +899,8 @@ def _kv8_attn(q, cache, o, lse, block_table, seq_lens, max_seqlen, workspace, ne
     slopes, per_seq = (None, 0) if alibi_slopes is None else _alibi(alibi_slopes, B, Hq, q.device)
     _check(lib.fa_kv8_attn(
         c, s, q.data_ptr(), o.data_ptr(), lse.data_ptr(), T, Hq, max_seqlen, q_st, o_st, _TORCH_TO_FA[dtype],
-        default_scale(d) if scale is None else float(scale), causal, window, slopes, per_seq, None if workspace is None else workspace.data_ptr(), size,
-        _stream(stream)))
+        default_scale(d) if scale is None else float(scale), causal, window, slopes, per_seq,
+        None if workspace is None else workspace.data_ptr(), size, _stream(stream)))
     return o, lse
 
 
