@@ -419,11 +419,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
   float unit = 1.f, unit_top = 0.f;  // acc is in units of `unit`
   __syncthreads();
-  // One row tile: all pieces of the queries but the last in registers. The last one is read from
-  // shared memory at its use; with it in registers the f16 form spilled in the loop (d = 128, 32
-  // sequences of up to 4096 tokens, 32 heads: 127 us against 102.5 us; bf16 as well, 32 sequences
-  // of up to 16384 tokens: 104.4 us against 102.2 us). Two row tiles have no register to spare.
-  constexpr int kHeld = NT == 1 ? NP - 1 : 0;
+  // One row tile: two pieces of the queries stay in registers, f16's third one is read from shared
+  // memory at its use. With all three held the f16 form spilled in the loop (d = 128, 32 sequences
+  // of up to 4096 tokens, 32 heads: 132 us against 103 us), with one of bf16's two in shared memory
+  // 32 sequences of up to 16384 tokens took 102 us against 100.5 us. Two row tiles have no
+  // register to spare.
+  constexpr int kHeld = NT == 1 ? 2 : 0;
   uint2 q_reg[NT == 1 ? KQ : 1][NP];
 #pragma unroll
   for (int i = 0; i < KQ; ++i)
@@ -909,11 +910,11 @@ cudaError_t launch_tiles(const Kv8AttnParams& p, int tiles, cudaStream_t st) {
 // Splits (times: bf16, d = 128, eight key heads where nothing else is said).
 // * Up to eight blocks a sequence and row tile join within a cluster, each
 //   sequence sharing out its own keys: no workspace, no second kernel. One
-//   sequence of 1000 tokens takes 7.0 us so, 9.9 us with the second kernel.
+//   sequence of 1000 tokens takes 6.95 us so, 7.6 us with the second kernel.
 // * Where eight splits leave the GPU empty and a block's share is more than
 //   kClusterKeys keys, one resident set of blocks and the joining kernel: one
-//   sequence of 4096 tokens 10.3 us against 12.3 us in a cluster; twice as many
-//   blocks at 131071 tokens 56 us against 50 us.
+//   sequence of 4096 tokens 8.3 us against 9.9 us in a cluster; twice as many
+//   blocks at 131071 tokens 55 us against 49 us.
 // * Where the units alone fill the GPU (kSplitBlocks sets of slots) a split has at
 //   least kSplitKeys keys: its start and its merge cost about 4 us. 16 sequences
 //   with 5 queries and a window of 1024 (f16, d = 64, 16 heads) 14.6 us against
