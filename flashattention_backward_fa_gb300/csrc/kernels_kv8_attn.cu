@@ -48,7 +48,6 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <climits>
 
 #include "fa_serve.h"
 #include "rope_common.cuh"
@@ -168,18 +167,20 @@ __device__ __forceinline__ Range key_range(const Kv8AttnParams& p, int b, int ro
   return r;
 }
 
-// The sequence that comes at `place` in the order of falling lengths, equal ones by their number.
-// `lens` is shared memory for kThreads numbers.
-__device__ __forceinline__ int sequence_of(const Kv8AttnParams& p, int place, int* lens) {
+// The sequence that comes at `place` in the order of falling lengths (up to 2^24 - 1), equal ones
+// by their number. `ranks` is shared memory for kThreads numbers.
+__device__ __forceinline__ int sequence_of(const Kv8AttnParams& p, int place, int* ranks) {
+  static_assert(kThreads == 128, "a number takes 7 bits");
   __shared__ int found;
-  const int me = threadIdx.x, mine = me < p.B ? __ldg(p.c.seq_lens + me) : INT_MIN;
-  lens[me] = mine;
+  const int me = threadIdx.x;
+  const int mine = me < p.B ? min(max(__ldg(p.c.seq_lens + me), 0), (1 << 24) - 1) * kThreads + kThreads - 1 - me : -1;
+  ranks[me] = mine;
   __syncthreads();
   int before = 0;
+#pragma unroll 4
   for (int i = 0; i < p.B; i += 4) {
-    const int4 x = *reinterpret_cast<const int4*>(lens + i);  // (those past the last are behind all)
-    before += (x.x > mine || (x.x == mine && i < me)) + (x.y > mine || (x.y == mine && i + 1 < me)) +
-              (x.z > mine || (x.z == mine && i + 2 < me)) + (x.w > mine || (x.w == mine && i + 3 < me));
+    const int4 x = *reinterpret_cast<const int4*>(ranks + i);  // (those past the last are behind all)
+    before += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
   }
   if (me < p.B && before == place) found = me;
   __syncthreads();
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   // One row tile: two pieces of the queries stay in registers, f16's third one is read from shared
   // memory at its use. With all three held the f16 form spilled in the loop (d = 128, 32 sequences
   // of up to 4096 tokens, 32 heads: 132 us against 103 us), with one of bf16's two in shared memory
-  // 32 sequences of up to 16384 tokens took 102 us against 100.5 us. Two row tiles have no
+  // 32 sequences of up to 16384 tokens took 102 us against 100 us. Two row tiles have no
   // register to spare.
   constexpr int kHeld = NT == 1 ? 2 : 0;
   uint2 q_reg[NT == 1 ? KQ : 1][NP];
@@ -917,18 +918,21 @@ cudaError_t launch_tiles(const Kv8AttnParams& p, int tiles, cudaStream_t st) {
 //   blocks at 131071 tokens 55 us against 49 us.
 // * Where the units alone fill the GPU (kSplitBlocks sets of slots) a split has at
 //   least kSplitKeys keys: its start and its merge cost about 4 us. 16 sequences
-//   with 5 queries and a window of 1024 (f16, d = 64, 16 heads) 14.6 us against
-//   22.9 us with two sets; 32 sequences of up to 16384 tokens 102 us, 141 us
-//   unsplit (unequal lengths) and 122 us with splits from 2048 keys on.
+//   with 5 queries and a window of 1024 (f16, d = 64, 16 heads) 14.2 us against
+//   22.9 us with two sets; 32 sequences of up to 16384 tokens 100 us, 140 us
+//   unsplit (unequal lengths) and 118 us with splits from 2048 keys on.
 // * Where the blocks come in several rounds, the longest sequences come first: a
-//   round's free places go to shorter ones (same batch 108 us in the given order; 8
-//   sequences of up to 32768 tokens with 64 heads 69 -> 60 us). Each block ranks
-//   the lengths for itself, which it can up to its number of threads; equal lengths
-//   take 176 us against 174.5 us without (32 of 4096 tokens, 32 key heads). More
-//   sequences are taken in the given order.
+//   round's free places go to shorter ones (same batch 100 us against 107 us in the
+//   given order; 8 sequences of up to 32768 tokens with 64 heads 59 us against 69 us).
+//   Each block ranks the lengths for itself, which it can up to its number of threads,
+//   in up to a microsecond: worth it where a block may have more than kOrderKeys keys
+//   (128 sequences of up to 2048 tokens 56.3 us against 57.7 us, of up to 1024 tokens
+//   36.8 us against 36.0 us, of up to 500 tokens 27.1 us against 25.1 us). Where all
+//   lengths are equal it costs 1% (32 of 4096 tokens, 32 key heads, 173.6 us against
+//   172.5 us).
 Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int causal, int window) {
   constexpr long long kClusterKeys = 256, hop = kHopKeys;
-  constexpr long long kSplitBlocks = 1, kSplitKeys = 4096;
+  constexpr long long kSplitBlocks = 1, kSplitKeys = 4096, kOrderKeys = 1024;
   Kv8AttnPlan plan;
   const long long R = (long long)T * (Hq / H);
   // More than eight rows: 16 a block, further ones in blocks of their own that find the cache in
@@ -952,7 +956,7 @@ Kv8AttnPlan kv8_attn_plan(int B, int T, int Hq, int H, int d, int key_limit, int
   plan.chunk = (int)round_hop((range + splits - 1) / splits);
   plan.splits = (int)((range + plan.chunk - 1) / plan.chunk);
   if (plan.splits == 1) plan.cluster = 0;
-  plan.longest_first = B > 1 && B <= kThreads && units * plan.splits > slots;
+  plan.longest_first = B > 1 && B <= kThreads && units * plan.splits > slots && plan.chunk > kOrderKeys;
   plan.workspace = 0;
   if (plan.splits > 1 && !plan.cluster)
     plan.workspace = ((size_t)B * Hq * T * plan.splits * (d + 1) * 4 + 255) / 256 * 256;

@@ -297,11 +297,12 @@ def test_attention_against_float64(case):
 
 
 @pytest.mark.parametrize("B,T,Hq,H,d,page,width,dtype", [
-    (127, 1, 4, 4, 64, 16, 0, torch.float16),
-    (128, 1, 8, 4, 128, 32, 0, torch.bfloat16),
-    (129, 1, 4, 4, 64, 16, 0, torch.bfloat16),      # taken in their own order
+    (127, 1, 4, 4, 64, 16, 2048, torch.float16),
+    (128, 1, 8, 4, 128, 32, 2048, torch.bfloat16),
+    (129, 1, 4, 4, 64, 16, 2048, torch.bfloat16),   # taken in the given order
+    (128, 1, 4, 4, 64, 16, 0, torch.bfloat16),      # short blocks, in the given order
     (32, 1, 8, 8, 64, 16, 16384, torch.bfloat16),   # clusters of four blocks a sequence
-    (3, 40, 32, 4, 64, 16, 0, torch.float16),       # forty row tiles a key head
+    (3, 40, 32, 4, 64, 16, 2048, torch.float16),    # twenty row tiles a key head
     (2, 64, 64, 4, 128, 64, 9000, torch.bfloat16),
 ])
 def test_unequal_lengths_in_several_rounds_of_blocks(B, T, Hq, H, d, page, width, dtype):
