@@ -544,7 +544,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
     bool other = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (step_bad >> u & 1u) vs[u] = unit;
+      if (step_bad >> u & 1u)
+        vs[u] = unit;
+      else
+        unit_top = fmaxf(unit_top, vs[u]);  // (also where the first scale is the unit that acc begins with)
       pv[u] = 1.f;
       other |= vs[u] != unit;
     }
@@ -554,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       float to = vs[0];
 #pragma unroll
       for (int u = 1; u < U; ++u) to = fmaxf(to, vs[u]);
-      unit_top = fmaxf(unit_top, to);
       to = fmaxf(fmaxf(to, unit_top * 5.421010862427522e-20f), 1.1754944e-38f);
       const float f = unit / to;
 #pragma unroll
