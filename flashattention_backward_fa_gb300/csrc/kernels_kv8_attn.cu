@@ -23,15 +23,17 @@
 //   48 more ALU operations a step, at 2 a clock and SM.
 // * V's codes are widened to f16 (exact) for the f16 instruction, because the
 //   weights P need its range: an e4m3 piece ends 2^-18 below the largest weight,
-//   and a long sequence can hold most of its mass below that. They are summed in
-//   units of their page's scale; the sums are rescaled on the rare page whose scale
-//   differs (exact for powers of two).
-// * Running maximum and sum per row in fp32, kept per lane; the reference m
-//   moves only when a score exceeds it by 2^15 (P is then at most 2^15, inside
-//   f16), and is set so that the maximum's P is 2^7, so warps agree on a new m a few
-//   times a sequence and vote otherwise. P is rounded to f16 (2^-12 of itself);
-//   for f16 outputs, whose own rounding is no larger, its rounding residual is
-//   multiplied too.
+//   and a long sequence can hold most of its mass below that.
+// * Running maximum and sum per row in fp32, kept per lane. A row has two references
+//   in the exponent: m for the sum of its weights 2^(s - m), and mv for its outputs,
+//   whose factors are P = 2^(s - mv) times the page's V scale. P is what enters f16, so
+//   what counts there is a key's weight times the size of its page's values: pages
+//   with values of any two sizes may lie in one step, and a page that a row does not
+//   attend to has no say in its mv. A reference moves only when it is exceeded by 2^15
+//   (P is then at most 2^15, inside f16), and is set so that the largest P is 2^7, so
+//   warps agree on new ones a few times a sequence and vote otherwise. P is rounded to
+//   f16 (2^-11 of itself, or 2^-32 of the row's largest below 2^-21 of it); for f16
+//   outputs, whose own rounding is no larger, its rounding residual is multiplied too.
 // * Four warps take steps of 32 keys (two tiles, whose chains of instructions
 //   overlap) in turn. The next step is on its way to the warp's own part of shared
 //   memory (cp.async), so a warp waits for itself alone, and 96 KB an SM are in
@@ -62,9 +64,10 @@ constexpr int kMaxCluster = 8;
 constexpr int kTile = 16;       // keys of an instruction
 constexpr int U = 2;            // tiles of a step
 constexpr int kHopKeys = kTile * U * kWarps;  // keys of a step of all warps; splits are multiples of it
-constexpr float kNoMax = -3.0e38f;  // m before any score
-constexpr float kHead = 7.f;    // a new m is set that far below the maximum, whose P is then 2^7
-constexpr float kTop = 15.f;    // scores may pass m by this much before it moves (log2): P stays within 2^15
+constexpr float kNoMax = -3.0e38f;  // m and mv before any score
+constexpr float kHead = 7.f;    // a new reference is set that far below the maximum, whose P is then 2^7
+constexpr float kTop = 15.f;    // scores may pass a reference by this much before it moves (log2): P stays within 2^15
+constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100: V scales below it count as it for mv
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   }
 
   // This lane's rows are 2c and 2c + 1 of every tile: scale, position, slope.
-  float m[NT][2], l[NT][2], slope[NT][2];
+  float m[NT][2], mv[NT][2], l[NT][2], slope[NT][2];
   int pos[NT][2];
   int all_lo = 0, all_hi = kr.hi;  // keys [all_lo, all_hi) are attended by every live row of the block
 #pragma unroll
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       const bool live = row < R && t < kr.count && pos[nt][e] >= 0;
       if (!live) pos[nt][e] = -1;
       slope[nt][e] = live && p.alibi ? __ldg(p.alibi + b * p.alibi_sb + h * p.G + row % p.G) * 1.4426950408889634f : 0.f;
-      m[nt][e] = kNoMax;
+      m[nt][e] = mv[nt][e] = kNoMax;
       l[nt][e] = 0.f;
     }
   {
@@ -418,7 +421,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
-  float unit = 1.f, unit_top = 0.f;  // acc is in units of `unit`
   __syncthreads();
   // One row tile: two pieces of the queries stay in registers, f16's third one is read from shared
   // memory at its use. With all three held the f16 form spilled in the loop (d = 128, 32 sequences
@@ -509,29 +511,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
           for (int e = 0; e < 4; ++e)
             if (!attends(u, nt, e)) sc[u][nt][e] = -INFINITY;
     }
+    float lv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (step_bad >> u & 1u) vs[u] = 0.f;  // (was not fetched)
+      lv[u] = lg2_approx(fmaxf(fabsf(vs[u]), kLeastScale));
+    }
     bool over = false;
-    float top[NT][2];
+    float top[NT][2], top_v[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        top[nt][e] = fmaxf(sc[0][nt][e], sc[0][nt][e + 2]);
-        top[nt][e] = fmax3(top[nt][e], sc[1][nt][e], sc[1][nt][e + 2]);
-        over |= top[nt][e] > m[nt][e] + kTop;
+        top[nt][e] = top_v[nt][e] = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float x = fmaxf(sc[u][nt][e], sc[u][nt][e + 2]);
+          top[nt][e] = fmaxf(top[nt][e], x);
+          top_v[nt][e] = fmaxf(top_v[nt][e], x + lv[u]);
+        }
+        over |= top[nt][e] > m[nt][e] + kTop || top_v[nt][e] > mv[nt][e] + kTop;
       }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = top[nt][e];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          float x = top[nt][e], y = top_v[nt][e];
+#pragma unroll
+          for (int lanes = 4; lanes <= 16; lanes *= 2) {
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, lanes));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, lanes));
+          }
           if (x > m[nt][e] + kTop) {
-            const float to = x - kHead, f = ex2_approx(m[nt][e] - to);
-            m[nt][e] = to;
-            l[nt][e] *= f;
+            l[nt][e] *= ex2_approx(m[nt][e] - (x - kHead));
+            m[nt][e] = x - kHead;
+          }
+          if (y > mv[nt][e] + kTop) {
+            const float to = y - kHead, f = ex2_approx(mv[nt][e] - to);
+            mv[nt][e] = to;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
               acc[i][nt][e] *= f;
@@ -540,35 +558,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
           }
         }
     }
-    float pv[U];
-    bool other = false;
+    // 2^(m - mv), which takes a weight of the sum to its P: in two factors, because with V scales up to
+    // 2^120 and down to 2^-100 it alone may leave fp32's range
+    float to_p[NT][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (step_bad >> u & 1u)
-        vs[u] = unit;
-      else
-        unit_top = fmaxf(unit_top, vs[u]);  // (also where the first scale is the unit that acc begins with)
-      pv[u] = 1.f;
-      other |= vs[u] != unit;
-    }
-    if (other) {
-      // another V scale: the sums go over to its unit (the larger one of a step's two), but not
-      // below 2^-64 of the largest so far (P takes the rest), so that they stay in range
-      float to = vs[0];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int u = 1; u < U; ++u) to = fmaxf(to, vs[u]);
-      to = fmaxf(fmaxf(to, unit_top * 5.421010862427522e-20f), 1.1754944e-38f);
-      const float f = unit / to;
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][nt][e] *= f;
-      unit = to;
-#pragma unroll
-      for (int u = 0; u < U; ++u) pv[u] = vs[u] / to;
-    }
+      for (int e = 0; e < 2; ++e) to_p[nt][e] = ex2_approx(m[nt][e] - mv[nt][e] + 10.f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t b0[NT], b1[NT], d0[NT], d1[NT];
@@ -579,10 +575,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
         for (int e = 0; e < 4; ++e) {
           x[e] = ex2_approx(sc[u][nt][e] - m[nt][e & 1]);
           l[nt][e & 1] += x[e];
-        }
-        if (pv[u] != 1.f) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] *= pv[u];
+          x[e] *= vs[u] * 0.0009765625f * to_p[nt][e & 1];
         }
         const uint32_t lo = pack2<false>(x[0], x[1]), hi = pack2<false>(x[2], x[3]);
         if (kResidual) {
@@ -723,11 +716,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       if (pos[nt][e] < 0) sum = 0.f;  // a padding row (unmasked in whole steps)
       lse2[nt][e] = sum == 0.f ? -INFINITY : top + lg2_approx(sum);
       const bool none = sum == 0.f;  // (its sums may hold NaN all the same: a padding row's)
-      const float f = ex2_approx(m[nt][e] - top) / sum * unit;
+      const float f = 1024.f / sum, g = ex2_approx(mv[nt][e] - top - 10.f);  // (in two factors as above)
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
-        acc[i][nt][e] = none ? 0.f : acc[i][nt][e] * f;
-        acc[i][nt][e + 2] = none ? 0.f : acc[i][nt][e + 2] * f;
+        acc[i][nt][e] = none ? 0.f : acc[i][nt][e] * f * g;
+        acc[i][nt][e + 2] = none ? 0.f : acc[i][nt][e + 2] * f * g;
       }
     }
   // Every warp's outputs in shared memory, summed there by (row, four values). Lane (r, c) holds

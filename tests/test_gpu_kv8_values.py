@@ -96,3 +96,130 @@ def test_sums_survive_pages_of_zeros_behind_a_scale_of_one():
     q[..., 0] = 1.0
     o, _ = _check(q, cache, table, [n] * B)
     assert bool(o.isfinite().all())
+
+
+# (page, log2 of the small page's size under the large one's)
+FAR = [(16, 9, F16), (16, 20, F16), (16, 26, F16), (16, 26, BF16), (16, 30, BF16), (16, 60, BF16), (16, 100, BF16)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,ratio,dtype", FAR)
+def test_weight_on_the_page_of_smaller_values(page, ratio, dtype, d):
+    """Two pages in one step of 32 keys: nearly all the weight is on the one with the small values, the
+    other one's is e^-80."""
+    g = torch.Generator().manual_seed(71)
+    top = 10 if dtype == F16 else 0
+    for small in (0, 1):
+        k = torch.randn(1, 2 * page, 1, d, generator=g) * 0.1
+        k[..., 0] = 0.0
+        k[0, (1 - small) * page:(2 - small) * page, 0, 0] = -10.0
+        size = torch.full((2 * page,), 2.0 ** top)
+        size[small * page:(small + 1) * page] = 2.0 ** (top - ratio)
+        v = torch.randn(1, 2 * page, 1, d, generator=g) * size[None, :, None, None]
+        table = torch.tensor([[1, 0]], dtype=torch.int32)
+        cache = _cache(k.to(dtype), v.to(dtype), page, table)
+        q = (torch.randn(1, 1, 3, d, generator=g) * 0.1).to(dtype)
+        q[..., 0] = 8.0
+        _check(q.cuda(), cache, table, [2 * page])
+
+
+@pytest.mark.parametrize("dtype,ratio", [(F16, 20), (F16, 28), (BF16, 28), (BF16, 40), (BF16, 110)])
+@pytest.mark.parametrize("page,length,T", [(16, 17, 2), (16, 40, 25), (32, 33, 2), (64, 200, 12)])
+def test_large_values_that_a_row_does_not_see(page, length, T, dtype, ratio):
+    """The last tokens' values are far larger than those before: rows before them must not notice."""
+    g = torch.Generator().manual_seed(73)
+    d, Hq, H = 64, 6, 2
+    n = -(-length // page)
+    top = 12 if dtype == F16 else 0
+    size = torch.full((length,), 2.0 ** (top - ratio))
+    size[(length - 1) // page * page:] = 2.0 ** top
+    k = torch.randn(1, length, H, d, generator=g).to(dtype)
+    v = (torch.randn(1, length, H, d, generator=g) * size[None, :, None, None]).to(dtype)
+    table = torch.randperm(n, generator=g)[None].int()
+    cache = _cache(k, v, page, table)
+    q = torch.randn(1, T, Hq, d, generator=g).to(dtype).cuda()
+    _check(q, cache, table, [length], scale=0.125)
+    _check(q, cache, table, [length], scale=0.125, window=min(20, length))
+
+
+@pytest.mark.parametrize("weight", [-18, -24, -30])
+def test_small_weights_on_large_values(weight):
+    """A page with 2^weight of the others' weights and values 2^40 times theirs makes the output; its
+    weights must not be rounded as if they did not matter. Steps of one warp and of several."""
+    g = torch.Generator().manual_seed(79)
+    d, page = 128, 16
+    for n, large in ((32, 1), (32, 0), (640, 33), (640, 0)):
+        k = torch.zeros(1, n, 1, d)
+        k[0, large * page:(large + 1) * page, 0, 0] = weight * math.log(2.0)
+        size = torch.ones(n)
+        size[large * page:(large + 1) * page] = 2.0 ** 40
+        v = torch.randn(1, n, 1, d, generator=g) * size[None, :, None, None]
+        table = torch.randperm(n // page, generator=g)[None].int()
+        cache = _cache(k.to(BF16), v.to(BF16), page, table)
+        q = torch.zeros(1, 1, 1, d, dtype=BF16, device="cuda")
+        q[..., 0] = 1.0
+        _check(q, cache, table, [n])
+
+
+@pytest.mark.parametrize("order", [[0, 1, 2, 3], [3, 2, 1, 0], [1, 3, 0, 2], [2, 0, 3, 1]])
+@pytest.mark.parametrize("T,window", [(1, 0), (3, 16), (20, 16), (50, 40)])
+def test_pages_of_four_sizes(order, T, window):
+    """Every step holds two sizes; rows reach different pages of the four."""
+    g = torch.Generator().manual_seed(83)
+    page, d, n = 16, 128, 64
+    size = torch.tensor([2.0 ** -60, 1.0, 2.0 ** 13, 2.0 ** 40])[order].repeat_interleave(page)
+    k = torch.randn(2, n, 2, d, generator=g).to(BF16)
+    v = (torch.randn(2, n, 2, d, generator=g) * size[None, :, None, None]).to(BF16)
+    table = torch.randperm(8, generator=g).view(2, 4).int()
+    cache = _cache(k, v, page, table)
+    q = torch.randn(2, T, 4, d, generator=g).to(BF16).cuda()
+    _check(q, cache, table, [n, n], scale=0.1, window=window)
+    _check(q, cache, table, [n, n - 11], [T, max(T - 2, 0)], scale=0.1, window=window)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -95, 2.0 ** 100, 2.0 ** 124])
+def test_values_of_one_extreme_size(size):
+    """Scales near both ends of the range, alone and beside pages of zeros."""
+    g = torch.Generator().manual_seed(89)
+    page, d, n = 16, 64, 400
+    k = torch.randn(1, n, 1, d, generator=g).to(BF16)
+    v = (torch.randn(1, n, 1, d, generator=g).clamp(-3, 3) * size).to(BF16)
+    v[:, 16:48] = 0.0
+    table = torch.randperm(n // page, generator=g)[None].int()
+    cache = _cache(k, v, page, table)
+    q = torch.randn(1, 2, 2, d, generator=g).to(BF16).cuda()
+    _check(q, cache, table, [n], scale=0.2)
+
+
+def test_scales_that_are_no_powers_of_two():
+    """A cache filled by its user: any positive scales, V's also 0 (the page stands for zeros)."""
+    g = torch.Generator().manual_seed(97)
+    pages, page, H, d = 9, 16, 2, 128
+    cache = fa.kv8_cache_alloc(pages, page, H, d)
+    for x in (cache.k, cache.v):
+        x.copy_((torch.randn(x.shape, generator=g) * 60).clamp(-440, 440))
+    cache.k_scale.copy_(0.003 * (0.5 + torch.rand(pages, H, generator=g)))
+    cache.v_scale.copy_(torch.pow(10.0, 6 * torch.rand(pages, H, generator=g) - 4))
+    cache.v_scale[4, 0] = 0.0
+    table = torch.randperm(pages, generator=g)[None].int()
+    for dtype in (BF16, F16):
+        q = torch.randn(1, 3, 4, d, generator=g).to(dtype).cuda()
+        _check(q, cache, table, [pages * page - 5], scale=0.1)
+
+
+def test_rising_and_falling_scores_with_changing_scales():
+    """The running maximum and the pages' scales move against each other from step to step."""
+    g = torch.Generator().manual_seed(101)
+    page, d, n = 16, 64, 1280
+    for sign in (1.0, -1.0):
+        for dtype in (BF16, F16):
+            ramp = torch.arange(n) / n
+            k = torch.zeros(1, n, 1, d)
+            k[0, :, 0, 0] = sign * 40 * ramp
+            e = torch.randint(-8, 9, (n // page,), generator=g).repeat_interleave(page) - sign * 30 * (ramp - 0.5) / 2
+            v = torch.randn(1, n, 1, d, generator=g).clamp(-3, 3) * torch.exp2(e / 2)[None, :, None, None]
+            table = torch.randperm(n // page, generator=g)[None].int()
+            cache = _cache(k.to(dtype), v.to(dtype), page, table)
+            q = torch.zeros(1, 2, 2, d, dtype=dtype, device="cuda")
+            q[..., 0] = 1.0
+            _check(q, cache, table, [n])
