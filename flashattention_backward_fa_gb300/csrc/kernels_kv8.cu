@@ -137,8 +137,8 @@ __device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T)
 // weights are loaded once for all heads, and the next head's rows are on their way
 // while one is finished. kRows rows of a page a thread; blockDim.x * kRows * 16
 // values hold a page's new rows. kNorm: 0 append alone, 1 / 2 norm and rotation
-// with partners rot / 2 apart / neighbours.
-template <typename T, int D, int kRows, int kNorm>
+// with partners rot / 2 apart / neighbours; kPartial: rot < D.
+template <typename T, int D, int kRows, int kNorm, bool kPartial>
 __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows == 4 ? 4 : 8) : 1)
     kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   constexpr int G = D / 16;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
   head += group * span;
   const int turns = kNorm == 0 ? 1 : (heads + beside - 1) / beside, head_end = group * span + heads;
   const fa_strides& st = is_q ? p.q_st : is_v ? p.v_st : p.k_st;
-  const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % G, p.rot);
+  const LanePlace at = lane_place<D, kNeighbours, kPartial>(threadIdx.x % G, p.rot);
   const T* src = static_cast<const T*>(is_q ? p.q : is_v ? p.v : p.k) + b * st.b + (long long)(first + row0) * st.n +
                  at.a;
   const int hop = at.b - at.a;
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
     if (kNorm != 0 && !is_v) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], lw, cc[i], ss[i], p.eps);
+        norm_rope_lane<T, D, kNeighbours>(ra[i], rb[i], at, lw, cc[i], ss[i], p.eps);
         if (!live[i]) {  // zeros, also where a NaN among the weights has reached them
           zero8(ra[i]);
           zero8(rb[i]);
@@ -334,20 +334,26 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
   if (kNorm != 0) copies_wait<0>();
 }
 
+template <typename T, int D, int kRows, int kNorm, bool kPartial>
+cudaError_t launch_norm(const Kv8AppendParams& p, dim3 grid, int threads, cudaStream_t st) {
+  constexpr auto kKernel = kv8_append_kernel<T, D, kRows, kNorm, kPartial>;
+  const cudaError_t e = allow_smem<kKernel>(RowRing<T, 2 * kRows, kAhead>::bytes(512));
+  if (e != cudaSuccess) return e;
+  return launch_chained(kKernel, grid, threads, RowRing<T, 2 * kRows, kAhead>::bytes(threads), 1, p, st);
+}
+
 template <typename T, int D, int kRows>
 cudaError_t launch_rows(const Kv8AppendParams& p, dim3 grid, int threads, cudaStream_t st) {
   if constexpr (kRows <= 2) {
     if (p.q != nullptr) {
-      const int ring = RowRing<T, 2 * kRows, kAhead>::bytes(threads);
-      constexpr int most = RowRing<T, 2 * kRows, kAhead>::bytes(512);
-      const cudaError_t e = p.neighbours ? allow_smem<kv8_append_kernel<T, D, kRows, 2>>(most)
-                                         : allow_smem<kv8_append_kernel<T, D, kRows, 1>>(most);
-      if (e != cudaSuccess) return e;
-      return p.neighbours ? launch_chained(kv8_append_kernel<T, D, kRows, 2>, grid, threads, ring, 1, p, st)
-                          : launch_chained(kv8_append_kernel<T, D, kRows, 1>, grid, threads, ring, 1, p, st);
+      if (p.rot < D)
+        return p.neighbours ? launch_norm<T, D, kRows, 2, true>(p, grid, threads, st)
+                            : launch_norm<T, D, kRows, 1, true>(p, grid, threads, st);
+      return p.neighbours ? launch_norm<T, D, kRows, 2, false>(p, grid, threads, st)
+                          : launch_norm<T, D, kRows, 1, false>(p, grid, threads, st);
     }
   }
-  return launch_chained(kv8_append_kernel<T, D, kRows, 0>, grid, threads, 0, 1, p, st);
+  return launch_chained(kv8_append_kernel<T, D, kRows, 0, true>, grid, threads, 0, 1, p, st);
 }
 
 template <typename T, int D>

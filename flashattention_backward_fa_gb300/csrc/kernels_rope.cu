@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const __
 
 // Each row group takes sd.span consecutive rows, as in the forward; its lanes
 // keep the weight gradients of their columns.
-template <typename T, int D, bool kNeighbours>
+template <typename T, int D, bool kNeighbours, bool kPartial>
 __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int G = D / 16, kGroups = kRopeThreads / G;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
   const long long rows = (long long)p.B * p.N * sd.H;
   const long long first = ((long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * kGroups + group) * sd.span;
   const int live = (int)min((long long)sd.span, max(rows - first, 0ll));
-  const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % G, p.rot);
+  const LanePlace at = lane_place<D, kNeighbours, kPartial>(threadIdx.x % G, p.rot);
   RowWalk wx;
   wx.start(first, p.N, sd.H, sd.x_st);
   RowWalk wg = wx.in(sd.out_st), wo = wx.in(sd.dx_st);
@@ -123,13 +123,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
       if (kNeighbours) {
         const uint64_t cj = f2_pack(c[j], c[j]), sj = f2_pack(s[j], -s[j]);
         const uint64_t ck = f2_pack(c[4 + j], c[4 + j]), sk = f2_pack(s[4 + j], -s[4 + j]);
-        ga[j] = f2_fma(ga[j], cj, f2_mul(f2_swap(ga[j]), sj));
-        gb[j] = f2_fma(gb[j], ck, f2_mul(f2_swap(gb[j]), sk));
+        ga[j] = f2_fma(ga[j], cj, f2_mul(f2_if(at.turn_a, f2_swap(ga[j])), sj));
+        gb[j] = f2_fma(gb[j], ck, f2_mul(f2_if(at.turn_b, f2_swap(gb[j])), sk));
       } else {
         const uint64_t cj = f2_pack(c[2 * j], c[2 * j + 1]), sj = f2_pack(s[2 * j], s[2 * j + 1]);
         const uint64_t nj = f2_pack(-s[2 * j], -s[2 * j + 1]);
-        const uint64_t da = f2_fma(ga[j], cj, f2_mul(gb[j], sj));
-        gb[j] = f2_fma(gb[j], cj, f2_mul(ga[j], nj));
+        const uint64_t da = f2_fma(ga[j], cj, f2_mul(f2_if(at.turn_a, gb[j]), sj));
+        gb[j] = f2_fma(gb[j], cj, f2_mul(f2_if(at.turn_a, ga[j]), nj));
         ga[j] = da;
       }
     }
@@ -343,15 +343,18 @@ cudaError_t launch_fwd(const RopeParams& p, cudaStream_t st) {
                       : launch_ring<norm_rope_fwd_kernel<T, 128, false>>(p, bytes, st);
 }
 
-template <typename T>
-cudaError_t launch_bwd(const RopeParams& p, cudaStream_t st) {
+template <typename T, int D, bool kPartial>
+cudaError_t launch_bwd_d(const RopeParams& p, cudaStream_t st) {
   constexpr int bytes = RowRing<T, 4, kBwdDepth>::bytes(kRopeThreads);
   static_assert(bytes >= kRopeThreads * 16 * 4, "the block's weight gradients fit into the ring");
-  if (p.d == 64)
-    return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, 64, true>>(p, bytes, st)
-                        : launch_ring<norm_rope_bwd_kernel<T, 64, false>>(p, bytes, st);
-  return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, 128, true>>(p, bytes, st)
-                      : launch_ring<norm_rope_bwd_kernel<T, 128, false>>(p, bytes, st);
+  return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, D, true, kPartial>>(p, bytes, st)
+                      : launch_ring<norm_rope_bwd_kernel<T, D, false, kPartial>>(p, bytes, st);
+}
+
+template <typename T>
+cudaError_t launch_bwd(const RopeParams& p, cudaStream_t st) {
+  if (p.d == 64) return p.rot < 64 ? launch_bwd_d<T, 64, true>(p, st) : launch_bwd_d<T, 64, false>(p, st);
+  return p.rot < 128 ? launch_bwd_d<T, 128, true>(p, st) : launch_bwd_d<T, 128, false>(p, st);
 }
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }

@@ -127,16 +127,22 @@ __device__ __forceinline__ void read4(const float* p, float* f) {
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
 }
 
-// First values of the two chunks of lane j of a row.
+// First values of the two chunks of lane j of a row, and which of them are rotated (both or none
+// where one chunk holds the other's partners). The others go through the same arithmetic with
+// cos = 1, sin = 0, and with 0 in the partner's place: an infinity or NaN times sin would reach a
+// value that it has nothing to do with. kPartial false: rot = D, all are rotated and nothing is
+// put in place. (Zeros by selects where needed or not took the backward at bf16 4x16x2048x128
+// 0.5 us and the append with norm 0.8 us more; a branch around the rotation 2.7 us more there.)
 struct LanePlace {
   int a, b;
+  bool turn_a, turn_b;
 };
-template <int D, bool kNeighbours>
+template <int D, bool kNeighbours, bool kPartial>
 __device__ __forceinline__ LanePlace lane_place(int j, int rot) {
-  if (kNeighbours) return {8 * j, 8 * j + D / 2};
+  if (kNeighbours) return {8 * j, 8 * j + D / 2, !kPartial || 8 * j < rot, !kPartial || 8 * j + D / 2 < rot};
   const int pairs = rot >> 4;  // lanes that hold rotated values
-  if (j < pairs) return {8 * j, 8 * j + (rot >> 1)};
-  return {rot + 16 * (j - pairs), rot + 16 * (j - pairs) + 8};
+  if (!kPartial || j < pairs) return {8 * j, 8 * j + (rot >> 1), true, true};
+  return {rot + 16 * (j - pairs), rot + 16 * (j - pairs) + 8, false, false};
 }
 
 // cos and sin of a lane's eight pairs (a token's table rows hold rot / 2 values each): pairs
@@ -163,6 +169,13 @@ __device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);
   return f2_pack(hi, lo);
+}
+
+// v, or zeros.
+__device__ __forceinline__ uint64_t f2_if(bool yes, uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return f2_pack(yes ? lo : 0.f, yes ? hi : 0.f);
 }
 
 __device__ __forceinline__ void read_pairs(const float* p, uint64_t (&f)[4]) {
@@ -198,8 +211,8 @@ __device__ __forceinline__ float inv_sqrt(float x) {
 
 // Forward of a lane's 16 values, in place; every lane of the warp calls it (shuffles).
 template <typename T, int D, bool kNeighbours>
-__device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const LaneWeights& w, const float (&c)[8],
-                                               const float (&s)[8], float eps) {
+__device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const LanePlace& at, const LaneWeights& w,
+                                               const float (&c)[8], const float (&s)[8], float eps) {
   uint64_t a[4], b[4];
   ra.unpack(a);
   rb.unpack(b);
@@ -216,13 +229,18 @@ __device__ __forceinline__ void norm_rope_lane(Raw8<T>& ra, Raw8<T>& rb, const L
   for (int i = 0; i < 4; ++i) {
     a[i] = f2_mul(a[i], f2_mul(r, w.a[i]));
     b[i] = f2_mul(b[i], f2_mul(r, w.b[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     if (kNeighbours) {
-      a[i] = f2_fma(a[i], f2_pack(c[i], c[i]), f2_mul(f2_swap(a[i]), f2_pack(-s[i], s[i])));
-      b[i] = f2_fma(b[i], f2_pack(c[4 + i], c[4 + i]), f2_mul(f2_swap(b[i]), f2_pack(-s[4 + i], s[4 + i])));
+      a[i] = f2_fma(a[i], f2_pack(c[i], c[i]), f2_mul(f2_if(at.turn_a, f2_swap(a[i])), f2_pack(-s[i], s[i])));
+      b[i] = f2_fma(b[i], f2_pack(c[4 + i], c[4 + i]),
+                    f2_mul(f2_if(at.turn_b, f2_swap(b[i])), f2_pack(-s[4 + i], s[4 + i])));
     } else {
       const uint64_t ci = f2_pack(c[2 * i], c[2 * i + 1]), si = f2_pack(s[2 * i], s[2 * i + 1]);
-      const uint64_t oa = f2_fma(a[i], ci, f2_mul(b[i], f2_pack(-s[2 * i], -s[2 * i + 1])));
-      b[i] = f2_fma(b[i], ci, f2_mul(a[i], si));
+      const uint64_t ni = f2_pack(-s[2 * i], -s[2 * i + 1]);
+      const uint64_t oa = f2_fma(a[i], ci, f2_mul(f2_if(at.turn_a, b[i]), ni));
+      b[i] = f2_fma(b[i], ci, f2_mul(f2_if(at.turn_a, a[i]), si));
       a[i] = oa;
     }
   }
@@ -318,7 +336,7 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
                                                const float* cos, const float* sin, int rot, float eps,
                                                const TableAt& table_at) {
   RowRing<T, 2, kDepth> ring(smem);
-  const LanePlace at = lane_place<D, kNeighbours>(threadIdx.x % (D / 16), rot);
+  const LanePlace at = lane_place<D, kNeighbours, true>(threadIdx.x % (D / 16), rot);  // (costs nothing here)
   const int live = (int)min((long long)count, max(rows - first, 0ll));
   RowWalk in;
   in.start(first, N, H, x_st);
@@ -361,7 +379,7 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
     ring.take(0, a);
     ring.take(1, b);
     ring.step(ring.got);
-    norm_rope_lane<T, D, kNeighbours>(a, b, lw, c, s, eps);
+    norm_rope_lane<T, D, kNeighbours>(a, b, at, lw, c, s, eps);
     if (i < live) {
       T* p = out + to.at;
       store8(a, p);
