@@ -27,6 +27,10 @@ cudaError_t allow_smem(int bytes) {
 // Launches a kernel whose blocks may take their places while the kernel before it in the stream
 // ends (sooner where that one calls let_next_begin). Each of them waits for that kernel's end
 // (wait_for_previous) before it touches memory; towards other kernels this is an ordinary launch.
+// What such a kernel reads may have been written while its first blocks were already there, so it is
+// not read-only for the kernel's lifetime: no __ldg (ld.global.nc) and no const __restrict__ there,
+// but ordinary loads or cp.async, at the same times (with __ldcg, which the compiler does not move,
+// for the rows the append took 33.1 us instead of 30.5 us).
 // Between two of these kernels it saves 1 to 3 us: bf16 norm and rotation 1x32x8192x128 46.9 ->
 // 44.2 us, append 32.8 -> 30.6 us, 100 tokens of attention 6.2 -> 5.5 us. cluster > 1: blocks of a
 // cluster along x.

@@ -125,8 +125,8 @@ struct NewTokens {
 
 __device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T) {
   NewTokens n;
-  n.count = c.new_lens ? min(max(__ldg(c.new_lens + b), 0), T) : T;
-  n.len = max(__ldg(c.seq_lens + b), 0);
+  n.count = c.new_lens ? min(max(c.new_lens[b], 0), T) : T;
+  n.len = max(c.seq_lens[b], 0);
   n.start = n.len - n.count;
   return n;
 }
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
   }
   if (rows <= 0) return;
   // (checked once the rows' loads are under way)
-  const int id = is_q ? 0 : __ldg(c.table + b * c.table_stride + pg);
+  const int id = is_q ? 0 : c.table[b * c.table_stride + pg];
   // Row groups beside each other: rows of the page, or, with few tokens, q's further heads.
   const int groups = blockDim.x / G;
   int row0 = threadIdx.x / G, beside = 1, head = 0;

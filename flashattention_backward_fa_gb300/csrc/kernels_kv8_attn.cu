@@ -155,8 +155,8 @@ struct Range {
 
 __device__ __forceinline__ Range key_range(const Kv8AttnParams& p, int b, int row_lo, int row_hi) {
   Range r;
-  r.len = max(__ldg(p.c.seq_lens + b), 0);
-  r.count = p.c.new_lens ? min(max(__ldg(p.c.new_lens + b), 0), p.T) : p.T;
+  r.len = max(p.c.seq_lens[b], 0);
+  r.count = p.c.new_lens ? min(max(p.c.new_lens[b], 0), p.T) : p.T;
   r.keys = min(r.len, p.key_limit);
   // rows [row_lo, row_hi) hold tokens t_lo .. t_hi at positions len - count + t
   const int t_lo = max(row_lo / p.G, r.count - r.len), t_hi = min((row_hi - 1) / p.G, r.count - 1);
@@ -176,7 +176,7 @@ __device__ __forceinline__ int sequence_of(const Kv8AttnParams& p, int place, in
   static_assert(kThreads == 128, "a number takes 7 bits");
   __shared__ int found;
   const int me = threadIdx.x;
-  const int mine = me < p.B ? min(max(__ldg(p.c.seq_lens + me), 0), (1 << 24) - 1) * kThreads + kThreads - 1 - me : -1;
+  const int mine = me < p.B ? min(max(p.c.seq_lens[me], 0), (1 << 24) - 1) * kThreads + kThreads - 1 - me : -1;
   ranks[me] = mine;
   __syncthreads();
   int before = 0;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   auto pages_of = [&](int key) {
     Pages pg;
 #pragma unroll
-    for (int u = 0; u < U; ++u) pg.id[u] = key + kTile * u < end ? __ldg(table + ((key + kTile * u) >> shift)) : -1;
+    for (int u = 0; u < U; ++u) pg.id[u] = key + kTile * u < end ? table[(key + kTile * u) >> shift] : -1;
     return pg;
   };
   auto fetch = [&](const Pages& pg) {
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
     float x[KQ][8], top = 0.f;
 #pragma unroll
     for (int i = 0; i < KQ; ++i) {
-      const uint4 raw = live ? __ldg(reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 16 * c + 8 * (i & 1)))
+      const uint4 raw = live ? *reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 16 * c + 8 * (i & 1))
                              : make_uint4(0u, 0u, 0u, 0u);
       unpack2<kBf16>(raw.x, x[i][0], x[i][1]);
       unpack2<kBf16>(raw.y, x[i][2], x[i][3]);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       pos[nt][e] = kr.len - kr.count + t;
       const bool live = row < R && t < kr.count && pos[nt][e] >= 0;
       if (!live) pos[nt][e] = -1;
-      slope[nt][e] = live && p.alibi ? __ldg(p.alibi + b * p.alibi_sb + h * p.G + row % p.G) * 1.4426950408889634f : 0.f;
+      slope[nt][e] = live && p.alibi ? p.alibi[b * p.alibi_sb + h * p.G + row % p.G] * 1.4426950408889634f : 0.f;
       m[nt][e] = mv[nt][e] = kNoMax;
       l[nt][e] = 0.f;
     }

@@ -31,7 +31,7 @@ constexpr int kBwdBlocks = 152 * 2;   // one resident set: every block adds a ro
 
 // The token's rows in the tables: its position, clamped into them.
 __device__ __forceinline__ long long table_row(const RopeParams& p, long long b, int n) {
-  const int pos = p.positions ? __ldg(p.positions + b * p.pos_stride + n) : n;
+  const int pos = p.positions ? p.positions[b * p.pos_stride + n] : n;
   return (long long)min(max(pos, 0), p.max_pos - 1) * (p.rot >> 1);
 }
 

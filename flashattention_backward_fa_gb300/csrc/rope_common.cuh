@@ -84,7 +84,7 @@ struct Raw8<float> {
 template <typename T>
 __device__ __forceinline__ void load8(Raw8<T>& v, const T* p) {
 #pragma unroll
-  for (int i = 0; i < Raw8<T>::kQuads; ++i) v.q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  for (int i = 0; i < Raw8<T>::kQuads; ++i) v.q[i] = reinterpret_cast<const uint4*>(p)[i];
 }
 template <typename T>
 __device__ __forceinline__ void store8(const Raw8<T>& v, T* p) {
