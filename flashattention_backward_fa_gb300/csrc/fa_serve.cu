@@ -182,8 +182,9 @@ int check_attn(int B, int T, int Hq, int H, int d, int page_size, int max_pages,
   if (window < 0 || Hq % H != 0) return FA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || page_size < 16 || page_size > 128 || (page_size & (page_size - 1)))
     return FA_ERR_UNSUPPORTED;
-  if (B > 65535 || H > 1024 || Hq > (1 << 16) || T > (1 << 24)) return FA_ERR_UNSUPPORTED;
-  if ((long long)H * (((long long)T * (Hq / H) + 7) / 8) > 65535) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || H > 1024 || Hq > (1 << 16) || T > (1 << 19)) return FA_ERR_UNSUPPORTED;
+  // rows, and the blocks of a sequence (the grid's x extent), are counted in 31 bits
+  if ((long long)T * Hq > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if ((long long)max_pages * page_size > (1 << 30)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }

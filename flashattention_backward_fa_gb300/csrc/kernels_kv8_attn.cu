@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   const uint32_t ring = smem_u32(dyn);
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-  const int h = blockIdx.y % p.c.H, rt = blockIdx.y / p.c.H, R = p.T * p.G;
+  // blocks: splits fastest, then heads, then row tiles (x has room for any number of them), then sequences
+  const int split = blockIdx.x % p.splits, unit = blockIdx.x / p.splits;
+  const int h = unit % p.c.H, rt = unit / p.c.H, R = p.T * p.G;
   const int row0 = rt * kRows;
   // (and no let_next_begin here: blocks of the next call would take the places of this one's; the
   // call at 131071 tokens took 57 us with it at the start, 51.4 us at the end, 51.2 us without)
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   const int b = p.longest_first ? sequence_of(p, blockIdx.z, reinterpret_cast<int*>(q_frag)) : blockIdx.z;
   const Range kr = key_range(p, b, row0, min(row0 + kRows, R));
   const int chunk = split_keys(p, kr);
-  const int begin = kr.lo + blockIdx.x * chunk, end = min(kr.hi, begin + chunk);
+  const int begin = kr.lo + split * chunk, end = min(kr.hi, begin + chunk);
   // (the joining kernel counts splits the same way; the blocks of a cluster all come along)
   if (begin >= end && p.splits > 1 && !p.cluster) return;
 
@@ -764,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       *reinterpret_cast<uint2*>(out(row, x)) = make_uint2(pack2<kBf16>(v.x, v.y), pack2<kBf16>(v.z, v.w));
       if (x == 0) out_lse(row, block_lse[row]);
     } else {
-      const long long to = (((long long)b * p.c.H + h) * R + row0 + row) * p.splits + blockIdx.x;
+      const long long to = (((long long)b * p.c.H + h) * R + row0 + row) * p.splits + split;
       *reinterpret_cast<float4*>(p.part_o + to * D + 4 * x) = v;
       if (x == 0) p.part_lse[to] = block_lse[row];
     }
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
   // Each block of the cluster joins its share of the items from all of them.
   cluster_sync();
   const int n = p.splits;
-  for (int item = blockIdx.x * kThreads + threadIdx.x; item < items; item += n * kThreads) {
+  for (int item = split * kThreads + threadIdx.x; item < items; item += n * kThreads) {
     const int row = item / (D / 4), x = item % (D / 4);
     float part[kMaxCluster], top = -INFINITY;
     float4 o[kMaxCluster];
@@ -891,7 +893,8 @@ cudaError_t launch_nt(const Kv8AttnParams& p, cudaStream_t st) {
   constexpr int kBytes = Ring<D>::kBytes;
   cudaError_t e = allow_smem<kKernel>(kBytes);
   if (e != cudaSuccess) return e;
-  e = launch_chained(kKernel, dim3(p.splits, p.c.H * p.row_tiles, p.B), kThreads, kBytes, p.cluster ? p.splits : 1, p, st);
+  const dim3 grid(p.splits * p.c.H * p.row_tiles, 1, p.B);
+  e = launch_chained(kKernel, grid, kThreads, kBytes, p.cluster ? p.splits : 1, p, st);
   if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
   return launch_chained(kv8_join_kernel<T, D, NT>, dim3(p.T * p.G, p.c.H, p.B), 32 * kJoinWarps, 0, 1, p, st);
 }

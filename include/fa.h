@@ -411,7 +411,8 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * for the same sizes; its contents on entry do not matter. The size is 0 where
  * the call needs none (workspace may then be null) and for sizes that the call
  * refuses; calls that overlap on the GPU need workspaces of their own. o must
- * not overlap q. The same inputs give the same bits on every run. */
+ * not overlap q. The same inputs give the same bits on every run. T <= 2^19,
+ * Hq <= 2^16, T * Hq <= 2^30. */
 size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,
                                   int causal, int window);
 int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, void* o, float* lse, int T, int Hq,

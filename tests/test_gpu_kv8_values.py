@@ -223,3 +223,34 @@ def test_rising_and_falling_scores_with_changing_scales():
             q = torch.zeros(1, 2, 2, d, dtype=dtype, device="cuda")
             q[..., 0] = 1.0
             _check(q, cache, table, [n])
+
+
+@pytest.mark.parametrize("T,Hq,H,window", [(32777, 16, 16, 40), (16385, 64, 1, 33)])
+def test_more_row_tiles_than_16_bits_count(T, Hq, H, window):
+    """A whole prompt's queries in one call: 65556 and 65540 row tiles; rows at both ends and between."""
+    g = torch.Generator().manual_seed(103)
+    page, d, n = 128, 64, T + 5
+    pages = -(-n // page)
+    k, v = (torch.randn(1, n, H, d, generator=g).to(BF16) for _ in range(2))
+    table = torch.randperm(pages, generator=g)[None].int()
+    cache = _cache(k, v, page, table)
+    q = torch.randn(1, T, Hq, d, generator=g).to(BF16)
+    o, lse = fa.kv8_attention(q.cuda(), cache, _cu(table), _cu([n]), n, scale=0.1, window=window)
+    o, lse = ref.f64(o), ref.f64(lse)
+    at = table[0].long()
+    k, v = ((ref.f64(c.float())[at] * ref.f64(s)[at][:, None, :, None]).flatten(0, 1)
+            for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    for t in [0, 1, 15, 16, 17, T // 3, T // 2 + 1, T - 18, T - 17, T - 2, T - 1]:
+        i = n - T + t
+        keys = slice(max(0, i - window + 1), i + 1)
+        for hq in (0, Hq // 2, Hq - 1):
+            h = hq // (Hq // H)
+            kk, vv, qq = k[keys, h], v[keys, h], ref.f64(q[0, t, hq])
+            s = kk @ qq * 0.1
+            p = s.softmax(0)
+            delta = (d + 8) * 2.0 ** -23 * 0.1 * float((kk.abs() @ qq.abs()).max()) + 64 * 2.0 ** -24 + \
+                2.0 ** -21 * 0.1 * float(qq.abs().max() * kk.abs().sum(-1).max())
+            want, size = p @ vv, p @ vv.abs()
+            bound = 2.0 ** -8 * want.abs() * (1 + 2.0 ** -6) + size * (2 * delta + 2.0 ** -11 + 128 * 2.0 ** -23)
+            assert bool(((o[0, t, hq] - want).abs() <= bound).all()), (t, hq)
+            assert abs(float(lse[0, hq, t] - s.logsumexp(0))) <= delta + 2.0 ** -16 + 2.0 ** -22 * 8
