@@ -18,9 +18,11 @@
 // * K's codes enter the e4m3 instruction (k32, measured at 0.94 a clock and SM,
 //   four times the f16 rate, sums exact to fp32) as they are. The queries are
 //   divided by a power of two of each row and written as two (bf16) or three (f16)
-//   e4m3 pieces, each the rounding error of those before it times 16: exact down
-//   to 2^-22 (2^-26) of the row's largest value. Widening K to f16 instead took
-//   48 more ALU operations a step, at 2 a clock and SM.
+//   e4m3 pieces, each the rounding error of those before it times 16. The largest
+//   value of a row is brought to [2^7, 2^8) and the pieces end at 2^-13 (2^-17), so a
+//   query is exact where its bits end at 2^-20 (2^-24) of the row's largest value, and
+//   else off by at most 2^-21 (2^-25) of it. Widening K to f16 instead took 48 more ALU
+//   operations a step, at 2 a clock and SM.
 // * V's codes are widened to f16 (exact) for the f16 instruction, because the
 //   weights P need its range: an e4m3 piece ends 2^-18 below the largest weight,
 //   and a long sequence can hold most of its mass below that.
@@ -34,6 +36,11 @@
 //   warps agree on new ones a few times a sequence and vote otherwise. P is rounded to
 //   f16 (2^-11 of itself, or 2^-32 of the row's largest below 2^-21 of it); for f16
 //   outputs, whose own rounding is no larger, its rounding residual is multiplied too.
+//   bf16 outputs are rounded by 2^-8 of themselves: with the residual their error
+//   against 64 bits is the same to two digits (1.6e-3), and one to five percent of the
+//   time more (32 sequences of up to 16384 tokens 100.5 us against 98.7 us, 128 of up to
+//   500 tokens 26.6 us against 25.2 us), with two row tiles an eighth (16 sequences of
+//   8192 tokens with 16 rows a key head 75.3 us against 66.8 us).
 // * Four warps take steps of 32 keys (two tiles, whose chains of instructions
 //   overlap) in turn. The next step is on its way to the warp's own part of shared
 //   memory (cp.async), so a warp waits for itself alone, and 96 KB an SM are in
@@ -425,10 +432,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(con
       for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
   __syncthreads();
   // One row tile: two pieces of the queries stay in registers, f16's third one is read from shared
-  // memory at its use. With all three held the f16 form spilled in the loop (d = 128, 32 sequences
-  // of up to 4096 tokens, 32 heads: 132 us against 103 us), with one of bf16's two in shared memory
-  // 32 sequences of up to 16384 tokens took 102 us against 100 us. Two row tiles have no
-  // register to spare.
+  // memory at its use. With all three held the f16 form spilled more in the loop (d = 128, 32
+  // sequences of up to 4096 tokens, 32 heads: 132 us against 103 us), with one of bf16's two in
+  // shared memory 32 sequences of up to 16384 tokens took 102 us against 100 us. Two row tiles have
+  // no register to spare. (At d = 128 f16 still spills 20 bytes at 168 registers and, with two row
+  // tiles, 48 bytes at 255; bf16 with two row tiles 16.)
   constexpr int kHeld = NT == 1 ? 2 : 0;
   uint2 q_reg[NT == 1 ? KQ : 1][NP];
 #pragma unroll

@@ -343,7 +343,8 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
  * p * strides.b + t * strides.n + h * strides.h + i (strides multiples of 16,
  * bases 16-byte aligned; [num_pages, page_size, H, d] and [num_pages, H,
  * page_size, d] storage are both expressible, the second reads fastest), and
- * stand for code * scale with k_scale, v_scale contiguous fp32 [num_pages, H].
+ * stand for code * scale with k_scale, v_scale contiguous fp32 [num_pages, H],
+ * finite and not negative.
  *
  * Sequences: sequence b has seq_lens[b] tokens (device int32 [B]); its token j
  * is in page block_table[b * table_stride + j / page_size] (device int32,
@@ -412,7 +413,11 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * the call needs none (workspace may then be null) and for sizes that the call
  * refuses; calls that overlap on the GPU need workspaces of their own. o must
  * not overlap q. The same inputs give the same bits on every run. T <= 2^19,
- * Hq <= 2^16, T * Hq <= 2^30. */
+ * Hq <= 2^16, T * Hq <= 2^30.
+ * Scores, softmax sums and outputs are held in fp32. Held in fewer bits: q, off
+ * by at most 2^-21 (bf16) or 2^-25 (fp16) of the largest value of its row; the
+ * products of a weight and its page's V scale, off by at most 2^-11 (bf16) or
+ * 2^-22 (fp16) of themselves, or by 2^-32 of the row's largest such product. */
 size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,
                                   int causal, int window);
 int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, void* o, float* lse, int T, int Hq,

@@ -225,6 +225,22 @@ def test_rising_and_falling_scores_with_changing_scales():
             _check(q, cache, table, [n])
 
 
+@pytest.mark.parametrize("outlier", [2.0 ** 6, 2.0 ** 12, 2.0 ** 16])
+def test_an_outlier_channel_of_the_queries(outlier):
+    """One channel of q far above the others, where the keys are small: what the pieces of the others lose
+    stays within the stated share of the largest."""
+    g = torch.Generator().manual_seed(107)
+    page, d, n = 32, 128, 300
+    table = torch.randperm(10, generator=g)[None].int()
+    for dtype in (BF16, F16):
+        k = torch.randn(1, n, 2, d, generator=g)
+        k[..., 77] *= 2.0 ** -9
+        q = torch.randn(1, 2, 8, d, generator=g)
+        q[..., 77] = outlier * 0.9 * torch.sign(q[..., 77])
+        cache = _cache(k.to(dtype), torch.randn(1, n, 2, d, generator=g).to(dtype), page, table)
+        _check(q.to(dtype).cuda(), cache, table, [n], scale=0.09)
+
+
 @pytest.mark.parametrize("T,Hq,H,window", [(32777, 16, 16, 40), (16385, 64, 1, 33)])
 def test_more_row_tiles_than_16_bits_count(T, Hq, H, window):
     """A whole prompt's queries in one call: 65556 and 65540 row tiles; rows at both ends and between."""
