@@ -754,6 +754,8 @@ def _readable(t: torch.Tensor) -> torch.Tensor:
     """A gradient as the kernels read it: a copy where its strides (an expanded one's zeros,
     unaligned rows) or its base do not allow reading it in place."""
     s = t.stride()
+    if len(s) != 4:
+        return t  # refused by the call's own checks
     unit = 8 if t.element_size() == 2 else 1
     if s[3] != 1 or min(s) < 1 or any(x % unit for x in s[:3]) or t.data_ptr() % 16:
         return t.clone(memory_format=torch.contiguous_format)

@@ -407,8 +407,8 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * m |i - j| with optional ALiBi slopes as for fa_fwd_alibi (m =
  * alibi_slopes[b * alibi_stride_b + hq]). A row without keys, and a padding
  * row, gets O = 0 and lse = -inf. A NaN in k or v reaches only the rows that
- * attend to its token. max_seqlen: an upper bound of seq_lens (it sizes the
- * launch). `workspace`: 256-byte aligned, fa_kv8_attn_workspace_size(...) bytes
+ * attend to its token. max_seqlen: an upper bound of seq_lens, at least 1 (it
+ * sizes the launch). `workspace`: 256-byte aligned, fa_kv8_attn_workspace_size(...) bytes
  * for the same sizes; its contents on entry do not matter. The size is 0 where
  * the call needs none (workspace may then be null) and for sizes that the call
  * refuses; calls that overlap on the GPU need workspaces of their own. o must

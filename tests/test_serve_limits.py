@@ -1,5 +1,7 @@
-"""Limits of the cache calls that the header states, on the CPU: sizes up to them are not refused."""
+"""Limits of the norm-and-rotation and cache calls, on the CPU: what is refused, and that sizes up to the
+header's limits are not."""
 import pytest
+import torch
 
 import flashattention_backward_fa_gb300 as fa
 from flashattention_backward_fa_gb300 import binding
@@ -29,3 +31,10 @@ def test_attention_takes_any_prompt_up_to_the_stated_limits(lib, T, Hq, H):  # n
                                     (1, (1 << 16) + 1, 1)])
 def test_attention_refuses_more(lib, T, Hq, H):  # noqa: F811
     assert _attn(lib, T, Hq, H) == EUNSUP
+
+
+@pytest.mark.parametrize("shape", [(4, 64), (2, 4, 64), (1, 2, 4, 8, 64)])
+def test_autograd_call_names_what_is_wrong_with_the_shape(shape):
+    x = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        fa.qk_norm_rope_func(x, x)
