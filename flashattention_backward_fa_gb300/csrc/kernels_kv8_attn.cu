@@ -34,13 +34,14 @@
 //   attend to has no say in its mv. A reference moves only when it is exceeded by 2^15
 //   (P is then at most 2^15, inside f16), and is set so that the largest P is 2^7, so
 //   warps agree on new ones a few times a sequence and vote otherwise. P is rounded to
-//   f16 (2^-11 of itself, or 2^-32 of the row's largest below 2^-21 of it); for f16
-//   outputs, whose own rounding is no larger, its rounding residual is multiplied too.
-//   bf16 outputs are rounded by 2^-8 of themselves: with the residual their error
-//   against 64 bits is the same to two digits (1.6e-3), and one to five percent of the
-//   time more (32 sequences of up to 16384 tokens 100.5 us against 98.7 us, 128 of up to
-//   500 tokens 26.6 us against 25.2 us), with two row tiles an eighth (16 sequences of
-//   8192 tokens with 16 rows a key head 75.3 us against 66.8 us).
+//   f16 (2^-11 of itself, or 2^-32 of the row's largest below 2^-21 of it), and its
+//   rounding residual is multiplied too (then 2^-22). bf16 outputs with two row tiles go
+//   without the residual: their own rounding is 2^-8, the error against 64 bits the same
+//   to two digits (1.6e-3), and the products bound that form (16 sequences of 8192 tokens
+//   with 16 rows a key head 75.3 us with it, 66.8 us without). With one row tile, which
+//   the cache's bytes bound, it costs 1 to 5% (32 sequences of up to 16384 tokens 100.5 us
+//   against 98.7 us, 128 of up to 500 tokens 26.6 us against 25.2 us) and brings the
+//   outputs to those of 32-bit weights but for 1e-5 to 7e-5 (5e-4 to 9e-4 without).
 // * Four warps take steps of 32 keys (two tiles, whose chains of instructions
 //   overlap) in turn. The next step is on its way to the warp's own part of shared
 //   memory (cp.async), so a warp waits for itself alone, and 96 KB an SM are in
@@ -290,7 +291,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) kv8_attn_kernel(const __grid_constant__ Kv8AttnParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr bool kResidual = !kBf16;   // see the head of the file
+  constexpr bool kResidual = !kBf16 || NT == 1;  // see the head of the file
   constexpr int NP = kBf16 ? 2 : 3;    // e4m3 pieces of a query
   constexpr int KS = D / 16;           // row tiles of O^T
   constexpr int KQ = D / 32;           // instructions over the head dimension (S)

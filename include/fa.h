@@ -416,8 +416,8 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * Hq <= 2^16, T * Hq <= 2^30.
  * Scores, softmax sums and outputs are held in fp32. Held in fewer bits: q, off
  * by at most 2^-21 (bf16) or 2^-25 (fp16) of the largest value of its row; the
- * products of a weight and its page's V scale, off by at most 2^-11 (bf16) or
- * 2^-22 (fp16) of themselves, or by 2^-32 of the row's largest such product. */
+ * products of a weight and its page's V scale, off by at most 2^-22 of themselves
+ * (bf16 with T * Hq / H > 8: 2^-11), or by 2^-32 of the row's largest such product. */
 size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,
                                   int causal, int window);
 int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, void* o, float* lse, int T, int Hq,

@@ -6,7 +6,7 @@ by (d + 8) * 2^-23 * A (fp32 sums) + 64 * 2^-24 (ex2.approx, |s - m| < 64 where 
 query's e4m3 pieces leave, at most 2^-21 (bf16, two pieces) or 2^-25 (f16, three) of its largest value:
 Q = |scale| * max|q| * max_j sum_i |k_ji| of it. Together delta; a weight is off by 2 delta relative (its
 own, and the sum's). Its product with the page's scale s_j is rounded to f16 (half a step: 2^-11 relative,
-with its residual 2^-22) in units in which the largest p_j s_j of a warp is at least 2^7, so products below 2^-14 of
+with its residual 2^-22; bf16 has the residual up to eight rows a key head) in units in which the largest p_j s_j of a warp is at least 2^7, so products below 2^-14 of
 the unit lose up to 2^-25 of it: 2^-32 of the largest p_j s_j, times a code of at most 448. n keys are
 summed in fp32: (n + 64) * 2^-23. The output is rounded to its type.
 """
@@ -23,7 +23,7 @@ pytestmark = pytest.mark.gpu
 BF16, F16 = torch.bfloat16, torch.float16
 HALF = {BF16: 2.0 ** -8, F16: 2.0 ** -11}     # half a step of the type, relative to the value
 TINY = {BF16: 2.0 ** -126, F16: 2.0 ** -25}   # half a step of f16's subnormals; fp32's may count as zero
-WEIGHT = {BF16: 2.0 ** -11, F16: 2.0 ** -22}
+RESIDUAL_ROWS = {BF16: 8, F16: 1 << 30}       # most rows (tokens x query heads) of a key head with the residual
 PIECES = {BF16: 2.0 ** -21, F16: 2.0 ** -25}
 
 
@@ -61,7 +61,8 @@ def _check(q, cache, table, lens, new=None, scale=1.0, causal=True, window=0):
             delta = (d + 8) * 2.0 ** -23 * A + 64 * 2.0 ** -24 + PIECES[dtype] * Q
             want, size = p @ v[:, h], p @ v[:, h].abs()
             most = (p * unit[:, h]).amax(-1)
-            rel = 2 * delta + WEIGHT[dtype] + (n + 64) * 2.0 ** -23
+            weight = 2.0 ** -22 if T * (Hq // H) <= RESIDUAL_ROWS[dtype] else 2.0 ** -11
+            rel = 2 * delta + weight + (n + 64) * 2.0 ** -23
             bound = HALF[dtype] * want.abs() * (1 + 2.0 ** -6) + size * rel[:, None] + \
                 (n * 448 * 2.0 ** -32 * most)[:, None] + TINY[dtype]
             err = (got[b, :count, hq] - want).abs()
@@ -223,6 +224,22 @@ def test_rising_and_falling_scores_with_changing_scales():
             q = torch.zeros(1, 2, 2, d, dtype=dtype, device="cuda")
             q[..., 0] = 1.0
             _check(q, cache, table, [n])
+
+
+@pytest.mark.parametrize("Hq,T", [(1, 1), (4, 2), (8, 1), (4, 5)])
+@pytest.mark.parametrize("n", [2, 16, 100, 3000])
+def test_values_that_cancel(n, Hq, T):
+    """Outputs far smaller than the values: a weight's rounding to f16 alone would show beside the output's."""
+    g = torch.Generator().manual_seed(109)
+    page, d = 16, 128
+    sign = torch.ones(n) - 2 * (torch.arange(n) % 2)
+    for dtype in (BF16, F16):
+        k = torch.randn(1, n, 1, d, generator=g)
+        v = sign[None, :, None, None] * (1 + torch.randint(0, 2, (1, n, 1, d), generator=g) / 8)
+        table = torch.randperm(-(-n // page), generator=g)[None].int()
+        cache = _cache(k.to(dtype), v.to(dtype), page, table)
+        q = (torch.randn(1, T, Hq, d, generator=g) * 0.02).to(dtype).cuda()
+        _check(q, cache, table, [n], new=[min(T, n)], scale=0.3)
 
 
 @pytest.mark.parametrize("outlier", [2.0 ** 6, 2.0 ** 12, 2.0 ** 16])
