@@ -60,6 +60,11 @@ class _Kv8SeqsArg(ctypes.Structure):
                 ("new_lens", ctypes.c_void_p), ("B", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
+class _CrossShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Nq", ctypes.c_int), ("Nk", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("d", ctypes.c_int), ("q_lens", ctypes.c_void_p), ("k_lens", ctypes.c_void_p)]
+
+
 class FaError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"{ERROR_CODES.get(code, code)}: {msg}")
@@ -131,6 +136,13 @@ def load_library(path: str = LIB_PATH):
     lib.fa_kv8_attn_workspace_size.restype = sz
     lib.fa_kv8_attn.argtypes = [cache, seqs, vp, vp, vp, i, i, i, st, st, i, f, i, i, vp, i64, vp, sz, vp]
     lib.fa_kv8_attn.restype = i
+    shape = ctypes.POINTER(_CrossShape)
+    lib.fa_cross_fwd_workspace_size.argtypes, lib.fa_cross_fwd_workspace_size.restype = [shape, i], sz
+    lib.fa_cross_bwd_workspace_size.argtypes, lib.fa_cross_bwd_workspace_size.restype = [shape, i], sz
+    lib.fa_cross_fwd.argtypes = [shape] + [vp] * 5 + [st] * 4 + [i, f, vp, sz, vp]
+    lib.fa_cross_fwd.restype = i
+    lib.fa_cross_bwd.argtypes = [shape] + [vp] * 9 + [st] * 8 + [i, f, vp, sz, vp]
+    lib.fa_cross_bwd.restype = i
     _lib = lib
     return lib
 
@@ -769,6 +781,144 @@ def qk_norm_rope_func(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     flash_attn_func takes them. Gradients reach q, k and the weights."""
     return _QkNormRopeFunc.apply(_readable(q), _readable(k), q_weight, k_weight, cos, sin, positions, float(eps),
                                  bool(interleaved))
+
+
+# ------------------------------- cross attention -------------------------------
+@lru_cache(maxsize=1024)
+def _cross_workspace(backward: bool, B: int, Nq: int, Nk: int, Hq: int, Hk: int, d: int, code: int) -> int:
+    lib = _lib or load_library()
+    size = lib.fa_cross_bwd_workspace_size if backward else lib.fa_cross_fwd_workspace_size
+    return size(_CrossShape(B, Nq, Nk, Hq, Hk, d), code)
+
+
+def fa_cross_fwd_workspace_size(B: int, Nq: int, Nk: int, Hq: int, Hk: int, d: int, dtype) -> int:
+    return _cross_workspace(False, B, Nq, Nk, Hq, Hk, d, _TORCH_TO_FA[dtype])
+
+
+def fa_cross_bwd_workspace_size(B: int, Nq: int, Nk: int, Hq: int, Hk: int, d: int, dtype) -> int:
+    return _cross_workspace(True, B, Nq, Nk, Hq, Hk, d, _TORCH_TO_FA[dtype])
+
+
+def _cross_shape(q, k, q_lens, k_lens):
+    """(the C struct, q's shape, k's shape, dtype, device index) of queries and keys that go together."""
+    shape, dtype, dev = _new_tensor(q, "q")
+    B, Nq, Hq, d = shape
+    kshape = k.shape
+    if len(kshape) != 4 or kshape[0] != B or kshape[3] != d:
+        raise ValueError(f"k must be [{B}, Nk, Hk, {d}] as q is {list(shape)}")
+    return (_CrossShape(B, Nq, kshape[1], Hq, kshape[2], d, _int32(q_lens, (B,), dev, "q_lens"),
+                        _int32(k_lens, (B,), dev, "k_lens")), shape, kshape, dtype, dev)
+
+
+def _lse(lse, shape, dev: int):
+    B, N, H, _ = shape
+    if lse.dtype is not torch.float32 or lse.shape != (B, H, N) or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError(f"lse must be a contiguous float32 [B, Hq, Nq] tensor on cuda:{dev}")
+    return lse.data_ptr()
+
+
+def _workspace_arg(workspace, dev: int):
+    """(pointer, bytes) of the caller's workspace (None passes through)."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _cross_fwd(q, k, v, o, lse, workspace, q_lens, k_lens, scale, stream):
+    c, shape, kshape, dtype, dev = _cross_shape(q, k, q_lens, k_lens)
+    code = _TORCH_TO_FA[dtype]
+    B, Nq, Hq, d = shape
+    strides = (_rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k"),
+               _rows_layout(v, kshape, dtype, dev, "v"))
+    if o is None:
+        device = q.device
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+        size = _cross_workspace(False, B, Nq, kshape[1], Hq, kshape[2], d, code)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+        o_st, ws = _strides(Nq * Hq * d, Hq * d, d), (workspace.data_ptr() if size else None, size)
+    else:
+        o_st, ws = _rows_layout(o, shape, dtype, dev, "o"), _workspace_arg(workspace, dev)
+    _check((_lib or load_library()).fa_cross_fwd(
+        c, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _lse(lse, shape, dev), *strides, o_st, code,
+        default_scale(d) if scale is None else float(scale), *ws, _stream(stream)))
+    return o, lse
+
+
+def fa_cross_fwd(q, k, v, o, lse, workspace=None, q_lens=None, k_lens=None, scale=None, stream=None):
+    """Cross attention through the C ABI: fills o ([B, Nq, Hq, d]) and lse ([B, Hq, Nq] fp32). ``workspace`` is a
+    uint8 CUDA tensor of fa_cross_fwd_workspace_size(...) bytes (None where that is 0)."""
+    _cross_fwd(q, k, v, o, lse, workspace, q_lens, k_lens, scale, stream)
+
+
+def cross_attention_forward(q, k, v, q_lens=None, k_lens=None, scale=None):
+    """Attention of q [B, Nq, Hq, d] over k and v [B, Nk, Hk, d] of another sequence; returns (o, lse).
+
+    Hq is a multiple of Hk (shared key heads). ``q_lens``, ``k_lens`` (int32 [B], None: all) count the real
+    rows of each sequence of a padded batch: queries past them, and queries without keys, get o = 0 and
+    lse = -inf, and what lies in padding rows reaches nothing."""
+    return _cross_fwd(q, k, v, None, None, None, q_lens, k_lens, scale, None)
+
+
+def _cross_bwd(q, k, v, o, do, lse, outs, q_lens, k_lens, scale, stream):
+    """``outs``: (dq, dk, dv, workspace) of the caller, or None to allocate them."""
+    c, shape, kshape, dtype, dev = _cross_shape(q, k, q_lens, k_lens)
+    code = _TORCH_TO_FA[dtype]
+    B, Nq, Hq, d = shape
+    Nk, Hk = kshape[1], kshape[2]
+    strides = [_rows_layout(t, s, dtype, dev, n) for t, s, n in
+               ((q, shape, "q"), (k, kshape, "k"), (v, kshape, "v"), (o, shape, "o"), (do, shape, "do"))]
+    if outs is None:
+        dq, dk, dv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
+        size = _cross_workspace(True, B, Nq, Nk, Hq, Hk, d, code)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        kv_st, ws = _strides(Nk * Hk * d, Hk * d, d), (workspace.data_ptr(), size)
+        strides += [_strides(Nq * Hq * d, Hq * d, d), kv_st, kv_st]
+    else:
+        dq, dk, dv, workspace = outs
+        ws = _workspace_arg(workspace, dev)
+        strides += [_rows_layout(t, s, dtype, dev, n) for t, s, n in
+                    ((dq, shape, "dq"), (dk, kshape, "dk"), (dv, kshape, "dv"))]
+    _check((_lib or load_library()).fa_cross_bwd(
+        c, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), _lse(lse, shape, dev), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), *strides, code, default_scale(d) if scale is None else float(scale), *ws,
+        _stream(stream)))
+    return dq, dk, dv
+
+
+def fa_cross_bwd(q, k, v, o, do, lse, dq, dk, dv, workspace, q_lens=None, k_lens=None, scale=None, stream=None):
+    """Its backward through the C ABI: fills dq, dk and dv. ``workspace`` is a uint8 CUDA tensor of
+    fa_cross_bwd_workspace_size(...) bytes."""
+    _cross_bwd(q, k, v, o, do, lse, (dq, dk, dv, workspace), q_lens, k_lens, scale, stream)
+
+
+def cross_attention_backward(q, k, v, o, do, lse, q_lens=None, k_lens=None, scale=None):
+    """Allocate the gradients and the workspace and run the backward; returns (dq, dk, dv), contiguous. o and
+    lse are cross_attention_forward's."""
+    return _cross_bwd(q, k, v, o, do, lse, None, q_lens, k_lens, scale, None)
+
+
+class _CrossAttnFunc(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, q_lens, k_lens, scale):
+        o, lse = cross_attention_forward(q, k, v, q_lens, k_lens, scale)
+        ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
+        return (*cross_attention_backward(q, k, v, o, _readable(do), lse, q_lens, k_lens, ctx.scale), None, None, None)
+
+
+def cross_attn_func(q, k, v, q_lens=None, k_lens=None, softmax_scale=None):
+    """Cross attention of q [B, Nq, Hq, d] over k, v [B, Nk, Hk, d] with autograd (forward fa_cross_fwd, backward
+    fa_cross_bwd); lengths as for cross_attention_forward."""
+    return _CrossAttnFunc.apply(_readable(q), _readable(k), _readable(v), q_lens, k_lens, softmax_scale)
 
 
 # ---------------------------- 8-bit key/value cache ----------------------------

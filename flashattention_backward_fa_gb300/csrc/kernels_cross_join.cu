@@ -1,0 +1,207 @@
+// Cross attention: what stands before and behind its products.
+//
+// * preprocess: D_i = rowsum(dO o O) and L_i, stored negated as the backward's
+//   addends, for every query row that takes part (-inf and 0 elsewhere, which makes
+//   the row's probabilities 0);
+// * join of the forward's splits: with their log-sum-exps l_s,
+//   O = sum_s 2^(l_s - l) O_s, l = log2 sum_s 2^l_s;
+// * joins of dQ and of dK, dV: sums over the splits in ascending order, so that the
+//   same inputs give the same bits on every run.
+//
+// All are bound by memory; a thread takes 16 bytes of a 16-bit result.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_cross.h"
+#include "fa_serve.h"
+#include "rope_common.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x) { return static_cast<float>(x); }
+
+// One warp a query row (b, h, i), i fastest over the padded rows.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __grid_constant__ CrossParams p) {
+  let_next_begin();
+  wait_for_previous();
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)p.B * p.Hq * p.nq_pad, apart = (long long)gridDim.x * (kJoinThreads / 32);
+  for (long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows; row += apart) {
+    const long long bh = row / p.nq_pad;
+    const int i = (int)(row - bh * p.nq_pad), b = (int)(bh / p.Hq), h = (int)(bh - (long long)b * p.Hq);
+    float acc = 0.f, nl = -INFINITY;
+    if (i < cross_q_len(p, b)) {
+      const T* o = static_cast<const T*>(p.o) + b * p.o_st.b + i * p.o_st.n + h * p.o_st.h;
+      const T* g = static_cast<const T*>(p.dout) + b * p.do_st.b + i * p.do_st.n + h * p.do_st.h;
+      for (int e = lane; e < p.d; e += 32) acc = fmaf(to_f32(o[e]), to_f32(g[e]), acc);
+      acc = row_sum<32>(acc);
+      const float l = p.lse[bh * p.Nq + i];
+      nl = l == -INFINITY ? l : -(l * 1.4426950408889634f);  // (-inf: a row without keys)
+    }
+    if (lane == 0) {
+      p.nD[row] = -acc;
+      p.nL2[row] = nl;
+    }
+  }
+}
+
+// Four consecutive values as T.
+template <typename T>
+__device__ __forceinline__ void store4(T* to, const float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) to[e] = static_cast<T>(v[e]);
+}
+template <>
+__device__ __forceinline__ void store4<__half>(__half* to, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(to) = make_uint2(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]));
+}
+template <>
+__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* to, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(to) = make_uint2(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]));
+}
+
+// Four values of a split's row (d is a multiple of 4 for 16-bit types; fp32 rows of any d by single values).
+__device__ __forceinline__ void load_part(const float* from, int left, bool vec, float (&v)[4]) {
+  if (vec) {
+    const float4 a = *reinterpret_cast<const float4*>(from);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = e < left ? from[e] : 0.f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_row(T* to, int left, const float (&v)[4]) {
+  if (left >= 4) {
+    store4(to, v);
+  } else {
+    for (int e = 0; e < left; ++e) to[e] = static_cast<T>(v[e]);
+  }
+}
+
+// A thread takes four values of a row (b, t, h) of [B, Nq, Hq, d].
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) cross_join_fwd_kernel(const __grid_constant__ CrossParams p) {
+  let_next_begin();
+  wait_for_previous();
+  const int quads = (p.d + 3) >> 2;
+  const long long n = (long long)p.B * p.Nq * p.Hq * quads;
+  const long long rows = (long long)p.B * p.Nq * p.Hq;
+  const bool vec = (p.d & 3) == 0;
+  for (long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kJoinThreads) {
+    const long long row = x / quads, bt = row / p.Hq;
+    const int e = 4 * (int)(x - row * quads), h = (int)(row - bt * p.Hq), b = (int)(bt / p.Nq);
+    const int t = (int)(bt - (long long)b * p.Nq);
+    const long long at = ((long long)b * p.Hq + h) * p.Nq + t;
+    float m = -INFINITY;
+    for (int s = 0; s < p.plan.k_splits; ++s) m = fmaxf(m, p.part_lse[s * rows + at]);
+    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.plan.k_splits; ++s) {
+      const float l = p.part_lse[s * rows + at];
+      if (l == -INFINITY) continue;
+      const float w = exp2f(l - m);
+      float a[4];
+      load_part(p.part + (s * rows + row) * p.d + e, p.d - e, vec, a);
+      sum += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(w, a[i], v[i]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= inv;
+    store_row(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h + e, p.d - e, v);
+    if (e == 0) p.lse_out[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// Sums over the splits of [splits][.., N, H, d] from `part`, `apart` floats between
+// splits, times `mul`; rows from their sequence's length on get zeros.
+template <typename T, bool kKeys>
+__device__ __forceinline__ void join_rows(const CrossParams& p, const float* part, long long apart, int splits, int N,
+                                          int H, void* out, const fa_strides& st, float mul) {
+  const int quads = (p.d + 3) >> 2;
+  const long long n = (long long)p.B * N * H * quads;
+  const bool vec = (p.d & 3) == 0;
+  for (long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kJoinThreads) {
+    const long long row = x / quads, bt = row / H;
+    const int e = 4 * (int)(x - row * quads), h = (int)(row - bt * H), b = (int)(bt / N);
+    const int t = (int)(bt - (long long)b * N);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t < (kKeys ? cross_k_len(p, b) : cross_q_len(p, b))) {
+      for (int s = 0; s < splits; ++s) {
+        float a[4];
+        load_part(part + s * apart + row * p.d + e, p.d - e, vec, a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += a[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] *= mul;
+    }
+    store_row(static_cast<T*>(out) + b * st.b + t * st.n + h * st.h + e, p.d - e, v);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) cross_join_dq_kernel(const __grid_constant__ CrossParams p) {
+  let_next_begin();
+  wait_for_previous();
+  join_rows<T, false>(p, p.part, (long long)p.B * p.Nq * p.Hq * p.d, p.plan.k_splits, p.Nq, p.Hq, p.out, p.out_st,
+                      p.scale);
+}
+
+// y: 0 dK, 1 dV.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) cross_join_dkdv_kernel(const __grid_constant__ CrossParams p) {
+  let_next_begin();
+  wait_for_previous();
+  const long long size = (long long)p.B * p.Nk * p.Hk * p.d;
+  const bool is_v = blockIdx.y != 0;
+  join_rows<T, true>(p, p.part_kv + (is_v ? size : 0), 2 * size, p.plan.q_splits, p.Nk, p.Hk, is_v ? p.dv : p.dk,
+                     is_v ? p.dv_st : p.dk_st, is_v ? 1.f : p.scale);
+}
+
+int join_blocks(const CrossParams& p, int N, int H) {
+  const long long n = (long long)p.B * N * H * ((p.d + 3) / 4);
+  const long long blocks = (n + kJoinThreads - 1) / kJoinThreads;
+  return (int)(blocks < 152 * 16 ? blocks : 152 * 16);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st) {
+  const long long rows = (long long)p.B * p.Hq * p.nq_pad, blocks = (rows + 7) / 8;
+  const dim3 grid((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32));
+  if (dtype == FA_F32) return launch_chained(cross_preprocess_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(cross_preprocess_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
+                          : launch_chained(cross_preprocess_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+}
+
+cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t st) {
+  const dim3 grid(join_blocks(p, p.Nq, p.Hq));
+  if (dtype == FA_F32) return launch_chained(cross_join_fwd_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(cross_join_fwd_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
+                          : launch_chained(cross_join_fwd_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+}
+
+cudaError_t launch_cross_join_dq(const CrossParams& p, int dtype, cudaStream_t st) {
+  const dim3 grid(join_blocks(p, p.Nq, p.Hq));
+  if (dtype == FA_F32) return launch_chained(cross_join_dq_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(cross_join_dq_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
+                          : launch_chained(cross_join_dq_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+}
+
+cudaError_t launch_cross_join_dkdv(const CrossParams& p, int dtype, cudaStream_t st) {
+  const dim3 grid(join_blocks(p, p.Nk, p.Hk), 2);
+  if (dtype == FA_F32) return launch_chained(cross_join_dkdv_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(cross_join_dkdv_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
+                          : launch_chained(cross_join_dkdv_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+}
+
+}  // namespace fa

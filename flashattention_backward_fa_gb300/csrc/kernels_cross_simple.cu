@@ -1,0 +1,396 @@
+// Cross attention on the CUDA cores, in fp32 (d <= 128), forward and backward.
+//
+//   S = scale q k^T over the keys j < k_len, O = softmax(S) V, L = log sum exp S
+//   P = exp(S - L), dP = dO V^T, dS = P o (dP - D), D = rowsum(dO o O)
+//   dQ = scale dS K;  dV = sum P^T dO, dK = scale sum dS^T Q over a group's heads
+//
+// fp32 needs about 1e-7 relative accuracy, which the tf32 tensor-core kind cannot
+// give, so the products are FFMA. A block holds 32 rows (queries; keys in the dK/dV
+// kernel) and walks 64 columns at a time (keys; queries of all heads of the group).
+// 128 threads as 8 x 16: a thread has 4 x 4 of the 32 x 64 products (rows ty + 8 i,
+// columns tx + 16 j, both operands read in 16-byte pieces of rows DP + 4 floats
+// apart, which no two threads of a quarter warp have in the same bank) and 4 rows x
+// DP / 16 columns of the 32 x DP sums. Rows and columns past a sequence's length are
+// zeros in shared memory, so nothing of what lies there reaches a product.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_cross.h"
+#include "fa_serve.h"
+#include "rope_common.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kRows = 32, kCols = 64, kThreads = 128;
+constexpr int kPad = kCols + 4;  // floats between the rows of a 32 x 64 tile
+
+template <int DP>
+struct Tile {
+  static constexpr int kApart = DP + 4;  // floats between rows
+  static constexpr int bytes(int rows) { return rows * kApart * 4; }
+};
+
+// Rows [0, rows) of a tensor (row stride `st`, d values each) to shared memory as fp32 [most][DP],
+// zeros past `rows` and d.
+template <typename T, int DP>
+__device__ __forceinline__ void stage(float* to, const T* from, int64_t st, int rows, int most, int d) {
+  for (int x = threadIdx.x; x < most * DP; x += kThreads) {
+    const int r = x / DP, e = x - r * DP;
+    to[r * Tile<DP>::kApart + e] = r < rows && e < d ? static_cast<float>(from[r * st + e]) : 0.f;
+  }
+}
+
+// s[i][j] = row ty + 8 i of a . row tx + 16 j of b.
+template <int DP>
+__device__ __forceinline__ void rows_by_rows(const float* a, const float* b, float (&s)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  uint64_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+#pragma unroll 4
+  for (int e = 0; e < DP; e += 4) {
+    uint64_t x[4][2], y[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(a + (ty + 8 * i) * Tile<DP>::kApart + e);
+      const float4 w = *reinterpret_cast<const float4*>(b + (tx + 16 * i) * Tile<DP>::kApart + e);
+      x[i][0] = f2_pack(u.x, u.y), x[i][1] = f2_pack(u.z, u.w);
+      y[i][0] = f2_pack(w.x, w.y), y[i][1] = f2_pack(w.z, w.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f2_fma(x[i][1], y[j][1], f2_fma(x[i][0], y[j][0], acc[i][j]));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      f2_unpack(acc[i][j], lo, hi);
+      s[i][j] = lo + hi;
+    }
+}
+
+// acc[i][c] += sum over the columns x of row ty + 8 i of w (32 x 64) times row x of b; a thread's columns
+// of DP are 4 tx + 64 c ..  + 3 (as two pairs).
+template <int DP>
+__device__ __forceinline__ void weights_by_rows(const float* w, const float* b, uint64_t (&acc)[4][DP / 64][2]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+  for (int x = 0; x < kCols; x += 4) {
+    float f[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 u = *reinterpret_cast<const float4*>(w + (ty + 8 * i) * kPad + x);
+      f[i][0] = u.x, f[i][1] = u.y, f[i][2] = u.z, f[i][3] = u.w;
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(b + (x + y) * Tile<DP>::kApart + 4 * tx + 64 * c);
+        const uint64_t lo = f2_pack(v.x, v.y), hi = f2_pack(v.z, v.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t ff = f2_pack(f[i][y], f[i][y]);
+          acc[i][c][0] = f2_fma(ff, lo, acc[i][c][0]);
+          acc[i][c][1] = f2_fma(ff, hi, acc[i][c][1]);
+        }
+      }
+  }
+}
+
+// A thread's 4 x 4 into a 32 x 64 tile.
+__device__ __forceinline__ void put_tile(float* to, const float (&s)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) to[(ty + 8 * i) * kPad + tx + 16 * j] = s[i][j];
+}
+
+// A thread's sums of row ty + 8 i, times mul, to `to` (a row of d values).
+template <typename T, int DP>
+__device__ __forceinline__ void put_row(T* to, const uint64_t (&acc)[DP / 64][2], float mul, int d) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c) {
+    float v[4];
+    f2_unpack(acc[c][0], v[0], v[1]);
+    f2_unpack(acc[c][1], v[2], v[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * (threadIdx.x & 15) + 64 * c + e < d) to[4 * (threadIdx.x & 15) + 64 * c + e] = static_cast<T>(v[e] * mul);
+  }
+}
+
+template <int DP>
+__device__ __forceinline__ void clear(uint64_t (&acc)[4][DP / 64][2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
+}
+
+// Over the 16 threads that share a row.
+__device__ __forceinline__ float row_max16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Grid: x the query tile, y head, z batch * split.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) cross_fwd_simple_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ __align__(16) float sm[];
+  let_next_begin();
+  wait_for_previous();
+  float *q = sm, *k = q + kRows * Tile<DP>::kApart, *v = k + kCols * Tile<DP>::kApart, *w = v + kCols * Tile<DP>::kApart;
+  const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, h = blockIdx.y;
+  const int i0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int j_end = min(nk, (split + 1) * p.plan.k_chunk);
+  const T* kp = static_cast<const T*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
+  const T* vp = static_cast<const T*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
+  uint64_t acc[4][DP / 64][2];
+  clear<DP>(acc);
+  float m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  if (i0 < nq)
+    stage<T, DP>(q, static_cast<const T*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
+                 kRows, p.d);
+  for (int j0 = split * p.plan.k_chunk; i0 < nq && j0 < j_end; j0 += kCols) {
+    __syncthreads();
+    stage<T, DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
+    stage<T, DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
+    __syncthreads();
+    float s[4][4];
+    rows_by_rows<DP>(q, k, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = j0 + tx + 16 * j < j_end ? s[i][j] * p.scale_log2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+      const float now = fmaxf(m[i], row_max16(top));
+      const float base = now == -INFINITY ? 0.f : now;  // every score so far is -inf
+      const float was = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = exp2f(s[i][j] - base);
+        sum += s[i][j];
+      }
+      l[i] = l[i] * was + row_sum<16>(sum);
+      m[i] = now;
+      const uint64_t f = f2_pack(was, was);
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        acc[i][c][0] = f2_mul(acc[i][c][0], f);
+        acc[i][c][1] = f2_mul(acc[i][c][1], f);
+      }
+    }
+    put_tile(w, s);
+    __syncthreads();
+    weights_by_rows<DP>(w, v, acc);
+  }
+  const long long rows = (long long)p.B * p.Nq * p.Hq;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = i0 + ty + 8 * i;
+    if (t >= p.Nq) continue;
+    const bool has = t < nq && l[i] != 0.f;  // (a NaN sum counts as there)
+    const long long at = ((long long)b * p.Hq + h) * p.Nq + t;
+    const float lse2 = has ? m[i] + log2f(l[i]) : -INFINITY;
+    if (splits > 1) {
+      if (tx == 0) p.part_lse[split * rows + at] = lse2;
+      if (has)
+        put_row<float, DP>(p.part + (split * rows + ((long long)b * p.Nq + t) * p.Hq + h) * p.d, acc[i], 1.f / l[i], p.d);
+    } else {
+      if (!has)
+#pragma unroll
+        for (int c = 0; c < DP / 64; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
+      if (tx == 0) p.lse_out[at] = has ? lse2 * 0.6931471805599453f : -INFINITY;
+      put_row<T, DP>(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h, acc[i],
+                     has ? 1.f / l[i] : 0.f, p.d);
+    }
+  }
+}
+
+// dQ. Grid as the forward's.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) cross_dq_simple_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ __align__(16) float sm[];
+  let_next_begin();
+  wait_for_previous();
+  float *q = sm, *g = q + kRows * Tile<DP>::kApart, *k = g + kRows * Tile<DP>::kApart,
+        *v = k + kCols * Tile<DP>::kApart, *w = v + kCols * Tile<DP>::kApart;
+  const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, h = blockIdx.y;
+  const int i0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int j_end = min(nk, (split + 1) * p.plan.k_chunk);
+  const T* kp = static_cast<const T*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
+  const T* vp = static_cast<const T*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
+  uint64_t acc[4][DP / 64][2];
+  clear<DP>(acc);
+  float nl[4], nd[4];
+  if (i0 < nq) {
+    stage<T, DP>(q, static_cast<const T*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
+                 kRows, p.d);
+    stage<T, DP>(g, static_cast<const T*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
+                 nq - i0, kRows, p.d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long at = ((long long)b * p.Hq + h) * p.nq_pad + i0 + ty + 8 * i;
+      nl[i] = i0 + ty + 8 * i < nq ? p.nL2[at] : -INFINITY;
+      nd[i] = i0 + ty + 8 * i < nq ? p.nD[at] : 0.f;
+    }
+  }
+  for (int j0 = split * p.plan.k_chunk; i0 < nq && j0 < j_end; j0 += kCols) {
+    __syncthreads();
+    stage<T, DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
+    stage<T, DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    rows_by_rows<DP>(q, k, s);
+    rows_by_rows<DP>(g, v, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s[i][j] = j0 + tx + 16 * j < j_end && nl[i] != -INFINITY
+                      ? exp2f(fmaf(s[i][j], p.scale_log2, nl[i])) * (dp[i][j] + nd[i])
+                      : 0.f;
+    put_tile(w, s);
+    __syncthreads();
+    weights_by_rows<DP>(w, k, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = i0 + ty + 8 * i;
+    if (t >= p.Nq) continue;
+    if (splits > 1) {
+      if (t < nq)
+        put_row<float, DP>(p.part + (((long long)split * p.B + b) * p.Nq + t) * p.Hq * p.d + (long long)h * p.d, acc[i],
+                           1.f, p.d);
+    } else {
+      put_row<T, DP>(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h, acc[i], p.scale, p.d);
+    }
+  }
+}
+
+// dK and dV. Grid: x the key tile, y key head, z batch * split of the query steps (64
+// queries of one head of the group each, heads outermost).
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) cross_dkdv_simple_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ __align__(16) float sm[];
+  let_next_begin();
+  wait_for_previous();
+  float *k = sm, *v = k + kRows * Tile<DP>::kApart, *q = v + kRows * Tile<DP>::kApart,
+        *g = q + kCols * Tile<DP>::kApart, *w = g + kCols * Tile<DP>::kApart, *u = w + kRows * kPad;
+  const int splits = p.plan.q_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, hk = blockIdx.y;
+  const int j0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int per_head = (p.Nq + kCols - 1) / kCols, steps = per_head * p.G;
+  const int s_end = min(steps, (split + 1) * p.plan.q_chunk);
+  uint64_t dk[4][DP / 64][2], dv[4][DP / 64][2];
+  clear<DP>(dk);
+  clear<DP>(dv);
+  if (j0 < nk) {
+    stage<T, DP>(k, static_cast<const T*>(p.k) + b * p.k_st.b + (int64_t)j0 * p.k_st.n + hk * p.k_st.h, p.k_st.n, nk - j0,
+                 kRows, p.d);
+    stage<T, DP>(v, static_cast<const T*>(p.v) + b * p.v_st.b + (int64_t)j0 * p.v_st.n + hk * p.v_st.h, p.v_st.n, nk - j0,
+                 kRows, p.d);
+  }
+  for (int st = split * p.plan.q_chunk; j0 < nk && st < s_end; ++st) {
+    const int h = hk * p.G + st / per_head, i0 = st % per_head * kCols;
+    if (i0 >= nq) continue;
+    __syncthreads();
+    stage<T, DP>(q, static_cast<const T*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
+                 kCols, p.d);
+    stage<T, DP>(g, static_cast<const T*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
+                 nq - i0, kCols, p.d);
+    float nl[4], nd[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = i0 + tx + 16 * j;
+      const long long at = ((long long)b * p.Hq + h) * p.nq_pad + t;
+      nl[j] = t < nq ? p.nL2[at] : -INFINITY;
+      nd[j] = t < nq ? p.nD[at] : 0.f;
+    }
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    rows_by_rows<DP>(k, q, s);
+    rows_by_rows<DP>(v, g, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = j0 + ty + 8 * i < nk && nl[j] != -INFINITY;
+        s[i][j] = in ? exp2f(fmaf(s[i][j], p.scale_log2, nl[j])) : 0.f;
+        dp[i][j] = in ? s[i][j] * (dp[i][j] + nd[j]) : 0.f;
+      }
+    put_tile(w, s);
+    put_tile(u, dp);
+    __syncthreads();
+    weights_by_rows<DP>(w, g, dv);
+    weights_by_rows<DP>(u, q, dk);
+  }
+  const long long size = (long long)p.B * p.Nk * p.Hk * p.d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = j0 + ty + 8 * i;
+    if (j >= p.Nk) continue;
+    if (splits > 1) {
+      if (j >= nk) continue;
+      float* to = p.part_kv + 2 * split * size + (((long long)b * p.Nk + j) * p.Hk + hk) * p.d;
+      put_row<float, DP>(to, dk[i], 1.f, p.d);
+      put_row<float, DP>(to + size, dv[i], 1.f, p.d);
+    } else {
+      put_row<T, DP>(static_cast<T*>(p.dk) + b * p.dk_st.b + j * p.dk_st.n + hk * p.dk_st.h, dk[i], p.scale, p.d);
+      put_row<T, DP>(static_cast<T*>(p.dv) + b * p.dv_st.b + j * p.dv_st.n + hk * p.dv_st.h, dv[i], 1.f, p.d);
+    }
+  }
+}
+
+constexpr int kFwd = 0, kDq = 1, kDkdv = 2;
+
+template <typename T, int DP, int kWhat>
+cudaError_t launch_t(const CrossParams& p, cudaStream_t st) {
+  constexpr int bytes = Tile<DP>::bytes(kWhat == kFwd ? kRows + 2 * kCols : 2 * kRows + 2 * kCols) +
+                        kRows * kPad * 4 * (kWhat == kDkdv ? 2 : 1);
+  constexpr auto kKernel = kWhat == kFwd  ? cross_fwd_simple_kernel<T, DP>
+                           : kWhat == kDq ? cross_dq_simple_kernel<T, DP>
+                                          : cross_dkdv_simple_kernel<T, DP>;
+  const cudaError_t e = allow_smem<kKernel>(bytes);
+  if (e != cudaSuccess) return e;
+  const bool keys = kWhat == kDkdv;
+  const dim3 grid(((keys ? p.Nk : p.Nq) + kRows - 1) / kRows, keys ? p.Hk : p.Hq,
+                  p.B * (keys ? p.plan.q_splits : p.plan.k_splits));
+  return launch_chained(kKernel, grid, kThreads, bytes, 1, p, st);
+}
+
+template <int kWhat>
+cudaError_t launch(const CrossParams& p, int dtype, cudaStream_t st) {
+  if (dtype == FA_F32) return p.d <= 64 ? launch_t<float, 64, kWhat>(p, st) : launch_t<float, 128, kWhat>(p, st);
+  if (dtype == FA_BF16)
+    return p.d <= 64 ? launch_t<__nv_bfloat16, 64, kWhat>(p, st) : launch_t<__nv_bfloat16, 128, kWhat>(p, st);
+  return p.d <= 64 ? launch_t<__half, 64, kWhat>(p, st) : launch_t<__half, 128, kWhat>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_fwd_simple(const CrossParams& p, int dtype, cudaStream_t st) { return launch<kFwd>(p, dtype, st); }
+cudaError_t launch_cross_dq_simple(const CrossParams& p, int dtype, cudaStream_t st) { return launch<kDq>(p, dtype, st); }
+cudaError_t launch_cross_dkdv_simple(const CrossParams& p, int dtype, cudaStream_t st) {
+  return launch<kDkdv>(p, dtype, st);
+}
+
+}  // namespace fa

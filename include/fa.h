@@ -425,6 +425,51 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
                 int window, const float* alibi_slopes, int64_t alibi_stride_b, void* workspace,
                 size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Cross attention: queries attend to the states of another sequence, of another
+ * length (an encoder's), with shared key heads and padded batches.
+ *
+ *   O = softmax(scale q k^T) v over the first k_len keys, lse its log-sum-exp
+ *   (natural log); the backward takes O and lse as the forward gave them.
+ *
+ * q, o, dout, dq: [B, Nq, Hq, d]; k, v, dk, dv: [B, Nk, Hk, d], each with its own
+ * strides; lse contiguous fp32 [B, Hq, Nq]. Query heads h * Hq / Hk .. share key
+ * head h (Hq a multiple of Hk); dk and dv are summed over them. No causal mask, no
+ * dropout. q_lens, k_lens: device int32 [B], the real rows of each sequence, clamped
+ * into [0, Nq] and [0, Nk] (null: all). Queries from q_len on, and queries of a
+ * sequence without keys, get O = 0 and lse = -inf; they and the keys from k_len on
+ * get zero gradients and have no part in any other, whatever lies there (NaN too).
+ *
+ * fp16 / bf16 with d in {64, 128}, strides multiples of 8; fp32 with d <= 128, any
+ * positive strides; all tensors 16-byte aligned; scale > 0. Outputs must not overlap
+ * inputs. B and Hq <= 65535, B * Hq <= 2^24, Nq and Nk <= 2^24, Nq * Hq / Hk <= 2^30.
+ * The same inputs give the same bits on every run. `workspace`: 256-byte aligned,
+ * fa_cross_*_workspace_size(...) bytes for the same shape; its contents on entry do
+ * not matter. The forward's size is 0 where it needs none (workspace may then be null)
+ * and both are for shapes that the calls refuse; calls that overlap on the GPU need
+ * workspaces of their own.
+ * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
+ * fp32. In 16 bits: P and dS as operands of the products, with their rounding residual
+ * wherever a probability of the tile may exceed 1/64 (as fa_fwd and fa_bwd). Errors as
+ * fa_fwd / fa_bwd.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int B, Nq, Nk, Hq, Hk, d;
+  const int* q_lens;
+  const int* k_lens;
+} fa_cross_shape;
+
+size_t fa_cross_fwd_workspace_size(const fa_cross_shape* shape, fa_dtype dtype);
+int fa_cross_fwd(const fa_cross_shape* shape, const void* q, const void* k, const void* v, void* o, float* lse,
+                 fa_strides q_strides, fa_strides k_strides, fa_strides v_strides, fa_strides o_strides, fa_dtype dtype,
+                 float scale, void* workspace, size_t workspace_bytes, void* stream);
+size_t fa_cross_bwd_workspace_size(const fa_cross_shape* shape, fa_dtype dtype);
+int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, const void* v, const void* o,
+                 const void* dout, const float* lse, void* dq, void* dk, void* dv, fa_strides q_strides,
+                 fa_strides k_strides, fa_strides v_strides, fa_strides o_strides, fa_strides dout_strides,
+                 fa_strides dq_strides, fa_strides dk_strides, fa_strides dv_strides, fa_dtype dtype, float scale,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads (and with clear != 0 resets) the status word of the current device.
  * Call after synchronising the streams the kernels ran on. *status receives
  * the raw bits (1 = a bounded wait timed out; 2 = an FA_DQ_ORDERED dK/dV
