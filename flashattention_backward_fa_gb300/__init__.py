@@ -18,7 +18,8 @@ from .binding import (FA_BF16, FA_BWD_DKDV, FA_BWD_DQ, FA_BWD_PREPROCESS, FA_DQ_
                       fa_strerror, fa_varlen_bwd, fa_varlen_bwd_workspace_size, fa_varlen_fwd, flash_attn_func,
                       flash_attn_varlen_func, header_functions, Kv8Cache, kv8_append, kv8_attention,
                       kv8_cache_alloc, kv8_norm_rope_append, load_library, qk_norm_rope_backward,
-                      qk_norm_rope_forward, qk_norm_rope_func, rope_tables, varlen_attention_backward, varlen_attention_forward)
+                      qk_norm_rope_forward, qk_norm_rope_func, rope_axes, rope_axis_tables, rope_tables,
+                      varlen_attention_backward, varlen_attention_forward)
 
 __all__ = ["FA_BF16", "FA_BWD_DKDV", "FA_BWD_DQ", "FA_BWD_PREPROCESS", "FA_DQ_ATOMIC", "FA_DQ_DETERMINISTIC",
            "FA_DQ_ORDERED", "FA_DQ_RECOMPUTE", "FA_F16", "FA_F32", "FaError", "FaStrides",
@@ -30,7 +31,7 @@ __all__ = ["FA_BF16", "FA_BWD_DKDV", "FA_BWD_DQ", "FA_BWD_PREPROCESS", "FA_DQ_AT
            "fa_kv8_attn", "fa_kv8_attn_workspace_size", "fa_kv8_norm_rope_append", "fa_qk_norm_rope_bwd",
            "fa_qk_norm_rope_bwd_workspace_size", "fa_qk_norm_rope_fwd", "Kv8Cache", "kv8_append", "kv8_attention",
            "kv8_cache_alloc", "kv8_norm_rope_append", "qk_norm_rope_backward", "qk_norm_rope_forward",
-           "qk_norm_rope_func", "rope_tables",
+           "qk_norm_rope_func", "rope_axes", "rope_axis_tables", "rope_tables",
            "cross_attention_backward", "cross_attention_forward", "cross_attn_func", "fa_cross_bwd",
            "fa_cross_bwd_workspace_size", "fa_cross_fwd", "fa_cross_fwd_workspace_size",
            "varlen_attention_backward", "varlen_attention_forward"]

@@ -60,6 +60,11 @@ class _Kv8SeqsArg(ctypes.Structure):
                 ("new_lens", ctypes.c_void_p), ("B", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
+class _RopeAxes(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int), ("pair_axis", ctypes.c_char_p), ("positions", ctypes.c_void_p),
+                ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64), ("stride_axis", ctypes.c_int64)]
+
+
 class _CrossShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("Nq", ctypes.c_int), ("Nk", ctypes.c_int), ("Hq", ctypes.c_int),
                 ("Hk", ctypes.c_int), ("d", ctypes.c_int), ("q_lens", ctypes.c_void_p), ("k_lens", ctypes.c_void_p)]
@@ -136,6 +141,13 @@ def load_library(path: str = LIB_PATH):
     lib.fa_kv8_attn_workspace_size.restype = sz
     lib.fa_kv8_attn.argtypes = [cache, seqs, vp, vp, vp, i, i, i, st, st, i, f, i, i, vp, i64, vp, sz, vp]
     lib.fa_kv8_attn.restype = i
+    axes = ctypes.POINTER(_RopeAxes)
+    lib.fa_qk_norm_rope_axes_fwd.argtypes = [vp] * 8 + [axes] + [i] * 8 + [st] * 4 + [i, i, f, vp]
+    lib.fa_qk_norm_rope_axes_fwd.restype = i
+    lib.fa_qk_norm_rope_axes_bwd.argtypes = [vp] * 12 + [axes] + [i] * 8 + [st] * 6 + [i, i, f, vp, sz, vp]
+    lib.fa_qk_norm_rope_axes_bwd.restype = i
+    lib.fa_kv8_norm_rope_axes_append.argtypes = [cache, seqs] + [vp] * 8 + [axes] + [i] * 5 + [st] * 4 + [i, i, f, vp]
+    lib.fa_kv8_norm_rope_axes_append.restype = i
     shape = ctypes.POINTER(_CrossShape)
     lib.fa_cross_fwd_workspace_size.argtypes, lib.fa_cross_fwd_workspace_size.restype = [shape, i], sz
     lib.fa_cross_bwd_workspace_size.argtypes, lib.fa_cross_bwd_workspace_size.restype = [shape, i], sz
@@ -631,6 +643,54 @@ def _positions(positions, B: int, N: int, dev: int):
     return _int32(positions, (B, N), dev, "positions"), positions.stride(0)
 
 
+@lru_cache(maxsize=256)
+def _axis_bytes(axes: tuple):
+    """(number of axes, one byte a pair) of the axes of the pairs."""
+    if not axes or any(not isinstance(a, int) or not 0 <= a < 4 for a in axes):
+        raise ValueError("axes must be the axis, 0 to 3, of each rotated pair")
+    return max(axes) + 1, bytes(axes)
+
+
+def _axes_arg(positions, axes, pairs: int, B: int, N: int, dev: int) -> _RopeAxes:
+    """The C struct of int32 positions [N, A] or [B, N, A] and the pairs' axes; without axes, of positions [N]
+    or [B, N] on one."""
+    if positions is None or positions.dtype is not torch.int32 or positions.get_device() != dev:
+        raise ValueError(f"positions must be an int32 tensor on cuda:{dev}")
+    if pairs == 0:
+        raise ValueError("positions of their own need the tables cos and sin")
+    shape, st = positions.shape, positions.stride()
+    if axes is None:
+        used, which, shape, st = 1, None, (*shape, 1), (*st, 0)
+    else:
+        used, which = _axis_bytes(tuple(axes))
+        if len(which) != pairs:
+            raise ValueError(f"axes must have an entry for each of the tables' {pairs} pairs, not {len(which)}")
+    if len(shape) == 2:
+        shape, st = (B, *shape), (0, *st)
+    if len(shape) != 3 or shape[0] != B or shape[1] != N or not used <= shape[2]:
+        raise ValueError(f"positions must be [{N}, A] or [{B}, {N}, A] with at least {used} axes"
+                         if axes is not None else f"positions must be [{N}] or [{B}, {N}]")
+    return _RopeAxes(used, which, positions.data_ptr(), *st)
+
+
+def rope_axes(sections, interleaved: bool = False) -> tuple:
+    """The axis of each rotated pair, for sections[a] pairs of axis a: one axis after the other, or (interleaved)
+    in turn while they last."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or sum(left) < 1:
+        raise ValueError("sections must be the numbers of pairs of one to four axes")
+    if not interleaved:
+        return tuple(a for a, n in enumerate(left) for _ in range(n))
+    return tuple(a for turn in range(max(left)) for a, n in enumerate(left) if turn < n)
+
+
+def rope_axis_tables(max_pos: int, sections, base: float = 10000.0, device="cuda"):
+    """cos and sin tables [max_pos, pairs] for rope_axes(sections) where every axis has frequencies of its own
+    (of rotations of 2 * sections[a] values). Axes that share one row of frequencies take rope_tables."""
+    parts = [rope_tables(max_pos, 2 * int(n), base, device) for n in sections if int(n)]
+    return tuple(torch.cat(t, 1) for t in zip(*parts))
+
+
 def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"):
     """cos and sin tables [max_pos, rot_dim / 2] (fp32) of the angles pos * base^(-2i / rot_dim),
     computed in float64 (in fp32 the angles of far positions lose their fraction)."""
@@ -641,7 +701,7 @@ def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"
     return angle.cos().float(), angle.sin().float()
 
 
-def _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream):
+def _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream, axes):
     shape, dtype, dev = _new_tensor(q, "q")
     B, N, Hq, d = shape
     kshape = k.shape
@@ -658,26 +718,30 @@ def _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, 
     else:
         qo_st = _rows_layout(q_out, shape, dtype, dev, "q_out")
         ko_st = _rows_layout(k_out, kshape, dtype, dev, "k_out")
-    _check((_lib or load_library()).fa_qk_norm_rope_fwd(
-        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *ptrs, *_positions(positions, B, N, dev), B,
-        N, Hq, Hk, d, rot, interleaved, rows, q_st, k_st, qo_st, ko_st, _TORCH_TO_FA[dtype], wt, eps,
-        _stream(stream)))
+    lib = _lib or load_library()
+    if axes is None:
+        call, where = lib.fa_qk_norm_rope_fwd, _positions(positions, B, N, dev)
+    else:
+        call, where = lib.fa_qk_norm_rope_axes_fwd, (_axes_arg(positions, axes, rot // 2, B, N, dev),)
+    _check(call(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), *ptrs, *where, B, N, Hq, Hk, d, rot,
+                interleaved, rows, q_st, k_st, qo_st, ko_st, _TORCH_TO_FA[dtype], wt, eps, _stream(stream)))
     return q_out, k_out
 
 
 def fa_qk_norm_rope_fwd(q, k, q_out, k_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
-                        eps=1e-6, interleaved=False, stream=None):
+                        eps=1e-6, interleaved=False, stream=None, axes=None):
     """Per-head RMS norm and rotation through the C ABI: fills q_out and k_out (shaped as q and k)."""
-    _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream)
+    _norm_rope_fwd(q, k, q_out, k_out, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream, axes)
 
 
 def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
-                         interleaved=False):
+                         interleaved=False, axes=None):
     """Allocate the outputs and run the norm and rotation; returns (q_out, k_out), contiguous.
 
     q [B, N, Hq, d], k [B, N, Hk, d]; weights [d] (None: ones); tables as from rope_tables (None: no
-    rotation); positions int32 [N] or [B, N] (None: 0 .. N - 1)."""
-    return _norm_rope_fwd(q, k, None, None, q_weight, k_weight, cos, sin, positions, eps, interleaved, None)
+    rotation); positions int32 [N] or [B, N] (None: 0 .. N - 1). ``axes`` (as from rope_axes): the axis of
+    each rotated pair, for positions [N, A] or [B, N, A] on A axes (fa_qk_norm_rope_axes_fwd)."""
+    return _norm_rope_fwd(q, k, None, None, q_weight, k_weight, cos, sin, positions, eps, interleaved, None, axes)
 
 
 @lru_cache(maxsize=None)
@@ -695,7 +759,8 @@ def _weight_grad(g, w, dev: int, name: str):
     return g.data_ptr()
 
 
-def _norm_rope_bwd(q, k, dq_out, dk_out, outs, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream):
+def _norm_rope_bwd(q, k, dq_out, dk_out, outs, q_weight, k_weight, cos, sin, positions, eps, interleaved, stream,
+                   axes):
     """``outs``: (dq, dk, dq_weight, dk_weight, workspace) of the caller, or None to allocate them."""
     shape, dtype, dev = _new_tensor(q, "q")
     B, N, Hq, d = shape
@@ -724,34 +789,40 @@ def _norm_rope_bwd(q, k, dq_out, dk_out, outs, q_weight, k_weight, cos, sin, pos
         if workspace.get_device() != dev:
             raise ValueError(f"workspace must be a CUDA tensor on cuda:{dev}")
         size = workspace.numel() * workspace.element_size()
-    _check((_lib or load_library()).fa_qk_norm_rope_bwd(
+    lib = _lib or load_library()
+    if axes is None:
+        call, where = lib.fa_qk_norm_rope_bwd, _positions(positions, B, N, dev)
+    else:
+        call, where = lib.fa_qk_norm_rope_axes_bwd, (_axes_arg(positions, axes, rot // 2, B, N, dev),)
+    _check(call(
         q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), qw, kw, dqw_ptr,
-        dkw_ptr, cp, sp, *_positions(positions, B, N, dev), B, N, Hq, Hk, d, rot, bool(interleaved), rows, q_st, k_st,
-        gq_st, gk_st, dq_st, dk_st, _TORCH_TO_FA[dtype], wt, float(eps), workspace.data_ptr(), size, _stream(stream)))
+        dkw_ptr, cp, sp, *where, B, N, Hq, Hk, d, rot, bool(interleaved), rows, q_st, k_st, gq_st, gk_st, dq_st, dk_st,
+        _TORCH_TO_FA[dtype], wt, float(eps), workspace.data_ptr(), size, _stream(stream)))
     return dq, dk, dqw, dkw
 
 
 def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, q_weight=None, k_weight=None,
-                        cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, stream=None):
+                        cos=None, sin=None, positions=None, eps=1e-6, interleaved=False, stream=None, axes=None):
     """Its backward through the C ABI: fills dq, dk and, where there are weights, dq_weight and dk_weight.
     ``workspace`` is a uint8 CUDA tensor of fa_qk_norm_rope_bwd_workspace_size(d) bytes."""
     _norm_rope_bwd(q, k, dq_out, dk_out, (dq, dk, dq_weight, dk_weight, workspace), q_weight, k_weight, cos, sin,
-                   positions, eps, interleaved, stream)
+                   positions, eps, interleaved, stream, axes)
 
 
 def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
-                          eps=1e-6, interleaved=False):
+                          eps=1e-6, interleaved=False, axes=None):
     """Allocate the gradients and the workspace and run the backward; returns
     (dq, dk, dq_weight, dk_weight), contiguous, None for a weight that is None."""
-    return _norm_rope_bwd(q, k, dq_out, dk_out, None, q_weight, k_weight, cos, sin, positions, eps, interleaved, None)
+    return _norm_rope_bwd(q, k, dq_out, dk_out, None, q_weight, k_weight, cos, sin, positions, eps, interleaved, None,
+                          axes)
 
 
 class _QkNormRopeFunc(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, axes):
         ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
-        ctx.cfg = (eps, interleaved)
-        return qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        ctx.cfg = (eps, interleaved, axes)
+        return qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, axes)
 
     @staticmethod
     @once_differentiable
@@ -759,7 +830,7 @@ class _QkNormRopeFunc(torch.autograd.Function):
         q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
         grads = qk_norm_rope_backward(q, k, _readable(dq_out), _readable(dk_out), q_weight, k_weight, cos, sin,
                                       positions, *ctx.cfg)
-        return (*grads, None, None, None, None, None)
+        return (*grads, None, None, None, None, None, None)
 
 
 def _readable(t: torch.Tensor) -> torch.Tensor:
@@ -775,12 +846,13 @@ def _readable(t: torch.Tensor) -> torch.Tensor:
 
 
 def qk_norm_rope_func(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
-                      interleaved=False):
+                      interleaved=False, axes=None):
     """Per-head RMS norm and rotation of q [B, N, Hq, d] and k [B, N, Hk, d] with autograd
     (forward fa_qk_norm_rope_fwd, backward fa_qk_norm_rope_bwd): (q_out, k_out), as
-    flash_attn_func takes them. Gradients reach q, k and the weights."""
+    flash_attn_func takes them. Gradients reach q, k and the weights. ``positions`` and ``axes`` as for
+    qk_norm_rope_forward."""
     return _QkNormRopeFunc.apply(_readable(q), _readable(k), q_weight, k_weight, cos, sin, positions, float(eps),
-                                 bool(interleaved))
+                                 bool(interleaved), None if axes is None else tuple(axes))
 
 
 # ------------------------------- cross attention -------------------------------
@@ -982,7 +1054,7 @@ def kv8_append(cache: Kv8Cache, k, v, block_table, seq_lens, new_lens=None, stre
 
 
 def _norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
-                      interleaved, stream):
+                      interleaved, stream, positions, axes):
     shape, dtype, dev = _new_tensor(q, "q")
     B, T, Hq, d = shape
     c, s = _kv8_args(cache, B, d, dtype, dev, block_table, seq_lens, new_lens)
@@ -994,26 +1066,34 @@ def _norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block
         qo_st = _strides(T * Hq * d, Hq * d, d)
     else:
         qo_st = _rows_layout(q_out, shape, dtype, dev, "q_out")
-    _check((_lib or load_library()).fa_kv8_norm_rope_append(
-        c, s, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *ptrs, T, Hq, rot, interleaved, rows,
+    lib = _lib or load_library()
+    if positions is axes is None:
+        call, where = lib.fa_kv8_norm_rope_append, ()
+    else:
+        call, where = lib.fa_kv8_norm_rope_axes_append, (_axes_arg(positions, axes, rot // 2, B, T, dev),)
+    _check(call(
+        c, s, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), *ptrs, *where, T, Hq, rot, interleaved, rows,
         _rows_layout(q, shape, dtype, dev, "q"), _rows_layout(k, kshape, dtype, dev, "k"),
         _rows_layout(v, kshape, dtype, dev, "v"), qo_st, _TORCH_TO_FA[dtype], wt, eps, _stream(stream)))
     return q_out
 
 
 def fa_kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens,
-                            new_lens=None, eps=1e-6, interleaved=False, stream=None):
+                            new_lens=None, eps=1e-6, interleaved=False, stream=None, positions=None, axes=None):
     """Norm and rotation of new q and k, then k and v into the cache, through the C ABI: fills q_out."""
     _norm_rope_append(cache, q, k, v, q_out, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
-                      interleaved, stream)
+                      interleaved, stream, positions, axes)
 
 
 def kv8_norm_rope_append(cache: Kv8Cache, q, k, v, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens=None,
-                         eps=1e-6, interleaved=False):
+                         eps=1e-6, interleaved=False, positions=None, axes=None):
     """qk_norm_rope_forward of new q and k at their positions and kv8_append of the result in one
-    launch; returns the normed and rotated q (zeros in padding rows)."""
+    launch; returns the normed and rotated q (zeros in padding rows).
+
+    A token's position is its place in its sequence, or what ``positions`` says: int32 [T] or [B, T], or with
+    ``axes`` (as from rope_axes) [T, A] or [B, T, A] (fa_kv8_norm_rope_axes_append)."""
     return _norm_rope_append(cache, q, k, v, None, q_weight, k_weight, cos, sin, block_table, seq_lens, new_lens, eps,
-                             interleaved, None)
+                             interleaved, None, positions, axes)
 
 
 @lru_cache(maxsize=1024)

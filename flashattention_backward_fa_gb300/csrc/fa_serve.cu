@@ -46,6 +46,24 @@ int check_tensor(const void* ptr, fa_strides st, fa_dtype dtype) {
   return FA_OK;
 }
 
+// The axes of a call's positions into *to.
+int check_axes(const fa_rope_axes* a, int rot_dim, fa::RopeAxes* to) {
+  if (!a || a->axes < 1 || a->axes > 4 || rot_dim < 2 || !a->positions) return FA_ERR_INVALID_ARG;
+  if (a->stride_b < 0 || a->stride_n < 0 || a->stride_axis < 0) return FA_ERR_INVALID_ARG;
+  if (!aligned_to(a->positions, 4)) return FA_ERR_ALIGNMENT;
+  std::memset(to, 0, sizeof(*to));
+  for (int i = 0; a->pair_axis && i < rot_dim / 2; ++i) {
+    if (a->pair_axis[i] >= a->axes) return FA_ERR_INVALID_ARG;
+    to->pair_axis[i >> 4] |= (uint32_t)a->pair_axis[i] << (2 * (i & 15));
+  }
+  to->axes = a->axes;
+  to->positions = a->positions;
+  to->sb = a->stride_b;
+  to->sn = a->stride_n;
+  to->sa = a->stride_axis;
+  return FA_OK;
+}
+
 int first_error(std::initializer_list<int> codes) {
   for (int c : codes)
     if (c) return c;
@@ -127,7 +145,7 @@ int append_run(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q
                void* q_out, const void* q_weight, const void* k_weight, const float* cos_table,
                const float* sin_table, int T, int Hq, int rot_dim, int interleaved, int max_pos, fa_strides q_strides,
                fa_strides k_strides, fa_strides v_strides, fa_strides q_out_strides, fa_dtype dtype,
-               fa_dtype weight_dtype, float eps, bool norm, void* stream) {
+               fa_dtype weight_dtype, float eps, bool norm, bool has_axes, const fa_rope_axes* axes, void* stream) {
   int shift = 0;
   int rc = check_cache(cache, seqs, &shift);
   if (rc) return rc;
@@ -143,6 +161,7 @@ int append_run(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q
     return rc;
   fa::Kv8AppendParams p;
   std::memset(&p, 0, sizeof(p));
+  if (has_axes && (rc = check_axes(axes, rot_dim, &p.ax))) return rc;
   fill_cache(p.c, cache, seqs, shift);
   p.k = k;
   p.v = v;
@@ -170,10 +189,87 @@ int append_run(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q
     p.eps = eps;
   }
   if ((rc = fa::check_device_ptrs({cache->k, cache->v, cache->k_scale, cache->v_scale, seqs->block_table,
-                                   seqs->seq_lens, seqs->new_lens, k, v, p.q, p.q_out, p.q_w, p.k_w, p.cos, p.sin})))
+                                   seqs->seq_lens, seqs->new_lens, k, v, p.q, p.q_out, p.q_w, p.k_w, p.cos, p.sin,
+                                   p.ax.positions})))
     return rc;
   if ((rc = fa::status_ptr(&p.c.status))) return rc;
   return cuda_rc(fa::launch_kv8_append(p, dtype == FA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+// The two norm-and-rotation calls, with one position a token or (has_axes) positions on several axes.
+int norm_rope_fwd_run(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                      const void* k_weight, const float* cos_table, const float* sin_table, const int* positions,
+                      int64_t pos_stride, int B, int N, int Hq, int Hk, int d, int rot_dim, int interleaved,
+                      int max_pos, fa_strides q_strides, fa_strides k_strides, fa_strides q_out_strides,
+                      fa_strides k_out_strides, fa_dtype dtype, fa_dtype weight_dtype, float eps, bool has_axes,
+                      const fa_rope_axes* axes, void* stream) {
+  int rc = check_rope(B, N, Hq, Hk, d, rot_dim, max_pos, dtype, weight_dtype, eps);
+  if (rc) return rc;
+  if (pos_stride < 0) return FA_ERR_INVALID_ARG;
+  if ((rc = first_error({check_tensor(q, q_strides, dtype), check_tensor(k, k_strides, dtype),
+                         check_tensor(q_out, q_out_strides, dtype), check_tensor(k_out, k_out_strides, dtype),
+                         check_rope_ptrs(q_weight, k_weight, cos_table, sin_table, positions, rot_dim,
+                                         weight_dtype)})))
+    return rc;
+  fa::RopeParams p;
+  fill_rope(p, q, k, q_weight, k_weight, cos_table, sin_table, positions, pos_stride, B, N, Hq, Hk, d, rot_dim,
+            interleaved, max_pos, weight_dtype, eps);
+  if (has_axes && (rc = check_axes(axes, rot_dim, &p.ax))) return rc;
+  p.q.out = q_out;
+  p.k.out = k_out;
+  p.q.x_st = q_strides;
+  p.k.x_st = k_strides;
+  p.q.out_st = q_out_strides;
+  p.k.out_st = k_out_strides;
+  if ((rc = fa::check_device_ptrs({q, k, q_out, k_out, q_weight, k_weight, cos_table, sin_table, positions,
+                                   p.ax.positions})))
+    return rc;
+  return cuda_rc(fa::launch_norm_rope_fwd(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int norm_rope_bwd_run(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                      const void* q_weight, const void* k_weight, void* dq_weight, void* dk_weight,
+                      const float* cos_table, const float* sin_table, const int* positions, int64_t pos_stride,
+                      int B, int N, int Hq, int Hk, int d, int rot_dim, int interleaved, int max_pos,
+                      fa_strides q_strides, fa_strides k_strides, fa_strides dq_out_strides,
+                      fa_strides dk_out_strides, fa_strides dq_strides, fa_strides dk_strides, fa_dtype dtype,
+                      fa_dtype weight_dtype, float eps, bool has_axes, const fa_rope_axes* axes, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = check_rope(B, N, Hq, Hk, d, rot_dim, max_pos, dtype, weight_dtype, eps);
+  if (rc) return rc;
+  if (pos_stride < 0) return FA_ERR_INVALID_ARG;
+  if (!q_weight != !dq_weight || !k_weight != !dk_weight) return FA_ERR_INVALID_ARG;
+  const int w = weight_dtype == FA_F32 ? 4 : 2;
+  if (!aligned_to(dq_weight, w) || !aligned_to(dk_weight, w)) return FA_ERR_ALIGNMENT;
+  if ((rc = first_error({check_tensor(q, q_strides, dtype), check_tensor(k, k_strides, dtype),
+                         check_tensor(dq_out, dq_out_strides, dtype), check_tensor(dk_out, dk_out_strides, dtype),
+                         check_tensor(dq, dq_strides, dtype), check_tensor(dk, dk_strides, dtype),
+                         check_rope_ptrs(q_weight, k_weight, cos_table, sin_table, positions, rot_dim,
+                                         weight_dtype)})))
+    return rc;
+  if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(d))
+    return FA_ERR_WORKSPACE;
+  fa::RopeParams p;
+  fill_rope(p, q, k, q_weight, k_weight, cos_table, sin_table, positions, pos_stride, B, N, Hq, Hk, d, rot_dim,
+            interleaved, max_pos, weight_dtype, eps);
+  if (has_axes && (rc = check_axes(axes, rot_dim, &p.ax))) return rc;
+  p.q.dout = dq_out;
+  p.k.dout = dk_out;
+  p.q.dx = dq;
+  p.k.dx = dk;
+  p.q.dw = dq_weight;
+  p.k.dw = dk_weight;
+  p.q.x_st = q_strides;
+  p.k.x_st = k_strides;
+  p.q.out_st = dq_out_strides;
+  p.k.out_st = dk_out_strides;
+  p.q.dx_st = dq_strides;
+  p.k.dx_st = dk_strides;
+  p.part = static_cast<float*>(workspace);
+  if ((rc = fa::check_device_ptrs({q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos_table,
+                                   sin_table, positions, p.ax.positions, workspace})))
+    return rc;
+  return cuda_rc(fa::launch_norm_rope_bwd(p, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 // Checks that do not depend on pointers, shared with the workspace size.
@@ -204,26 +300,20 @@ int fa_qk_norm_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, 
                         int64_t pos_stride, int B, int N, int Hq, int Hk, int d, int rot_dim, int interleaved,
                         int max_pos, fa_strides q_strides, fa_strides k_strides, fa_strides q_out_strides,
                         fa_strides k_out_strides, fa_dtype dtype, fa_dtype weight_dtype, float eps, void* stream) {
-  int rc = check_rope(B, N, Hq, Hk, d, rot_dim, max_pos, dtype, weight_dtype, eps);
-  if (rc) return rc;
-  if (pos_stride < 0) return FA_ERR_INVALID_ARG;
-  if ((rc = first_error({check_tensor(q, q_strides, dtype), check_tensor(k, k_strides, dtype),
-                         check_tensor(q_out, q_out_strides, dtype), check_tensor(k_out, k_out_strides, dtype),
-                         check_rope_ptrs(q_weight, k_weight, cos_table, sin_table, positions, rot_dim,
-                                         weight_dtype)})))
-    return rc;
-  fa::RopeParams p;
-  fill_rope(p, q, k, q_weight, k_weight, cos_table, sin_table, positions, pos_stride, B, N, Hq, Hk, d, rot_dim,
-            interleaved, max_pos, weight_dtype, eps);
-  p.q.out = q_out;
-  p.k.out = k_out;
-  p.q.x_st = q_strides;
-  p.k.x_st = k_strides;
-  p.q.out_st = q_out_strides;
-  p.k.out_st = k_out_strides;
-  if ((rc = fa::check_device_ptrs({q, k, q_out, k_out, q_weight, k_weight, cos_table, sin_table, positions})))
-    return rc;
-  return cuda_rc(fa::launch_norm_rope_fwd(p, dtype, static_cast<cudaStream_t>(stream)));
+  return norm_rope_fwd_run(q, k, q_out, k_out, q_weight, k_weight, cos_table, sin_table, positions, pos_stride, B, N, Hq, Hk, d, rot_dim,
+                           interleaved, max_pos, q_strides, k_strides, q_out_strides, k_out_strides, dtype, weight_dtype,
+                           eps, false, nullptr, stream);
+}
+
+int fa_qk_norm_rope_axes_fwd(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                             const void* k_weight, const float* cos_table, const float* sin_table,
+                             const fa_rope_axes* axes, int B, int N, int Hq, int Hk, int d, int rot_dim,
+                             int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
+                             fa_strides q_out_strides, fa_strides k_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                             float eps, void* stream) {
+  return norm_rope_fwd_run(q, k, q_out, k_out, q_weight, k_weight, cos_table, sin_table, nullptr, 0, B, N, Hq, Hk, d, rot_dim,
+                           interleaved, max_pos, q_strides, k_strides, q_out_strides, k_out_strides, dtype, weight_dtype,
+                           eps, true, axes, stream);
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
@@ -237,46 +327,29 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
                         fa_strides q_strides, fa_strides k_strides, fa_strides dq_out_strides,
                         fa_strides dk_out_strides, fa_strides dq_strides, fa_strides dk_strides, fa_dtype dtype,
                         fa_dtype weight_dtype, float eps, void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = check_rope(B, N, Hq, Hk, d, rot_dim, max_pos, dtype, weight_dtype, eps);
-  if (rc) return rc;
-  if (pos_stride < 0) return FA_ERR_INVALID_ARG;
-  if (!q_weight != !dq_weight || !k_weight != !dk_weight) return FA_ERR_INVALID_ARG;
-  const int w = weight_dtype == FA_F32 ? 4 : 2;
-  if (!aligned_to(dq_weight, w) || !aligned_to(dk_weight, w)) return FA_ERR_ALIGNMENT;
-  if ((rc = first_error({check_tensor(q, q_strides, dtype), check_tensor(k, k_strides, dtype),
-                         check_tensor(dq_out, dq_out_strides, dtype), check_tensor(dk_out, dk_out_strides, dtype),
-                         check_tensor(dq, dq_strides, dtype), check_tensor(dk, dk_strides, dtype),
-                         check_rope_ptrs(q_weight, k_weight, cos_table, sin_table, positions, rot_dim,
-                                         weight_dtype)})))
-    return rc;
-  if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < fa_qk_norm_rope_bwd_workspace_size(d))
-    return FA_ERR_WORKSPACE;
-  fa::RopeParams p;
-  fill_rope(p, q, k, q_weight, k_weight, cos_table, sin_table, positions, pos_stride, B, N, Hq, Hk, d, rot_dim,
-            interleaved, max_pos, weight_dtype, eps);
-  p.q.dout = dq_out;
-  p.k.dout = dk_out;
-  p.q.dx = dq;
-  p.k.dx = dk;
-  p.q.dw = dq_weight;
-  p.k.dw = dk_weight;
-  p.q.x_st = q_strides;
-  p.k.x_st = k_strides;
-  p.q.out_st = dq_out_strides;
-  p.k.out_st = dk_out_strides;
-  p.q.dx_st = dq_strides;
-  p.k.dx_st = dk_strides;
-  p.part = static_cast<float*>(workspace);
-  if ((rc = fa::check_device_ptrs({q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos_table,
-                                   sin_table, positions, workspace})))
-    return rc;
-  return cuda_rc(fa::launch_norm_rope_bwd(p, dtype, static_cast<cudaStream_t>(stream)));
+  return norm_rope_bwd_run(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos_table, sin_table,
+                           positions, pos_stride, B, N, Hq, Hk, d, rot_dim, interleaved, max_pos, q_strides, k_strides,
+                           dq_out_strides, dk_out_strides, dq_strides, dk_strides, dtype, weight_dtype, eps, false, nullptr,
+                           workspace, workspace_bytes, stream);
+}
+
+int fa_qk_norm_rope_axes_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                             const void* q_weight, const void* k_weight, void* dq_weight, void* dk_weight,
+                             const float* cos_table, const float* sin_table, const fa_rope_axes* axes, int B, int N,
+                             int Hq, int Hk, int d, int rot_dim, int interleaved, int max_pos, fa_strides q_strides,
+                             fa_strides k_strides, fa_strides dq_out_strides, fa_strides dk_out_strides,
+                             fa_strides dq_strides, fa_strides dk_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                             float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  return norm_rope_bwd_run(q, k, dq_out, dk_out, dq, dk, q_weight, k_weight, dq_weight, dk_weight, cos_table, sin_table,
+                           nullptr, 0, B, N, Hq, Hk, d, rot_dim, interleaved, max_pos, q_strides, k_strides,
+                           dq_out_strides, dk_out_strides, dq_strides, dk_strides, dtype, weight_dtype, eps, true, axes,
+                           workspace, workspace_bytes, stream);
 }
 
 int fa_kv8_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* k, const void* v, int T,
                   fa_strides k_strides, fa_strides v_strides, fa_dtype dtype, void* stream) {
   return append_run(cache, seqs, nullptr, k, v, nullptr, nullptr, nullptr, nullptr, nullptr, T, 0, 0, 0, 0, {},
-                    k_strides, v_strides, {}, dtype, dtype, 0.f, false, stream);
+                    k_strides, v_strides, {}, dtype, dtype, 0.f, false, false, nullptr, stream);
 }
 
 int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, const void* k,
@@ -287,7 +360,18 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
                             float eps, void* stream) {
   return append_run(cache, seqs, q, k, v, q_out, q_weight, k_weight, cos_table, sin_table, T, Hq, rot_dim,
                     interleaved, max_pos, q_strides, k_strides, v_strides, q_out_strides, dtype, weight_dtype, eps,
-                    true, stream);
+                    true, false, nullptr, stream);
+}
+
+int fa_kv8_norm_rope_axes_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, const void* k,
+                                 const void* v, void* q_out, const void* q_weight, const void* k_weight,
+                                 const float* cos_table, const float* sin_table, const fa_rope_axes* axes, int T, int Hq,
+                                 int rot_dim, int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
+                                 fa_strides v_strides, fa_strides q_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                                 float eps, void* stream) {
+  return append_run(cache, seqs, q, k, v, q_out, q_weight, k_weight, cos_table, sin_table, T, Hq, rot_dim,
+                    interleaved, max_pos, q_strides, k_strides, v_strides, q_out_strides, dtype, weight_dtype, eps,
+                    true, true, axes, stream);
 }
 
 size_t fa_kv8_attn_workspace_size(int B, int T, int Hq, int H, int d, int page_size, int max_pages, int max_seqlen,

@@ -67,8 +67,18 @@ struct RopeSide {
   int span;  // set by the launcher: consecutive rows of a row group
 };
 
+// Positions with several axes: pair i of the rotated values takes the table row of the position on its
+// axis, 2 bits a pair (axes <= 4, pairs <= 64). axes = 0: one position a token, the call's own way.
+struct RopeAxes {
+  int axes;
+  uint32_t pair_axis[4];
+  const int* positions;  // [B, N, axes] by its strides
+  int64_t sb, sn, sa;
+};
+
 struct RopeParams {
   RopeSide q, k;
+  RopeAxes ax;
   const float* cos;  // [max_pos, rot / 2]
   const float* sin;
   const int* positions;  // [B, N], rows pos_stride apart, or null: 0 .. N - 1
@@ -124,6 +134,7 @@ struct Kv8AppendParams {
   const float* sin;
   int rot, max_pos, neighbours, w_f32;
   float eps;
+  RopeAxes ax;  // axes = 0: positions are places in the sequences
   int kv_heads, q_heads;  // set by the launcher: heads of k and v, and of q, that a block takes
 };
 cudaError_t launch_kv8_append(Kv8AppendParams& p, bool bf16, cudaStream_t st);

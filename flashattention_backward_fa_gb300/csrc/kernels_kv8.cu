@@ -137,8 +137,9 @@ __device__ __forceinline__ NewTokens new_tokens(const Kv8Cache& c, int b, int T)
 // weights are loaded once for all heads, and the next head's rows are on their way
 // while one is finished. kRows rows of a page a thread; blockDim.x * kRows * 16
 // values hold a page's new rows. kNorm: 0 append alone, 1 / 2 norm and rotation
-// with partners rot / 2 apart / neighbours; kPartial: rot < D.
-template <typename T, int D, int kRows, int kNorm, bool kPartial>
+// with partners rot / 2 apart / neighbours; kPartial: rot < D; kAxes: positions are
+// given (on one axis or several), not places in the sequences.
+template <typename T, int D, int kRows, int kNorm, bool kPartial, bool kAxes>
 __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows == 4 ? 4 : 8) : 1)
     kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   constexpr int G = D / 16;
@@ -240,9 +241,13 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
   if (kNorm != 0 && !is_v) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const long long row =
-          live[i] ? (long long)min(n.start + first + row0 + i * groups, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
-      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, live[i] ? p.rot : 0, cc[i], ss[i]);
+      const int t = first + row0 + i * groups;
+      if constexpr (kAxes) {
+        load_rotation_axes<kNeighbours>(p.ax, p.cos, p.sin, p.max_pos, b, t, at, live[i] ? p.rot : 0, cc[i], ss[i]);
+      } else {
+        const long long row = live[i] ? (long long)min(n.start + t, max(p.max_pos - 1, 0)) * (p.rot >> 1) : 0;
+        load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, live[i] ? p.rot : 0, cc[i], ss[i]);
+      }
     }
     stage_weights<T>(is_q ? p.q_w : p.k_w, p.w_f32, D, w);
     __syncthreads();
@@ -334,9 +339,9 @@ __global__ void __launch_bounds__(kNorm == 0 ? 256 : 512, kNorm == 0 ? (kRows ==
   if (kNorm != 0) copies_wait<0>();
 }
 
-template <typename T, int D, int kRows, int kNorm, bool kPartial>
+template <typename T, int D, int kRows, int kNorm, bool kPartial, bool kAxes = false>
 cudaError_t launch_norm(const Kv8AppendParams& p, dim3 grid, int threads, cudaStream_t st) {
-  constexpr auto kKernel = kv8_append_kernel<T, D, kRows, kNorm, kPartial>;
+  constexpr auto kKernel = kv8_append_kernel<T, D, kRows, kNorm, kPartial, kAxes>;
   const cudaError_t e = allow_smem<kKernel>(RowRing<T, 2 * kRows, kAhead>::bytes(512));
   if (e != cudaSuccess) return e;
   return launch_chained(kKernel, grid, threads, RowRing<T, 2 * kRows, kAhead>::bytes(threads), 1, p, st);
@@ -346,6 +351,10 @@ template <typename T, int D, int kRows>
 cudaError_t launch_rows(const Kv8AppendParams& p, dim3 grid, int threads, cudaStream_t st) {
   if constexpr (kRows <= 2) {
     if (p.q != nullptr) {
+      // (whole heads have no form of their own here: the zeros in the partners' places cost less than it)
+      if (p.ax.axes)
+        return p.neighbours ? launch_norm<T, D, kRows, 2, true, true>(p, grid, threads, st)
+                            : launch_norm<T, D, kRows, 1, true, true>(p, grid, threads, st);
       if (p.rot < D)
         return p.neighbours ? launch_norm<T, D, kRows, 2, true>(p, grid, threads, st)
                             : launch_norm<T, D, kRows, 1, true>(p, grid, threads, st);
@@ -353,7 +362,7 @@ cudaError_t launch_rows(const Kv8AppendParams& p, dim3 grid, int threads, cudaSt
                           : launch_norm<T, D, kRows, 1, false>(p, grid, threads, st);
     }
   }
-  return launch_chained(kv8_append_kernel<T, D, kRows, 0, true>, grid, threads, 0, 1, p, st);
+  return launch_chained(kv8_append_kernel<T, D, kRows, 0, true, false>, grid, threads, 0, 1, p, st);
 }
 
 template <typename T, int D>

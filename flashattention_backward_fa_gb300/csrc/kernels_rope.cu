@@ -35,7 +35,19 @@ __device__ __forceinline__ long long table_row(const RopeParams& p, long long b,
   return (long long)min(max(pos, 0), p.max_pos - 1) * (p.rot >> 1);
 }
 
-template <typename T, int D, bool kNeighbours>
+// cos and sin of a lane's pairs for token (b, n); 1 and 0 where there is none.
+template <bool kNeighbours, bool kAxes>
+__device__ __forceinline__ void token_rotation(const RopeParams& p, long long b, int n, bool has, const LanePlace& at,
+                                               float (&c)[8], float (&s)[8]) {
+  if constexpr (kAxes) {
+    load_rotation_axes<kNeighbours>(p.ax, p.cos, p.sin, p.max_pos, b, n, at, has ? p.rot : 0, c, s);
+  } else {
+    const long long row = has && p.rot ? table_row(p, b, n) : 0;
+    load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, has ? p.rot : 0, c, s);
+  }
+}
+
+template <typename T, int D, bool kNeighbours, bool kAxes>
 __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ __align__(16) float w[D];
@@ -47,13 +59,15 @@ __global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const __
       (long long)(blockIdx.x - (is_k ? p.q_blocks : 0)) * (kRopeThreads / (D / 16)) + threadIdx.x / (D / 16);
   norm_rope_rows<T, D, kNeighbours, kFwdDepth>(
       ring, static_cast<const T*>(sd.x), static_cast<T*>(sd.out), sd.x_st, sd.out_st, (long long)p.B * p.N * sd.H, p.N,
-      sd.H, group * sd.span, sd.span, sd.w, p.w_f32, w, p.cos, p.sin, p.rot, p.eps,
-      [&](long long b, int n) { return p.rot ? table_row(p, b, n) : 0ll; });
+      sd.H, group * sd.span, sd.span, sd.w, p.w_f32, w, p.rot, p.eps,
+      [&](long long b, int n, bool has, const LanePlace& at, float (&c)[8], float (&s)[8]) {
+        token_rotation<kNeighbours, kAxes>(p, b, n, has, at, c, s);
+      });
 }
 
 // Each row group takes sd.span consecutive rows, as in the forward; its lanes
 // keep the weight gradients of their columns.
-template <typename T, int D, bool kNeighbours, bool kPartial>
+template <typename T, int D, bool kNeighbours, bool kPartial, bool kAxes>
 __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int G = D / 16, kGroups = kRopeThreads / G;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -105,11 +119,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) norm_rope_bwd_kernel(const __
   bool token = true;
   for (int i = 0; i < sd.span; ++i) {
     fetch();
-    if (token) {
-      const bool ok = i < live;
-      const long long row = ok && p.rot ? table_row(p, wo.b, wo.n) : 0;
-      load_rotation<kNeighbours>(p.cos + row, p.sin + row, at, ok ? p.rot : 0, c, s);
-    }
+    if (token) token_rotation<kNeighbours, kAxes>(p, wo.b, wo.n, i < live, at, c, s);
     copies_wait<kBwdDepth - 1>();
     Raw8<T> raw;
     uint64_t xa[4], xb[4], ga[4], gb[4];
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
     RowWalk a;
     a.start(row, p.N, sd.H, sd.x_st);
     const float* x = static_cast<const float*>(sd.x) + a.at;
-    const long long at = p.rot ? table_row(p, a.b, a.n) : 0;
+    const long long at = p.rot && !p.ax.axes ? table_row(p, a.b, a.n) : 0;
     float xv[4], gv[4], ss = 0.f;
     const float* go = kBackward ? static_cast<const float*>(sd.dout) + a.offset(sd.out_st) : nullptr;
 #pragma unroll
@@ -270,7 +280,13 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_any_f32_kernel(const _
         const int pair = p.neighbours ? e >> 1 : (e < h ? e : e - h);
         const int other = p.neighbours ? e ^ 1 : (e < h ? e + h : e - h);
         const bool low = p.neighbours ? (e & 1) == 0 : e < h;
-        const float c = p.cos[at + pair], s = low == kBackward ? p.sin[at + pair] : -p.sin[at + pair];
+        long long place = at + pair;
+        if (p.ax.axes) {
+          const int axis = p.ax.pair_axis[pair >> 4] >> (2 * (pair & 15)) & 3;
+          const int pos = p.ax.positions[a.b * p.ax.sb + a.n * p.ax.sn + axis * p.ax.sa];
+          place = (long long)min(max(pos, 0), p.max_pos - 1) * h + pair;
+        }
+        const float c = p.cos[place], s = low == kBackward ? p.sin[place] : -p.sin[place];
         y[j] = fmaf(y[j], c, buf[warp][other] * s);
       }
     }
@@ -333,28 +349,36 @@ cudaError_t launch_ring(const RopeParams& p, int bytes, cudaStream_t st) {
   return launch_chained(kKernel, p.blocks, kRopeThreads, bytes, 1, p, st);
 }
 
-template <typename T>
-cudaError_t launch_fwd(const RopeParams& p, cudaStream_t st) {
+template <typename T, int D, bool kAxes>
+cudaError_t launch_fwd_d(const RopeParams& p, cudaStream_t st) {
   constexpr int bytes = RowRing<T, 2, kFwdDepth>::bytes(kRopeThreads);
-  if (p.d == 64)
-    return p.neighbours ? launch_ring<norm_rope_fwd_kernel<T, 64, true>>(p, bytes, st)
-                        : launch_ring<norm_rope_fwd_kernel<T, 64, false>>(p, bytes, st);
-  return p.neighbours ? launch_ring<norm_rope_fwd_kernel<T, 128, true>>(p, bytes, st)
-                      : launch_ring<norm_rope_fwd_kernel<T, 128, false>>(p, bytes, st);
+  return p.neighbours ? launch_ring<norm_rope_fwd_kernel<T, D, true, kAxes>>(p, bytes, st)
+                      : launch_ring<norm_rope_fwd_kernel<T, D, false, kAxes>>(p, bytes, st);
 }
 
-template <typename T, int D, bool kPartial>
+template <typename T>
+cudaError_t launch_fwd(const RopeParams& p, cudaStream_t st) {
+  if (p.d == 64) return p.ax.axes ? launch_fwd_d<T, 64, true>(p, st) : launch_fwd_d<T, 64, false>(p, st);
+  return p.ax.axes ? launch_fwd_d<T, 128, true>(p, st) : launch_fwd_d<T, 128, false>(p, st);
+}
+
+template <typename T, int D, bool kPartial, bool kAxes>
 cudaError_t launch_bwd_d(const RopeParams& p, cudaStream_t st) {
   constexpr int bytes = RowRing<T, 4, kBwdDepth>::bytes(kRopeThreads);
   static_assert(bytes >= kRopeThreads * 16 * 4, "the block's weight gradients fit into the ring");
-  return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, D, true, kPartial>>(p, bytes, st)
-                      : launch_ring<norm_rope_bwd_kernel<T, D, false, kPartial>>(p, bytes, st);
+  return p.neighbours ? launch_ring<norm_rope_bwd_kernel<T, D, true, kPartial, kAxes>>(p, bytes, st)
+                      : launch_ring<norm_rope_bwd_kernel<T, D, false, kPartial, kAxes>>(p, bytes, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_bwd_r(const RopeParams& p, cudaStream_t st) {
+  if (p.ax.axes) return p.rot < D ? launch_bwd_d<T, D, true, true>(p, st) : launch_bwd_d<T, D, false, true>(p, st);
+  return p.rot < D ? launch_bwd_d<T, D, true, false>(p, st) : launch_bwd_d<T, D, false, false>(p, st);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const RopeParams& p, cudaStream_t st) {
-  if (p.d == 64) return p.rot < 64 ? launch_bwd_d<T, 64, true>(p, st) : launch_bwd_d<T, 64, false>(p, st);
-  return p.rot < 128 ? launch_bwd_d<T, 128, true>(p, st) : launch_bwd_d<T, 128, false>(p, st);
+  return p.d == 64 ? launch_bwd_r<T, 64>(p, st) : launch_bwd_r<T, 128>(p, st);
 }
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }

@@ -165,6 +165,43 @@ __device__ __forceinline__ void load_rotation(const float* cos_row, const float*
   }
 }
 
+// The same where the pairs' rows differ by their axes (RopeAxes): the token's positions on all axes are
+// read side by side, then each run of four pairs with one axis by 16-byte loads and others value by
+// value. b, n: the token's place in the positions. Reading the positions run by run instead, each load
+// waiting for its own, and all values one by one are the two plainer forms.
+template <bool kNeighbours, typename Axes>
+__device__ __forceinline__ void load_rotation_axes(const Axes& ax, const float* cos, const float* sin, int max_pos,
+                                                   long long b, long long n, const LanePlace& at, int rot,
+                                                   float (&c)[8], float (&s)[8]) {
+  const int run[2] = {kNeighbours ? at.a >> 1 : at.a, kNeighbours ? at.b >> 1 : at.a + 4};
+  const bool has[2] = {at.a < rot, (kNeighbours ? at.b : at.a) < rot};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  if (!has[0] && !has[1]) return;
+  const int* from = ax.positions + b * ax.sb + n * ax.sn;
+  long long row[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) row[a] = a < ax.axes ? (long long)min(max(from[a * ax.sa], 0), max_pos - 1) * (rot >> 1) : 0;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (!has[r]) continue;
+    const uint32_t bits = ax.pair_axis[run[r] >> 4] >> (2 * (run[r] & 15)) & 0xFFu;  // four pairs
+    const auto row_of = [&](uint32_t x) { return x < 2 ? (x == 0 ? row[0] : row[1]) : (x == 2 ? row[2] : row[3]); };
+    if (bits == (bits & 3u) * 0x55u) {
+      const long long w = row_of(bits & 3u) + run[r];
+      read4(cos + w, c + 4 * r);
+      read4(sin + w, s + 4 * r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long w = row_of(bits >> (2 * i) & 3u) + run[r] + i;
+        c[4 * r + i] = cos[w];
+        s[4 * r + i] = sin[w];
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);
@@ -327,14 +364,13 @@ struct RowRing {
 // Rows [first, first + count) of one tensor by one row group (D / 16 lanes; the
 // groups of a warp call it together, each with its own rows and all with the same
 // count). kDepth - 1 rows are on their way while a row is computed.
-// table_at(b, n): offset of the token's table rows. The weights are staged into w (a
+// rotation(b, n, has, at, c, s): the token's cos and sin (has: there is one). The weights are staged into w (a
 // block-wide step) once the first copies are under way.
-template <typename T, int D, bool kNeighbours, int kDepth, typename TableAt>
+template <typename T, int D, bool kNeighbours, int kDepth, typename Rotation>
 __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, const fa_strides& x_st,
                                                const fa_strides& out_st, long long rows, int N, int H, long long first,
-                                               int count, const void* weights, bool w_f32, float* w,
-                                               const float* cos, const float* sin, int rot, float eps,
-                                               const TableAt& table_at) {
+                                               int count, const void* weights, bool w_f32, float* w, int rot, float eps,
+                                               const Rotation& rotation) {
   RowRing<T, 2, kDepth> ring(smem);
   const LanePlace at = lane_place<D, kNeighbours, true>(threadIdx.x % (D / 16), rot);  // (costs nothing here)
   const int live = (int)min((long long)count, max(rows - first, 0ll));
@@ -369,11 +405,7 @@ __device__ __forceinline__ void norm_rope_rows(void* smem, const T* x, T* out, c
   bool token = true;
   for (int i = 0; i < count; ++i) {
     fetch();
-    if (token) {
-      const bool ok = i < live;
-      const long long row = ok ? table_at(to.b, to.n) : 0;
-      load_rotation<kNeighbours>(cos + row, sin + row, at, ok ? rot : 0, c, s);
-    }
+    if (token) rotation(to.b, to.n, i < live, at, c, s);
     copies_wait<kDepth - 1>();
     Raw8<T> a, b;
     ring.take(0, a);

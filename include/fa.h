@@ -336,6 +336,37 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
                         fa_dtype weight_dtype, float eps, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The same with positions on several axes (time, height and width of images and
+ * video; text tokens have the same position on each): pair i of the rotated values
+ * takes column i of the table row of the token's position on the pair's axis,
+ * cos_table[pos[pair_axis[i]]][i]. pair_axis: rot_dim / 2 entries in [0, axes) in HOST
+ * memory, read during the call (null: all 0). positions: device int32, axis a of
+ * token (b, n) at b * stride_b + n * stride_n + a * stride_axis (strides not
+ * negative), clamped into [0, max_pos). 1 to 4 axes; rot_dim > 0. Everything else as
+ * above, the backward's workspace too.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int axes;
+  const unsigned char* pair_axis;
+  const int* positions;
+  int64_t stride_b, stride_n, stride_axis;
+} fa_rope_axes;
+
+int fa_qk_norm_rope_axes_fwd(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                             const void* k_weight, const float* cos_table, const float* sin_table,
+                             const fa_rope_axes* axes, int B, int N, int Hq, int Hk, int d, int rot_dim,
+                             int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
+                             fa_strides q_out_strides, fa_strides k_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                             float eps, void* stream);
+int fa_qk_norm_rope_axes_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                             const void* q_weight, const void* k_weight, void* dq_weight, void* dk_weight,
+                             const float* cos_table, const float* sin_table, const fa_rope_axes* axes, int B, int N,
+                             int Hq, int Hk, int d, int rot_dim, int interleaved, int max_pos, fa_strides q_strides,
+                             fa_strides k_strides, fa_strides dq_out_strides, fa_strides dk_out_strides,
+                             fa_strides dq_strides, fa_strides dk_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                             float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * A paged key/value cache in 8 bits, with a scale for each page and head.
  *
  * Pages hold page_size tokens (16, 32, 64 or 128) of H key heads, d in {64,
@@ -398,6 +429,15 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
                             int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
                             fa_strides v_strides, fa_strides q_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
                             float eps, void* stream);
+
+/* The same with positions that are given (axes, as above; token n of a sequence is row n
+ * of the call's tensors) instead of the tokens' places in their sequences. */
+int fa_kv8_norm_rope_axes_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, const void* k,
+                                 const void* v, void* q_out, const void* q_weight, const void* k_weight,
+                                 const float* cos_table, const float* sin_table, const fa_rope_axes* axes, int T, int Hq,
+                                 int rot_dim, int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
+                                 fa_strides v_strides, fa_strides q_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
+                                 float eps, void* stream);
 
 /* Attention of the new tokens' queries q ([B, T, Hq, d], fp16 or bf16) over the
  * cache: o ([B, T, Hq, d], q's type) and lse ([B, Hq, T] contiguous fp32, natural
