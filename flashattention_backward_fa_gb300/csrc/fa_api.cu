@@ -76,19 +76,28 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 4-D map over a [B, N, H, d] tensor (dims innermost first: d, N, H, B), 128-byte
-// swizzle, boxes of 64 head-dim elements x `rows` sequence rows.
-bool make_map(CUtensorMap* m, const void* base, const AttnParams& p, bool bf16, int rows) {
+}  // namespace
+
+namespace fa {
+bool make_tensor_map(CUtensorMap* m, const void* base, bool bf16, int B, int N, int H, int d, fa_strides st, int rows,
+                     int heads) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.N, (cuuint64_t)p.H, (cuuint64_t)p.B};
-  const cuuint64_t strides[3] = {(cuuint64_t)p.sn * 2, (cuuint64_t)p.sh * 2, (cuuint64_t)p.sb * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)st.n * 2, (cuuint64_t)st.h * 2, (cuuint64_t)st.b * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)heads, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace fa
+
+namespace {
+
+bool make_map(CUtensorMap* m, const void* base, const AttnParams& p, bool bf16, int rows) {
+  return fa::make_tensor_map(m, base, bf16, p.B, p.N, p.H, p.d, {p.sb, p.sn, p.sh}, rows, 1);
 }
 
 // The attention bias as a 4-D map (keys, query rows, heads, batches); a
@@ -157,6 +166,9 @@ WsLayout ws_layout(int B, int H, int N, int d, int dtype, int deterministic) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
+namespace fa {
 // Tensor-map encoding (cuTensorMapEncodeTiled) is a driver call that needs a
 // current context on the calling thread. A thread whose CUDA calls so far bound
 // none (pointer queries, this library's cached lookups) would see it fail, so
@@ -168,9 +180,6 @@ int bind_device_context() {
   return FA_OK;
 }
 
-}  // namespace
-
-namespace fa {
 // Every buffer a kernel touches must be memory of the current device (or
 // managed memory): a host or another device's pointer would make the kernels
 // fault. Checked last, after the cheap argument checks and before any launch.
@@ -194,6 +203,7 @@ int check_device_ptrs(std::initializer_list<const void*> ptrs) {
 
 namespace {
 
+using fa::bind_device_context;
 using fa::check_device_ptrs;
 
 // Validation shared by the forward and the backward. Returns FA_OK or an error.

@@ -6,18 +6,6 @@
 
 #include "fa_cross.h"
 
-namespace fa {
-
-CrossPlan cross_plan(int B, int Nq, int Nk, int Hq, int Hk, int d, int dtype) {
-  CrossPlan c;
-  const long long q_units = (long long)B * Hq * ((Nq + 31) / 32), k_units = (long long)B * Hk * ((Nk + 31) / 32);
-  cross_splits(Nk, 64, q_units, 304, 2, &c.k_splits, &c.k_chunk);
-  cross_splits((Nq + 63) / 64 * (Hq / Hk), 1, k_units, 304, 2, &c.q_splits, &c.q_chunk);
-  return c;
-}
-
-}  // namespace fa
-
 namespace {
 
 using fa::aligned_to;
@@ -33,9 +21,11 @@ int check_shape(const fa_cross_shape* s, fa_dtype dtype) {
     return FA_ERR_INVALID_ARG;
   if (dtype != FA_F32 && dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
   if (dtype == FA_F32 ? s->d > 128 : (s->d != 64 && s->d != 128)) return FA_ERR_UNSUPPORTED;
-  // batches and heads are grid extents; rows of a head, and query steps of a group, are counted in 31 bits
+  // batches and heads are grid extents; the kernels' units of work and their steps are counted in 31 bits
   if (s->B > 65535 || s->Hq > 65535 || s->Nq > (1 << 24) || s->Nk > (1 << 24)) return FA_ERR_UNSUPPORTED;
   if ((long long)s->B * s->Hq > (1 << 24) || (long long)s->Nq * (s->Hq / s->Hk) > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if ((long long)s->B * s->Hq * ((s->Nq + 31ll) / 32) > (1 << 30) || (long long)s->B * s->Hk * ((s->Nk + 31ll) / 32) > (1 << 30))
+    return FA_ERR_UNSUPPORTED;
   if (!aligned_to(s->q_lens, 4) || !aligned_to(s->k_lens, 4)) return FA_ERR_ALIGNMENT;
   return FA_OK;
 }
@@ -79,8 +69,53 @@ void fill(CrossParams& p, const fa_cross_shape* s, const CrossPlan& plan, float 
   p.plan = plan;
 }
 
-CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype) {
-  return fa::cross_plan(s->B, s->Nq, s->Nk, s->Hq, s->Hk, s->d, dtype);
+long long div_up(long long a, long long b) { return (a + b - 1) / b; }
+
+// Splits of an axis of `steps` for `units` independent pieces of work on `places` that run them round by
+// round: the number that makes the rounds' steps fewest, where a unit costs `start` steps more than its
+// own and the join `join` in all.
+int best_splits(long long units, int steps, int places, int start, int join) {
+  const long long most = std::min<long long>(steps, 4 * places / units + 1);
+  int best = 1;
+  long long least = div_up(units, places) * (steps + start);
+  for (int s = 2; s <= most; ++s) {
+    const long long cost = div_up(units * s, places) * (div_up(steps, s) + start) + join;
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return (int)div_up(steps, div_up(steps, best));
+}
+
+CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype, bool backward) {
+  CrossPlan c;
+  const int G = s->Hq / s->Hk;
+  c.q_tile = fa::cross_tile(s->Nq, G, 7, 0);
+  c.step = fa::cross_tile(s->Nq, G, 6, 2);
+  c.q_splits = 1;
+  if (dtype == FA_F32) {
+    const long long q_units = (long long)s->B * s->Hq * div_up(s->Nq, 32), k_units = (long long)s->B * s->Hk * div_up(s->Nk, 32);
+    c.k_splits = best_splits(q_units, (int)div_up(s->Nk, 64), 304, 1, 3);
+    if (backward) c.q_splits = best_splits(k_units, (int)div_up(s->Nq, 64) * G, 152, 1, 3);
+    return c;
+  }
+  const long long groups = (long long)s->B * s->Hk, tiles = c.q_tile.count(s->Nq, G);
+  if (!backward) {
+    c.k_splits = best_splits(groups * div_up(tiles, 2), (int)div_up(s->Nk, 128), 152, 1, 4);
+  } else {
+    c.k_splits = best_splits(groups * tiles, (int)div_up(s->Nk, 128), 152, 1, 4);
+    c.q_splits = best_splits(groups * div_up(s->Nk, 128), c.step.count(s->Nq, G), 152, 2, 6);
+  }
+  return c;
+}
+
+// TMA maps: of the rows of a query tile, and of 128 keys.
+bool q_map(CUtensorMap* m, const CrossParams& p, const void* base, fa_strides st, fa::CrossTile t, fa_dtype dtype) {
+  return fa::make_tensor_map(m, base, dtype == FA_BF16, p.B, p.Nq, p.Hq, p.d, st, t.queries(), t.heads());
+}
+bool k_map(CUtensorMap* m, const CrossParams& p, const void* base, fa_strides st, fa_dtype dtype) {
+  return fa::make_tensor_map(m, base, dtype == FA_BF16, p.B, p.Nk, p.Hk, p.d, st, 128, 1);
 }
 
 // Forward: [outputs of the splits | their log-sum-exps], none without splits.
@@ -113,11 +148,11 @@ BwdLayout bwd_layout(const fa_cross_shape* s, const CrossPlan& c) {
 extern "C" {
 
 size_t fa_cross_fwd_workspace_size(const fa_cross_shape* shape, fa_dtype dtype) {
-  return check_shape(shape, dtype) ? 0 : fwd_layout(shape, plan_of(shape, dtype)).total;
+  return check_shape(shape, dtype) ? 0 : fwd_layout(shape, plan_of(shape, dtype, false)).total;
 }
 
 size_t fa_cross_bwd_workspace_size(const fa_cross_shape* shape, fa_dtype dtype) {
-  return check_shape(shape, dtype) ? 0 : bwd_layout(shape, plan_of(shape, dtype)).total;
+  return check_shape(shape, dtype) ? 0 : bwd_layout(shape, plan_of(shape, dtype, true)).total;
 }
 
 int fa_cross_fwd(const fa_cross_shape* shape, const void* q, const void* k, const void* v, void* o, float* lse,
@@ -128,7 +163,7 @@ int fa_cross_fwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   if ((rc = check_all({q, k, v, o}, {q_strides, k_strides, v_strides, o_strides}, dtype))) return rc;
   if (!lse) return FA_ERR_INVALID_ARG;
   if (!aligned_to(lse, 16)) return FA_ERR_ALIGNMENT;
-  const CrossPlan plan = plan_of(shape, dtype);
+  const CrossPlan plan = plan_of(shape, dtype, false);
   const FwdLayout w = fwd_layout(shape, plan);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total))) return rc;
   if ((rc = fa::check_device_ptrs({q, k, v, o, lse, shape->q_lens, shape->k_lens, w.total ? workspace : nullptr})))
@@ -150,7 +185,17 @@ int fa_cross_fwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   }
   if ((rc = fa::status_ptr(&p.status))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = fa::launch_cross_fwd_simple(p, dtype, st);
+  cudaError_t e;
+  if (dtype == FA_F32) {
+    e = fa::launch_cross_fwd_f32(p, st);
+  } else {
+    CUtensorMap maps[3];
+    if ((rc = fa::bind_device_context())) return rc;
+    if (!q_map(&maps[0], p, q, q_strides, plan.q_tile, dtype) || !k_map(&maps[1], p, k, k_strides, dtype) ||
+        !k_map(&maps[2], p, v, v_strides, dtype))
+      return FA_ERR_CUDA;
+    e = fa::launch_cross_fwd_tc(p, dtype == FA_BF16, maps, st);
+  }
   if (e == cudaSuccess && plan.k_splits > 1) e = fa::launch_cross_join_fwd(p, dtype, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -168,7 +213,7 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
     return rc;
   if (!lse) return FA_ERR_INVALID_ARG;
   if (!aligned_to(lse, 16)) return FA_ERR_ALIGNMENT;
-  const CrossPlan plan = plan_of(shape, dtype);
+  const CrossPlan plan = plan_of(shape, dtype, true);
   const BwdLayout w = bwd_layout(shape, plan);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total))) return rc;
   if ((rc = fa::check_device_ptrs({q, k, v, o, dout, lse, dq, dk, dv, shape->q_lens, shape->k_lens, workspace})))
@@ -199,10 +244,22 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   p.part_kv = reinterpret_cast<float*>(ws + w.dkdv);
   if ((rc = fa::status_ptr(&p.status))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = dtype == FA_F32, bf16 = dtype == FA_BF16;
+  CUtensorMap steps[4], tiles[4];  // Q, K, V, dO of the two kernels
+  if (!f32) {
+    if ((rc = fa::bind_device_context())) return rc;
+    if (!q_map(&steps[0], p, q, q_strides, plan.step, dtype) || !q_map(&steps[3], p, dout, dout_strides, plan.step, dtype) ||
+        !q_map(&tiles[0], p, q, q_strides, plan.q_tile, dtype) ||
+        !q_map(&tiles[3], p, dout, dout_strides, plan.q_tile, dtype) || !k_map(&steps[1], p, k, k_strides, dtype) ||
+        !k_map(&steps[2], p, v, v_strides, dtype))
+      return FA_ERR_CUDA;
+    tiles[1] = steps[1];
+    tiles[2] = steps[2];
+  }
   cudaError_t e = fa::launch_cross_preprocess(p, dtype, st);
-  if (e == cudaSuccess) e = fa::launch_cross_dkdv_simple(p, dtype, st);
+  if (e == cudaSuccess) e = f32 ? fa::launch_cross_dkdv_f32(p, st) : fa::launch_cross_dkdv_tc(p, bf16, steps, st);
   if (e == cudaSuccess && plan.q_splits > 1) e = fa::launch_cross_join_dkdv(p, dtype, st);
-  if (e == cudaSuccess) e = fa::launch_cross_dq_simple(p, dtype, st);
+  if (e == cudaSuccess) e = f32 ? fa::launch_cross_dq_f32(p, st) : fa::launch_cross_dq_tc(p, bf16, tiles, st);
   if (e == cudaSuccess && plan.k_splits > 1) e = fa::launch_cross_join_dq(p, dtype, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

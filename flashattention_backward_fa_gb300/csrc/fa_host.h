@@ -1,5 +1,6 @@
 // Host-side entry shared by the C-ABI translation units.
 #pragma once
+#include <cuda.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -54,6 +55,14 @@ int check_bwd_args(int B, int H, int N, int d, fa_strides strides, fa_dtype dtyp
 // FA_OK if every non-null pointer is memory of the current device (or managed
 // memory), FA_ERR_INVALID_ARG otherwise; the last check before a launch.
 int check_device_ptrs(std::initializer_list<const void*> ptrs);
+
+// 4-D map over a 16-bit [B, N, H, d] tensor (dims innermost first: d, N, H, B), 128-byte
+// swizzle, boxes of 64 head-dim elements x `rows` sequence rows x `heads` heads. Needs the
+// device's context on this thread (bind_device_context).
+bool make_tensor_map(CUtensorMap* m, const void* base, bool bf16, int B, int N, int H, int d, fa_strides st, int rows,
+                     int heads);
+// Makes the current device's primary context current on the calling thread.
+int bind_device_context();
 
 // Address of the current device's status word.
 int status_ptr(unsigned int** out);

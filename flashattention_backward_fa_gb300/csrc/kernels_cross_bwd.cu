@@ -1,0 +1,947 @@
+// Backward of cross attention on the sm_103a tensor cores: two kernels over the same
+// recomputed probabilities, one that holds keys and walks queries (dK, dV), one that holds
+// queries and walks keys (dQ), so that every sum is formed on chip in a fixed order.
+//
+//   S = Q K^T, P = exp2(S * scale*log2e - L*log2e), dP = dO V^T, dS = P o (dP - D)
+//   dV += P^T dO, dK += dS^T Q over the queries of all heads of a group; dQ += dS K
+//
+// dK/dV: keys on the 128 TMEM lanes, steps of 64 query rows (of one head of the group, or
+// of several where queries are few; the steps run over all heads of the group, so shared
+// key heads cost no extra sums), S^T and dP^T in double buffers, P^T and dS^T written back
+// over them in 16 bits with their rounding residual where the tile holds probabilities
+// above 1/64, dV and dK in TMEM. dQ: 128 query rows on the lanes, steps of 128 keys.
+// Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
+// ones, warps 4-19 do the row math.
+//
+// Both are persistent grids, one CTA an SM, that take their units in a fixed stride; steps,
+// ring stages and barrier phases run on from unit to unit, so that the next unit's loads
+// and first MMAs overlap this one's end. Where there are fewer units than SMs (few keys
+// and many queries, or the other way round) the walked axis is cut into splits whose fp32
+// sums a second kernel adds in order.
+//
+// Masks. Query columns and key columns past their sequence's length get P = dS = 0 by
+// selects (S and dP there may be NaN); the rows of Q, dO and K that such columns meet in the
+// accumulating MMAs are zeroed in shared memory first (0 * NaN).
+#include "fa_cross.h"
+
+namespace fa {
+
+namespace {
+
+constexpr int kThreads = 640;  // 4 role warps + 4 row-math warpgroups
+constexpr int kStep = 64;      // query rows of a step of the dK/dV kernel
+
+// ------------------------------- dK and dV -------------------------------
+template <int D>
+struct KCfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kKVPanel = 128 * 128;   // 16 KB: 128 rows x 64 elements
+  static constexpr uint32_t kKVTile = kPanels * kKVPanel;
+  static constexpr uint32_t kQPanel = kStep * 128;  // 8 KB: 64 rows x 64 elements
+  static constexpr uint32_t kQTile = kPanels * kQPanel;
+  static constexpr int kNS = 4;                     // Q/dO ring stages
+  static constexpr uint32_t oK = 0;
+  static constexpr uint32_t oV = oK + kKVTile;
+  static constexpr uint32_t oQ = oV + kKVTile;
+  static constexpr uint32_t oDO = oQ + kNS * kQTile;
+  static constexpr uint32_t oL = oDO + kNS * kQTile;
+  static constexpr uint32_t oD = oL + kNS * kStep * 4;
+  static constexpr uint32_t oBar = oD + kNS * kStep * 4;
+  static constexpr int bKV = 0;                     // K, V of a unit landed
+  static constexpr int bQFull = 1;
+  static constexpr int bQEmpty = bQFull + kNS;
+  static constexpr int bSFull = bQEmpty + kNS;      // [2] S^T landed
+  static constexpr int bDPFull = bSFull + 2;        // [2] dP^T landed
+  static constexpr int bSEmpty = bDPFull + 2;       // [2] dV done with the P^T image
+  static constexpr int bDPEmpty = bSEmpty + 2;      // [2] dK done with the dS^T image
+  static constexpr int bPFull = bDPEmpty + 2;       // [2] P^T image written
+  static constexpr int bDSFull = bPFull + 2;        // [2] dS^T image written
+  static constexpr int bAcc = bDSFull + 2;          // a unit's dV, dK complete in TMEM
+  static constexpr int bDrain = bAcc + 1;           // one per MMA-issuing warp
+  static constexpr int bKVFree = bDrain + 3;        // a unit's last reads of K, V done
+  static constexpr int bAccFree = bKVFree + 1;      // the epilogue has read dV, dK
+  static constexpr int kBars = bAccFree + 1;
+  static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
+  static constexpr uint32_t oAbort = oTmemSlot + 8;
+  static constexpr uint32_t oFlags = oAbort + 8;    // [buffer][8 warps] split votes
+  static constexpr uint32_t kSmem = oFlags + 64 + 1024;  // + slack for 1024-byte alignment
+  static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
+};
+
+// One key tile of a (batch, key head) against the query steps of one split.
+struct KUnit {
+  int b, hk, split, j0, nq, nk;
+  int first, steps;  // steps first .. first + steps - 1 of the sequence's live ones (0: nothing to compute)
+  int chunks;        // live chunks of a head's queries
+};
+
+__device__ __forceinline__ int k_units(const CrossParams& p) {
+  return p.B * p.Hk * ((p.Nk + 127) / 128) * p.plan.q_splits;
+}
+
+// idx: split fastest, then the tiles of a (batch, key head), which share its queries through L2.
+__device__ __forceinline__ void k_unit(const CrossParams& p, int idx, KUnit& u) {
+  const int tiles = (p.Nk + 127) / 128;
+  const int rest = idx / p.plan.q_splits;
+  u.split = idx - rest * p.plan.q_splits;
+  const int bh = rest / tiles;
+  u.j0 = (rest - bh * tiles) * 128;
+  u.b = bh / p.Hk;
+  u.hk = bh - u.b * p.Hk;
+  u.nq = cross_q_len(p, u.b);
+  u.nk = cross_k_len(p, u.b);
+  u.chunks = p.plan.step.chunks(u.nq);
+  const int total = u.chunks * (p.G >> p.plan.step.h_log), per = (total + p.plan.q_splits - 1) / p.plan.q_splits;
+  u.first = u.split * per;
+  u.steps = u.j0 < u.nk ? max(min(per, total - u.first), 0) : 0;
+}
+
+// Head (of all) and first query of a live step.
+__device__ __forceinline__ void k_step(const CrossParams& p, const KUnit& u, int it, int& h0, int& q0) {
+  const int s = u.first + it, group = s / u.chunks;
+  h0 = u.hk * p.G + (group << p.plan.step.h_log);
+  q0 = (s - group * u.chunks) << p.plan.step.q_log;
+}
+
+// Columns 32 c .. 32 c + 31 of a step that hold a real query.
+__device__ __forceinline__ uint32_t step_columns(const CrossTile& t, int c, int left) {
+  const int q = t.queries(), rows = q << t.h_log;
+  uint32_t m;
+  if (q >= 32) {
+    const int in = q == 64 ? 32 * c : 0;  // the chunk's first query
+    m = bit_range(0, left - in);
+  } else {
+    m = bit_range(0, min(q, left));
+    for (int s = q; s < 32; s <<= 1) m |= m << s;
+  }
+  return m & bit_range(0, rows - 32 * c);
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_dkdv_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmDO) {
+  using C = KCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
+  auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
+  const int units = k_units(p);
+  const int rows = 1 << (p.plan.step.q_log + p.plan.step.h_log);
+  // The first unit from idx on in this CTA's stride that has steps; -1: none.
+  auto next_work = [&](int idx, KUnit& u) -> int {
+    for (; idx < units; idx += gridDim.x) {
+      k_unit(p, idx, u);
+      if (u.steps > 0) return idx;
+    }
+    return -1;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::bKV), 1);
+    for (int s = 0; s < C::kNS; ++s) {
+      mbar_init(bar(C::bQFull + s), 1);
+      mbar_init(bar(C::bQEmpty + s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(C::bSFull + x), 1);
+      mbar_init(bar(C::bDPFull + x), 1);
+      mbar_init(bar(C::bSEmpty + x), 1);
+      mbar_init(bar(C::bDPEmpty + x), 1);
+      mbar_init(bar(C::bPFull + x), 256);   // two warpgroups
+      mbar_init(bar(C::bDSFull + x), 256);
+    }
+    for (int x = 0; x < 3; ++x) mbar_init(bar(C::bDrain + x), 1);
+    mbar_init(bar(C::bAcc), 1);
+    mbar_init(bar(C::bKVFree), 2);          // S^T and dP^T issuers
+    mbar_init(bar(C::bAccFree), 8 * 32);    // the epilogue pair's row-math warps
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(sb + C::oTmemSlot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmDO);
+  }
+  if (rows < kStep) {  // the rows that no copy reaches: the accumulating MMAs read them with weight 0
+    for (int x = threadIdx.x; x < 2 * C::kNS * (int)C::kQTile / 16; x += kThreads)
+      st_shared_v4(sb + C::oQ + 16 * x, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::oTmemSlot);
+  const uint32_t tS = tmem, tdP = tmem + 128, tdV = tmem + 256, tdK = tmem + 256 + D;
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)(2 * C::kPanels * 128 + 2 * 4) * rows;
+      int kl = 0, G = 0;  // units and steps loaded
+      bool ok = true;
+      KUnit u;
+      for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u)) {
+        // K and V of this unit, once the previous unit's last reads of them are done
+        if (kl > 0 && !mbar_wait(bar(C::bKVFree), (kl - 1) & 1, abort_flag, p.status)) break;
+        mbar_arrive_expect_tx(bar(C::bKV), 2 * C::kKVTile);
+        for (int pn = 0; pn < C::kPanels; ++pn) {
+          tma_load_4d(sb + C::oK + pn * C::kKVPanel, &tmK, bar(C::bKV), 64 * pn, u.j0, u.hk, u.b);
+          tma_load_4d(sb + C::oV + pn * C::kKVPanel, &tmV, bar(C::bKV), 64 * pn, u.j0, u.hk, u.b);
+        }
+        ++kl;
+        for (int it = 0; it < u.steps; ++it, ++G) {
+          const int s = G % C::kNS;
+          if (!mbar_wait(bar(C::bQEmpty + s), ((G / C::kNS) & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          int h0, q0;
+          k_step(p, u, it, h0, q0);
+          mbar_arrive_expect_tx(bar(C::bQFull + s), q_bytes);
+          for (int pn = 0; pn < C::kPanels; ++pn) {
+            tma_load_4d(sb + C::oQ + s * C::kQTile + pn * C::kQPanel, &tmQ, bar(C::bQFull + s), 64 * pn, q0, h0, u.b);
+            tma_load_4d(sb + C::oDO + s * C::kQTile + pn * C::kQPanel, &tmDO, bar(C::bQFull + s), 64 * pn, q0, h0, u.b);
+          }
+          const int q = p.plan.step.queries();
+          for (int h = 0; h < p.plan.step.heads(); ++h) {
+            const long long at = ((long long)u.b * p.Hq + h0 + h) * p.nq_pad + q0;
+            bulk_load(sb + C::oL + (s * kStep + h * q) * 4, p.nL2 + at, q * 4, bar(C::bQFull + s));
+            bulk_load(sb + C::oD + (s * kStep + h * q) * 4, p.nD + at, q * 4, bar(C::bQFull + s));
+          }
+        }
+      }
+      if (*abort_flag) {
+        // Let every copy this thread started land before the CTA exits.
+        if (kl > 0) mbar_wait_drain(bar(C::bKV), (kl - 1) & 1, p.status);
+        for (int x = max(0, G - C::kNS); x < G; ++x)
+          mbar_wait_drain(bar(C::bQFull + x % C::kNS), (x / C::kNS) & 1, p.status);
+      }
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------ S^T (warp 1) / dP^T (warp 3) MMA issuer ----------------
+    // S^T = K Q^T or dP^T = V dO^T: M = 128 keys, N = 64 queries, K = d, both K-major.
+    const bool isS = warp == 1;
+    constexpr uint32_t idS = make_idesc(128, kStep, kBf16, false, false);
+    const uint64_t dA0 = make_sdesc(sb + (isS ? C::oK : C::oV), 16, 1024),
+                   dB0 = make_sdesc(sb + (isS ? C::oQ : C::oDO), 16, 1024);
+    const uint32_t tD = isS ? tS : tdP;
+    const int bF = isS ? C::bSFull : C::bDPFull, bE = isS ? C::bSEmpty : C::bDPEmpty;
+    int kl = 0, G = 0;
+    bool ok = true;
+    KUnit u;
+    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      ok = warp_wait<kIssuerPoll>(bar(C::bKV), kl & 1, abort_flag, p.status);
+      for (int it = 0; ok && it < u.steps; ++it, ++G) {
+        const int s = G % C::kNS, bb = G & 1;
+        if (!warp_wait<kIssuerPoll>(bar(C::bQFull + s), (G / C::kNS) & 1, abort_flag, p.status) ||
+            !warp_wait<kIssuerPoll>(bar(bE + bb), ((G >> 1) & 1) ^ 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bq = desc_add(dB0, s * C::kQTile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss_w(tD + 64 * bb, desc_add(dA0, (kk >> 2) * C::kKVPanel + (kk & 3) * 32),
+                      desc_add(bq, (kk >> 2) * C::kQPanel + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+        tc_commit_w(bar(bF + bb));
+      }
+      if (!ok) break;
+      tc_commit_w(bar(C::bKVFree));  // this unit's last reads of K / V
+    }
+    // Every MMA this warp issued is complete before the CTA frees TMEM and exits.
+    const int dr = isS ? 0 : 2;
+    tc_commit_w(bar(C::bDrain + dr));
+    if (lane == 0) mbar_wait_drain(bar(C::bDrain + dr), 0, p.status);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ----------------------------- dV / dK MMA issuer ----------------------------
+    constexpr uint32_t idG = make_idesc(128, D, kBf16, false, true);
+    const uint64_t mQ0 = make_sdesc(sb + C::oQ, C::kQPanel, 1024), mO0 = make_sdesc(sb + C::oDO, C::kQPanel, 1024);
+    int kl = 0, G = 0;
+    bool ok = true;
+    KUnit u;
+    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      for (int it = 0; it < u.steps; ++it, ++G) {
+        const int bt = G & 1, st = G % C::kNS;
+        if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
+            // a unit's first MMAs overwrite the accumulators that the previous unit's epilogue reads
+            (it == 0 && kl > 0 && !warp_wait<kConsumerPoll>(bar(C::bAccFree), (kl - 1) & 1, abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        int h0, q0;
+        k_step(p, u, it, h0, q0);
+        // Rows of queries past the sequence's end, as far as they are the tensors' (past them: zeros by
+        // TMA). S^T is formed; dP^T may still read dO: its columns of these rows are not used.
+        const int q = p.plan.step.queries(), from = u.nq - q0, to = min(q, p.Nq - q0);
+        if (from < to) {
+          for (int h = 0; h < p.plan.step.heads(); ++h) {
+            zero_rows<C::kPanels>(sb + C::oQ + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
+            zero_rows<C::kPanels>(sb + C::oDO + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
+          }
+        }
+        tc_fence_after();
+        bool split = false;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) split |= flags[8 * bt + x] != 0;
+        const uint32_t first = it > 0 ? 1u : 0u;
+        const uint64_t qd = desc_add(mQ0, st * C::kQTile), gd = desc_add(mO0, st * C::kQTile);
+        // dV += P^T dO: K step kk reads the 8 rounded columns at 16kk of the P^T image and, on split
+        // tiles, the 8 residual columns at 16kk + 8.
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk, desc_add(gd, 2048 * kk), idG, kk > 0 ? 1u : first);
+        if (split) {
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk + 8, desc_add(gd, 2048 * kk), idG, 1u);
+        }
+        tc_commit_w(bar(C::bSEmpty + bt));
+        // dK once the dS^T image is in place; dV above only needed P^T.
+        if (!warp_wait<kConsumerPoll>(bar(C::bDSFull + bt), (G >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk, desc_add(qd, 2048 * kk), idG, kk > 0 ? 1u : first);
+        if (split) {
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk + 8, desc_add(qd, 2048 * kk), idG, 1u);
+        }
+        tc_commit_w(bar(C::bDPEmpty + bt));
+        tc_commit_w(bar(C::bQEmpty + st));
+      }
+      if (!ok) break;
+      tc_commit_w(bar(C::bAcc));
+    }
+    tc_commit_w(bar(C::bDrain + 1));
+    if (lane == 0) mbar_wait_drain(bar(C::bDrain + 1), 0, p.status);
+    __syncwarp();
+  } else {
+    // ------------------------- row-math warpgroups --------------------------
+    // rg = 0, 1 take the even steps (TMEM buffer 0) and rg = 2, 3 the odd ones, counted
+    // across units; warpgroup rg & 1 takes query columns [32 (rg & 1), + 32). Two phases a
+    // step: P^T from S^T (released to the dV MMA at once), then dS^T from dP^T and the kept
+    // fp32 P. The pair that ran a unit's last step writes its epilogue; the other goes on.
+    const int rg = (warp - 4) >> 2, wq = warp & 3, c = rg & 1, bb = rg >> 1;
+    const int jl = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tSc = tS + lane_off + 64 * bb + 32 * c, tdPc = tdP + lane_off + 64 * bb + 32 * c;
+    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    const long long size = (long long)p.B * p.Nk * p.Hk * D;
+    int kl = 0, G = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
+      KUnit u;
+      k_unit(p, idx, u);
+      const int j = u.j0 + jl;
+      for (int it = (bb ^ G) & 1; it < u.steps; it += 2) {
+        const int gs = G + it, s = gs % C::kNS;
+        int h0, q0;
+        k_step(p, u, it, h0, q0);
+        const uint32_t allow = j < u.nk ? step_columns(p.plan.step, c, u.nq - q0) : 0u;
+        if (!warp_wait<kRowMathPoll>(bar(C::bQFull + s), (gs / C::kNS) & 1, abort_flag, p.status) ||
+            !warp_wait<kRowMathPoll>(bar(C::bSFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float4* L4 = reinterpret_cast<const float4*>(smem + C::oL + s * kStep * 4 + 128 * c);
+        const float4* D4 = reinterpret_cast<const float4*>(smem + C::oD + s * kStep * 4 + 128 * c);
+        float P[32];  // of this thread's 32 pairs, for the dS phase
+        bool split_h[2];
+        // ---- phase 1: the P^T image over the S^T columns ----
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t sr[16];
+          __syncwarp();  // per-lane branches above: converge for the TMEM load
+          tmem_ld16(tSc + 16 * hh, sr);
+          tmem_ld_wait16(sr);
+          float cmax = 0.f;
+          auto p_phase = [&](auto masked) {
+#pragma unroll
+            for (int x = 0; x < 16; x += 4) {
+              const float4 l4 = L4[(16 * hh + x) >> 2];
+              float pv[4];
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[x]), __uint_as_float(sr[x + 1])), c2, f2_pack(l4.x, l4.y)),
+                        pv[0], pv[1]);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3])), c2, f2_pack(l4.z, l4.w)),
+                        pv[2], pv[3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int bit = 16 * hh + x + y;
+                pv[y] = ex2_approx(pv[y]);
+                if constexpr (decltype(masked)::value) pv[y] = ((allow >> bit) & 1u) ? pv[y] : 0.f;
+                P[bit] = pv[y];
+              }
+              cmax = fmax3(cmax, pv[0], pv[1]);
+              cmax = fmax3(cmax, pv[2], pv[3]);
+            }
+          };
+          if (allow == 0xFFFFFFFFu)
+            p_phase(std::false_type{});
+          else
+            p_phase(std::true_type{});
+          __syncwarp();  // reconverge before the collective vote and TMEM stores
+          uint32_t hp[8], ep[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
+          split_h[hh] = __any_sync(0xFFFFFFFFu, cmax > kSplitThreshold);
+          if (split_h[hh]) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              ep[x] = pack2_residual<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1], hp[x]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ep[x] = 0u;
+          }
+          // this K step's image: 8 rounded columns, then 8 residual columns
+          tmem_st8<0>(tSc + 16 * hh, hp);
+          tmem_st8<0>(tSc + 16 * hh + 8, ep);
+        }
+        tmem_st_wait();
+        if (lane == 0) flags[8 * bb + 4 * c + wq] = (split_h[0] || split_h[1]) ? 1 : 0;
+        tc_fence_before();
+        warp_arrive(bar(C::bPFull + bb));
+        // ---- phase 2: dS^T = P o (dP^T + (-D)) ----
+        if (!warp_wait<kRowMathPoll>(bar(C::bDPFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t dr[16];
+          __syncwarp();
+          tmem_ld16(tdPc + 16 * hh, dr);
+          tmem_ld_wait16(dr);
+          float ds[16];
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const float4 d4 = D4[(16 * hh + x) >> 2];
+            const uint64_t d01 =
+                f2_add(f2_pack(__uint_as_float(dr[x]), __uint_as_float(dr[x + 1])), f2_pack(d4.x, d4.y));
+            const uint64_t d23 =
+                f2_add(f2_pack(__uint_as_float(dr[x + 2]), __uint_as_float(dr[x + 3])), f2_pack(d4.z, d4.w));
+            f2_unpack(f2_mul(f2_pack(P[16 * hh + x], P[16 * hh + x + 1]), d01), ds[x], ds[x + 1]);
+            f2_unpack(f2_mul(f2_pack(P[16 * hh + x + 2], P[16 * hh + x + 3]), d23), ds[x + 2], ds[x + 3]);
+          }
+          if (allow != 0xFFFFFFFFu) {  // (dP^T of what is not there may be NaN)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) ds[x] = ((allow >> (16 * hh + x)) & 1u) ? ds[x] : 0.f;
+          }
+          __syncwarp();
+          uint32_t hd[8], ed[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) hd[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
+          if (split_h[hh]) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ed[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hd[x]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ed[x] = 0u;
+          }
+          tmem_st8<0>(tdPc + 16 * hh, hd);
+          tmem_st8<0>(tdPc + 16 * hh + 8, ed);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(bar(C::bDSFull + bb));
+      }
+      if (!ok) break;
+      // Epilogue, by the pair that ran the unit's last step: dV, then dK, each warpgroup half of the
+      // columns; both accumulators are released (AccFree) before dK's stores.
+      const bool epi = u.steps > 0 ? bb == ((G + u.steps - 1) & 1) : bb == 0;
+      if (epi) {
+        constexpr int kChunks = D / 64;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          const bool isK = which == 1;
+          uint32_t r[kChunks][32];
+          if (u.steps > 0) {
+            if (!isK) {
+              if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            __syncwarp();  // the stores are per lane: converge for the TMEM loads
+            const uint32_t col0 = (isK ? tdK : tdV) + lane_off + c * (D / 2);
+#pragma unroll
+            for (int cc = 0; cc < kChunks; ++cc) tmem_ld32(col0 + 32 * cc, r[cc]);
+            if constexpr (kChunks == 2)
+              tmem_ld_wait2(r[0], r[1]);
+            else
+              tmem_ld_wait(r[0]);
+            if (isK) {
+              tc_fence_before();
+              warp_arrive(bar(C::bAccFree));
+            }
+          }
+          if (u.steps == 0 || j >= u.nk) {
+#pragma unroll
+            for (int cc = 0; cc < kChunks; ++cc)
+#pragma unroll
+              for (int x = 0; x < 32; ++x) r[cc][x] = 0u;
+          }
+          if (p.plan.q_splits > 1) {
+            if (j < u.nk) {
+              float* to = p.part_kv + 2 * u.split * size + (isK ? 0 : size) +
+                          (((long long)u.b * p.Nk + j) * p.Hk + u.hk) * D + c * (D / 2);
+#pragma unroll
+              for (int cc = 0; cc < kChunks; ++cc) store32_f(to + 32 * cc, r[cc], 1.f);
+            }
+          } else if (j < p.Nk) {
+            const fa_strides& st = isK ? p.dk_st : p.dv_st;
+            uint16_t* to = static_cast<uint16_t*>(isK ? p.dk : p.dv) + u.b * st.b + j * st.n + u.hk * st.h + c * (D / 2);
+#pragma unroll
+            for (int cc = 0; cc < kChunks; ++cc) store32_h<kBf16>(to + 32 * cc, r[cc], isK ? p.scale : 1.f);
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+      }
+      if (u.steps > 0) ++kl;
+      G += u.steps;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------- dQ -----------------------------------
+template <int D>
+struct QCfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kPanel = 128 * 128;
+  static constexpr uint32_t kTile = kPanels * kPanel;  // one 128-row tile of Q, dO, K or V
+  static constexpr int kNV = 2;                        // V ring stages
+  static constexpr int kNK = D == 64 ? 4 : 3;          // K ring stages (read by S and by dQ)
+  static constexpr uint32_t oQ = 0;
+  static constexpr uint32_t oDO = oQ + kTile;
+  static constexpr uint32_t oV = oDO + kTile;
+  static constexpr uint32_t oK = oV + kNV * kTile;
+  static constexpr uint32_t oBar = oK + kNK * kTile;
+  static constexpr int bRes = 0;                       // Q, dO of a unit landed
+  static constexpr int bVFull = 1;
+  static constexpr int bVEmpty = bVFull + kNV;
+  static constexpr int bKFull = bVEmpty + kNV;
+  static constexpr int bKEmpty = bKFull + kNK;
+  static constexpr int bSFull = bKEmpty + kNK;         // [2] S and dP landed
+  static constexpr int bSEmpty = bSFull + 2;           // [2] dQ MMA done with the image
+  static constexpr int bDPEmpty = bSEmpty + 2;         // row math has read dP
+  static constexpr int bPFull = bDPEmpty + 1;          // [2] dS image written
+  static constexpr int bAcc = bPFull + 2;
+  static constexpr int bDrain = bAcc + 1;              // one per MMA-issuing warp
+  static constexpr int bResFree = bDrain + 3;          // a unit's last reads of Q and dO done
+  static constexpr int bAccFree = bResFree + 1;        // the epilogue has read the accumulator
+  static constexpr int kBars = bAccFree + 1;
+  static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
+  static constexpr uint32_t oAbort = oTmemSlot + 8;
+  static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [buffer][16 warps] split votes
+  static constexpr uint32_t kSmem = oFlags + 2 * 16 * 4 + 1024;  // + slack for 1024-byte alignment
+  static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_dq_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmDO) {
+  using C = QCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
+  auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
+  const int units = cross_units<1>(p);
+  auto next_work = [&](int idx, CrossUnit& u) -> int {
+    for (; idx < units; idx += gridDim.x) {
+      cross_unit<1>(p, idx, u);
+      if (u.blocks > 0) return idx;
+    }
+    return -1;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::bRes), 1);
+    for (int s = 0; s < C::kNV; ++s) {
+      mbar_init(bar(C::bVFull + s), 1);
+      mbar_init(bar(C::bVEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kNK; ++s) {
+      mbar_init(bar(C::bKFull + s), 1);
+      mbar_init(bar(C::bKEmpty + s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(C::bSFull + x), 2);
+      mbar_init(bar(C::bSEmpty + x), 1);
+      mbar_init(bar(C::bPFull + x), 512);
+    }
+    mbar_init(bar(C::bDPEmpty), 512);
+    mbar_init(bar(C::bAcc), 1);
+    for (int x = 0; x < 3; ++x) mbar_init(bar(C::bDrain + x), 1);
+    mbar_init(bar(C::bResFree), 2);    // S and dP issuers
+    mbar_init(bar(C::bAccFree), 512);  // every row-math warp
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(sb + C::oTmemSlot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmDO);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::oTmemSlot);
+  const uint32_t tS = tmem, tdP = tmem + 256, tAcc = tmem + 384;
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      const uint32_t q_bytes = 2u * C::kPanels * 128u << (p.plan.q_tile.q_log + p.plan.q_tile.h_log);
+      int kl = 0, G = 0, issuedV = 0, issuedK = 0;
+      bool ok = true;
+      CrossUnit u;
+      for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u)) {
+        if (kl > 0 && !mbar_wait(bar(C::bResFree), (kl - 1) & 1, abort_flag, p.status)) break;
+        const CrossRows r = cross_rows(p, u, u.first);
+        mbar_arrive_expect_tx(bar(C::bRes), q_bytes);
+        for (int pn = 0; pn < C::kPanels; ++pn) {
+          tma_load_4d(sb + C::oQ + pn * C::kPanel, &tmQ, bar(C::bRes), 64 * pn, r.q0, r.h0, u.b);
+          tma_load_4d(sb + C::oDO + pn * C::kPanel, &tmDO, bar(C::bRes), 64 * pn, r.q0, r.h0, u.b);
+        }
+        ++kl;
+        for (int it = 0; it < u.blocks; ++it, ++G) {
+          const int row = u.j_begin + 128 * it, sv = G % C::kNV, sk = G % C::kNK;
+          if (!mbar_wait(bar(C::bVEmpty + sv), ((G / C::kNV) & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::bVFull + sv), C::kTile);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(sb + C::oV + sv * C::kTile + pn * C::kPanel, &tmV, bar(C::bVFull + sv), 64 * pn, row, u.hk, u.b);
+          issuedV = G + 1;
+          if (!mbar_wait(bar(C::bKEmpty + sk), ((G / C::kNK) & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::bKFull + sk), C::kTile);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(sb + C::oK + sk * C::kTile + pn * C::kPanel, &tmK, bar(C::bKFull + sk), 64 * pn, row, u.hk, u.b);
+          issuedK = G + 1;
+        }
+      }
+      if (*abort_flag) {
+        if (kl > 0) mbar_wait_drain(bar(C::bRes), (kl - 1) & 1, p.status);
+        for (int x = max(0, issuedV - C::kNV); x < issuedV; ++x)
+          mbar_wait_drain(bar(C::bVFull + x % C::kNV), (x / C::kNV) & 1, p.status);
+        for (int x = max(0, issuedK - C::kNK); x < issuedK; ++x)
+          mbar_wait_drain(bar(C::bKFull + x % C::kNK), (x / C::kNK) & 1, p.status);
+      }
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------ S (warp 1) / dP (warp 3) MMA issuer -------------------
+    const bool isS = warp == 1;
+    constexpr uint32_t idS = make_idesc(128, 128, kBf16, false, false);
+    const uint64_t dA0 = make_sdesc(sb + (isS ? C::oQ : C::oDO), 16, 1024),
+                   dB0 = make_sdesc(sb + (isS ? C::oK : C::oV), 16, 1024);
+    int kl = 0, G = 0;
+    bool ok = true;
+    CrossUnit u;
+    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      ok = warp_wait<kIssuerPoll>(bar(C::bRes), kl & 1, abort_flag, p.status);
+      for (int it = 0; ok && it < u.blocks; ++it, ++G) {
+        const int bb = G & 1, st = isS ? G % C::kNK : G % C::kNV;
+        const bool landed = isS ? warp_wait<kIssuerPoll>(bar(C::bKFull + st), (G / C::kNK) & 1, abort_flag, p.status)
+                                : warp_wait<kIssuerPoll>(bar(C::bVFull + st), (G / C::kNV) & 1, abort_flag, p.status);
+        // S: its buffer's image is consumed; dP: the row math has read the step before's
+        if (!landed || (isS && !warp_wait<kIssuerPoll>(bar(C::bSEmpty + bb), ((G >> 1) & 1) ^ 1, abort_flag, p.status)) ||
+            (!isS && G > 0 && !warp_wait<kIssuerPoll>(bar(C::bDPEmpty), (G - 1) & 1, abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bd = desc_add(dB0, st * C::kTile);
+        const uint32_t tD = isS ? tS + 128 * bb : tdP;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ss_w(tD, desc_add(dA0, (kk >> 2) * C::kPanel + (kk & 3) * 32),
+                      desc_add(bd, (kk >> 2) * C::kPanel + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+        tc_commit_w(bar(C::bSFull + bb));
+        if (!isS) tc_commit_w(bar(C::bVEmpty + st));
+      }
+      if (!ok) break;
+      tc_commit_w(bar(C::bResFree));  // this unit's last reads of Q / dO
+    }
+    const int dr = isS ? 0 : 2;
+    tc_commit_w(bar(C::bDrain + dr));
+    if (lane == 0) mbar_wait_drain(bar(C::bDrain + dr), 0, p.status);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------ dQ MMA issuer -----------------------------
+    constexpr uint32_t idO = make_idesc(128, D, kBf16, false, true);
+    const uint64_t b0 = make_sdesc(sb + C::oK, C::kPanel, 1024);
+    int kl = 0, G = 0;
+    bool ok = true;
+    CrossUnit u;
+    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      for (int it = 0; it < u.blocks; ++it, ++G) {
+        const int bt = G & 1, sk = G % C::kNK;
+        if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
+            (it == 0 && kl > 0 && !warp_wait<kConsumerPoll>(bar(C::bAccFree), (kl - 1) & 1, abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        // K's rows from the sequence's end on, as far as they are the tensor's (S, which read them, is formed)
+        const int from = u.j_end - u.j_begin - 128 * it, to = min(128, p.Nk - u.j_begin - 128 * it);
+        if (from < to) zero_rows<C::kPanels>(sb + C::oK + sk * C::kTile, C::kPanel, from, to);
+        tc_fence_after();
+        const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 16 * bt);
+        int any = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) any |= f4[x].x | f4[x].y | f4[x].z | f4[x].w;
+        const uint64_t bop = desc_add(b0, sk * C::kTile);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ts_w(tAcc, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO, kk > 0 || it > 0 ? 1u : 0u);
+        if (any) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_ts_w(tAcc, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
+        }
+        tc_commit_w(bar(C::bSEmpty + bt));
+        tc_commit_w(bar(C::bKEmpty + sk));
+      }
+      if (!ok) break;
+      tc_commit_w(bar(C::bAcc));
+    }
+    tc_commit_w(bar(C::bDrain + 1));
+    if (lane == 0) mbar_wait_drain(bar(C::bDrain + 1), 0, p.status);
+    __syncwarp();
+  } else {
+    // ---------------- row-math warpgroups + epilogue ----------------------
+    // Warpgroup c takes key columns [32c, 32c + 32) of every step, in halves of 16, and a
+    // quarter of the epilogue's columns.
+    const int c = (warp - 4) >> 2, wq = warp & 3;
+    const int il = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tdPc = tdP + lane_off + 32 * c;
+    const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
+    const bool row_in = row_h < p.plan.q_tile.heads();
+    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    int kl = 0, G = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
+      CrossUnit u;
+      cross_unit<1>(p, idx, u);
+      const CrossRows rt = cross_rows(p, u, u.first);
+      const int i = rt.q0 + row_q, h = rt.h0 + row_h;
+      float nL2 = -INFINITY, nD = 0.f;
+      if (u.blocks > 0 && row_in) {  // (rows past the sequence hold -inf and 0)
+        const long long at = ((long long)u.b * p.Hq + h) * p.nq_pad + i;
+        nL2 = p.nL2[at];
+        nD = p.nD[at];
+      }
+      const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
+      for (int it = 0; it < u.blocks; ++it) {
+        const int gs = G + it, bb = gs & 1;
+        const uint32_t tSc = tS + lane_off + 128 * bb + 32 * c;
+        const uint32_t allow = bit_range(0, u.j_end - u.j_begin - 128 * it - 32 * c);
+        if (!warp_wait<kRowMathPoll>(bar(C::bSFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // both halves of dP come in with S, so the dP buffer is released before any arithmetic
+        uint32_t sr[16], dr[2][16];
+        __syncwarp();
+        tmem_ld16(tSc, sr);
+        tmem_ld16(tdPc, dr[0]);
+        tmem_ld16(tdPc + 16, dr[1]);
+        tmem_ld_wait16x3(sr, dr[0], dr[1]);
+        tc_fence_before();
+        warp_arrive(bar(C::bDPEmpty));
+        bool lo_any = false;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          if (hh == 1) {
+            __syncwarp();
+            tmem_ld16(tSc + 16, sr);
+            tmem_ld_wait16(sr);
+          }
+          float ds[16];
+          float cmax = 0.f;
+          auto elementwise = [&](auto masked) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, l2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              const uint64_t dd = f2_add(f2_pack(__uint_as_float(dr[hh][e]), __uint_as_float(dr[hh][e + 1])), d2);
+              f2_unpack(f2_mul(f2_pack(p0, p1), dd), ds[e], ds[e + 1]);
+              if constexpr (decltype(masked)::value) {
+                const bool in0 = (allow >> (16 * hh + e)) & 1u, in1 = (allow >> (16 * hh + e + 1)) & 1u;
+                p0 = in0 ? p0 : 0.f;
+                p1 = in1 ? p1 : 0.f;
+                ds[e] = in0 ? ds[e] : 0.f;
+                ds[e + 1] = in1 ? ds[e + 1] : 0.f;
+              }
+              cmax = fmax3(cmax, p0, p1);
+            }
+          };
+          // (the mask is the same for the whole warp)
+          if (allow == 0xFFFFFFFFu)
+            elementwise(std::false_type{});
+          else
+            elementwise(std::true_type{});
+          uint32_t hv[8], ev[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) hv[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
+          const bool split = __any_sync(0xFFFFFFFFu, row_in && cmax > kSplitThreshold);
+          lo_any |= split;
+          if (split) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ev[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hv[x]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ev[x] = 0u;
+          }
+          tmem_st8<0>(tSc + 16 * hh, hv);
+          tmem_st8<0>(tSc + 16 * hh + 8, ev);
+        }
+        tmem_st_wait();
+        if (lane == 0) flags[16 * bb + 4 * c + wq] = lo_any ? 1 : 0;
+        tc_fence_before();
+        warp_arrive(bar(C::bPFull + bb));
+      }
+      if (!ok) break;
+      // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
+      // (AccFree) before the stores, so the next unit's first MMA can start meanwhile.
+      constexpr int kChunks = D / 64;  // 16-column TMEM loads per thread
+      uint32_t r[kChunks][16];
+      if (u.blocks > 0) {
+        if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t col0 = tAcc + lane_off + c * (D / 4);
+        tmem_ld16(col0, r[0]);
+        if constexpr (kChunks == 2) {
+          tmem_ld16(col0 + 16, r[1]);
+          tmem_ld_wait16x2(r[0], r[1]);
+        } else {
+          tmem_ld_wait16(r[0]);
+        }
+        tc_fence_before();
+        warp_arrive(bar(C::bAccFree));
+        ++kl;
+      }
+      if (u.blocks == 0 || i >= u.nq) {
+#pragma unroll
+        for (int cc = 0; cc < kChunks; ++cc)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) r[cc][x] = 0u;
+      }
+      if (row_in && i < p.Nq) {
+        if (p.plan.k_splits > 1) {
+          if (i < u.nq) {
+            float* to = p.part + ((((long long)u.split * p.B + u.b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4);
+#pragma unroll
+            for (int cc = 0; cc < kChunks; ++cc)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                reinterpret_cast<float4*>(to + 16 * cc)[x] =
+                    make_float4(__uint_as_float(r[cc][4 * x]), __uint_as_float(r[cc][4 * x + 1]),
+                                __uint_as_float(r[cc][4 * x + 2]), __uint_as_float(r[cc][4 * x + 3]));
+          }
+        } else {
+          uint16_t* to = static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4);
+#pragma unroll
+          for (int cc = 0; cc < kChunks; ++cc) {
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              w[x] = pack2<kBf16>(__uint_as_float(r[cc][2 * x]) * p.scale, __uint_as_float(r[cc][2 * x + 1]) * p.scale);
+            uint4* gp = reinterpret_cast<uint4*>(to + 16 * cc);
+            gp[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            gp[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
+      __syncwarp();
+      G += u.blocks;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename Kernel>
+cudaError_t launch_persistent(Kernel kern, uint32_t bytes, long long units, const CrossParams& p, const CUtensorMap* maps,
+                              cudaStream_t st) {
+  const int smem = (int)(bytes > kMinSmemOneCtaPerSm ? bytes : kMinSmemOneCtaPerSm);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(units < 152 ? units : 152), kThreads, smem, st>>>(p, maps[0], maps[1], maps[2], maps[3]);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_dkdv_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st) {
+  const long long units = (long long)p.B * p.Hk * ((p.Nk + 127) / 128) * p.plan.q_splits;
+  if (p.d == 128)
+    return bf16 ? launch_persistent(cross_dkdv_kernel<128, true>, KCfg<128>::kSmem, units, p, maps, st)
+                : launch_persistent(cross_dkdv_kernel<128, false>, KCfg<128>::kSmem, units, p, maps, st);
+  return bf16 ? launch_persistent(cross_dkdv_kernel<64, true>, KCfg<64>::kSmem, units, p, maps, st)
+              : launch_persistent(cross_dkdv_kernel<64, false>, KCfg<64>::kSmem, units, p, maps, st);
+}
+
+cudaError_t launch_cross_dq_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st) {
+  const long long units = (long long)p.B * p.Hk * p.plan.q_tile.count(p.Nq, p.G) * p.plan.k_splits;
+  if (p.d == 128)
+    return bf16 ? launch_persistent(cross_dq_kernel<128, true>, QCfg<128>::kSmem, units, p, maps, st)
+                : launch_persistent(cross_dq_kernel<128, false>, QCfg<128>::kSmem, units, p, maps, st);
+  return bf16 ? launch_persistent(cross_dq_kernel<64, true>, QCfg<64>::kSmem, units, p, maps, st)
+              : launch_persistent(cross_dq_kernel<64, false>, QCfg<64>::kSmem, units, p, maps, st);
+}
+
+}  // namespace fa

@@ -12,9 +12,6 @@
 // apart, which no two threads of a quarter warp have in the same bank) and 4 rows x
 // DP / 16 columns of the 32 x DP sums. Rows and columns past a sequence's length are
 // zeros in shared memory, so nothing of what lies there reaches a product.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "fa_cross.h"
 #include "fa_serve.h"
 #include "rope_common.cuh"
@@ -34,11 +31,11 @@ struct Tile {
 
 // Rows [0, rows) of a tensor (row stride `st`, d values each) to shared memory as fp32 [most][DP],
 // zeros past `rows` and d.
-template <typename T, int DP>
-__device__ __forceinline__ void stage(float* to, const T* from, int64_t st, int rows, int most, int d) {
+template <int DP>
+__device__ __forceinline__ void stage(float* to, const float* from, int64_t st, int rows, int most, int d) {
   for (int x = threadIdx.x; x < most * DP; x += kThreads) {
     const int r = x / DP, e = x - r * DP;
-    to[r * Tile<DP>::kApart + e] = r < rows && e < d ? static_cast<float>(from[r * st + e]) : 0.f;
+    to[r * Tile<DP>::kApart + e] = r < rows && e < d ? from[r * st + e] : 0.f;
   }
 }
 
@@ -115,8 +112,8 @@ __device__ __forceinline__ void put_tile(float* to, const float (&s)[4][4]) {
 }
 
 // A thread's sums of row ty + 8 i, times mul, to `to` (a row of d values).
-template <typename T, int DP>
-__device__ __forceinline__ void put_row(T* to, const uint64_t (&acc)[DP / 64][2], float mul, int d) {
+template <int DP>
+__device__ __forceinline__ void put_row(float* to, const uint64_t (&acc)[DP / 64][2], float mul, int d) {
 #pragma unroll
   for (int c = 0; c < DP / 64; ++c) {
     float v[4];
@@ -124,7 +121,7 @@ __device__ __forceinline__ void put_row(T* to, const uint64_t (&acc)[DP / 64][2]
     f2_unpack(acc[c][1], v[2], v[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (4 * (threadIdx.x & 15) + 64 * c + e < d) to[4 * (threadIdx.x & 15) + 64 * c + e] = static_cast<T>(v[e] * mul);
+      if (4 * (threadIdx.x & 15) + 64 * c + e < d) to[4 * (threadIdx.x & 15) + 64 * c + e] = v[e] * mul;
   }
 }
 
@@ -144,8 +141,8 @@ __device__ __forceinline__ float row_max16(float v) {
 }
 
 // Grid: x the query tile, y head, z batch * split.
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_fwd_simple_kernel(const __grid_constant__ CrossParams p) {
+template <int DP>
+__global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_constant__ CrossParams p) {
   extern __shared__ __align__(16) float sm[];
   let_next_begin();
   wait_for_previous();
@@ -153,21 +150,21 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_simple_kernel(const __grid
   const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, h = blockIdx.y;
   const int i0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int j_end = min(nk, (split + 1) * p.plan.k_chunk);
-  const T* kp = static_cast<const T*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
-  const T* vp = static_cast<const T*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
+  const int per = ((nk + kCols - 1) / kCols + splits - 1) / splits * kCols, j_end = min(nk, (split + 1) * per);
+  const float* kp = static_cast<const float*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
+  const float* vp = static_cast<const float*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
   uint64_t acc[4][DP / 64][2];
   clear<DP>(acc);
   float m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
   if (i0 < nq)
-    stage<T, DP>(q, static_cast<const T*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
+    stage<DP>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
                  kRows, p.d);
-  for (int j0 = split * p.plan.k_chunk; i0 < nq && j0 < j_end; j0 += kCols) {
+  for (int j0 = split * per; i0 < nq && j0 < j_end; j0 += kCols) {
     __syncthreads();
-    stage<T, DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
-    stage<T, DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
+    stage<DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
+    stage<DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
     __syncthreads();
     float s[4][4];
     rows_by_rows<DP>(q, k, s);
@@ -212,21 +209,21 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_simple_kernel(const __grid
     if (splits > 1) {
       if (tx == 0) p.part_lse[split * rows + at] = lse2;
       if (has)
-        put_row<float, DP>(p.part + (split * rows + ((long long)b * p.Nq + t) * p.Hq + h) * p.d, acc[i], 1.f / l[i], p.d);
+        put_row<DP>(p.part + (split * rows + ((long long)b * p.Nq + t) * p.Hq + h) * p.d, acc[i], 1.f / l[i], p.d);
     } else {
       if (!has)
 #pragma unroll
         for (int c = 0; c < DP / 64; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
       if (tx == 0) p.lse_out[at] = has ? lse2 * 0.6931471805599453f : -INFINITY;
-      put_row<T, DP>(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h, acc[i],
+      put_row<DP>(static_cast<float*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h, acc[i],
                      has ? 1.f / l[i] : 0.f, p.d);
     }
   }
 }
 
 // dQ. Grid as the forward's.
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_dq_simple_kernel(const __grid_constant__ CrossParams p) {
+template <int DP>
+__global__ void __launch_bounds__(kThreads) cross_dq_f32_kernel(const __grid_constant__ CrossParams p) {
   extern __shared__ __align__(16) float sm[];
   let_next_begin();
   wait_for_previous();
@@ -235,16 +232,16 @@ __global__ void __launch_bounds__(kThreads) cross_dq_simple_kernel(const __grid_
   const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, h = blockIdx.y;
   const int i0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int j_end = min(nk, (split + 1) * p.plan.k_chunk);
-  const T* kp = static_cast<const T*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
-  const T* vp = static_cast<const T*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
+  const int per = ((nk + kCols - 1) / kCols + splits - 1) / splits * kCols, j_end = min(nk, (split + 1) * per);
+  const float* kp = static_cast<const float*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
+  const float* vp = static_cast<const float*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
   uint64_t acc[4][DP / 64][2];
   clear<DP>(acc);
   float nl[4], nd[4];
   if (i0 < nq) {
-    stage<T, DP>(q, static_cast<const T*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
+    stage<DP>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
                  kRows, p.d);
-    stage<T, DP>(g, static_cast<const T*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
+    stage<DP>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
                  nq - i0, kRows, p.d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -253,10 +250,10 @@ __global__ void __launch_bounds__(kThreads) cross_dq_simple_kernel(const __grid_
       nd[i] = i0 + ty + 8 * i < nq ? p.nD[at] : 0.f;
     }
   }
-  for (int j0 = split * p.plan.k_chunk; i0 < nq && j0 < j_end; j0 += kCols) {
+  for (int j0 = split * per; i0 < nq && j0 < j_end; j0 += kCols) {
     __syncthreads();
-    stage<T, DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
-    stage<T, DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
+    stage<DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
+    stage<DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
     __syncthreads();
     float s[4][4], dp[4][4];
     rows_by_rows<DP>(q, k, s);
@@ -278,18 +275,18 @@ __global__ void __launch_bounds__(kThreads) cross_dq_simple_kernel(const __grid_
     if (t >= p.Nq) continue;
     if (splits > 1) {
       if (t < nq)
-        put_row<float, DP>(p.part + (((long long)split * p.B + b) * p.Nq + t) * p.Hq * p.d + (long long)h * p.d, acc[i],
+        put_row<DP>(p.part + (((long long)split * p.B + b) * p.Nq + t) * p.Hq * p.d + (long long)h * p.d, acc[i],
                            1.f, p.d);
     } else {
-      put_row<T, DP>(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h, acc[i], p.scale, p.d);
+      put_row<DP>(static_cast<float*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h, acc[i], p.scale, p.d);
     }
   }
 }
 
 // dK and dV. Grid: x the key tile, y key head, z batch * split of the query steps (64
 // queries of one head of the group each, heads outermost).
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) cross_dkdv_simple_kernel(const __grid_constant__ CrossParams p) {
+template <int DP>
+__global__ void __launch_bounds__(kThreads) cross_dkdv_f32_kernel(const __grid_constant__ CrossParams p) {
   extern __shared__ __align__(16) float sm[];
   let_next_begin();
   wait_for_previous();
@@ -298,24 +295,23 @@ __global__ void __launch_bounds__(kThreads) cross_dkdv_simple_kernel(const __gri
   const int splits = p.plan.q_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, hk = blockIdx.y;
   const int j0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int per_head = (p.Nq + kCols - 1) / kCols, steps = per_head * p.G;
-  const int s_end = min(steps, (split + 1) * p.plan.q_chunk);
+  const int per_head = (nq + kCols - 1) / kCols, steps = per_head * p.G, per = (steps + splits - 1) / splits;
+  const int s_end = min(steps, (split + 1) * per);
   uint64_t dk[4][DP / 64][2], dv[4][DP / 64][2];
   clear<DP>(dk);
   clear<DP>(dv);
   if (j0 < nk) {
-    stage<T, DP>(k, static_cast<const T*>(p.k) + b * p.k_st.b + (int64_t)j0 * p.k_st.n + hk * p.k_st.h, p.k_st.n, nk - j0,
+    stage<DP>(k, static_cast<const float*>(p.k) + b * p.k_st.b + (int64_t)j0 * p.k_st.n + hk * p.k_st.h, p.k_st.n, nk - j0,
                  kRows, p.d);
-    stage<T, DP>(v, static_cast<const T*>(p.v) + b * p.v_st.b + (int64_t)j0 * p.v_st.n + hk * p.v_st.h, p.v_st.n, nk - j0,
+    stage<DP>(v, static_cast<const float*>(p.v) + b * p.v_st.b + (int64_t)j0 * p.v_st.n + hk * p.v_st.h, p.v_st.n, nk - j0,
                  kRows, p.d);
   }
-  for (int st = split * p.plan.q_chunk; j0 < nk && st < s_end; ++st) {
+  for (int st = split * per; j0 < nk && st < s_end; ++st) {
     const int h = hk * p.G + st / per_head, i0 = st % per_head * kCols;
-    if (i0 >= nq) continue;
     __syncthreads();
-    stage<T, DP>(q, static_cast<const T*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
+    stage<DP>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
                  kCols, p.d);
-    stage<T, DP>(g, static_cast<const T*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
+    stage<DP>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
                  nq - i0, kCols, p.d);
     float nl[4], nd[4];
 #pragma unroll
@@ -351,24 +347,24 @@ __global__ void __launch_bounds__(kThreads) cross_dkdv_simple_kernel(const __gri
     if (splits > 1) {
       if (j >= nk) continue;
       float* to = p.part_kv + 2 * split * size + (((long long)b * p.Nk + j) * p.Hk + hk) * p.d;
-      put_row<float, DP>(to, dk[i], 1.f, p.d);
-      put_row<float, DP>(to + size, dv[i], 1.f, p.d);
+      put_row<DP>(to, dk[i], 1.f, p.d);
+      put_row<DP>(to + size, dv[i], 1.f, p.d);
     } else {
-      put_row<T, DP>(static_cast<T*>(p.dk) + b * p.dk_st.b + j * p.dk_st.n + hk * p.dk_st.h, dk[i], p.scale, p.d);
-      put_row<T, DP>(static_cast<T*>(p.dv) + b * p.dv_st.b + j * p.dv_st.n + hk * p.dv_st.h, dv[i], 1.f, p.d);
+      put_row<DP>(static_cast<float*>(p.dk) + b * p.dk_st.b + j * p.dk_st.n + hk * p.dk_st.h, dk[i], p.scale, p.d);
+      put_row<DP>(static_cast<float*>(p.dv) + b * p.dv_st.b + j * p.dv_st.n + hk * p.dv_st.h, dv[i], 1.f, p.d);
     }
   }
 }
 
 constexpr int kFwd = 0, kDq = 1, kDkdv = 2;
 
-template <typename T, int DP, int kWhat>
+template <int DP, int kWhat>
 cudaError_t launch_t(const CrossParams& p, cudaStream_t st) {
   constexpr int bytes = Tile<DP>::bytes(kWhat == kFwd ? kRows + 2 * kCols : 2 * kRows + 2 * kCols) +
                         kRows * kPad * 4 * (kWhat == kDkdv ? 2 : 1);
-  constexpr auto kKernel = kWhat == kFwd  ? cross_fwd_simple_kernel<T, DP>
-                           : kWhat == kDq ? cross_dq_simple_kernel<T, DP>
-                                          : cross_dkdv_simple_kernel<T, DP>;
+  constexpr auto kKernel = kWhat == kFwd  ? cross_fwd_f32_kernel<DP>
+                           : kWhat == kDq ? cross_dq_f32_kernel<DP>
+                                          : cross_dkdv_f32_kernel<DP>;
   const cudaError_t e = allow_smem<kKernel>(bytes);
   if (e != cudaSuccess) return e;
   const bool keys = kWhat == kDkdv;
@@ -378,19 +374,14 @@ cudaError_t launch_t(const CrossParams& p, cudaStream_t st) {
 }
 
 template <int kWhat>
-cudaError_t launch(const CrossParams& p, int dtype, cudaStream_t st) {
-  if (dtype == FA_F32) return p.d <= 64 ? launch_t<float, 64, kWhat>(p, st) : launch_t<float, 128, kWhat>(p, st);
-  if (dtype == FA_BF16)
-    return p.d <= 64 ? launch_t<__nv_bfloat16, 64, kWhat>(p, st) : launch_t<__nv_bfloat16, 128, kWhat>(p, st);
-  return p.d <= 64 ? launch_t<__half, 64, kWhat>(p, st) : launch_t<__half, 128, kWhat>(p, st);
+cudaError_t launch(const CrossParams& p, cudaStream_t st) {
+  return p.d <= 64 ? launch_t<64, kWhat>(p, st) : launch_t<128, kWhat>(p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_fwd_simple(const CrossParams& p, int dtype, cudaStream_t st) { return launch<kFwd>(p, dtype, st); }
-cudaError_t launch_cross_dq_simple(const CrossParams& p, int dtype, cudaStream_t st) { return launch<kDq>(p, dtype, st); }
-cudaError_t launch_cross_dkdv_simple(const CrossParams& p, int dtype, cudaStream_t st) {
-  return launch<kDkdv>(p, dtype, st);
-}
+cudaError_t launch_cross_fwd_f32(const CrossParams& p, cudaStream_t st) { return launch<kFwd>(p, st); }
+cudaError_t launch_cross_dq_f32(const CrossParams& p, cudaStream_t st) { return launch<kDq>(p, st); }
+cudaError_t launch_cross_dkdv_f32(const CrossParams& p, cudaStream_t st) { return launch<kDkdv>(p, st); }
 
 }  // namespace fa

@@ -1,0 +1,545 @@
+// Forward of cross attention on the sm_103a tensor cores: O and the row log-sum-exp of
+// queries over the keys of another sequence, with shared key heads, padded batches
+// and splits of the key axis.
+//
+//   S = Q K_j^T (fp32, TMEM), m = running row maximum of S * scale * log2e,
+//   P = exp2(S * scale * log2e - m), l += rowsum(P), O += P V_j;  O / l, m + log2 l
+//
+// A persistent grid: one CTA an SM takes units in a fixed stride. A unit is two 128-row
+// tiles A and B of query rows that share a key head (of one head, or of several where
+// queries are few) against the keys of one split. TMEM: S_A [0, 128), S_B [128, 256),
+// O_A [256, 256 + d), O_B after it. One warp issues all MMAs, per key block
+// O_A(j), S_A(j+1), O_B(j), S_B(j+1): while tile A's softmax warps turn S_A into P_A, the
+// tensor cores run tile B. Eight softmax warps a tile: a row is split between two
+// warps (the same TMEM lane), 64 keys of a block each, that exchange only their
+// halves' maxima a block and their sums at the end. P goes back over the S columns it
+// came from as a 16-bit image (eight rounded columns, then eight residual columns per
+// 16 keys; the residual MMAs run where a probability may exceed 1/64 of the row's
+// sum) and the O MMA reads it from TMEM. The row's reference m moves only when a block's
+// maximum exceeds it by more than 2^8.
+//
+// Few keys a unit are the common case here (a text's 77 to 512), so a unit is short: steps,
+// ring stages and barrier phases run on from unit to unit, the next unit's queries and
+// first keys are loaded and its first S MMAs issued while the last block's softmax
+// and the epilogue of this one run. Only the O accumulator is handed over: its next first
+// MMA waits until the epilogue has loaded it (OFree).
+//
+// Masks. Keys from the split's end on get P = 0 by selects, so K's rows there may hold
+// anything; V's rows there are zeroed in shared memory before the MMA (0 * NaN). Rows of
+// Q that are not there give rows of S that nobody reads.
+#include "fa_cross.h"
+
+namespace fa {
+
+namespace {
+
+constexpr int kThreads = 576;  // TMA warp, MMA warp, 2 x 8 softmax warps
+constexpr float kRescaleLog2 = 8.f;
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D>
+struct Cfg {
+  static constexpr int kPanels = D / 64;
+  static constexpr uint32_t kPanel = 128 * 128;        // 16 KB: 128 rows x 64 elements
+  static constexpr uint32_t kTile = kPanels * kPanel;  // one 128-row tile of Q, K or V
+  static constexpr int kNK = D == 64 ? 4 : 2;          // K ring stages
+  static constexpr int kNV = D == 64 ? 4 : 2;          // V ring stages
+  static constexpr uint32_t oQ = 0;                    // [2 tiles]
+  static constexpr uint32_t oK = 2 * kTile;
+  static constexpr uint32_t oV = oK + kNK * kTile;
+  static constexpr uint32_t oBar = oV + kNV * kTile;
+  static constexpr int bQ = 0;                         // [2] a unit's Q tile landed
+  static constexpr int bQFree = bQ + 2;                // [2] its last S MMA done
+  static constexpr int bKFull = bQFree + 2;
+  static constexpr int bKEmpty = bKFull + kNK;
+  static constexpr int bVFull = bKEmpty + kNK;
+  static constexpr int bVEmpty = bVFull + kNV;
+  static constexpr int bSFull = bVEmpty + kNV;         // [2] S landed
+  static constexpr int bPFull = bSFull + 2;            // [2] P image written
+  static constexpr int bODone = bPFull + 2;            // [2] O MMA of a block done
+  static constexpr int bOFree = bODone + 2;            // [2] the epilogue has read O
+  static constexpr int bDrain = bOFree + 2;
+  static constexpr int bXchg = bDrain + 1;             // [tile][lane quarter][block parity] row-maximum exchange
+  static constexpr int bSum = bXchg + 16;              // [tile][lane quarter] final row-sum exchange
+  static constexpr int kBars = bSum + 8;
+  static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
+  static constexpr uint32_t oAbort = oTmemSlot + 8;
+  static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [tile][8 warps] split votes
+  // row maxima [tile][block parity][half][128 rows], then the sums [tile][half][128 rows]
+  static constexpr uint32_t oXchg = oFlags + 2 * 8 * 4;
+  static constexpr uint32_t kSmem = oXchg + (2 * 2 * 2 + 2 * 2) * 128 * 4 + 1024;  // + slack for 1024-byte alignment
+  static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
+};
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_fwd_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
+  auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
+  const int units = cross_units<2>(p);
+  // The first unit from idx on in this CTA's stride that has blocks to compute; -1: none.
+  auto next_work = [&](int idx, CrossUnit& u) -> int {
+    for (; idx < units; idx += gridDim.x) {
+      cross_unit<2>(p, idx, u);
+      if (u.blocks > 0) return idx;
+    }
+    return -1;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(C::bQ + x), 1);
+      mbar_init(bar(C::bQFree + x), 1);
+      mbar_init(bar(C::bSFull + x), 1);
+      mbar_init(bar(C::bPFull + x), 256);  // the tile's eight softmax warps
+      mbar_init(bar(C::bODone + x), 1);
+      mbar_init(bar(C::bOFree + x), 256);
+    }
+    for (int s = 0; s < C::kNK; ++s) {
+      mbar_init(bar(C::bKFull + s), 1);
+      mbar_init(bar(C::bKEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kNV; ++s) {
+      mbar_init(bar(C::bVFull + s), 1);
+      mbar_init(bar(C::bVEmpty + s), 1);
+    }
+    mbar_init(bar(C::bDrain), 1);
+    for (int x = 0; x < 16; ++x) mbar_init(bar(C::bXchg + x), 64);  // the two warps of a row quarter
+    for (int x = 0; x < 8; ++x) mbar_init(bar(C::bSum + x), 64);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(sb + C::oTmemSlot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::oTmemSlot);
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)C::kPanels * 128u << (p.plan.q_tile.q_log + p.plan.q_tile.h_log);
+      int t = 0, nq[2] = {0, 0}, issuedK = 0, issuedV = 0;  // blocks and tiles loaded
+      bool ok = true;
+      CrossUnit u;
+      for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const CrossRows r = cross_rows(p, u, u.first + x);
+          if (!ok || !r.live) continue;
+          if (nq[x] > 0 && !mbar_wait(bar(C::bQFree + x), (nq[x] - 1) & 1, abort_flag, p.status)) {
+            ok = false;
+            continue;
+          }
+          mbar_arrive_expect_tx(bar(C::bQ + x), q_bytes);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(sb + C::oQ + x * C::kTile + pn * C::kPanel, &tmQ, bar(C::bQ + x), 64 * pn, r.q0, r.h0, u.b);
+          ++nq[x];
+        }
+        for (int j = 0; ok && j < u.blocks; ++j, ++t) {
+          const int sk = t % C::kNK, sv = t % C::kNV, row = u.j_begin + 128 * j;
+          if (!mbar_wait(bar(C::bKEmpty + sk), ((t / C::kNK) & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::bKFull + sk), C::kTile);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(sb + C::oK + sk * C::kTile + pn * C::kPanel, &tmK, bar(C::bKFull + sk), 64 * pn, row, u.hk, u.b);
+          issuedK = t + 1;
+          if (!mbar_wait(bar(C::bVEmpty + sv), ((t / C::kNV) & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::bVFull + sv), C::kTile);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(sb + C::oV + sv * C::kTile + pn * C::kPanel, &tmV, bar(C::bVFull + sv), 64 * pn, row, u.hk, u.b);
+          issuedV = t + 1;
+        }
+      }
+      if (*abort_flag) {
+        // Let every copy this thread started land before the CTA exits.
+        for (int x = 0; x < 2; ++x)
+          if (nq[x] > 0) mbar_wait_drain(bar(C::bQ + x), (nq[x] - 1) & 1, p.status);
+        for (int j = max(0, issuedK - C::kNK); j < issuedK; ++j)
+          mbar_wait_drain(bar(C::bKFull + j % C::kNK), (j / C::kNK) & 1, p.status);
+        for (int j = max(0, issuedV - C::kNV); j < issuedV; ++j)
+          mbar_wait_drain(bar(C::bVFull + j % C::kNV), (j / C::kNV) & 1, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------- MMA issuer --------------------------------
+    // S_X = Q_X K_j^T: M = 128 rows, N = 128 keys, K = d (both K-major). O_X += P_X V_j:
+    // M = 128, N = d, K = 128 keys; A = the P image in TMEM, B = V_j read MN-major.
+    constexpr uint32_t idS = make_idesc(128, 128, kBf16, false, false);
+    constexpr uint32_t idO = make_idesc(128, D, kBf16, false, true);
+    const uint64_t dQ0 = make_sdesc(sb + C::oQ, 16, 1024);
+    const uint64_t dK0 = make_sdesc(sb + C::oK, 16, 1024);
+    const uint64_t dV0 = make_sdesc(sb + C::oV, C::kPanel, 1024);
+    int steps[2] = {0, 0}, tiles[2] = {0, 0};  // blocks and units a tile has been through
+    bool ok = true;
+    // S of tile x for block t of the CTA (K landed); last: the unit's last for this tile.
+    auto issue_s = [&](int x, int t, bool last) {
+      const uint64_t kd = desc_add(dK0, (t % C::kNK) * C::kTile), qd = desc_add(dQ0, x * C::kTile);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc_mma_ss_w(tmem + 128 * x, desc_add(qd, (k >> 2) * C::kPanel + (k & 3) * 32),
+                    desc_add(kd, (k >> 2) * C::kPanel + (k & 3) * 32), idS, k > 0 ? 1u : 0u);
+      tc_commit_w(bar(C::bSFull + x));
+      if (last) tc_commit_w(bar(C::bQFree + x));
+    };
+    auto issue_o = [&](int x, int t, bool first) {
+      const uint64_t vd = desc_add(dV0, (t % C::kNV) * C::kTile);
+      const uint32_t tO = tmem + 256 + D * x, tP = tmem + 128 * x;
+      const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 8 * x);
+      const int4 fa = f4[0], fb = f4[1];
+      const bool split = (fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w) != 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) tc_mma_ts_w(tO, tP + 16 * k, desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
+      if (split) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tc_mma_ts_w(tO, tP + 16 * k + 8, desc_add(vd, 2048 * k), idO, 1u);
+      }
+      tc_commit_w(bar(C::bODone + x));
+    };
+    CrossUnit u, next;
+    bool live[2] = {false, false}, live_next[2];  // the unit's tiles, and the next unit's
+    int idx = next_work(blockIdx.x, u), t = 0;
+    if (idx >= 0) {
+      ok = warp_wait<kIssuerPoll>(bar(C::bKFull), 0, abort_flag, p.status);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        live[x] = cross_rows(p, u, u.first + x).live;
+        if (!ok || !live[x]) continue;
+        ok = warp_wait<kIssuerPoll>(bar(C::bQ + x), 0, abort_flag, p.status);
+        if (!ok) continue;
+        tc_fence_after();
+        issue_s(x, 0, u.blocks == 1);
+      }
+      if (ok) tc_commit_w(bar(C::bKEmpty));
+    }
+    while (ok && idx >= 0) {
+      const int after = next_work(idx + gridDim.x, next);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) live_next[x] = after >= 0 && cross_rows(p, next, next.first + x).live;
+      for (int j = 0; ok && j < u.blocks; ++j, ++t) {
+        const int sv = t % C::kNV;
+        const bool inside = j + 1 < u.blocks, more = inside || after >= 0;
+        if (!warp_wait<kIssuerPoll>(bar(C::bVFull + sv), (t / C::kNV) & 1, abort_flag, p.status) ||
+            (more && !warp_wait<kIssuerPoll>(bar(C::bKFull + (t + 1) % C::kNK), ((t + 1) / C::kNK) & 1, abort_flag,
+                                             p.status))) {
+          ok = false;
+          break;
+        }
+        // V's rows from the sequence's end on, as far as they are the tensor's (past it: zeros by TMA).
+        const int from = u.j_end - u.j_begin - 128 * j, to = min(128, p.Nk - u.j_begin - 128 * j);
+        if (from < to) zero_rows<C::kPanels>(sb + C::oV + sv * C::kTile, C::kPanel, from, to);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok) continue;
+          if (live[x]) {
+            if (!warp_wait<kIssuerPoll>(bar(C::bPFull + x), steps[x] & 1, abort_flag, p.status) ||
+                (j == 0 && tiles[x] > 0 &&
+                 !warp_wait<kIssuerPoll>(bar(C::bOFree + x), (tiles[x] - 1) & 1, abort_flag, p.status))) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            issue_o(x, t, j == 0);
+            ++steps[x];
+            if (!inside) ++tiles[x];
+          }
+          if (inside ? live[x] : live_next[x]) {
+            if (!inside && !warp_wait<kIssuerPoll>(bar(C::bQ + x), tiles[x] & 1, abort_flag, p.status)) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            issue_s(x, t + 1, inside ? j + 2 == u.blocks : next.blocks == 1);
+          }
+        }
+        if (!ok) break;
+        tc_commit_w(bar(C::bVEmpty + sv));                             // V read by both O MMAs
+        if (more) tc_commit_w(bar(C::bKEmpty + (t + 1) % C::kNK));  // the next K read by both S MMAs
+      }
+      u = next;
+      idx = after;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) live[x] = live_next[x];
+    }
+    // Every MMA this warp issued is complete before the CTA frees TMEM and exits.
+    tc_commit_w(bar(C::bDrain));
+    if (lane == 0) mbar_wait_drain(bar(C::bDrain), 0, p.status);
+    __syncwarp();
+  } else {
+    // ------------------------------ softmax warps ------------------------------
+    // warps 2-17; a warp reaches TMEM lanes 32 (warp % 4) .. + 31
+    const int x = (warp - 2) >> 3;           // tile
+    const int half = ((warp - 2) >> 2) & 1;  // keys [64 half, 64 half + 64) of a block
+    const int wq = warp & 3;
+    const int il = wq * 32 + lane;  // row in the tile, TMEM lane
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + 128 * x + 64 * half;           // this warp's 64 S columns
+    const uint32_t tO = tmem + lane_off + 256 + D * x + (D / 2) * half;  // and D/2 O columns
+    float* xchg = reinterpret_cast<float*>(smem + C::oXchg);
+    float* xl = xchg + 8 * 128 + (x * 2) * 128;
+    const int pq = 4 * x + wq;  // the two warps holding rows 32 wq .. 32 wq + 31 of tile x
+    const float c2 = p.scale_log2;
+    const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
+    const bool row_in = row_h < p.plan.q_tile.heads();
+    const long long rows = (long long)p.B * p.Nq * p.Hq;
+    int n = 0, done = 0;  // blocks and units this tile has been through
+    bool ok = true;
+    // Waits block (the hardware suspends the warp): each tile's warps idle about half the
+    // time, and spinning would take issue slots from the other tile's warps.
+    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
+      CrossUnit u;
+      cross_unit<2>(p, idx, u);
+      const CrossRows rt = cross_rows(p, u, u.first + x);
+      if (!rt.there) continue;
+      float mref = -INFINITY, lsum = 0.f;  // lsum: this half's part of the row sum
+      const int blocks = rt.live ? u.blocks : 0;
+      for (int j = 0; j < blocks; ++j, ++n) {
+        if (!warp_wait<false>(bar(C::bSFull + x), n & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int hi = u.j_end - u.j_begin - 128 * j - 64 * half;  // this warp's real keys: columns 0 .. hi - 1
+        // Pass 1: this half's maximum of S.
+        float hmax = -INFINITY;
+        {
+          uint32_t s0[32], s1[32];
+          tmem_ld32(tS, s0);
+          tmem_ld32(tS + 32, s1);
+          tmem_ld_wait2(s0, s1);
+          if (hi >= 64) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              m0 = fmax3(m0, __uint_as_float(s0[e]), __uint_as_float(s0[e + 1]));
+              m1 = fmax3(m1, __uint_as_float(s1[e]), __uint_as_float(s1[e + 1]));
+            }
+            hmax = fmaxf(m0, m1);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              hmax = (e < hi) ? fmaxf(hmax, __uint_as_float(s0[e])) : hmax;
+              hmax = (32 + e < hi) ? fmaxf(hmax, __uint_as_float(s1[e])) : hmax;
+            }
+          }
+        }
+        // The block maximum of the row: this half's and the other warp's (slots alternate
+        // with the block parity, so a slot is rewritten only after the partner has passed
+        // the next exchange, i.e. has read it).
+        float* xs = xchg + ((x * 2 + (n & 1)) * 2) * 128;
+        xs[half * 128 + il] = hmax;
+        warp_arrive(bar(C::bXchg + 2 * pq + (n & 1)));
+        if (!warp_wait<false>(bar(C::bXchg + 2 * pq + (n & 1)), (n >> 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        const float bmax = fmaxf(hmax, xs[(half ^ 1) * 128 + il]) * c2;  // (scale > 0)
+        // Lazy rescale. Both warps of a row take the same decision; each rescales its D/2 O columns.
+        const bool mv = bmax > mref + kRescaleLog2;
+        const float alpha = mv ? ex2_approx(mref - bmax) : 1.f;  // 0 when mref = -inf
+        // (warp-wide decision: the wait and the TMEM accesses below are collective)
+        if (j > 0 && __any_sync(0xffffffffu, mv && mref != -INFINITY)) {
+          // this tile's O MMA of the block before is done before its rows are rescaled
+          if (!warp_wait<false>(bar(C::bODone + x), (n - 1) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < D / 64; ++cc) {
+            uint32_t r[32];
+            tmem_ld32(tO + 32 * cc, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tmem_st32(tO + 32 * cc, r);
+          }
+        }
+        if (mv) {
+          lsum *= alpha;
+          mref = bmax;
+        }
+        const float base = mref == -INFINITY ? 0.f : mref;  // (every score so far is -inf or NaN)
+        // Pass 2, 32 keys at a time: P (0 past the end), this half's running sum, and the
+        // 16-bit image of the two MMA K steps over the same columns. A chunk writes residual
+        // columns where the block's largest probability may exceed 1/64 of this half's sum so
+        // far (a part of the final row sum, so the bound holds for the final P); zeros otherwise.
+        const uint64_t cc2 = f2_pack(c2, c2), nm2 = f2_pack(-base, -base);
+        const float pmax = ex2_approx(bmax - base);
+        bool split = false;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t cur[32];
+          __syncwarp();
+          tmem_ld32(tS + 32 * q, cur);
+          tmem_ld_wait(cur);
+          uint64_t sum2 = f2_pack(0.f, 0.f);
+          if (hi >= 64) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sum2 = f2_add(sum2, f2_pack(p0, p1));
+              cur[e] = __float_as_uint(p0);
+              cur[e + 1] = __float_as_uint(p1);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
+              p0 = (32 * q + e < hi) ? ex2_approx(p0) : 0.f;
+              p1 = (32 * q + e + 1 < hi) ? ex2_approx(p1) : 0.f;
+              sum2 = f2_add(sum2, f2_pack(p0, p1));
+              cur[e] = __float_as_uint(p0);
+              cur[e + 1] = __float_as_uint(p1);
+            }
+          }
+          __syncwarp();
+          float s0, s1;
+          f2_unpack(sum2, s0, s1);
+          lsum += s0 + s1;
+          const bool sp = __any_sync(0xffffffffu, row_in && pmax > kSplitThreshold * lsum);
+          split |= sp;
+          // (sp is warp-uniform: a real branch, the residuals are computed only when needed)
+          if (sp) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float a = __uint_as_float(cur[16 * k + 2 * e]), c = __uint_as_float(cur[16 * k + 2 * e + 1]);
+                w[e] = pack2<kBf16>(a, c);
+                w[8 + e] = pack2_residual<kBf16>(a, c, w[e]);
+              }
+              tmem_st16(tS + 32 * q + 16 * k, w);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                w[e] = pack2<kBf16>(__uint_as_float(cur[16 * k + 2 * e]), __uint_as_float(cur[16 * k + 2 * e + 1]));
+                w[8 + e] = 0u;
+              }
+              tmem_st16(tS + 32 * q + 16 * k, w);
+            }
+          }
+        }
+        tmem_st_wait();
+        if (lane == 0) flags[8 * x + 4 * half + wq] = split ? 1 : 0;
+        tc_fence_before();
+        warp_arrive(bar(C::bPFull + x));
+      }
+      if (!ok) break;
+      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time (all of
+      // them in registers at once spilled). The accumulator is released (OFree) behind its last load.
+      float ltot = 0.f;
+      if (blocks > 0) {
+        xl[half * 128 + il] = lsum;
+        warp_arrive(bar(C::bSum + pq));
+        if (!warp_wait<false>(bar(C::bSum + pq), done & 1, abort_flag, p.status) ||
+            !warp_wait<false>(bar(C::bODone + x), (n - 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        ltot = lsum + xl[(half ^ 1) * 128 + il];
+        tc_fence_after();
+        ++done;
+      }
+      const int i = rt.q0 + row_q, h = rt.h0 + row_h;
+      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < u.nq && ltot != 0.f;  // (a NaN sum counts as there)
+      const float inv = 1.f / ltot, lse2 = has ? mref + lg2(ltot) : -INFINITY;
+      const long long at = ((long long)u.b * p.Hq + h) * p.Nq + i;
+      const bool parts = p.plan.k_splits > 1;
+      if (in && half == 0) {
+        if (parts)
+          p.part_lse[u.split * rows + at] = lse2;
+        else
+          p.lse_out[at] = has ? lse2 * 0.6931471805599453f : -INFINITY;
+      }
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t r[32];
+        if (blocks > 0) {
+          __syncwarp();
+          tmem_ld32(tO + 32 * cc, r);
+          tmem_ld_wait(r);
+          if (cc == D / 64 - 1) {
+            tc_fence_before();
+            warp_arrive(bar(C::bOFree + x));
+          }
+        }
+        if (!has) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        const int col = (D / 2) * half + 32 * cc;
+        if (in && parts) {
+          if (has) store32_f(p.part + (u.split * rows + ((long long)u.b * p.Nq + i) * p.Hq + h) * D + col, r, inv);
+        } else if (in) {
+          store32_h<kBf16>(static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + col, r,
+                           has ? inv : 0.f);
+        }
+      }
+      __syncwarp();  // (the stores are per lane: converge for the next unit's collective accesses)
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_t(const CrossParams& p, const CUtensorMap* maps, cudaStream_t st) {
+  using C = Cfg<D>;
+  auto kern = cross_fwd_kernel<D, kBf16>;
+  const int smem = (int)(C::kSmem > kMinSmemOneCtaPerSm ? C::kSmem : kMinSmemOneCtaPerSm);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)p.B * p.Hk * ((p.plan.q_tile.count(p.Nq, p.G) + 1) / 2) * p.plan.k_splits;
+  kern<<<(unsigned)(units < 152 ? units : 152), kThreads, smem, st>>>(p, maps[0], maps[1], maps[2]);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_fwd_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st) {
+  if (p.d == 128) return bf16 ? launch_t<128, true>(p, maps, st) : launch_t<128, false>(p, maps, st);
+  return bf16 ? launch_t<64, true>(p, maps, st) : launch_t<64, false>(p, maps, st);
+}
+
+}  // namespace fa

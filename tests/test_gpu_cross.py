@@ -50,6 +50,17 @@ def test_sizes(size, dtype):
     run(*make(*size, dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("size,q_lens,k_lens", [
+    ((8, 520, 300, 16, 8, 64), None, None),
+    ((9, 300, 400, 16, 4, 128), [300, 0, 1, 129, 200, 300, 64, 257, 300], [400, 400, 129, 0, 1, 256, 300, 128, 399]),
+    ((40, 70, 130, 8, 8, 64), None, [(37 * b) % 131 for b in range(40)]),
+])
+def test_many_units_a_block(size, q_lens, k_lens, dtype):
+    """More units of work than the GPU has places, some of them empty, so that blocks go from one to the next."""
+    run(*make(*size, dtype), q_lens, k_lens)
+
+
 @pytest.mark.parametrize("d", [1, 17, 63, 96, 128])
 def test_fp32_head_dimensions(d):
     run(*make(2, 70, 45, 4, 2, d, F32))
