@@ -127,11 +127,18 @@ __device__ __forceinline__ void cross_unit(const CrossParams& p, int idx, CrossU
   u.blocks = any ? max(u.j_end - u.j_begin + 127, 0) >> 7 : 0;
 }
 
-// 32 fp32 values as 16-bit or fp32 to consecutive places.
+// The same number, opaque to the compiler: what is computed from it is computed anew instead of being kept
+// in registers since the first time (the row-math loops have none to spare, and their spills miss L1).
+__device__ __forceinline__ int again(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+// 16 fp32 values of the accumulators, times mul as 16-bit values, or as they are, to consecutive places.
 template <bool kBf16>
-__device__ __forceinline__ void store32_h(uint16_t* to, const uint32_t (&r)[32], float mul) {
+__device__ __forceinline__ void store16_h(uint16_t* to, const uint32_t* r, float mul) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < 2; ++t) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -139,9 +146,9 @@ __device__ __forceinline__ void store32_h(uint16_t* to, const uint32_t (&r)[32],
     reinterpret_cast<uint4*>(to)[t] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-__device__ __forceinline__ void store32_f(float* to, const uint32_t (&r)[32], float mul) {
+__device__ __forceinline__ void store16_f(float* to, const uint32_t* r, float mul = 1.f) {
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int t = 0; t < 4; ++t)
     reinterpret_cast<float4*>(to)[t] =
         make_float4(__uint_as_float(r[4 * t]) * mul, __uint_as_float(r[4 * t + 1]) * mul,
                     __uint_as_float(r[4 * t + 2]) * mul, __uint_as_float(r[4 * t + 3]) * mul);

@@ -342,18 +342,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tSc = tS + lane_off + 64 * bb + 32 * c, tdPc = tdP + lane_off + 64 * bb + 32 * c;
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-    const long long size = (long long)p.B * p.Nk * p.Hk * D;
     int kl = 0, G = 0;
     bool ok = true;
     for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
-      KUnit u;
-      k_unit(p, idx, u);
-      const int j = u.j0 + jl;
-      for (int it = (bb ^ G) & 1; it < u.steps; it += 2) {
+      // The columns with real queries of any step but a head's last (or last few heads') and of that one,
+      // none for a lane without a key; chunk: the step's place among a head's chunks.
+      int steps, chunks, chunk;
+      uint32_t full, tail;
+      {
+        KUnit u;
+        k_unit(p, idx, u);
+        steps = u.steps;
+        chunks = max(u.chunks, 1);
+        chunk = (u.first + ((bb ^ G) & 1)) % chunks;
+        full = step_columns(p.plan.step, c, kStep);
+        tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
+        if (u.j0 + jl >= u.nk) full = tail = 0u;
+      }
+      for (int it = (bb ^ G) & 1; it < steps; it += 2) {
         const int gs = G + it, s = gs % C::kNS;
-        int h0, q0;
-        k_step(p, u, it, h0, q0);
-        const uint32_t allow = j < u.nk ? step_columns(p.plan.step, c, u.nq - q0) : 0u;
+        const uint32_t allow = chunk == chunks - 1 ? tail : full;
+        chunk += 2;
+        chunk -= chunk >= chunks ? chunks : 0;
+        chunk -= chunk >= chunks ? chunks : 0;  // (a head of one chunk)
         if (!warp_wait<kRowMathPoll>(bar(C::bQFull + s), (gs / C::kNS) & 1, abort_flag, p.status) ||
             !warp_wait<kRowMathPoll>(bar(C::bSFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
           ok = false;
@@ -464,60 +475,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // Epilogue, by the pair that ran the unit's last step: dV, then dK, each warpgroup half of the
-      // columns; both accumulators are released (AccFree) before dK's stores.
-      const bool epi = u.steps > 0 ? bb == ((G + u.steps - 1) & 1) : bb == 0;
+      // columns; both accumulators are released (AccFree) behind the last load.
+      const bool epi = steps > 0 ? bb == ((G + steps - 1) & 1) : bb == 0;
       if (epi) {
-        constexpr int kChunks = D / 64;
+        KUnit u;
+        k_unit(p, again(idx), u);
+        const int j = u.j0 + jl;
+        const long long size = (long long)p.B * p.Nk * p.Hk * D;
+        if (steps > 0) {
+          if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
 #pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-          const bool isK = which == 1;
-          uint32_t r[kChunks][32];
-          if (u.steps > 0) {
-            if (!isK) {
-              if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-            }
-            __syncwarp();  // the stores are per lane: converge for the TMEM loads
-            const uint32_t col0 = (isK ? tdK : tdV) + lane_off + c * (D / 2);
+        for (int part = 0; part < D / 16; ++part) {  // 16 columns of dV, then of dK
+          const bool isK = part >= D / 32;
+          const int col = c * (D / 2) + 16 * (part & (D / 32 - 1));
+          uint32_t r[16];  // (set on every path: left undefined on one, 25 values of the steps' loop spilled)
 #pragma unroll
-            for (int cc = 0; cc < kChunks; ++cc) tmem_ld32(col0 + 32 * cc, r[cc]);
-            if constexpr (kChunks == 2)
-              tmem_ld_wait2(r[0], r[1]);
-            else
-              tmem_ld_wait(r[0]);
-            if (isK) {
+          for (int x = 0; x < 16; ++x) r[x] = 0u;
+          if (steps > 0) {
+            __syncwarp();  // the stores are per lane: converge for the TMEM load
+            tmem_ld16((isK ? tdK : tdV) + lane_off + col, r);
+            tmem_ld_wait16(r);
+            if (part == D / 16 - 1) {
               tc_fence_before();
               warp_arrive(bar(C::bAccFree));
             }
           }
-          if (u.steps == 0 || j >= u.nk) {
-#pragma unroll
-            for (int cc = 0; cc < kChunks; ++cc)
-#pragma unroll
-              for (int x = 0; x < 32; ++x) r[cc][x] = 0u;
-          }
           if (p.plan.q_splits > 1) {
             if (j < u.nk) {
               float* to = p.part_kv + 2 * u.split * size + (isK ? 0 : size) +
-                          (((long long)u.b * p.Nk + j) * p.Hk + u.hk) * D + c * (D / 2);
-#pragma unroll
-              for (int cc = 0; cc < kChunks; ++cc) store32_f(to + 32 * cc, r[cc], 1.f);
+                          (((long long)u.b * p.Nk + j) * p.Hk + u.hk) * D + col;
+              store16_f(to, r);
             }
           } else if (j < p.Nk) {
             const fa_strides& st = isK ? p.dk_st : p.dv_st;
-            uint16_t* to = static_cast<uint16_t*>(isK ? p.dk : p.dv) + u.b * st.b + j * st.n + u.hk * st.h + c * (D / 2);
 #pragma unroll
-            for (int cc = 0; cc < kChunks; ++cc) store32_h<kBf16>(to + 32 * cc, r[cc], isK ? p.scale : 1.f);
+            for (int x = 0; x < 16; ++x) r[x] = j < u.nk ? r[x] : 0u;  // (0 * NaN of a real query's)
+            store16_h<kBf16>(static_cast<uint16_t*>(isK ? p.dk : p.dv) + u.b * st.b + j * st.n + u.hk * st.h + col, r,
+                             isK ? p.scale : 1.f);
           }
         }
-        if (!ok) break;
         __syncwarp();
       }
-      if (u.steps > 0) ++kl;
-      G += u.steps;
+      if (steps > 0) ++kl;
+      G += steps;
     }
   }
 
@@ -762,21 +767,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     int kl = 0, G = 0;
     bool ok = true;
     for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
-      CrossUnit u;
-      cross_unit<1>(p, idx, u);
-      const CrossRows rt = cross_rows(p, u, u.first);
-      const int i = rt.q0 + row_q, h = rt.h0 + row_h;
+      int blocks, left = -32 * c;  // left: real keys from this warpgroup's first column on
       float nL2 = -INFINITY, nD = 0.f;
-      if (u.blocks > 0 && row_in) {  // (rows past the sequence hold -inf and 0)
-        const long long at = ((long long)u.b * p.Hq + h) * p.nq_pad + i;
-        nL2 = p.nL2[at];
-        nD = p.nD[at];
+      {
+        CrossUnit u;
+        cross_unit<1>(p, idx, u);
+        const CrossRows rt = cross_rows(p, u, u.first);
+        blocks = u.blocks;
+        left += u.j_end - u.j_begin;
+        if (blocks > 0 && row_in) {  // (rows past the sequence hold -inf and 0)
+          const long long at = ((long long)u.b * p.Hq + rt.h0 + row_h) * p.nq_pad + rt.q0 + row_q;
+          nL2 = p.nL2[at];
+          nD = p.nD[at];
+        }
       }
       const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
-      for (int it = 0; it < u.blocks; ++it) {
+      for (int it = 0; it < blocks; ++it) {
         const int gs = G + it, bb = gs & 1;
         const uint32_t tSc = tS + lane_off + 128 * bb + 32 * c;
-        const uint32_t allow = bit_range(0, u.j_end - u.j_begin - 128 * it - 32 * c);
+        const uint32_t allow = bit_range(0, left - 128 * it);
         if (!warp_wait<kRowMathPoll>(bar(C::bSFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
           ok = false;
           break;
@@ -850,7 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (AccFree) before the stores, so the next unit's first MMA can start meanwhile.
       constexpr int kChunks = D / 64;  // 16-column TMEM loads per thread
       uint32_t r[kChunks][16];
-      if (u.blocks > 0) {
+#pragma unroll
+      for (int cc = 0; cc < kChunks; ++cc)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) r[cc][x] = 0u;
+      if (blocks > 0) {
         if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
           ok = false;
           break;
@@ -868,40 +881,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bAccFree));
         ++kl;
       }
-      if (u.blocks == 0 || i >= u.nq) {
-#pragma unroll
-        for (int cc = 0; cc < kChunks; ++cc)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) r[cc][x] = 0u;
-      }
+      CrossUnit u;
+      cross_unit<1>(p, again(idx), u);
+      const CrossRows rt = cross_rows(p, u, u.first);
+      const int i = rt.q0 + row_q, h = rt.h0 + row_h;
       if (row_in && i < p.Nq) {
         if (p.plan.k_splits > 1) {
           if (i < u.nq) {
             float* to = p.part + ((((long long)u.split * p.B + u.b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4);
 #pragma unroll
-            for (int cc = 0; cc < kChunks; ++cc)
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                reinterpret_cast<float4*>(to + 16 * cc)[x] =
-                    make_float4(__uint_as_float(r[cc][4 * x]), __uint_as_float(r[cc][4 * x + 1]),
-                                __uint_as_float(r[cc][4 * x + 2]), __uint_as_float(r[cc][4 * x + 3]));
+            for (int cc = 0; cc < kChunks; ++cc) store16_f(to + 16 * cc, r[cc]);
           }
         } else {
           uint16_t* to = static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4);
+          const bool real = i < u.nq;  // (what stands in other rows of the accumulator may be NaN)
 #pragma unroll
           for (int cc = 0; cc < kChunks; ++cc) {
-            uint32_t w[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              w[x] = pack2<kBf16>(__uint_as_float(r[cc][2 * x]) * p.scale, __uint_as_float(r[cc][2 * x + 1]) * p.scale);
-            uint4* gp = reinterpret_cast<uint4*>(to + 16 * cc);
-            gp[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            gp[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int x = 0; x < 16; ++x) r[cc][x] = real ? r[cc][x] : 0u;
+            store16_h<kBf16>(to + 16 * cc, r[cc], p.scale);
           }
         }
       }
       __syncwarp();
-      G += u.blocks;
+      G += blocks;
     }
   }
 

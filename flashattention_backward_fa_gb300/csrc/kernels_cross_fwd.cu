@@ -306,25 +306,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c2 = p.scale_log2;
     const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
     const bool row_in = row_h < p.plan.q_tile.heads();
-    const long long rows = (long long)p.B * p.Nq * p.Hq;
     int n = 0, done = 0;  // blocks and units this tile has been through
     bool ok = true;
     // Waits block (the hardware suspends the warp): each tile's warps idle about half the
     // time, and spinning would take issue slots from the other tile's warps.
     for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
-      CrossUnit u;
-      cross_unit<2>(p, idx, u);
-      const CrossRows rt = cross_rows(p, u, u.first + x);
-      if (!rt.there) continue;
+      int blocks, left = -64 * half;  // left: this warp's real keys from the block's start on
+      {
+        CrossUnit u;
+        cross_unit<2>(p, idx, u);
+        const CrossRows rt = cross_rows(p, u, u.first + x);
+        if (!rt.there) continue;
+        blocks = rt.live ? u.blocks : 0;
+        left += u.j_end - u.j_begin;
+      }
       float mref = -INFINITY, lsum = 0.f;  // lsum: this half's part of the row sum
-      const int blocks = rt.live ? u.blocks : 0;
       for (int j = 0; j < blocks; ++j, ++n) {
         if (!warp_wait<false>(bar(C::bSFull + x), n & 1, abort_flag, p.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int hi = u.j_end - u.j_begin - 128 * j - 64 * half;  // this warp's real keys: columns 0 .. hi - 1
+        const int hi = left - 128 * j;  // columns 0 .. hi - 1
         // Pass 1: this half's maximum of S.
         float hmax = -INFINITY;
         {
@@ -460,8 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bPFull + x));
       }
       if (!ok) break;
-      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time (all of
-      // them in registers at once spilled). The accumulator is released (OFree) behind its last load.
+      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 16 at a time. The accumulator is released (OFree) behind its last load.
       float ltot = 0.f;
       if (blocks > 0) {
         xl[half * 128 + il] = lsum;
@@ -475,7 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++done;
       }
+      CrossUnit u;
+      cross_unit<2>(p, again(idx), u);
+      const CrossRows rt = cross_rows(p, u, u.first + x);
       const int i = rt.q0 + row_q, h = rt.h0 + row_h;
+      const long long rows = (long long)p.B * p.Nq * p.Hq;
       const bool in = row_in && i < p.Nq, has = blocks > 0 && i < u.nq && ltot != 0.f;  // (a NaN sum counts as there)
       const float inv = 1.f / ltot, lse2 = has ? mref + lg2(ltot) : -INFINITY;
       const long long at = ((long long)u.b * p.Hq + h) * p.Nq + i;
@@ -486,27 +492,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           p.lse_out[at] = has ? lse2 * 0.6931471805599453f : -INFINITY;
       }
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t r[16];  // (set on every path: left undefined on one, values of the blocks' loop spilled)
 #pragma unroll
-      for (int cc = 0; cc < D / 64; ++cc) {
-        uint32_t r[32];
+        for (int e = 0; e < 16; ++e) r[e] = 0u;
         if (blocks > 0) {
           __syncwarp();
-          tmem_ld32(tO + 32 * cc, r);
-          tmem_ld_wait(r);
-          if (cc == D / 64 - 1) {
+          tmem_ld16(tO + 16 * cc, r);
+          tmem_ld_wait16(r);
+          if (cc == D / 32 - 1) {
             tc_fence_before();
             warp_arrive(bar(C::bOFree + x));
           }
         }
-        if (!has) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0u;
-        }
-        const int col = (D / 2) * half + 32 * cc;
+        const int col = (D / 2) * half + 16 * cc;
         if (in && parts) {
-          if (has) store32_f(p.part + (u.split * rows + ((long long)u.b * p.Nq + i) * p.Hq + h) * D + col, r, inv);
+          if (has) store16_f(p.part + (u.split * rows + ((long long)u.b * p.Nq + i) * p.Hq + h) * D + col, r, inv);
         } else if (in) {
-          store32_h<kBf16>(static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + col, r,
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = has ? r[e] : 0u;
+          store16_h<kBf16>(static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + col, r,
                            has ? inv : 0.f);
         }
       }

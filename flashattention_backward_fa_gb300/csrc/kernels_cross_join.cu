@@ -22,12 +22,11 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x) { return static_cast<float>(x); }
+// -L * log2(e) of a real row (a row without keys: -inf).
+__device__ __forceinline__ float neg_lse2(float l) { return l == -INFINITY ? l : -(l * 1.4426950408889634f); }
 
-// One warp a query row (b, h, i), i fastest over the padded rows.
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __grid_constant__ CrossParams p) {
+// fp32, any d: one warp a query row (b, h, i), i fastest over the padded rows.
+__global__ void __launch_bounds__(kJoinThreads) cross_preprocess_f32_kernel(const __grid_constant__ CrossParams p) {
   let_next_begin();
   wait_for_previous();
   const int lane = threadIdx.x & 31;
@@ -37,16 +36,59 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __
     const int i = (int)(row - bh * p.nq_pad), b = (int)(bh / p.Hq), h = (int)(bh - (long long)b * p.Hq);
     float acc = 0.f, nl = -INFINITY;
     if (i < cross_q_len(p, b)) {
-      const T* o = static_cast<const T*>(p.o) + b * p.o_st.b + i * p.o_st.n + h * p.o_st.h;
-      const T* g = static_cast<const T*>(p.dout) + b * p.do_st.b + i * p.do_st.n + h * p.do_st.h;
-      for (int e = lane; e < p.d; e += 32) acc = fmaf(to_f32(o[e]), to_f32(g[e]), acc);
+      const float* o = static_cast<const float*>(p.o) + b * p.o_st.b + i * p.o_st.n + h * p.o_st.h;
+      const float* g = static_cast<const float*>(p.dout) + b * p.do_st.b + i * p.do_st.n + h * p.do_st.h;
+      for (int e = lane; e < p.d; e += 32) acc = fmaf(o[e], g[e], acc);
       acc = row_sum<32>(acc);
-      const float l = p.lse[bh * p.Nq + i];
-      nl = l == -INFINITY ? l : -(l * 1.4426950408889634f);  // (-inf: a row without keys)
+      nl = neg_lse2(p.lse[bh * p.Nq + i]);
     }
     if (lane == 0) {
       p.nD[row] = -acc;
       p.nL2[row] = nl;
+    }
+  }
+}
+
+// 16-bit types: D / 8 lanes a row, 16 bytes of O and of dO each, kRowsEach rows of one (b, h) a
+// thread with all their loads under way at once. (A warp a row with 2 bytes a lane took 34 us at
+// 4x16x2048x128, where the copy rate allows 10.)
+template <int D>
+constexpr int preprocess_rows() { return kJoinThreads / (D / 8) * 4; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __grid_constant__ CrossParams p) {
+  constexpr int kLanes = D / 8, kRowsEach = 4, kApart = kJoinThreads / kLanes;
+  let_next_begin();
+  wait_for_previous();
+  const int blocks = (p.nq_pad + preprocess_rows<D>() - 1) / preprocess_rows<D>(), bh = blockIdx.x / blocks;
+  const int b = bh / p.Hq, h = bh - b * p.Hq, nq = cross_q_len(p, b);
+  const int first = (blockIdx.x - bh * blocks) * preprocess_rows<D>() + threadIdx.x / kLanes, e = 8 * (threadIdx.x % kLanes);
+  const T* o = static_cast<const T*>(p.o) + b * p.o_st.b + h * p.o_st.h + e;
+  const T* g = static_cast<const T*>(p.dout) + b * p.do_st.b + h * p.do_st.h + e;
+  Raw8<T> ro[kRowsEach], rg[kRowsEach];
+#pragma unroll
+  for (int r = 0; r < kRowsEach; ++r) {
+    const int i = first + r * kApart;
+    zero8(ro[r]);
+    zero8(rg[r]);
+    if (i < nq) {
+      load8(ro[r], o + i * p.o_st.n);
+      load8(rg[r], g + i * p.do_st.n);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRowsEach; ++r) {
+    const int i = first + r * kApart;
+    uint64_t x[4], y[4], s0 = 0ull;
+    ro[r].unpack(x);
+    rg[r].unpack(y);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s0 = f2_fma(x[c], y[c], s0);
+    const float acc = row_sum<kLanes>(f2_sum(s0));
+    if (e == 0 && i < p.nq_pad) {
+      const long long row = (long long)bh * p.nq_pad + i;
+      p.nD[row] = -acc;
+      p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
     }
   }
 }
@@ -176,11 +218,19 @@ int join_blocks(const CrossParams& p, int N, int H) {
 }  // namespace
 
 cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st) {
-  const long long rows = (long long)p.B * p.Hq * p.nq_pad, blocks = (rows + 7) / 8;
-  const dim3 grid((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32));
-  if (dtype == FA_F32) return launch_chained(cross_preprocess_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
-  return dtype == FA_BF16 ? launch_chained(cross_preprocess_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
-                          : launch_chained(cross_preprocess_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+  const long long heads = (long long)p.B * p.Hq;
+  if (dtype == FA_F32) {
+    const long long blocks = (heads * p.nq_pad + 7) / 8;
+    return launch_chained(cross_preprocess_f32_kernel, dim3((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32)),
+                          kJoinThreads, 0, 1, p, st);
+  }
+  const int rows = p.d == 64 ? preprocess_rows<64>() : preprocess_rows<128>();
+  const dim3 grid((unsigned)(heads * ((p.nq_pad + rows - 1) / rows)));
+  if (p.d == 64)
+    return dtype == FA_BF16 ? launch_chained(cross_preprocess_kernel<__nv_bfloat16, 64>, grid, kJoinThreads, 0, 1, p, st)
+                            : launch_chained(cross_preprocess_kernel<__half, 64>, grid, kJoinThreads, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(cross_preprocess_kernel<__nv_bfloat16, 128>, grid, kJoinThreads, 0, 1, p, st)
+                          : launch_chained(cross_preprocess_kernel<__half, 128>, grid, kJoinThreads, 0, 1, p, st);
 }
 
 cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t st) {
