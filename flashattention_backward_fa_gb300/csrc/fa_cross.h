@@ -127,31 +127,99 @@ __device__ __forceinline__ void cross_unit(const CrossParams& p, int idx, CrossU
   u.blocks = any ? max(u.j_end - u.j_begin + 127, 0) >> 7 : 0;
 }
 
-// The same number, opaque to the compiler: what is computed from it is computed anew instead of being kept
-// in registers since the first time (the row-math loops have none to spare, and their spills miss L1).
-__device__ __forceinline__ int again(int x) {
-  asm volatile("" : "+r"(x));
-  return x;
+// A value that every lane of a converged warp holds alike, as one that the compiler knows to be uniform.
+// The MMA-issuing warps' loops run over units that are decoded from lengths in memory; with trip counts
+// and stages that were not known to be uniform an MMA took about 100 cycles to issue instead of 25.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// What a row-math warp needs of its unit at the end only, kept in shared memory meanwhile (the loops have no
+// registers to spare, and decoding the unit again waits for the lengths in memory).
+struct CrossNote {
+  int a[8];
+};
+__device__ __forceinline__ void keep_note(volatile CrossNote* note, int a, int b, int c, int d, int e) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    note->a[0] = a;
+    note->a[1] = b;
+    note->a[2] = c;
+    note->a[3] = d;
+    note->a[4] = e;
+  }
+  __syncwarp();
 }
 
-// 16 fp32 values of the accumulators, times mul as 16-bit values, or as they are, to consecutive places.
-template <bool kBf16>
-__device__ __forceinline__ void store16_h(uint16_t* to, const uint32_t* r, float mul) {
+// Four 16-byte pieces of a lane's row, u[0 .. 3], to the quad's four lanes: lane q of a quad gets piece q of
+// row r (of the quad's four rows) in u[r]. The stores behind it then cover 64 consecutive bytes of a row with
+// four lanes instead of 16 with one (a warp's store instruction touches 8 lines instead of 32; the epilogue
+// of a 128-row tile was bound by that, 3300 cycles).
+__device__ __forceinline__ void quad_transpose(uint4 (&u)[4]) {
+  const int q = threadIdx.x & 3;
+  const auto swap = [](uint4& a, uint4& b, bool hi, int o) {  // hi lanes give a and get b's place, the others the reverse
+    uint4 give = hi ? a : b;
+    give.x = __shfl_xor_sync(0xffffffffu, give.x, o);
+    give.y = __shfl_xor_sync(0xffffffffu, give.y, o);
+    give.z = __shfl_xor_sync(0xffffffffu, give.z, o);
+    give.w = __shfl_xor_sync(0xffffffffu, give.w, o);
+    if (hi)
+      a = give;
+    else
+      b = give;
+  };
+  swap(u[0], u[1], q & 1, 1);
+  swap(u[2], u[3], q & 1, 1);
+  swap(u[0], u[2], q & 2, 2);
+  swap(u[1], u[3], q & 2, 2);
+}
+
+// Stores of a converged warp's 32 rows, 64 bytes of each: u holds the lane's own row's, `to` the place of
+// the lane's own row, or null where the row is not stored.
+__device__ __forceinline__ void store_rows64(uint4 (&u)[4], char* to) {
+  quad_transpose(u);
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int r = 0; r < 4; ++r) {
+    char* at = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), (lane & ~3) + r));
+    if (at != nullptr) reinterpret_cast<uint4*>(at)[lane & 3] = u[r];
+  }
+}
+
+// 32 fp32 values of a row as 16-bit ones times mul, 16 as they are (times mul).
+template <bool kBf16>
+__device__ __forceinline__ void pack64(uint4 (&u)[4], const uint32_t (&r)[32], float mul) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = pack2<kBf16>(__uint_as_float(r[8 * t + 2 * e]) * mul, __uint_as_float(r[8 * t + 2 * e + 1]) * mul);
-    reinterpret_cast<uint4*>(to)[t] = make_uint4(w[0], w[1], w[2], w[3]);
+    u[t] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-__device__ __forceinline__ void store16_f(float* to, const uint32_t* r, float mul = 1.f) {
+__device__ __forceinline__ void pack64(uint4 (&u)[4], const uint32_t* r, float mul) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    reinterpret_cast<float4*>(to)[t] =
-        make_float4(__uint_as_float(r[4 * t]) * mul, __uint_as_float(r[4 * t + 1]) * mul,
-                    __uint_as_float(r[4 * t + 2]) * mul, __uint_as_float(r[4 * t + 3]) * mul);
+  for (int t = 0; t < 4; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(__uint_as_float(r[4 * t + e]) * mul);
+    u[t] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// 32 columns of a converged warp's 32 accumulator rows to memory: as 16-bit values at `out`, or as fp32 at
+// `part`, times mul; both null where the row is not stored.
+template <bool kBf16>
+__device__ __forceinline__ void store_columns32(const uint32_t (&r)[32], float mul, bool parts, float* part, uint16_t* out) {
+  uint4 u[4];
+  if (parts) {
+    pack64(u, r, mul);
+    store_rows64(u, reinterpret_cast<char*>(part));
+    pack64(u, r + 16, mul);
+    store_rows64(u, reinterpret_cast<char*>(part != nullptr ? part + 16 : nullptr));
+  } else {
+    pack64<kBf16>(u, r, mul);
+    store_rows64(u, reinterpret_cast<char*>(out));
+  }
 }
 
 // Zeros to rows [from, to) of a tile of 128-byte rows in kPanels panels in shared memory, by one

@@ -64,7 +64,8 @@ struct KCfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = oAbort + 8;    // [buffer][8 warps] split votes
-  static constexpr uint32_t kSmem = oFlags + 64 + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t oNotes = oFlags + 64;   // [16 row-math warps]
+  static constexpr uint32_t kSmem = oNotes + 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
@@ -240,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     KUnit u;
     for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      idx = uniform(idx);
+      u.steps = uniform(u.steps);
       ok = warp_wait<kIssuerPoll>(bar(C::bKV), kl & 1, abort_flag, p.status);
       for (int it = 0; ok && it < u.steps; ++it, ++G) {
         const int s = G % C::kNS, bb = G & 1;
@@ -272,6 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     KUnit u;
     for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      idx = uniform(idx);
+      u.steps = uniform(u.steps);
       for (int it = 0; it < u.steps; ++it, ++G) {
         const int bt = G & 1, st = G % C::kNS;
         if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
@@ -280,21 +285,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        int h0, q0;
-        k_step(p, u, it, h0, q0);
         // Rows of queries past the sequence's end, as far as they are the tensors' (past them: zeros by
         // TMA). S^T is formed; dP^T may still read dO: its columns of these rows are not used.
-        const int q = p.plan.step.queries(), from = u.nq - q0, to = min(q, p.Nq - q0);
-        if (from < to) {
-          for (int h = 0; h < p.plan.step.heads(); ++h) {
+        if (u.nq < p.Nq) {
+          int h0, q0;
+          k_step(p, u, it, h0, q0);
+          const int q = p.plan.step.queries(), from = u.nq - q0, to = min(q, p.Nq - q0);
+          for (int h = 0; from < to && h < p.plan.step.heads(); ++h) {
             zero_rows<C::kPanels>(sb + C::oQ + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
             zero_rows<C::kPanels>(sb + C::oDO + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
           }
         }
         tc_fence_after();
-        bool split = false;
+        int any = 0;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) split |= flags[8 * bt + x] != 0;
+        for (int x = 0; x < 8; ++x) any |= flags[8 * bt + x];
+        const bool split = uniform(any) != 0;
         const uint32_t first = it > 0 ? 1u : 0u;
         const uint64_t qd = desc_add(mQ0, st * C::kQTile), gd = desc_add(mO0, st * C::kQTile);
         // dV += P^T dO: K step kk reads the 8 rounded columns at 16kk of the P^T image and, on split
@@ -342,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tSc = tS + lane_off + 64 * bb + 32 * c, tdPc = tdP + lane_off + 64 * bb + 32 * c;
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 4);
     int kl = 0, G = 0;
     bool ok = true;
     for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
@@ -358,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         full = step_columns(p.plan.step, c, kStep);
         tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
         if (u.j0 + jl >= u.nk) full = tail = 0u;
+        keep_note(note, u.b, u.hk, u.j0, u.nk, u.split);
       }
       for (int it = (bb ^ G) & 1; it < steps; it += 2) {
         const int gs = G + it, s = gs % C::kNS;
@@ -478,10 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // columns; both accumulators are released (AccFree) behind the last load.
       const bool epi = steps > 0 ? bb == ((G + steps - 1) & 1) : bb == 0;
       if (epi) {
-        KUnit u;
-        k_unit(p, again(idx), u);
-        const int j = u.j0 + jl;
-        const long long size = (long long)p.B * p.Nk * p.Hk * D;
         if (steps > 0) {
           if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
             ok = false;
@@ -489,35 +493,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
         }
+        const int b = note->a[0], hk = note->a[1], j = note->a[2] + jl, nk = note->a[3];
+        const long long size = (long long)p.B * p.Nk * p.Hk * D;
+        const bool parts = p.plan.q_splits > 1;
 #pragma unroll 1
-        for (int part = 0; part < D / 16; ++part) {  // 16 columns of dV, then of dK
-          const bool isK = part >= D / 32;
-          const int col = c * (D / 2) + 16 * (part & (D / 32 - 1));
-          uint32_t r[16];  // (set on every path: left undefined on one, 25 values of the steps' loop spilled)
+        for (int cc = 0; cc < D / 32; ++cc) {  // 32 columns of dV, then of dK
+          const bool isK = cc >= D / 64;
+          const int col = c * (D / 2) + 32 * (cc & (D / 64 - 1));
+          uint32_t r[32];  // (set on every path: left undefined on one, 25 values of the steps' loop spilled)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) r[x] = 0u;
+          for (int x = 0; x < 32; ++x) r[x] = 0u;
+          __syncwarp();
           if (steps > 0) {
-            __syncwarp();  // the stores are per lane: converge for the TMEM load
-            tmem_ld16((isK ? tdK : tdV) + lane_off + col, r);
-            tmem_ld_wait16(r);
-            if (part == D / 16 - 1) {
+            tmem_ld32((isK ? tdK : tdV) + lane_off + col, r);
+            tmem_ld_wait(r);
+            if (cc == D / 32 - 1) {
               tc_fence_before();
               warp_arrive(bar(C::bAccFree));
             }
           }
-          if (p.plan.q_splits > 1) {
-            if (j < u.nk) {
-              float* to = p.part_kv + 2 * u.split * size + (isK ? 0 : size) +
-                          (((long long)u.b * p.Nk + j) * p.Hk + u.hk) * D + col;
-              store16_f(to, r);
-            }
-          } else if (j < p.Nk) {
-            const fa_strides& st = isK ? p.dk_st : p.dv_st;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) r[x] = j < u.nk ? r[x] : 0u;  // (0 * NaN of a real query's)
-            store16_h<kBf16>(static_cast<uint16_t*>(isK ? p.dk : p.dv) + u.b * st.b + j * st.n + u.hk * st.h + col, r,
-                             isK ? p.scale : 1.f);
-          }
+          for (int x = 0; x < 32; ++x) r[x] = j < nk ? r[x] : 0u;  // (0 * NaN of a real query's)
+          float* to_part = parts && j < nk ? p.part_kv + 2 * note->a[4] * size + (isK ? 0 : size) +
+                                                 (((long long)b * p.Nk + j) * p.Hk + hk) * D + col
+                                           : nullptr;
+          const fa_strides& st = isK ? p.dk_st : p.dv_st;
+          uint16_t* to_out = !parts && j < p.Nk ? static_cast<uint16_t*>(isK ? p.dk : p.dv) + b * st.b + j * st.n + hk * st.h +
+                                                      col
+                                                : nullptr;
+          store_columns32<kBf16>(r, isK && !parts ? p.scale : 1.f, parts, to_part, to_out);
         }
         __syncwarp();
       }
@@ -565,7 +569,8 @@ struct QCfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [buffer][16 warps] split votes
-  static constexpr uint32_t kSmem = oFlags + 2 * 16 * 4 + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t oNotes = oFlags + 2 * 16 * 4;        // [16 row-math warps]
+  static constexpr uint32_t kSmem = oNotes + 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
@@ -684,6 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     CrossUnit u;
     for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      idx = uniform(idx);
+      u.blocks = uniform(u.blocks);
       ok = warp_wait<kIssuerPoll>(bar(C::bRes), kl & 1, abort_flag, p.status);
       for (int it = 0; ok && it < u.blocks; ++it, ++G) {
         const int bb = G & 1, st = isS ? G % C::kNK : G % C::kNV;
@@ -720,6 +727,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     CrossUnit u;
     for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
+      idx = uniform(idx);
+      u.blocks = uniform(u.blocks);
+      u.j_begin = uniform(u.j_begin);
+      u.j_end = uniform(u.j_end);
       for (int it = 0; it < u.blocks; ++it, ++G) {
         const int bt = G & 1, sk = G % C::kNK;
         if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
@@ -739,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           tc_mma_ts_w(tAcc, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO, kk > 0 || it > 0 ? 1u : 0u);
-        if (any) {
+        if (uniform(any)) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             tc_mma_ts_w(tAcc, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
@@ -764,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
     const bool row_in = row_h < p.plan.q_tile.heads();
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 4);
     int kl = 0, G = 0;
     bool ok = true;
     for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
@@ -775,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CrossRows rt = cross_rows(p, u, u.first);
         blocks = u.blocks;
         left += u.j_end - u.j_begin;
+        keep_note(note, rt.q0, rt.h0, u.b, u.nq, u.split);
         if (blocks > 0 && row_in) {  // (rows past the sequence hold -inf and 0)
           const long long at = ((long long)u.b * p.Hq + rt.h0 + row_h) * p.nq_pad + rt.q0 + row_q;
           nL2 = p.nL2[at];
@@ -857,12 +870,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
       // (AccFree) before the stores, so the next unit's first MMA can start meanwhile.
-      constexpr int kChunks = D / 64;  // 16-column TMEM loads per thread
-      uint32_t r[kChunks][16];
+      uint32_t r[32];  // (D / 4 of them)
 #pragma unroll
-      for (int cc = 0; cc < kChunks; ++cc)
-#pragma unroll
-        for (int x = 0; x < 16; ++x) r[cc][x] = 0u;
+      for (int x = 0; x < 32; ++x) r[x] = 0u;
       if (blocks > 0) {
         if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
           ok = false;
@@ -870,37 +880,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t col0 = tAcc + lane_off + c * (D / 4);
-        tmem_ld16(col0, r[0]);
-        if constexpr (kChunks == 2) {
-          tmem_ld16(col0 + 16, r[1]);
-          tmem_ld_wait16x2(r[0], r[1]);
+        if constexpr (D == 128) {
+          tmem_ld32(col0, r);
+          tmem_ld_wait(r);
         } else {
-          tmem_ld_wait16(r[0]);
+          uint32_t half[16];
+          tmem_ld16(col0, half);
+          tmem_ld_wait16(half);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) r[x] = half[x];
         }
         tc_fence_before();
         warp_arrive(bar(C::bAccFree));
         ++kl;
       }
-      CrossUnit u;
-      cross_unit<1>(p, again(idx), u);
-      const CrossRows rt = cross_rows(p, u, u.first);
-      const int i = rt.q0 + row_q, h = rt.h0 + row_h;
-      if (row_in && i < p.Nq) {
-        if (p.plan.k_splits > 1) {
-          if (i < u.nq) {
-            float* to = p.part + ((((long long)u.split * p.B + u.b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4);
+      const int i = note->a[0] + row_q, h = note->a[1] + row_h, b = note->a[2], nq = note->a[3];
+      const bool parts = p.plan.k_splits > 1, in = row_in && i < (parts ? nq : p.Nq);
 #pragma unroll
-            for (int cc = 0; cc < kChunks; ++cc) store16_f(to + 16 * cc, r[cc]);
-          }
-        } else {
-          uint16_t* to = static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4);
-          const bool real = i < u.nq;  // (what stands in other rows of the accumulator may be NaN)
+      for (int x = 0; x < 32; ++x) r[x] = i < nq ? r[x] : 0u;  // (rows that are not there may hold NaN)
+      float* to_part = parts && in ? p.part + ((((long long)note->a[4] * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
+                                   : nullptr;
+      uint16_t* to_out = !parts && in ? static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h +
+                                            c * (D / 4)
+                                      : nullptr;
+      const float mul = parts ? 1.f : p.scale;
+      if constexpr (D == 128) {
+        store_columns32<kBf16>(r, mul, parts, to_part, to_out);
+      } else if (parts) {
+        uint4 v[4];
+        pack64(v, r, mul);
+        store_rows64(v, reinterpret_cast<char*>(to_part));
+      } else if (to_out != nullptr) {  // 32 bytes a row
 #pragma unroll
-          for (int cc = 0; cc < kChunks; ++cc) {
+        for (int t = 0; t < 2; ++t) {
+          uint32_t w[4];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) r[cc][x] = real ? r[cc][x] : 0u;
-            store16_h<kBf16>(to + 16 * cc, r[cc], p.scale);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack2<kBf16>(__uint_as_float(r[8 * t + 2 * e]) * mul, __uint_as_float(r[8 * t + 2 * e + 1]) * mul);
+          reinterpret_cast<uint4*>(to_out)[t] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       __syncwarp();

@@ -70,8 +70,9 @@ struct Cfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [tile][8 warps] split votes
+  static constexpr uint32_t oNotes = oFlags + 2 * 8 * 4;        // [16 softmax warps]
   // row maxima [tile][block parity][half][128 rows], then the sums [tile][half][128 rows]
-  static constexpr uint32_t oXchg = oFlags + 2 * 8 * 4;
+  static constexpr uint32_t oXchg = oNotes + 16 * sizeof(CrossNote);
   static constexpr uint32_t kSmem = oXchg + (2 * 2 * 2 + 2 * 2) * 128 * 4 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tO = tmem + 256 + D * x, tP = tmem + 128 * x;
       const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 8 * x);
       const int4 fa = f4[0], fb = f4[1];
-      const bool split = (fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w) != 0;
+      const bool split = uniform(fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w) != 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) tc_mma_ts_w(tO, tP + 16 * k, desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
       if (split) {
@@ -224,11 +225,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     CrossUnit u, next;
     bool live[2] = {false, false}, live_next[2];  // the unit's tiles, and the next unit's
     int idx = next_work(blockIdx.x, u), t = 0;
+    const auto known = [&](int& i, CrossUnit& w) {
+      i = uniform(i);
+      w.blocks = uniform(w.blocks);
+      w.j_begin = uniform(w.j_begin);
+      w.j_end = uniform(w.j_end);
+    };
+    known(idx, u);
     if (idx >= 0) {
       ok = warp_wait<kIssuerPoll>(bar(C::bKFull), 0, abort_flag, p.status);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        live[x] = cross_rows(p, u, u.first + x).live;
+        live[x] = uniform(cross_rows(p, u, u.first + x).live);
         if (!ok || !live[x]) continue;
         ok = warp_wait<kIssuerPoll>(bar(C::bQ + x), 0, abort_flag, p.status);
         if (!ok) continue;
@@ -238,9 +246,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) tc_commit_w(bar(C::bKEmpty));
     }
     while (ok && idx >= 0) {
-      const int after = next_work(idx + gridDim.x, next);
+      int after = next_work(idx + gridDim.x, next);
+      known(after, next);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) live_next[x] = after >= 0 && cross_rows(p, next, next.first + x).live;
+      for (int x = 0; x < 2; ++x) live_next[x] = uniform(after >= 0 && cross_rows(p, next, next.first + x).live);
       for (int j = 0; ok && j < u.blocks; ++j, ++t) {
         const int sv = t % C::kNV;
         const bool inside = j + 1 < u.blocks, more = inside || after >= 0;
@@ -306,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c2 = p.scale_log2;
     const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
     const bool row_in = row_h < p.plan.q_tile.heads();
+    volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 2);
     int n = 0, done = 0;  // blocks and units this tile has been through
     bool ok = true;
     // Waits block (the hardware suspends the warp): each tile's warps idle about half the
@@ -319,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!rt.there) continue;
         blocks = rt.live ? u.blocks : 0;
         left += u.j_end - u.j_begin;
+        keep_note(note, rt.q0, rt.h0, u.b, u.nq, u.split);
       }
       float mref = -INFINITY, lsum = 0.f;  // lsum: this half's part of the row sum
       for (int j = 0; j < blocks; ++j, ++n) {
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bPFull + x));
       }
       if (!ok) break;
-      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 16 at a time. The accumulator is released (OFree) behind its last load.
+      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time. The accumulator is released (OFree) behind its last load.
       float ltot = 0.f;
       if (blocks > 0) {
         xl[half * 128 + il] = lsum;
@@ -477,46 +488,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++done;
       }
-      CrossUnit u;
-      cross_unit<2>(p, again(idx), u);
-      const CrossRows rt = cross_rows(p, u, u.first + x);
-      const int i = rt.q0 + row_q, h = rt.h0 + row_h;
-      const long long rows = (long long)p.B * p.Nq * p.Hq;
-      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < u.nq && ltot != 0.f;  // (a NaN sum counts as there)
-      const float inv = 1.f / ltot, lse2 = has ? mref + lg2(ltot) : -INFINITY;
-      const long long at = ((long long)u.b * p.Hq + h) * p.Nq + i;
+      const int i = note->a[0] + row_q, h = note->a[1] + row_h, b = note->a[2], part = note->a[4];
+      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < note->a[3] && ltot != 0.f;  // (a NaN sum is there)
+      const float inv = has ? 1.f / ltot : 0.f, lse2 = has ? mref + lg2(ltot) : -INFINITY;
+      const long long at = ((long long)b * p.Hq + h) * p.Nq + i, rows = (long long)p.B * p.Nq * p.Hq;
       const bool parts = p.plan.k_splits > 1;
       if (in && half == 0) {
         if (parts)
-          p.part_lse[u.split * rows + at] = lse2;
+          p.part_lse[part * rows + at] = lse2;
         else
           p.lse_out[at] = has ? lse2 * 0.6931471805599453f : -INFINITY;
       }
+      // (rows without keys of the split: the join does not read their part)
+      float* to_part = parts && in && has ? p.part + (part * rows + ((long long)b * p.Nq + i) * p.Hq + h) * D + (D / 2) * half
+                                          : nullptr;
+      uint16_t* to_out = !parts && in ? static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h +
+                                            (D / 2) * half
+                                      : nullptr;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t r[16];  // (set on every path: left undefined on one, values of the blocks' loop spilled)
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t r[32];  // (set on every path: left undefined on one, values of the blocks' loop spilled)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = 0u;
+        for (int e = 0; e < 32; ++e) r[e] = 0u;
+        __syncwarp();
         if (blocks > 0) {
-          __syncwarp();
-          tmem_ld16(tO + 16 * cc, r);
-          tmem_ld_wait16(r);
-          if (cc == D / 32 - 1) {
+          tmem_ld32(tO + 32 * cc, r);
+          tmem_ld_wait(r);
+          if (cc == D / 64 - 1) {
             tc_fence_before();
             warp_arrive(bar(C::bOFree + x));
           }
         }
-        const int col = (D / 2) * half + 16 * cc;
-        if (in && parts) {
-          if (has) store16_f(p.part + (u.split * rows + ((long long)u.b * p.Nq + i) * p.Hq + h) * D + col, r, inv);
-        } else if (in) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = has ? r[e] : 0u;
-          store16_h<kBf16>(static_cast<uint16_t*>(p.out) + u.b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + col, r,
-                           has ? inv : 0.f);
-        }
+        for (int e = 0; e < 32; ++e) r[e] = has ? r[e] : 0u;
+        store_columns32<kBf16>(r, inv, parts, to_part ? to_part + 32 * cc : nullptr, to_out ? to_out + 32 * cc : nullptr);
       }
-      __syncwarp();  // (the stores are per lane: converge for the next unit's collective accesses)
+      __syncwarp();
     }
   }
 
