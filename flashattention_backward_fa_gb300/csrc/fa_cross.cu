@@ -67,6 +67,7 @@ void fill(CrossParams& p, const fa_cross_shape* s, const CrossPlan& plan, float 
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.plan = plan;
+  p.few_cluster = plan.few_cluster;
 }
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }
@@ -88,12 +89,40 @@ int best_splits(long long units, int steps, int places, int start, int join) {
   return (int)div_up(steps, div_up(steps, best));
 }
 
+// Whether the forward's kernel of few rows takes a call: always up to 16 rows a key head, and up to 64 where
+// the row tiles, which read the keys once each, are few and so are the keys. Measured against the kernel of
+// 128-row tiles, us: 16 rows, 8 sequences of 16 heads d = 128 over 8192 keys 92 / 127; 64 rows, 1 x 16 d = 64
+// over 500 keys 11.0 / 14.3, over 8192 keys 24 / 25, d = 128 over 16383 keys 70 / 45; 32 rows (256 row tiles),
+// 8 x 16 over 8192 keys 129 / 128.
+bool few_rows(long long groups, long long rows, int Nk) {
+  return groups <= 65535 && (rows <= 16 || (rows <= 64 && groups * div_up(rows, 16) <= 64 && Nk <= 4096));
+}
+
+// Its shares of the keys: clusters of two to eight blocks while there are no more blocks than the GPU holds
+// twice over and each has 128 keys (32 sequences x 8 heads of up to 4096 keys: 62 us; four times over 64, eight
+// times 79); shares through the workspace where clusters of eight leave the GPU empty and their blocks would
+// have over 2048 keys (16 heads, d = 64, 8192 keys: cluster 11.5 us, workspace 16.9).
+void few_plan(long long units, int Nk, CrossPlan* c) {
+  c->k_splits = c->few_cluster = 1;
+  while (c->few_cluster < 8 && units * c->few_cluster * 2 <= 608 && c->few_cluster * 2 * 128 <= Nk + 127) c->few_cluster *= 2;
+  if (units * 8 <= 152 && Nk > 8 * 2048) {
+    c->few_cluster = 0;
+    c->k_splits = (int)std::min<long long>(304 / units, Nk / 256);
+  }
+}
+
 CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype, bool backward) {
   CrossPlan c;
   const int G = s->Hq / s->Hk;
   c.q_tile = fa::cross_tile(s->Nq, G, 7, 0);
   c.step = fa::cross_tile(s->Nq, G, 6, 2);
   c.q_splits = 1;
+  c.few_cluster = 0;
+  c.few = !backward && dtype != FA_F32 && few_rows((long long)s->B * s->Hk, (long long)s->Nq * G, s->Nk);
+  if (c.few) {
+    few_plan((long long)s->B * s->Hk * div_up((long long)s->Nq * G, 16), s->Nk, &c);
+    return c;
+  }
   if (dtype == FA_F32) {
     const long long q_units = (long long)s->B * s->Hq * div_up(s->Nq, 32), k_units = (long long)s->B * s->Hk * div_up(s->Nk, 32);
     c.k_splits = best_splits(q_units, (int)div_up(s->Nk, 64), 304, 1, 3);
@@ -188,6 +217,8 @@ int fa_cross_fwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   cudaError_t e;
   if (dtype == FA_F32) {
     e = fa::launch_cross_fwd_f32(p, st);
+  } else if (plan.few) {
+    e = fa::launch_cross_few(p, dtype == FA_BF16, st);
   } else {
     CUtensorMap maps[3];
     if ((rc = fa::bind_device_context())) return rc;

@@ -32,11 +32,20 @@ inline CrossTile cross_tile(int Nq, int G, int most, int least) {
   return t;
 }
 
+// P and dS enter the backward's products in 16 bits, with their rounding residual beside them where the tile
+// holds a probability above this. Roundings of many small weights average out; those of one that makes up
+// the row do not. Error of bf16 gradients against 64 bits (2-norm, of themselves): 1.7e-3 with the residual
+// everywhere, 2.4e-3 without. At 1/64, as in fa_bwd, nearly every tile of a few hundred keys had one above it
+// and took half as many products again (dK/dV 4x16 2048x512 84 -> 77 us, 1x32/8 8192x4096 985 -> 822 us).
+constexpr float kCrossSplit = 0.25f;
+
 struct CrossPlan {
   int k_splits;  // each takes an even share of a sequence's key blocks
   int q_splits;  // of its query steps (steps run over the group's heads and its queries)
   CrossTile q_tile;  // of the forward and dQ (128 rows)
   CrossTile step;    // of the dK/dV kernel's query steps (64 rows)
+  bool few;          // the forward's kernel of few rows
+  int few_cluster;
 };
 
 struct CrossParams {
@@ -68,6 +77,7 @@ struct CrossParams {
   float* part_lse;
   float* part_kv;
   CrossPlan plan;
+  int few_cluster;  // few rows: blocks of a cluster that share a sequence's keys (0: k_splits through the workspace)
   unsigned int* status;
 };
 
@@ -246,6 +256,9 @@ cudaError_t launch_cross_fwd_tc(const CrossParams& p, bool bf16, const CUtensorM
 cudaError_t launch_cross_dkdv_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
 // maps: Q (boxes of the tile's rows), K, V (boxes of 128 rows), dO (as Q).
 cudaError_t launch_cross_dq_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
+
+// Forward of few rows a key head (16-bit types).
+cudaError_t launch_cross_few(const CrossParams& p, bool bf16, cudaStream_t st);
 
 cudaError_t launch_cross_fwd_f32(const CrossParams& p, cudaStream_t st);
 cudaError_t launch_cross_dq_f32(const CrossParams& p, cudaStream_t st);

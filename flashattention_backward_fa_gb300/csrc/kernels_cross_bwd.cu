@@ -9,7 +9,7 @@
 // of several where queries are few; the steps run over all heads of the group, so shared
 // key heads cost no extra sums), S^T and dP^T in double buffers, P^T and dS^T written back
 // over them in 16 bits with their rounding residual where the tile holds probabilities
-// above 1/64, dV and dK in TMEM. dQ: 128 query rows on the lanes, steps of 128 keys.
+// above kCrossSplit, dV and dK in TMEM. dQ: 128 query rows on the lanes, steps of 128 keys.
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t hp[8], ep[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
-          split_h[hh] = __any_sync(0xFFFFFFFFu, cmax > kSplitThreshold);
+          split_h[hh] = __any_sync(0xFFFFFFFFu, cmax > kCrossSplit);
           if (split_h[hh]) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t hv[8], ev[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hv[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
-          const bool split = __any_sync(0xFFFFFFFFu, row_in && cmax > kSplitThreshold);
+          const bool split = __any_sync(0xFFFFFFFFu, row_in && cmax > kCrossSplit);
           lo_any |= split;
           if (split) {
 #pragma unroll

@@ -13,10 +13,14 @@
 // tensor cores run tile B. Eight softmax warps a tile: a row is split between two
 // warps (the same TMEM lane), 64 keys of a block each, that exchange only their
 // halves' maxima a block and their sums at the end. P goes back over the S columns it
-// came from as a 16-bit image (eight rounded columns, then eight residual columns per
-// 16 keys; the residual MMAs run where a probability may exceed 1/64 of the row's
-// sum) and the O MMA reads it from TMEM. The row's reference m moves only when a block's
-// maximum exceeds it by more than 2^8.
+// came from, rounded to 16 bits, and the O MMA reads it from TMEM. The row's reference m
+// moves only when a block's maximum exceeds it by more than 2^8.
+//
+// The rounding of P moves an output by at most half a step of each weight, about what the
+// rounding of the output itself does (bf16, 2-norm error against 64 bits: 1.7e-3 with
+// exact weights, 2.2e-3 with rounded ones, of 512 keys). Its residual as a second product,
+// as in fa_fwd, ran for nearly every tile of a few hundred keys, whose largest weights
+// are not small, and took half as many MMAs again.
 //
 // Few keys a unit are the common case here (a text's 77 to 512), so a unit is short: steps,
 // ring stages and barrier phases run on from unit to unit, the next unit's queries and
@@ -64,14 +68,15 @@ struct Cfg {
   static constexpr int bODone = bPFull + 2;            // [2] O MMA of a block done
   static constexpr int bOFree = bODone + 2;            // [2] the epilogue has read O
   static constexpr int bDrain = bOFree + 2;
-  static constexpr int bXchg = bDrain + 1;             // [tile][lane quarter][block parity] row-maximum exchange
-  static constexpr int bSum = bXchg + 16;              // [tile][lane quarter] final row-sum exchange
-  static constexpr int kBars = bSum + 8;
+  static constexpr int bXchg = bDrain + 1;             // [tile][lane quarter] row-maximum exchange
+  static constexpr int bSum = bXchg + 8;              // [tile][lane quarter] final row-sum exchange
+  static constexpr int bFast = bSum + 8;               // [tile][lane quarter] outcome of the one-pass form exchanged
+  static constexpr int kBars = bFast + 8;
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
-  static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [tile][8 warps] split votes
-  static constexpr uint32_t oNotes = oFlags + 2 * 8 * 4;        // [16 softmax warps]
-  // row maxima [tile][block parity][half][128 rows], then the sums [tile][half][128 rows]
+  static constexpr uint32_t oFast = (oAbort + 8 + 15) & ~15u;    // [exchange parity][16 softmax warps] outcomes
+  static constexpr uint32_t oNotes = oFast + 2 * 16 * 4;         // [16 softmax warps]
+  // row maxima [tile][exchange parity][half][128 rows], then the sums [tile][half][128 rows]
   static constexpr uint32_t oXchg = oNotes + 16 * sizeof(CrossNote);
   static constexpr uint32_t kSmem = oXchg + (2 * 2 * 2 + 2 * 2) * 128 * 4 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
@@ -87,7 +92,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
-  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
   const int units = cross_units<2>(p);
   // The first unit from idx on in this CTA's stride that has blocks to compute; -1: none.
@@ -117,8 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::bVEmpty + s), 1);
     }
     mbar_init(bar(C::bDrain), 1);
-    for (int x = 0; x < 16; ++x) mbar_init(bar(C::bXchg + x), 64);  // the two warps of a row quarter
-    for (int x = 0; x < 8; ++x) mbar_init(bar(C::bSum + x), 64);
+    for (int x = 0; x < 8; ++x) {  // the two warps of a row quarter
+      mbar_init(bar(C::bXchg + x), 64);
+      mbar_init(bar(C::bSum + x), 64);
+      mbar_init(bar(C::bFast + x), 64);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -211,15 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue_o = [&](int x, int t, bool first) {
       const uint64_t vd = desc_add(dV0, (t % C::kNV) * C::kTile);
       const uint32_t tO = tmem + 256 + D * x, tP = tmem + 128 * x;
-      const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 8 * x);
-      const int4 fa = f4[0], fb = f4[1];
-      const bool split = uniform(fa.x | fa.y | fa.z | fa.w | fb.x | fb.y | fb.z | fb.w) != 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) tc_mma_ts_w(tO, tP + 16 * k, desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
-      if (split) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) tc_mma_ts_w(tO, tP + 16 * k + 8, desc_add(vd, 2048 * k), idO, 1u);
-      }
+      for (int k = 0; k < 8; ++k)  // (a half's image: the first 32 of its 64 columns)
+        tc_mma_ts_w(tO, tP + 64 * (k >> 2) + 8 * (k & 3), desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
       tc_commit_w(bar(C::bODone + x));
     };
     CrossUnit u, next;
@@ -316,12 +317,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
     const bool row_in = row_h < p.plan.q_tile.heads();
     volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 2);
+    volatile int* fast = reinterpret_cast<volatile int*>(smem + C::oFast);
+    int nx = 0, nf = 0;   // exchanges of maxima and of outcomes so far
     int n = 0, done = 0;  // blocks and units this tile has been through
     bool ok = true;
     // Waits block (the hardware suspends the warp): each tile's warps idle about half the
     // time, and spinning would take issue slots from the other tile's warps.
     for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
       int blocks, left = -64 * half;  // left: this warp's real keys from the block's start on
+      bool real;                      // a real query's row: what else lies in the tile has no vote below
       {
         CrossUnit u;
         cross_unit<2>(p, idx, u);
@@ -329,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!rt.there) continue;
         blocks = rt.live ? u.blocks : 0;
         left += u.j_end - u.j_begin;
+        real = row_in && rt.q0 + row_q < u.nq;
         keep_note(note, rt.q0, rt.h0, u.b, u.nq, u.split);
       }
       float mref = -INFINITY, lsum = 0.f;  // lsum: this half's part of the row sum
@@ -339,6 +344,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const int hi = left - 128 * j;  // columns 0 .. hi - 1
+        // One pass with the reference as it stands, which it nearly always does after a row's first block:
+        // P, its sum and its image are kept in registers until both warps of the rows say that no row's
+        // maximum asks for a new reference. The two passes below (maximum, exchange, P) run otherwise.
+        uint32_t img[32];
+        if (j > 0) {
+          const float base = mref == -INFINITY ? 0.f : mref;
+          const uint64_t cc2 = f2_pack(c2, c2), nm2 = f2_pack(-base, -base);
+          float top = -INFINITY;
+          uint64_t sum2 = f2_pack(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t cur[32];
+            __syncwarp();
+            tmem_ld32(tS + 32 * q, cur);
+            tmem_ld_wait(cur);
+            if (hi >= 64) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float p0, p1;
+                top = fmax3(top, __uint_as_float(cur[e]), __uint_as_float(cur[e + 1]));
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                sum2 = f2_add(sum2, f2_pack(p0, p1));
+                img[16 * q + e / 2] = pack2<kBf16>(p0, p1);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float p0, p1;
+                const bool in0 = 32 * q + e < hi, in1 = 32 * q + e + 1 < hi;
+                top = in0 ? fmaxf(top, __uint_as_float(cur[e])) : top;
+                top = in1 ? fmaxf(top, __uint_as_float(cur[e + 1])) : top;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
+                p0 = in0 ? ex2_approx(p0) : 0.f;
+                p1 = in1 ? ex2_approx(p1) : 0.f;
+                sum2 = f2_add(sum2, f2_pack(p0, p1));
+                img[16 * q + e / 2] = pack2<kBf16>(p0, p1);
+              }
+            }
+          }
+          float s0, s1;
+          f2_unpack(sum2, s0, s1);
+          const bool moves = __any_sync(0xffffffffu, real && top * c2 > mref + kRescaleLog2);
+          if (lane == 0) fast[16 * (nf & 1) + (warp - 2)] = moves;
+          warp_arrive(bar(C::bFast + pq));
+          if (!warp_wait<false>(bar(C::bFast + pq), nf & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const bool either = moves || fast[16 * (nf & 1) + ((warp - 2) ^ 4)] != 0;
+          ++nf;
+          if (!either) {
+            lsum += s0 + s1;
+            tmem_st32(tS, img);
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(bar(C::bPFull + x));
+            continue;
+          }
+        }
         // Pass 1: this half's maximum of S.
         float hmax = -INFINITY;
         {
@@ -363,15 +429,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // The block maximum of the row: this half's and the other warp's (slots alternate
-        // with the block parity, so a slot is rewritten only after the partner has passed
-        // the next exchange, i.e. has read it).
-        float* xs = xchg + ((x * 2 + (n & 1)) * 2) * 128;
+        // from exchange to exchange, so a slot is rewritten only after the partner has passed
+        // the next one, i.e. has read it).
+        float* xs = xchg + ((x * 2 + (nx & 1)) * 2) * 128;
         xs[half * 128 + il] = hmax;
-        warp_arrive(bar(C::bXchg + 2 * pq + (n & 1)));
-        if (!warp_wait<false>(bar(C::bXchg + 2 * pq + (n & 1)), (n >> 1) & 1, abort_flag, p.status)) {
+        warp_arrive(bar(C::bXchg + pq));
+        if (!warp_wait<false>(bar(C::bXchg + pq), nx & 1, abort_flag, p.status)) {
           ok = false;
           break;
         }
+        ++nx;
         const float bmax = fmaxf(hmax, xs[(half ^ 1) * 128 + il]) * c2;  // (scale > 0)
         // Lazy rescale. Both warps of a row take the same decision; each rescales its D/2 O columns.
         const bool mv = bmax > mref + kRescaleLog2;
@@ -399,13 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mref = bmax;
         }
         const float base = mref == -INFINITY ? 0.f : mref;  // (every score so far is -inf or NaN)
-        // Pass 2, 32 keys at a time: P (0 past the end), this half's running sum, and the
-        // 16-bit image of the two MMA K steps over the same columns. A chunk writes residual
-        // columns where the block's largest probability may exceed 1/64 of this half's sum so
-        // far (a part of the final row sum, so the bound holds for the final P); zeros otherwise.
+        // Pass 2, 32 keys at a time: P (0 past the end), this half's running sum, and the image.
         const uint64_t cc2 = f2_pack(c2, c2), nm2 = f2_pack(-base, -base);
-        const float pmax = ex2_approx(bmax - base);
-        bool split = false;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t cur[32];
@@ -413,63 +475,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tS + 32 * q, cur);
           tmem_ld_wait(cur);
           uint64_t sum2 = f2_pack(0.f, 0.f);
-          if (hi >= 64) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              sum2 = f2_add(sum2, f2_pack(p0, p1));
-              cur[e] = __float_as_uint(p0);
-              cur[e + 1] = __float_as_uint(p1);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
-              p0 = (32 * q + e < hi) ? ex2_approx(p0) : 0.f;
-              p1 = (32 * q + e + 1 < hi) ? ex2_approx(p1) : 0.f;
-              sum2 = f2_add(sum2, f2_pack(p0, p1));
-              cur[e] = __float_as_uint(p0);
-              cur[e + 1] = __float_as_uint(p1);
-            }
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
+            p0 = (32 * q + e < hi) ? ex2_approx(p0) : 0.f;
+            p1 = (32 * q + e + 1 < hi) ? ex2_approx(p1) : 0.f;
+            sum2 = f2_add(sum2, f2_pack(p0, p1));
+            img[16 * q + e / 2] = pack2<kBf16>(p0, p1);
           }
-          __syncwarp();
           float s0, s1;
           f2_unpack(sum2, s0, s1);
           lsum += s0 + s1;
-          const bool sp = __any_sync(0xffffffffu, row_in && pmax > kSplitThreshold * lsum);
-          split |= sp;
-          // (sp is warp-uniform: a real branch, the residuals are computed only when needed)
-          if (sp) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float a = __uint_as_float(cur[16 * k + 2 * e]), c = __uint_as_float(cur[16 * k + 2 * e + 1]);
-                w[e] = pack2<kBf16>(a, c);
-                w[8 + e] = pack2_residual<kBf16>(a, c, w[e]);
-              }
-              tmem_st16(tS + 32 * q + 16 * k, w);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                w[e] = pack2<kBf16>(__uint_as_float(cur[16 * k + 2 * e]), __uint_as_float(cur[16 * k + 2 * e + 1]));
-                w[8 + e] = 0u;
-              }
-              tmem_st16(tS + 32 * q + 16 * k, w);
-            }
-          }
         }
+        __syncwarp();
+        tmem_st32(tS, img);
         tmem_st_wait();
-        if (lane == 0) flags[8 * x + 4 * half + wq] = split ? 1 : 0;
         tc_fence_before();
         warp_arrive(bar(C::bPFull + x));
       }

@@ -128,39 +128,67 @@ __device__ __forceinline__ void store_row(T* to, int left, const float (&v)[4]) 
   }
 }
 
-// A thread takes four values of a row (b, t, h) of [B, Nq, Hq, d].
-template <typename T>
+// kWide warps take a row (b, t, h) of [B, Nq, Hq, d], each every kWide-th split: a lane has one split's weight and
+// four values (lanes past d / 4 none), and eight splits' loads are under way at once. (A thread a
+// row piece with the splits one after the other took 45 us for 32 rows of 76 splits, one load's latency each.)
+template <typename T, int kWide>
 __global__ void __launch_bounds__(kJoinThreads) cross_join_fwd_kernel(const __grid_constant__ CrossParams p) {
+  constexpr int kRowsBlock = kJoinThreads / 32 / kWide;
+  __shared__ __align__(16) float part_sum[kJoinThreads / 32][128];
   let_next_begin();
   wait_for_previous();
-  const int quads = (p.d + 3) >> 2;
-  const long long n = (long long)p.B * p.Nq * p.Hq * quads;
-  const long long rows = (long long)p.B * p.Nq * p.Hq;
-  const bool vec = (p.d & 3) == 0;
-  for (long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kJoinThreads) {
-    const long long row = x / quads, bt = row / p.Hq;
-    const int e = 4 * (int)(x - row * quads), h = (int)(row - bt * p.Hq), b = (int)(bt / p.Nq);
-    const int t = (int)(bt - (long long)b * p.Nq);
-    const long long at = ((long long)b * p.Hq + h) * p.Nq + t;
-    float m = -INFINITY;
-    for (int s = 0; s < p.plan.k_splits; ++s) m = fmaxf(m, p.part_lse[s * rows + at]);
-    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < p.plan.k_splits; ++s) {
-      const float l = p.part_lse[s * rows + at];
-      if (l == -INFINITY) continue;
-      const float w = exp2f(l - m);
-      float a[4];
-      load_part(p.part + (s * rows + row) * p.d + e, p.d - e, vec, a);
-      sum += w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fmaf(w, a[i], v[i]);
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= inv;
-    store_row(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h + e, p.d - e, v);
-    if (e == 0) p.lse_out[at] = sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp % kWide;
+  const long long rows = (long long)p.B * p.Nq * p.Hq, row = (long long)blockIdx.x * kRowsBlock + warp / kWide;
+  const bool vec = (p.d & 3) == 0, in = row < rows;
+  const long long bt = row / p.Hq;
+  const int h = (int)(row - bt * p.Hq), b = (int)(bt / p.Nq), t = (int)(bt - (long long)b * p.Nq), e = 4 * lane;
+  const long long at = ((long long)b * p.Hq + h) * p.Nq + t;
+  const int n = p.plan.k_splits;
+  float m = -INFINITY, sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (in) {
+    for (int s = lane; s < n; s += 32) m = fmaxf(m, p.part_lse[s * rows + at]);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int s0 = 0; s0 < n; s0 += 32) {  // 32 splits' weights, one a lane
+    const int s = s0 + lane;
+    const float w = in && s < n ? exp2f(p.part_lse[s * rows + at] - base) : 0.f;
+    sum += row_sum<32>(w);
+#pragma unroll 1
+    for (int y0 = mine; y0 < 32 && s0 + y0 < n; y0 += 8 * kWide) {
+      float a[8][4], f[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int from = y0 + y * kWide;
+        f[y] = __shfl_sync(0xffffffffu, w, from & 31);
+        if (from >= 32 || s0 + from >= n) f[y] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[y][i] = 0.f;
+        if (f[y] != 0.f && e < p.d)  // (without keys a split has no output there)
+          load_part(p.part + ((long long)(s0 + from) * rows + row) * p.d + e, p.d - e, vec, a[y]);
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(f[y], a[y][i], v[i]);
+    }
+  }
+  if (kWide > 1) {
+    *reinterpret_cast<float4*>(&part_sum[warp][e]) = make_float4(v[0], v[1], v[2], v[3]);
+    __syncthreads();
+    if (mine != 0) return;
+#pragma unroll
+    for (int w = 1; w < kWide; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += part_sum[warp + w][e + i];
+  }
+  if (!in) return;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;  // (a NaN sum is there)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] *= inv;
+  if (e < p.d) store_row(static_cast<T*>(p.out) + b * p.out_st.b + t * p.out_st.n + h * p.out_st.h + e, p.d - e, v);
+  if (lane == 0) p.lse_out[at] = sum != 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Sums over the splits of [splits][.., N, H, d] from `part`, `apart` floats between
@@ -177,11 +205,19 @@ __device__ __forceinline__ void join_rows(const CrossParams& p, const float* par
     const int t = (int)(bt - (long long)b * N);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (t < (kKeys ? cross_k_len(p, b) : cross_q_len(p, b))) {
-      for (int s = 0; s < splits; ++s) {
-        float a[4];
-        load_part(part + s * apart + row * p.d + e, p.d - e, vec, a);
+      // (in order; eight loads under way at once)
+      for (int s0 = 0; s0 < splits; s0 += 8) {
+        float a[8][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += a[i];
+        for (int s = 0; s < 8; ++s) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[s][i] = 0.f;
+          if (s0 + s < splits) load_part(part + (s0 + s) * apart + row * p.d + e, p.d - e, vec, a[s]);
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] += a[s][i];
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] *= mul;
@@ -233,11 +269,18 @@ cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_
                           : launch_chained(cross_preprocess_kernel<__half, 128>, grid, kJoinThreads, 0, 1, p, st);
 }
 
+template <typename T>
+static cudaError_t launch_join_fwd(const CrossParams& p, cudaStream_t st) {
+  const long long rows = (long long)p.B * p.Nq * p.Hq;
+  const int n = p.plan.k_splits;
+  if (n > 16) return launch_chained(cross_join_fwd_kernel<T, 8>, dim3((unsigned)rows), kJoinThreads, 0, 1, p, st);
+  if (n > 8) return launch_chained(cross_join_fwd_kernel<T, 2>, dim3((unsigned)((rows + 3) / 4)), kJoinThreads, 0, 1, p, st);
+  return launch_chained(cross_join_fwd_kernel<T, 1>, dim3((unsigned)((rows + 7) / 8)), kJoinThreads, 0, 1, p, st);
+}
+
 cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t st) {
-  const dim3 grid(join_blocks(p, p.Nq, p.Hq));
-  if (dtype == FA_F32) return launch_chained(cross_join_fwd_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
-  return dtype == FA_BF16 ? launch_chained(cross_join_fwd_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
-                          : launch_chained(cross_join_fwd_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+  if (dtype == FA_F32) return launch_join_fwd<float>(p, st);
+  return dtype == FA_BF16 ? launch_join_fwd<__nv_bfloat16>(p, st) : launch_join_fwd<__half>(p, st);
 }
 
 cudaError_t launch_cross_join_dq(const CrossParams& p, int dtype, cudaStream_t st) {

@@ -489,8 +489,10 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * and both are for shapes that the calls refuse; calls that overlap on the GPU need
  * workspaces of their own.
  * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
- * fp32. In 16 bits: P and dS as operands of the products, with their rounding residual
- * wherever a probability of the tile may exceed 1/64 (as fa_fwd and fa_bwd). Errors as
+ * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, rounded
+ * once (off by at most 2^-9 of themselves in bf16, 2^-12 in fp16); their rounding residual
+ * is multiplied too in the backward where a probability of the tile exceeds 1/4, and in the
+ * forward where a key head has few query rows (16, or up to 64 in small calls). Errors as
  * fa_fwd / fa_bwd.
  * ------------------------------------------------------------------------- */
 typedef struct {

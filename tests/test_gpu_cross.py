@@ -61,6 +61,31 @@ def test_many_units_a_block(size, q_lens, k_lens, dtype):
     run(*make(*size, dtype), q_lens, k_lens)
 
 
+FEW = [
+    # few rows a key head: one block, clusters of two to eight, shares through the workspace, several row tiles
+    ((1, 1, 5000, 2, 1, 128), None), ((1, 1, 9001, 1, 1, 64), None), ((2, 3, 4111, 4, 2, 64), [4111, 17]),
+    ((3, 1, 700, 32, 8, 128), [700, 1, 0]), ((40, 1, 333, 16, 8, 64), [(53 * b) % 334 for b in range(40)]),
+    ((2, 17, 1500, 2, 2, 64), None), ((1, 31, 900, 4, 2, 128), None), ((1, 64, 600, 3, 3, 64), [599]),
+    ((1, 1, 40, 64, 1, 128), None), ((100, 1, 60, 8, 8, 64), None), ((1, 2, 6000, 8, 1, 128), [5999]),
+    ((1, 5, 5000, 3, 1, 64), [129]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("size,k_lens", FEW)
+def test_few_rows(size, k_lens, dtype):
+    """Forward of single and few new tokens, with the bounds; what lies behind the lengths reaches nothing."""
+    q, k, v, _ = make(*size, dtype)
+    o, lse = fa.cross_attention_forward(q, k, v, k_lens=ints(k_lens))
+    Reference(q, k, v, None, ints(k_lens)).check_forward(o, lse)
+    if k_lens is not None:
+        for b, n in enumerate(k_lens):
+            k[b, n:], v[b, n:] = math.nan, math.inf
+        o2, lse2 = fa.cross_attention_forward(q, k, v, k_lens=ints(k_lens))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert fa.fa_get_device_status() == 0
+
+
 @pytest.mark.parametrize("d", [1, 17, 63, 96, 128])
 def test_fp32_head_dimensions(d):
     run(*make(2, 70, 45, 4, 2, d, F32))
