@@ -72,6 +72,8 @@ void fill(CrossParams& p, const fa_cross_shape* s, const CrossPlan& plan, float 
 
 long long div_up(long long a, long long b) { return (a + b - 1) / b; }
 
+constexpr int kPlaces = 152;  // SMs, one block of the tensor-core kernels each
+
 // Splits of an axis of `steps` for `units` independent pieces of work on `places` that run them round by
 // round: the number that makes the rounds' steps fewest, where a unit costs `start` steps more than its
 // own and the join `join` in all.
@@ -111,6 +113,28 @@ void few_plan(long long units, int Nk, CrossPlan* c) {
   }
 }
 
+// The backward's splits and blocks. Splits: until dK/dV has 128 units or they are down to 16 query steps, dQ 64 units or
+// 8 key blocks. Blocks: as many as there are units, but not under 16 steps (8 key blocks) each while 128 blocks
+// remain. Measured, us (dK/dV splits / blocks, dQ splits / blocks): 16 heads, 4095 queries over 77 keys, d = 64: 16 / 128,
+// 1 / 256 73; 4 / 32, 1 / 104 120; 32 / 256, 1 / 512 86. 16/4 heads, 1024 over 1024, batch 2: 2 / 128, 1 / 128 84; 1 / 64, 1 / 62
+// 98. 64 queries over 16384 keys: 1 / 512, 4 / 64 130; 1 / 512, 1 / 16 227.
+void bwd_plan(const fa_cross_shape* s, long long groups, long long tiles, CrossPlan* c) {
+  const int steps = c->step.count(s->Nq, s->Hq / s->Hk), blocks = (int)div_up(s->Nk, 128);
+  const long long kv = groups * div_up(s->Nk, 128), q = groups * tiles;
+  const auto splits = [](long long units, long long most, int n, int least) {  // of n steps a unit
+    const long long want = std::min<long long>(div_up(most, units), std::max(1, n / least));
+    return (int)div_up(n, div_up(n, want));
+  };
+  c->q_splits = splits(kv, 128, steps, 16);
+  c->k_splits = splits(q, 64, blocks, 8);
+  const auto share = [](long long units, int n, int least) {
+    const long long each = std::max(1, least / n);  // units of a block
+    return (int)std::max(div_up(units, each), std::min(units, 128ll));
+  };
+  c->kv_blocks = share(kv * c->q_splits, (int)div_up(steps, c->q_splits), 16);
+  c->q_blocks = share(q * c->k_splits, (int)div_up(blocks, c->k_splits), 8);
+}
+
 CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype, bool backward) {
   CrossPlan c;
   const int G = s->Hq / s->Hk;
@@ -131,10 +155,9 @@ CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype, bool backward) {
   }
   const long long groups = (long long)s->B * s->Hk, tiles = c.q_tile.count(s->Nq, G);
   if (!backward) {
-    c.k_splits = best_splits(groups * div_up(tiles, 2), (int)div_up(s->Nk, 128), 152, 1, 4);
+    c.k_splits = best_splits(groups * div_up(tiles, 2), (int)div_up(s->Nk, 128), kPlaces, 1, 4);
   } else {
-    c.k_splits = best_splits(groups * tiles, (int)div_up(s->Nk, 128), 152, 1, 4);
-    c.q_splits = best_splits(groups * div_up(s->Nk, 128), c.step.count(s->Nq, G), 152, 2, 6);
+    bwd_plan(s, groups, tiles, &c);
   }
   return c;
 }
@@ -276,22 +299,18 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   if ((rc = fa::status_ptr(&p.status))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f32 = dtype == FA_F32, bf16 = dtype == FA_BF16;
-  CUtensorMap steps[4], tiles[4];  // Q, K, V, dO of the two kernels
+  CUtensorMap maps[6];
   if (!f32) {
     if ((rc = fa::bind_device_context())) return rc;
-    if (!q_map(&steps[0], p, q, q_strides, plan.step, dtype) || !q_map(&steps[3], p, dout, dout_strides, plan.step, dtype) ||
-        !q_map(&tiles[0], p, q, q_strides, plan.q_tile, dtype) ||
-        !q_map(&tiles[3], p, dout, dout_strides, plan.q_tile, dtype) || !k_map(&steps[1], p, k, k_strides, dtype) ||
-        !k_map(&steps[2], p, v, v_strides, dtype))
+    if (!q_map(&maps[0], p, q, q_strides, plan.step, dtype) || !q_map(&maps[1], p, dout, dout_strides, plan.step, dtype) ||
+        !q_map(&maps[2], p, q, q_strides, plan.q_tile, dtype) ||
+        !q_map(&maps[3], p, dout, dout_strides, plan.q_tile, dtype) || !k_map(&maps[4], p, k, k_strides, dtype) ||
+        !k_map(&maps[5], p, v, v_strides, dtype))
       return FA_ERR_CUDA;
-    tiles[1] = steps[1];
-    tiles[2] = steps[2];
   }
   cudaError_t e = fa::launch_cross_preprocess(p, dtype, st);
-  if (e == cudaSuccess) e = f32 ? fa::launch_cross_dkdv_f32(p, st) : fa::launch_cross_dkdv_tc(p, bf16, steps, st);
-  if (e == cudaSuccess && plan.q_splits > 1) e = fa::launch_cross_join_dkdv(p, dtype, st);
-  if (e == cudaSuccess) e = f32 ? fa::launch_cross_dq_f32(p, st) : fa::launch_cross_dq_tc(p, bf16, tiles, st);
-  if (e == cudaSuccess && plan.k_splits > 1) e = fa::launch_cross_join_dq(p, dtype, st);
+  if (e == cudaSuccess) e = f32 ? fa::launch_cross_bwd_f32(p, st) : fa::launch_cross_bwd_tc(p, bf16, maps, st);
+  if (e == cudaSuccess && (plan.q_splits > 1 || plan.k_splits > 1)) e = fa::launch_cross_join_bwd(p, dtype, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

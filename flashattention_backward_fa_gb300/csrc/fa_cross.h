@@ -44,7 +44,8 @@ struct CrossPlan {
   int q_splits;  // of its query steps (steps run over the group's heads and its queries)
   CrossTile q_tile;  // of the forward and dQ (128 rows)
   CrossTile step;    // of the dK/dV kernel's query steps (64 rows)
-  bool few;          // the forward's kernel of few rows
+  int kv_blocks, q_blocks;  // the backward's blocks for dK/dV and for dQ, which share out the units
+  bool few;                 // the forward's kernel of few rows
   int few_cluster;
 };
 
@@ -245,23 +246,35 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, uint32_t panel, int fro
 
 cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t st);
-cudaError_t launch_cross_join_dq(const CrossParams& p, int dtype, cudaStream_t st);
-cudaError_t launch_cross_join_dkdv(const CrossParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_cross_join_bwd(const CrossParams& p, int dtype, cudaStream_t st);
+
+// launch_chained (fa_serve.h) for the kernels that take tensor maps beside their parameters.
+template <typename... Args>
+cudaError_t launch_chained_maps(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // maps: Q (boxes of the tile's queries x heads), K, V (boxes of 128 rows), all of 64 head-dim
 // elements, 128-byte swizzle.
 cudaError_t launch_cross_fwd_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
 
-// maps: Q (boxes of the query step's rows), K, V (boxes of 128 rows), dO (as Q).
-cudaError_t launch_cross_dkdv_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
-// maps: Q (boxes of the tile's rows), K, V (boxes of 128 rows), dO (as Q).
-cudaError_t launch_cross_dq_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
+// dK, dV and dQ. maps: Q and dO of the query steps, Q and dO of the query tiles, K, V (boxes of 128 rows).
+cudaError_t launch_cross_bwd_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
 
 // Forward of few rows a key head (16-bit types).
 cudaError_t launch_cross_few(const CrossParams& p, bool bf16, cudaStream_t st);
 
 cudaError_t launch_cross_fwd_f32(const CrossParams& p, cudaStream_t st);
-cudaError_t launch_cross_dq_f32(const CrossParams& p, cudaStream_t st);
-cudaError_t launch_cross_dkdv_f32(const CrossParams& p, cudaStream_t st);
+cudaError_t launch_cross_bwd_f32(const CrossParams& p, cudaStream_t st);
 
 }  // namespace fa

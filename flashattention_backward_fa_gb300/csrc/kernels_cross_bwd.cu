@@ -1,6 +1,6 @@
-// Backward of cross attention on the sm_103a tensor cores: two kernels over the same
-// recomputed probabilities, one that holds keys and walks queries (dK, dV), one that holds
-// queries and walks keys (dQ), so that every sum is formed on chip in a fixed order.
+// Backward of cross attention on the sm_103a tensor cores: two kinds of blocks over the
+// same recomputed probabilities, one that holds keys and walks queries (dK, dV), one that
+// holds queries and walks keys (dQ), so that every sum is formed on chip in a fixed order.
 //
 //   S = Q K^T, P = exp2(S * scale*log2e - L*log2e), dP = dO V^T, dS = P o (dP - D)
 //   dV += P^T dO, dK += dS^T Q over the queries of all heads of a group; dQ += dS K
@@ -13,16 +13,21 @@
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //
-// Both are persistent grids, one CTA an SM, that take their units in a fixed stride; steps,
-// ring stages and barrier phases run on from unit to unit, so that the next unit's loads
-// and first MMAs overlap this one's end. Where there are fewer units than SMs (few keys
-// and many queries, or the other way round) the walked axis is cut into splits whose fp32
-// sums a second kernel adds in order.
+// One CTA an SM. Both kinds are in one launch, dK/dV first. A block takes a few units (key
+// tiles; query tiles) in a fixed stride, enough of them to outweigh its start; steps, ring
+// stages and barrier phases run on from unit to unit, so that the next unit's loads and
+// first MMAs overlap this one's end. Where there are few units for the GPU (few keys and
+// many queries, or the other way round) the walked axis is cut into splits whose fp32 sums
+// a second kernel adds in order.
 //
 // Masks. Query columns and key columns past their sequence's length get P = dS = 0 by
 // selects (S and dP there may be NaN); the rows of Q, dO and K that such columns meet in the
 // accumulating MMAs are zeroed in shared memory first (0 * NaN).
+#include <algorithm>
+
 #include "fa_cross.h"
+#include "fa_serve.h"
+#include "rope_common.cuh"
 
 namespace fa {
 
@@ -64,8 +69,8 @@ struct KCfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = oAbort + 8;    // [buffer][8 warps] split votes
-  static constexpr uint32_t oNotes = oFlags + 64;   // [16 row-math warps]
-  static constexpr uint32_t kSmem = oNotes + 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t oNotes = oFlags + 64;   // [2][16 row-math warps]
+  static constexpr uint32_t kSmem = oNotes + 2 * 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
@@ -118,14 +123,12 @@ __device__ __forceinline__ uint32_t step_columns(const CrossTile& t, int c, int 
   return m & bit_range(0, rows - 32 * c);
 }
 
+// A block's share: the units first, first + stride, ...
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1)
-    cross_dkdv_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQ,
-                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __grid_constant__ CUtensorMap tmDO) {
+__device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                           const CUtensorMap& tmV, const CUtensorMap& tmDO, uint8_t* smem, int first,
+                                           int stride) {
   using C = KCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rows = 1 << (p.plan.step.q_log + p.plan.step.h_log);
   // The first unit from idx on in this CTA's stride that has steps; -1: none.
   auto next_work = [&](int idx, KUnit& u) -> int {
-    for (; idx < units; idx += gridDim.x) {
+    for (; idx < units; idx += stride) {
       k_unit(p, idx, u);
       if (u.steps > 0) return idx;
     }
@@ -178,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       st_shared_v4(sb + C::oQ + 16 * x, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -190,8 +194,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = (uint32_t)(2 * C::kPanels * 128 + 2 * 4) * rows;
       int kl = 0, G = 0;  // units and steps loaded
       bool ok = true;
-      KUnit u;
-      for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u)) {
+      KUnit u, next;
+      int after = next_work(first, next);
+      for (int idx = after; ok && idx >= 0; idx = after) {
+        u = next;
+        after = next_work(idx + stride, next);
         // K and V of this unit, once the previous unit's last reads of them are done
         if (kl > 0 && !mbar_wait(bar(C::bKVFree), (kl - 1) & 1, abort_flag, p.status)) break;
         mbar_arrive_expect_tx(bar(C::bKV), 2 * C::kKVTile);
@@ -239,10 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bF = isS ? C::bSFull : C::bDPFull, bE = isS ? C::bSEmpty : C::bDPEmpty;
     int kl = 0, G = 0;
     bool ok = true;
-    KUnit u;
-    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
-      idx = uniform(idx);
+    KUnit u, next;
+    int after = next_work(first, next);
+    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
+      u = next;
       u.steps = uniform(u.steps);
+      after = next_work(idx + stride, next);
       ok = warp_wait<kIssuerPoll>(bar(C::bKV), kl & 1, abort_flag, p.status);
       for (int it = 0; ok && it < u.steps; ++it, ++G) {
         const int s = G % C::kNS, bb = G & 1;
@@ -273,10 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t mQ0 = make_sdesc(sb + C::oQ, C::kQPanel, 1024), mO0 = make_sdesc(sb + C::oDO, C::kQPanel, 1024);
     int kl = 0, G = 0;
     bool ok = true;
-    KUnit u;
-    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
-      idx = uniform(idx);
+    KUnit u, next;
+    int after = next_work(first, next);
+    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
+      u = next;
       u.steps = uniform(u.steps);
+      int chunk = u.first % u.chunks;  // of a head's queries
+      after = next_work(idx + stride, next);
       for (int it = 0; it < u.steps; ++it, ++G) {
         const int bt = G & 1, st = G % C::kNS;
         if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
@@ -287,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Rows of queries past the sequence's end, as far as they are the tensors' (past them: zeros by
         // TMA). S^T is formed; dP^T may still read dO: its columns of these rows are not used.
-        if (u.nq < p.Nq) {
-          int h0, q0;
-          k_step(p, u, it, h0, q0);
-          const int q = p.plan.step.queries(), from = u.nq - q0, to = min(q, p.Nq - q0);
+        if (++chunk == u.chunks) {
+          chunk = 0;
+          const int q0 = (u.chunks - 1) << p.plan.step.q_log, q = p.plan.step.queries();
+          const int from = u.nq - q0, to = min(q, p.Nq - q0);
           for (int h = 0; from < to && h < p.plan.step.heads(); ++h) {
             zero_rows<C::kPanels>(sb + C::oQ + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
             zero_rows<C::kPanels>(sb + C::oDO + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
@@ -301,13 +313,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 8; ++x) any |= flags[8 * bt + x];
         const bool split = uniform(any) != 0;
-        const uint32_t first = it > 0 ? 1u : 0u;
+        const uint32_t keep = it > 0 ? 1u : 0u;
         const uint64_t qd = desc_add(mQ0, st * C::kQTile), gd = desc_add(mO0, st * C::kQTile);
         // dV += P^T dO: K step kk reads the 8 rounded columns at 16kk of the P^T image and, on split
         // tiles, the 8 residual columns at 16kk + 8.
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
-          tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk, desc_add(gd, 2048 * kk), idG, kk > 0 ? 1u : first);
+          tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk, desc_add(gd, 2048 * kk), idG, kk > 0 ? 1u : keep);
         if (split) {
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
-          tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk, desc_add(qd, 2048 * kk), idG, kk > 0 ? 1u : first);
+          tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk, desc_add(qd, 2048 * kk), idG, kk > 0 ? 1u : keep);
         if (split) {
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)
@@ -351,22 +363,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 4);
     int kl = 0, G = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
-      // The columns with real queries of any step but a head's last (or last few heads') and of that one,
-      // none for a lane without a key; chunk: the step's place among a head's chunks.
-      int steps, chunks, chunk;
+    // The unit at hand and, decoded before its epilogue, the next one: steps, chunks of a head's queries, the first
+    // step's chunk, the columns with real queries of any step but a head's last (or last few heads') and of that
+    // one, and whether the lane has a real key. The rest is noted. (A lane without one needs no mask: its row of
+    // P^T and dS^T reaches nothing but its own row of dV and dK, which the epilogue drops. It has no vote.)
+    struct {
+      int steps, chunks, first;
       uint32_t full, tail;
-      {
-        KUnit u;
-        k_unit(p, idx, u);
-        steps = u.steps;
-        chunks = max(u.chunks, 1);
-        chunk = (u.first + ((bb ^ G) & 1)) % chunks;
-        full = step_columns(p.plan.step, c, kStep);
-        tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
-        if (u.j0 + jl >= u.nk) full = tail = 0u;
-        keep_note(note, u.b, u.hk, u.j0, u.nk, u.split);
-      }
+      bool real;
+    } cur, next;
+    const auto decode = [&](int idx, int slot, auto& to) {
+      KUnit u;
+      k_unit(p, idx, u);
+      to.steps = u.steps;
+      to.chunks = max(u.chunks, 1);
+      to.first = u.first % to.chunks;
+      to.full = step_columns(p.plan.step, c, kStep);
+      to.tail = step_columns(p.plan.step, c, u.nq - ((to.chunks - 1) << p.plan.step.q_log));
+      to.real = u.j0 + jl < u.nk;
+      keep_note(note + 16 * slot, u.b, u.hk, u.j0, u.nk, u.split);
+    };
+    int slot = 0;
+    decode(first, 0, cur);
+    for (int idx = first; ok && idx < units; idx += stride, cur = next, slot ^= 1) {
+      const int steps = cur.steps, chunks = cur.chunks;
+      const uint32_t full = cur.full, tail = cur.tail;
+      int chunk = cur.first + ((bb ^ G) & 1);
+      chunk -= chunk >= chunks ? chunks : 0;
       for (int it = (bb ^ G) & 1; it < steps; it += 2) {
         const int gs = G + it, s = gs % C::kNS;
         const uint32_t allow = chunk == chunks - 1 ? tail : full;
@@ -387,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint32_t sr[16];
-          __syncwarp();  // per-lane branches above: converge for the TMEM load
+          __syncwarp();
           tmem_ld16(tSc + 16 * hh, sr);
           tmem_ld_wait16(sr);
           float cmax = 0.f;
@@ -411,15 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               cmax = fmax3(cmax, pv[2], pv[3]);
             }
           };
-          if (allow == 0xFFFFFFFFu)
+          if (allow == 0xFFFFFFFFu)  // (the same for the whole warp)
             p_phase(std::false_type{});
           else
             p_phase(std::true_type{});
-          __syncwarp();  // reconverge before the collective vote and TMEM stores
           uint32_t hp[8], ep[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
-          split_h[hh] = __any_sync(0xFFFFFFFFu, cmax > kCrossSplit);
+          split_h[hh] = __any_sync(0xFFFFFFFFu, cur.real && cmax > kCrossSplit);
           if (split_h[hh]) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
@@ -482,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bDSFull + bb));
       }
       if (!ok) break;
+      if (idx + stride < units) decode(idx + stride, slot ^ 1, next);
       // Epilogue, by the pair that ran the unit's last step: dV, then dK, each warpgroup half of the
       // columns; both accumulators are released (AccFree) behind the last load.
       const bool epi = steps > 0 ? bb == ((G + steps - 1) & 1) : bb == 0;
@@ -493,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
         }
-        const int b = note->a[0], hk = note->a[1], j = note->a[2] + jl, nk = note->a[3];
+        const volatile CrossNote* at_hand = note + 16 * slot;
+        const int b = at_hand->a[0], hk = at_hand->a[1], j = at_hand->a[2] + jl, nk = at_hand->a[3];
         const long long size = (long long)p.B * p.Nk * p.Hk * D;
         const bool parts = p.plan.q_splits > 1;
 #pragma unroll 1
@@ -514,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = j < nk ? r[x] : 0u;  // (0 * NaN of a real query's)
-          float* to_part = parts && j < nk ? p.part_kv + 2 * note->a[4] * size + (isK ? 0 : size) +
+          float* to_part = parts && j < nk ? p.part_kv + 2 * at_hand->a[4] * size + (isK ? 0 : size) +
                                                  (((long long)b * p.Nk + j) * p.Hk + hk) * D + col
                                            : nullptr;
           const fa_strides& st = isK ? p.dk_st : p.dv_st;
@@ -569,19 +593,16 @@ struct QCfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [buffer][16 warps] split votes
-  static constexpr uint32_t oNotes = oFlags + 2 * 16 * 4;        // [16 row-math warps]
-  static constexpr uint32_t kSmem = oNotes + 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t oNotes = oFlags + 2 * 16 * 4;        // [2][16 row-math warps]
+  static constexpr uint32_t kSmem = oNotes + 2 * 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1)
-    cross_dq_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQ,
-                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmDO) {
+__device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                         const CUtensorMap& tmV, const CUtensorMap& tmDO, uint8_t* smem, int first,
+                                         int stride) {
   using C = QCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
@@ -589,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
   const int units = cross_units<1>(p);
   auto next_work = [&](int idx, CrossUnit& u) -> int {
-    for (; idx < units; idx += gridDim.x) {
+    for (; idx < units; idx += stride) {
       cross_unit<1>(p, idx, u);
       if (u.blocks > 0) return idx;
     }
@@ -629,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmV);
     prefetch_tmap(&tmDO);
   }
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -641,8 +663,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = 2u * C::kPanels * 128u << (p.plan.q_tile.q_log + p.plan.q_tile.h_log);
       int kl = 0, G = 0, issuedV = 0, issuedK = 0;
       bool ok = true;
-      CrossUnit u;
-      for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u)) {
+      CrossUnit u, next;
+      int after = next_work(first, next);
+      for (int idx = after; ok && idx >= 0; idx = after) {
+        u = next;
+        after = next_work(idx + stride, next);
         if (kl > 0 && !mbar_wait(bar(C::bResFree), (kl - 1) & 1, abort_flag, p.status)) break;
         const CrossRows r = cross_rows(p, u, u.first);
         mbar_arrive_expect_tx(bar(C::bRes), q_bytes);
@@ -687,10 +712,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                    dB0 = make_sdesc(sb + (isS ? C::oK : C::oV), 16, 1024);
     int kl = 0, G = 0;
     bool ok = true;
-    CrossUnit u;
-    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
-      idx = uniform(idx);
+    CrossUnit u, next;
+    int after = next_work(first, next);
+    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
+      u = next;
       u.blocks = uniform(u.blocks);
+      after = next_work(idx + stride, next);
       ok = warp_wait<kIssuerPoll>(bar(C::bRes), kl & 1, abort_flag, p.status);
       for (int it = 0; ok && it < u.blocks; ++it, ++G) {
         const int bb = G & 1, st = isS ? G % C::kNK : G % C::kNV;
@@ -725,10 +752,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t b0 = make_sdesc(sb + C::oK, C::kPanel, 1024);
     int kl = 0, G = 0;
     bool ok = true;
-    CrossUnit u;
-    for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u), ++kl) {
-      idx = uniform(idx);
+    CrossUnit u, next;
+    int after = next_work(first, next);
+    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
+      u = next;
       u.blocks = uniform(u.blocks);
+      after = next_work(idx + stride, next);
       u.j_begin = uniform(u.j_begin);
       u.j_end = uniform(u.j_end);
       for (int it = 0; it < u.blocks; ++it, ++G) {
@@ -778,22 +807,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 4);
     int kl = 0, G = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
-      int blocks, left = -32 * c;  // left: real keys from this warpgroup's first column on
-      float nL2 = -INFINITY, nD = 0.f;
-      {
-        CrossUnit u;
-        cross_unit<1>(p, idx, u);
-        const CrossRows rt = cross_rows(p, u, u.first);
-        blocks = u.blocks;
-        left += u.j_end - u.j_begin;
-        keep_note(note, rt.q0, rt.h0, u.b, u.nq, u.split);
-        if (blocks > 0 && row_in) {  // (rows past the sequence hold -inf and 0)
-          const long long at = ((long long)u.b * p.Hq + rt.h0 + row_h) * p.nq_pad + rt.q0 + row_q;
-          nL2 = p.nL2[at];
-          nD = p.nD[at];
-        }
+    // The unit at hand and, decoded before its epilogue, the next one: blocks, real keys from this warpgroup's first
+    // column on, the row's -L and -D (-inf and 0 past the sequence). The rest is noted.
+    struct {
+      int blocks, left;
+      float nL2, nD;
+    } cur, next;
+    const auto decode = [&](int idx, int slot, auto& to) {
+      CrossUnit u;
+      cross_unit<1>(p, idx, u);
+      const CrossRows rt = cross_rows(p, u, u.first);
+      to.blocks = u.blocks;
+      to.left = u.j_end - u.j_begin - 32 * c;
+      to.nL2 = -INFINITY;
+      to.nD = 0.f;
+      if (u.blocks > 0 && row_in) {
+        const long long at = ((long long)u.b * p.Hq + rt.h0 + row_h) * p.nq_pad + rt.q0 + row_q;
+        to.nL2 = p.nL2[at];
+        to.nD = p.nD[at];
       }
+      keep_note(note + 16 * slot, rt.q0, rt.h0, u.b, u.nq, u.split);
+    };
+    int slot = 0;
+    decode(first, 0, cur);
+    for (int idx = first; ok && idx < units; idx += stride, cur = next, slot ^= 1) {
+      const int blocks = cur.blocks, left = cur.left;
+      const float nL2 = cur.nL2, nD = cur.nD;
       const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
       for (int it = 0; it < blocks; ++it) {
         const int gs = G + it, bb = gs & 1;
@@ -868,6 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bPFull + bb));
       }
       if (!ok) break;
+      if (idx + stride < units) decode(idx + stride, slot ^ 1, next);
       // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
       // (AccFree) before the stores, so the next unit's first MMA can start meanwhile.
       uint32_t r[32];  // (D / 4 of them)
@@ -894,11 +934,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bAccFree));
         ++kl;
       }
-      const int i = note->a[0] + row_q, h = note->a[1] + row_h, b = note->a[2], nq = note->a[3];
+      const volatile CrossNote* at_hand = note + 16 * slot;
+      const int i = at_hand->a[0] + row_q, h = at_hand->a[1] + row_h, b = at_hand->a[2], nq = at_hand->a[3];
       const bool parts = p.plan.k_splits > 1, in = row_in && i < (parts ? nq : p.Nq);
 #pragma unroll
       for (int x = 0; x < 32; ++x) r[x] = i < nq ? r[x] : 0u;  // (rows that are not there may hold NaN)
-      float* to_part = parts && in ? p.part + ((((long long)note->a[4] * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
+      float* to_part = parts && in ? p.part + ((((long long)at_hand->a[4] * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
                                    : nullptr;
       uint16_t* to_out = !parts && in ? static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h +
                                             c * (D / 4)
@@ -934,34 +975,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename Kernel>
-cudaError_t launch_persistent(Kernel kern, uint32_t bytes, long long units, const CrossParams& p, const CUtensorMap* maps,
-                              cudaStream_t st) {
-  const int smem = (int)(bytes > kMinSmemOneCtaPerSm ? bytes : kMinSmemOneCtaPerSm);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// One launch for both: blocks [0, kv_blocks) take the units of dK/dV, the others those of dQ, so that they share
+// the GPU and each other's tails.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_bwd_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQStep,
+                     const __grid_constant__ CUtensorMap tmDOStep, const __grid_constant__ CUtensorMap tmQTile,
+                     const __grid_constant__ CUtensorMap tmDOTile, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV) {
+  extern __shared__ uint8_t smem_raw[];
+  let_next_begin();
+  const int kv = p.plan.kv_blocks;
+  if ((int)blockIdx.x < kv)
+    dkdv_block<D, kBf16>(p, tmQStep, tmK, tmV, tmDOStep, align1024(smem_raw), blockIdx.x, kv);
+  else
+    dq_block<D, kBf16>(p, tmQTile, tmK, tmV, tmDOTile, align1024(smem_raw), blockIdx.x - kv, gridDim.x - kv);
+}
+
+template <int D, bool kBf16>
+cudaError_t launch_t(const CrossParams& p, const CUtensorMap* m, cudaStream_t st) {
+  constexpr int bytes = (int)std::max(std::max(KCfg<D>::kSmem, QCfg<D>::kSmem), kMinSmemOneCtaPerSm);
+  constexpr auto kKernel = cross_bwd_kernel<D, kBf16>;
+  const cudaError_t e = allow_smem<kKernel>(bytes);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(units < 152 ? units : 152), kThreads, smem, st>>>(p, maps[0], maps[1], maps[2], maps[3]);
-  return cudaGetLastError();
+  return launch_chained_maps(kKernel, dim3(p.plan.kv_blocks + p.plan.q_blocks), kThreads, bytes, st, p, m[0], m[1], m[2],
+                             m[3], m[4], m[5]);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_dkdv_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st) {
-  const long long units = (long long)p.B * p.Hk * ((p.Nk + 127) / 128) * p.plan.q_splits;
-  if (p.d == 128)
-    return bf16 ? launch_persistent(cross_dkdv_kernel<128, true>, KCfg<128>::kSmem, units, p, maps, st)
-                : launch_persistent(cross_dkdv_kernel<128, false>, KCfg<128>::kSmem, units, p, maps, st);
-  return bf16 ? launch_persistent(cross_dkdv_kernel<64, true>, KCfg<64>::kSmem, units, p, maps, st)
-              : launch_persistent(cross_dkdv_kernel<64, false>, KCfg<64>::kSmem, units, p, maps, st);
-}
-
-cudaError_t launch_cross_dq_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st) {
-  const long long units = (long long)p.B * p.Hk * p.plan.q_tile.count(p.Nq, p.G) * p.plan.k_splits;
-  if (p.d == 128)
-    return bf16 ? launch_persistent(cross_dq_kernel<128, true>, QCfg<128>::kSmem, units, p, maps, st)
-                : launch_persistent(cross_dq_kernel<128, false>, QCfg<128>::kSmem, units, p, maps, st);
-  return bf16 ? launch_persistent(cross_dq_kernel<64, true>, QCfg<64>::kSmem, units, p, maps, st)
-              : launch_persistent(cross_dq_kernel<64, false>, QCfg<64>::kSmem, units, p, maps, st);
+cudaError_t launch_cross_bwd_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st) {
+  if (p.d == 128) return bf16 ? launch_t<128, true>(p, maps, st) : launch_t<128, false>(p, maps, st);
+  return bf16 ? launch_t<64, true>(p, maps, st) : launch_t<64, false>(p, maps, st);
 }
 
 }  // namespace fa

@@ -29,14 +29,34 @@ struct Tile {
   static constexpr int bytes(int rows) { return rows * kApart * 4; }
 };
 
-// Rows [0, rows) of a tensor (row stride `st`, d values each) to shared memory as fp32 [most][DP],
-// zeros past `rows` and d.
-template <int DP>
-__device__ __forceinline__ void stage(float* to, const float* from, int64_t st, int rows, int most, int d) {
-  for (int x = threadIdx.x; x < most * DP; x += kThreads) {
+// Rows [0, rows) of a tensor (row stride `st`, d values each) to shared memory as [kMost][DP], zeros past `rows`
+// and d; by 16 bytes where the tensor's strides allow it (vec), all of a thread's loads under way at once.
+template <int DP, int kMost>
+__device__ __forceinline__ void stage(float* to, const float* from, int64_t st, int rows, int d, bool vec) {
+  if (vec) {
+    constexpr int kEach = kMost * DP / 4 / kThreads;
+    float4 v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int x = threadIdx.x + i * kThreads, r = x / (DP / 4), e = 4 * (x % (DP / 4));
+      v[i] = r < rows && e < d ? *reinterpret_cast<const float4*>(from + r * st + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int x = threadIdx.x + i * kThreads, r = x / (DP / 4), e = 4 * (x % (DP / 4));
+      *reinterpret_cast<float4*>(to + r * Tile<DP>::kApart + e) = v[i];
+    }
+    return;
+  }
+#pragma unroll 8
+  for (int x = threadIdx.x; x < kMost * DP; x += kThreads) {
     const int r = x / DP, e = x - r * DP;
     to[r * Tile<DP>::kApart + e] = r < rows && e < d ? from[r * st + e] : 0.f;
   }
+}
+
+__device__ __forceinline__ bool vec_rows(const CrossParams& p, const fa_strides& st) {
+  return ((p.d | (int)(st.b & 3) | (int)(st.n & 3) | (int)(st.h & 3)) & 3) == 0;
 }
 
 // s[i][j] = row ty + 8 i of a . row tx + 16 j of b.
@@ -159,12 +179,11 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_co
 #pragma unroll
   for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
   if (i0 < nq)
-    stage<DP>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
-                 kRows, p.d);
+    stage<DP, kRows>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0, p.d, vec_rows(p, p.q_st));
   for (int j0 = split * per; i0 < nq && j0 < j_end; j0 += kCols) {
     __syncthreads();
-    stage<DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
-    stage<DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
+    stage<DP, kCols>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, p.d, vec_rows(p, p.k_st));
+    stage<DP, kCols>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, p.d, vec_rows(p, p.v_st));
     __syncthreads();
     float s[4][4];
     rows_by_rows<DP>(q, k, s);
@@ -221,16 +240,13 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_co
   }
 }
 
-// dQ. Grid as the forward's.
+// dQ of a query tile x and head h over the keys of one split (z: batch * split).
 template <int DP>
-__global__ void __launch_bounds__(kThreads) cross_dq_f32_kernel(const __grid_constant__ CrossParams p) {
-  extern __shared__ __align__(16) float sm[];
-  let_next_begin();
-  wait_for_previous();
+__device__ __forceinline__ void dq_block(const CrossParams& p, float* sm, int x, int h, int z) {
   float *q = sm, *g = q + kRows * Tile<DP>::kApart, *k = g + kRows * Tile<DP>::kApart,
         *v = k + kCols * Tile<DP>::kApart, *w = v + kCols * Tile<DP>::kApart;
-  const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, h = blockIdx.y;
-  const int i0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int splits = p.plan.k_splits, b = z / splits, split = z - b * splits;
+  const int i0 = x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int per = ((nk + kCols - 1) / kCols + splits - 1) / splits * kCols, j_end = min(nk, (split + 1) * per);
   const float* kp = static_cast<const float*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
@@ -239,10 +255,8 @@ __global__ void __launch_bounds__(kThreads) cross_dq_f32_kernel(const __grid_con
   clear<DP>(acc);
   float nl[4], nd[4];
   if (i0 < nq) {
-    stage<DP>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
-                 kRows, p.d);
-    stage<DP>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
-                 nq - i0, kRows, p.d);
+    stage<DP, kRows>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0, p.d, vec_rows(p, p.q_st));
+    stage<DP, kRows>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n, nq - i0, p.d, vec_rows(p, p.do_st));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long at = ((long long)b * p.Hq + h) * p.nq_pad + i0 + ty + 8 * i;
@@ -252,8 +266,8 @@ __global__ void __launch_bounds__(kThreads) cross_dq_f32_kernel(const __grid_con
   }
   for (int j0 = split * per; i0 < nq && j0 < j_end; j0 += kCols) {
     __syncthreads();
-    stage<DP>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, kCols, p.d);
-    stage<DP>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, kCols, p.d);
+    stage<DP, kCols>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, p.d, vec_rows(p, p.k_st));
+    stage<DP, kCols>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, p.d, vec_rows(p, p.v_st));
     __syncthreads();
     float s[4][4], dp[4][4];
     rows_by_rows<DP>(q, k, s);
@@ -283,17 +297,14 @@ __global__ void __launch_bounds__(kThreads) cross_dq_f32_kernel(const __grid_con
   }
 }
 
-// dK and dV. Grid: x the key tile, y key head, z batch * split of the query steps (64
-// queries of one head of the group each, heads outermost).
+// dK and dV of a key tile x and key head hk over one split of the query steps (64 queries of one head of the group
+// each, heads outermost; z: batch * split).
 template <int DP>
-__global__ void __launch_bounds__(kThreads) cross_dkdv_f32_kernel(const __grid_constant__ CrossParams p) {
-  extern __shared__ __align__(16) float sm[];
-  let_next_begin();
-  wait_for_previous();
+__device__ __forceinline__ void dkdv_block(const CrossParams& p, float* sm, int x, int hk, int z) {
   float *k = sm, *v = k + kRows * Tile<DP>::kApart, *q = v + kRows * Tile<DP>::kApart,
         *g = q + kCols * Tile<DP>::kApart, *w = g + kCols * Tile<DP>::kApart, *u = w + kRows * kPad;
-  const int splits = p.plan.q_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, hk = blockIdx.y;
-  const int j0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int splits = p.plan.q_splits, b = z / splits, split = z - b * splits;
+  const int j0 = x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int per_head = (nq + kCols - 1) / kCols, steps = per_head * p.G, per = (steps + splits - 1) / splits;
   const int s_end = min(steps, (split + 1) * per);
@@ -301,18 +312,14 @@ __global__ void __launch_bounds__(kThreads) cross_dkdv_f32_kernel(const __grid_c
   clear<DP>(dk);
   clear<DP>(dv);
   if (j0 < nk) {
-    stage<DP>(k, static_cast<const float*>(p.k) + b * p.k_st.b + (int64_t)j0 * p.k_st.n + hk * p.k_st.h, p.k_st.n, nk - j0,
-                 kRows, p.d);
-    stage<DP>(v, static_cast<const float*>(p.v) + b * p.v_st.b + (int64_t)j0 * p.v_st.n + hk * p.v_st.h, p.v_st.n, nk - j0,
-                 kRows, p.d);
+    stage<DP, kRows>(k, static_cast<const float*>(p.k) + b * p.k_st.b + (int64_t)j0 * p.k_st.n + hk * p.k_st.h, p.k_st.n, nk - j0, p.d, vec_rows(p, p.k_st));
+    stage<DP, kRows>(v, static_cast<const float*>(p.v) + b * p.v_st.b + (int64_t)j0 * p.v_st.n + hk * p.v_st.h, p.v_st.n, nk - j0, p.d, vec_rows(p, p.v_st));
   }
   for (int st = split * per; j0 < nk && st < s_end; ++st) {
     const int h = hk * p.G + st / per_head, i0 = st % per_head * kCols;
     __syncthreads();
-    stage<DP>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0,
-                 kCols, p.d);
-    stage<DP>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n,
-                 nq - i0, kCols, p.d);
+    stage<DP, kCols>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0, p.d, vec_rows(p, p.q_st));
+    stage<DP, kCols>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n, nq - i0, p.d, vec_rows(p, p.do_st));
     float nl[4], nd[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -356,32 +363,49 @@ __global__ void __launch_bounds__(kThreads) cross_dkdv_f32_kernel(const __grid_c
   }
 }
 
-constexpr int kFwd = 0, kDq = 1, kDkdv = 2;
-
-template <int DP, int kWhat>
-cudaError_t launch_t(const CrossParams& p, cudaStream_t st) {
-  constexpr int bytes = Tile<DP>::bytes(kWhat == kFwd ? kRows + 2 * kCols : 2 * kRows + 2 * kCols) +
-                        kRows * kPad * 4 * (kWhat == kDkdv ? 2 : 1);
-  constexpr auto kKernel = kWhat == kFwd  ? cross_fwd_f32_kernel<DP>
-                           : kWhat == kDq ? cross_dq_f32_kernel<DP>
-                                          : cross_dkdv_f32_kernel<DP>;
-  const cudaError_t e = allow_smem<kKernel>(bytes);
-  if (e != cudaSuccess) return e;
-  const bool keys = kWhat == kDkdv;
-  const dim3 grid(((keys ? p.Nk : p.Nq) + kRows - 1) / kRows, keys ? p.Hk : p.Hq,
-                  p.B * (keys ? p.plan.q_splits : p.plan.k_splits));
-  return launch_chained(kKernel, grid, kThreads, bytes, 1, p, st);
+// One launch for both: the blocks of dK/dV, then those of dQ.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) cross_bwd_f32_kernel(const __grid_constant__ CrossParams p) {
+  extern __shared__ __align__(16) float sm[];
+  let_next_begin();
+  wait_for_previous();
+  const int k_tiles = (p.Nk + kRows - 1) / kRows, q_tiles = (p.Nq + kRows - 1) / kRows;
+  const int kv = k_tiles * p.Hk * p.B * p.plan.q_splits;
+  const bool is_kv = (int)blockIdx.x < kv;
+  const int idx = is_kv ? blockIdx.x : blockIdx.x - kv, tiles = is_kv ? k_tiles : q_tiles, heads = is_kv ? p.Hk : p.Hq;
+  const int rest = idx / tiles, x = idx - rest * tiles, z = rest / heads, h = rest - z * heads;
+  if (is_kv)
+    dkdv_block<DP>(p, sm, x, h, z);
+  else
+    dq_block<DP>(p, sm, x, h, z);
 }
 
-template <int kWhat>
-cudaError_t launch(const CrossParams& p, cudaStream_t st) {
-  return p.d <= 64 ? launch_t<64, kWhat>(p, st) : launch_t<128, kWhat>(p, st);
+template <int DP>
+cudaError_t launch_fwd_t(const CrossParams& p, cudaStream_t st) {
+  constexpr int bytes = Tile<DP>::bytes(kRows + 2 * kCols) + kRows * kPad * 4;
+  const cudaError_t e = allow_smem<cross_fwd_f32_kernel<DP>>(bytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((p.Nq + kRows - 1) / kRows, p.Hq, p.B * p.plan.k_splits);
+  return launch_chained(cross_fwd_f32_kernel<DP>, grid, kThreads, bytes, 1, p, st);
+}
+
+template <int DP>
+cudaError_t launch_bwd_t(const CrossParams& p, cudaStream_t st) {
+  constexpr int bytes = Tile<DP>::bytes(2 * kRows + 2 * kCols) + 2 * kRows * kPad * 4;
+  const cudaError_t e = allow_smem<cross_bwd_f32_kernel<DP>>(bytes);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)((p.Nk + kRows - 1) / kRows) * p.Hk * p.B * p.plan.q_splits +
+                           (long long)((p.Nq + kRows - 1) / kRows) * p.Hq * p.B * p.plan.k_splits;
+  return launch_chained(cross_bwd_f32_kernel<DP>, dim3((unsigned)blocks), kThreads, bytes, 1, p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_cross_fwd_f32(const CrossParams& p, cudaStream_t st) { return launch<kFwd>(p, st); }
-cudaError_t launch_cross_dq_f32(const CrossParams& p, cudaStream_t st) { return launch<kDq>(p, st); }
-cudaError_t launch_cross_dkdv_f32(const CrossParams& p, cudaStream_t st) { return launch<kDkdv>(p, st); }
+cudaError_t launch_cross_fwd_f32(const CrossParams& p, cudaStream_t st) {
+  return p.d <= 64 ? launch_fwd_t<64>(p, st) : launch_fwd_t<128>(p, st);
+}
+cudaError_t launch_cross_bwd_f32(const CrossParams& p, cudaStream_t st) {
+  return p.d <= 64 ? launch_bwd_t<64>(p, st) : launch_bwd_t<128>(p, st);
+}
 
 }  // namespace fa

@@ -31,7 +31,11 @@
 // Masks. Keys from the split's end on get P = 0 by selects, so K's rows there may hold
 // anything; V's rows there are zeroed in shared memory before the MMA (0 * NaN). Rows of
 // Q that are not there give rows of S that nobody reads.
+#include <algorithm>
+
 #include "fa_cross.h"
+#include "fa_serve.h"
+#include "rope_common.cuh"
 
 namespace fa {
 
@@ -75,9 +79,9 @@ struct Cfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFast = (oAbort + 8 + 15) & ~15u;    // [exchange parity][16 softmax warps] outcomes
-  static constexpr uint32_t oNotes = oFast + 2 * 16 * 4;         // [16 softmax warps]
+  static constexpr uint32_t oNotes = oFast + 2 * 16 * 4;         // [2][16 softmax warps]
   // row maxima [tile][exchange parity][half][128 rows], then the sums [tile][half][128 rows]
-  static constexpr uint32_t oXchg = oNotes + 16 * sizeof(CrossNote);
+  static constexpr uint32_t oXchg = oNotes + 2 * 16 * sizeof(CrossNote);
   static constexpr uint32_t kSmem = oXchg + (2 * 2 * 2 + 2 * 2) * 128 * 4 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
@@ -88,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
+  let_next_begin();
   uint8_t* smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -138,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  wait_for_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -323,19 +329,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // Waits block (the hardware suspends the warp): each tile's warps idle about half the
     // time, and spinning would take issue slots from the other tile's warps.
-    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x) {
-      int blocks, left = -64 * half;  // left: this warp's real keys from the block's start on
-      bool real;                      // a real query's row: what else lies in the tile has no vote below
-      {
-        CrossUnit u;
-        cross_unit<2>(p, idx, u);
-        const CrossRows rt = cross_rows(p, u, u.first + x);
-        if (!rt.there) continue;
-        blocks = rt.live ? u.blocks : 0;
-        left += u.j_end - u.j_begin;
-        real = row_in && rt.q0 + row_q < u.nq;
-        keep_note(note, rt.q0, rt.h0, u.b, u.nq, u.split);
-      }
+    // The unit at hand and, decoded while its last block's O MMA runs, the next one: blocks of this tile (-1: the
+    // tile does not exist), this warp's real keys from the first block on, whether the lane's row is a real
+    // query's (what else lies in the tile has no vote below); the rest is noted.
+    struct {
+      int blocks, left;
+      bool real;
+    } cur, next;
+    const auto decode = [&](int idx, int slot, auto& to) {
+      CrossUnit u;
+      cross_unit<2>(p, idx, u);
+      const CrossRows rt = cross_rows(p, u, u.first + x);
+      to.blocks = !rt.there ? -1 : rt.live ? u.blocks : 0;
+      to.left = u.j_end - u.j_begin - 64 * half;
+      to.real = row_in && rt.q0 + row_q < u.nq;
+      keep_note(note + 16 * slot, rt.q0, rt.h0, u.b, u.nq, u.split);
+    };
+    int slot = 0;
+    decode(blockIdx.x, 0, cur);
+    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x, cur = next, slot ^= 1) {
+      const bool real = cur.real;
+      const int blocks = max(cur.blocks, 0), left = cur.left;
       float mref = -INFINITY, lsum = 0.f;  // lsum: this half's part of the row sum
       for (int j = 0; j < blocks; ++j, ++n) {
         if (!warp_wait<false>(bar(C::bSFull + x), n & 1, abort_flag, p.status)) {
@@ -495,6 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bPFull + x));
       }
       if (!ok) break;
+      if (idx + (int)gridDim.x < units) decode(idx + gridDim.x, slot ^ 1, next);
+      if (cur.blocks < 0) continue;
       // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time. The accumulator is released (OFree) behind its last load.
       float ltot = 0.f;
       if (blocks > 0) {
@@ -509,8 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++done;
       }
-      const int i = note->a[0] + row_q, h = note->a[1] + row_h, b = note->a[2], part = note->a[4];
-      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < note->a[3] && ltot != 0.f;  // (a NaN sum is there)
+      const volatile CrossNote* at_hand = note + 16 * slot;
+      const int i = at_hand->a[0] + row_q, h = at_hand->a[1] + row_h, b = at_hand->a[2], part = at_hand->a[4];
+      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < at_hand->a[3] && ltot != 0.f;  // (a NaN sum is there)
       const float inv = has ? 1.f / ltot : 0.f, lse2 = has ? mref + lg2(ltot) : -INFINITY;
       const long long at = ((long long)b * p.Hq + h) * p.Nq + i, rows = (long long)p.B * p.Nq * p.Hq;
       const bool parts = p.plan.k_splits > 1;
@@ -559,14 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool kBf16>
 cudaError_t launch_t(const CrossParams& p, const CUtensorMap* maps, cudaStream_t st) {
-  using C = Cfg<D>;
-  auto kern = cross_fwd_kernel<D, kBf16>;
-  const int smem = (int)(C::kSmem > kMinSmemOneCtaPerSm ? C::kSmem : kMinSmemOneCtaPerSm);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int bytes = (int)std::max(Cfg<D>::kSmem, kMinSmemOneCtaPerSm);
+  constexpr auto kKernel = cross_fwd_kernel<D, kBf16>;
+  const cudaError_t e = allow_smem<kKernel>(bytes);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.B * p.Hk * ((p.plan.q_tile.count(p.Nq, p.G) + 1) / 2) * p.plan.k_splits;
-  kern<<<(unsigned)(units < 152 ? units : 152), kThreads, smem, st>>>(p, maps[0], maps[1], maps[2]);
-  return cudaGetLastError();
+  return launch_chained_maps(kKernel, dim3((unsigned)std::min<long long>(units, 152)), kThreads, bytes, st, p, maps[0],
+                             maps[1], maps[2]);
 }
 
 }  // namespace

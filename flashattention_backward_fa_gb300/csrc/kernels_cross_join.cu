@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "fa_cross.h"
 #include "fa_serve.h"
 #include "rope_common.cuh"
@@ -226,21 +228,20 @@ __device__ __forceinline__ void join_rows(const CrossParams& p, const float* par
   }
 }
 
+// y: 0 dQ, 1 dK, 2 dV, as far as they are in splits.
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) cross_join_dq_kernel(const __grid_constant__ CrossParams p) {
+__global__ void __launch_bounds__(kJoinThreads) cross_join_bwd_kernel(const __grid_constant__ CrossParams p) {
   let_next_begin();
   wait_for_previous();
-  join_rows<T, false>(p, p.part, (long long)p.B * p.Nq * p.Hq * p.d, p.plan.k_splits, p.Nq, p.Hq, p.out, p.out_st,
-                      p.scale);
-}
-
-// y: 0 dK, 1 dV.
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) cross_join_dkdv_kernel(const __grid_constant__ CrossParams p) {
-  let_next_begin();
-  wait_for_previous();
+  if (blockIdx.y == 0) {
+    if (p.plan.k_splits > 1)
+      join_rows<T, false>(p, p.part, (long long)p.B * p.Nq * p.Hq * p.d, p.plan.k_splits, p.Nq, p.Hq, p.out, p.out_st,
+                          p.scale);
+    return;
+  }
+  if (p.plan.q_splits == 1) return;
   const long long size = (long long)p.B * p.Nk * p.Hk * p.d;
-  const bool is_v = blockIdx.y != 0;
+  const bool is_v = blockIdx.y == 2;
   join_rows<T, true>(p, p.part_kv + (is_v ? size : 0), 2 * size, p.plan.q_splits, p.Nk, p.Hk, is_v ? p.dv : p.dk,
                      is_v ? p.dv_st : p.dk_st, is_v ? 1.f : p.scale);
 }
@@ -283,18 +284,13 @@ cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t 
   return dtype == FA_BF16 ? launch_join_fwd<__nv_bfloat16>(p, st) : launch_join_fwd<__half>(p, st);
 }
 
-cudaError_t launch_cross_join_dq(const CrossParams& p, int dtype, cudaStream_t st) {
-  const dim3 grid(join_blocks(p, p.Nq, p.Hq));
-  if (dtype == FA_F32) return launch_chained(cross_join_dq_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
-  return dtype == FA_BF16 ? launch_chained(cross_join_dq_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
-                          : launch_chained(cross_join_dq_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
-}
-
-cudaError_t launch_cross_join_dkdv(const CrossParams& p, int dtype, cudaStream_t st) {
-  const dim3 grid(join_blocks(p, p.Nk, p.Hk), 2);
-  if (dtype == FA_F32) return launch_chained(cross_join_dkdv_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
-  return dtype == FA_BF16 ? launch_chained(cross_join_dkdv_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
-                          : launch_chained(cross_join_dkdv_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
+cudaError_t launch_cross_join_bwd(const CrossParams& p, int dtype, cudaStream_t st) {
+  const dim3 grid(std::max(p.plan.k_splits > 1 ? join_blocks(p, p.Nq, p.Hq) : 1,
+                           p.plan.q_splits > 1 ? join_blocks(p, p.Nk, p.Hk) : 1),
+                  3);
+  if (dtype == FA_F32) return launch_chained(cross_join_bwd_kernel<float>, grid, kJoinThreads, 0, 1, p, st);
+  return dtype == FA_BF16 ? launch_chained(cross_join_bwd_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, 1, p, st)
+                          : launch_chained(cross_join_bwd_kernel<__half>, grid, kJoinThreads, 0, 1, p, st);
 }
 
 }  // namespace fa
