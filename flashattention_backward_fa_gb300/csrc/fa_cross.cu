@@ -129,7 +129,7 @@ void bwd_plan(const fa_cross_shape* s, long long groups, long long tiles, CrossP
   c->k_splits = splits(q, 64, blocks, 8);
   const auto share = [](long long units, int n, int least) {
     const long long each = std::max(1, least / n);  // units of a block
-    return (int)std::max(div_up(units, each), std::min(units, 128ll));
+    return (int)std::max({div_up(units, each), std::min(units, 128ll), div_up(units, fa::kMostUnits)});
   };
   c->kv_blocks = share(kv * c->q_splits, (int)div_up(steps, c->q_splits), 16);
   c->q_blocks = share(q * c->k_splits, (int)div_up(blocks, c->k_splits), 8);

@@ -89,42 +89,34 @@ __device__ __forceinline__ int cross_k_len(const CrossParams& p, int b) {
   return p.k_lens ? min(max(p.k_lens[b], 0), p.Nk) : p.Nk;
 }
 
-// One (batch, key head), a split of the keys, and up to kTiles consecutive row tiles of
-// the group: what a block of the forward (two tiles) or of dQ (one) works on at a time.
+// One (batch, key head), a split of the keys, and up to two consecutive row tiles of the
+// group: what a block of the forward (two tiles) or of dQ (one) works on at a time. A
+// block's units are decoded once, side by side, into records in shared memory: the lengths
+// in memory and the divisions, about 2000 cycles, were as much as two key blocks' work
+// where every warp decoded its next unit by itself.
 struct CrossUnit {
-  int b, hk, split, nq, first;  // first: the first tile
-  int j_begin, j_end, blocks;   // keys, and their blocks of 128 (0: nothing to compute)
+  int b, hk, split, nq;
+  int j_begin, j_end, blocks;  // keys, and their blocks of 128 (0: nothing to compute)
+  int q0[2], h0[2];            // first query and head (of all heads) of a tile
+  int has;                     // bit x: tile x exists; bit 2 + x: it has a real query
+  __device__ __forceinline__ bool there(int x) const { return has >> x & 1; }
+  __device__ __forceinline__ bool live(int x) const { return has >> (2 + x) & 1; }
 };
-// A row tile of a unit.
-struct CrossRows {
-  int q0, h0;        // first query and head (of all heads)
-  bool there, live;  // the tile exists, and has a real query (where its unit has blocks)
-};
+constexpr int kMostUnits = 32;  // of a block
 
 template <int kTiles>
 __device__ __forceinline__ int cross_units(const CrossParams& p) {
   return p.B * p.Hk * ((p.plan.q_tile.count(p.Nq, p.G) + kTiles - 1) / kTiles) * p.plan.k_splits;
 }
 
-__device__ __forceinline__ CrossRows cross_rows(const CrossParams& p, const CrossUnit& u, int tile) {
-  const CrossTile& t = p.plan.q_tile;
-  const int chunks = t.chunks(p.Nq), group = tile / chunks;
-  CrossRows r;
-  r.q0 = (tile - group * chunks) << t.q_log;
-  r.h0 = u.hk * p.G + (group << t.h_log);
-  r.there = (group << t.h_log) < p.G;
-  r.live = r.there && r.q0 < u.nq;
-  return r;
-}
-
 // idx: split fastest, then the tiles of a (batch, key head), which share its keys through L2.
 template <int kTiles>
 __device__ __forceinline__ void cross_unit(const CrossParams& p, int idx, CrossUnit& u) {
-  const int sets = (p.plan.q_tile.count(p.Nq, p.G) + kTiles - 1) / kTiles;
+  const CrossTile& t = p.plan.q_tile;
+  const int sets = (t.count(p.Nq, p.G) + kTiles - 1) / kTiles, chunks = t.chunks(p.Nq);
   const int rest = idx / p.plan.k_splits;
   u.split = idx - rest * p.plan.k_splits;
-  const int bh = rest / sets;
-  u.first = (rest - bh * sets) * kTiles;
+  const int bh = rest / sets, set = rest - bh * sets;
   u.b = bh / p.Hk;
   u.hk = bh - u.b * p.Hk;
   u.nq = cross_q_len(p, u.b);
@@ -132,33 +124,21 @@ __device__ __forceinline__ void cross_unit(const CrossParams& p, int idx, CrossU
   const int nk = cross_k_len(p, u.b), per = ((nk + 127) / 128 + p.plan.k_splits - 1) / p.plan.k_splits * 128;
   u.j_begin = u.split * per;
   u.j_end = min(nk, u.j_begin + per);
-  bool any = false;
+  u.has = 0;
 #pragma unroll
-  for (int x = 0; x < kTiles; ++x) any |= cross_rows(p, u, u.first + x).live;
-  u.blocks = any ? max(u.j_end - u.j_begin + 127, 0) >> 7 : 0;
+  for (int x = 0; x < kTiles; ++x) {
+    const int tile = set * kTiles + x, group = tile / chunks;
+    u.q0[x] = (tile - group * chunks) << t.q_log;
+    u.h0[x] = u.hk * p.G + (group << t.h_log);
+    if ((group << t.h_log) < p.G) u.has |= (1 << x) | (u.q0[x] < u.nq ? 4 << x : 0);
+  }
+  u.blocks = u.has >> 2 ? max(u.j_end - u.j_begin + 127, 0) >> 7 : 0;
 }
 
 // A value that every lane of a converged warp holds alike, as one that the compiler knows to be uniform.
 // The MMA-issuing warps' loops run over units that are decoded from lengths in memory; with trip counts
 // and stages that were not known to be uniform an MMA took about 100 cycles to issue instead of 25.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-// What a row-math warp needs of its unit at the end only, kept in shared memory meanwhile (the loops have no
-// registers to spare, and decoding the unit again waits for the lengths in memory).
-struct CrossNote {
-  int a[8];
-};
-__device__ __forceinline__ void keep_note(volatile CrossNote* note, int a, int b, int c, int d, int e) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    note->a[0] = a;
-    note->a[1] = b;
-    note->a[2] = c;
-    note->a[3] = d;
-    note->a[4] = e;
-  }
-  __syncwarp();
-}
 
 // Four 16-byte pieces of a lane's row, u[0 .. 3], to the quad's four lanes: lane q of a quad gets piece q of
 // row r (of the quad's four rows) in u[r]. The stores behind it then cover 64 consecutive bytes of a row with

@@ -69,8 +69,8 @@ struct KCfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = oAbort + 8;    // [buffer][8 warps] split votes
-  static constexpr uint32_t oNotes = oFlags + 64;   // [2][16 row-math warps]
-  static constexpr uint32_t kSmem = oNotes + 2 * 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t oUnits = oFlags + 64;   // [kMostUnits]
+  static constexpr uint32_t kSmem = oUnits + kMostUnits * 40 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
@@ -78,7 +78,7 @@ struct KCfg {
 struct KUnit {
   int b, hk, split, j0, nq, nk;
   int first, steps;  // steps first .. first + steps - 1 of the sequence's live ones (0: nothing to compute)
-  int chunks;        // live chunks of a head's queries
+  int chunks, chunk;  // live chunks of a head's queries, the first step's
 };
 
 __device__ __forceinline__ int k_units(const CrossParams& p) {
@@ -100,6 +100,7 @@ __device__ __forceinline__ void k_unit(const CrossParams& p, int idx, KUnit& u) 
   const int total = u.chunks * (p.G >> p.plan.step.h_log), per = (total + p.plan.q_splits - 1) / p.plan.q_splits;
   u.first = u.split * per;
   u.steps = u.j0 < u.nk ? max(min(per, total - u.first), 0) : 0;
+  u.chunk = u.first % max(u.chunks, 1);
 }
 
 // Head (of all) and first query of a live step.
@@ -134,15 +135,13 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
   volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
-  const int units = k_units(p);
+  const int mine = (k_units(p) - first + stride - 1) / stride;  // units of this block
+  KUnit* const unit = reinterpret_cast<KUnit*>(smem + C::oUnits);
   const int rows = 1 << (p.plan.step.q_log + p.plan.step.h_log);
-  // The first unit from idx on in this CTA's stride that has steps; -1: none.
-  auto next_work = [&](int idx, KUnit& u) -> int {
-    for (; idx < units; idx += stride) {
-      k_unit(p, idx, u);
-      if (u.steps > 0) return idx;
-    }
-    return -1;
+  // The first unit from the i-th on that has steps (mine: none).
+  const auto next_work = [&](int i) {
+    while (i < mine && unit[i].steps == 0) ++i;
+    return i;
   };
 
   if (threadIdx.x == 0) {
@@ -182,6 +181,11 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
     fence_proxy_async_smem();
   }
   wait_for_previous();
+  if ((int)threadIdx.x < mine) {
+    KUnit u;
+    k_unit(p, first + threadIdx.x * stride, u);
+    unit[threadIdx.x] = u;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -194,11 +198,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       const uint32_t q_bytes = (uint32_t)(2 * C::kPanels * 128 + 2 * 4) * rows;
       int kl = 0, G = 0;  // units and steps loaded
       bool ok = true;
-      KUnit u, next;
-      int after = next_work(first, next);
-      for (int idx = after; ok && idx >= 0; idx = after) {
-        u = next;
-        after = next_work(idx + stride, next);
+      for (int i = next_work(0); ok && i < mine; i = next_work(i + 1)) {
+        const KUnit& u = unit[i];
         // K and V of this unit, once the previous unit's last reads of them are done
         if (kl > 0 && !mbar_wait(bar(C::bKVFree), (kl - 1) & 1, abort_flag, p.status)) break;
         mbar_arrive_expect_tx(bar(C::bKV), 2 * C::kKVTile);
@@ -246,14 +247,11 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
     const int bF = isS ? C::bSFull : C::bDPFull, bE = isS ? C::bSEmpty : C::bDPEmpty;
     int kl = 0, G = 0;
     bool ok = true;
-    KUnit u, next;
-    int after = next_work(first, next);
-    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
-      u = next;
-      u.steps = uniform(u.steps);
-      after = next_work(idx + stride, next);
+    for (int i = next_work(0); ok && i < mine; i = next_work(i + 1), ++kl) {
+      i = uniform(i);
+      const int steps = uniform(unit[i].steps);
       ok = warp_wait<kIssuerPoll>(bar(C::bKV), kl & 1, abort_flag, p.status);
-      for (int it = 0; ok && it < u.steps; ++it, ++G) {
+      for (int it = 0; ok && it < steps; ++it, ++G) {
         const int s = G % C::kNS, bb = G & 1;
         if (!warp_wait<kIssuerPoll>(bar(C::bQFull + s), (G / C::kNS) & 1, abort_flag, p.status) ||
             !warp_wait<kIssuerPoll>(bar(bE + bb), ((G >> 1) & 1) ^ 1, abort_flag, p.status)) {
@@ -282,14 +280,11 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
     const uint64_t mQ0 = make_sdesc(sb + C::oQ, C::kQPanel, 1024), mO0 = make_sdesc(sb + C::oDO, C::kQPanel, 1024);
     int kl = 0, G = 0;
     bool ok = true;
-    KUnit u, next;
-    int after = next_work(first, next);
-    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
-      u = next;
-      u.steps = uniform(u.steps);
-      int chunk = u.first % u.chunks;  // of a head's queries
-      after = next_work(idx + stride, next);
-      for (int it = 0; it < u.steps; ++it, ++G) {
+    for (int i = next_work(0); ok && i < mine; i = next_work(i + 1), ++kl) {
+      i = uniform(i);
+      const int steps = uniform(unit[i].steps), chunks = uniform(unit[i].chunks), nq = uniform(unit[i].nq);
+      int chunk = uniform(unit[i].chunk);
+      for (int it = 0; it < steps; ++it, ++G) {
         const int bt = G & 1, st = G % C::kNS;
         if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
             // a unit's first MMAs overwrite the accumulators that the previous unit's epilogue reads
@@ -299,10 +294,10 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
         }
         // Rows of queries past the sequence's end, as far as they are the tensors' (past them: zeros by
         // TMA). S^T is formed; dP^T may still read dO: its columns of these rows are not used.
-        if (++chunk == u.chunks) {
+        if (++chunk == chunks) {
           chunk = 0;
-          const int q0 = (u.chunks - 1) << p.plan.step.q_log, q = p.plan.step.queries();
-          const int from = u.nq - q0, to = min(q, p.Nq - q0);
+          const int q0 = (chunks - 1) << p.plan.step.q_log, q = p.plan.step.queries();
+          const int from = nq - q0, to = min(q, p.Nq - q0);
           for (int h = 0; from < to && h < p.plan.step.heads(); ++h) {
             zero_rows<C::kPanels>(sb + C::oQ + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
             zero_rows<C::kPanels>(sb + C::oDO + st * C::kQTile, C::kQPanel, h * q + from, h * q + to);
@@ -360,36 +355,19 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tSc = tS + lane_off + 64 * bb + 32 * c, tdPc = tdP + lane_off + 64 * bb + 32 * c;
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-    volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 4);
     int kl = 0, G = 0;
     bool ok = true;
-    // The unit at hand and, decoded before its epilogue, the next one: steps, chunks of a head's queries, the first
-    // step's chunk, the columns with real queries of any step but a head's last (or last few heads') and of that
-    // one, and whether the lane has a real key. The rest is noted. (A lane without one needs no mask: its row of
-    // P^T and dS^T reaches nothing but its own row of dV and dK, which the epilogue drops. It has no vote.)
-    struct {
-      int steps, chunks, first;
-      uint32_t full, tail;
-      bool real;
-    } cur, next;
-    const auto decode = [&](int idx, int slot, auto& to) {
-      KUnit u;
-      k_unit(p, idx, u);
-      to.steps = u.steps;
-      to.chunks = max(u.chunks, 1);
-      to.first = u.first % to.chunks;
-      to.full = step_columns(p.plan.step, c, kStep);
-      to.tail = step_columns(p.plan.step, c, u.nq - ((to.chunks - 1) << p.plan.step.q_log));
-      to.real = u.j0 + jl < u.nk;
-      keep_note(note + 16 * slot, u.b, u.hk, u.j0, u.nk, u.split);
-    };
-    int slot = 0;
-    decode(first, 0, cur);
-    for (int idx = first; ok && idx < units; idx += stride, cur = next, slot ^= 1) {
-      const int steps = cur.steps, chunks = cur.chunks;
-      const uint32_t full = cur.full, tail = cur.tail;
-      int chunk = cur.first + ((bb ^ G) & 1);
+    for (int ui = 0; ok && ui < mine; ++ui) {
+      const KUnit& u = unit[ui];
+      const int steps = u.steps, chunks = max(u.chunks, 1);
+      int chunk = u.chunk + ((bb ^ G) & 1);
       chunk -= chunk >= chunks ? chunks : 0;
+      // The columns with real queries of any step but a head's last (or last few heads') and of that one, and whether
+      // the lane has a real key. (A lane without one needs no mask: its row of P^T and dS^T reaches nothing but its
+      // own row of dV and dK, which the epilogue drops. It has no vote.)
+      const uint32_t full = step_columns(p.plan.step, c, kStep);
+      const uint32_t tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
+      const bool real = u.j0 + jl < u.nk;
       for (int it = (bb ^ G) & 1; it < steps; it += 2) {
         const int gs = G + it, s = gs % C::kNS;
         const uint32_t allow = chunk == chunks - 1 ? tail : full;
@@ -441,7 +419,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           uint32_t hp[8], ep[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
-          split_h[hh] = __any_sync(0xFFFFFFFFu, cur.real && cmax > kCrossSplit);
+          split_h[hh] = __any_sync(0xFFFFFFFFu, real && cmax > kCrossSplit);
           if (split_h[hh]) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
@@ -504,7 +482,6 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
         warp_arrive(bar(C::bDSFull + bb));
       }
       if (!ok) break;
-      if (idx + stride < units) decode(idx + stride, slot ^ 1, next);
       // Epilogue, by the pair that ran the unit's last step: dV, then dK, each warpgroup half of the
       // columns; both accumulators are released (AccFree) behind the last load.
       const bool epi = steps > 0 ? bb == ((G + steps - 1) & 1) : bb == 0;
@@ -516,8 +493,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           }
           tc_fence_after();
         }
-        const volatile CrossNote* at_hand = note + 16 * slot;
-        const int b = at_hand->a[0], hk = at_hand->a[1], j = at_hand->a[2] + jl, nk = at_hand->a[3];
+        const int b = u.b, hk = u.hk, j = u.j0 + jl, nk = u.nk;
         const long long size = (long long)p.B * p.Nk * p.Hk * D;
         const bool parts = p.plan.q_splits > 1;
 #pragma unroll 1
@@ -538,7 +514,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           }
 #pragma unroll
           for (int x = 0; x < 32; ++x) r[x] = j < nk ? r[x] : 0u;  // (0 * NaN of a real query's)
-          float* to_part = parts && j < nk ? p.part_kv + 2 * at_hand->a[4] * size + (isK ? 0 : size) +
+          float* to_part = parts && j < nk ? p.part_kv + 2 * u.split * size + (isK ? 0 : size) +
                                                  (((long long)b * p.Nk + j) * p.Hk + hk) * D + col
                                            : nullptr;
           const fa_strides& st = isK ? p.dk_st : p.dv_st;
@@ -593,8 +569,8 @@ struct QCfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [buffer][16 warps] split votes
-  static constexpr uint32_t oNotes = oFlags + 2 * 16 * 4;        // [2][16 row-math warps]
-  static constexpr uint32_t kSmem = oNotes + 2 * 16 * sizeof(CrossNote) + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t oUnits = oFlags + 2 * 16 * 4;        // [kMostUnits]
+  static constexpr uint32_t kSmem = oUnits + kMostUnits * sizeof(CrossUnit) + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
@@ -608,13 +584,11 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
   volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
-  const int units = cross_units<1>(p);
-  auto next_work = [&](int idx, CrossUnit& u) -> int {
-    for (; idx < units; idx += stride) {
-      cross_unit<1>(p, idx, u);
-      if (u.blocks > 0) return idx;
-    }
-    return -1;
+  const int mine = (cross_units<1>(p) - first + stride - 1) / stride;  // units of this block
+  CrossUnit* const unit = reinterpret_cast<CrossUnit*>(smem + C::oUnits);
+  const auto next_work = [&](int i) {
+    while (i < mine && unit[i].blocks == 0) ++i;
+    return i;
   };
 
   if (threadIdx.x == 0) {
@@ -651,6 +625,11 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     prefetch_tmap(&tmDO);
   }
   wait_for_previous();
+  if ((int)threadIdx.x < mine) {
+    CrossUnit u;
+    cross_unit<1>(p, first + threadIdx.x * stride, u);
+    unit[threadIdx.x] = u;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -663,17 +642,13 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
       const uint32_t q_bytes = 2u * C::kPanels * 128u << (p.plan.q_tile.q_log + p.plan.q_tile.h_log);
       int kl = 0, G = 0, issuedV = 0, issuedK = 0;
       bool ok = true;
-      CrossUnit u, next;
-      int after = next_work(first, next);
-      for (int idx = after; ok && idx >= 0; idx = after) {
-        u = next;
-        after = next_work(idx + stride, next);
+      for (int i = next_work(0); ok && i < mine; i = next_work(i + 1)) {
+        const CrossUnit& u = unit[i];
         if (kl > 0 && !mbar_wait(bar(C::bResFree), (kl - 1) & 1, abort_flag, p.status)) break;
-        const CrossRows r = cross_rows(p, u, u.first);
         mbar_arrive_expect_tx(bar(C::bRes), q_bytes);
         for (int pn = 0; pn < C::kPanels; ++pn) {
-          tma_load_4d(sb + C::oQ + pn * C::kPanel, &tmQ, bar(C::bRes), 64 * pn, r.q0, r.h0, u.b);
-          tma_load_4d(sb + C::oDO + pn * C::kPanel, &tmDO, bar(C::bRes), 64 * pn, r.q0, r.h0, u.b);
+          tma_load_4d(sb + C::oQ + pn * C::kPanel, &tmQ, bar(C::bRes), 64 * pn, u.q0[0], u.h0[0], u.b);
+          tma_load_4d(sb + C::oDO + pn * C::kPanel, &tmDO, bar(C::bRes), 64 * pn, u.q0[0], u.h0[0], u.b);
         }
         ++kl;
         for (int it = 0; it < u.blocks; ++it, ++G) {
@@ -712,14 +687,11 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
                    dB0 = make_sdesc(sb + (isS ? C::oK : C::oV), 16, 1024);
     int kl = 0, G = 0;
     bool ok = true;
-    CrossUnit u, next;
-    int after = next_work(first, next);
-    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
-      u = next;
-      u.blocks = uniform(u.blocks);
-      after = next_work(idx + stride, next);
+    for (int i = next_work(0); ok && i < mine; i = next_work(i + 1), ++kl) {
+      i = uniform(i);
+      const int blocks = uniform(unit[i].blocks);
       ok = warp_wait<kIssuerPoll>(bar(C::bRes), kl & 1, abort_flag, p.status);
-      for (int it = 0; ok && it < u.blocks; ++it, ++G) {
+      for (int it = 0; ok && it < blocks; ++it, ++G) {
         const int bb = G & 1, st = isS ? G % C::kNK : G % C::kNV;
         const bool landed = isS ? warp_wait<kIssuerPoll>(bar(C::bKFull + st), (G / C::kNK) & 1, abort_flag, p.status)
                                 : warp_wait<kIssuerPoll>(bar(C::bVFull + st), (G / C::kNV) & 1, abort_flag, p.status);
@@ -752,15 +724,11 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     const uint64_t b0 = make_sdesc(sb + C::oK, C::kPanel, 1024);
     int kl = 0, G = 0;
     bool ok = true;
-    CrossUnit u, next;
-    int after = next_work(first, next);
-    for (int idx = uniform(after); ok && idx >= 0; idx = uniform(after), ++kl) {
-      u = next;
-      u.blocks = uniform(u.blocks);
-      after = next_work(idx + stride, next);
-      u.j_begin = uniform(u.j_begin);
-      u.j_end = uniform(u.j_end);
-      for (int it = 0; it < u.blocks; ++it, ++G) {
+    for (int i = next_work(0); ok && i < mine; i = next_work(i + 1), ++kl) {
+      i = uniform(i);
+      const int blocks = uniform(unit[i].blocks);
+      const int j_begin = uniform(unit[i].j_begin), j_end = uniform(unit[i].j_end);
+      for (int it = 0; it < blocks; ++it, ++G) {
         const int bt = G & 1, sk = G % C::kNK;
         if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
             (it == 0 && kl > 0 && !warp_wait<kConsumerPoll>(bar(C::bAccFree), (kl - 1) & 1, abort_flag, p.status))) {
@@ -768,7 +736,7 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
           break;
         }
         // K's rows from the sequence's end on, as far as they are the tensor's (S, which read them, is formed)
-        const int from = u.j_end - u.j_begin - 128 * it, to = min(128, p.Nk - u.j_begin - 128 * it);
+        const int from = j_end - j_begin - 128 * it, to = min(128, p.Nk - j_begin - 128 * it);
         if (from < to) zero_rows<C::kPanels>(sb + C::oK + sk * C::kTile, C::kPanel, from, to);
         tc_fence_after();
         const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 16 * bt);
@@ -804,35 +772,24 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
     const bool row_in = row_h < p.plan.q_tile.heads();
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-    volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 4);
     int kl = 0, G = 0;
     bool ok = true;
-    // The unit at hand and, decoded before its epilogue, the next one: blocks, real keys from this warpgroup's first
-    // column on, the row's -L and -D (-inf and 0 past the sequence). The rest is noted.
-    struct {
-      int blocks, left;
-      float nL2, nD;
-    } cur, next;
-    const auto decode = [&](int idx, int slot, auto& to) {
-      CrossUnit u;
-      cross_unit<1>(p, idx, u);
-      const CrossRows rt = cross_rows(p, u, u.first);
-      to.blocks = u.blocks;
-      to.left = u.j_end - u.j_begin - 32 * c;
-      to.nL2 = -INFINITY;
-      to.nD = 0.f;
-      if (u.blocks > 0 && row_in) {
-        const long long at = ((long long)u.b * p.Hq + rt.h0 + row_h) * p.nq_pad + rt.q0 + row_q;
-        to.nL2 = p.nL2[at];
-        to.nD = p.nD[at];
+    // The next unit's -L and -D of this row (-inf and 0 past the sequence) are on their way while one is worked on.
+    const auto row_of = [&](int ui, float& nl, float& nd) {
+      nl = -INFINITY;
+      nd = 0.f;
+      if (ui < mine && unit[ui].blocks > 0 && row_in) {
+        const long long at = ((long long)unit[ui].b * p.Hq + unit[ui].h0[0] + row_h) * p.nq_pad + unit[ui].q0[0] + row_q;
+        nl = p.nL2[at];
+        nd = p.nD[at];
       }
-      keep_note(note + 16 * slot, rt.q0, rt.h0, u.b, u.nq, u.split);
     };
-    int slot = 0;
-    decode(first, 0, cur);
-    for (int idx = first; ok && idx < units; idx += stride, cur = next, slot ^= 1) {
-      const int blocks = cur.blocks, left = cur.left;
-      const float nL2 = cur.nL2, nD = cur.nD;
+    float nL2, nD, nL2_next, nD_next;
+    row_of(0, nL2, nD);
+    for (int ui = 0; ok && ui < mine; ++ui, nL2 = nL2_next, nD = nD_next) {
+      const CrossUnit& u = unit[ui];
+      const int blocks = u.blocks, left = u.j_end - u.j_begin - 32 * c;  // real keys from this warpgroup's first column on
+      row_of(ui + 1, nL2_next, nD_next);
       const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
       for (int it = 0; it < blocks; ++it) {
         const int gs = G + it, bb = gs & 1;
@@ -907,7 +864,6 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         warp_arrive(bar(C::bPFull + bb));
       }
       if (!ok) break;
-      if (idx + stride < units) decode(idx + stride, slot ^ 1, next);
       // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
       // (AccFree) before the stores, so the next unit's first MMA can start meanwhile.
       uint32_t r[32];  // (D / 4 of them)
@@ -934,12 +890,11 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         warp_arrive(bar(C::bAccFree));
         ++kl;
       }
-      const volatile CrossNote* at_hand = note + 16 * slot;
-      const int i = at_hand->a[0] + row_q, h = at_hand->a[1] + row_h, b = at_hand->a[2], nq = at_hand->a[3];
+      const int i = u.q0[0] + row_q, h = u.h0[0] + row_h, b = u.b, nq = u.nq;
       const bool parts = p.plan.k_splits > 1, in = row_in && i < (parts ? nq : p.Nq);
 #pragma unroll
       for (int x = 0; x < 32; ++x) r[x] = i < nq ? r[x] : 0u;  // (rows that are not there may hold NaN)
-      float* to_part = parts && in ? p.part + ((((long long)at_hand->a[4] * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
+      float* to_part = parts && in ? p.part + ((((long long)u.split * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
                                    : nullptr;
       uint16_t* to_out = !parts && in ? static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h +
                                             c * (D / 4)

@@ -79,9 +79,9 @@ struct Cfg {
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFast = (oAbort + 8 + 15) & ~15u;    // [exchange parity][16 softmax warps] outcomes
-  static constexpr uint32_t oNotes = oFast + 2 * 16 * 4;         // [2][16 softmax warps]
+  static constexpr uint32_t oUnits = oFast + 2 * 16 * 4;         // [kMostUnits]
   // row maxima [tile][exchange parity][half][128 rows], then the sums [tile][half][128 rows]
-  static constexpr uint32_t oXchg = oNotes + 2 * 16 * sizeof(CrossNote);
+  static constexpr uint32_t oXchg = oUnits + kMostUnits * sizeof(CrossUnit);
   static constexpr uint32_t kSmem = oXchg + (2 * 2 * 2 + 2 * 2) * 128 * 4 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
@@ -98,14 +98,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
-  const int units = cross_units<2>(p);
-  // The first unit from idx on in this CTA's stride that has blocks to compute; -1: none.
-  auto next_work = [&](int idx, CrossUnit& u) -> int {
-    for (; idx < units; idx += gridDim.x) {
-      cross_unit<2>(p, idx, u);
-      if (u.blocks > 0) return idx;
-    }
-    return -1;
+  const int mine = (cross_units<2>(p) - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // units of this block
+  CrossUnit* const unit = reinterpret_cast<CrossUnit*>(smem + C::oUnits);
+  // The first from the i-th on that has blocks to compute (mine: none).
+  const auto next_work = [&](int i) {
+    while (i < mine && unit[i].blocks == 0) ++i;
+    return i;
   };
 
   if (threadIdx.x == 0) {
@@ -144,6 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmV);
   }
   wait_for_previous();
+  if ((int)threadIdx.x < mine) {
+    CrossUnit u;
+    cross_unit<2>(p, blockIdx.x + threadIdx.x * gridDim.x, u);
+    unit[threadIdx.x] = u;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -155,19 +158,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = (uint32_t)C::kPanels * 128u << (p.plan.q_tile.q_log + p.plan.q_tile.h_log);
       int t = 0, nq[2] = {0, 0}, issuedK = 0, issuedV = 0;  // blocks and tiles loaded
       bool ok = true;
-      CrossUnit u;
-      for (int idx = next_work(blockIdx.x, u); ok && idx >= 0; idx = next_work(idx + gridDim.x, u)) {
+      for (int i = next_work(0); ok && i < mine; i = next_work(i + 1)) {
+        const CrossUnit& u = unit[i];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const CrossRows r = cross_rows(p, u, u.first + x);
-          if (!ok || !r.live) continue;
+          if (!ok || !u.live(x)) continue;
           if (nq[x] > 0 && !mbar_wait(bar(C::bQFree + x), (nq[x] - 1) & 1, abort_flag, p.status)) {
             ok = false;
             continue;
           }
           mbar_arrive_expect_tx(bar(C::bQ + x), q_bytes);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(sb + C::oQ + x * C::kTile + pn * C::kPanel, &tmQ, bar(C::bQ + x), 64 * pn, r.q0, r.h0, u.b);
+            tma_load_4d(sb + C::oQ + x * C::kTile + pn * C::kPanel, &tmQ, bar(C::bQ + x), 64 * pn, u.q0[x], u.h0[x], u.b);
           ++nq[x];
         }
         for (int j = 0; ok && j < u.blocks; ++j, ++t) {
@@ -229,22 +231,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_mma_ts_w(tO, tP + 64 * (k >> 2) + 8 * (k & 3), desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
       tc_commit_w(bar(C::bODone + x));
     };
-    CrossUnit u, next;
-    bool live[2] = {false, false}, live_next[2];  // the unit's tiles, and the next unit's
-    int idx = next_work(blockIdx.x, u), t = 0;
-    const auto known = [&](int& i, CrossUnit& w) {
-      i = uniform(i);
-      w.blocks = uniform(w.blocks);
-      w.j_begin = uniform(w.j_begin);
-      w.j_end = uniform(w.j_end);
+    struct {
+      int i, blocks, j_begin, j_end;
+      bool live[2];
+    } u, next;  // the unit at hand and the next one (i = mine: none)
+    const auto read = [&](int i, auto& to) {
+      to.i = uniform(next_work(i));
+      const CrossUnit& from = unit[min(to.i, mine - 1)];
+      to.blocks = uniform(from.blocks);
+      to.j_begin = uniform(from.j_begin);
+      to.j_end = uniform(from.j_end);
+      const int has = uniform(from.has);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) to.live[x] = to.i < mine && (has >> (2 + x) & 1);
     };
-    known(idx, u);
-    if (idx >= 0) {
+    int t = 0;
+    read(0, u);
+    if (u.i < mine) {
       ok = warp_wait<kIssuerPoll>(bar(C::bKFull), 0, abort_flag, p.status);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        live[x] = uniform(cross_rows(p, u, u.first + x).live);
-        if (!ok || !live[x]) continue;
+        if (!ok || !u.live[x]) continue;
         ok = warp_wait<kIssuerPoll>(bar(C::bQ + x), 0, abort_flag, p.status);
         if (!ok) continue;
         tc_fence_after();
@@ -252,14 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) tc_commit_w(bar(C::bKEmpty));
     }
-    while (ok && idx >= 0) {
-      int after = next_work(idx + gridDim.x, next);
-      known(after, next);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) live_next[x] = uniform(after >= 0 && cross_rows(p, next, next.first + x).live);
+    while (ok && u.i < mine) {
+      read(u.i + 1, next);
       for (int j = 0; ok && j < u.blocks; ++j, ++t) {
         const int sv = t % C::kNV;
-        const bool inside = j + 1 < u.blocks, more = inside || after >= 0;
+        const bool inside = j + 1 < u.blocks, more = inside || next.i < mine;
         if (!warp_wait<kIssuerPoll>(bar(C::bVFull + sv), (t / C::kNV) & 1, abort_flag, p.status) ||
             (more && !warp_wait<kIssuerPoll>(bar(C::bKFull + (t + 1) % C::kNK), ((t + 1) / C::kNK) & 1, abort_flag,
                                              p.status))) {
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok) continue;
-          if (live[x]) {
+          if (u.live[x]) {
             if (!warp_wait<kIssuerPoll>(bar(C::bPFull + x), steps[x] & 1, abort_flag, p.status) ||
                 (j == 0 && tiles[x] > 0 &&
                  !warp_wait<kIssuerPoll>(bar(C::bOFree + x), (tiles[x] - 1) & 1, abort_flag, p.status))) {
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++steps[x];
             if (!inside) ++tiles[x];
           }
-          if (inside ? live[x] : live_next[x]) {
+          if (inside ? u.live[x] : next.live[x]) {
             if (!inside && !warp_wait<kIssuerPoll>(bar(C::bQ + x), tiles[x] & 1, abort_flag, p.status)) {
               ok = false;
               continue;
@@ -298,9 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) tc_commit_w(bar(C::bKEmpty + (t + 1) % C::kNK));  // the next K read by both S MMAs
       }
       u = next;
-      idx = after;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) live[x] = live_next[x];
     }
     // Every MMA this warp issued is complete before the CTA frees TMEM and exits.
     tc_commit_w(bar(C::bDrain));
@@ -322,34 +323,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c2 = p.scale_log2;
     const int row_q = il & (p.plan.q_tile.queries() - 1), row_h = il >> p.plan.q_tile.q_log;
     const bool row_in = row_h < p.plan.q_tile.heads();
-    volatile CrossNote* note = reinterpret_cast<volatile CrossNote*>(smem + C::oNotes) + (warp - 2);
     volatile int* fast = reinterpret_cast<volatile int*>(smem + C::oFast);
     int nx = 0, nf = 0;   // exchanges of maxima and of outcomes so far
     int n = 0, done = 0;  // blocks and units this tile has been through
     bool ok = true;
     // Waits block (the hardware suspends the warp): each tile's warps idle about half the
     // time, and spinning would take issue slots from the other tile's warps.
-    // The unit at hand and, decoded while its last block's O MMA runs, the next one: blocks of this tile (-1: the
-    // tile does not exist), this warp's real keys from the first block on, whether the lane's row is a real
-    // query's (what else lies in the tile has no vote below); the rest is noted.
-    struct {
-      int blocks, left;
-      bool real;
-    } cur, next;
-    const auto decode = [&](int idx, int slot, auto& to) {
-      CrossUnit u;
-      cross_unit<2>(p, idx, u);
-      const CrossRows rt = cross_rows(p, u, u.first + x);
-      to.blocks = !rt.there ? -1 : rt.live ? u.blocks : 0;
-      to.left = u.j_end - u.j_begin - 64 * half;
-      to.real = row_in && rt.q0 + row_q < u.nq;
-      keep_note(note + 16 * slot, rt.q0, rt.h0, u.b, u.nq, u.split);
-    };
-    int slot = 0;
-    decode(blockIdx.x, 0, cur);
-    for (int idx = blockIdx.x; ok && idx < units; idx += gridDim.x, cur = next, slot ^= 1) {
-      const bool real = cur.real;
-      const int blocks = max(cur.blocks, 0), left = cur.left;
+    for (int ui = 0; ok && ui < mine; ++ui) {
+      const CrossUnit& u = unit[ui];
+      if (!u.there(x)) continue;
+      // this warp's real keys from the first block on; a real query's row: what else lies in the tile has no vote
+      const int blocks = u.live(x) ? u.blocks : 0, left = u.j_end - u.j_begin - 64 * half;
+      const bool real = row_in && u.q0[x] + row_q < u.nq;
       float mref = -INFINITY, lsum = 0.f;  // lsum: this half's part of the row sum
       for (int j = 0; j < blocks; ++j, ++n) {
         if (!warp_wait<false>(bar(C::bSFull + x), n & 1, abort_flag, p.status)) {
@@ -358,11 +343,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const int hi = left - 128 * j;  // columns 0 .. hi - 1
-        // One pass with the reference as it stands, which it nearly always does after a row's first block:
-        // P, its sum and its image are kept in registers until both warps of the rows say that no row's
-        // maximum asks for a new reference. The two passes below (maximum, exchange, P) run otherwise.
+        // A row's first reference is the maximum of its first 16 scores, which both of its warps read.
+        if (j == 0) {
+          uint32_t cur[16];
+          const int in = hi + 64 * half;
+          tmem_ld16(tS - 64 * half, cur);
+          tmem_ld_wait16(cur);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mref = e < in ? fmaxf(mref, __uint_as_float(cur[e])) : mref;
+          mref *= c2;
+        }
+        // One pass with the reference as it stands, which it nearly always does: P, its sum and its image are
+        // kept in registers until both warps of the rows say that no row's maximum asks for a new reference.
+        // The two passes below (maximum, exchange, P) run otherwise.
         uint32_t img[32];
-        if (j > 0) {
+        {
           const float base = mref == -INFINITY ? 0.f : mref;
           const uint64_t cc2 = f2_pack(c2, c2), nm2 = f2_pack(-base, -base);
           float top = -INFINITY;
@@ -509,8 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bPFull + x));
       }
       if (!ok) break;
-      if (idx + (int)gridDim.x < units) decode(idx + gridDim.x, slot ^ 1, next);
-      if (cur.blocks < 0) continue;
       // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time. The accumulator is released (OFree) behind its last load.
       float ltot = 0.f;
       if (blocks > 0) {
@@ -525,9 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++done;
       }
-      const volatile CrossNote* at_hand = note + 16 * slot;
-      const int i = at_hand->a[0] + row_q, h = at_hand->a[1] + row_h, b = at_hand->a[2], part = at_hand->a[4];
-      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < at_hand->a[3] && ltot != 0.f;  // (a NaN sum is there)
+      const int i = u.q0[x] + row_q, h = u.h0[x] + row_h, b = u.b, part = u.split;
+      const bool in = row_in && i < p.Nq, has = blocks > 0 && i < u.nq && ltot != 0.f;  // (a NaN sum is there)
       const float inv = has ? 1.f / ltot : 0.f, lse2 = has ? mref + lg2(ltot) : -INFINITY;
       const long long at = ((long long)b * p.Hq + h) * p.Nq + i, rows = (long long)p.B * p.Nq * p.Hq;
       const bool parts = p.plan.k_splits > 1;
@@ -581,7 +573,8 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap* maps, cudaStream_t
   const cudaError_t e = allow_smem<kKernel>(bytes);
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.B * p.Hk * ((p.plan.q_tile.count(p.Nq, p.G) + 1) / 2) * p.plan.k_splits;
-  return launch_chained_maps(kKernel, dim3((unsigned)std::min<long long>(units, 152)), kThreads, bytes, st, p, maps[0],
+  const long long blocks = std::max(std::min(units, 152ll), (units + kMostUnits - 1) / kMostUnits);
+  return launch_chained_maps(kKernel, dim3((unsigned)blocks), kThreads, bytes, st, p, maps[0],
                              maps[1], maps[2]);
 }
 
