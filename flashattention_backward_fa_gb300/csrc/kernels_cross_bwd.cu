@@ -61,8 +61,11 @@ struct KCfg {
   static constexpr int bDPEmpty = bSEmpty + 2;      // [2] dK done with the dS^T image
   static constexpr int bPFull = bDPEmpty + 2;       // [2] P^T image written
   static constexpr int bDSFull = bPFull + 2;        // [2] dS^T image written
-  static constexpr int bAcc = bDSFull + 2;          // a unit's dV, dK complete in TMEM
-  static constexpr int bDrain = bAcc + 1;           // one per MMA-issuing warp
+  // [2] a unit's dV, dK complete in TMEM: a barrier for each pair of row-math warpgroups, which waits for the units
+  // whose epilogue it writes (on one barrier for both, a pair that skips the other's units could take the
+  // phase before last for the one that it waits for)
+  static constexpr int bAcc = bDSFull + 2;
+  static constexpr int bDrain = bAcc + 2;           // one per MMA-issuing warp
   static constexpr int bKVFree = bDrain + 3;        // a unit's last reads of K, V done
   static constexpr int bAccFree = bKVFree + 1;      // the epilogue has read dV, dK
   static constexpr int kBars = bAccFree + 1;
@@ -157,9 +160,9 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       mbar_init(bar(C::bDPEmpty + x), 1);
       mbar_init(bar(C::bPFull + x), 256);   // two warpgroups
       mbar_init(bar(C::bDSFull + x), 256);
+      mbar_init(bar(C::bAcc + x), 1);
     }
     for (int x = 0; x < 3; ++x) mbar_init(bar(C::bDrain + x), 1);
-    mbar_init(bar(C::bAcc), 1);
     mbar_init(bar(C::bKVFree), 2);          // S^T and dP^T issuers
     mbar_init(bar(C::bAccFree), 8 * 32);    // the epilogue pair's row-math warps
     *abort_flag = 0;
@@ -339,7 +342,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
         tc_commit_w(bar(C::bQEmpty + st));
       }
       if (!ok) break;
-      tc_commit_w(bar(C::bAcc));
+      tc_commit_w(bar(C::bAcc + ((G - 1) & 1)));  // (the pair that ran the last step)
     }
     tc_commit_w(bar(C::bDrain + 1));
     if (lane == 0) mbar_wait_drain(bar(C::bDrain + 1), 0, p.status);
@@ -355,7 +358,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tSc = tS + lane_off + 64 * bb + 32 * c, tdPc = tdP + lane_off + 64 * bb + 32 * c;
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-    int kl = 0, G = 0;
+    int written = 0, G = 0;  // units whose epilogue this pair wrote, steps of all units
     bool ok = true;
     for (int ui = 0; ok && ui < mine; ++ui) {
       const KUnit& u = unit[ui];
@@ -487,11 +490,12 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       const bool epi = steps > 0 ? bb == ((G + steps - 1) & 1) : bb == 0;
       if (epi) {
         if (steps > 0) {
-          if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
+          if (!warp_wait<kRowMathPoll>(bar(C::bAcc + bb), written & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          ++written;
         }
         const int b = u.b, hk = u.hk, j = u.j0 + jl, nk = u.nk;
         const long long size = (long long)p.B * p.Nk * p.Hk * D;
@@ -525,7 +529,6 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
         }
         __syncwarp();
       }
-      if (steps > 0) ++kl;
       G += steps;
     }
   }

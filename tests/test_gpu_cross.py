@@ -55,10 +55,21 @@ def test_sizes(size, dtype):
     ((8, 520, 300, 16, 8, 64), None, None),
     ((9, 300, 400, 16, 4, 128), [300, 0, 1, 129, 200, 300, 64, 257, 300], [400, 400, 129, 0, 1, 256, 300, 128, 399]),
     ((40, 70, 130, 8, 8, 64), None, [(37 * b) % 131 for b in range(40)]),
+    # one query step a key tile, several tiles a block: accumulators change hands at every step
+    ((2, 40, 4000, 16, 16, 64), None, None), ((3, 33, 3000, 16, 8, 128), [33, 1, 20], [3000, 2999, 1300]),
+    ((1, 70, 2600, 32, 32, 128), None, None), ((40, 130, 100, 8, 4, 64), [(29 * b) % 131 for b in range(40)], None),
 ])
 def test_many_units_a_block(size, q_lens, k_lens, dtype):
-    """More units of work than the GPU has places, some of them empty, so that blocks go from one to the next."""
-    run(*make(*size, dtype), q_lens, k_lens)
+    """More units of work than the GPU has places, some of them empty, so that blocks go from one to the next. The
+    same bits again and again."""
+    q, k, v, do = make(*size, dtype)
+    first = run(q, k, v, do, q_lens, k_lens)
+    ql, kl = ints(q_lens), ints(k_lens)
+    for _ in range(20):
+        o, lse = fa.cross_attention_forward(q, k, v, ql, kl)
+        for a, b in zip(first, (o, lse) + fa.cross_attention_backward(q, k, v, o, do, lse, ql, kl)):
+            assert torch.equal(a, b)
+    assert fa.fa_get_device_status() == 0
 
 
 FEW = [
