@@ -129,8 +129,11 @@ struct KVCfg {
   static constexpr int bDQFull = bDSFull + 2;                  // [2]: dQ^T MMAs (and dK) done
   static constexpr int bStaged = bDQFull + 2;                  // [2]: dQ^T staged over the image
   static constexpr int bStageFree = bStaged + 2;               // [2]: staging read by the TMA unit
-  static constexpr int bAcc = bStageFree + 2;                  // a unit's dV, dK complete in TMEM
-  static constexpr int bDrain = bAcc + 1;                      // one per MMA-issuing warp
+  // [2]: a unit's dV, dK complete in TMEM, one barrier per warpgroup pair: a pair waits for the units
+  // whose epilogue it writes only, and on one barrier for both it could take an earlier unit's phase
+  // of the same parity for its own (units of one step: N <= 64)
+  static constexpr int bAcc = bStageFree + 2;
+  static constexpr int bDrain = bAcc + 2;                      // one per MMA-issuing warp
   static constexpr int bKVFree = bDrain + 3;                   // a unit's last reads of K, V done
   static constexpr int bAccFree = bKVFree + 1;                 // the epilogue has read dV, dK
   static constexpr int bUnit = bAccFree + 1;                   // [kUnitSlots]: next unit published
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(KVCfg<D, kAtomic, kBias>::kThreads, 1)
       mbar_init(bar(C::bStageFree + x), 1);                    // the reducer
     }
     for (int x = 0; x < 3; ++x) mbar_init(bar(C::bDrain + x), 1);
-    mbar_init(bar(C::bAcc), 1);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(C::bAcc + x), 1);
     mbar_init(bar(C::bKVFree), kAtomic ? 3 : 2);               // S^T, dP^T (and dQ^T) issuers
     mbar_init(bar(C::bAccFree), 8 * 32);                       // the epilogue pair's row-math warps
     for (int x = 0; x < kUnitSlots; ++x) {
@@ -570,7 +573,7 @@ __global__ void __launch_bounds__(KVCfg<D, kAtomic, kBias>::kThreads, 1)
             tc_commit_w(bar(C::bQEmpty + st));
           }
           if (!ok) break;
-          tc_commit_w(bar(C::bAcc));
+          tc_commit_w(bar(C::bAcc + ((G + g.nsteps - 1) & 1)));
           if constexpr (kAtomic) tc_commit_w(bar(C::bKVFree));  // the dQ^T MMAs read K
           G += g.nsteps;
           ++kl;
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(KVCfg<D, kAtomic, kBias>::kThreads, 1)
     const uint32_t tSc = tS + lane_off + 64 * bb + 32 * c, tdPc = tdP + lane_off + 64 * bb + 32 * c;
     const uint32_t imgRow = sb + C::oImg + 2 * bb * C::kPTile + jl * 128;
     const float inv_scale = kBias ? 1.f / p.scale : 0.f;
-    int idx = first, k = 0, kl = 0, G = 0;
+    int idx = first, k = 0, kl = 0, G = 0;  // kl: units whose epilogue this pair wrote
     bool ok = true;
     while (ok && idx >= 0) {
       KVUnit g;
@@ -830,10 +833,11 @@ __global__ void __launch_bounds__(KVCfg<D, kAtomic, kBias>::kThreads, 1)
             uint32_t r[kChunks][32];
             if (nsteps > 0) {
               if (!isK) {
-                if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
+                if (!warp_wait<kRowMathPoll>(bar(C::bAcc + bb), kl & 1, abort_flag, p.status)) {
                   ok = false;
                   break;
                 }
+                ++kl;
                 tc_fence_after();
               }
               __syncwarp();  // the stores above are per-lane: converge for the TMEM loads
@@ -872,7 +876,6 @@ __global__ void __launch_bounds__(KVCfg<D, kAtomic, kBias>::kThreads, 1)
           }
           if (!ok) break;
         }
-        if (nsteps > 0) ++kl;
         (void)bh;
         G += nsteps;
       }
