@@ -47,6 +47,7 @@ struct CrossPlan {
   int kv_blocks, q_blocks;  // the backward's blocks for dK/dV and for dQ, which share out the units
   bool few;                 // the forward's kernel of few rows
   int few_cluster;
+  bool few_sorted;          // its blocks take the sequences in the order of falling lengths
 };
 
 struct CrossParams {

@@ -16,7 +16,8 @@
 // Rows of keys past the end are copied as zeros. The warps' results meet in shared memory,
 // the shares of a sequence in the distributed shared memory of a cluster (up to eight
 // blocks); where that leaves the GPU empty (few heads, long states) more shares go through
-// the workspace and the joining kernel.
+// the workspace and the joining kernel. Where blocks of unequal lengths come in several
+// rounds the longest sequences go first.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -95,7 +96,21 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
   wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, in_quad = lane & 3;
   const int shares = p.few_cluster ? p.few_cluster : p.plan.k_splits, share = blockIdx.x;
-  const int b = blockIdx.z / p.Hk, hk = blockIdx.z - b * p.Hk;
+  int b = blockIdx.z / p.Hk;
+  const int hk = blockIdx.z - b * p.Hk;
+  if (p.plan.few_sorted) {  // the b-th longest sequence (the lower number first)
+    __shared__ int lens[kThreads], found;
+    if ((int)threadIdx.x < p.B) lens[threadIdx.x] = cross_k_len(p, threadIdx.x);
+    __syncthreads();
+    if ((int)threadIdx.x < p.B) {
+      int before = 0;
+      for (int i = 0; i < p.B; ++i)
+        before += lens[i] > lens[threadIdx.x] || (lens[i] == lens[threadIdx.x] && i < (int)threadIdx.x);
+      if (before == b) found = threadIdx.x;
+    }
+    __syncthreads();
+    b = found;
+  }
   const int nk = cross_k_len(p, b), nq = cross_q_len(p, b);
   const int tiles = (nk + kK - 1) / kK, per = (tiles + shares - 1) / shares;
   const int t_end = min(tiles, (share + 1) * per);

@@ -79,6 +79,8 @@ FEW = [
     ((2, 17, 1500, 2, 2, 64), None), ((1, 31, 900, 4, 2, 128), None), ((1, 64, 600, 3, 3, 64), [599]),
     ((1, 1, 40, 64, 1, 128), None), ((100, 1, 60, 8, 8, 64), None), ((1, 2, 6000, 8, 1, 128), [5999]),
     ((1, 5, 5000, 3, 1, 64), [129]),
+    # several rounds of long blocks, longest sequences first; equal lengths, none
+    ((70, 1, 2100, 8, 8, 128), [(1000 + 700 * b) % 2101 for b in range(70)]), ((128, 1, 2048, 4, 4, 64), [2048, 0, 5] * 42 + [7, 7]),
 ]
 
 
