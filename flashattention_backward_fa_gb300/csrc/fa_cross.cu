@@ -153,13 +153,13 @@ CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype, bool backward) {
     c.few_sorted = s->k_lens && s->B > 1 && s->B <= 128 && units * shares > 304 && (long long)s->Nk * s->d / shares >= 1 << 17;
     return c;
   }
+  const long long groups = (long long)s->B * s->Hk, rows = (long long)s->Nq * G;
   if (dtype == FA_F32) {
-    const long long q_units = (long long)s->B * s->Hq * div_up(s->Nq, 32), k_units = (long long)s->B * s->Hk * div_up(s->Nk, 32);
-    c.k_splits = best_splits(q_units, (int)div_up(s->Nk, 64), 304, 1, 3);
-    if (backward) c.q_splits = best_splits(k_units, (int)div_up(s->Nq, 64) * G, 152, 1, 3);
+    c.k_splits = best_splits(groups * div_up(rows, 32), (int)div_up(s->Nk, 64), 304, 1, 3);
+    if (backward) c.q_splits = best_splits(groups * div_up(s->Nk, 32), (int)div_up(rows, 64), 152, 1, 3);
     return c;
   }
-  const long long groups = (long long)s->B * s->Hk, tiles = c.q_tile.count(s->Nq, G);
+  const long long tiles = c.q_tile.count(s->Nq, G);
   if (!backward) {
     c.k_splits = best_splits(groups * div_up(tiles, 2), (int)div_up(s->Nk, 128), kPlaces, 1, 4);
   } else {

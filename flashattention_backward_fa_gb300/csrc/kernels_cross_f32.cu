@@ -5,8 +5,8 @@
 //   dQ = scale dS K;  dV = sum P^T dO, dK = scale sum dS^T Q over a group's heads
 //
 // fp32 needs about 1e-7 relative accuracy, which the tf32 tensor-core kind cannot
-// give, so the products are FFMA. A block holds 32 rows (queries; keys in the dK/dV
-// kernel) and walks 64 columns at a time (keys; queries of all heads of the group).
+// give, so the products are FFMA. A block holds 32 rows (query rows of a group of heads;
+// keys in the dK/dV kernel) and walks 64 columns at a time (keys; query rows).
 // 128 threads as 8 x 16: a thread has 4 x 4 of the 32 x 64 products (rows ty + 8 i,
 // columns tx + 16 j, both operands read in 16-byte pieces of rows DP + 4 floats
 // apart, which no two threads of a quarter warp have in the same bank) and 4 rows x
@@ -29,17 +29,38 @@ struct Tile {
   static constexpr int bytes(int rows) { return rows * kApart * 4; }
 };
 
-// Rows [0, rows) of a tensor (row stride `st`, d values each) to shared memory as [kMost][DP], zeros past `rows`
-// and d; by 16 bytes where the tensor's strides allow it (vec), all of a thread's loads under way at once.
-template <int DP, int kMost>
-__device__ __forceinline__ void stage(float* to, const float* from, int64_t st, int rows, int d, bool vec) {
+// Where a row of a (batch, head) is in its tensor: the rows of one key head, or those of all query heads of its
+// group, the heads of a query side by side (so that few queries fill a tile, the real ones are the first, and
+// keys are read once for a group).
+struct KeyRows {
+  int64_t at, n;
+  __device__ __forceinline__ KeyRows(const fa_strides& st, int b, int h, int first)
+      : at(b * st.b + h * st.h + first * st.n), n(st.n) {}
+  __device__ __forceinline__ int64_t operator()(int r) const { return at + r * n; }
+};
+struct GroupRows {
+  int64_t at, n, h;
+  int first, G;
+  __device__ __forceinline__ GroupRows(const fa_strides& st, int b, int hk, int G_, int first_)
+      : at(b * st.b + (int64_t)(hk * G_) * st.h), n(st.n), h(st.h), first(first_), G(G_) {}
+  __device__ __forceinline__ int64_t operator()(int r) const {
+    const int t = (first + r) / G;
+    return at + t * n + (first + r - t * G) * h;
+  }
+};
+
+// Rows [0, rows) of a tensor (d values each) to shared memory as [kMost][DP], zeros past `rows` and d; by
+// 16 bytes where the tensor's strides allow it (vec), all of a thread's loads under way at once.
+template <int DP, int kMost, typename Rows>
+__device__ __forceinline__ void stage(float* to, const void* tensor, const Rows& row, int rows, int d, bool vec) {
+  const float* from = static_cast<const float*>(tensor);
   if (vec) {
     constexpr int kEach = kMost * DP / 4 / kThreads;
     float4 v[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int x = threadIdx.x + i * kThreads, r = x / (DP / 4), e = 4 * (x % (DP / 4));
-      v[i] = r < rows && e < d ? *reinterpret_cast<const float4*>(from + r * st + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i] = r < rows && e < d ? *reinterpret_cast<const float4*>(from + row(r) + e) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -51,7 +72,7 @@ __device__ __forceinline__ void stage(float* to, const float* from, int64_t st, 
 #pragma unroll 8
   for (int x = threadIdx.x; x < kMost * DP; x += kThreads) {
     const int r = x / DP, e = x - r * DP;
-    to[r * Tile<DP>::kApart + e] = r < rows && e < d ? from[r * st + e] : 0.f;
+    to[r * Tile<DP>::kApart + e] = r < rows && e < d ? from[row(r) + e] : 0.f;
   }
 }
 
@@ -153,6 +174,12 @@ __device__ __forceinline__ void clear(uint64_t (&acc)[4][DP / 64][2]) {
     for (int c = 0; c < DP / 64; ++c) acc[i][c][0] = acc[i][c][1] = 0ull;
 }
 
+// Place of row r of a group in the backward's -L and -D.
+__device__ __forceinline__ int64_t stats_row(const CrossParams& p, int b, int hk, int r) {
+  const int t = r / p.G;
+  return ((int64_t)b * p.Hq + hk * p.G + r - t * p.G) * p.nq_pad + t;
+}
+
 // Over the 16 threads that share a row.
 __device__ __forceinline__ float row_max16(float v) {
 #pragma unroll
@@ -160,30 +187,27 @@ __device__ __forceinline__ float row_max16(float v) {
   return v;
 }
 
-// Grid: x the query tile, y head, z batch * split.
+// Grid: x the tile of the group's query rows, y key head, z batch * split.
 template <int DP>
 __global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_constant__ CrossParams p) {
   extern __shared__ __align__(16) float sm[];
   let_next_begin();
   wait_for_previous();
   float *q = sm, *k = q + kRows * Tile<DP>::kApart, *v = k + kCols * Tile<DP>::kApart, *w = v + kCols * Tile<DP>::kApart;
-  const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, h = blockIdx.y;
-  const int i0 = blockIdx.x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, hk = blockIdx.y;
+  const int r0 = blockIdx.x * kRows, live = cross_q_len(p, b) * p.G - r0, nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int per = ((nk + kCols - 1) / kCols + splits - 1) / splits * kCols, j_end = min(nk, (split + 1) * per);
-  const float* kp = static_cast<const float*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
-  const float* vp = static_cast<const float*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
   uint64_t acc[4][DP / 64][2];
   clear<DP>(acc);
   float m[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
-  if (i0 < nq)
-    stage<DP, kRows>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0, p.d, vec_rows(p, p.q_st));
-  for (int j0 = split * per; i0 < nq && j0 < j_end; j0 += kCols) {
+  if (live > 0) stage<DP, kRows>(q, p.q, GroupRows(p.q_st, b, hk, p.G, r0), live, p.d, vec_rows(p, p.q_st));
+  for (int j0 = split * per; live > 0 && j0 < j_end; j0 += kCols) {
     __syncthreads();
-    stage<DP, kCols>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, p.d, vec_rows(p, p.k_st));
-    stage<DP, kCols>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, p.d, vec_rows(p, p.v_st));
+    stage<DP, kCols>(k, p.k, KeyRows(p.k_st, b, hk, j0), j_end - j0, p.d, vec_rows(p, p.k_st));
+    stage<DP, kCols>(v, p.v, KeyRows(p.v_st, b, hk, j0), j_end - j0, p.d, vec_rows(p, p.v_st));
     __syncthreads();
     float s[4][4];
     rows_by_rows<DP>(q, k, s);
@@ -220,9 +244,9 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_co
   const long long rows = (long long)p.B * p.Nq * p.Hq;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = i0 + ty + 8 * i;
+    const int r = ty + 8 * i, t = (r0 + r) / p.G, h = hk * p.G + r0 + r - t * p.G;
     if (t >= p.Nq) continue;
-    const bool has = t < nq && l[i] != 0.f;  // (a NaN sum counts as there)
+    const bool has = r < live && l[i] != 0.f;  // (a NaN sum counts as there)
     const long long at = ((long long)b * p.Hq + h) * p.Nq + t;
     const float lse2 = has ? m[i] + log2f(l[i]) : -INFINITY;
     if (splits > 1) {
@@ -240,34 +264,33 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_co
   }
 }
 
-// dQ of a query tile x and head h over the keys of one split (z: batch * split).
+// dQ of a tile x of a group's query rows over the keys of one split (z: batch * split).
 template <int DP>
-__device__ __forceinline__ void dq_block(const CrossParams& p, float* sm, int x, int h, int z) {
+__device__ __forceinline__ void dq_block(const CrossParams& p, float* sm, int x, int hk, int z) {
   float *q = sm, *g = q + kRows * Tile<DP>::kApart, *k = g + kRows * Tile<DP>::kApart,
         *v = k + kCols * Tile<DP>::kApart, *w = v + kCols * Tile<DP>::kApart;
   const int splits = p.plan.k_splits, b = z / splits, split = z - b * splits;
-  const int i0 = x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int r0 = x * kRows, live = cross_q_len(p, b) * p.G - r0, nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int per = ((nk + kCols - 1) / kCols + splits - 1) / splits * kCols, j_end = min(nk, (split + 1) * per);
-  const float* kp = static_cast<const float*>(p.k) + b * p.k_st.b + (h / p.G) * p.k_st.h;
-  const float* vp = static_cast<const float*>(p.v) + b * p.v_st.b + (h / p.G) * p.v_st.h;
   uint64_t acc[4][DP / 64][2];
   clear<DP>(acc);
   float nl[4], nd[4];
-  if (i0 < nq) {
-    stage<DP, kRows>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0, p.d, vec_rows(p, p.q_st));
-    stage<DP, kRows>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n, nq - i0, p.d, vec_rows(p, p.do_st));
+  if (live > 0) {
+    stage<DP, kRows>(q, p.q, GroupRows(p.q_st, b, hk, p.G, r0), live, p.d, vec_rows(p, p.q_st));
+    stage<DP, kRows>(g, p.dout, GroupRows(p.do_st, b, hk, p.G, r0), live, p.d, vec_rows(p, p.do_st));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const long long at = ((long long)b * p.Hq + h) * p.nq_pad + i0 + ty + 8 * i;
-      nl[i] = i0 + ty + 8 * i < nq ? p.nL2[at] : -INFINITY;
-      nd[i] = i0 + ty + 8 * i < nq ? p.nD[at] : 0.f;
+      const int r = ty + 8 * i;
+      const int64_t at = stats_row(p, b, hk, r0 + r);
+      nl[i] = r < live ? p.nL2[at] : -INFINITY;
+      nd[i] = r < live ? p.nD[at] : 0.f;
     }
   }
-  for (int j0 = split * per; i0 < nq && j0 < j_end; j0 += kCols) {
+  for (int j0 = split * per; live > 0 && j0 < j_end; j0 += kCols) {
     __syncthreads();
-    stage<DP, kCols>(k, kp + (int64_t)j0 * p.k_st.n, p.k_st.n, j_end - j0, p.d, vec_rows(p, p.k_st));
-    stage<DP, kCols>(v, vp + (int64_t)j0 * p.v_st.n, p.v_st.n, j_end - j0, p.d, vec_rows(p, p.v_st));
+    stage<DP, kCols>(k, p.k, KeyRows(p.k_st, b, hk, j0), j_end - j0, p.d, vec_rows(p, p.k_st));
+    stage<DP, kCols>(v, p.v, KeyRows(p.v_st, b, hk, j0), j_end - j0, p.d, vec_rows(p, p.v_st));
     __syncthreads();
     float s[4][4], dp[4][4];
     rows_by_rows<DP>(q, k, s);
@@ -285,10 +308,10 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, float* sm, int x,
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = i0 + ty + 8 * i;
+    const int r = ty + 8 * i, t = (r0 + r) / p.G, h = hk * p.G + r0 + r - t * p.G;
     if (t >= p.Nq) continue;
     if (splits > 1) {
-      if (t < nq)
+      if (r < live)
         put_row<DP>(p.part + (((long long)split * p.B + b) * p.Nq + t) * p.Hq * p.d + (long long)h * p.d, acc[i],
                            1.f, p.d);
     } else {
@@ -297,36 +320,35 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, float* sm, int x,
   }
 }
 
-// dK and dV of a key tile x and key head hk over one split of the query steps (64 queries of one head of the group
-// each, heads outermost; z: batch * split).
+// dK and dV of a key tile x and key head hk over one split of the query steps (64 rows of the group; z: batch * split).
 template <int DP>
 __device__ __forceinline__ void dkdv_block(const CrossParams& p, float* sm, int x, int hk, int z) {
   float *k = sm, *v = k + kRows * Tile<DP>::kApart, *q = v + kRows * Tile<DP>::kApart,
         *g = q + kCols * Tile<DP>::kApart, *w = g + kCols * Tile<DP>::kApart, *u = w + kRows * kPad;
   const int splits = p.plan.q_splits, b = z / splits, split = z - b * splits;
-  const int j0 = x * kRows, nq = cross_q_len(p, b), nk = cross_k_len(p, b);
+  const int j0 = x * kRows, rows = cross_q_len(p, b) * p.G, nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int per_head = (nq + kCols - 1) / kCols, steps = per_head * p.G, per = (steps + splits - 1) / splits;
+  const int steps = (rows + kCols - 1) / kCols, per = (steps + splits - 1) / splits;
   const int s_end = min(steps, (split + 1) * per);
   uint64_t dk[4][DP / 64][2], dv[4][DP / 64][2];
   clear<DP>(dk);
   clear<DP>(dv);
   if (j0 < nk) {
-    stage<DP, kRows>(k, static_cast<const float*>(p.k) + b * p.k_st.b + (int64_t)j0 * p.k_st.n + hk * p.k_st.h, p.k_st.n, nk - j0, p.d, vec_rows(p, p.k_st));
-    stage<DP, kRows>(v, static_cast<const float*>(p.v) + b * p.v_st.b + (int64_t)j0 * p.v_st.n + hk * p.v_st.h, p.v_st.n, nk - j0, p.d, vec_rows(p, p.v_st));
+    stage<DP, kRows>(k, p.k, KeyRows(p.k_st, b, hk, j0), nk - j0, p.d, vec_rows(p, p.k_st));
+    stage<DP, kRows>(v, p.v, KeyRows(p.v_st, b, hk, j0), nk - j0, p.d, vec_rows(p, p.v_st));
   }
   for (int st = split * per; j0 < nk && st < s_end; ++st) {
-    const int h = hk * p.G + st / per_head, i0 = st % per_head * kCols;
+    const int r0 = st * kCols;
     __syncthreads();
-    stage<DP, kCols>(q, static_cast<const float*>(p.q) + b * p.q_st.b + (int64_t)i0 * p.q_st.n + h * p.q_st.h, p.q_st.n, nq - i0, p.d, vec_rows(p, p.q_st));
-    stage<DP, kCols>(g, static_cast<const float*>(p.dout) + b * p.do_st.b + (int64_t)i0 * p.do_st.n + h * p.do_st.h, p.do_st.n, nq - i0, p.d, vec_rows(p, p.do_st));
+    stage<DP, kCols>(q, p.q, GroupRows(p.q_st, b, hk, p.G, r0), rows - r0, p.d, vec_rows(p, p.q_st));
+    stage<DP, kCols>(g, p.dout, GroupRows(p.do_st, b, hk, p.G, r0), rows - r0, p.d, vec_rows(p, p.do_st));
     float nl[4], nd[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = i0 + tx + 16 * j;
-      const long long at = ((long long)b * p.Hq + h) * p.nq_pad + t;
-      nl[j] = t < nq ? p.nL2[at] : -INFINITY;
-      nd[j] = t < nq ? p.nD[at] : 0.f;
+      const int r = r0 + tx + 16 * j;
+      const int64_t at = stats_row(p, b, hk, r);
+      nl[j] = r < rows ? p.nL2[at] : -INFINITY;
+      nd[j] = r < rows ? p.nD[at] : 0.f;
     }
     __syncthreads();
     float s[4][4], dp[4][4];
@@ -369,15 +391,15 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32_kernel(const __grid_co
   extern __shared__ __align__(16) float sm[];
   let_next_begin();
   wait_for_previous();
-  const int k_tiles = (p.Nk + kRows - 1) / kRows, q_tiles = (p.Nq + kRows - 1) / kRows;
+  const int k_tiles = (p.Nk + kRows - 1) / kRows, q_tiles = (p.Nq * p.G + kRows - 1) / kRows;
   const int kv = k_tiles * p.Hk * p.B * p.plan.q_splits;
   const bool is_kv = (int)blockIdx.x < kv;
-  const int idx = is_kv ? blockIdx.x : blockIdx.x - kv, tiles = is_kv ? k_tiles : q_tiles, heads = is_kv ? p.Hk : p.Hq;
-  const int rest = idx / tiles, x = idx - rest * tiles, z = rest / heads, h = rest - z * heads;
+  const int idx = is_kv ? blockIdx.x : blockIdx.x - kv, tiles = is_kv ? k_tiles : q_tiles;
+  const int rest = idx / tiles, x = idx - rest * tiles, z = rest / p.Hk, hk = rest - z * p.Hk;
   if (is_kv)
-    dkdv_block<DP>(p, sm, x, h, z);
+    dkdv_block<DP>(p, sm, x, hk, z);
   else
-    dq_block<DP>(p, sm, x, h, z);
+    dq_block<DP>(p, sm, x, hk, z);
 }
 
 template <int DP>
@@ -385,7 +407,7 @@ cudaError_t launch_fwd_t(const CrossParams& p, cudaStream_t st) {
   constexpr int bytes = Tile<DP>::bytes(kRows + 2 * kCols) + kRows * kPad * 4;
   const cudaError_t e = allow_smem<cross_fwd_f32_kernel<DP>>(bytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid((p.Nq + kRows - 1) / kRows, p.Hq, p.B * p.plan.k_splits);
+  const dim3 grid((p.Nq * p.G + kRows - 1) / kRows, p.Hk, p.B * p.plan.k_splits);
   return launch_chained(cross_fwd_f32_kernel<DP>, grid, kThreads, bytes, 1, p, st);
 }
 
@@ -395,7 +417,7 @@ cudaError_t launch_bwd_t(const CrossParams& p, cudaStream_t st) {
   const cudaError_t e = allow_smem<cross_bwd_f32_kernel<DP>>(bytes);
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)((p.Nk + kRows - 1) / kRows) * p.Hk * p.B * p.plan.q_splits +
-                           (long long)((p.Nq + kRows - 1) / kRows) * p.Hq * p.B * p.plan.k_splits;
+                           (long long)((p.Nq * p.G + kRows - 1) / kRows) * p.Hk * p.B * p.plan.k_splits;
   return launch_chained(cross_bwd_f32_kernel<DP>, dim3((unsigned)blocks), kThreads, bytes, 1, p, st);
 }
 
