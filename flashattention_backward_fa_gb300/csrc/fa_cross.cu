@@ -24,8 +24,9 @@ int check_shape(const fa_cross_shape* s, fa_dtype dtype) {
   // batches and heads are grid extents; the kernels' units of work and their steps are counted in 31 bits
   if (s->B > 65535 || s->Hq > 65535 || s->Nq > (1 << 24) || s->Nk > (1 << 24)) return FA_ERR_UNSUPPORTED;
   if ((long long)s->B * s->Hq > (1 << 24) || (long long)s->Nq * (s->Hq / s->Hk) > (1 << 30)) return FA_ERR_UNSUPPORTED;
-  if ((long long)s->B * s->Hq * ((s->Nq + 31ll) / 32) > (1 << 30) || (long long)s->B * s->Hk * ((s->Nk + 31ll) / 32) > (1 << 30))
-    return FA_ERR_UNSUPPORTED;
+  const long long q_tiles = (long long)s->B * s->Hq * ((s->Nq + 31ll) / 32);
+  const long long k_tiles = (long long)s->B * s->Hk * ((s->Nk + 31ll) / 32);
+  if (q_tiles > (1 << 30) || k_tiles > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (!aligned_to(s->q_lens, 4) || !aligned_to(s->k_lens, 4)) return FA_ERR_ALIGNMENT;
   return FA_OK;
 }
@@ -106,18 +107,19 @@ bool few_rows(long long groups, long long rows, int Nk) {
 // have over 2048 keys (16 heads, d = 64, 8192 keys: cluster 11.5 us, workspace 16.9).
 void few_plan(long long units, int Nk, CrossPlan* c) {
   c->k_splits = c->few_cluster = 1;
-  while (c->few_cluster < 8 && units * c->few_cluster * 2 <= 608 && c->few_cluster * 2 * 128 <= Nk + 127) c->few_cluster *= 2;
+  while (c->few_cluster < 8 && units * c->few_cluster * 2 <= 608 && c->few_cluster * 2 * 128 <= Nk + 127)
+    c->few_cluster *= 2;
   if (units * 8 <= 152 && Nk > 8 * 2048) {
     c->few_cluster = 0;
     c->k_splits = (int)std::min<long long>(304 / units, Nk / 256);
   }
 }
 
-// The backward's splits and blocks. Splits: until dK/dV has 128 units or they are down to 16 query steps, dQ 64 units or
-// 8 key blocks. Blocks: as many as there are units, but not under 16 steps (8 key blocks) each while 128 blocks
-// remain. Measured, us (dK/dV splits / blocks, dQ splits / blocks): 16 heads, 4095 queries over 77 keys, d = 64: 16 / 128,
-// 1 / 256 73; 4 / 32, 1 / 104 120; 32 / 256, 1 / 512 86. 16/4 heads, 1024 over 1024, batch 2: 2 / 128, 1 / 128 84; 1 / 64, 1 / 62
-// 98. 64 queries over 16384 keys: 1 / 512, 4 / 64 130; 1 / 512, 1 / 16 227.
+// The backward's splits and blocks. Splits: until dK/dV has 128 units or they are down to 16 query steps, dQ 64
+// units or 8 key blocks. Blocks: as many as there are units, but not under 16 steps (8 key blocks) each while 128
+// blocks remain. Measured, us (dK/dV splits / blocks, dQ splits / blocks): 16 heads, 4095 queries over 77 keys,
+// d = 64: 16 / 128, 1 / 256 73; 4 / 32, 1 / 104 120; 32 / 256, 1 / 512 86. 16/4 heads, 1024 over 1024, batch 2:
+// 2 / 128, 1 / 128 84; 1 / 64, 1 / 62 98. 64 queries over 16384 keys: 1 / 512, 4 / 64 130; 1 / 512, 1 / 16 227.
 void bwd_plan(const fa_cross_shape* s, long long groups, long long tiles, CrossPlan* c) {
   const int steps = c->step.count(s->Nq, s->Hq / s->Hk), blocks = (int)div_up(s->Nk, 128);
   const long long kv = groups * div_up(s->Nk, 128), q = groups * tiles;
@@ -147,10 +149,11 @@ CrossPlan plan_of(const fa_cross_shape* s, fa_dtype dtype, bool backward) {
   if (c.few) {
     const long long units = (long long)s->B * s->Hk * div_up((long long)s->Nq * G, 16);
     few_plan(units, s->Nk, &c);
-    // By falling lengths where blocks come in several rounds and are long: 32 sequences x 8 heads of up to 4096 keys
-    // 61.9 -> 54.6 us, 64 x 8 of up to 2048 59.4 -> 50.5; 100 x 8 heads of 64 of up to 1000 keys 28.8 -> 32.5 us.
+    // By falling lengths where blocks come in several rounds and are long: 32 sequences x 8 heads of up to 4096
+    // keys 61.9 -> 54.6 us, 64 x 8 of up to 2048 59.4 -> 50.5; 100 x 8 heads of 64 of up to 1000 keys 28.8 -> 32.5.
     const int shares = std::max(c.few_cluster, c.k_splits);
-    c.few_sorted = s->k_lens && s->B > 1 && s->B <= 128 && units * shares > 304 && (long long)s->Nk * s->d / shares >= 1 << 17;
+    c.few_sorted = s->k_lens && s->B > 1 && s->B <= 128 && units * shares > 304 &&
+                   (long long)s->Nk * s->d / shares >= 1 << 17;
     return c;
   }
   const long long groups = (long long)s->B * s->Hk, rows = (long long)s->Nq * G;
@@ -308,7 +311,8 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   CUtensorMap maps[6];
   if (!f32) {
     if ((rc = fa::bind_device_context())) return rc;
-    if (!q_map(&maps[0], p, q, q_strides, plan.step, dtype) || !q_map(&maps[1], p, dout, dout_strides, plan.step, dtype) ||
+    if (!q_map(&maps[0], p, q, q_strides, plan.step, dtype) ||
+        !q_map(&maps[1], p, dout, dout_strides, plan.step, dtype) ||
         !q_map(&maps[2], p, q, q_strides, plan.q_tile, dtype) ||
         !q_map(&maps[3], p, dout, dout_strides, plan.q_tile, dtype) || !k_map(&maps[4], p, k, k_strides, dtype) ||
         !k_map(&maps[5], p, v, v_strides, dtype))

@@ -36,7 +36,8 @@ inline CrossTile cross_tile(int Nq, int G, int most, int least) {
 // holds a probability above this. Roundings of many small weights average out; those of one that makes up
 // the row do not. Error of bf16 gradients against 64 bits (2-norm, of themselves): 1.7e-3 with the residual
 // everywhere, 2.4e-3 without. At 1/64, as in fa_bwd, nearly every tile of a few hundred keys had one above it
-// and took half as many products again (dK/dV 4x16 2048x512 84 -> 77 us, 1x32/8 8192x4096 985 -> 822 us).
+// and took half as many products again (dK/dV by itself, 4x16 2048x512 84 us, 1x32/8 8192x4096 985; with 1/4
+// 77 and 822 us).
 constexpr float kCrossSplit = 0.25f;
 
 struct CrossPlan {
@@ -147,7 +148,8 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 // of a 128-row tile was bound by that, 3300 cycles).
 __device__ __forceinline__ void quad_transpose(uint4 (&u)[4]) {
   const int q = threadIdx.x & 3;
-  const auto swap = [](uint4& a, uint4& b, bool hi, int o) {  // hi lanes give a and get b's place, the others the reverse
+  // hi lanes give a and get b's place, the others the reverse
+  const auto swap = [](uint4& a, uint4& b, bool hi, int o) {
     uint4 give = hi ? a : b;
     give.x = __shfl_xor_sync(0xffffffffu, give.x, o);
     give.y = __shfl_xor_sync(0xffffffffu, give.y, o);
@@ -171,7 +173,8 @@ __device__ __forceinline__ void store_rows64(uint4 (&u)[4], char* to) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    char* at = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), (lane & ~3) + r));
+    const auto whole = reinterpret_cast<unsigned long long>(to);
+    char* at = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, whole, (lane & ~3) + r));
     if (at != nullptr) reinterpret_cast<uint4*>(at)[lane & 3] = u[r];
   }
 }
@@ -201,7 +204,8 @@ __device__ __forceinline__ void pack64(uint4 (&u)[4], const uint32_t* r, float m
 // 32 columns of a converged warp's 32 accumulator rows to memory: as 16-bit values at `out`, or as fp32 at
 // `part`, times mul; both null where the row is not stored.
 template <bool kBf16>
-__device__ __forceinline__ void store_columns32(const uint32_t (&r)[32], float mul, bool parts, float* part, uint16_t* out) {
+__device__ __forceinline__ void store_columns32(const uint32_t (&r)[32], float mul, bool parts, float* part,
+                                                uint16_t* out) {
   uint4 u[4];
   if (parts) {
     pack64(u, r, mul);
@@ -231,7 +235,8 @@ cudaError_t launch_cross_join_bwd(const CrossParams& p, int dtype, cudaStream_t 
 
 // launch_chained (fa_serve.h) for the kernels that take tensor maps beside their parameters.
 template <typename... Args>
-cudaError_t launch_chained_maps(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const Args&... args) {
+cudaError_t launch_chained_maps(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st,
+                                const Args&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -222,7 +222,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           mbar_arrive_expect_tx(bar(C::bQFull + s), q_bytes);
           for (int pn = 0; pn < C::kPanels; ++pn) {
             tma_load_4d(sb + C::oQ + s * C::kQTile + pn * C::kQPanel, &tmQ, bar(C::bQFull + s), 64 * pn, q0, h0, u.b);
-            tma_load_4d(sb + C::oDO + s * C::kQTile + pn * C::kQPanel, &tmDO, bar(C::bQFull + s), 64 * pn, q0, h0, u.b);
+            tma_load_4d(sb + C::oDO + s * C::kQTile + pn * C::kQPanel, &tmDO, bar(C::bQFull + s), 64 * pn, q0, h0,
+                        u.b);
           }
           const int q = p.plan.step.queries();
           for (int h = 0; h < p.plan.step.heads(); ++h) {
@@ -365,9 +366,9 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       const int steps = u.steps, chunks = max(u.chunks, 1);
       int chunk = u.chunk + ((bb ^ G) & 1);
       chunk -= chunk >= chunks ? chunks : 0;
-      // The columns with real queries of any step but a head's last (or last few heads') and of that one, and whether
-      // the lane has a real key. (A lane without one needs no mask: its row of P^T and dS^T reaches nothing but its
-      // own row of dV and dK, which the epilogue drops. It has no vote.)
+      // The columns with real queries of any step but a head's last (or last few heads') and of that one, and
+      // whether the lane has a real key. (A lane without one needs no mask: its row of P^T and dS^T reaches nothing
+      // but its own row of dV and dK, which the epilogue drops. It has no vote.)
       const uint32_t full = step_columns(p.plan.step, c, kStep);
       const uint32_t tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
       const bool real = u.j0 + jl < u.nk;
@@ -400,10 +401,10 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
             for (int x = 0; x < 16; x += 4) {
               const float4 l4 = L4[(16 * hh + x) >> 2];
               float pv[4];
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[x]), __uint_as_float(sr[x + 1])), c2, f2_pack(l4.x, l4.y)),
-                        pv[0], pv[1]);
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3])), c2, f2_pack(l4.z, l4.w)),
-                        pv[2], pv[3]);
+              const uint64_t s01 = f2_pack(__uint_as_float(sr[x]), __uint_as_float(sr[x + 1]));
+              const uint64_t s23 = f2_pack(__uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3]));
+              f2_unpack(f2_fma(s01, c2, f2_pack(l4.x, l4.y)), pv[0], pv[1]);
+              f2_unpack(f2_fma(s23, c2, f2_pack(l4.z, l4.w)), pv[2], pv[3]);
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 const int bit = 16 * hh + x + y;
@@ -522,9 +523,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
                                                  (((long long)b * p.Nk + j) * p.Hk + hk) * D + col
                                            : nullptr;
           const fa_strides& st = isK ? p.dk_st : p.dv_st;
-          uint16_t* to_out = !parts && j < p.Nk ? static_cast<uint16_t*>(isK ? p.dk : p.dv) + b * st.b + j * st.n + hk * st.h +
-                                                      col
-                                                : nullptr;
+          uint16_t* const grad = static_cast<uint16_t*>(isK ? p.dk : p.dv);
+          uint16_t* to_out = !parts && j < p.Nk ? grad + b * st.b + j * st.n + hk * st.h + col : nullptr;
           store_columns32<kBf16>(r, isK && !parts ? p.scale : 1.f, parts, to_part, to_out);
         }
         __syncwarp();
@@ -662,7 +662,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
           }
           mbar_arrive_expect_tx(bar(C::bVFull + sv), C::kTile);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(sb + C::oV + sv * C::kTile + pn * C::kPanel, &tmV, bar(C::bVFull + sv), 64 * pn, row, u.hk, u.b);
+            tma_load_4d(sb + C::oV + sv * C::kTile + pn * C::kPanel, &tmV, bar(C::bVFull + sv), 64 * pn, row, u.hk,
+                        u.b);
           issuedV = G + 1;
           if (!mbar_wait(bar(C::bKEmpty + sk), ((G / C::kNK) & 1) ^ 1, abort_flag, p.status)) {
             ok = false;
@@ -670,7 +671,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
           }
           mbar_arrive_expect_tx(bar(C::bKFull + sk), C::kTile);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(sb + C::oK + sk * C::kTile + pn * C::kPanel, &tmK, bar(C::bKFull + sk), 64 * pn, row, u.hk, u.b);
+            tma_load_4d(sb + C::oK + sk * C::kTile + pn * C::kPanel, &tmK, bar(C::bKFull + sk), 64 * pn, row, u.hk,
+                        u.b);
           issuedK = G + 1;
         }
       }
@@ -699,7 +701,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         const bool landed = isS ? warp_wait<kIssuerPoll>(bar(C::bKFull + st), (G / C::kNK) & 1, abort_flag, p.status)
                                 : warp_wait<kIssuerPoll>(bar(C::bVFull + st), (G / C::kNV) & 1, abort_flag, p.status);
         // S: its buffer's image is consumed; dP: the row math has read the step before's
-        if (!landed || (isS && !warp_wait<kIssuerPoll>(bar(C::bSEmpty + bb), ((G >> 1) & 1) ^ 1, abort_flag, p.status)) ||
+        if (!landed ||
+            (isS && !warp_wait<kIssuerPoll>(bar(C::bSEmpty + bb), ((G >> 1) & 1) ^ 1, abort_flag, p.status)) ||
             (!isS && G > 0 && !warp_wait<kIssuerPoll>(bar(C::bDPEmpty), (G - 1) & 1, abort_flag, p.status))) {
           ok = false;
           break;
@@ -782,7 +785,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
       nl = -INFINITY;
       nd = 0.f;
       if (ui < mine && unit[ui].blocks > 0 && row_in) {
-        const long long at = ((long long)unit[ui].b * p.Hq + unit[ui].h0[0] + row_h) * p.nq_pad + unit[ui].q0[0] + row_q;
+        const CrossUnit& u = unit[ui];
+        const long long at = ((long long)u.b * p.Hq + u.h0[0] + row_h) * p.nq_pad + u.q0[0] + row_q;
         nl = p.nL2[at];
         nd = p.nD[at];
       }
@@ -791,7 +795,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     row_of(0, nL2, nD);
     for (int ui = 0; ok && ui < mine; ++ui, nL2 = nL2_next, nD = nD_next) {
       const CrossUnit& u = unit[ui];
-      const int blocks = u.blocks, left = u.j_end - u.j_begin - 32 * c;  // real keys from this warpgroup's first column on
+      // left: real keys from this warpgroup's first column on
+      const int blocks = u.blocks, left = u.j_end - u.j_begin - 32 * c;
       row_of(ui + 1, nL2_next, nD_next);
       const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
       for (int it = 0; it < blocks; ++it) {
@@ -899,9 +904,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
       for (int x = 0; x < 32; ++x) r[x] = i < nq ? r[x] : 0u;  // (rows that are not there may hold NaN)
       float* to_part = parts && in ? p.part + ((((long long)u.split * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
                                    : nullptr;
-      uint16_t* to_out = !parts && in ? static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h +
-                                            c * (D / 4)
-                                      : nullptr;
+      uint16_t* const grad = static_cast<uint16_t*>(p.out);
+      uint16_t* to_out = !parts && in ? grad + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4) : nullptr;
       const float mul = parts ? 1.f : p.scale;
       if constexpr (D == 128) {
         store_columns32<kBf16>(r, mul, parts, to_part, to_out);
@@ -934,7 +938,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
 }
 
 // One launch for both: blocks [0, kv_blocks) take the units of dK/dV, the others those of dQ, so that they share
-// the GPU and each other's tails.
+// the GPU and each other's tails (4x16 2048x512 77 + 50 us in two launches, 118 in one; 1x32/8 8192x4096 823 + 507
+// and 1300).
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_bwd_kernel(const __grid_constant__ CrossParams p, const __grid_constant__ CUtensorMap tmQStep,
@@ -956,8 +961,8 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap* m, cudaStream_t st
   constexpr auto kKernel = cross_bwd_kernel<D, kBf16>;
   const cudaError_t e = allow_smem<kKernel>(bytes);
   if (e != cudaSuccess) return e;
-  return launch_chained_maps(kKernel, dim3(p.plan.kv_blocks + p.plan.q_blocks), kThreads, bytes, st, p, m[0], m[1], m[2],
-                             m[3], m[4], m[5]);
+  return launch_chained_maps(kKernel, dim3(p.plan.kv_blocks + p.plan.q_blocks), kThreads, bytes, st, p, m[0], m[1],
+                             m[2], m[3], m[4], m[5]);
 }
 
 }  // namespace

@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32_kernel(const __grid_co
   extern __shared__ __align__(16) float sm[];
   let_next_begin();
   wait_for_previous();
-  float *q = sm, *k = q + kRows * Tile<DP>::kApart, *v = k + kCols * Tile<DP>::kApart, *w = v + kCols * Tile<DP>::kApart;
+  float *q = sm, *k = q + kRows * Tile<DP>::kApart, *v = k + kCols * Tile<DP>::kApart;
+  float* w = v + kCols * Tile<DP>::kApart;
   const int splits = p.plan.k_splits, b = blockIdx.z / splits, split = blockIdx.z - b * splits, hk = blockIdx.y;
   const int r0 = blockIdx.x * kRows, live = cross_q_len(p, b) * p.G - r0, nk = cross_k_len(p, b);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;

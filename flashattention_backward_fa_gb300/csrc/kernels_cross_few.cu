@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const __grid_con
     const int tq = rr / p.G, h = hk * p.G + rr - tq * p.G;
     const bool has = tq < nq && sum != 0.f;
     out = has ? out / sum : 0.f;
-    static_cast<uint16_t*>(p.out)[b * p.out_st.b + tq * p.out_st.n + h * p.out_st.h + c] = (uint16_t)pack2<kBf16>(out, 0.f);
+    uint16_t* to = static_cast<uint16_t*>(p.out) + b * p.out_st.b + tq * p.out_st.n + h * p.out_st.h + c;
+    *to = (uint16_t)pack2<kBf16>(out, 0.f);
     if (c == 0)
       p.lse_out[((long long)b * p.Hq + h) * p.Nq + tq] = has ? (mm + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   }

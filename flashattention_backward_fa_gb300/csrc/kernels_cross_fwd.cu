@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(bar(C::bQ + x), q_bytes);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(sb + C::oQ + x * C::kTile + pn * C::kPanel, &tmQ, bar(C::bQ + x), 64 * pn, u.q0[x], u.h0[x], u.b);
+            tma_load_4d(sb + C::oQ + x * C::kTile + pn * C::kPanel, &tmQ, bar(C::bQ + x), 64 * pn, u.q0[x], u.h0[x],
+                        u.b);
           ++nq[x];
         }
         for (int j = 0; ok && j < u.blocks; ++j, ++t) {
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(bar(C::bKFull + sk), C::kTile);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(sb + C::oK + sk * C::kTile + pn * C::kPanel, &tmK, bar(C::bKFull + sk), 64 * pn, row, u.hk, u.b);
+            tma_load_4d(sb + C::oK + sk * C::kTile + pn * C::kPanel, &tmK, bar(C::bKFull + sk), 64 * pn, row, u.hk,
+                        u.b);
           issuedK = t + 1;
           if (!mbar_wait(bar(C::bVEmpty + sv), ((t / C::kNV) & 1) ^ 1, abort_flag, p.status)) {
             ok = false;
@@ -188,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(bar(C::bVFull + sv), C::kTile);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(sb + C::oV + sv * C::kTile + pn * C::kPanel, &tmV, bar(C::bVFull + sv), 64 * pn, row, u.hk, u.b);
+            tma_load_4d(sb + C::oV + sv * C::kTile + pn * C::kPanel, &tmV, bar(C::bVFull + sv), 64 * pn, row, u.hk,
+                        u.b);
           issuedV = t + 1;
         }
       }
@@ -504,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar(C::bPFull + x));
       }
       if (!ok) break;
-      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time. The accumulator is released (OFree) behind its last load.
+      // Epilogue: the row sum of both halves; this warp's D/2 columns of O / l, 32 at a time. The accumulator is
+      // released (OFree) behind its last load.
       float ltot = 0.f;
       if (blocks > 0) {
         xl[half * 128 + il] = lsum;
@@ -530,11 +534,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.lse_out[at] = has ? lse2 * 0.6931471805599453f : -INFINITY;
       }
       // (rows without keys of the split: the join does not read their part)
-      float* to_part = parts && in && has ? p.part + (part * rows + ((long long)b * p.Nq + i) * p.Hq + h) * D + (D / 2) * half
-                                          : nullptr;
-      uint16_t* to_out = !parts && in ? static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h +
-                                            (D / 2) * half
-                                      : nullptr;
+      float* to_part = nullptr;
+      uint16_t* to_out = nullptr;
+      if (parts && in && has)
+        to_part = p.part + (part * rows + ((long long)b * p.Nq + i) * p.Hq + h) * D + D / 2 * half;
+      if (!parts && in)
+        to_out = static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + D / 2 * half;
 #pragma unroll 1
       for (int cc = 0; cc < D / 64; ++cc) {
         uint32_t r[32];  // (set on every path: left undefined on one, values of the blocks' loop spilled)
@@ -551,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) r[e] = has ? r[e] : 0u;
-        store_columns32<kBf16>(r, inv, parts, to_part ? to_part + 32 * cc : nullptr, to_out ? to_out + 32 * cc : nullptr);
+        store_columns32<kBf16>(r, inv, parts, to_part ? to_part + 32 * cc : nullptr,
+                               to_out ? to_out + 32 * cc : nullptr);
       }
       __syncwarp();
     }
@@ -574,8 +580,7 @@ cudaError_t launch_t(const CrossParams& p, const CUtensorMap* maps, cudaStream_t
   if (e != cudaSuccess) return e;
   const long long units = (long long)p.B * p.Hk * ((p.plan.q_tile.count(p.Nq, p.G) + 1) / 2) * p.plan.k_splits;
   const long long blocks = std::max(std::min(units, 152ll), (units + kMostUnits - 1) / kMostUnits);
-  return launch_chained_maps(kKernel, dim3((unsigned)blocks), kThreads, bytes, st, p, maps[0],
-                             maps[1], maps[2]);
+  return launch_chained_maps(kKernel, dim3((unsigned)blocks), kThreads, bytes, st, p, maps[0], maps[1], maps[2]);
 }
 
 }  // namespace

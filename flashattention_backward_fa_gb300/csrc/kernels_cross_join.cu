@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __
   wait_for_previous();
   const int blocks = (p.nq_pad + preprocess_rows<D>() - 1) / preprocess_rows<D>(), bh = blockIdx.x / blocks;
   const int b = bh / p.Hq, h = bh - b * p.Hq, nq = cross_q_len(p, b);
-  const int first = (blockIdx.x - bh * blocks) * preprocess_rows<D>() + threadIdx.x / kLanes, e = 8 * (threadIdx.x % kLanes);
+  const int e = 8 * (threadIdx.x % kLanes);
+  const int first = (blockIdx.x - bh * blocks) * preprocess_rows<D>() + threadIdx.x / kLanes;
   const T* o = static_cast<const T*>(p.o) + b * p.o_st.b + h * p.o_st.h + e;
   const T* g = static_cast<const T*>(p.dout) + b * p.do_st.b + h * p.do_st.h + e;
   Raw8<T> ro[kRowsEach], rg[kRowsEach];
@@ -201,7 +202,8 @@ __device__ __forceinline__ void join_rows(const CrossParams& p, const float* par
   const int quads = (p.d + 3) >> 2;
   const long long n = (long long)p.B * N * H * quads;
   const bool vec = (p.d & 3) == 0;
-  for (long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kJoinThreads) {
+  const long long apart_x = (long long)gridDim.x * kJoinThreads;
+  for (long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x; x < n; x += apart_x) {
     const long long row = x / quads, bt = row / H;
     const int e = 4 * (int)(x - row * quads), h = (int)(row - bt * H), b = (int)(bt / N);
     const int t = (int)(bt - (long long)b * N);
@@ -263,11 +265,12 @@ cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_
   }
   const int rows = p.d == 64 ? preprocess_rows<64>() : preprocess_rows<128>();
   const dim3 grid((unsigned)(heads * ((p.nq_pad + rows - 1) / rows)));
+  const bool bf16 = dtype == FA_BF16;
   if (p.d == 64)
-    return dtype == FA_BF16 ? launch_chained(cross_preprocess_kernel<__nv_bfloat16, 64>, grid, kJoinThreads, 0, 1, p, st)
-                            : launch_chained(cross_preprocess_kernel<__half, 64>, grid, kJoinThreads, 0, 1, p, st);
-  return dtype == FA_BF16 ? launch_chained(cross_preprocess_kernel<__nv_bfloat16, 128>, grid, kJoinThreads, 0, 1, p, st)
-                          : launch_chained(cross_preprocess_kernel<__half, 128>, grid, kJoinThreads, 0, 1, p, st);
+    return launch_chained(bf16 ? cross_preprocess_kernel<__nv_bfloat16, 64> : cross_preprocess_kernel<__half, 64>, grid,
+                          kJoinThreads, 0, 1, p, st);
+  return launch_chained(bf16 ? cross_preprocess_kernel<__nv_bfloat16, 128> : cross_preprocess_kernel<__half, 128>, grid,
+                        kJoinThreads, 0, 1, p, st);
 }
 
 template <typename T>
@@ -275,7 +278,8 @@ static cudaError_t launch_join_fwd(const CrossParams& p, cudaStream_t st) {
   const long long rows = (long long)p.B * p.Nq * p.Hq;
   const int n = p.plan.k_splits;
   if (n > 16) return launch_chained(cross_join_fwd_kernel<T, 8>, dim3((unsigned)rows), kJoinThreads, 0, 1, p, st);
-  if (n > 8) return launch_chained(cross_join_fwd_kernel<T, 2>, dim3((unsigned)((rows + 3) / 4)), kJoinThreads, 0, 1, p, st);
+  if (n > 8)
+    return launch_chained(cross_join_fwd_kernel<T, 2>, dim3((unsigned)((rows + 3) / 4)), kJoinThreads, 0, 1, p, st);
   return launch_chained(cross_join_fwd_kernel<T, 1>, dim3((unsigned)((rows + 7) / 8)), kJoinThreads, 0, 1, p, st);
 }
 
