@@ -167,7 +167,8 @@ __device__ __forceinline__ void load_rotation(const float* cos_row, const float*
 
 // The same where the pairs' rows differ by their axes (RopeAxes): the token's positions on all axes are
 // read side by side, then each run of four pairs with one axis by 16-byte loads and others value by
-// value. b, n: the token's place in the positions.
+// value (16-byte loads of every axis' row with selects instead: bf16 4x16x2048x128 into the cache, axes in
+// turn, 45.5 us against 44.0). b, n: the token's place in the positions.
 template <bool kNeighbours, typename Axes>
 __device__ __forceinline__ void load_rotation_axes(const Axes& ax, const float* cos, const float* sin, int max_pos,
                                                    long long b, long long n, const LanePlace& at, int rot,

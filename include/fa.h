@@ -490,7 +490,8 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * workspaces of their own.
  * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
  * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, rounded
- * once (off by at most 2^-9 of themselves in bf16, 2^-12 in fp16); their rounding residual
+ * once (off by at most 2^-8 of themselves in bf16, 2^-11 in fp16 and 2^-25 where they are
+ * below its normal values); their rounding residual
  * is multiplied too in the backward where a probability of the tile exceeds 1/4, and in the
  * forward where a key head has few query rows (16, or up to 64 in small calls). Errors as
  * fa_fwd / fa_bwd.
