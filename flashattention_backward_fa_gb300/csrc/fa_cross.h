@@ -179,6 +179,26 @@ __device__ __forceinline__ void store_rows64(uint4 (&u)[4], char* to) {
   }
 }
 
+// The same with 32 bytes of each row, by pairs of lanes.
+__device__ __forceinline__ void store_rows32(uint4 (&u)[2], char* to) {
+  const int lane = threadIdx.x & 31;
+  uint4 give = lane & 1 ? u[0] : u[1];
+  give.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+  give.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+  give.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+  give.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+  if (lane & 1)
+    u[0] = give;
+  else
+    u[1] = give;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const auto whole = reinterpret_cast<unsigned long long>(to);
+    char* at = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, whole, (lane & ~1) + r));
+    if (at != nullptr) reinterpret_cast<uint4*>(at)[lane & 1] = u[r];
+  }
+}
+
 // 32 fp32 values of a row as 16-bit ones times mul, 16 as they are (times mul).
 template <bool kBf16>
 __device__ __forceinline__ void pack64(uint4 (&u)[4], const uint32_t (&r)[32], float mul) {
@@ -215,6 +235,23 @@ __device__ __forceinline__ void store_columns32(const uint32_t (&r)[32], float m
   } else {
     pack64<kBf16>(u, r, mul);
     store_rows64(u, reinterpret_cast<char*>(out));
+  }
+}
+
+// The same with the first 16 columns of r.
+template <bool kBf16>
+__device__ __forceinline__ void store_columns16(const uint32_t (&r)[32], float mul, bool parts, float* part,
+                                                uint16_t* out) {
+  uint4 u[4];
+  if (parts) {
+    pack64(u, r, mul);
+    store_rows64(u, reinterpret_cast<char*>(part));
+  } else {
+    uint4 v[2];
+    pack64<kBf16>(u, r, mul);
+    v[0] = u[0];
+    v[1] = u[1];
+    store_rows32(v, reinterpret_cast<char*>(out));
   }
 }
 

@@ -564,11 +564,16 @@ struct QCfg {
   static constexpr int bSEmpty = bSFull + 2;           // [2] dQ MMA done with the image
   static constexpr int bDPEmpty = bSEmpty + 2;         // row math has read dP
   static constexpr int bPFull = bDPEmpty + 1;          // [2] dS image written
-  static constexpr int bAcc = bPFull + 2;
-  static constexpr int bDrain = bAcc + 1;              // one per MMA-issuing warp
+  // Accumulators, units in turn. With d = 64 there is room for two, and a unit's epilogue runs behind the next
+  // unit's first step, so that its last dQ MMA and the next S and dP are under way meanwhile: with one key block a
+  // unit (77 keys) 5.6 k cycles a unit before, 3.8 since (backward of 2x16/4 4095x77 57 -> 52 us). With one accumulator the next unit's first MMA waited for
+  // the epilogue (4x16 2048x512 138 -> 139.5 us).
+  static constexpr int kAcc = D == 64 ? 2 : 1;
+  static constexpr int bAcc = bPFull + 2;              // [kAcc] dQ of a unit complete
+  static constexpr int bDrain = bAcc + kAcc;           // one per MMA-issuing warp
   static constexpr int bResFree = bDrain + 3;          // a unit's last reads of Q and dO done
-  static constexpr int bAccFree = bResFree + 1;        // the epilogue has read the accumulator
-  static constexpr int kBars = bAccFree + 1;
+  static constexpr int bAccFree = bResFree + 1;        // [kAcc] the epilogue has read the accumulator
+  static constexpr int kBars = bAccFree + kAcc;
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [buffer][16 warps] split votes
@@ -610,10 +615,12 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
       mbar_init(bar(C::bPFull + x), 512);
     }
     mbar_init(bar(C::bDPEmpty), 512);
-    mbar_init(bar(C::bAcc), 1);
+    for (int x = 0; x < C::kAcc; ++x) {
+      mbar_init(bar(C::bAcc + x), 1);
+      mbar_init(bar(C::bAccFree + x), 512);  // every row-math warp
+    }
     for (int x = 0; x < 3; ++x) mbar_init(bar(C::bDrain + x), 1);
     mbar_init(bar(C::bResFree), 2);    // S and dP issuers
-    mbar_init(bar(C::bAccFree), 512);  // every row-math warp
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -734,10 +741,12 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
       i = uniform(i);
       const int blocks = uniform(unit[i].blocks);
       const int j_begin = uniform(unit[i].j_begin), j_end = uniform(unit[i].j_end);
+      const int x = kl % C::kAcc, turn = kl / C::kAcc;
       for (int it = 0; it < blocks; ++it, ++G) {
         const int bt = G & 1, sk = G % C::kNK;
         if (!warp_wait<kConsumerPoll>(bar(C::bPFull + bt), (G >> 1) & 1, abort_flag, p.status) ||
-            (it == 0 && kl > 0 && !warp_wait<kConsumerPoll>(bar(C::bAccFree), (kl - 1) & 1, abort_flag, p.status))) {
+            (it == 0 && turn > 0 &&
+             !warp_wait<kConsumerPoll>(bar(C::bAccFree + x), (turn - 1) & 1, abort_flag, p.status))) {
           ok = false;
           break;
         }
@@ -748,21 +757,21 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 16 * bt);
         int any = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) any |= f4[x].x | f4[x].y | f4[x].z | f4[x].w;
+        for (int f = 0; f < 4; ++f) any |= f4[f].x | f4[f].y | f4[f].z | f4[f].w;
         const uint64_t bop = desc_add(b0, sk * C::kTile);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc_mma_ts_w(tAcc, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO, kk > 0 || it > 0 ? 1u : 0u);
+          tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO, kk > 0 || it > 0 ? 1u : 0u);
         if (uniform(any)) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts_w(tAcc, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
+            tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
         }
         tc_commit_w(bar(C::bSEmpty + bt));
         tc_commit_w(bar(C::bKEmpty + sk));
       }
       if (!ok) break;
-      tc_commit_w(bar(C::bAcc));
+      tc_commit_w(bar(C::bAcc + x));
     }
     tc_commit_w(bar(C::bDrain + 1));
     if (lane == 0) mbar_wait_drain(bar(C::bDrain + 1), 0, p.status);
@@ -793,137 +802,135 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     };
     float nL2, nD, nL2_next, nD_next;
     row_of(0, nL2, nD);
-    for (int ui = 0; ok && ui < mine; ++ui, nL2 = nL2_next, nD = nD_next) {
-      const CrossUnit& u = unit[ui];
+    constexpr bool kLater = C::kAcc == 2;  // (see kAcc; the round of ui = mine then has an epilogue alone)
+    for (int ui = 0; ok && ui < mine + kLater; ++ui, nL2 = nL2_next, nD = nD_next) {
+      const CrossUnit& u = unit[min(ui, mine - 1)];
       // left: real keys from this warpgroup's first column on
-      const int blocks = u.blocks, left = u.j_end - u.j_begin - 32 * c;
-      row_of(ui + 1, nL2_next, nD_next);
+      const int blocks = ui < mine ? u.blocks : 0, left = u.j_end - u.j_begin - 32 * c;
+      if (!kLater) row_of(ui + 1, nL2_next, nD_next);
       const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
-      for (int it = 0; it < blocks; ++it) {
-        const int gs = G + it, bb = gs & 1;
-        const uint32_t tSc = tS + lane_off + 128 * bb + 32 * c;
-        const uint32_t allow = bit_range(0, left - 128 * it);
-        if (!warp_wait<kRowMathPoll>(bar(C::bSFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        // both halves of dP come in with S, so the dP buffer is released before any arithmetic
-        uint32_t sr[16], dr[2][16];
-        __syncwarp();
-        tmem_ld16(tSc, sr);
-        tmem_ld16(tdPc, dr[0]);
-        tmem_ld16(tdPc + 16, dr[1]);
-        tmem_ld_wait16x3(sr, dr[0], dr[1]);
-        tc_fence_before();
-        warp_arrive(bar(C::bDPEmpty));
-        bool lo_any = false;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          if (hh == 1) {
-            __syncwarp();
-            tmem_ld16(tSc + 16, sr);
-            tmem_ld_wait16(sr);
+      int it = 0;
+      do {
+        if (it < blocks) {
+          const int gs = G + it, bb = gs & 1;
+          const uint32_t tSc = tS + lane_off + 128 * bb + 32 * c;
+          const uint32_t allow = bit_range(0, left - 128 * it);
+          if (!warp_wait<kRowMathPoll>(bar(C::bSFull + bb), (gs >> 1) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
           }
-          float ds[16];
-          float cmax = 0.f;
-          auto elementwise = [&](auto masked) {
+          tc_fence_after();
+          // both halves of dP come in with S, so the dP buffer is released before any arithmetic
+          uint32_t sr[16], dr[2][16];
+          __syncwarp();
+          tmem_ld16(tSc, sr);
+          tmem_ld16(tdPc, dr[0]);
+          tmem_ld16(tdPc + 16, dr[1]);
+          tmem_ld_wait16x3(sr, dr[0], dr[1]);
+          tc_fence_before();
+          warp_arrive(bar(C::bDPEmpty));
+          bool lo_any = false;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float p0, p1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, l2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              const uint64_t dd = f2_add(f2_pack(__uint_as_float(dr[hh][e]), __uint_as_float(dr[hh][e + 1])), d2);
-              f2_unpack(f2_mul(f2_pack(p0, p1), dd), ds[e], ds[e + 1]);
-              if constexpr (decltype(masked)::value) {
-                const bool in0 = (allow >> (16 * hh + e)) & 1u, in1 = (allow >> (16 * hh + e + 1)) & 1u;
-                p0 = in0 ? p0 : 0.f;
-                p1 = in1 ? p1 : 0.f;
-                ds[e] = in0 ? ds[e] : 0.f;
-                ds[e + 1] = in1 ? ds[e + 1] : 0.f;
-              }
-              cmax = fmax3(cmax, p0, p1);
+          for (int hh = 0; hh < 2; ++hh) {
+            if (hh == 1) {
+              __syncwarp();
+              tmem_ld16(tSc + 16, sr);
+              tmem_ld_wait16(sr);
             }
-          };
-          // (the mask is the same for the whole warp)
-          if (allow == 0xFFFFFFFFu)
-            elementwise(std::false_type{});
-          else
-            elementwise(std::true_type{});
-          uint32_t hv[8], ev[8];
+            float ds[16];
+            float cmax = 0.f;
+            auto elementwise = [&](auto masked) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) hv[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
-          const bool split = __any_sync(0xFFFFFFFFu, row_in && cmax > kCrossSplit);
-          lo_any |= split;
-          if (split) {
+              for (int e = 0; e < 16; e += 2) {
+                float p0, p1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, l2), p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                const uint64_t dd = f2_add(f2_pack(__uint_as_float(dr[hh][e]), __uint_as_float(dr[hh][e + 1])), d2);
+                f2_unpack(f2_mul(f2_pack(p0, p1), dd), ds[e], ds[e + 1]);
+                if constexpr (decltype(masked)::value) {
+                  const bool in0 = (allow >> (16 * hh + e)) & 1u, in1 = (allow >> (16 * hh + e + 1)) & 1u;
+                  p0 = in0 ? p0 : 0.f;
+                  p1 = in1 ? p1 : 0.f;
+                  ds[e] = in0 ? ds[e] : 0.f;
+                  ds[e + 1] = in1 ? ds[e + 1] : 0.f;
+                }
+                cmax = fmax3(cmax, p0, p1);
+              }
+            };
+            // (the mask is the same for the whole warp)
+            if (allow == 0xFFFFFFFFu)
+              elementwise(std::false_type{});
+            else
+              elementwise(std::true_type{});
+            uint32_t hv[8], ev[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) ev[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hv[x]);
-          } else {
+            for (int x = 0; x < 8; ++x) hv[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
+            const bool split = __any_sync(0xFFFFFFFFu, row_in && cmax > kCrossSplit);
+            lo_any |= split;
+            if (split) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) ev[x] = 0u;
+              for (int x = 0; x < 8; ++x) ev[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hv[x]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) ev[x] = 0u;
+            }
+            tmem_st8<0>(tSc + 16 * hh, hv);
+            tmem_st8<0>(tSc + 16 * hh + 8, ev);
           }
-          tmem_st8<0>(tSc + 16 * hh, hv);
-          tmem_st8<0>(tSc + 16 * hh + 8, ev);
+          tmem_st_wait();
+          if (lane == 0) flags[16 * bb + 4 * c + wq] = lo_any ? 1 : 0;
+          tc_fence_before();
+          warp_arrive(bar(C::bPFull + bb));
         }
-        tmem_st_wait();
-        if (lane == 0) flags[16 * bb + 4 * c + wq] = lo_any ? 1 : 0;
-        tc_fence_before();
-        warp_arrive(bar(C::bPFull + bb));
-      }
-      if (!ok) break;
-      // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
-      // (AccFree) before the stores, so the next unit's first MMA can start meanwhile.
-      uint32_t r[32];  // (D / 4 of them)
+        if (kLater ? it > 0 : it + 1 < blocks) continue;
+        if (kLater) row_of(ui + 1, nL2_next, nD_next);
+        if (kLater && ui == 0) continue;
+        // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
+        // (AccFree) before the stores, so the next MMA into it can start meanwhile.
+        const CrossUnit& to = unit[ui - kLater];
+        uint32_t r[32];  // (D / 4 of them)
 #pragma unroll
-      for (int x = 0; x < 32; ++x) r[x] = 0u;
-      if (blocks > 0) {
-        if (!warp_wait<kRowMathPoll>(bar(C::bAcc), kl & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
+        for (int x = 0; x < 32; ++x) r[x] = 0u;
+        if (to.blocks > 0) {
+          const int x = kl % C::kAcc;
+          if (!warp_wait<kRowMathPoll>(bar(C::bAcc + x), kl / C::kAcc & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t col0 = tAcc + 64 * x + lane_off + c * (D / 4);
+          if constexpr (D == 128) {
+            tmem_ld32(col0, r);
+            tmem_ld_wait(r);
+          } else {
+            uint32_t half[16];
+            tmem_ld16(col0, half);
+            tmem_ld_wait16(half);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) r[y] = half[y];
+          }
+          tc_fence_before();
+          warp_arrive(bar(C::bAccFree + x));
+          ++kl;
         }
-        tc_fence_after();
-        const uint32_t col0 = tAcc + lane_off + c * (D / 4);
-        if constexpr (D == 128) {
-          tmem_ld32(col0, r);
-          tmem_ld_wait(r);
-        } else {
-          uint32_t half[16];
-          tmem_ld16(col0, half);
-          tmem_ld_wait16(half);
+        const int i = to.q0[0] + row_q, h = to.h0[0] + row_h, b = to.b, nq = to.nq;
+        const bool parts = p.plan.k_splits > 1, in = row_in && i < (parts ? nq : p.Nq);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) r[x] = half[x];
-        }
-        tc_fence_before();
-        warp_arrive(bar(C::bAccFree));
-        ++kl;
-      }
-      const int i = u.q0[0] + row_q, h = u.h0[0] + row_h, b = u.b, nq = u.nq;
-      const bool parts = p.plan.k_splits > 1, in = row_in && i < (parts ? nq : p.Nq);
-#pragma unroll
-      for (int x = 0; x < 32; ++x) r[x] = i < nq ? r[x] : 0u;  // (rows that are not there may hold NaN)
-      float* to_part = parts && in ? p.part + ((((long long)u.split * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4)
-                                   : nullptr;
-      uint16_t* const grad = static_cast<uint16_t*>(p.out);
-      uint16_t* to_out = !parts && in ? grad + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4) : nullptr;
-      const float mul = parts ? 1.f : p.scale;
-      if constexpr (D == 128) {
-        store_columns32<kBf16>(r, mul, parts, to_part, to_out);
-      } else if (parts) {
-        uint4 v[4];
-        pack64(v, r, mul);
-        store_rows64(v, reinterpret_cast<char*>(to_part));
-      } else if (to_out != nullptr) {  // 32 bytes a row
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack2<kBf16>(__uint_as_float(r[8 * t + 2 * e]) * mul, __uint_as_float(r[8 * t + 2 * e + 1]) * mul);
-          reinterpret_cast<uint4*>(to_out)[t] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      __syncwarp();
+        for (int x = 0; x < 32; ++x) r[x] = i < nq ? r[x] : 0u;  // (rows that are not there may hold NaN)
+        float* to_part = nullptr;
+        uint16_t* to_out = nullptr;
+        if (parts && in)
+          to_part = p.part + ((((long long)to.split * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4);
+        if (!parts && in)
+          to_out = static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4);
+        const float mul = parts ? 1.f : p.scale;
+        if constexpr (D == 128)
+          store_columns32<kBf16>(r, mul, parts, to_part, to_out);
+        else
+          store_columns16<kBf16>(r, mul, parts, to_part, to_out);
+        __syncwarp();
+      } while (ok && ++it < blocks);
       G += blocks;
     }
   }
