@@ -566,8 +566,8 @@ struct QCfg {
   static constexpr int bPFull = bDPEmpty + 1;          // [2] dS image written
   // Accumulators, units in turn. With d = 64 there is room for two, and a unit's epilogue runs behind the next
   // unit's first step, so that its last dQ MMA and the next S and dP are under way meanwhile: with one key block a
-  // unit (77 keys) 5.6 k cycles a unit before, 3.8 since (backward of 2x16/4 4095x77 57 -> 52 us). With one accumulator the next unit's first MMA waited for
-  // the epilogue (4x16 2048x512 138 -> 139.5 us).
+  // unit (77 keys) 5.6 k cycles a unit before, 3.8 since (backward of 2x16/4 4095x77 57 -> 52 us). With one
+  // accumulator the next unit's first MMA waited for the epilogue (4x16 2048x512 138 -> 139.5 us).
   static constexpr int kAcc = D == 64 ? 2 : 1;
   static constexpr int bAcc = bPFull + 2;              // [kAcc] dQ of a unit complete
   static constexpr int bDrain = bAcc + kAcc;           // one per MMA-issuing warp

@@ -99,6 +99,22 @@ def test_few_rows(size, k_lens, dtype):
     assert fa.fa_get_device_status() == 0
 
 
+@pytest.mark.parametrize("size, k_lens", [
+    ((1, 100, 3000, 2, 2, 64), None),
+    ((3, 100, 2500, 2, 2, 128), [2500, 0, 129]),
+    ((7, 31, 2049, 8, 2, 64), [1, 128, 129, 256, 257, 1000, 2049]),
+    ((1, 64, 9000, 4, 2, 128), [8897]),
+    ((44, 70, 1300, 4, 4, 64), [0, 1, 100, 128, 129, 300, 513, 1024, 1025, 1200, 1300] * 4),
+])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_one_row_tile(size, k_lens, dtype):
+    """Up to 128 query rows a key head and keys enough to share out: even and odd key blocks, some without a block."""
+    q, k, v, do = make(*size, dtype)
+    lens = None if k_lens is None else ints(k_lens)
+    o, lse = fa.cross_attention_forward(q, k, v, k_lens=lens)
+    Reference(q, k, v, None, lens).check_forward(o, lse)
+
+
 @pytest.mark.parametrize("d", [1, 17, 63, 96, 128])
 def test_fp32_head_dimensions(d):
     run(*make(2, 70, 45, 4, 2, d, F32))
