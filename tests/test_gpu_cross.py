@@ -80,7 +80,8 @@ FEW = [
     ((1, 1, 40, 64, 1, 128), None), ((100, 1, 60, 8, 8, 64), None), ((1, 2, 6000, 8, 1, 128), [5999]),
     ((1, 5, 5000, 3, 1, 64), [129]),
     # several rounds of long blocks, longest sequences first; equal lengths, none
-    ((70, 1, 2100, 8, 8, 128), [(1000 + 700 * b) % 2101 for b in range(70)]), ((128, 1, 2048, 4, 4, 64), [2048, 0, 5] * 42 + [7, 7]),
+    ((70, 1, 2100, 8, 8, 128), [(1000 + 700 * b) % 2101 for b in range(70)]),
+    ((128, 1, 2048, 4, 4, 64), [2048, 0, 5] * 42 + [7, 7]),
 ]
 
 
@@ -217,14 +218,38 @@ def test_strides(dtype):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("Nq", [1, 520])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_past_32_bits(Nq, dtype):
+    """Rows 2^22 values apart, all tensors in one buffer: places beyond 2^31 values have the bits of packed tensors."""
+    Nk, H, d, apart = 520, 2, 64, 1 << 22
+    packed = make(1, Nq, Nk, H, H, d, dtype)
+    want = run(*packed)
+    room = torch.empty(519 * apart + 8 * H * d, dtype=dtype, device="cuda")
+    at = lambda i, N: room.as_strided((1, N, H, d), (Nk * apart, apart, d, 1), i * H * d)  # noqa: E731
+    q, k, v, do, o, dq, dk, dv = (at(i, N) for i, N in enumerate((Nq, Nk, Nk, Nq, Nq, Nq, Nk, Nk)))
+    for t, x in zip((q, k, v, do), packed):
+        t.copy_(x)
+    lse = torch.empty((1, H, Nq), device="cuda")
+    size = (1, Nq, Nk, H, H, d, dtype)
+    ws = [torch.empty(max(n(*size), 1), dtype=torch.uint8, device="cuda")
+          for n in (fa.fa_cross_fwd_workspace_size, fa.fa_cross_bwd_workspace_size)]
+    fa.fa_cross_fwd(q, k, v, o, lse, ws[0])
+    fa.fa_cross_bwd(q, k, v, o, do, lse, dq, dk, dv, ws[1])
+    for a, b in zip(want, (o, lse, dq, dk, dv)):
+        assert torch.equal(a, b)
+
+
 def test_outputs_of_the_caller():
     """The C entry points fill what they are given, with its strides, and nothing beside it."""
     q, k, v, do = make(2, 100, 70, 4, 2, 64, BF16)
     want = run(q, k, v, do)
     ws = torch.full((max(1, fa.fa_cross_fwd_workspace_size(2, 100, 70, 4, 2, 64, BF16)),), 255, dtype=torch.uint8,
                     device="cuda")
-    wb = torch.full((fa.fa_cross_bwd_workspace_size(2, 100, 70, 4, 2, 64, BF16),), 255, dtype=torch.uint8, device="cuda")
-    wide = [torch.full((2, t.shape[1] + 2, t.shape[2] + 1, 64 + 8), 7.0, dtype=BF16, device="cuda") for t in (q, q, k, k)]
+    wb = torch.full((fa.fa_cross_bwd_workspace_size(2, 100, 70, 4, 2, 64, BF16),), 255, dtype=torch.uint8,
+                    device="cuda")
+    wide = [torch.full((2, t.shape[1] + 2, t.shape[2] + 1, 64 + 8), 7.0, dtype=BF16, device="cuda")
+            for t in (q, q, k, k)]
     o, dq, dk, dv = (w[:, 1:-1, :-1, :64] for w in wide)
     lse = torch.empty((2, 4, 100), device="cuda")
     fa.fa_cross_fwd(q, k, v, o, lse, ws)
