@@ -9,7 +9,12 @@
 // of several where queries are few; the steps run over all heads of the group, so shared
 // key heads cost no extra sums), S^T and dP^T in double buffers, P^T and dS^T written back
 // over them in 16 bits with their rounding residual where the tile holds probabilities
-// above kCrossSplit, dV and dK in TMEM. dQ: 128 query rows on the lanes, steps of 128 keys.
+// above kCrossSplit, dV and dK in TMEM. dQ: 128 query rows on the lanes, steps of 128 keys,
+// dS always with its residual: a row's dS add up to 0, their roundings do not, and what is
+// left of them is multiplied by the mean of the keys under P, which is not small where q and
+// k share a large channel (error of dQ with such channels, bf16 3x16 1551 over 160 keys,
+// 2.7e-3 without residuals, 2.1e-3 with them; of the result's own rounding 1.7e-3; backward
+// of 1x32/8 8192x4096 1325 -> 1388 us). What remains is D's error by the 16 bits of O.
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //
@@ -576,8 +581,7 @@ struct QCfg {
   static constexpr int kBars = bAccFree + kAcc;
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
-  static constexpr uint32_t oFlags = (oAbort + 8 + 15) & ~15u;  // [buffer][16 warps] split votes
-  static constexpr uint32_t oUnits = oFlags + 2 * 16 * 4;        // [kMostUnits]
+  static constexpr uint32_t oUnits = oAbort + 8;       // [kMostUnits]
   static constexpr uint32_t kSmem = oUnits + kMostUnits * sizeof(CrossUnit) + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
@@ -590,7 +594,6 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
-  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
   const int mine = (cross_units<1>(p) - first + stride - 1) / stride;  // units of this block
   CrossUnit* const unit = reinterpret_cast<CrossUnit*>(smem + C::oUnits);
@@ -754,19 +757,13 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         const int from = j_end - j_begin - 128 * it, to = min(128, p.Nk - j_begin - 128 * it);
         if (from < to) zero_rows<C::kPanels>(sb + C::oK + sk * C::kTile, C::kPanel, from, to);
         tc_fence_after();
-        const int4* f4 = reinterpret_cast<const int4*>(const_cast<const int*>(flags) + 16 * bt);
-        int any = 0;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) any |= f4[f].x | f4[f].y | f4[f].z | f4[f].w;
         const uint64_t bop = desc_add(b0, sk * C::kTile);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO, kk > 0 || it > 0 ? 1u : 0u);
-        if (uniform(any)) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
         tc_commit_w(bar(C::bSEmpty + bt));
         tc_commit_w(bar(C::bKEmpty + sk));
       }
@@ -778,8 +775,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     __syncwarp();
   } else {
     // ---------------- row-math warpgroups + epilogue ----------------------
-    // Warpgroup c takes key columns [32c, 32c + 32) of every step, in halves of 16, and a
-    // quarter of the epilogue's columns.
+    // Warpgroup c takes key columns [32c, 32c + 32) of every step, in halves of 16 (a K step of the dQ MMA: 8
+    // rounded columns, then 8 residual ones), and a quarter of the epilogue's columns.
     const int c = (warp - 4) >> 2, wq = warp & 3;
     const int il = wq * 32 + lane;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
@@ -829,7 +826,6 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
           tmem_ld_wait16x3(sr, dr[0], dr[1]);
           tc_fence_before();
           warp_arrive(bar(C::bDPEmpty));
-          bool lo_any = false;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             if (hh == 1) {
@@ -838,7 +834,6 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
               tmem_ld_wait16(sr);
             }
             float ds[16];
-            float cmax = 0.f;
             auto elementwise = [&](auto masked) {
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
@@ -850,12 +845,9 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
                 f2_unpack(f2_mul(f2_pack(p0, p1), dd), ds[e], ds[e + 1]);
                 if constexpr (decltype(masked)::value) {
                   const bool in0 = (allow >> (16 * hh + e)) & 1u, in1 = (allow >> (16 * hh + e + 1)) & 1u;
-                  p0 = in0 ? p0 : 0.f;
-                  p1 = in1 ? p1 : 0.f;
                   ds[e] = in0 ? ds[e] : 0.f;
                   ds[e + 1] = in1 ? ds[e + 1] : 0.f;
                 }
-                cmax = fmax3(cmax, p0, p1);
               }
             };
             // (the mask is the same for the whole warp)
@@ -863,23 +855,15 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
               elementwise(std::false_type{});
             else
               elementwise(std::true_type{});
-            uint32_t hv[8], ev[8];
+            uint32_t hv[16];  // rounded, then the residuals
 #pragma unroll
-            for (int x = 0; x < 8; ++x) hv[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
-            const bool split = __any_sync(0xFFFFFFFFu, row_in && cmax > kCrossSplit);
-            lo_any |= split;
-            if (split) {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) ev[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hv[x]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 8; ++x) ev[x] = 0u;
+            for (int x = 0; x < 8; ++x) {
+              hv[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
+              hv[8 + x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hv[x]);
             }
-            tmem_st8<0>(tSc + 16 * hh, hv);
-            tmem_st8<0>(tSc + 16 * hh + 8, ev);
+            tmem_st16(tSc + 16 * hh, hv);
           }
           tmem_st_wait();
-          if (lane == 0) flags[16 * bb + 4 * c + wq] = lo_any ? 1 : 0;
           tc_fence_before();
           warp_arrive(bar(C::bPFull + bb));
         }

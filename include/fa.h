@@ -486,15 +486,16 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * The same inputs give the same bits on every run. `workspace`: 256-byte aligned,
  * fa_cross_*_workspace_size(...) bytes for the same shape; its contents on entry do
  * not matter. The forward's size is 0 where it needs none (workspace may then be null)
- * and both are for shapes that the calls refuse; calls that overlap on the GPU need
+ * and both are 0 for shapes that the calls refuse; calls that overlap on the GPU need
  * workspaces of their own.
  * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
  * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, rounded
  * once (off by at most 2^-8 of themselves in bf16, 2^-11 in fp16 and 2^-25 where they are
- * below its normal values); their rounding residual
- * is multiplied too in the backward where a probability of the tile exceeds 1/4, and in the
- * forward where a key head has few query rows (16, or up to 64 in small calls). Errors as
- * fa_fwd / fa_bwd.
+ * below its normal values); their rounding residual is multiplied too in dq, in dk and dv
+ * where a probability of the tile exceeds 1/4, and in the forward where a key head has few
+ * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits: with a
+ * handful of keys that is the larger part of the error of dq and dk. Errors as fa_fwd /
+ * fa_bwd.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int B, Nq, Nk, Hq, Hk, d;
