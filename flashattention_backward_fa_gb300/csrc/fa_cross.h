@@ -266,6 +266,21 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, uint32_t panel, int fro
   __syncwarp();
 }
 
+// c += a b of 16 x 8 x 16, one warp.
+template <bool kBf16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kBf16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_cross_join_bwd(const CrossParams& p, int dtype, cudaStream_t st);

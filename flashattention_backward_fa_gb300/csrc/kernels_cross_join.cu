@@ -1,8 +1,8 @@
 // Cross attention: what stands before and behind its products.
 //
-// * preprocess: D_i = rowsum(dO o O) and L_i, stored negated as the backward's
-//   addends, for every query row that takes part (-inf and 0 elsewhere, which makes
-//   the row's probabilities 0);
+// * preprocess: D_i = rowsum(dO o O) (or, with few keys, sum_j P_ij dP_ij, which it
+//   is) and L_i, stored negated as the backward's addends, for every query row that
+//   takes part (-inf and 0 elsewhere, which makes the row's probabilities 0);
 // * join of the forward's splits: with their log-sum-exps l_s,
 //   O = sum_s 2^(l_s - l) O_s, l = log2 sum_s 2^l_s;
 // * joins of dQ and of dK, dV: sums over the splits in ascending order, so that the
@@ -92,6 +92,72 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __
       const long long row = (long long)bh * p.nq_pad + i;
       p.nD[row] = -acc;
       p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
+    }
+  }
+}
+
+// 16-bit types and up to kFewKeysMost keys: D = sum_j P_ij dP_ij from the scores instead. rowsum(dO o O) has the
+// rounding of O to 16 bits in it, and over a handful of keys, where O is as large as V, that was the larger part
+// of the error of dQ and dK (1.6 to 2.2 times the results' own rounding; 1.0 to 1.4 so). A warp takes 16 rows of
+// one (b, h); S and dP by m16n8k16, everything by 4-byte loads of the operands' places. The backward of 2x16/4
+// 4095 over 16 keys, d = 64, takes 62 us with it and 51 without, 1x2 128 over 5 10.2 and 9.6 (a row's dots with
+// every key by lanes and shuffles: 88 and 11.7); beyond 16 keys O is smaller and the gain with it.
+constexpr int kFewKeysMost = 16;
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads)
+    cross_preprocess_few_keys_kernel(const __grid_constant__ CrossParams p) {
+  let_next_begin();
+  wait_for_previous();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, in_quad = lane & 3;
+  const int blocks = p.nq_pad / 128, bh = blockIdx.x / blocks, b = bh / p.Hq, h = bh - b * p.Hq;
+  const int nq = cross_q_len(p, b), nk = cross_k_len(p, b), row0 = (blockIdx.x - bh * blocks) * 128 + warp * 16;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_st.b + h * p.q_st.h + 2 * in_quad;
+  const uint16_t* g = static_cast<const uint16_t*>(p.dout) + b * p.do_st.b + h * p.do_st.h + 2 * in_quad;
+  const uint16_t* k = static_cast<const uint16_t*>(p.k) + b * p.k_st.b + h / p.G * p.k_st.h + 2 * in_quad;
+  const uint16_t* v = static_cast<const uint16_t*>(p.v) + b * p.v_st.b + h / p.G * p.v_st.h + 2 * in_quad;
+  const auto pair_at = [](bool real, const uint16_t* at) {
+    return real ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+  };
+  float s[2][4], dp[2][4];
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = dp[n][e] = 0.f;
+#pragma unroll
+  for (int st = 0; st < D / 16; ++st) {
+    uint32_t aq[4], ag[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {  // rows quad and quad + 8, columns 2 in_quad and + 8
+      const int i = row0 + quad + 8 * (x & 1), col = 16 * st + 8 * (x >> 1);
+      aq[x] = pair_at(i < nq, q + (i < nq ? i * p.q_st.n : 0) + col);
+      ag[x] = pair_at(i < nq, g + (i < nq ? i * p.do_st.n : 0) + col);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int j = 8 * n + quad;
+      const uint16_t *kj = k + (j < nk ? j * p.k_st.n : 0) + 16 * st, *vj = v + (j < nk ? j * p.v_st.n : 0) + 16 * st;
+      mma16816<kBf16>(s[n], aq, pair_at(j < nk, kj), pair_at(j < nk, kj + 8));
+      mma16816<kBf16>(dp[n], ag, pair_at(j < nk, vj), pair_at(j < nk, vj + 8));
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int i = row0 + quad + 8 * half;
+    const float nl = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
+    float acc = 0.f;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (nl != -INFINITY && 8 * n + 2 * in_quad + e < nk)
+          acc = fmaf(exp2f(fmaf(s[n][2 * half + e], p.scale_log2, nl)), dp[n][2 * half + e], acc);
+    acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+    acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+    if (in_quad == 0) {
+      const long long row = (long long)bh * p.nq_pad + i;
+      p.nD[row] = -acc;
+      p.nL2[row] = nl;
     }
   }
 }
@@ -263,9 +329,17 @@ cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_
     return launch_chained(cross_preprocess_f32_kernel, dim3((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32)),
                           kJoinThreads, 0, 1, p, st);
   }
+  const bool bf16 = dtype == FA_BF16;
+  if (p.Nk <= kFewKeysMost) {
+    const dim3 grid((unsigned)(heads * (p.nq_pad / 128)));
+    if (p.d == 64)
+      return bf16 ? launch_chained(cross_preprocess_few_keys_kernel<64, true>, grid, kJoinThreads, 0, 1, p, st)
+                  : launch_chained(cross_preprocess_few_keys_kernel<64, false>, grid, kJoinThreads, 0, 1, p, st);
+    return bf16 ? launch_chained(cross_preprocess_few_keys_kernel<128, true>, grid, kJoinThreads, 0, 1, p, st)
+                : launch_chained(cross_preprocess_few_keys_kernel<128, false>, grid, kJoinThreads, 0, 1, p, st);
+  }
   const int rows = p.d == 64 ? preprocess_rows<64>() : preprocess_rows<128>();
   const dim3 grid((unsigned)(heads * ((p.nq_pad + rows - 1) / rows)));
-  const bool bf16 = dtype == FA_BF16;
   if (p.d == 64)
     return launch_chained(bf16 ? cross_preprocess_kernel<__nv_bfloat16, 64> : cross_preprocess_kernel<__half, 64>, grid,
                           kJoinThreads, 0, 1, p, st);

@@ -434,8 +434,9 @@ int fa_kv8_norm_rope_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, 
  * of the call's tensors) instead of the tokens' places in their sequences. */
 int fa_kv8_norm_rope_axes_append(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* q, const void* k,
                                  const void* v, void* q_out, const void* q_weight, const void* k_weight,
-                                 const float* cos_table, const float* sin_table, const fa_rope_axes* axes, int T, int Hq,
-                                 int rot_dim, int interleaved, int max_pos, fa_strides q_strides, fa_strides k_strides,
+                                 const float* cos_table, const float* sin_table, const fa_rope_axes* axes, int T,
+                                 int Hq, int rot_dim, int interleaved, int max_pos, fa_strides q_strides,
+                                 fa_strides k_strides,
                                  fa_strides v_strides, fa_strides q_out_strides, fa_dtype dtype, fa_dtype weight_dtype,
                                  float eps, void* stream);
 
@@ -493,8 +494,8 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * once (off by at most 2^-8 of themselves in bf16, 2^-11 in fp16 and 2^-25 where they are
  * below its normal values); their rounding residual is multiplied too in dq, in dk and dv
  * where a probability of the tile exceeds 1/4, and in the forward where a key head has few
- * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits: with a
- * handful of keys that is the larger part of the error of dq and dk. Errors as fa_fwd /
+ * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits,
+ * or, with Nk <= 16, the scores, sum_j P_ij dP_ij (o is not read then). Errors as fa_fwd /
  * fa_bwd.
  * ------------------------------------------------------------------------- */
 typedef struct {
