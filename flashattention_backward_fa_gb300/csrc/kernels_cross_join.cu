@@ -97,67 +97,85 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __
 }
 
 // 16-bit types and up to kFewKeysMost keys: D = sum_j P_ij dP_ij from the scores instead. rowsum(dO o O) has the
-// rounding of O to 16 bits in it, and over a handful of keys, where O is as large as V, that was the larger part
-// of the error of dQ and dK (1.6 to 2.2 times the results' own rounding; 1.0 to 1.4 so). A warp takes 16 rows of
-// one (b, h); S and dP by m16n8k16, everything by 4-byte loads of the operands' places. The backward of 2x16/4
-// 4095 over 16 keys, d = 64, takes 62 us with it and 51 without, 1x2 128 over 5 10.2 and 9.6 (a row's dots with
-// every key by lanes and shuffles: 88 and 11.7); beyond 16 keys O is smaller and the gain with it.
-constexpr int kFewKeysMost = 16;
+// rounding of O to 16 bits in it, and over a handful of keys, where O is as large as V, or a few dozen where q, k
+// and v have large channels, that was the larger part of the error of dQ and dK (1.6 to 2.4 times the results' own
+// rounding; 1.0 to 1.4 so). A warp takes 16 rows of one (b, h), S and dP by m16n8k16, the block's keys and values in
+// shared memory, 16-byte pieces swizzled by row. The backward of 2x16/4 4095 over 16 keys, d = 64, takes 53.6 us
+// with it and 51.2 without, over 64 keys 59.6 and 51.0, 4x16 2048 over 64 keys, d = 128, 97 and 84, 1x2 128 over 5
+// 9.8 and 9.6; with more keys the two products cost more, and O is smaller.
+constexpr int kFewKeysMost = 64;
 
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
     cross_preprocess_few_keys_kernel(const __grid_constant__ CrossParams p) {
+  __shared__ __align__(128) uint16_t sk[kFewKeysMost * D], sv[kFewKeysMost * D];
   let_next_begin();
   wait_for_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, in_quad = lane & 3;
   const int blocks = p.nq_pad / 128, bh = blockIdx.x / blocks, b = bh / p.Hq, h = bh - b * p.Hq;
   const int nq = cross_q_len(p, b), nk = cross_k_len(p, b), row0 = (blockIdx.x - bh * blocks) * 128 + warp * 16;
+  const int tiles = (nk + 7) / 8;
+  const uint16_t* k = static_cast<const uint16_t*>(p.k) + b * p.k_st.b + h / p.G * p.k_st.h;
+  const uint16_t* v = static_cast<const uint16_t*>(p.v) + b * p.v_st.b + h / p.G * p.v_st.h;
+  for (int x = threadIdx.x; x < 8 * tiles * (D / 8); x += kJoinThreads) {
+    const int j = x / (D / 8), piece = x % (D / 8), to = j * D + 8 * (piece ^ (j & 7));
+    uint4 kv[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (j < nk) {
+      kv[0] = *reinterpret_cast<const uint4*>(k + j * p.k_st.n + 8 * piece);
+      kv[1] = *reinterpret_cast<const uint4*>(v + j * p.v_st.n + 8 * piece);
+    }
+    *reinterpret_cast<uint4*>(sk + to) = kv[0];
+    *reinterpret_cast<uint4*>(sv + to) = kv[1];
+  }
+  // Q and dO as A operands: rows quad and quad + 8, columns 2 in_quad and + 8 of every 16 (zeros where there is none)
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + b * p.q_st.b + h * p.q_st.h + 2 * in_quad;
   const uint16_t* g = static_cast<const uint16_t*>(p.dout) + b * p.do_st.b + h * p.do_st.h + 2 * in_quad;
-  const uint16_t* k = static_cast<const uint16_t*>(p.k) + b * p.k_st.b + h / p.G * p.k_st.h + 2 * in_quad;
-  const uint16_t* v = static_cast<const uint16_t*>(p.v) + b * p.v_st.b + h / p.G * p.v_st.h + 2 * in_quad;
-  const auto pair_at = [](bool real, const uint16_t* at) {
-    return real ? *reinterpret_cast<const uint32_t*>(at) : 0u;
-  };
-  float s[2][4], dp[2][4];
+  uint32_t aq[D / 16][4], ag[D / 16][4];
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
+  for (int x = 0; x < 4; ++x) {
+    const int i = row0 + quad + 8 * (x & 1);
+    const uint16_t *qi = q + (i < nq ? i * p.q_st.n : 0), *gi = g + (i < nq ? i * p.do_st.n : 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[n][e] = dp[n][e] = 0.f;
-#pragma unroll
-  for (int st = 0; st < D / 16; ++st) {
-    uint32_t aq[4], ag[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {  // rows quad and quad + 8, columns 2 in_quad and + 8
-      const int i = row0 + quad + 8 * (x & 1), col = 16 * st + 8 * (x >> 1);
-      aq[x] = pair_at(i < nq, q + (i < nq ? i * p.q_st.n : 0) + col);
-      ag[x] = pair_at(i < nq, g + (i < nq ? i * p.do_st.n : 0) + col);
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int j = 8 * n + quad;
-      const uint16_t *kj = k + (j < nk ? j * p.k_st.n : 0) + 16 * st, *vj = v + (j < nk ? j * p.v_st.n : 0) + 16 * st;
-      mma16816<kBf16>(s[n], aq, pair_at(j < nk, kj), pair_at(j < nk, kj + 8));
-      mma16816<kBf16>(dp[n], ag, pair_at(j < nk, vj), pair_at(j < nk, vj + 8));
+    for (int st = 0; st < D / 16; ++st) {
+      const int col = 16 * st + 8 * (x >> 1);
+      aq[st][x] = i < nq ? *reinterpret_cast<const uint32_t*>(qi + col) : 0u;
+      ag[st][x] = i < nq ? *reinterpret_cast<const uint32_t*>(gi + col) : 0u;
     }
   }
+  float nl[2], acc[2] = {0.f, 0.f};
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int i = row0 + quad + 8 * half;
-    const float nl = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
-    float acc = 0.f;
+    nl[half] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
+  }
+  __syncthreads();
+  const int mat = lane >> 3, mrow = lane & 7;  // ldmatrix: lane i gives the address of row i % 8 of matrix i / 8
+  for (int n = 0; n < tiles; ++n) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int st = 0; st < D / 32; ++st) {
+      uint32_t kb[4], vb[4];
+      const int at = (8 * n + mrow) * D + 8 * ((4 * st + mat) ^ mrow);
+      ldmatrix4(kb, smem_u32(sk + at));
+      ldmatrix4(vb, smem_u32(sv + at));
+      mma16816<kBf16>(s, aq[2 * st], kb[0], kb[1]);
+      mma16816<kBf16>(dp, ag[2 * st], vb[0], vb[1]);
+      mma16816<kBf16>(s, aq[2 * st + 1], kb[2], kb[3]);
+      mma16816<kBf16>(dp, ag[2 * st + 1], vb[2], vb[3]);
+    }
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (nl != -INFINITY && 8 * n + 2 * in_quad + e < nk)
-          acc = fmaf(exp2f(fmaf(s[n][2 * half + e], p.scale_log2, nl)), dp[n][2 * half + e], acc);
-    acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-    acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+    for (int e = 0; e < 4; ++e)
+      if (nl[e >> 1] != -INFINITY && 8 * n + 2 * in_quad + (e & 1) < nk)
+        acc[e >> 1] = fmaf(exp2f(fmaf(s[e], p.scale_log2, nl[e >> 1])), dp[e], acc[e >> 1]);
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    acc[half] += __shfl_xor_sync(0xffffffffu, acc[half], 1);
+    acc[half] += __shfl_xor_sync(0xffffffffu, acc[half], 2);
     if (in_quad == 0) {
-      const long long row = (long long)bh * p.nq_pad + i;
-      p.nD[row] = -acc;
-      p.nL2[row] = nl;
+      const long long row = (long long)bh * p.nq_pad + row0 + quad + 8 * half;
+      p.nD[row] = -acc[half];
+      p.nL2[row] = nl[half];
     }
   }
 }

@@ -10,7 +10,7 @@ Bounds. u is half a step of the tensors' type (eps / 2). What is computed differ
   tensor cores add in no more steps), so a score by n 2^-24 scale sum |q k|, n = d + 8, and P by that much of
   itself and 2^-21 (exp2, log2 and the division, each a few 2^-24); sums over keys or queries by their number;
 * the backward's D = rowsum(dO o O) takes the O that the forward rounded: off by u sum |dO O|, and by the
-  fp32 sum's share; with 16-bit tensors of up to 16 keys it is sum P dP instead, off by what P and dP are and
+  fp32 sum's share; with 16-bit tensors of up to 64 keys it is sum P dP instead, off by what P and dP are and
   the fp32 sum's share.
 """
 import math
@@ -67,8 +67,8 @@ class Reference:
                 self.dq[b, :n, h] = scale * ds @ kh
                 self.dk[b, :m, h // G] += scale * ds.T @ qh
                 dp_err = (d + 8) * e * (g.abs() @ vh.abs().T)
-                if up and Nk <= 16:
-                    go = (p * dp_err + (p_rel + 24 * e) * p * dp.abs()).sum(-1, keepdim=True)
+                if up and Nk <= 64:
+                    go = (p * dp_err + (p_rel + (Nk + 16) * e) * p * dp.abs()).sum(-1, keepdim=True)
                 else:
                     go = (g.abs() * self.o_tol[b, :n, h]).sum(-1, keepdim=True) + \
                         (d + 8) * e * (g.abs() * self.o[b, :n, h].abs()).sum(-1, keepdim=True)
