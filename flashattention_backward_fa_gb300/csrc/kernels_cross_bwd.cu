@@ -14,7 +14,7 @@
 // left of them is multiplied by the mean of the keys under P, which is not small where q and
 // k share a large channel (error of dQ with such channels, bf16 3x16 1551 over 160 keys,
 // 2.7e-3 without residuals, 2.1e-3 with them; of the result's own rounding 1.7e-3; backward
-// of 1x32/8 8192x4096 1325 -> 1388 us). What remains is D's error by the 16 bits of O.
+// of 1x32/8 8192x4096 1325 -> 1388 us). What remains is, over more than 64 keys, D's error by O's 16 bits.
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //
@@ -760,7 +760,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         const uint64_t bop = desc_add(b0, sk * C::kTile);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO, kk > 0 || it > 0 ? 1u : 0u);
+          tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk, desc_add(bop, 2048 * kk), idO,
+                      kk > 0 || it > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           tc_mma_ts_w(tAcc + 64 * x, tS + 128 * bt + 16 * kk + 8, desc_add(bop, 2048 * kk), idO, 1u);
