@@ -1,6 +1,6 @@
 // Cross attention: what stands before and behind its products.
 //
-// * preprocess: D_i = rowsum(dO o O) (or, with few keys, sum_j P_ij dP_ij, which it
+// * preprocess: D_i = rowsum(dO o O) (or, over few keys, sum_j P_ij dP_ij, which it
 //   is) and L_i, stored negated as the backward's addends, for every query row that
 //   takes part (-inf and 0 elsewhere, which makes the row's probabilities 0);
 // * join of the forward's splits: with their log-sum-exps l_s,
@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_cross.h"
 #include "fa_serve.h"
@@ -51,70 +52,65 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_f32_kernel(cons
   }
 }
 
-// 16-bit types: D / 8 lanes a row, 16 bytes of O and of dO each, kRowsEach rows of one (b, h) a
-// thread with all their loads under way at once. (A warp a row with 2 bytes a lane took 34 us at
-// 4x16x2048x128, where the copy rate allows 10.)
+// 16-bit types, D = rowsum(dO o O) of the rows [row0, row0 + kRows) of one (b, h): D / 8 lanes a row, 16 bytes of O
+// and of dO each, four rows a thread with all their loads under way at once. (A warp a row with 2 bytes a lane took 34
+// us at 4x16x2048x128, where the copy rate allows 10.)
 template <int D>
 constexpr int preprocess_rows() { return kJoinThreads / (D / 8) * 4; }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __grid_constant__ CrossParams p) {
+template <typename T, int D, int kRows>
+__device__ __forceinline__ void rows_from_output(const CrossParams& p, int bh, int b, int h, int nq, int row0) {
   constexpr int kLanes = D / 8, kRowsEach = 4, kApart = kJoinThreads / kLanes;
-  let_next_begin();
-  wait_for_previous();
-  const int blocks = (p.nq_pad + preprocess_rows<D>() - 1) / preprocess_rows<D>(), bh = blockIdx.x / blocks;
-  const int b = bh / p.Hq, h = bh - b * p.Hq, nq = cross_q_len(p, b);
   const int e = 8 * (threadIdx.x % kLanes);
-  const int first = (blockIdx.x - bh * blocks) * preprocess_rows<D>() + threadIdx.x / kLanes;
   const T* o = static_cast<const T*>(p.o) + b * p.o_st.b + h * p.o_st.h + e;
   const T* g = static_cast<const T*>(p.dout) + b * p.do_st.b + h * p.do_st.h + e;
-  Raw8<T> ro[kRowsEach], rg[kRowsEach];
+#pragma unroll 1
+  for (int first = row0 + threadIdx.x / kLanes; first < row0 + kRows; first += kRowsEach * kApart) {
+    Raw8<T> ro[kRowsEach], rg[kRowsEach];
 #pragma unroll
-  for (int r = 0; r < kRowsEach; ++r) {
-    const int i = first + r * kApart;
-    zero8(ro[r]);
-    zero8(rg[r]);
-    if (i < nq) {
-      load8(ro[r], o + i * p.o_st.n);
-      load8(rg[r], g + i * p.do_st.n);
+    for (int r = 0; r < kRowsEach; ++r) {
+      const int i = first + r * kApart;
+      zero8(ro[r]);
+      zero8(rg[r]);
+      if (i < nq) {
+        load8(ro[r], o + i * p.o_st.n);
+        load8(rg[r], g + i * p.do_st.n);
+      }
     }
-  }
 #pragma unroll
-  for (int r = 0; r < kRowsEach; ++r) {
-    const int i = first + r * kApart;
-    uint64_t x[4], y[4], s0 = 0ull;
-    ro[r].unpack(x);
-    rg[r].unpack(y);
+    for (int r = 0; r < kRowsEach; ++r) {
+      const int i = first + r * kApart;
+      uint64_t x[4], y[4], s0 = 0ull;
+      ro[r].unpack(x);
+      rg[r].unpack(y);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s0 = f2_fma(x[c], y[c], s0);
-    const float acc = row_sum<kLanes>(f2_sum(s0));
-    if (e == 0 && i < p.nq_pad) {
-      const long long row = (long long)bh * p.nq_pad + i;
-      p.nD[row] = -acc;
-      p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
+      for (int c = 0; c < 4; ++c) s0 = f2_fma(x[c], y[c], s0);
+      const float acc = row_sum<kLanes>(f2_sum(s0));
+      if (e == 0 && i < p.nq_pad) {
+        const long long row = (long long)bh * p.nq_pad + i;
+        p.nD[row] = -acc;
+        p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
+      }
     }
   }
 }
 
-// 16-bit types and up to kFewKeysMost keys: D = sum_j P_ij dP_ij from the scores instead. rowsum(dO o O) has the
+// 16-bit types, sequences of up to kFewKeysMost keys (real ones: a sequence's gradients do not depend on what its
+// batch is padded to): D = sum_j P_ij dP_ij from the scores instead. rowsum(dO o O) has the
 // rounding of O to 16 bits in it, and over a handful of keys, where O is as large as V, or a few dozen where q, k
 // and v have large channels, that was the larger part of the error of dQ and dK (1.6 to 2.4 times the results' own
-// rounding; 1.0 to 1.4 so). A warp takes 16 rows of one (b, h), S and dP by m16n8k16, the block's keys and values in
-// shared memory, 16-byte pieces swizzled by row. The backward of 2x16/4 4095 over 16 keys, d = 64, takes 53.6 us
-// with it and 51.2 without, over 64 keys 59.6 and 51.0, 4x16 2048 over 64 keys, d = 128, 97 and 84, 1x2 128 over 5
-// 9.8 and 9.6; with more keys the two products cost more, and O is smaller.
+// rounding; 1.0 to 1.4 so). A warp takes 16 of the 128 rows [row0, ..), S and dP by m16n8k16, the block's keys and
+// values in shared memory, 16-byte pieces swizzled by row. The backward of 2x16/4 4095 over 16 keys, d = 64, takes
+// 53.6 us with it and 51.2 without, over 64 keys 59.6 and 51.0, 4x16 2048 over 64 keys, d = 128, 97 and 84, 1x2 128
+// over 5 9.8 and 9.6; with more keys the two products cost more, and O is smaller.
 constexpr int kFewKeysMost = 64;
 
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads)
-    cross_preprocess_few_keys_kernel(const __grid_constant__ CrossParams p) {
-  __shared__ __align__(128) uint16_t sk[kFewKeysMost * D], sv[kFewKeysMost * D];
-  let_next_begin();
-  wait_for_previous();
+__device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, int b, int h, int nq, int nk, int row0,
+                                                 uint16_t* sk, uint16_t* sv) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, in_quad = lane & 3;
-  const int blocks = p.nq_pad / 128, bh = blockIdx.x / blocks, b = bh / p.Hq, h = bh - b * p.Hq;
-  const int nq = cross_q_len(p, b), nk = cross_k_len(p, b), row0 = (blockIdx.x - bh * blocks) * 128 + warp * 16;
   const int tiles = (nk + 7) / 8;
+  row0 += warp * 16;
   const uint16_t* k = static_cast<const uint16_t*>(p.k) + b * p.k_st.b + h / p.G * p.k_st.h;
   const uint16_t* v = static_cast<const uint16_t*>(p.v) + b * p.v_st.b + h / p.G * p.v_st.h;
   for (int x = threadIdx.x; x < 8 * tiles * (D / 8); x += kJoinThreads) {
@@ -178,6 +174,25 @@ __global__ void __launch_bounds__(kJoinThreads)
       p.nL2[row] = nl[half];
     }
   }
+}
+
+// kScores, kOutput: which of the two forms the call's sequences take; both: each by its length.
+template <int D, bool kBf16, bool kScores, bool kOutput>
+__global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __grid_constant__ CrossParams p) {
+  using T = std::conditional_t<kBf16, __nv_bfloat16, __half>;
+  constexpr int kRows = kScores ? 128 : preprocess_rows<D>();
+  __shared__ __align__(128) uint16_t sk[kScores ? kFewKeysMost * D : 1], sv[kScores ? kFewKeysMost * D : 1];
+  let_next_begin();
+  wait_for_previous();
+  const int blocks = (p.nq_pad + kRows - 1) / kRows, bh = blockIdx.x / blocks, b = bh / p.Hq, h = bh - b * p.Hq;
+  const int nq = cross_q_len(p, b), nk = cross_k_len(p, b), row0 = (blockIdx.x - bh * blocks) * kRows;
+  if constexpr (kScores) {
+    if (!kOutput || nk <= kFewKeysMost) {
+      rows_from_scores<D, kBf16>(p, bh, b, h, nq, nk, row0, sk, sv);
+      return;
+    }
+  }
+  if constexpr (kOutput) rows_from_output<T, D, kRows>(p, bh, b, h, nq, row0);
 }
 
 // Four consecutive values as T.
@@ -338,6 +353,17 @@ int join_blocks(const CrossParams& p, int N, int H) {
   return (int)(blocks < 152 * 16 ? blocks : 152 * 16);
 }
 
+template <int D, bool kBf16>
+cudaError_t launch_preprocess(const CrossParams& p, cudaStream_t st) {
+  const auto launch = [&](auto kernel, int rows) {
+    const long long blocks = (long long)p.B * p.Hq * ((p.nq_pad + rows - 1) / rows);
+    return launch_chained(kernel, dim3((unsigned)blocks), kJoinThreads, 0, 1, p, st);
+  };
+  if (p.Nk <= kFewKeysMost) return launch(cross_preprocess_kernel<D, kBf16, true, false>, 128);
+  if (p.k_lens) return launch(cross_preprocess_kernel<D, kBf16, true, true>, 128);
+  return launch(cross_preprocess_kernel<D, kBf16, false, true>, preprocess_rows<D>());
+}
+
 }  // namespace
 
 cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st) {
@@ -347,22 +373,8 @@ cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_
     return launch_chained(cross_preprocess_f32_kernel, dim3((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32)),
                           kJoinThreads, 0, 1, p, st);
   }
-  const bool bf16 = dtype == FA_BF16;
-  if (p.Nk <= kFewKeysMost) {
-    const dim3 grid((unsigned)(heads * (p.nq_pad / 128)));
-    if (p.d == 64)
-      return bf16 ? launch_chained(cross_preprocess_few_keys_kernel<64, true>, grid, kJoinThreads, 0, 1, p, st)
-                  : launch_chained(cross_preprocess_few_keys_kernel<64, false>, grid, kJoinThreads, 0, 1, p, st);
-    return bf16 ? launch_chained(cross_preprocess_few_keys_kernel<128, true>, grid, kJoinThreads, 0, 1, p, st)
-                : launch_chained(cross_preprocess_few_keys_kernel<128, false>, grid, kJoinThreads, 0, 1, p, st);
-  }
-  const int rows = p.d == 64 ? preprocess_rows<64>() : preprocess_rows<128>();
-  const dim3 grid((unsigned)(heads * ((p.nq_pad + rows - 1) / rows)));
-  if (p.d == 64)
-    return launch_chained(bf16 ? cross_preprocess_kernel<__nv_bfloat16, 64> : cross_preprocess_kernel<__half, 64>, grid,
-                          kJoinThreads, 0, 1, p, st);
-  return launch_chained(bf16 ? cross_preprocess_kernel<__nv_bfloat16, 128> : cross_preprocess_kernel<__half, 128>, grid,
-                        kJoinThreads, 0, 1, p, st);
+  if (p.d == 64) return dtype == FA_BF16 ? launch_preprocess<64, true>(p, st) : launch_preprocess<64, false>(p, st);
+  return dtype == FA_BF16 ? launch_preprocess<128, true>(p, st) : launch_preprocess<128, false>(p, st);
 }
 
 template <typename T>

@@ -495,8 +495,8 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * below its normal values); their rounding residual is multiplied too in dq, in dk and dv
  * where a probability of the tile exceeds 1/4, and in the forward where a key head has few
  * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits,
- * or, with Nk <= 64, the scores, sum_j P_ij dP_ij (o is not read then). Errors as fa_fwd /
- * fa_bwd.
+ * or, for sequences of up to 64 real keys, the scores, sum_j P_ij dP_ij (o is not read then). Errors
+ * as fa_fwd / fa_bwd.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int B, Nq, Nk, Hq, Hk, d;

@@ -46,7 +46,11 @@ CASES = {
     # few rows a key head: the forward multiplies P's residual
     "few_rows": dict(off=("o", "split_o"), own={}, most=1.2, dtype=BF16, B=2, Nq=3, Nk=1000, Hq=4, Hk=2, d=128),
     "few_rows_f16": dict(off=("o", "split_o"), own={}, most=1.15, dtype=F16, B=2, Nq=1, Nk=1499, Hq=8, Hk=8, d=64),
-    # D over up to 64 keys comes from the scores
+    # D of sequences of up to 64 keys comes from the scores, whatever the batch is padded to
+    "d_of_short": dict(off=("dq", "d_scores"), own=ONCE, most=1.35, dtype=BF16, B=4, Nq=300, Nk=512, Hq=2, Hk=2, d=64,
+                       k_lens=[4, 8, 24, 60]),
+    "d_of_short_f16": dict(off=("dq", "d_scores"), own=ONCE, most=1.25, dtype=F16, B=4, Nq=150, Nk=300, Hq=2, Hk=1,
+                           d=128, k_lens=[4, 8, 24, 40]),
     "d_of_short_only": dict(off=("dq", "d_scores"), own=ONCE, most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
                             d=128, k_lens=[4, 8, 30]),
 }
