@@ -52,45 +52,42 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_f32_kernel(cons
   }
 }
 
-// 16-bit types, D = rowsum(dO o O) of the rows [row0, row0 + kRows) of one (b, h): D / 8 lanes a row, 16 bytes of O
-// and of dO each, four rows a thread with all their loads under way at once. (A warp a row with 2 bytes a lane took 34
-// us at 4x16x2048x128, where the copy rate allows 10.)
+// 16-bit types, D = rowsum(dO o O) of the rows [row0, row0 + preprocess_rows) of one (b, h): D / 8 lanes a row, 16
+// bytes of O and of dO each, four rows a thread with all their loads under way at once. (A warp a row with 2 bytes a
+// lane took 34 us at 4x16x2048x128, where the copy rate allows 10.)
 template <int D>
 constexpr int preprocess_rows() { return kJoinThreads / (D / 8) * 4; }
 
-template <typename T, int D, int kRows>
+template <typename T, int D>
 __device__ __forceinline__ void rows_from_output(const CrossParams& p, int bh, int b, int h, int nq, int row0) {
-  constexpr int kLanes = D / 8, kRowsEach = 4, kApart = kJoinThreads / kLanes;
-  const int e = 8 * (threadIdx.x % kLanes);
+  constexpr int kLanes = D / 8, kApart = kJoinThreads / kLanes, kRowsEach = 4;
+  const int e = 8 * (threadIdx.x % kLanes), first = row0 + threadIdx.x / kLanes;
   const T* o = static_cast<const T*>(p.o) + b * p.o_st.b + h * p.o_st.h + e;
   const T* g = static_cast<const T*>(p.dout) + b * p.do_st.b + h * p.do_st.h + e;
-#pragma unroll 1
-  for (int first = row0 + threadIdx.x / kLanes; first < row0 + kRows; first += kRowsEach * kApart) {
-    Raw8<T> ro[kRowsEach], rg[kRowsEach];
+  Raw8<T> ro[kRowsEach], rg[kRowsEach];
 #pragma unroll
-    for (int r = 0; r < kRowsEach; ++r) {
-      const int i = first + r * kApart;
-      zero8(ro[r]);
-      zero8(rg[r]);
-      if (i < nq) {
-        load8(ro[r], o + i * p.o_st.n);
-        load8(rg[r], g + i * p.do_st.n);
-      }
+  for (int r = 0; r < kRowsEach; ++r) {
+    const int i = first + r * kApart;
+    zero8(ro[r]);
+    zero8(rg[r]);
+    if (i < nq) {
+      load8(ro[r], o + i * p.o_st.n);
+      load8(rg[r], g + i * p.do_st.n);
     }
+  }
 #pragma unroll
-    for (int r = 0; r < kRowsEach; ++r) {
-      const int i = first + r * kApart;
-      uint64_t x[4], y[4], s0 = 0ull;
-      ro[r].unpack(x);
-      rg[r].unpack(y);
+  for (int r = 0; r < kRowsEach; ++r) {
+    const int i = first + r * kApart;
+    uint64_t x[4], y[4], s0 = 0ull;
+    ro[r].unpack(x);
+    rg[r].unpack(y);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s0 = f2_fma(x[c], y[c], s0);
-      const float acc = row_sum<kLanes>(f2_sum(s0));
-      if (e == 0 && i < p.nq_pad) {
-        const long long row = (long long)bh * p.nq_pad + i;
-        p.nD[row] = -acc;
-        p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
-      }
+    for (int c = 0; c < 4; ++c) s0 = f2_fma(x[c], y[c], s0);
+    const float acc = row_sum<kLanes>(f2_sum(s0));
+    if (e == 0 && i < p.nq_pad) {
+      const long long row = (long long)bh * p.nq_pad + i;
+      p.nD[row] = -acc;
+      p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
     }
   }
 }
@@ -106,8 +103,8 @@ __device__ __forceinline__ void rows_from_output(const CrossParams& p, int bh, i
 constexpr int kFewKeysMost = 64;
 
 template <int D, bool kBf16>
-__device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, int b, int h, int nq, int nk, int row0,
-                                                 uint16_t* sk, uint16_t* sv) {
+__device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, int b, int h, int nq, int nk, int row0) {
+  __shared__ __align__(128) uint16_t sk[kFewKeysMost * D], sv[kFewKeysMost * D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, in_quad = lane & 3;
   const int tiles = (nk + 7) / 8;
   row0 += warp * 16;
@@ -176,23 +173,22 @@ __device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, i
   }
 }
 
-// kScores, kOutput: which of the two forms the call's sequences take; both: each by its length.
-template <int D, bool kBf16, bool kScores, bool kOutput>
+// kForm: the form of all of the call's sequences, or of those whose length calls for it (kByLength; the others' blocks
+// leave); kEither: each block its sequence's.
+enum PreprocessForm { kScores, kOutput, kEither };
+
+template <int D, bool kBf16, PreprocessForm kForm, bool kByLength>
 __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_kernel(const __grid_constant__ CrossParams p) {
   using T = std::conditional_t<kBf16, __nv_bfloat16, __half>;
-  constexpr int kRows = kScores ? 128 : preprocess_rows<D>();
-  __shared__ __align__(128) uint16_t sk[kScores ? kFewKeysMost * D : 1], sv[kScores ? kFewKeysMost * D : 1];
+  constexpr int kRows = kForm == kOutput ? preprocess_rows<D>() : 128;
+  static_assert(kForm != kEither || preprocess_rows<D>() == 128, "a block has the same rows in both forms");
   let_next_begin();
   wait_for_previous();
   const int blocks = (p.nq_pad + kRows - 1) / kRows, bh = blockIdx.x / blocks, b = bh / p.Hq, h = bh - b * p.Hq;
   const int nq = cross_q_len(p, b), nk = cross_k_len(p, b), row0 = (blockIdx.x - bh * blocks) * kRows;
-  if constexpr (kScores) {
-    if (!kOutput || nk <= kFewKeysMost) {
-      rows_from_scores<D, kBf16>(p, bh, b, h, nq, nk, row0, sk, sv);
-      return;
-    }
-  }
-  if constexpr (kOutput) rows_from_output<T, D, kRows>(p, bh, b, h, nq, row0);
+  const bool scores = kByLength ? nk <= kFewKeysMost : kForm == kScores;
+  if (scores && kForm != kOutput) rows_from_scores<D, kBf16>(p, bh, b, h, nq, nk, row0);
+  if (!scores && kForm != kScores) rows_from_output<T, D>(p, bh, b, h, nq, row0);
 }
 
 // Four consecutive values as T.
@@ -359,9 +355,17 @@ cudaError_t launch_preprocess(const CrossParams& p, cudaStream_t st) {
     const long long blocks = (long long)p.B * p.Hq * ((p.nq_pad + rows - 1) / rows);
     return launch_chained(kernel, dim3((unsigned)blocks), kJoinThreads, 0, 1, p, st);
   };
-  if (p.Nk <= kFewKeysMost) return launch(cross_preprocess_kernel<D, kBf16, true, false>, 128);
-  if (p.k_lens) return launch(cross_preprocess_kernel<D, kBf16, true, true>, 128);
-  return launch(cross_preprocess_kernel<D, kBf16, false, true>, preprocess_rows<D>());
+  if (p.Nk <= kFewKeysMost) return launch(cross_preprocess_kernel<D, kBf16, kScores, false>, 128);
+  if (!p.k_lens) return launch(cross_preprocess_kernel<D, kBf16, kOutput, false>, preprocess_rows<D>());
+  // One kernel for both with d = 64, two with d = 128, where the scores' 118 registers leave two blocks an SM
+  // (backward, us, one / two kernels: 4x16 2048 over 512, d = 64, 96 / 96, with short sequences among them 78 / 80,
+  // 2x16/4 4095 over 77 54 / 56; d = 128 136 / 125, 113 / 113 and 91 / 93).
+  if constexpr (D == 64) {
+    return launch(cross_preprocess_kernel<D, kBf16, kEither, true>, 128);
+  } else {
+    const cudaError_t e = launch(cross_preprocess_kernel<D, kBf16, kScores, true>, 128);
+    return e == cudaSuccess ? launch(cross_preprocess_kernel<D, kBf16, kOutput, true>, preprocess_rows<D>()) : e;
+  }
 }
 
 }  // namespace
