@@ -40,6 +40,14 @@ inline CrossTile cross_tile(int Nq, int G, int most, int least) {
 // 77 and 822 us).
 constexpr float kCrossSplit = 0.25f;
 
+// fp16 has no normal values below 2^-14, where P is over more than 2^14 keys: the dV product takes P * 2^15 (at most
+// 2^15), with 2^-15 on the sums; -L * log2(e) is kept with the 15 added. Without, over 40000 even keys dV was 3.4
+// times as far off as its own rounding (1.4 so).
+template <bool kBf16>
+constexpr float kCrossPLog2 = kBf16 ? 0.f : 15.f;
+template <bool kBf16>
+constexpr float kCrossPUnit = kBf16 ? 1.f : 32768.f;
+
 struct CrossPlan {
   int k_splits;  // each takes an even share of a sequence's key blocks
   int q_splits;  // of its query steps (steps run over the group's heads and its queries)
@@ -67,7 +75,7 @@ struct CrossParams {
   float* lse_out;
   fa_strides q_st, k_st, v_st, o_st, do_st, out_st, dk_st, dv_st;
   float scale, scale_log2;
-  // Backward: -L * log2(e) and -D of every query row, [B * Hq, nq_pad], -inf and 0
+  // Backward: -L * log2(e) (+ kCrossPLog2) and -D of every query row, [B * Hq, nq_pad], -inf and 0
   // where a row is not there (padding, past its sequence, without keys).
   float* nL2;
   float* nD;

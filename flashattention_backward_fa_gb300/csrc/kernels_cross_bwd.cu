@@ -377,6 +377,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       const uint32_t full = step_columns(p.plan.step, c, kStep);
       const uint32_t tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
       const bool real = u.j0 + jl < u.nk;
+      const uint64_t unit2 = f2_pack(1.f / kCrossPUnit<kBf16>, 1.f / kCrossPUnit<kBf16>);
       for (int it = (bb ^ G) & 1; it < steps; it += 2) {
         const int gs = G + it, s = gs % C::kNS;
         const uint32_t allow = chunk == chunks - 1 ? tail : full;
@@ -391,7 +392,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
         tc_fence_after();
         const float4* L4 = reinterpret_cast<const float4*>(smem + C::oL + s * kStep * 4 + 128 * c);
         const float4* D4 = reinterpret_cast<const float4*>(smem + C::oD + s * kStep * 4 + 128 * c);
-        float P[32];  // of this thread's 32 pairs, for the dS phase
+        float P[32];  // of this thread's 32 pairs (times kCrossPUnit), for the dS phase
         bool split_h[2];
         // ---- phase 1: the P^T image over the S^T columns ----
 #pragma unroll
@@ -428,7 +429,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           uint32_t hp[8], ep[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
-          split_h[hh] = __any_sync(0xFFFFFFFFu, real && cmax > kCrossSplit);
+          split_h[hh] = __any_sync(0xFFFFFFFFu, real && cmax > kCrossSplit * kCrossPUnit<kBf16>);
           if (split_h[hh]) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
@@ -465,8 +466,14 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
                 f2_add(f2_pack(__uint_as_float(dr[x]), __uint_as_float(dr[x + 1])), f2_pack(d4.x, d4.y));
             const uint64_t d23 =
                 f2_add(f2_pack(__uint_as_float(dr[x + 2]), __uint_as_float(dr[x + 3])), f2_pack(d4.z, d4.w));
-            f2_unpack(f2_mul(f2_pack(P[16 * hh + x], P[16 * hh + x + 1]), d01), ds[x], ds[x + 1]);
-            f2_unpack(f2_mul(f2_pack(P[16 * hh + x + 2], P[16 * hh + x + 3]), d23), ds[x + 2], ds[x + 3]);
+            uint64_t p01 = f2_pack(P[16 * hh + x], P[16 * hh + x + 1]);
+            uint64_t p23 = f2_pack(P[16 * hh + x + 2], P[16 * hh + x + 3]);
+            if constexpr (!kBf16) {
+              p01 = f2_mul(p01, unit2);
+              p23 = f2_mul(p23, unit2);
+            }
+            f2_unpack(f2_mul(p01, d01), ds[x], ds[x + 1]);
+            f2_unpack(f2_mul(p23, d23), ds[x + 2], ds[x + 3]);
           }
           if (allow != 0xFFFFFFFFu) {  // (dP^T of what is not there may be NaN)
 #pragma unroll
@@ -530,7 +537,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           const fa_strides& st = isK ? p.dk_st : p.dv_st;
           uint16_t* const grad = static_cast<uint16_t*>(isK ? p.dk : p.dv);
           uint16_t* to_out = !parts && j < p.Nk ? grad + b * st.b + j * st.n + hk * st.h + col : nullptr;
-          store_columns32<kBf16>(r, isK && !parts ? p.scale : 1.f, parts, to_part, to_out);
+          const float mul = isK ? (parts ? 1.f : p.scale) : 1.f / kCrossPUnit<kBf16>;
+          store_columns32<kBf16>(r, mul, parts, to_part, to_out);
         }
         __syncwarp();
       }
@@ -794,7 +802,7 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
       if (ui < mine && unit[ui].blocks > 0 && row_in) {
         const CrossUnit& u = unit[ui];
         const long long at = ((long long)u.b * p.Hq + u.h0[0] + row_h) * p.nq_pad + u.q0[0] + row_q;
-        nl = p.nL2[at];
+        nl = p.nL2[at] - kCrossPLog2<kBf16>;
         nd = p.nD[at];
       }
     };

@@ -87,7 +87,8 @@ __device__ __forceinline__ void rows_from_output(const CrossParams& p, int bh, i
     if (e == 0 && i < p.nq_pad) {
       const long long row = (long long)bh * p.nq_pad + i;
       p.nD[row] = -acc;
-      p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) : -INFINITY;
+      p.nL2[row] = i < nq ? neg_lse2(p.lse[(long long)bh * p.Nq + i]) + kCrossPLog2<std::is_same_v<T, __nv_bfloat16>>
+                          : -INFINITY;
     }
   }
 }
@@ -168,7 +169,7 @@ __device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, i
     if (in_quad == 0) {
       const long long row = (long long)bh * p.nq_pad + row0 + quad + 8 * half;
       p.nD[row] = -acc[half];
-      p.nL2[row] = nl[half];
+      p.nL2[row] = nl[half] + kCrossPLog2<kBf16>;
     }
   }
 }

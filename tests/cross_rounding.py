@@ -53,6 +53,9 @@ CASES = {
                            d=128, k_lens=[4, 8, 24, 40]),
     "d_of_short_only": dict(off=("dq", "d_scores"), own=ONCE, most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
                             d=128, k_lens=[4, 8, 30]),
+    # fp16: P of many keys, below fp16's normal values
+    "dv_long": dict(off=("dv", "scaled"), own=ROUNDED_O, most=1.6, dtype=F16, B=1, Nq=130, Nk=40000, Hq=1, Hk=1, d=64,
+                    sharp=0.1),
 }
 
 
