@@ -190,15 +190,19 @@ FwdLayout fwd_layout(const fa_cross_shape* s, const CrossPlan& c) {
   return {lse, lse + round256(rows * 4)};
 }
 
-// Backward: [-L * log2(e) | -D | dQ of the splits | dK and dV of the splits].
+// Backward: [-L * log2(e) | -D | fp16: |dO| | maxima | dQ of the splits | dK and dV of the splits].
 struct BwdLayout {
-  size_t nD, dq, dkdv, total;
+  size_t nD, dout_norm, maxima, dq, dkdv, total;
 };
-BwdLayout bwd_layout(const fa_cross_shape* s, const CrossPlan& c) {
+BwdLayout bwd_layout(const fa_cross_shape* s, const CrossPlan& c, fa_dtype dtype) {
   const size_t vec = round256((size_t)s->B * s->Hq * (((size_t)s->Nq + 127) & ~size_t(127)) * 4);
   BwdLayout w;
   w.nD = vec;
-  w.dq = 2 * vec;
+  w.dout_norm = w.maxima = w.dq = 2 * vec;
+  if (dtype == FA_F16) {
+    w.maxima = w.dout_norm + vec;
+    w.dq = w.maxima + round256((size_t)s->B * s->Hk * sizeof(fa::CrossMaxima));
+  }
   w.dkdv = w.dq + (c.k_splits > 1 ? round256((size_t)c.k_splits * s->B * s->Nq * s->Hq * s->d * 4) : 0);
   w.total = w.dkdv + (c.q_splits > 1 ? round256((size_t)c.q_splits * 2 * s->B * s->Nk * s->Hk * s->d * 4) : 0);
   return w;
@@ -213,7 +217,7 @@ size_t fa_cross_fwd_workspace_size(const fa_cross_shape* shape, fa_dtype dtype) 
 }
 
 size_t fa_cross_bwd_workspace_size(const fa_cross_shape* shape, fa_dtype dtype) {
-  return check_shape(shape, dtype) ? 0 : bwd_layout(shape, plan_of(shape, dtype, true)).total;
+  return check_shape(shape, dtype) ? 0 : bwd_layout(shape, plan_of(shape, dtype, true), dtype).total;
 }
 
 int fa_cross_fwd(const fa_cross_shape* shape, const void* q, const void* k, const void* v, void* o, float* lse,
@@ -277,7 +281,7 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   if (!lse) return FA_ERR_INVALID_ARG;
   if (!aligned_to(lse, 16)) return FA_ERR_ALIGNMENT;
   const CrossPlan plan = plan_of(shape, dtype, true);
-  const BwdLayout w = bwd_layout(shape, plan);
+  const BwdLayout w = bwd_layout(shape, plan, dtype);
   if ((rc = check_workspace(workspace, workspace_bytes, w.total))) return rc;
   if ((rc = fa::check_device_ptrs({q, k, v, o, dout, lse, dq, dk, dv, shape->q_lens, shape->k_lens, workspace})))
     return rc;
@@ -303,6 +307,8 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   char* ws = static_cast<char*>(workspace);
   p.nL2 = reinterpret_cast<float*>(ws);
   p.nD = reinterpret_cast<float*>(ws + w.nD);
+  p.dout_norm = reinterpret_cast<float*>(ws + w.dout_norm);
+  p.maxima = reinterpret_cast<fa::CrossMaxima*>(ws + w.maxima);
   p.part = reinterpret_cast<float*>(ws + w.dq);
   p.part_kv = reinterpret_cast<float*>(ws + w.dkdv);
   if ((rc = fa::status_ptr(&p.status))) return rc;

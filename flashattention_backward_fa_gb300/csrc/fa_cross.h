@@ -48,6 +48,19 @@ constexpr float kCrossPLog2 = kBf16 ? 0.f : 15.f;
 template <bool kBf16>
 constexpr float kCrossPUnit = kBf16 ? 1.f : 32768.f;
 
+// dS in fp16. |dS| <= P bound with bound_i = |dO_i| max_j |V_j| + |D_i| (2-norms, the sequence's real keys): above
+// 65504 it is infinite and below 2^-14 loses its bits and its residual, both within the range of ordinary calls (loss
+// scaling; upstream gradients of 1e-3 over 4096 keys). So dS enters dQ's product times 2^e of its row, and dK's times
+// 2^e of its key head (by the largest bound of the group's rows), 2^e bound in [2^14, 2^15), and the sums are
+// multiplied by 2^-e. dQ of 200 queries over 4096 keys with dO of 1e-3 6.2 -> 1.0 times its own rounding, dK 2.3 -> 1.0.
+__device__ __forceinline__ int cross_exponent(float bound) {
+  return min(max(14 + 127 - (__float_as_int(bound) >> 23 & 255), -64), 100);  // (0, infinity, NaN: any will do)
+}
+__device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }
+struct CrossMaxima {  // of a (batch, key head): bits of floats that are not negative
+  unsigned int v, dout, D, pad;  // of |V_j|^2, |dO_i| and |D_i|
+};
+
 struct CrossPlan {
   int k_splits;  // each takes an even share of a sequence's key blocks
   int q_splits;  // of its query steps (steps run over the group's heads and its queries)
@@ -80,6 +93,9 @@ struct CrossParams {
   float* nL2;
   float* nD;
   int nq_pad;
+  // fp16 (cross_exponent): |dO_i| of every query row, [B * Hq, nq_pad], and the maxima of every (batch, key head).
+  float* dout_norm;
+  CrossMaxima* maxima;
   // Split results in fp32: the forward's normalised outputs [k_splits][B, Nq, Hq, d]
   // and their log2-sum-exp2 [k_splits][B, Hq, Nq] (-inf: the split has no key of the
   // row, and no output is there); dQ [k_splits][B, Nq, Hq, d]; dK and dV
@@ -294,6 +310,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ int cross_head_exponent(const CrossMaxima& m) {
+  return cross_exponent(__uint_as_float(m.dout) * sqrtf(__uint_as_float(m.v)) + __uint_as_float(m.D));
 }
 
 cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st);

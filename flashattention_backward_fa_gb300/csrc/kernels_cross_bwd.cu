@@ -78,7 +78,7 @@ struct KCfg {
   static constexpr uint32_t oAbort = oTmemSlot + 8;
   static constexpr uint32_t oFlags = oAbort + 8;    // [buffer][8 warps] split votes
   static constexpr uint32_t oUnits = oFlags + 64;   // [kMostUnits]
-  static constexpr uint32_t kSmem = oUnits + kMostUnits * 40 + 1024;  // + slack for 1024-byte alignment
+  static constexpr uint32_t kSmem = oUnits + kMostUnits * 44 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
 
@@ -87,7 +87,9 @@ struct KUnit {
   int b, hk, split, j0, nq, nk;
   int first, steps;  // steps first .. first + steps - 1 of the sequence's live ones (0: nothing to compute)
   int chunks, chunk;  // live chunks of a head's queries, the first step's
+  int exp;            // fp16: dS is multiplied as dS * 2^exp (cross_exponent)
 };
+static_assert(sizeof(KUnit) == 44, "as KCfg::kSmem has it");
 
 __device__ __forceinline__ int k_units(const CrossParams& p) {
   return p.B * p.Hk * ((p.Nk + 127) / 128) * p.plan.q_splits;
@@ -192,6 +194,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
   if ((int)threadIdx.x < mine) {
     KUnit u;
     k_unit(p, first + threadIdx.x * stride, u);
+    u.exp = kBf16 ? 0 : cross_head_exponent(p.maxima[u.b * p.Hk + u.hk]);
     unit[threadIdx.x] = u;
   }
   tc_fence_before();
@@ -377,7 +380,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       const uint32_t full = step_columns(p.plan.step, c, kStep);
       const uint32_t tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
       const bool real = u.j0 + jl < u.nk;
-      const uint64_t unit2 = f2_pack(1.f / kCrossPUnit<kBf16>, 1.f / kCrossPUnit<kBf16>);
+      const float to_ds = kBf16 ? 1.f : power_of_2(u.exp - (int)kCrossPLog2<kBf16>);  // from P's power of 2 to dS's
+      const uint64_t to_ds2 = f2_pack(to_ds, to_ds);
       for (int it = (bb ^ G) & 1; it < steps; it += 2) {
         const int gs = G + it, s = gs % C::kNS;
         const uint32_t allow = chunk == chunks - 1 ? tail : full;
@@ -469,8 +473,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
             uint64_t p01 = f2_pack(P[16 * hh + x], P[16 * hh + x + 1]);
             uint64_t p23 = f2_pack(P[16 * hh + x + 2], P[16 * hh + x + 3]);
             if constexpr (!kBf16) {
-              p01 = f2_mul(p01, unit2);
-              p23 = f2_mul(p23, unit2);
+              p01 = f2_mul(p01, to_ds2);
+              p23 = f2_mul(p23, to_ds2);
             }
             f2_unpack(f2_mul(p01, d01), ds[x], ds[x + 1]);
             f2_unpack(f2_mul(p23, d23), ds[x + 2], ds[x + 3]);
@@ -537,7 +541,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           const fa_strides& st = isK ? p.dk_st : p.dv_st;
           uint16_t* const grad = static_cast<uint16_t*>(isK ? p.dk : p.dv);
           uint16_t* to_out = !parts && j < p.Nk ? grad + b * st.b + j * st.n + hk * st.h + col : nullptr;
-          const float mul = isK ? (parts ? 1.f : p.scale) : 1.f / kCrossPUnit<kBf16>;
+          float mul = isK && !parts ? p.scale : 1.f;
+          if (!kBf16) mul *= isK ? power_of_2(-u.exp) : 1.f / kCrossPUnit<kBf16>;
           store_columns32<kBf16>(r, mul, parts, to_part, to_out);
         }
         __syncwarp();
@@ -796,24 +801,33 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
     int kl = 0, G = 0;
     bool ok = true;
     // The next unit's -L and -D of this row (-inf and 0 past the sequence) are on their way while one is worked on.
-    const auto row_of = [&](int ui, float& nl, float& nd) {
+    // (fp16: -L with the row's exponent added, which makes P and dS 2^e times as large, and 2^-e)
+    const auto row_of = [&](int ui, float& nl, float& nd, float& back) {
       nl = -INFINITY;
       nd = 0.f;
+      back = 1.f;
       if (ui < mine && unit[ui].blocks > 0 && row_in) {
         const CrossUnit& u = unit[ui];
         const long long at = ((long long)u.b * p.Hq + u.h0[0] + row_h) * p.nq_pad + u.q0[0] + row_q;
-        nl = p.nL2[at] - kCrossPLog2<kBf16>;
+        nl = p.nL2[at];
         nd = p.nD[at];
+        if constexpr (!kBf16) {
+          const float v_norm = sqrtf(__uint_as_float(p.maxima[u.b * p.Hk + u.hk].v));
+          const int e = cross_exponent(p.dout_norm[at] * v_norm + fabsf(nd));
+          nl += (float)e - kCrossPLog2<kBf16>;
+          back = power_of_2(-e);
+        }
       }
     };
-    float nL2, nD, nL2_next, nD_next;
-    row_of(0, nL2, nD);
+    float nL2, nD, back_now, nL2_next, nD_next, back_next, back_last = 1.f;
+    row_of(0, nL2, nD, back_now);
     constexpr bool kLater = C::kAcc == 2;  // (see kAcc; the round of ui = mine then has an epilogue alone)
-    for (int ui = 0; ok && ui < mine + kLater; ++ui, nL2 = nL2_next, nD = nD_next) {
+    for (int ui = 0; ok && ui < mine + kLater;
+         ++ui, nL2 = nL2_next, nD = nD_next, back_last = back_now, back_now = back_next) {
       const CrossUnit& u = unit[min(ui, mine - 1)];
       // left: real keys from this warpgroup's first column on
       const int blocks = ui < mine ? u.blocks : 0, left = u.j_end - u.j_begin - 32 * c;
-      if (!kLater) row_of(ui + 1, nL2_next, nD_next);
+      if (!kLater) row_of(ui + 1, nL2_next, nD_next, back_next);
       const uint64_t l2 = f2_pack(nL2, nL2), d2 = f2_pack(nD, nD);
       int it = 0;
       do {
@@ -877,7 +891,7 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
           warp_arrive(bar(C::bPFull + bb));
         }
         if (kLater ? it > 0 : it + 1 < blocks) continue;
-        if (kLater) row_of(ui + 1, nL2_next, nD_next);
+        if (kLater) row_of(ui + 1, nL2_next, nD_next, back_next);
         if (kLater && ui == 0) continue;
         // Epilogue: columns [c d / 4, (c + 1) d / 4). The accumulator is loaded and released
         // (AccFree) before the stores, so the next MMA into it can start meanwhile.
@@ -917,7 +931,8 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
           to_part = p.part + ((((long long)to.split * p.B + b) * p.Nq + i) * p.Hq + h) * D + c * (D / 4);
         if (!parts && in)
           to_out = static_cast<uint16_t*>(p.out) + b * p.out_st.b + i * p.out_st.n + h * p.out_st.h + c * (D / 4);
-        const float mul = parts ? 1.f : p.scale;
+        float mul = parts ? 1.f : p.scale;
+        if (!kBf16) mul *= kLater ? back_last : back_now;
         if constexpr (D == 128)
           store_columns32<kBf16>(r, mul, parts, to_part, to_out);
         else

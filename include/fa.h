@@ -491,8 +491,11 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * workspaces of their own.
  * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
  * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, rounded
- * once (off by at most 2^-8 of themselves in bf16, 2^-11 in fp16 and 2^-25 where they are
- * below its normal values, P of dv 2^-40: it is multiplied as P * 2^15); their rounding residual is multiplied too in dq, in dk and dv
+ * once: off by at most 2^-8 of themselves in bf16, 2^-11 in fp16. fp16 operands are taken
+ * into the type's range by powers of two (dS for dq by its row, dS for dk by its key head,
+ * P for dv by 2^15), so that small and large upstream gradients and long key axes cost
+ * no accuracy: what is below 2^-40 of the largest that |dout_i| max_j |v_j| + |D_i| allows
+ * is lost. Their rounding residual is multiplied too in dq, in dk and dv
  * where a probability of the tile exceeds 1/4, and in the forward where a key head has few
  * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits,
  * or, for sequences of up to 64 real keys, the scores, sum_j P_ij dP_ij (o is not read then). Errors

@@ -53,9 +53,20 @@ CASES = {
                            d=128, k_lens=[4, 8, 24, 40]),
     "d_of_short_only": dict(off=("dq", "d_scores"), own=ONCE, most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
                             d=128, k_lens=[4, 8, 30]),
-    # fp16: P of many keys, below fp16's normal values
+    # fp16: dS of small upstream gradients over many keys, and P of many keys, below fp16's normal values
+    "dq_small": dict(off=("dq", "scaled"), own=ROUNDED_O, most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
+                     do=1e-3),
+    "dk_small": dict(off=("dk", "scaled"), own=ROUNDED_O, most=1.6, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
+                     do=1e-3),
+    "dq_tiny": dict(off=("dq", "scaled"), own=ROUNDED_O, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
+                    do=1e-4, k_lens=[5000, 4097]),
+    "dk_tiny": dict(off=("dk", "scaled"), own=ROUNDED_O, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
+                    do=1e-4, k_lens=[5000, 4097]),
     "dv_long": dict(off=("dv", "scaled"), own=ROUNDED_O, most=1.6, dtype=F16, B=1, Nq=130, Nk=40000, Hq=1, Hk=1, d=64,
                     sharp=0.1),
+    # rows of unlike upstream gradients: each row of dQ by itself
+    "dq_rows_apart": dict(off=("dq", "scaled"), own=ONCE, most=1.5, rows=True, dtype=F16, B=1, Nq=64, Nk=64, Hq=4,
+                          Hk=4, d=64, spread=13),
 }
 
 

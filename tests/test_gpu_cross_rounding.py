@@ -40,3 +40,52 @@ def test_padding_does_not_coarsen(n, d, dtype):
     for name in ("dq", "dk", "dv"):
         a, b = batch[name][:1, :ref[name].shape[1]], own[name]
         assert ratio(a, ref[name], dtype) < 1.02 * ratio(b, ref[name], dtype), name
+
+
+@pytest.mark.parametrize("Nq,Nk,k_lens", [(5, 6, None), (200, 300, None), (70, 200, [5, 200])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_gradients_in_fp16(d, Nq, Nk, k_lens):
+    """dS beyond fp16's largest value, as loss scaling brings it about, where the gradients are within it: each as exact
+    as ever. dO V^T is 1e5 to 1e7 here; small queries and keys take dQ and dK back into the range."""
+    g = torch.Generator().manual_seed(d)
+    B, r = 2, lambda n, s: (torch.randn((B, n, 2, d), generator=g) * s).to(F16)  # noqa: E731
+    q, k, v, do = r(Nq, 1e-3), r(Nk, 1e-3), r(Nk, 100.0), r(Nq, 1000.0)
+    ref, x = definition(q, k, v, do, k_lens=k_lens), run(q, k, v, do, k_lens)
+    for name in ("dq", "dk", "dv"):
+        assert ref[name].abs().max() < 65000
+        off = ratio(x[name], ref[name], F16)
+        assert off < 1.7, name
+
+
+def test_gradients_of_zero_and_of_the_least_values_in_fp16():
+    """Rows, heads and a whole call whose dO or V is zero; the smallest values that fp16 has."""
+    g = torch.Generator().manual_seed(1)
+    r = lambda n, h: torch.randn((2, n, h, 64), generator=g).to(F16)  # noqa: E731
+    q, k, v, do = r(150, 4), r(130, 2), r(130, 2), r(150, 4)
+    do[0, 3:9], do[1, :, 1] = 0, 2.0 ** -24
+    v[1, :, 1] = 0
+    ref, x = definition(q, k, v, do), run(q, k, v, do)
+    assert not any(x[n].isnan().any() or x[n].isinf().any() for n in x)
+    for n in ("dq", "dk", "dv"):
+        assert ratio(x[n], ref[n], F16) < 1.7, n
+    assert not x["dq"][0, 3:9].any() and not x["dq"][1, :, 2:].any() and not x["dk"][1, :, 1].any()
+    x = run(q, k, v, torch.zeros_like(do))
+    assert not any(x[n].any() for n in ("dq", "dk", "dv"))
+    x = run(q, k, torch.zeros_like(v), do)
+    assert not x["dq"].any() and not x["dk"].any()
+
+
+def test_infinite_gradients_in_fp16():
+    """An infinity in dO spoils its own query's dQ and its key head's dK and dV, and nothing else."""
+    g = torch.Generator().manual_seed(2)
+    r = lambda n, h: torch.randn((2, n, h, 64), generator=g).to(F16)  # noqa: E731
+    q, k, v, do = r(90, 4), r(130, 2), r(130, 2), r(90, 4)
+    clean = run(q, k, v, do)
+    do[1, 7, 2, 5] = float("inf")
+    x = run(q, k, v, do)
+    assert not x["dq"][1, 7, 2].isfinite().any() and not x["dk"][1, :, 1].isfinite().any()
+    keep = torch.ones(2, 90, 4, dtype=torch.bool)
+    keep[1, 7, 2] = False
+    assert torch.equal(x["dq"][keep], clean["dq"][keep])
+    for n in ("dk", "dv"):
+        assert torch.equal(x[n][0], clean[n][0]) and torch.equal(x[n][1, :, 0], clean[n][1, :, 0])
