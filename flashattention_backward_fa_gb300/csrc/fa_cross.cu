@@ -53,6 +53,12 @@ int check_workspace(const void* ws, size_t have, size_t need) {
   return need && (!ws || !aligned_to(ws, 256) || have < need) ? FA_ERR_WORKSPACE : FA_OK;
 }
 
+// Query rows of a head in the backward's -L and -D: whole tiles of the kernels that read them (4 queries at least).
+int padded_queries(const fa_cross_shape* s, const CrossPlan& c) {
+  const int tile = std::max(c.q_tile.queries(), c.step.queries());
+  return (s->Nq + tile - 1) / tile * tile;
+}
+
 void fill(CrossParams& p, const fa_cross_shape* s, const CrossPlan& plan, float scale) {
   std::memset(&p, 0, sizeof(p));
   p.B = s->B;
@@ -64,7 +70,7 @@ void fill(CrossParams& p, const fa_cross_shape* s, const CrossPlan& plan, float 
   p.d = s->d;
   p.q_lens = s->q_lens;
   p.k_lens = s->k_lens;
-  p.nq_pad = (s->Nq + 127) & ~127;
+  p.nq_pad = padded_queries(s, plan);
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.plan = plan;
@@ -195,7 +201,7 @@ struct BwdLayout {
   size_t nD, dout_norm, maxima, dq, dkdv, total;
 };
 BwdLayout bwd_layout(const fa_cross_shape* s, const CrossPlan& c, fa_dtype dtype) {
-  const size_t vec = round256((size_t)s->B * s->Hq * (((size_t)s->Nq + 127) & ~size_t(127)) * 4);
+  const size_t vec = round256((size_t)s->B * s->Hq * padded_queries(s, c) * 4);
   BwdLayout w;
   w.nD = vec;
   w.dout_norm = w.maxima = w.dq = 2 * vec;

@@ -52,7 +52,8 @@ constexpr float kCrossPUnit = kBf16 ? 1.f : 32768.f;
 // 65504 it is infinite and below 2^-14 loses its bits and its residual, both within the range of ordinary calls (loss
 // scaling; upstream gradients of 1e-3 over 4096 keys). So dS enters dQ's product times 2^e of its row, and dK's times
 // 2^e of its key head (by the largest bound of the group's rows), 2^e bound in [2^14, 2^15), and the sums are
-// multiplied by 2^-e. dQ of 200 queries over 4096 keys with dO of 1e-3 6.2 -> 1.0 times its own rounding, dK 2.3 -> 1.0.
+// multiplied by 2^-e. dQ of 200 queries over 4096 keys with dO of 1e-3 6.2 -> 1.0 times its own rounding, dK 2.3 ->
+// 1.0; fp16 backward of 4x16 2048x512 124 -> 132 us, 2x16/4 4095x77 55 -> 60, 1x32/8 8192x4096 1398 -> 1455.
 __device__ __forceinline__ int cross_exponent(float bound) {
   return min(max(14 + 127 - (__float_as_int(bound) >> 23 & 255), -64), 100);  // (0, infinity, NaN: any will do)
 }

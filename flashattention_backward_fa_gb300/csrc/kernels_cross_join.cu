@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_preprocess_f32_kernel(cons
   }
 }
 
-// A block's maxima x and y (not negative, no NaN) into those of a (batch, key head), the same in any order. Once a block.
+// A block's maxima x and y (not negative, no NaN) into those of a (batch, key head), the same in any order.
+// Once a block.
 __device__ __forceinline__ void put_maxima(unsigned int* to_x, float x, unsigned int* to_y, float y) {
   constexpr int kWarps = kJoinThreads / 32;
   __shared__ unsigned int tops[2 * kWarps];
@@ -76,7 +77,8 @@ __global__ void __launch_bounds__(kJoinThreads) cross_clear_maxima_kernel(const 
   let_next_begin();
   wait_for_previous();
   const long long n = (long long)p.B * p.Hk;
-  for (long long i = (long long)blockIdx.x * kJoinThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kJoinThreads)
+  const long long apart = (long long)gridDim.x * kJoinThreads;
+  for (long long i = (long long)blockIdx.x * kJoinThreads + threadIdx.x; i < n; i += apart)
     p.maxima[i] = {0u, 0u, 0u, 0u};
 }
 
@@ -243,7 +245,8 @@ __device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, i
     acc[half] += __shfl_xor_sync(0xffffffffu, acc[half], 1);
     acc[half] += __shfl_xor_sync(0xffffffffu, acc[half], 2);
     const long long row = (long long)bh * p.nq_pad + row0 + quad + 8 * half;
-    if (in_quad == 0) {
+    const bool there = in_quad == 0 && row0 + quad + 8 * half < p.nq_pad;
+    if (there) {
       p.nD[row] = -acc[half];
       p.nL2[row] = nl[half] + kCrossPLog2<kBf16>;
     }
@@ -260,7 +263,7 @@ __device__ __forceinline__ void rows_from_scores(const CrossParams& p, int bh, i
       square += __shfl_xor_sync(0xffffffffu, square, 1);
       square += __shfl_xor_sync(0xffffffffu, square, 2);
       const float norm = sqrtf(square);  // (0 where there is no row, and so is acc)
-      if (in_quad == 0) p.dout_norm[row] = norm;
+      if (there) p.dout_norm[row] = norm;
       most = fmaxf(most, norm);
       most_D = fmaxf(most_D, fabsf(acc[half]));
     }
