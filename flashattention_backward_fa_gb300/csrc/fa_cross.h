@@ -32,14 +32,6 @@ inline CrossTile cross_tile(int Nq, int G, int most, int least) {
   return t;
 }
 
-// P and dS enter the products of dV and dK in 16 bits, with their rounding residual beside them where the tile
-// holds a probability above this. Roundings of many small weights average out; those of one that makes up
-// the row do not. Error of bf16 dK and dV against 64 bits (2-norm, of themselves): 1.7e-3 with the residual
-// everywhere, 2.4e-3 without. At 1/64, as in fa_bwd, nearly every tile of a few hundred keys had one above it
-// and took half as many products again (dK/dV by itself, 4x16 2048x512 84 us, 1x32/8 8192x4096 985; with 1/4
-// 77 and 822 us).
-constexpr float kCrossSplit = 0.25f;
-
 // fp16 has no normal values below 2^-14, where P is over more than 2^14 keys: the dV product takes P * 2^15 (at most
 // 2^15), with 2^-15 on the sums; -L * log2(e) is kept with the 15 added. Without, over 40000 even keys dV was 3.4
 // times as far off as its own rounding (1.4 so).

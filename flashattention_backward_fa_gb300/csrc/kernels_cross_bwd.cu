@@ -9,7 +9,11 @@
 // of several where queries are few; the steps run over all heads of the group, so shared
 // key heads cost no extra sums), S^T and dP^T in double buffers, P^T and dS^T written back
 // over them in 16 bits with their rounding residual where the tile holds probabilities
-// above kCrossSplit, dV and dK in TMEM. dQ: 128 query rows on the lanes, steps of 128 keys,
+// above kSplitThreshold, as in fa_bwd, dV and dK in TMEM (bf16 error of dK and dV against 64 bits,
+// 2-norm of themselves, 4x16 2048x512: 1.7e-3 and 1.7e-3, of which 1.66e-3 is the results' own rounding;
+// with the residuals above 1/4 only 2.35e-3 and 2.29e-3. 1x32/8 8192x4096 2.0e-3 and 1.9e-3 against
+// 2.35e-3 and 2.31e-3. Forward and backward 168 against 162 us, 2040 against 1950). dQ: 128
+// query rows on the lanes, steps of 128 keys,
 // dS always with its residual: a row's dS add up to 0, their roundings do not, and what is
 // left of them is multiplied by the mean of the keys under P, which is not small where q and
 // k share a large channel (error of dQ with such channels, bf16 3x16 1551 over 160 keys,
@@ -433,7 +437,7 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           uint32_t hp[8], ep[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
-          split_h[hh] = __any_sync(0xFFFFFFFFu, real && cmax > kCrossSplit * kCrossPUnit<kBf16>);
+          split_h[hh] = __any_sync(0xFFFFFFFFu, real && cmax > kSplitThreshold * kCrossPUnit<kBf16>);
           if (split_h[hh]) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)

@@ -496,7 +496,7 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * P for dv by 2^15), so that small and large upstream gradients and long key axes cost
  * no accuracy: what is below 2^-40 of the largest that |dout_i| max_j |v_j| + |D_i| allows
  * is lost. Their rounding residual is multiplied too in dq, in dk and dv
- * where a probability of the tile exceeds 1/4, and in the forward where a key head has few
+ * where a probability of the tile exceeds 1/64, and in the forward where a key head has few
  * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits,
  * or, for sequences of up to 64 real keys, the scores, sum_j P_ij dP_ij (o is not read then). Errors
  * as fa_fwd / fa_bwd.

@@ -29,8 +29,9 @@ def activations(g, shape, dtype, big=4.0):
 
 
 # What a case is about: an output, the switch of `emulate` that makes it coarser, and the limit between; `own`: the
-# roundings that the kernels make besides (P of the tile kernels' forward and, where no key has a quarter of a
+# roundings that the kernels make besides (P of the tile kernels' forward and, where no key has a 64th of a
 # row, P and dS of dV and dK once; D of more than 64 keys from the rounded o). Then the inputs.
+TILES = dict(split_o=False, d_scores=False)
 ONCE, ROUNDED_O = dict(split_o=False, split_kv=False), dict(split_o=False, split_kv=False, d_scores=False)
 CASES = {
     # dQ takes dS with its residual
@@ -38,7 +39,10 @@ CASES = {
                         d=128),
     "dq_channels_f16": dict(off=("dq", "split_dq"), own=ROUNDED_O, most=1.3, dtype=F16, B=1, Nq=700, Nk=160, Hq=2,
                             Hk=1, d=128),
-    # dK and dV take the residuals of dS and P where a row is made up of a few keys
+    # dK and dV take the residuals of dS and P where a key has a 64th of a row: over some hundreds of keys, and where a
+    # row is made up of a few
+    "dk_hundreds": dict(off=("dk", "split_kv"), own=TILES, most=1.2, dtype=BF16, B=1, Nq=500, Nk=300, Hq=2, Hk=1, d=128),
+    "dv_hundreds": dict(off=("dv", "split_kv"), own=TILES, most=1.2, dtype=F16, B=1, Nq=500, Nk=300, Hq=2, Hk=2, d=64),
     "dk_sharp": dict(off=("dk", "split_kv"), own={}, most=1.2, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
                      sharp=4.0),
     "dv_sharp": dict(off=("dv", "split_kv"), own={}, most=1.15, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
