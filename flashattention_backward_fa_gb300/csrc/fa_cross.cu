@@ -123,9 +123,13 @@ void few_plan(long long units, int Nk, CrossPlan* c) {
 
 // The backward's splits and blocks. Splits: until dK/dV has 128 units or they are down to 16 query steps, dQ 64
 // units or 8 key blocks. Blocks: as many as there are units, but not under 16 steps (8 key blocks) each while 128
-// blocks remain. Measured, us (dK/dV splits / blocks, dQ splits / blocks): 16 heads, 4095 queries over 77 keys,
-// d = 64: 16 / 128, 1 / 256 73; 4 / 32, 1 / 104 120; 32 / 256, 1 / 512 86. 16/4 heads, 1024 over 1024, batch 2:
-// 2 / 128, 1 / 128 84; 1 / 64, 1 / 62 98. 64 queries over 16384 keys: 1 / 512, 4 / 64 130; 1 / 512, 1 / 16 227.
+// blocks remain. Measured, bf16 backward, us (dK/dV splits / blocks, dQ splits / blocks; * what this plan takes):
+// 16 heads, 4095 queries over 77 keys, d = 64: *4 / 64, 1 / 128 39; 4 / 32, 1 / 104 54; 32 / 256, 1 / 512 49.
+// Two sequences of 16/4 heads: *16 / 128, 1 / 128 50.5; 8 / 64, 1 / 128 63; 16 / 128, 1 / 512 57; 32 / 256, 1 / 128 58.
+// 2 x 16/4 heads, 1024 over 1024: *2 / 128, 1 / 256 81; 1 / 64, 1 / 62 107; 4 / 256, 1 / 256 89.
+// 16 heads, 64 queries over 16384 keys: *1 / 128, 4 / 64 114; 1 / 128, 1 / 16 157.
+// 4 x 16 heads, 2048 over 512 keys (texts of 512, 227, 453 and 169): *1 / 256, 1 / 512 152 (133); 1 / 152, 1 / 304 157
+// (138); 1 / 128, 1 / 256 162 (143); 1 / 152, 1 / 152 167 (149); 2 / 512, 1 / 512 199 (174).
 void bwd_plan(const fa_cross_shape* s, long long groups, long long tiles, CrossPlan* c) {
   const int steps = c->step.count(s->Nq, s->Hq / s->Hk), blocks = (int)div_up(s->Nk, 128);
   const long long kv = groups * div_up(s->Nk, 128), q = groups * tiles;

@@ -17,8 +17,8 @@
 // dS always with its residual: a row's dS add up to 0, their roundings do not, and what is
 // left of them is multiplied by the mean of the keys under P, which is not small where q and
 // k share a large channel (error of dQ with such channels, bf16 3x16 1551 over 160 keys,
-// 2.7e-3 without residuals, 2.1e-3 with them; of the result's own rounding 1.7e-3; backward
-// of 1x32/8 8192x4096 1325 -> 1388 us). What remains is, over more than 64 keys, D's error by O's 16 bits.
+// 2.7e-3 without residuals, 2.1e-3 with them; of the result's own rounding 1.7e-3; 4% of the
+// backward's time). What remains is, over more than 64 keys, D's error by O's 16 bits.
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //

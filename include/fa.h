@@ -139,7 +139,13 @@ int fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int
  * mode; its contents on entry do not matter. Runs fa_bwd_stage
  * (FA_BWD_PREPROCESS), (FA_BWD_DKDV), (FA_BWD_DQ) in order on `stream`; with
  * FA_DQ_RECOMPUTE the dQ kernel runs on a library-owned side stream beside the
- * dK/dV kernel, joined back into `stream` before the call returns. */
+ * dK/dV kernel, joined back into `stream` before the call returns.
+ * fp16: P and dS = P o (dO V^T - D) enter the products as fp16 values, here and in
+ * every other backward of self-attention (packed, with ALiBi, with a bias). Where |dS|
+ * exceeds 65504 (large loss scales) gradients get infinite or NaN, and where it is below
+ * 2^-14 it is rounded to multiples of 2^-24: over 4096 keys with dO of 1e-3 dQ and dK are 8
+ * times as far off as their own rounding. Scale the loss so that dO is near 1, or
+ * use bf16, which has fp32's range. (fa_cross_bwd scales by itself.) */
 int fa_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
            void* dq, void* dk, void* dv, int B, int H, int N, int d, fa_strides strides, fa_dtype dtype,
            float scale, int causal, int window, float dropout_p, uint64_t seed, uint64_t offset,
@@ -490,16 +496,17 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * and both are 0 for shapes that the calls refuse; calls that overlap on the GPU need
  * workspaces of their own.
  * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
- * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, rounded
- * once: off by at most 2^-8 of themselves in bf16, 2^-11 in fp16. fp16 operands are taken
- * into the type's range by powers of two (dS for dq by its row, dS for dk by its key head,
- * P for dv by 2^15), so that small and large upstream gradients and long key axes cost
- * no accuracy: what is below 2^-40 of the largest that |dout_i| max_j |v_j| + |D_i| allows
- * is lost. Their rounding residual is multiplied too in dq, in dk and dv
- * where a probability of the tile exceeds 1/64, and in the forward where a key head has few
- * query rows (16, or up to 64 in small calls). D takes o as it is given, in 16 bits,
- * or, for sequences of up to 64 real keys, the scores, sum_j P_ij dP_ij (o is not read then). Errors
- * as fa_fwd / fa_bwd.
+ * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, off by
+ * at most 2^-8 of themselves in bf16 and 2^-11 in fp16. Their rounding residual is
+ * multiplied too in dq, in dk and dv where a probability of the tile exceeds 1/64, and in
+ * the forward where a key head has few query rows (16, or up to 64 in small calls).
+ * fp16 operands of the backward are taken into the type's range by powers of two (dS for
+ * dq by its row, dS for dk by its key head, P for dv by 2^15), so small and large upstream
+ * gradients and long key axes cost no accuracy: dS is off by at most 2^-40 of what
+ * |dout_i| max_j |v_j| + |D_i| allows, P of dv by 2^-40, P of the forward by 2^-25 of the
+ * row's largest, where these are more. D takes o as it is given, in 16 bits, or, for
+ * sequences of up to 64 real keys, the scores, sum_j P_ij dP_ij (o is not read then).
+ * Errors as fa_fwd / fa_bwd.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int B, Nq, Nk, Hq, Hk, d;
