@@ -124,12 +124,12 @@ void few_plan(long long units, int Nk, CrossPlan* c) {
 // The backward's splits and blocks. Splits: until dK/dV has 128 units or they are down to 16 query steps, dQ 64
 // units or 8 key blocks. Blocks: as many as there are units, but not under 16 steps (8 key blocks) each while 128
 // blocks remain. Measured, bf16 backward, us (dK/dV splits / blocks, dQ splits / blocks; * what this plan takes):
-// 16 heads, 4095 queries over 77 keys, d = 64: *4 / 64, 1 / 128 39; 4 / 32, 1 / 104 54; 32 / 256, 1 / 512 49.
-// Two sequences of 16/4 heads: *16 / 128, 1 / 128 50.5; 8 / 64, 1 / 128 63; 16 / 128, 1 / 512 57; 32 / 256, 1 / 128 58.
-// 2 x 16/4 heads, 1024 over 1024: *2 / 128, 1 / 256 81; 1 / 64, 1 / 62 107; 4 / 256, 1 / 256 89.
-// 16 heads, 64 queries over 16384 keys: *1 / 128, 4 / 64 114; 1 / 128, 1 / 16 157.
-// 4 x 16 heads, 2048 over 512 keys (texts of 512, 227, 453 and 169): *1 / 256, 1 / 512 152 (133); 1 / 152, 1 / 304 157
-// (138); 1 / 128, 1 / 256 162 (143); 1 / 152, 1 / 152 167 (149); 2 / 512, 1 / 512 199 (174).
+// 16 heads, 4095 queries over 77 keys, d = 64: *4 / 64, 1 / 128 38; 4 / 32, 1 / 104 57; 32 / 256, 1 / 512 55.
+// Two sequences of 16/4 heads: *16 / 128, 1 / 128 56; 8 / 64, 1 / 128 66; 16 / 128, 1 / 512 61; 32 / 256, 1 / 128 65.
+// 2 x 16/4 heads, 1024 over 1024: *2 / 128, 1 / 256 93; 1 / 64, 1 / 62 101; 4 / 256, 1 / 256 100.
+// 16 heads, 64 queries over 16384 keys: *1 / 128, 4 / 64 136; 1 / 128, 1 / 16 268.
+// 4 x 16 heads, 2048 over 512 keys (texts of 512, 227, 453 and 169): *1 / 256, 1 / 512 167 (143); 1 / 152, 1 / 304 166
+// (147); 1 / 128, 1 / 256 175 (150); 1 / 152, 1 / 152 178 (158); 2 / 512, 1 / 512 220 (187).
 void bwd_plan(const fa_cross_shape* s, long long groups, long long tiles, CrossPlan* c) {
   const int steps = c->step.count(s->Nq, s->Hq / s->Hk), blocks = (int)div_up(s->Nk, 128);
   const long long kv = groups * div_up(s->Nk, 128), q = groups * tiles;
@@ -200,18 +200,22 @@ FwdLayout fwd_layout(const fa_cross_shape* s, const CrossPlan& c) {
   return {lse, lse + round256(rows * 4)};
 }
 
-// Backward: [-L * log2(e) | -D | fp16: |dO| | maxima | dQ of the splits | dK and dV of the splits].
+// Backward: [-L * log2(e) | -D | fp16: |dO| | its maxima | norms of V | dQ of the splits (before it their D) | dK and
+// dV of the splits].
 struct BwdLayout {
-  size_t nD, dout_norm, maxima, dq, dkdv, total;
+  size_t nD, dout_norm, dout_most, v_norm, dq, dkdv, total;
 };
+int v_norms(const fa_cross_shape* s) { return (int)std::min<long long>(fa::kMostNorms, div_up(s->Nk, 128)); }
 BwdLayout bwd_layout(const fa_cross_shape* s, const CrossPlan& c, fa_dtype dtype) {
   const size_t vec = round256((size_t)s->B * s->Hq * padded_queries(s, c) * 4);
   BwdLayout w;
   w.nD = vec;
-  w.dout_norm = w.maxima = w.dq = 2 * vec;
+  w.dout_norm = w.dout_most = w.v_norm = w.dq = 2 * vec;
   if (dtype == FA_F16) {
-    w.maxima = w.dout_norm + vec;
-    w.dq = w.maxima + round256((size_t)s->B * s->Hk * sizeof(fa::CrossMaxima));
+    const size_t heads = (size_t)s->B * s->Hk;
+    w.dout_most = w.dout_norm + vec;
+    w.v_norm = w.dout_most + round256(heads * 4);
+    w.dq = w.v_norm + round256(heads * v_norms(s) * 4);
   }
   w.dkdv = w.dq + (c.k_splits > 1 ? round256((size_t)c.k_splits * s->B * s->Nq * s->Hq * s->d * 4) : 0);
   w.total = w.dkdv + (c.q_splits > 1 ? round256((size_t)c.q_splits * 2 * s->B * s->Nk * s->Hk * s->d * 4) : 0);
@@ -318,7 +322,9 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
   p.nL2 = reinterpret_cast<float*>(ws);
   p.nD = reinterpret_cast<float*>(ws + w.nD);
   p.dout_norm = reinterpret_cast<float*>(ws + w.dout_norm);
-  p.maxima = reinterpret_cast<fa::CrossMaxima*>(ws + w.maxima);
+  p.dout_most = reinterpret_cast<unsigned int*>(ws + w.dout_most);
+  p.v_norm = reinterpret_cast<float*>(ws + w.v_norm);
+  p.v_norms = v_norms(shape);
   p.part = reinterpret_cast<float*>(ws + w.dq);
   p.part_kv = reinterpret_cast<float*>(ws + w.dkdv);
   if ((rc = fa::status_ptr(&p.status))) return rc;
@@ -334,7 +340,7 @@ int fa_cross_bwd(const fa_cross_shape* shape, const void* q, const void* k, cons
         !k_map(&maps[5], p, v, v_strides, dtype))
       return FA_ERR_CUDA;
   }
-  cudaError_t e = fa::launch_cross_preprocess(p, dtype, st);
+  cudaError_t e = f32 ? fa::launch_cross_preprocess_f32(p, st) : fa::launch_cross_dot(p, bf16, maps + 2, st);
   if (e == cudaSuccess) e = f32 ? fa::launch_cross_bwd_f32(p, st) : fa::launch_cross_bwd_tc(p, bf16, maps, st);
   if (e == cudaSuccess && (plan.q_splits > 1 || plan.k_splits > 1)) e = fa::launch_cross_join_bwd(p, dtype, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

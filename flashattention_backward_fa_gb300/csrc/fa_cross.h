@@ -40,19 +40,18 @@ constexpr float kCrossPLog2 = kBf16 ? 0.f : 15.f;
 template <bool kBf16>
 constexpr float kCrossPUnit = kBf16 ? 1.f : 32768.f;
 
-// dS in fp16. |dS| <= P bound with bound_i = |dO_i| max_j |V_j| + |D_i| (2-norms, the sequence's real keys): above
-// 65504 it is infinite and below 2^-14 loses its bits and its residual, both within the range of ordinary calls (loss
-// scaling; upstream gradients of 1e-3 over 4096 keys). So dS enters dQ's product times 2^e of its row, and dK's times
-// 2^e of its key head (by the largest bound of the group's rows), 2^e bound in [2^14, 2^15), and the sums are
-// multiplied by 2^-e. dQ of 200 queries over 4096 keys with dO of 1e-3 6.2 -> 1.0 times its own rounding, dK 2.3 ->
-// 1.0; fp16 backward of 4x16 2048x512 124 -> 132 us, 2x16/4 4095x77 55 -> 60, 1x32/8 8192x4096 1398 -> 1455.
-__device__ __forceinline__ int cross_exponent(float bound) {
-  return min(max(14 + 127 - (__float_as_int(bound) >> 23 & 255), -64), 100);  // (0, infinity, NaN: any will do)
+// dS in fp16. |dP_ij - D_i| <= bound_i = 2 |dO_i| max_j |V_j| (2-norms, the sequence's real keys; D is a mean of
+// dP): above 65504 dS is infinite and below 2^-14 loses its bits and its residual, both within the range of ordinary
+// calls (loss scaling; upstream gradients of 1e-3 over 4096 keys). So dS enters dQ's product times 2^e of its row, and
+// dK's times 2^e of its key head (by the largest bound of the group's rows), 2^e bound in [2^14, 2^15), and the sums
+// are multiplied by 2^-e. dQ of 200 queries over 4096 keys with dO of 1e-3 6.2 -> 1.0 times its own rounding, dK 2.3
+// -> 1.0.
+__device__ __forceinline__ int cross_exponent(float dout_norm, float v_norm) {
+  const int bits = __float_as_int(2.f * dout_norm * v_norm);
+  return min(max(14 + 127 - (bits >> 23 & 255), -64), 100);  // (0, infinity, NaN: any will do)
 }
 __device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }
-struct CrossMaxima {  // of a (batch, key head): bits of floats that are not negative
-  unsigned int v, dout, D, pad;  // of |V_j|^2, |dO_i| and |D_i|
-};
+constexpr int kMostNorms = 64;  // partial maxima of |V_j|^2 of a (batch, key head)
 
 struct CrossPlan {
   int k_splits;  // each takes an even share of a sequence's key blocks
@@ -86,9 +85,12 @@ struct CrossParams {
   float* nL2;
   float* nD;
   int nq_pad;
-  // fp16 (cross_exponent): |dO_i| of every query row, [B * Hq, nq_pad], and the maxima of every (batch, key head).
+  // fp16 (cross_exponent): |dO_i| of every query row, [B * Hq, nq_pad], and of every (batch, key head) the largest
+  // (bits of a float that is not negative) and partial maxima of |V_j|^2, [B * Hk, v_norms].
   float* dout_norm;
-  CrossMaxima* maxima;
+  unsigned int* dout_most;
+  float* v_norm;
+  int v_norms;
   // Split results in fp32: the forward's normalised outputs [k_splits][B, Nq, Hq, d]
   // and their log2-sum-exp2 [k_splits][B, Hq, Nq] (-inf: the split has no key of the
   // row, and no output is there); dQ [k_splits][B, Nq, Hq, d]; dK and dV
@@ -117,6 +119,7 @@ struct CrossUnit {
   int b, hk, split, nq;
   int j_begin, j_end, blocks;  // keys, and their blocks of 128 (0: nothing to compute)
   int q0[2], h0[2];            // first query and head (of all heads) of a tile
+  float v_norm;                // fp16, dQ: the largest |V_j| (cross_v_norm)
   int has;                     // bit x: tile x exists; bit 2 + x: it has a real query
   __device__ __forceinline__ bool there(int x) const { return has >> x & 1; }
   __device__ __forceinline__ bool live(int x) const { return has >> (2 + x) & 1; }
@@ -305,11 +308,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int cross_head_exponent(const CrossMaxima& m) {
-  return cross_exponent(__uint_as_float(m.dout) * sqrtf(__uint_as_float(m.v)) + __uint_as_float(m.D));
+// max_j |V_j| of a (batch, key head).
+__device__ __forceinline__ float cross_v_norm(const CrossParams& p, int bh) {
+  float top = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < p.v_norms; ++i) top = fmaxf(top, p.v_norm[(long long)bh * p.v_norms + i]);
+  return sqrtf(top);
 }
 
-cudaError_t launch_cross_preprocess(const CrossParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_cross_preprocess_f32(const CrossParams& p, cudaStream_t st);
 cudaError_t launch_cross_join_fwd(const CrossParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_cross_join_bwd(const CrossParams& p, int dtype, cudaStream_t st);
 
@@ -333,6 +340,9 @@ cudaError_t launch_chained_maps(void (*kernel)(Args...), dim3 grid, int threads,
 // maps: Q (boxes of the tile's queries x heads), K, V (boxes of 128 rows), all of 64 head-dim
 // elements, 128-byte swizzle.
 cudaError_t launch_cross_fwd_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
+
+// -L * log2(e) and -D of the query rows, 16-bit types. maps: Q and dO of the query tiles, K, V (boxes of 128 rows).
+cudaError_t launch_cross_dot(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);
 
 // dK, dV and dQ. maps: Q and dO of the query steps, Q and dO of the query tiles, K, V (boxes of 128 rows).
 cudaError_t launch_cross_bwd_tc(const CrossParams& p, bool bf16, const CUtensorMap* maps, cudaStream_t st);

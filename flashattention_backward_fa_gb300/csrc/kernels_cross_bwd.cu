@@ -9,16 +9,14 @@
 // of several where queries are few; the steps run over all heads of the group, so shared
 // key heads cost no extra sums), S^T and dP^T in double buffers, P^T and dS^T written back
 // over them in 16 bits with their rounding residual where the tile holds probabilities
-// above kSplitThreshold, as in fa_bwd, dV and dK in TMEM (bf16 error of dK and dV against 64 bits,
-// 2-norm of themselves, 4x16 2048x512: 1.7e-3 and 1.7e-3, of which 1.66e-3 is the results' own rounding;
-// with the residuals above 1/4 only 2.35e-3 and 2.29e-3. 1x32/8 8192x4096 2.0e-3 and 1.9e-3 against
-// 2.35e-3 and 2.31e-3. Forward and backward 168 against 162 us, 2040 against 1950). dQ: 128
-// query rows on the lanes, steps of 128 keys,
-// dS always with its residual: a row's dS add up to 0, their roundings do not, and what is
-// left of them is multiplied by the mean of the keys under P, which is not small where q and
-// k share a large channel (error of dQ with such channels, bf16 3x16 1551 over 160 keys,
-// 2.7e-3 without residuals, 2.1e-3 with them; of the result's own rounding 1.7e-3; 4% of the
-// backward's time). What remains is, over more than 64 keys, D's error by O's 16 bits.
+// above kSplitThreshold, as in fa_bwd, dV and dK in TMEM. (Error against 64 bits, 2-norm, in
+// units of the result's own rounding, bf16 4x16 2048x512: dK and dV 1.00; with the residuals
+// above 1/4 only 1.41 and 1.38. 1x32/8 8192x4096 1.18 and 1.17 against 1.41 and 1.39. Forward
+// and backward 168 against 162 us, 2040 against 1950, measured with D from O.) dQ: 128 query rows
+// on the lanes, steps of 128 keys, dS always with its residual: a row's dS add up to 0, their
+// roundings do not, and what is left of them is multiplied by the mean of the keys under P, which
+// is not small where q and k have large channels (bf16 700 over 160 keys 1.46 without, 1.00 with
+// them; 4% of the backward's time). D comes from the scores (kernels_cross_dot.cu).
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //
@@ -198,7 +196,11 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
   if ((int)threadIdx.x < mine) {
     KUnit u;
     k_unit(p, first + threadIdx.x * stride, u);
-    u.exp = kBf16 ? 0 : cross_head_exponent(p.maxima[u.b * p.Hk + u.hk]);
+    u.exp = 0;
+    if constexpr (!kBf16) {
+      const int bh = u.b * p.Hk + u.hk;
+      u.exp = cross_exponent(__uint_as_float(p.dout_most[bh]), cross_v_norm(p, bh));
+    }
     unit[threadIdx.x] = u;
   }
   tc_fence_before();
@@ -658,6 +660,7 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
   if ((int)threadIdx.x < mine) {
     CrossUnit u;
     cross_unit<1>(p, first + threadIdx.x * stride, u);
+    u.v_norm = kBf16 ? 0.f : cross_v_norm(p, u.b * p.Hk + u.hk);
     unit[threadIdx.x] = u;
   }
   tc_fence_before();
@@ -816,8 +819,7 @@ __device__ __forceinline__ void dq_block(const CrossParams& p, const CUtensorMap
         nl = p.nL2[at];
         nd = p.nD[at];
         if constexpr (!kBf16) {
-          const float v_norm = sqrtf(__uint_as_float(p.maxima[u.b * p.Hk + u.hk].v));
-          const int e = cross_exponent(p.dout_norm[at] * v_norm + fabsf(nd));
+          const int e = cross_exponent(p.dout_norm[at], u.v_norm);
           nl += (float)e - kCrossPLog2<kBf16>;
           back = power_of_2(-e);
         }

@@ -502,10 +502,11 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * the forward where a key head has few query rows (16, or up to 64 in small calls).
  * fp16 operands of the backward are taken into the type's range by powers of two (dS for
  * dq by its row, dS for dk by its key head, P for dv by 2^15), so small and large upstream
- * gradients and long key axes cost no accuracy: dS is off by at most 2^-40 of what
- * |dout_i| max_j |v_j| + |D_i| allows, P of dv by 2^-40, P of the forward by 2^-25 of the
- * row's largest, where these are more. D takes o as it is given, in 16 bits, or, for
- * sequences of up to 64 real keys, the scores, sum_j P_ij dP_ij (o is not read then).
+ * gradients and long key axes cost no accuracy: dS is off by at most 2^-39 of what
+ * |dout_i| max_j |v_j| allows, P of dv by 2^-40, P of the forward by 2^-25 of the row's
+ * largest, where these are more. With 16-bit tensors D is formed from the scores, as
+ * sum_j P_ij dP_ij, and o is not read (its 16 bits in D would be most of dq's and dk's
+ * error where rows are sharp).
  * Errors as fa_fwd / fa_bwd.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -21,23 +21,22 @@ import torch
 BF16, F16 = torch.bfloat16, torch.float16
 
 
-def activations(g, shape, dtype, big=4.0):
-    """Unit spread, a few channels (three in a hundred, two at least) `big` times as large."""
-    x = torch.randn(shape, generator=g)
-    x[..., torch.randperm(shape[-1], generator=g)[:max(2, shape[-1] * 3 // 100)]] *= big
+def activations(g, shape, dtype, big=4.0, shared=False):
+    """Unit spread, a few channels (three in a hundred, two at least; shared: the first) `big` times as large."""
+    x, n = torch.randn(shape, generator=g), max(2, shape[-1] * 3 // 100)
+    x[..., torch.arange(n) if shared else torch.randperm(shape[-1], generator=g)[:n]] *= big
     return x.to(dtype)
 
 
 # What a case is about: an output, the switch of `emulate` that makes it coarser, and the limit between; `own`: the
 # roundings that the kernels make besides (P of the tile kernels' forward and, where no key has a 64th of a
-# row, P and dS of dV and dK once; D of more than 64 keys from the rounded o). Then the inputs.
-TILES = dict(split_o=False, d_scores=False)
-ONCE, ROUNDED_O = dict(split_o=False, split_kv=False), dict(split_o=False, split_kv=False, d_scores=False)
+# row, P and dS of dV and dK once). Then the inputs.
+TILES, ONCE = dict(split_o=False), dict(split_o=False, split_kv=False)
 CASES = {
     # dQ takes dS with its residual
-    "dq_channels": dict(off=("dq", "split_dq"), own=ROUNDED_O, most=1.3, dtype=BF16, B=1, Nq=700, Nk=160, Hq=2, Hk=1,
+    "dq_channels": dict(off=("dq", "split_dq"), own=ONCE, most=1.3, dtype=BF16, B=1, Nq=700, Nk=160, Hq=2, Hk=1,
                         d=128),
-    "dq_channels_f16": dict(off=("dq", "split_dq"), own=ROUNDED_O, most=1.3, dtype=F16, B=1, Nq=700, Nk=160, Hq=2,
+    "dq_channels_f16": dict(off=("dq", "split_dq"), own=ONCE, most=1.3, dtype=F16, B=1, Nq=700, Nk=160, Hq=2,
                             Hk=1, d=128),
     # dK and dV take the residuals of dS and P where a key has a 64th of a row: over some hundreds of keys, and where a
     # row is made up of a few
@@ -50,23 +49,30 @@ CASES = {
     # few rows a key head: the forward multiplies P's residual
     "few_rows": dict(off=("o", "split_o"), own={}, most=1.2, dtype=BF16, B=2, Nq=3, Nk=1000, Hq=4, Hk=2, d=128),
     "few_rows_f16": dict(off=("o", "split_o"), own={}, most=1.15, dtype=F16, B=2, Nq=1, Nk=1499, Hq=8, Hk=8, d=64),
-    # D of sequences of up to 64 keys comes from the scores, whatever the batch is padded to
+    # D comes from the scores, not from the rounded o: over few keys, alone or padded to many, where q, k and v share
+    # large channels, and where a row is nearly all one key
     "d_of_short": dict(off=("dq", "d_scores"), own=ONCE, most=1.35, dtype=BF16, B=4, Nq=300, Nk=512, Hq=2, Hk=2, d=64,
                        k_lens=[4, 8, 24, 60]),
     "d_of_short_f16": dict(off=("dq", "d_scores"), own=ONCE, most=1.25, dtype=F16, B=4, Nq=150, Nk=300, Hq=2, Hk=1,
                            d=128, k_lens=[4, 8, 24, 40]),
     "d_of_short_only": dict(off=("dq", "d_scores"), own=ONCE, most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
                             d=128, k_lens=[4, 8, 30]),
+    "d_shared": dict(off=("dq", "d_scores"), own=TILES, most=1.3, dtype=BF16, B=2, Nq=260, Nk=1500, Hq=2, Hk=1, d=128,
+                     k_lens=[1500, 333], shared=True),
+    "d_shared_f16": dict(off=("dq", "d_scores"), own=TILES, most=1.3, dtype=F16, B=1, Nq=100, Nk=4000, Hq=2, Hk=2,
+                         d=64, shared=True),
+    "d_sharp": dict(off=("dk", "d_scores"), own=TILES, most=1.5, dtype=BF16, B=1, Nq=300, Nk=200, Hq=2, Hk=2, d=64,
+                    sharp=8.0),
     # fp16: dS of small upstream gradients over many keys, and P of many keys, below fp16's normal values
-    "dq_small": dict(off=("dq", "scaled"), own=ROUNDED_O, most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
+    "dq_small": dict(off=("dq", "scaled"), own=ONCE, most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
                      do=1e-3),
-    "dk_small": dict(off=("dk", "scaled"), own=ROUNDED_O, most=1.6, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
+    "dk_small": dict(off=("dk", "scaled"), own=ONCE, most=1.6, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
                      do=1e-3),
-    "dq_tiny": dict(off=("dq", "scaled"), own=ROUNDED_O, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
+    "dq_tiny": dict(off=("dq", "scaled"), own=ONCE, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
                     do=1e-4, k_lens=[5000, 4097]),
-    "dk_tiny": dict(off=("dk", "scaled"), own=ROUNDED_O, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
+    "dk_tiny": dict(off=("dk", "scaled"), own=ONCE, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
                     do=1e-4, k_lens=[5000, 4097]),
-    "dv_long": dict(off=("dv", "scaled"), own=ROUNDED_O, most=1.6, dtype=F16, B=1, Nq=130, Nk=40000, Hq=1, Hk=1, d=64,
+    "dv_long": dict(off=("dv", "scaled"), own=ONCE, most=1.6, dtype=F16, B=1, Nq=130, Nk=40000, Hq=1, Hk=1, d=64,
                     sharp=0.1),
     # rows of unlike upstream gradients: each row of dQ by itself
     "dq_rows_apart": dict(off=("dq", "scaled"), own=ONCE, most=1.5, rows=True, dtype=F16, B=1, Nq=64, Nk=64, Hq=4,
@@ -77,8 +83,9 @@ CASES = {
 def inputs(case, seed=0):
     c, g = case, torch.Generator().manual_seed(seed)
     B, Nq, Nk, Hq, Hk, d, t = (c[n] for n in ("B", "Nq", "Nk", "Hq", "Hk", "d", "dtype"))
-    q = (activations(g, (B, Nq, Hq, d), torch.float32) * c.get("sharp", 1.0)).to(t)
-    k, v = activations(g, (B, Nk, Hk, d), t), activations(g, (B, Nk, Hk, d), t)
+    shared = c.get("shared", False)
+    q = (activations(g, (B, Nq, Hq, d), torch.float32, shared=shared) * c.get("sharp", 1.0)).to(t)
+    k, v = (activations(g, (B, Nk, Hk, d), t, shared=shared) for _ in range(2))
     do = torch.randn((B, Nq, Hq, d), generator=g) * c.get("do", 1.0)
     if "spread" in c:  # the first row's as it is, the last one's 2^-spread of it
         do = do * torch.exp2(-torch.linspace(0, c["spread"], Nq))[:, None, None]
@@ -150,7 +157,7 @@ def emulate(q, k, v, do, q_lens=None, k_lens=None, split_o=True, split_kv=True, 
         o = short(operand(p / top, t, split_o) @ vv * top, t)
         D = (p * dp).sum(-1, keepdim=True) if d_scores else (g * o).sum(-1, keepdim=True)
         ds = p * (dp - D)
-        bound = g.norm(dim=-1, keepdim=True) * vv.norm(dim=-1).max() + D.abs()
+        bound = 2 * g.norm(dim=-1, keepdim=True) * vv.norm(dim=-1).max()
         row = torch.exp2(exponent(bound)) if scaled else 1.0
         all_ = torch.exp2(exponent(bound.max())) if scaled else 1.0
         one = 2.0 ** 15 if scaled else 1.0
