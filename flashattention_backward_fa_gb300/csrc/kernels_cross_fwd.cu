@@ -11,17 +11,21 @@
 // O_A [256, 256 + d), O_B after it. One warp issues all MMAs, per key block
 // O_A(j), S_A(j+1), O_B(j), S_B(j+1): while tile A's softmax warps turn S_A into P_A, the
 // tensor cores run tile B. Eight softmax warps a tile: a row is split between two
-// warps (the same TMEM lane), 64 keys of a block each, that exchange only their
-// halves' maxima a block and their sums at the end. P goes back over the S columns it
-// came from, rounded to 16 bits, and the O MMA reads it from TMEM. The row's reference m
-// moves only when a block's maximum exceeds it by more than 2^8.
+// warps (the same TMEM lane), 64 keys of a block each, that exchange only whether a row's
+// reference has to move a block (and then their halves' maxima) and their sums at the end. P
+// goes back over the S columns it came from, per K step of 16 keys as 8 columns of 16-bit
+// values and 8 of their rounding residuals, and the O MMAs read both from TMEM. The row's
+// reference m moves only when a block's maximum exceeds it by more than 2^8.
 //
-// The rounding of P moves an output by at most half a step of each weight, about what the
-// rounding of the output itself does (bf16, 2-norm error against 64 bits: 1.66e-3 with
-// exact weights, 2.3e-3 with rounded ones, over 512 or 4096 keys). Its residual as a second
-// product, as in fa_fwd, is half as many MMAs again where they are what bounds the kernel: with
-// it for every tile, and 1.66e-3, 4x16 4096x512 takes 97 us instead of 70, 1x32/8 8192x4096 605
-// instead of 397, 1x16 64x16383 45 instead of 33, 2x16/4 4095x77, d = 64, 22.3 instead of 18.2.
+// The residuals are half as many MMAs again. Rounded once, P moves an output about as much as
+// the rounding of the output itself does (bf16, 2-norm error against 64 bits 2.3e-3 over 77 as
+// over 16383 keys; 1.66e-3 with residuals, which is the output's own rounding). What they cost
+// (us, with / without): 4x16 4096 over texts of 169 to 512 84 / 70, 2x16/4 4095 over 34 and 77,
+// d = 64, 21.3 / 18.2, 1x16 64 over 16383 40 / 33, 1x32/8 8192 over 4096 518 / 397, d = 64 459 /
+// 340. (In the form of one pass without them, which kept P's image in registers until both warps
+// agreed on the reference, they spilled: 97 and 605.) Not only for tiles with large weights,
+// as in fa_fwd: over a few hundred keys nearly every tile has some, and a branch in front of the
+// residuals' MMAs took 25% by itself.
 //
 // Few keys a unit are the common case here (a text's 77 to 512), so a unit is short: steps,
 // ring stages and barrier phases run on from unit to unit, the next unit's queries and
@@ -231,8 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd = desc_add(dV0, (t % C::kNV) * C::kTile);
       const uint32_t tO = tmem + 256 + D * x, tP = tmem + 128 * x;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)  // (a half's image: the first 32 of its 64 columns)
-        tc_mma_ts_w(tO, tP + 64 * (k >> 2) + 8 * (k & 3), desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
+      for (int k = 0; k < 8; ++k)  // (a K step's image: 8 rounded columns, then 8 of their residuals)
+        tc_mma_ts_w(tO, tP + 16 * k, desc_add(vd, 2048 * k), idO, k > 0 || !first ? 1u : 0u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) tc_mma_ts_w(tO, tP + 16 * k + 8, desc_add(vd, 2048 * k), idO, 1u);
       tc_commit_w(bar(C::bODone + x));
     };
     struct {
@@ -357,71 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; ++e) mref = e < in ? fmaxf(mref, __uint_as_float(cur[e])) : mref;
           mref *= c2;
         }
-        // One pass with the reference as it stands, which it nearly always does: P, its sum and its image are
-        // kept in registers until both warps of the rows say that no row's maximum asks for a new reference.
-        // The two passes below (maximum, exchange, P) run otherwise.
-        uint32_t img[32];
-        {
-          const float base = mref == -INFINITY ? 0.f : mref;
-          const uint64_t cc2 = f2_pack(c2, c2), nm2 = f2_pack(-base, -base);
-          float top = -INFINITY;
-          uint64_t sum2 = f2_pack(0.f, 0.f);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t cur[32];
-            __syncwarp();
-            tmem_ld32(tS + 32 * q, cur);
-            tmem_ld_wait(cur);
-            if (hi >= 64) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float p0, p1;
-                top = fmax3(top, __uint_as_float(cur[e]), __uint_as_float(cur[e + 1]));
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
-                p0 = ex2_approx(p0);
-                p1 = ex2_approx(p1);
-                sum2 = f2_add(sum2, f2_pack(p0, p1));
-                img[16 * q + e / 2] = pack2<kBf16>(p0, p1);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float p0, p1;
-                const bool in0 = 32 * q + e < hi, in1 = 32 * q + e + 1 < hi;
-                top = in0 ? fmaxf(top, __uint_as_float(cur[e])) : top;
-                top = in1 ? fmaxf(top, __uint_as_float(cur[e + 1])) : top;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
-                p0 = in0 ? ex2_approx(p0) : 0.f;
-                p1 = in1 ? ex2_approx(p1) : 0.f;
-                sum2 = f2_add(sum2, f2_pack(p0, p1));
-                img[16 * q + e / 2] = pack2<kBf16>(p0, p1);
-              }
-            }
-          }
-          float s0, s1;
-          f2_unpack(sum2, s0, s1);
-          const bool moves = __any_sync(0xffffffffu, real && top * c2 > mref + kRescaleLog2);
-          if (lane == 0) fast[16 * (nf & 1) + (warp - 2)] = moves;
-          warp_arrive(bar(C::bFast + pq));
-          if (!warp_wait<false>(bar(C::bFast + pq), nf & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const bool either = moves || fast[16 * (nf & 1) + ((warp - 2) ^ 4)] != 0;
-          ++nf;
-          if (!either) {
-            lsum += s0 + s1;
-            tmem_st32(tS, img);
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(bar(C::bPFull + x));
-            continue;
-          }
-        }
-        // Pass 1: this half's maximum of S.
+        // This half's maximum of S. Both warps of the rows move the reference where a row's maximum asks for it,
+        // which it nearly never does after the first block: the outcomes are exchanged before the maxima.
         float hmax = -INFINITY;
         {
           uint32_t s0[32], s1[32];
+          __syncwarp();
           tmem_ld32(tS, s0);
           tmem_ld32(tS + 32, s1);
           tmem_ld_wait2(s0, s1);
@@ -441,68 +388,98 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // The block maximum of the row: this half's and the other warp's (slots alternate
-        // from exchange to exchange, so a slot is rewritten only after the partner has passed
-        // the next one, i.e. has read it).
-        float* xs = xchg + ((x * 2 + (nx & 1)) * 2) * 128;
-        xs[half * 128 + il] = hmax;
-        warp_arrive(bar(C::bXchg + pq));
-        if (!warp_wait<false>(bar(C::bXchg + pq), nx & 1, abort_flag, p.status)) {
+        const bool moves = __any_sync(0xffffffffu, real && hmax * c2 > mref + kRescaleLog2);
+        if (lane == 0) fast[16 * (nf & 1) + (warp - 2)] = moves;
+        warp_arrive(bar(C::bFast + pq));
+        if (!warp_wait<false>(bar(C::bFast + pq), nf & 1, abort_flag, p.status)) {
           ok = false;
           break;
         }
-        ++nx;
-        const float bmax = fmaxf(hmax, xs[(half ^ 1) * 128 + il]) * c2;  // (scale > 0)
-        // Lazy rescale. Both warps of a row take the same decision; each rescales its D/2 O columns.
-        const bool mv = bmax > mref + kRescaleLog2;
-        const float alpha = mv ? ex2_approx(mref - bmax) : 1.f;  // 0 when mref = -inf
-        // (warp-wide decision: the wait and the TMEM accesses below are collective)
-        if (j > 0 && __any_sync(0xffffffffu, mv && mref != -INFINITY)) {
-          // this tile's O MMA of the block before is done before its rows are rescaled
-          if (!warp_wait<false>(bar(C::bODone + x), (n - 1) & 1, abort_flag, p.status)) {
+        const bool either = moves || fast[16 * (nf & 1) + ((warp - 2) ^ 4)] != 0;
+        ++nf;
+        if (either) {
+          // The block maximum of the row: this half's and the other warp's (slots alternate
+          // from exchange to exchange, so a slot is rewritten only after the partner has passed
+          // the next one, i.e. has read it).
+          float* xs = xchg + ((x * 2 + (nx & 1)) * 2) * 128;
+          xs[half * 128 + il] = hmax;
+          warp_arrive(bar(C::bXchg + pq));
+          if (!warp_wait<false>(bar(C::bXchg + pq), nx & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          tc_fence_after();
+          ++nx;
+          const float bmax = fmaxf(hmax, xs[(half ^ 1) * 128 + il]) * c2;  // (scale > 0)
+          // Lazy rescale. Both warps of a row take the same decision; each rescales its D/2 O columns.
+          const bool mv = bmax > mref + kRescaleLog2;
+          const float alpha = mv ? ex2_approx(mref - bmax) : 1.f;  // 0 when mref = -inf
+          // (warp-wide decision: the wait and the TMEM accesses below are collective)
+          if (j > 0 && __any_sync(0xffffffffu, mv && mref != -INFINITY)) {
+            // this tile's O MMA of the block before is done before its rows are rescaled
+            if (!warp_wait<false>(bar(C::bODone + x), (n - 1) & 1, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < D / 64; ++cc) {
+              uint32_t r[32];
+              tmem_ld32(tO + 32 * cc, r);
+              tmem_ld_wait(r);
 #pragma unroll
-          for (int cc = 0; cc < D / 64; ++cc) {
-            uint32_t r[32];
-            tmem_ld32(tO + 32 * cc, r);
-            tmem_ld_wait(r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tmem_st32(tO + 32 * cc, r);
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st32(tO + 32 * cc, r);
+            }
+          }
+          if (mv) {
+            lsum *= alpha;
+            mref = bmax;
           }
         }
-        if (mv) {
-          lsum *= alpha;
-          mref = bmax;
-        }
         const float base = mref == -INFINITY ? 0.f : mref;  // (every score so far is -inf or NaN)
-        // Pass 2, 32 keys at a time: P (0 past the end), this half's running sum, and the image.
+        // 32 keys at a time: P (0 past the end), this half's running sum, and the image.
         const uint64_t cc2 = f2_pack(c2, c2), nm2 = f2_pack(-base, -base);
+        uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t cur[32];
+          uint32_t cur[32], img[32];
           __syncwarp();
           tmem_ld32(tS + 32 * q, cur);
           tmem_ld_wait(cur);
-          uint64_t sum2 = f2_pack(0.f, 0.f);
+          const auto weights = [&](auto masked) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float p0, p1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
-            p0 = (32 * q + e < hi) ? ex2_approx(p0) : 0.f;
-            p1 = (32 * q + e + 1 < hi) ? ex2_approx(p1) : 0.f;
-            sum2 = f2_add(sum2, f2_pack(p0, p1));
-            img[16 * q + e / 2] = pack2<kBf16>(p0, p1);
-          }
-          float s0, s1;
-          f2_unpack(sum2, s0, s1);
-          lsum += s0 + s1;
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(cur[e]), __uint_as_float(cur[e + 1])), cc2, nm2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              if constexpr (decltype(masked)::value) {
+                p0 = 32 * q + e < hi ? p0 : 0.f;
+                p1 = 32 * q + e + 1 < hi ? p1 : 0.f;
+              }
+              sum2 = f2_add(sum2, f2_pack(p0, p1));
+              uint32_t &top = img[16 * (e >> 4) + ((e & 15) >> 1)], &rest = img[16 * (e >> 4) + ((e & 15) >> 1) + 8];
+              if constexpr (kBf16) {
+                top = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+                float r0, r1;
+                f2_unpack(f2_add(f2_pack(p0, p1), f2_pack(-__uint_as_float(__float_as_uint(p0) & 0xFFFF0000u),
+                                                          -__uint_as_float(__float_as_uint(p1) & 0xFFFF0000u))),
+                          r0, r1);
+                rest = pack2<kBf16>(r0, r1);
+              } else {
+                top = pack2<kBf16>(p0, p1);
+                rest = pack2_residual<kBf16>(p0, p1, top);
+              }
+            }
+          };
+          if (hi >= 64)
+            weights(std::false_type{});
+          else
+            weights(std::true_type{});
+          __syncwarp();
+          tmem_st32(tS + 32 * q, img);
         }
-        __syncwarp();
-        tmem_st32(tS, img);
+        lsum += f2_sum(sum2);
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(bar(C::bPFull + x));

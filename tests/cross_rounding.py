@@ -29,9 +29,9 @@ def activations(g, shape, dtype, big=4.0, shared=False):
 
 
 # What a case is about: an output, the switch of `emulate` that makes it coarser, and the limit between; `own`: the
-# roundings that the kernels make besides (P of the tile kernels' forward and, where no key has a 64th of a
-# row, P and dS of dV and dK once). Then the inputs.
-TILES, ONCE = dict(split_o=False), dict(split_o=False, split_kv=False)
+# roundings that the kernels make besides (where no key has a 64th of a row, P and dS of dV and dK once). Then the
+# inputs.
+ONCE = dict(split_kv=False)
 CASES = {
     # dQ takes dS with its residual
     "dq_channels": dict(off=("dq", "split_dq"), own=ONCE, most=1.3, dtype=BF16, B=1, Nq=700, Nk=160, Hq=2, Hk=1,
@@ -40,15 +40,19 @@ CASES = {
                             Hk=1, d=128),
     # dK and dV take the residuals of dS and P where a key has a 64th of a row: over some hundreds of keys, and where a
     # row is made up of a few
-    "dk_hundreds": dict(off=("dk", "split_kv"), own=TILES, most=1.2, dtype=BF16, B=1, Nq=500, Nk=300, Hq=2, Hk=1, d=128),
-    "dv_hundreds": dict(off=("dv", "split_kv"), own=TILES, most=1.2, dtype=F16, B=1, Nq=500, Nk=300, Hq=2, Hk=2, d=64),
+    "dk_hundreds": dict(off=("dk", "split_kv"), own={}, most=1.2, dtype=BF16, B=1, Nq=500, Nk=300, Hq=2, Hk=1, d=128),
+    "dv_hundreds": dict(off=("dv", "split_kv"), own={}, most=1.2, dtype=F16, B=1, Nq=500, Nk=300, Hq=2, Hk=2, d=64),
     "dk_sharp": dict(off=("dk", "split_kv"), own={}, most=1.2, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
                      sharp=4.0),
     "dv_sharp": dict(off=("dv", "split_kv"), own={}, most=1.15, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
                      sharp=4.0),
-    # few rows a key head: the forward multiplies P's residual
+    # the forward multiplies P's residual: few rows a key head, tiles of them, tiles over split keys
     "few_rows": dict(off=("o", "split_o"), own={}, most=1.2, dtype=BF16, B=2, Nq=3, Nk=1000, Hq=4, Hk=2, d=128),
     "few_rows_f16": dict(off=("o", "split_o"), own={}, most=1.15, dtype=F16, B=2, Nq=1, Nk=1499, Hq=8, Hk=8, d=64),
+    "tiles": dict(off=("o", "split_o"), own={}, most=1.15, dtype=BF16, B=2, Nq=300, Nk=512, Hq=2, Hk=2, d=128,
+                  k_lens=[512, 77]),
+    "tiles_f16": dict(off=("o", "split_o"), own={}, most=1.15, dtype=F16, B=1, Nq=200, Nk=300, Hq=4, Hk=1, d=64),
+    "tiles_long": dict(off=("o", "split_o"), own={}, most=1.15, dtype=BF16, B=1, Nq=128, Nk=9000, Hq=2, Hk=2, d=64),
     # D comes from the scores, not from the rounded o: over few keys, alone or padded to many, where q, k and v share
     # large channels, and where a row is nearly all one key
     "d_of_short": dict(off=("dq", "d_scores"), own=ONCE, most=1.35, dtype=BF16, B=4, Nq=300, Nk=512, Hq=2, Hk=2, d=64,
@@ -57,11 +61,11 @@ CASES = {
                            d=128, k_lens=[4, 8, 24, 40]),
     "d_of_short_only": dict(off=("dq", "d_scores"), own=ONCE, most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
                             d=128, k_lens=[4, 8, 30]),
-    "d_shared": dict(off=("dq", "d_scores"), own=TILES, most=1.3, dtype=BF16, B=2, Nq=260, Nk=1500, Hq=2, Hk=1, d=128,
+    "d_shared": dict(off=("dq", "d_scores"), own={}, most=1.3, dtype=BF16, B=2, Nq=260, Nk=1500, Hq=2, Hk=1, d=128,
                      k_lens=[1500, 333], shared=True),
-    "d_shared_f16": dict(off=("dq", "d_scores"), own=TILES, most=1.3, dtype=F16, B=1, Nq=100, Nk=4000, Hq=2, Hk=2,
+    "d_shared_f16": dict(off=("dq", "d_scores"), own={}, most=1.3, dtype=F16, B=1, Nq=100, Nk=4000, Hq=2, Hk=2,
                          d=64, shared=True),
-    "d_sharp": dict(off=("dk", "d_scores"), own=TILES, most=1.5, dtype=BF16, B=1, Nq=300, Nk=200, Hq=2, Hk=2, d=64,
+    "d_sharp": dict(off=("dk", "d_scores"), own={}, most=1.5, dtype=BF16, B=1, Nq=300, Nk=200, Hq=2, Hk=2, d=64,
                     sharp=8.0),
     # fp16: dS of small upstream gradients over many keys, and P of many keys, below fp16's normal values
     "dq_small": dict(off=("dq", "scaled"), own=ONCE, most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
