@@ -8,15 +8,15 @@
 // dK/dV: keys on the 128 TMEM lanes, steps of 64 query rows (of one head of the group, or
 // of several where queries are few; the steps run over all heads of the group, so shared
 // key heads cost no extra sums), S^T and dP^T in double buffers, P^T and dS^T written back
-// over them in 16 bits with their rounding residual where the tile holds probabilities
-// above kSplitThreshold, as in fa_bwd, dV and dK in TMEM. (Error against 64 bits, 2-norm, in
-// units of the result's own rounding, bf16 4x16 2048x512: dK and dV 1.00; with the residuals
-// above 1/4 only 1.41 and 1.38. 1x32/8 8192x4096 1.18 and 1.17 against 1.41 and 1.39. Forward
-// and backward 168 against 162 us, 2040 against 1950, measured with D from O.) dQ: 128 query rows
-// on the lanes, steps of 128 keys, dS always with its residual: a row's dS add up to 0, their
-// roundings do not, and what is left of them is multiplied by the mean of the keys under P, which
-// is not small where q and k have large channels (bf16 700 over 160 keys 1.46 without, 1.00 with
-// them; 4% of the backward's time). D comes from the scores (kernels_cross_dot.cu).
+// over them in 16 bits with their rounding residual, dV and dK in TMEM. dQ: 128 query rows on the
+// lanes, steps of 128 keys, dS with its residual as well. Rounded once, P and dS move dV and dK by
+// about as much as the rounding of the results (2-norm error against 64 bits 1.41 times that, 1.00
+// with residuals), and dQ by more: a row's dS add up to 0, their roundings do not, and what is left
+// of them is multiplied by the mean of the keys under P, which is not small where q and k have large
+// channels (bf16 700 over 160 keys 1.46). Times, us, with all residuals / with those of dV and dK in
+// tiles with a probability above 1/64 only, as in fa_bwd (1.0 to 1.4), whose vote costs some too:
+// bf16 4x16 2048 over texts of 169 to 512 138 / 142, 1x32/8 8192x4096 with even scores 1722 / 1632,
+// with large channels and the forward 2500 / 2445. D comes from the scores (kernels_cross_dot.cu).
 // Warp 0 issues TMA loads, warps 1 and 3 the S and dP MMAs, warp 2 the accumulating
 // ones, warps 4-19 do the row math.
 //
@@ -78,8 +78,7 @@ struct KCfg {
   static constexpr int kBars = bAccFree + 1;
   static constexpr uint32_t oTmemSlot = oBar + kBars * 8;
   static constexpr uint32_t oAbort = oTmemSlot + 8;
-  static constexpr uint32_t oFlags = oAbort + 8;    // [buffer][8 warps] split votes
-  static constexpr uint32_t oUnits = oFlags + 64;   // [kMostUnits]
+  static constexpr uint32_t oUnits = oAbort + 8;    // [kMostUnits]
   static constexpr uint32_t kSmem = oUnits + kMostUnits * 44 + 1024;  // + slack for 1024-byte alignment
   static_assert(kSmem <= 227u * 1024u, "shared memory budget exceeded");
 };
@@ -145,7 +144,6 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::oAbort);
-  volatile int* flags = reinterpret_cast<volatile int*>(smem + C::oFlags);
   auto bar = [&](int idx) -> uint32_t { return sb + C::oBar + 8u * idx; };
   const int mine = (k_units(p) - first + stride - 1) / stride;  // units of this block
   KUnit* const unit = reinterpret_cast<KUnit*>(smem + C::oUnits);
@@ -322,22 +320,16 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           }
         }
         tc_fence_after();
-        int any = 0;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) any |= flags[8 * bt + x];
-        const bool split = uniform(any) != 0;
         const uint32_t keep = it > 0 ? 1u : 0u;
         const uint64_t qd = desc_add(mQ0, st * C::kQTile), gd = desc_add(mO0, st * C::kQTile);
-        // dV += P^T dO: K step kk reads the 8 rounded columns at 16kk of the P^T image and, on split
-        // tiles, the 8 residual columns at 16kk + 8.
+        // dV += P^T dO: K step kk reads the 8 rounded columns at 16kk of the P^T image and the 8 residual
+        // columns at 16kk + 8.
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
           tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk, desc_add(gd, 2048 * kk), idG, kk > 0 ? 1u : keep);
-        if (split) {
 #pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk)
-            tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk + 8, desc_add(gd, 2048 * kk), idG, 1u);
-        }
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma_ts_w(tdV, tS + 64 * bt + 16 * kk + 8, desc_add(gd, 2048 * kk), idG, 1u);
         tc_commit_w(bar(C::bSEmpty + bt));
         // dK once the dS^T image is in place; dV above only needed P^T.
         if (!warp_wait<kConsumerPoll>(bar(C::bDSFull + bt), (G >> 1) & 1, abort_flag, p.status)) {
@@ -348,11 +340,9 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
           tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk, desc_add(qd, 2048 * kk), idG, kk > 0 ? 1u : keep);
-        if (split) {
 #pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk)
-            tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk + 8, desc_add(qd, 2048 * kk), idG, 1u);
-        }
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma_ts_w(tdK, tdP + 64 * bt + 16 * kk + 8, desc_add(qd, 2048 * kk), idG, 1u);
         tc_commit_w(bar(C::bDPEmpty + bt));
         tc_commit_w(bar(C::bQEmpty + st));
       }
@@ -380,12 +370,11 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
       const int steps = u.steps, chunks = max(u.chunks, 1);
       int chunk = u.chunk + ((bb ^ G) & 1);
       chunk -= chunk >= chunks ? chunks : 0;
-      // The columns with real queries of any step but a head's last (or last few heads') and of that one, and
-      // whether the lane has a real key. (A lane without one needs no mask: its row of P^T and dS^T reaches nothing
-      // but its own row of dV and dK, which the epilogue drops. It has no vote.)
+      // The columns with real queries of any step but a head's last (or last few heads') and of that one. (A lane
+      // without a real key needs no mask: its row of P^T and dS^T reaches nothing but its own row of dV and dK, which
+      // the epilogue drops.)
       const uint32_t full = step_columns(p.plan.step, c, kStep);
       const uint32_t tail = step_columns(p.plan.step, c, u.nq - ((chunks - 1) << p.plan.step.q_log));
-      const bool real = u.j0 + jl < u.nk;
       const float to_ds = kBf16 ? 1.f : power_of_2(u.exp - (int)kCrossPLog2<kBf16>);  // from P's power of 2 to dS's
       const uint64_t to_ds2 = f2_pack(to_ds, to_ds);
       for (int it = (bb ^ G) & 1; it < steps; it += 2) {
@@ -403,7 +392,6 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
         const float4* L4 = reinterpret_cast<const float4*>(smem + C::oL + s * kStep * 4 + 128 * c);
         const float4* D4 = reinterpret_cast<const float4*>(smem + C::oD + s * kStep * 4 + 128 * c);
         float P[32];  // of this thread's 32 pairs (times kCrossPUnit), for the dS phase
-        bool split_h[2];
         // ---- phase 1: the P^T image over the S^T columns ----
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -411,7 +399,6 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           __syncwarp();
           tmem_ld16(tSc + 16 * hh, sr);
           tmem_ld_wait16(sr);
-          float cmax = 0.f;
           auto p_phase = [&](auto masked) {
 #pragma unroll
             for (int x = 0; x < 16; x += 4) {
@@ -428,8 +415,6 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
                 if constexpr (decltype(masked)::value) pv[y] = ((allow >> bit) & 1u) ? pv[y] : 0.f;
                 P[bit] = pv[y];
               }
-              cmax = fmax3(cmax, pv[0], pv[1]);
-              cmax = fmax3(cmax, pv[2], pv[3]);
             }
           };
           if (allow == 0xFFFFFFFFu)  // (the same for the whole warp)
@@ -439,21 +424,15 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           uint32_t hp[8], ep[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hp[x] = pack2<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1]);
-          split_h[hh] = __any_sync(0xFFFFFFFFu, real && cmax > kSplitThreshold * kCrossPUnit<kBf16>);
-          if (split_h[hh]) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              ep[x] = pack2_residual<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1], hp[x]);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) ep[x] = 0u;
-          }
+          for (int x = 0; x < 8; ++x)
+            ep[x] = pack2_residual<kBf16>(P[16 * hh + 2 * x], P[16 * hh + 2 * x + 1], hp[x]);
+          __syncwarp();
           // this K step's image: 8 rounded columns, then 8 residual columns
           tmem_st8<0>(tSc + 16 * hh, hp);
           tmem_st8<0>(tSc + 16 * hh + 8, ep);
         }
         tmem_st_wait();
-        if (lane == 0) flags[8 * bb + 4 * c + wq] = (split_h[0] || split_h[1]) ? 1 : 0;
         tc_fence_before();
         warp_arrive(bar(C::bPFull + bb));
         // ---- phase 2: dS^T = P o (dP^T + (-D)) ----
@@ -493,13 +472,8 @@ __device__ __forceinline__ void dkdv_block(const CrossParams& p, const CUtensorM
           uint32_t hd[8], ed[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) hd[x] = pack2<kBf16>(ds[2 * x], ds[2 * x + 1]);
-          if (split_h[hh]) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) ed[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hd[x]);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) ed[x] = 0u;
-          }
+          for (int x = 0; x < 8; ++x) ed[x] = pack2_residual<kBf16>(ds[2 * x], ds[2 * x + 1], hd[x]);
           tmem_st8<0>(tdPc + 16 * hh, hd);
           tmem_st8<0>(tdPc + 16 * hh + 8, ed);
         }

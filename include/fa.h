@@ -496,10 +496,9 @@ int fa_kv8_attn(const fa_kv8_cache* cache, const fa_kv8_seqs* seqs, const void* 
  * and both are 0 for shapes that the calls refuse; calls that overlap on the GPU need
  * workspaces of their own.
  * Scores, softmax statistics, sums over splits and D = rowsum(dout o O) are held in
- * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products. Their
- * rounding residual is multiplied too, so that they are off by at most 2^-15 (bf16) and
- * 2^-22 (fp16) of themselves, but in dk and dv only where a probability of the tile exceeds
- * 1/64; elsewhere there by up to 2^-8 and 2^-11.
+ * fp32. In 16 bits (fp16 and bf16 tensors): P and dS as operands of the products, each with
+ * its rounding residual, so that they are off by at most 2^-15 (bf16) and 2^-22 (fp16) of
+ * themselves.
  * fp16 operands of the backward are taken into the type's range by powers of two (dS for
  * dq by its row, dS for dk by its key head, P for dv by 2^15), so small and large upstream
  * gradients and long key axes cost no accuracy: dS is off by at most 2^-39 of what

@@ -28,58 +28,56 @@ def activations(g, shape, dtype, big=4.0, shared=False):
     return x.to(dtype)
 
 
-# What a case is about: an output, the switch of `emulate` that makes it coarser, and the limit between; `own`: the
-# roundings that the kernels make besides (where no key has a 64th of a row, P and dS of dV and dK once). Then the
-# inputs.
-ONCE = dict(split_kv=False)
+# What a case is about: an output, the switch of `emulate` that makes it coarser, and the limit between, which the
+# kernels stay under; then the inputs.
 CASES = {
     # dQ takes dS with its residual
-    "dq_channels": dict(off=("dq", "split_dq"), own=ONCE, most=1.3, dtype=BF16, B=1, Nq=700, Nk=160, Hq=2, Hk=1,
-                        d=128),
-    "dq_channels_f16": dict(off=("dq", "split_dq"), own=ONCE, most=1.3, dtype=F16, B=1, Nq=700, Nk=160, Hq=2,
-                            Hk=1, d=128),
-    # dK and dV take the residuals of dS and P where a key has a 64th of a row: over some hundreds of keys, and where a
-    # row is made up of a few
-    "dk_hundreds": dict(off=("dk", "split_kv"), own={}, most=1.2, dtype=BF16, B=1, Nq=500, Nk=300, Hq=2, Hk=1, d=128),
-    "dv_hundreds": dict(off=("dv", "split_kv"), own={}, most=1.2, dtype=F16, B=1, Nq=500, Nk=300, Hq=2, Hk=2, d=64),
-    "dk_sharp": dict(off=("dk", "split_kv"), own={}, most=1.2, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
+    "dq_channels": dict(off=("dq", "split_dq"), most=1.3, dtype=BF16, B=1, Nq=700, Nk=160, Hq=2, Hk=1, d=128),
+    "dq_channels_f16": dict(off=("dq", "split_dq"), most=1.3, dtype=F16, B=1, Nq=700, Nk=160, Hq=2, Hk=1, d=128),
+    # dK and dV take the residuals of dS and P: where a row is made up of a few keys, over some hundreds, and over many
+    # of even weight
+    "dk_hundreds": dict(off=("dk", "split_kv"), most=1.2, dtype=BF16, B=1, Nq=500, Nk=300, Hq=2, Hk=1, d=128),
+    "dv_hundreds": dict(off=("dv", "split_kv"), most=1.2, dtype=F16, B=1, Nq=500, Nk=300, Hq=2, Hk=2, d=64),
+    "dk_even": dict(off=("dk", "split_kv"), most=1.2, dtype=BF16, B=1, Nq=300, Nk=3000, Hq=2, Hk=2, d=64, sharp=0.2),
+    "dv_even": dict(off=("dv", "split_kv"), most=1.15, dtype=F16, B=1, Nq=200, Nk=3000, Hq=2, Hk=1, d=128, sharp=0.2),
+    "dk_sharp": dict(off=("dk", "split_kv"), most=1.2, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
                      sharp=4.0),
-    "dv_sharp": dict(off=("dv", "split_kv"), own={}, most=1.15, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
+    "dv_sharp": dict(off=("dv", "split_kv"), most=1.15, dtype=BF16, B=1, Nq=300, Nk=64, Hq=2, Hk=2, d=64,
                      sharp=4.0),
     # the forward multiplies P's residual: few rows a key head, tiles of them, tiles over split keys
-    "few_rows": dict(off=("o", "split_o"), own={}, most=1.2, dtype=BF16, B=2, Nq=3, Nk=1000, Hq=4, Hk=2, d=128),
-    "few_rows_f16": dict(off=("o", "split_o"), own={}, most=1.15, dtype=F16, B=2, Nq=1, Nk=1499, Hq=8, Hk=8, d=64),
-    "tiles": dict(off=("o", "split_o"), own={}, most=1.15, dtype=BF16, B=2, Nq=300, Nk=512, Hq=2, Hk=2, d=128,
+    "few_rows": dict(off=("o", "split_o"), most=1.2, dtype=BF16, B=2, Nq=3, Nk=1000, Hq=4, Hk=2, d=128),
+    "few_rows_f16": dict(off=("o", "split_o"), most=1.15, dtype=F16, B=2, Nq=1, Nk=1499, Hq=8, Hk=8, d=64),
+    "tiles": dict(off=("o", "split_o"), most=1.15, dtype=BF16, B=2, Nq=300, Nk=512, Hq=2, Hk=2, d=128,
                   k_lens=[512, 77]),
-    "tiles_f16": dict(off=("o", "split_o"), own={}, most=1.15, dtype=F16, B=1, Nq=200, Nk=300, Hq=4, Hk=1, d=64),
-    "tiles_long": dict(off=("o", "split_o"), own={}, most=1.15, dtype=BF16, B=1, Nq=128, Nk=9000, Hq=2, Hk=2, d=64),
+    "tiles_f16": dict(off=("o", "split_o"), most=1.15, dtype=F16, B=1, Nq=200, Nk=300, Hq=4, Hk=1, d=64),
+    "tiles_long": dict(off=("o", "split_o"), most=1.15, dtype=BF16, B=1, Nq=128, Nk=9000, Hq=2, Hk=2, d=64),
     # D comes from the scores, not from the rounded o: over few keys, alone or padded to many, where q, k and v share
     # large channels, and where a row is nearly all one key
-    "d_of_short": dict(off=("dq", "d_scores"), own=ONCE, most=1.35, dtype=BF16, B=4, Nq=300, Nk=512, Hq=2, Hk=2, d=64,
+    "d_of_short": dict(off=("dq", "d_scores"), most=1.35, dtype=BF16, B=4, Nq=300, Nk=512, Hq=2, Hk=2, d=64,
                        k_lens=[4, 8, 24, 60]),
-    "d_of_short_f16": dict(off=("dq", "d_scores"), own=ONCE, most=1.25, dtype=F16, B=4, Nq=150, Nk=300, Hq=2, Hk=1,
+    "d_of_short_f16": dict(off=("dq", "d_scores"), most=1.25, dtype=F16, B=4, Nq=150, Nk=300, Hq=2, Hk=1,
                            d=128, k_lens=[4, 8, 24, 40]),
-    "d_of_short_only": dict(off=("dq", "d_scores"), own=ONCE, most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
+    "d_of_short_only": dict(off=("dq", "d_scores"), most=1.3, dtype=BF16, B=3, Nq=300, Nk=40, Hq=2, Hk=1,
                             d=128, k_lens=[4, 8, 30]),
-    "d_shared": dict(off=("dq", "d_scores"), own={}, most=1.3, dtype=BF16, B=2, Nq=260, Nk=1500, Hq=2, Hk=1, d=128,
+    "d_shared": dict(off=("dq", "d_scores"), most=1.3, dtype=BF16, B=2, Nq=260, Nk=1500, Hq=2, Hk=1, d=128,
                      k_lens=[1500, 333], shared=True),
-    "d_shared_f16": dict(off=("dq", "d_scores"), own={}, most=1.3, dtype=F16, B=1, Nq=100, Nk=4000, Hq=2, Hk=2,
+    "d_shared_f16": dict(off=("dq", "d_scores"), most=1.3, dtype=F16, B=1, Nq=100, Nk=4000, Hq=2, Hk=2,
                          d=64, shared=True),
-    "d_sharp": dict(off=("dk", "d_scores"), own={}, most=1.5, dtype=BF16, B=1, Nq=300, Nk=200, Hq=2, Hk=2, d=64,
+    "d_sharp": dict(off=("dk", "d_scores"), most=1.3, dtype=BF16, B=1, Nq=300, Nk=200, Hq=2, Hk=2, d=64,
                     sharp=8.0),
     # fp16: dS of small upstream gradients over many keys, and P of many keys, below fp16's normal values
-    "dq_small": dict(off=("dq", "scaled"), own=ONCE, most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
+    "dq_small": dict(off=("dq", "scaled"), most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
                      do=1e-3),
-    "dk_small": dict(off=("dk", "scaled"), own=ONCE, most=1.6, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
+    "dk_small": dict(off=("dk", "scaled"), most=1.3, dtype=F16, B=1, Nq=200, Nk=4096, Hq=2, Hk=1, d=128,
                      do=1e-3),
-    "dq_tiny": dict(off=("dq", "scaled"), own=ONCE, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
+    "dq_tiny": dict(off=("dq", "scaled"), most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
                     do=1e-4, k_lens=[5000, 4097]),
-    "dk_tiny": dict(off=("dk", "scaled"), own=ONCE, most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
+    "dk_tiny": dict(off=("dk", "scaled"), most=1.3, dtype=F16, B=2, Nq=70, Nk=5000, Hq=2, Hk=2, d=64,
                     do=1e-4, k_lens=[5000, 4097]),
-    "dv_long": dict(off=("dv", "scaled"), own=ONCE, most=1.6, dtype=F16, B=1, Nq=130, Nk=40000, Hq=1, Hk=1, d=64,
+    "dv_long": dict(off=("dv", "scaled"), most=1.3, dtype=F16, B=1, Nq=130, Nk=40000, Hq=1, Hk=1, d=64,
                     sharp=0.1),
     # rows of unlike upstream gradients: each row of dQ by itself
-    "dq_rows_apart": dict(off=("dq", "scaled"), own=ONCE, most=1.5, rows=True, dtype=F16, B=1, Nq=64, Nk=64, Hq=4,
+    "dq_rows_apart": dict(off=("dq", "scaled"), most=1.5, rows=True, dtype=F16, B=1, Nq=64, Nk=64, Hq=4,
                           Hk=4, d=64, spread=13),
 }
 

@@ -10,6 +10,6 @@ def test_case_tells_the_rounding(name):
     c = CASES[name]
     x, lens = inputs(c), c.get("k_lens")
     ref = definition(*x, k_lens=lens)
-    fine = ratio_of(c, emulate(*x, k_lens=lens, **c["own"]), ref)
-    coarse = ratio_of(c, emulate(*x, k_lens=lens, **{**c["own"], c["off"][1]: False}), ref)
+    fine = ratio_of(c, emulate(*x, k_lens=lens), ref)
+    coarse = ratio_of(c, emulate(*x, k_lens=lens, **{c["off"][1]: False}), ref)
     assert fine < c["most"] < coarse

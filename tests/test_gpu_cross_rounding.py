@@ -54,7 +54,7 @@ def test_large_gradients_in_fp16(d, Nq, Nk, k_lens):
     for name in ("dq", "dk", "dv"):
         assert ref[name].abs().max() < 65000
         off = ratio(x[name], ref[name], F16)
-        assert off < 1.7, name
+        assert off < 1.2, name
 
 
 def test_gradients_of_zero_and_of_the_least_values_in_fp16():
@@ -67,7 +67,7 @@ def test_gradients_of_zero_and_of_the_least_values_in_fp16():
     ref, x = definition(q, k, v, do), run(q, k, v, do)
     assert not any(x[n].isnan().any() or x[n].isinf().any() for n in x)
     for n in ("dq", "dk", "dv"):
-        assert ratio(x[n], ref[n], F16) < 1.7, n
+        assert ratio(x[n], ref[n], F16) < 1.2, n
     assert not x["dq"][0, 3:9].any() and not x["dq"][1, :, 2:].any() and not x["dk"][1, :, 1].any()
     x = run(q, k, v, torch.zeros_like(do))
     assert not any(x[n].any() for n in ("dq", "dk", "dv"))
