@@ -34,7 +34,7 @@ inline CrossTile cross_tile(int Nq, int G, int most, int least) {
 
 // fp16 has no normal values below 2^-14, where P is over more than 2^14 keys: the dV product takes P * 2^15 (at most
 // 2^15), with 2^-15 on the sums; -L * log2(e) is kept with the 15 added. Without, over 40000 even keys dV was 3.4
-// times as far off as its own rounding (1.4 so).
+// times as far off as its own rounding (1.0 so).
 template <bool kBf16>
 constexpr float kCrossPLog2 = kBf16 ? 0.f : 15.f;
 template <bool kBf16>

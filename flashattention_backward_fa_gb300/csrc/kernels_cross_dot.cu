@@ -10,7 +10,7 @@
 // up to -e, and dQ_i is off by scale e sum_j P_ij K_j. Where q and k share large channels, or a few keys make up
 // the row, that is more than everything else: error of dQ (bf16, 2-norm, in units of its own rounding) 1.05 to
 // 2.4 over 128 to 4096 keys with none to three of four large channels shared, of dK 3 with q eight times as sharp
-// over 200 keys. From the scores both are 1.0 to 1.2.
+// over 200 keys. From the scores both are 1.0.
 //
 // Bound by its two products over long keys (bf16 1x32/8 8192x4096 306 us, 1.80 PFLOP/s), by the starts and ends of
 // its units over few (4x16 2048 over texts of 169 to 512 32 us, fp16 2x16/4 4095 over 34 and 77 20, by themselves).
